@@ -50,7 +50,9 @@ typedef enum {
   QAT_ERR_UNSUPPORTED = 2, /* valid request this library does not implement       */
   QAT_ERR_CUDA = 3,        /* a CUDA runtime / launch error (see cudaGetLastError) */
   QAT_ERR_TIMEOUT = 4,     /* a bounded device-side wait expired (kernel returned)  */
-  QAT_ERR_WORKSPACE = 5    /* workspace missing or smaller than required            */
+  QAT_ERR_WORKSPACE = 5,   /* workspace missing or smaller than required            */
+  QAT_ERR_BAD_PAGE = 6     /* device-side: a page index or a sequence length that the cache
+                              or its block table cannot hold                         */
 } qat_status_t;
 
 /* quant_mode values */
@@ -272,6 +274,132 @@ QAT_API qat_status_t qat_fake_quant_tokens(const void* x, const float* mean, voi
 QAT_API qat_status_t qat_subtract_mean(const void* x, const float* mean, void* out, int B, int H,
                                        int N, int D, void* stream);
 
+/*
+ * qat_qk_norm_rope -- what makes the attention's queries and keys: the RMS norm of each
+ * head's D channels and the rotation by position, in one pass.
+ *   q, k     bf16 [B, Hq, N, D] and [B, Hk, N, D]; Hq or Hk may be 0 (that tensor is absent)
+ *   q_strides, k_strides  host pointers to three element strides {b, h, n}, D innermost, each
+ *            >= 0 and a multiple of 8 (the stride of an axis of length one is ignored); NULL:
+ *            contiguous.  Heads-innermost projections, slices of a fused projection and
+ *            broadcast axes (stride 0) are read in place.
+ *   q_out, k_out  bf16, contiguous [B, H, N, D] OUT (not the inputs' memory)
+ *   positions  int32 (device), the position of token n of sequence b at
+ *            positions[b * position_stride + n] (stride 0: one row for all); any int32.
+ *   phases   uint64 [rotary_dim / 2] (device): pair i turns by phases[i] / 2^64 of a full turn
+ *            per position, i.e. phases[i] = round(f_i / (2 pi) * 2^64) mod 2^64 for a frequency
+ *            of f_i radians per position.  The product with the position is taken modulo 2^64,
+ *            so the angle is exact to 2^-32 of a turn at every position.
+ *   rotary_dim  0 .. D, a multiple of 16: channels [0, rotary_dim) are rotated in pairs
+ *            (i, i + rotary_dim / 2), or (2i, 2i + 1) with interleaved = 1:
+ *            a' = amplitude (a cos - b sin), b' = amplitude (a sin + b cos).
+ *            The other channels are left as the norm gives them.  0: no rotation (positions
+ *            and phases are not read).
+ *   q_weight, k_weight  [D] fp32, or bf16 with weight_bf16 = 1 (device, 16-byte aligned):
+ *            z = x rsqrt(mean_d x_d^2 + eps) weight.  Both NULL: no norm, z = x.
+ *   eps      finite, > 0.
+ * Everything is computed in fp32 and rounded once, on the store.
+ * Errors: QAT_ERR_INVALID_ARG, QAT_ERR_CUDA.
+ */
+QAT_API qat_status_t qat_qk_norm_rope(
+    const void* q, const long long* q_strides, const void* k, const long long* k_strides,
+    void* q_out, void* k_out, const int* positions, long long position_stride,
+    const unsigned long long* phases, const void* q_weight, const void* k_weight, int weight_bf16,
+    int B, int Hq, int Hk, int N, int D, int rotary_dim, int interleaved, float amplitude,
+    float eps, void* stream);
+
+/*
+ * qat_qk_norm_rope_bwd -- the gradients of qat_qk_norm_rope.
+ *   dq_out, dk_out  bf16 [B, H, N, D] with strides as above: gradients of its outputs
+ *   dq, dk     bf16 [B, H, N, D] OUT, with strides as above (no two elements may share memory)
+ *   dq_weight, dk_weight  [D] OUT in the weights' type, or NULL.  Summed in a fixed order: the
+ *            same sizes give the same bits.
+ *   workspace  at least qat_qk_norm_rope_bwd_workspace_bytes(D) bytes, 256-byte aligned; not
+ *            used without weights.
+ *   Other arguments as in the forward.  No rows (B, N, or both Hq and Hk zero): the weights'
+ *   gradients are set to zero.
+ * Errors: as the forward; QAT_ERR_WORKSPACE.
+ */
+QAT_API size_t qat_qk_norm_rope_bwd_workspace_bytes(int D);
+QAT_API qat_status_t qat_qk_norm_rope_bwd(
+    const void* q, const long long* q_strides, const void* k, const long long* k_strides,
+    const void* dq_out, const long long* dq_out_strides, const void* dk_out,
+    const long long* dk_out_strides, const int* positions, long long position_stride,
+    const unsigned long long* phases, const void* q_weight, const void* k_weight, int weight_bf16,
+    void* dq, const long long* dq_strides, void* dk, const long long* dk_strides, void* dq_weight,
+    void* dk_weight, int B, int Hq, int Hk, int N, int D, int rotary_dim, int interleaved,
+    float amplitude, float eps, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * The FP8 key/value cache: pages of page_size tokens (16, 32, 64, 128 or 256),
+ *   k_codes, v_codes    E4M3 bytes [num_pages, H, page_size, D]
+ *   k_scales, v_scales  fp32       [num_pages, H, page_size]
+ * Position i of sequence b lies in slot i % page_size of page block_table[b, i / page_size]
+ * (int32 [B, max_pages], device); seq_lens[b] (int32, device) is the sequence's length.  Both
+ * are read on the device, so a captured call follows them.  Rule per (token, head) row:
+ *   amax = max |x|; code = E4M3_RNE_SATFINITE(fl32(x fl32(448 / amax))); scale = fl32(amax / 448);
+ *   value = code * scale.
+ * A row whose amax is below 2^-110 is stored as zeros.  A row with a NaN or an infinity is stored
+ * as codes 0 with scale NaN, and reads as NaN.
+ * A block table entry outside [0, num_pages) that a call needs, or a length above
+ * max_pages * page_size, is reported by the next qat_attn_device_status as QAT_ERR_BAD_PAGE; no
+ * memory outside the cache is touched.
+ *
+ * qat_kv_cache_append -- quantizes new keys and values into their pages.
+ *   k, v      bf16 [B, H, N, D] with element strides as in qat_qk_norm_rope
+ *   seq_lens  lengths AFTER the append
+ *   new_lens  int32 [B] (device) or NULL (N for every sequence): how many of a sequence's N rows
+ *             are new tokens, the first ones; rows behind them are padding and not read.  Values
+ *             above N count as N.  Row n of sequence b is position seq_lens[b] - new_lens[b] + n;
+ *             rows whose position would be negative are dropped.
+ *   Rows on a page outside the cache are dropped (see above).  Two rows must not go to one slot:
+ *   pages that sequences share are for reading.
+ * qat_kv_cache_read -- positions [begin, begin + N) of every sequence as bf16 [B, H, N, D],
+ *   contiguous, bf16_RN(fl32(code scale)); zeros behind a sequence's end; NaN on a page outside
+ *   the cache.
+ * Errors: QAT_ERR_INVALID_ARG (null or misaligned pointer, bad size, stride or D),
+ *   QAT_ERR_UNSUPPORTED (another page size; max_pages * page_size above 2^30), QAT_ERR_CUDA.
+ */
+QAT_API qat_status_t qat_kv_cache_append(const void* k, const long long* k_strides, const void* v,
+                                         const long long* v_strides, void* k_codes, void* v_codes,
+                                         float* k_scales, float* v_scales, const int* block_table,
+                                         const int* seq_lens, const int* new_lens, int B, int H,
+                                         int N, int D, int num_pages, int page_size, int max_pages,
+                                         void* stream);
+QAT_API qat_status_t qat_kv_cache_read(const void* k_codes, const void* v_codes,
+                                       const float* k_scales, const float* v_scales,
+                                       const int* block_table, const int* seq_lens, void* k_out,
+                                       void* v_out, int B, int H, int begin, int N, int D,
+                                       int num_pages, int page_size, int max_pages, void* stream);
+
+/*
+ * qat_attn_decode -- attention of each sequence's last T tokens over the FP8 cache.
+ *   q        bf16 [B, Hq, T, D]: token t of sequence b is position seq_lens[b] - T + t and sees the
+ *            keys up to its own; its key and value must be in the cache already
+ *   Hq       a multiple of Hkv: query heads [h G, (h + 1) G), G = Hq / Hkv, read KV head h
+ *   T        1 .. 16 (0: nothing to do);  B <= 4096
+ *   o        bf16 [B, Hq, T, D] OUT
+ *   lse      fp32 [B, Hq, T] OUT or NULL: base-2 log-sum-exp, as in qat_attn_fwd
+ *   quant_mode  QAT_QUANT_NONE or QAT_QUANT_P_FP8E4M3_ROW_TILE64 (the forward's rule, with tiles of
+ *            64 absolute positions; a tile whose largest p is below 2^-100 of the row's counts as
+ *            zeros)
+ *   A row that sees no key (position < 0) gets o = 0 and lse = -inf.
+ *   Only keys that a row sees can reach its output: what lies behind the sequence's end in its last
+ *   page, or in newer tokens' rows, may be anything the append can have stored, NaN rows included.
+ *   workspace  at least qat_attn_decode_workspace_bytes(D) bytes, 256-byte aligned; contents ignored
+ *            on entry, unspecified on exit.  Two calls that may overlap need two workspaces.
+ *   The work is split by the lengths on the device; the same lengths give the same bits.
+ * Errors: as the cache's entries, QAT_ERR_UNSUPPORTED also for T or B above the limits or more than
+ *   2^31 64-key tiles; QAT_ERR_WORKSPACE.  Pages outside the cache give NaN rows (see above).
+ */
+QAT_API size_t qat_attn_decode_workspace_bytes(int D);
+QAT_API qat_status_t qat_attn_decode(const void* q, const void* k_codes, const void* v_codes,
+                                     const float* k_scales, const float* v_scales,
+                                     const int* block_table, const int* seq_lens, void* o,
+                                     float* lse, int B, int Hq, int Hkv, int T, int D,
+                                     int num_pages, int page_size, int max_pages, float sm_scale,
+                                     int quant_mode, void* workspace, size_t workspace_bytes,
+                                     void* stream);
+
 /* Static, human-readable name of a status code (never NULL). */
 QAT_API const char* qat_status_string(qat_status_t status);
 
@@ -279,7 +407,9 @@ QAT_API const char* qat_status_string(qat_status_t status);
  * qat_attn_device_status -- synchronizes `stream`, then reads and clears the
  * library's device-side error word on the current device.  Kernels whose waits are
  * bounded set it when a wait expires (they then return early instead of hanging).
- * Returns QAT_OK, QAT_ERR_TIMEOUT, or QAT_ERR_CUDA if the synchronization failed.
+ * The cache's kernels also record page indices and lengths that the cache cannot hold.
+ * Returns QAT_OK, QAT_ERR_TIMEOUT, QAT_ERR_BAD_PAGE (no timeout), or QAT_ERR_CUDA if the
+ * synchronization failed.
  */
 QAT_API qat_status_t qat_attn_device_status(void* stream);
 

@@ -1,0 +1,171 @@
+"""Serving what was trained: the FP8 key/value cache and the attention of new tokens over it.
+
+``KVCache`` quantizes keys and values as they are written to its pages (FP8 E4M3, one absmax scale
+per token and head) and reads them back; ``qat_attention_decode`` computes the attention of each
+sequence's last tokens over it, with P fake-quantized as in training.  Block tables and lengths are
+read on the device, so every call can be captured into a CUDA graph and replayed as they change.
+"""
+
+from __future__ import annotations
+
+import math
+
+import torch
+
+from . import capi
+from .attention import _raise, check_device_status, _check_enabled, device_guard
+from .rope import _rows, _strides
+
+
+def _index(t, name, device, dims):
+    if not isinstance(t, torch.Tensor) or t.device != device:
+        raise ValueError(f"{name} must be a tensor on {device}")
+    if t.dtype != torch.int32:
+        raise ValueError(f"{name} must be torch.int32, got {t.dtype}")
+    if t.dim() != dims or not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous with {dims} dimension(s), got shape "
+                         f"{tuple(t.shape)}")
+
+
+class KVCache:
+    """Pages of keys and values: ``k`` and ``v`` are torch.float8_e4m3fn [pages, H, page_size, D],
+    ``k_scale`` and ``v_scale`` fp32 [pages, H, page_size]; a row's value is its codes times its
+    scale.  page_size is 16, 32, 64, 128 or 256, D 64 or 128.
+
+    ``block_table`` (int32 [B, pages per sequence]) and ``seq_lens`` (int32 [B]) place the
+    sequences: position i of sequence b is slot i % page_size of page block_table[b, i // page_size].
+    Entries outside the cache are never followed: such rows are dropped by ``append``, read as NaN,
+    and reported by ``check_device_status`` (or at once with check=True)."""
+
+    def __init__(self, k, v, k_scale, v_scale):
+        if not isinstance(k, torch.Tensor) or not k.is_cuda:
+            raise ValueError("k must be a CUDA tensor (this library has no CPU path)")
+        if k.dim() != 4:
+            raise ValueError(f"k must be [pages, H, page_size, D], got shape {tuple(k.shape)}")
+        pages, H, page, D = k.shape
+        if D not in (64, 128):
+            raise ValueError(f"the head dimension must be 64 or 128, got {D}")
+        if page not in (16, 32, 64, 128, 256):
+            raise ValueError(f"page_size must be 16, 32, 64, 128 or 256, got {page}")
+        if pages < 1 or H < 1:
+            raise ValueError("a cache has at least one page and one head")
+        for name, t, shape, dtype in (("k", k, (pages, H, page, D), torch.float8_e4m3fn),
+                                      ("v", v, (pages, H, page, D), torch.float8_e4m3fn),
+                                      ("k_scale", k_scale, (pages, H, page), torch.float32),
+                                      ("v_scale", v_scale, (pages, H, page), torch.float32)):
+            if not isinstance(t, torch.Tensor) or t.device != k.device:
+                raise ValueError(f"{name} must be a tensor on {k.device}")
+            if t.dtype != dtype:
+                raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+            if tuple(t.shape) != shape or not t.is_contiguous() or t.data_ptr() % 16:
+                raise ValueError(f"{name} must be contiguous {shape} on a 16-byte boundary, got shape "
+                                 f"{tuple(t.shape)}")
+        self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
+        self.num_pages, self.heads, self.page_size, self.D = pages, H, page, D
+        self.device = k.device
+
+    @classmethod
+    def empty(cls, num_pages: int, heads: int, page_size: int, D: int, device="cuda") -> "KVCache":
+        """A cache of unwritten pages (their contents are unspecified: nothing past a sequence's
+        length is ever used)."""
+        def codes():
+            return torch.empty((num_pages, heads, page_size, D), dtype=torch.float8_e4m3fn,
+                               device=device)
+
+        def scales():
+            return torch.empty((num_pages, heads, page_size), dtype=torch.float32, device=device)
+
+        return cls(codes(), codes(), scales(), scales())
+
+    def _tables(self, block_table, seq_lens):
+        _index(block_table, "block_table", self.device, 2)
+        _index(seq_lens, "seq_lens", self.device, 1)
+        B = seq_lens.shape[0]
+        if block_table.shape[0] != B:
+            raise ValueError(f"block_table has {block_table.shape[0]} rows for {B} sequences")
+        if block_table.shape[1] < 1:
+            raise ValueError("block_table has no pages")
+        return B
+
+    def append(self, k, v, block_table, seq_lens, new_lens=None, check: bool | None = None) -> None:
+        """Quantizes new keys and values, bf16 [B, H, N, D] with any strides that have D innermost,
+        into their pages.  ``seq_lens`` are the lengths after the append: row n of sequence b goes to
+        position seq_lens[b] - N + n, or, with int32 ``new_lens`` [B], to seq_lens[b] - new_lens[b] + n
+        for its first new_lens[b] rows (the others are padding).  No two rows may go to one slot."""
+        B = self._tables(block_table, seq_lens)
+        _rows(k, "k", self.device)
+        N = k.shape[2]
+        _rows(k, "k", self.device, B, N, self.D, self.heads)
+        _rows(v, "v", self.device, B, N, self.D, self.heads)
+        if new_lens is not None:
+            _index(new_lens, "new_lens", self.device, 1)
+            if new_lens.shape[0] != B:
+                raise ValueError(f"new_lens has {new_lens.shape[0]} entries for {B} sequences")
+        with device_guard(self.device):
+            st = capi.qat_kv_cache_append(
+                k, _strides(k), v, _strides(v), self.k, self.v, self.k_scale, self.v_scale,
+                block_table, seq_lens, new_lens, B, self.heads, N, self.D, self.num_pages,
+                self.page_size, block_table.shape[1])
+            _raise(st, "qat_kv_cache_append")
+            if _check_enabled(check):
+                check_device_status("qat_kv_cache_append")
+
+    def read(self, block_table, seq_lens, begin: int = 0, length: int | None = None,
+             check: bool | None = None):
+        """(k, v) of positions [begin, begin + length), bf16 [B, H, length, D] contiguous, zeros behind
+        a sequence's end.  Without ``length``: all that the block table can hold."""
+        B = self._tables(block_table, seq_lens)
+        if begin < 0 or (length is not None and length < 0):
+            raise ValueError("begin and length must not be negative")
+        if length is None:
+            length = max(block_table.shape[1] * self.page_size - begin, 0)
+        shape = (B, self.heads, length, self.D)
+        k_out = torch.empty(shape, dtype=torch.bfloat16, device=self.device)
+        v_out = torch.empty(shape, dtype=torch.bfloat16, device=self.device)
+        with device_guard(self.device):
+            st = capi.qat_kv_cache_read(self.k, self.v, self.k_scale, self.v_scale, block_table,
+                                        seq_lens, k_out, v_out, B, self.heads, begin, length, self.D,
+                                        self.num_pages, self.page_size, block_table.shape[1])
+            _raise(st, "qat_kv_cache_read")
+            if _check_enabled(check):
+                check_device_status("qat_kv_cache_read")
+        return k_out, v_out
+
+
+def qat_attention_decode(q, cache: KVCache, block_table, seq_lens, sm_scale: float | None = None,
+                         quant_mode: int = capi.QUANT_P_FP8E4M3_ROW_TILE64, return_lse: bool = False,
+                         workspace: torch.Tensor | None = None, check: bool | None = None):
+    """Attention of each sequence's last T tokens, q bf16 [B, Hq, T, D], over the cache, which holds
+    their own keys and values already: token t is position seq_lens[b] - T + t and sees the keys up to
+    its own.  Hq is a multiple of the cache's heads (consecutive query heads share one); T is at most
+    16.  Returns o bf16 [B, Hq, T, D], and with ``return_lse`` the base-2 log-sum-exp fp32 [B, Hq, T].
+    A row that sees no key gives o = 0, lse = -inf.  ``workspace``: uint8, at least
+    ``capi.qat_attn_decode_workspace_bytes(D)`` bytes, for one call at a time; allocated if None."""
+    if not isinstance(cache, KVCache):
+        raise TypeError("cache must be a KVCache")
+    B = cache._tables(block_table, seq_lens)
+    _rows(q, "q", cache.device)
+    if not q.is_contiguous():
+        raise ValueError("q must be contiguous")
+    Hq, T, D = q.shape[1:]
+    if q.shape[0] != B or D != cache.D:
+        raise ValueError(f"q has shape {tuple(q.shape)}, expected ({B}, Hq, T, {cache.D})")
+    if Hq < 1 or Hq % cache.heads:
+        raise ValueError(f"{Hq} query heads do not share the cache's {cache.heads} evenly")
+    if workspace is None:
+        workspace = torch.empty(capi.qat_attn_decode_workspace_bytes(D), dtype=torch.uint8,
+                                device=cache.device)
+    elif not workspace.is_cuda or workspace.device != cache.device or workspace.dtype != torch.uint8:
+        raise ValueError(f"workspace must be a uint8 tensor on {cache.device}")
+    o = torch.empty_like(q)
+    lse = torch.empty((B, Hq, T), dtype=torch.float32, device=cache.device) if return_lse else None
+    sm_scale = 1.0 / math.sqrt(D) if sm_scale is None else float(sm_scale)
+    with device_guard(cache.device):
+        st = capi.qat_attn_decode(q, cache.k, cache.v, cache.k_scale, cache.v_scale, block_table,
+                                  seq_lens, o, lse, B, Hq, cache.heads, T, D, cache.num_pages,
+                                  cache.page_size, block_table.shape[1], sm_scale, quant_mode, workspace,
+                                  workspace.numel())
+        _raise(st, "qat_attn_decode")
+        if _check_enabled(check):
+            check_device_status("qat_attn_decode")
+    return (o, lse) if return_lse else o

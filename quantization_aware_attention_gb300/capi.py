@@ -33,6 +33,13 @@ EXPORTED = (
     "qat_attn_bwd_smooth_k",
     "qat_subtract_mean",
     "qat_debug_set_wait_limit_us",
+    "qat_qk_norm_rope",
+    "qat_qk_norm_rope_bwd_workspace_bytes",
+    "qat_qk_norm_rope_bwd",
+    "qat_kv_cache_append",
+    "qat_kv_cache_read",
+    "qat_attn_decode_workspace_bytes",
+    "qat_attn_decode",
 )
 
 
@@ -43,6 +50,7 @@ class Status(enum.IntEnum):
     CUDA = 3
     TIMEOUT = 4
     WORKSPACE = 5
+    BAD_PAGE = 6
 
 
 QUANT_NONE = 0
@@ -58,6 +66,8 @@ class QatError(RuntimeError):
 
 _lib = None
 _vp, _i, _f, _sz = ctypes.c_void_p, ctypes.c_int, ctypes.c_float, ctypes.c_size_t
+_ll = ctypes.c_longlong
+_ll3 = _ll * 3
 
 
 def lib() -> ctypes.CDLL:
@@ -99,6 +109,21 @@ def lib() -> ctypes.CDLL:
         L.qat_subtract_mean.restype = _i
         L.qat_debug_set_wait_limit_us.argtypes = [_i, _vp]
         L.qat_debug_set_wait_limit_us.restype = _i
+        L.qat_qk_norm_rope.argtypes = [_vp] * 7 + [_ll] + [_vp] * 3 + [_i] * 8 + [_f, _f, _vp]
+        L.qat_qk_norm_rope.restype = _i
+        L.qat_qk_norm_rope_bwd_workspace_bytes.argtypes = [_i]
+        L.qat_qk_norm_rope_bwd_workspace_bytes.restype = _sz
+        L.qat_qk_norm_rope_bwd.argtypes = ([_vp] * 9 + [_ll] + [_vp] * 3 + [_i] + [_vp] * 6 + [_i] * 7
+                                           + [_f, _f, _vp, _sz, _vp])
+        L.qat_qk_norm_rope_bwd.restype = _i
+        L.qat_kv_cache_append.argtypes = [_vp] * 11 + [_i] * 7 + [_vp]
+        L.qat_kv_cache_append.restype = _i
+        L.qat_kv_cache_read.argtypes = [_vp] * 8 + [_i] * 8 + [_vp]
+        L.qat_kv_cache_read.restype = _i
+        L.qat_attn_decode_workspace_bytes.argtypes = [_i]
+        L.qat_attn_decode_workspace_bytes.restype = _sz
+        L.qat_attn_decode.argtypes = [_vp] * 9 + [_i] * 8 + [_f, _i, _vp, _sz, _vp]
+        L.qat_attn_decode.restype = _i
         _lib = L
     return _lib
 
@@ -204,3 +229,64 @@ def qat_attn_merge(o_q_acc, o_hp_acc, lse_acc, o_q_part, o_hp_part, lse_part, o_
                                        _ptr(o_q_part), _ptr(o_hp_part), _ptr(lse_part),
                                        _ptr(o_q_out), _ptr(o_hp_out), B, H, Nq, D,
                                        _stream(stream)))
+
+
+def _s3(strides):
+    """Three element strides as a host array, or NULL (contiguous)."""
+    return None if strides is None else _ll3(*strides)
+
+
+def qat_qk_norm_rope(q, q_strides, k, k_strides, q_out, k_out, positions, position_stride, phases,
+                     q_weight, k_weight, weight_bf16, B, Hq, Hk, N, D, rotary_dim, interleaved,
+                     amplitude, eps, stream=None) -> Status:
+    return Status(lib().qat_qk_norm_rope(
+        _ptr(q), _s3(q_strides), _ptr(k), _s3(k_strides), _ptr(q_out), _ptr(k_out), _ptr(positions),
+        position_stride, _ptr(phases), _ptr(q_weight), _ptr(k_weight), int(weight_bf16), B, Hq, Hk, N,
+        D, rotary_dim, interleaved, amplitude, eps, _stream(stream)))
+
+
+def qat_qk_norm_rope_bwd_workspace_bytes(D) -> int:
+    return int(lib().qat_qk_norm_rope_bwd_workspace_bytes(D))
+
+
+def qat_qk_norm_rope_bwd(q, q_strides, k, k_strides, dq_out, dq_out_strides, dk_out, dk_out_strides,
+                         positions, position_stride, phases, q_weight, k_weight, weight_bf16, dq,
+                         dq_strides, dk, dk_strides, dq_weight, dk_weight, B, Hq, Hk, N, D, rotary_dim,
+                         interleaved, amplitude, eps, workspace, workspace_bytes,
+                         stream=None) -> Status:
+    return Status(lib().qat_qk_norm_rope_bwd(
+        _ptr(q), _s3(q_strides), _ptr(k), _s3(k_strides), _ptr(dq_out), _s3(dq_out_strides),
+        _ptr(dk_out), _s3(dk_out_strides), _ptr(positions), position_stride, _ptr(phases),
+        _ptr(q_weight), _ptr(k_weight), int(weight_bf16), _ptr(dq), _s3(dq_strides), _ptr(dk),
+        _s3(dk_strides), _ptr(dq_weight), _ptr(dk_weight), B, Hq, Hk, N, D, rotary_dim, interleaved,
+        amplitude, eps, _ptr(workspace), workspace_bytes, _stream(stream)))
+
+
+def qat_kv_cache_append(k, k_strides, v, v_strides, k_codes, v_codes, k_scales, v_scales, block_table,
+                        seq_lens, new_lens, B, H, N, D, num_pages, page_size, max_pages,
+                        stream=None) -> Status:
+    return Status(lib().qat_kv_cache_append(
+        _ptr(k), _s3(k_strides), _ptr(v), _s3(v_strides), _ptr(k_codes), _ptr(v_codes),
+        _ptr(k_scales), _ptr(v_scales), _ptr(block_table), _ptr(seq_lens), _ptr(new_lens), B, H, N, D,
+        num_pages, page_size, max_pages, _stream(stream)))
+
+
+def qat_kv_cache_read(k_codes, v_codes, k_scales, v_scales, block_table, seq_lens, k_out, v_out, B, H,
+                      begin, N, D, num_pages, page_size, max_pages, stream=None) -> Status:
+    return Status(lib().qat_kv_cache_read(
+        _ptr(k_codes), _ptr(v_codes), _ptr(k_scales), _ptr(v_scales), _ptr(block_table),
+        _ptr(seq_lens), _ptr(k_out), _ptr(v_out), B, H, begin, N, D, num_pages, page_size, max_pages,
+        _stream(stream)))
+
+
+def qat_attn_decode_workspace_bytes(D) -> int:
+    return int(lib().qat_attn_decode_workspace_bytes(D))
+
+
+def qat_attn_decode(q, k_codes, v_codes, k_scales, v_scales, block_table, seq_lens, o, lse, B, Hq, Hkv,
+                    T, D, num_pages, page_size, max_pages, sm_scale, quant_mode, workspace,
+                    workspace_bytes, stream=None) -> Status:
+    return Status(lib().qat_attn_decode(
+        _ptr(q), _ptr(k_codes), _ptr(v_codes), _ptr(k_scales), _ptr(v_scales), _ptr(block_table),
+        _ptr(seq_lens), _ptr(o), _ptr(lse), B, Hq, Hkv, T, D, num_pages, page_size, max_pages,
+        float(sm_scale), int(quant_mode), _ptr(workspace), workspace_bytes, _stream(stream)))

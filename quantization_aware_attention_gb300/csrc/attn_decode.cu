@@ -1,0 +1,701 @@
+// attn_decode.cu -- attention of the last T tokens of each sequence over the FP8 key/value cache
+// (serving), with P fake-quantized as in training.
+//
+// Per query row (head, token) and visible key j (j <= its own position):
+//   s_j = sm_scale <q, k_j>,  k_j = code_j scale_j;  p_j = exp(s_j - m);  l = sum p_j
+//   quantized: per absolute 64-key tile amax = max p, p'_j = E4M3(p_j 448 / amax) amax / 448
+//   o = sum p'_j v_j / l;  lse = log2 sum exp(s_j).  A row that sees no key: o = 0, lse = -inf.
+//
+// What bounds it: the cache is read once, 2 (D + 4) bytes per key and KV head, and every byte
+// meets at most 16 query rows, so HBM does.  The kernel is built around keeping loads in flight:
+// every warp is its own worker with its own ring of 16-key slots filled by cp.async, no barrier
+// between warps, and all G = Hq / Hkv heads that share a KV head (times T tokens) are rows of one
+// 16-row tile, so that the cache is read once for all of them.
+//
+// Work split (stream-K): the batch's units -- 64-key tiles, ordered by sequence, KV head, row tile,
+// key -- are cut into equal contiguous ranges, one per warp, whatever the sequences' lengths.  An
+// (sequence, head, row tile) item inside one range is finished there; an item cut by a range
+// boundary leaves unnormalized fp32 partials with their m and l in the workspace, which
+// decode_merge_kernel adds in worker order (no atomics: the same lengths give the same bits).
+//
+// Products: mma.sync m16n8k16 with f16 operands and fp32 sums.  E4M3 codes are exact in f16, and
+// become f16 in registers (one conversion per two codes), so the scale of a key multiplies its
+// column of S, and the scale of a value its column of P.  q (bf16) is brought into f16 by a power
+// of two per row, which is exact for every element above 2^-32 of the row's largest.  P times the
+// value's scale is rounded to f16 (2^-11 relative; relative to a running power-of-two bound of the
+// scales, so that it neither overflows nor loses small weights: the largest is near 2^14, the
+// smallest kept whole 2^-28 of it).  With 16 rows at most these products need a tenth of the
+// tensor rate, and operands come from registers, so the 128-row tcgen05 tile would be mostly empty
+// rows; the memory pipeline is what has to be fed.
+//
+// Operand layout: the order of d in Q K^T and of the output columns in P V is free, so each lane
+// takes 16-byte runs of a row: for K chunk t + 4 h of key g (k-step s of the run: bytes 4 s..4 s + 3),
+// for V chunk g of keys 2t, 2t + 1, 2t + 8, 2t + 9, whose bytes are interleaved by key with prmt.
+// Chunks are XOR-swizzled by row so that these reads are free of bank conflicts.
+#include "qat_internal.h"
+#include "qat_quant.cuh"
+#include "sm100.cuh"
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+namespace qat {
+namespace {
+
+constexpr int kWarps = 8;
+constexpr int kTile = 64;    // keys per unit
+constexpr int kChunk = 16;   // keys per slot
+constexpr int kRows = 16;    // query rows per item
+constexpr int kMaxCtas = 152;
+constexpr int kWorkers = kMaxCtas * kWarps;
+constexpr float kTinyP = 7.888609052210118e-31f;  // 2^-100: a tile below it counts as zero (448 / amax
+                                                  // must stay finite)
+constexpr float kPTop = 16384.f;  // P x value scale / bound is at most this
+
+template <int D>
+struct Cfg {
+  static constexpr int kSlots = D == 128 ? 12 : 24;
+  static constexpr int kSlotBytes = kChunk * D + 4 * kChunk;  // codes, then scales
+  static constexpr int kRing = kSlots * kSlotBytes;
+  static constexpr int kSmem = kWarps * kRing;  // then B + 1 prefix sums
+};
+
+// Workspace: what each worker's range cut, then the partials.
+struct WorkerMeta {
+  int head;       // item whose beginning lies in an earlier range, or -1
+  int head_done;  // that item ends in this range
+  int tail;       // item that begins in this range and ends in a later one, or -1
+  int pad;
+};
+template <int D>
+struct Partial {
+  float o[kRows][D];
+  float ml[kRows][2];
+};
+template <int D>
+struct Workspace {
+  int workers;
+  int pad[3];
+  WorkerMeta meta[kWorkers];
+  Partial<D> part[kWorkers][2];  // [0] head, [1] tail
+};
+
+struct Params {
+  DecodeArgs a;
+  int R, mtiles;  // rows of a KV head (Hq / Hkv heads x T tokens), row tiles
+};
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+__device__ __forceinline__ uint32_t f16x2(float lo, float hi) {
+  const __half2 h = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+__device__ __forceinline__ uint32_t codes_to_f16x2(uint16_t c) {
+  uint32_t h2;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h2) : "h"(c));
+  return h2;
+}
+
+__device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
+                                         uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+      "{%0,%1,%2,%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// 16 bytes into shared memory, the first `bytes` from global memory and zeros behind them.
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, int bytes) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes)
+               : "memory");
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+__device__ __forceinline__ uint4 lds128(uint32_t a) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a) : "memory");
+  return v;
+}
+__device__ __forceinline__ uint2 lds64(uint32_t a) {
+  uint2 v;
+  asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a) : "memory");
+  return v;
+}
+__device__ __forceinline__ float2 lds_f2(uint32_t a) {
+  const uint2 v = lds64(a);
+  return make_float2(__uint_as_float(v.x), __uint_as_float(v.y));
+}
+
+// Byte offset of 16-byte chunk c of row r in a slot of K or V codes.
+template <int D>
+__device__ __forceinline__ uint32_t k_off(int r, int c) {
+  return D == 128 ? r * 128 + ((c ^ ((r & 1) << 2)) << 4) : r * 64 + (c << 4);
+}
+template <int D>
+__device__ __forceinline__ uint32_t v_off(int r, int c) {
+  if (D == 128) return r * 128 + ((c ^ (r & 6)) << 4);
+  return (r >> 1) * 128 + (((((r & 1) << 2) | c) ^ (((r >> 1) & 3) << 1)) << 4);
+}
+
+// A place in the batch's list of units.
+struct Cursor {
+  int b, h, mt, tile, tiles, len;
+};
+
+__device__ __forceinline__ int clamp_len(const DecodeArgs& a, int len) {
+  const long long cap = static_cast<long long>(a.max_pages) << a.page_shift;
+  return len > cap ? static_cast<int>(cap) : max(len, 0);
+}
+__device__ __forceinline__ int tiles_of(int len) { return len > 0 ? (len + kTile - 1) / kTile : 1; }
+
+__device__ __forceinline__ void enter_seq(const DecodeArgs& a, Cursor& c) {
+  c.len = c.b < a.B ? clamp_len(a, __ldg(a.seq_lens + c.b)) : 0;
+  c.tiles = tiles_of(c.len);
+}
+
+__device__ __forceinline__ void advance(const Params& p, Cursor& c) {
+  if (++c.tile < c.tiles) return;
+  c.tile = 0;
+  if (++c.mt < p.mtiles) return;
+  c.mt = 0;
+  if (++c.h < p.a.Hkv) return;
+  c.h = 0;
+  ++c.b;
+  enter_seq(p.a, c);
+}
+
+__device__ __forceinline__ int item_of(const Params& p, const Cursor& c) {
+  return (c.b * p.a.Hkv + c.h) * p.mtiles + c.mt;
+}
+
+template <int D, bool kQuant>
+__global__ void __launch_bounds__(32 * kWarps, 1) decode_kernel(const Params p) {
+  using C = Cfg<D>;
+  extern __shared__ __align__(16) uint8_t smem[];
+  int* prefix = reinterpret_cast<int*>(smem + C::kSmem);
+  __shared__ int warp_sum[kWarps];
+  const DecodeArgs& a = p.a;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int g = lane >> 2, t = lane & 3;
+
+  // prefix[b] = units before sequence b
+  const int per_seq = a.Hkv * p.mtiles;
+  {
+    const int chunk = (a.B + 32 * kWarps - 1) / (32 * kWarps);
+    const int b0 = min(tid * chunk, a.B), b1 = min(b0 + chunk, a.B);
+    int sum = 0;
+    for (int b = b0; b < b1; ++b) {
+      const int len = __ldg(a.seq_lens + b);
+      const int ok = clamp_len(a, len);
+      if (len > ok) atomicOr(a.err, kErrBadPage);
+      sum += tiles_of(ok) * per_seq;
+    }
+    int inc = sum;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int x = __shfl_up_sync(0xffffffffu, inc, o);
+      if (lane >= o) inc += x;
+    }
+    if (lane == 31) warp_sum[warp] = inc;
+    __syncthreads();
+    int base = inc - sum;
+    for (int w = 0; w < warp; ++w) base += warp_sum[w];
+    for (int b = b0; b < b1; ++b) {
+      prefix[b] = base;
+      base += tiles_of(clamp_len(a, __ldg(a.seq_lens + b))) * per_seq;
+    }
+    if (tid == 32 * kWarps - 1) prefix[a.B] = base;
+    __syncthreads();
+  }
+  const int W = prefix[a.B];
+  Workspace<D>* ws = static_cast<Workspace<D>*>(a.ws);
+  // workers: as few warps per CTA as give every worker a unit, spread over the CTAs
+  const int per_cta = min(kWarps, (W + static_cast<int>(gridDim.x) - 1) / static_cast<int>(gridDim.x));
+  const int workers = min(W, per_cta * static_cast<int>(gridDim.x));
+  if (blockIdx.x == 0 && tid == 0) ws->workers = workers;
+  if (warp >= per_cta) return;
+  const int id = blockIdx.x * per_cta + warp;
+  if (id >= workers) return;
+  const int u0 = static_cast<int>(static_cast<long long>(W) * id / workers);
+  const int u1 = static_cast<int>(static_cast<long long>(W) * (id + 1) / workers);
+
+  Cursor cc;  // what is computed next
+  {
+    int lo = 0, hi = a.B;  // the last b with prefix[b] <= u0
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (prefix[mid] <= u0) lo = mid; else hi = mid;
+    }
+    cc.b = lo;
+    enter_seq(a, cc);
+    int u = u0 - prefix[lo];
+    cc.tile = u % cc.tiles;
+    u /= cc.tiles;
+    cc.mt = u % p.mtiles;
+    cc.h = u / p.mtiles;
+  }
+  Cursor pc = cc;  // what is loaded next
+  int pu = u0, ps = 0;
+  int pages = -1;  // lane l: the page of 16-key chunk 32 (tile / 8) + l
+  const uint32_t ring = sm100::smem_addr(smem) + warp * C::kRing;
+  uint32_t pslot = 0, cslot = 0;
+
+  // Issues the next slot's copies (or none, at the end) as one group.
+  auto produce = [&](bool fresh) {
+    if (pu < u1) {
+      if (ps == 0 && (fresh || (pc.tile & 7) == 0)) {
+        const int pos = ((pc.tile & ~7) * 4 + lane) * kChunk;
+        pages = -2;
+        if (pos < pc.len) {
+          pages = __ldg(a.table + static_cast<long long>(pc.b) * a.max_pages + (pos >> a.page_shift));
+          if (pages < 0 || pages >= a.num_pages) {
+            atomicOr(a.err, kErrBadPage);
+            pages = -1;
+          }
+        }
+      }
+      const int c = ps & 3;
+      const bool val = ps >= 4;
+      const int page = __shfl_sync(0xffffffffu, pages, (pc.tile & 7) * 4 + c);
+      const int row0 = pc.tile * kTile + c * kChunk;
+      const int rows = page >= 0 ? min(kChunk, pc.len - row0) : 0;
+      const size_t at = ((static_cast<size_t>(max(page, 0)) * a.Hkv + pc.h) << a.page_shift) +
+                        (row0 & ((1 << a.page_shift) - 1));
+      const uint8_t* src = (val ? a.v_codes : a.k_codes) + at * D;
+      const uint32_t dst = ring + pslot * C::kSlotBytes;
+#pragma unroll
+      for (int i = 0; i < D / 32; ++i) {
+        const int idx = lane + 32 * i;
+        const int r = idx / (D / 16), ch = idx % (D / 16);
+        cp_async16(dst + (val ? v_off<D>(r, ch) : k_off<D>(r, ch)), src + idx * 16, r < rows ? 16 : 0);
+      }
+      if (lane < 4) {
+        const float* sc = (val ? a.v_scales : a.k_scales) + at + 4 * lane;
+        const uint32_t d = dst + kChunk * D + 16 * lane;
+        if (page == -1) {  // no such page: its keys have no value
+          const uint32_t nan = 0x7fc00000u;
+          asm volatile("st.shared.v4.u32 [%0], {%1,%1,%1,%1};" ::"r"(d), "r"(nan) : "memory");
+        } else {
+          cp_async16(d, sc, 4 * min(max(rows - 4 * lane, 0), 4));
+        }
+      }
+      pslot = pslot + 1 == C::kSlots ? 0 : pslot + 1;
+      if (++ps == 8) {
+        ps = 0;
+        ++pu;
+        advance(p, pc);
+      }
+    }
+    cp_commit();
+  };
+  produce(true);
+#pragma unroll 1
+  for (int i = 1; i < C::kSlots - 1; ++i) produce(false);
+
+  // Waits for the next slot; returns its address.
+  auto consume = [&]() {
+    cp_wait<C::kSlots - 2>();
+    __syncwarp();
+    const uint32_t s = ring + cslot * C::kSlotBytes;
+    cslot = cslot + 1 == C::kSlots ? 0 : cslot + 1;
+    return s;
+  };
+
+  constexpr int KS = D / 16;   // k-steps of Q K^T
+  constexpr int NT = D / 8;    // n-tiles of P V
+  uint32_t qa[KS][4];
+  float o[NT][4];
+  float m[2], l[2], rf[2], vref = 0.f;
+  int last[2];                 // the newest key each of the lane's two rows sees
+  bool begun = false;
+  if (lane == 0) ws->meta[id] = WorkerMeta{-1, 0, -1, 0};
+  int first_tile = cc.tile;    // of the current segment
+
+  for (int u = u0; u < u1; ++u) {
+    if (!begun) {
+      begun = true;
+      first_tile = cc.tile;
+      // the item's query rows g and g + 8 as f16 times a power of two
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        const int r = cc.mt * kRows + g + 8 * x;
+        uint4 raw[D / 32];
+#pragma unroll
+        for (int i = 0; i < D / 32; ++i) raw[i] = make_uint4(0u, 0u, 0u, 0u);
+        if (r < p.R) {
+          const uint4* src = reinterpret_cast<const uint4*>(
+              a.q + ((static_cast<size_t>(cc.b) * a.Hkv + cc.h) * p.R + r) * D);
+#pragma unroll
+          for (int h = 0; h < D / 64; ++h) {
+            raw[2 * h] = __ldg(src + 8 * h + 2 * t);
+            raw[2 * h + 1] = __ldg(src + 8 * h + 2 * t + 1);
+          }
+        }
+        float amax = 0.f;
+#pragma unroll
+        for (int i = 0; i < D / 32; ++i) {
+          const __nv_bfloat162* b = reinterpret_cast<const __nv_bfloat162*>(&raw[i]);
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const float2 f = __bfloat1622float2(b[k]);
+            amax = fmaxf(amax, fmaxf(fabsf(f.x), fabsf(f.y)));
+          }
+        }
+        amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+        amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
+        // amax in [2^e, 2^(e+1)) goes to [2^14, 2^15)
+        int e = static_cast<int>(__float_as_uint(amax) >> 23) - 127;
+        e = min(max(e, -100), 126);
+        const float up = __uint_as_float(static_cast<uint32_t>(127 + 14 - e) << 23);
+        rf[x] = a.qk_scale * __uint_as_float(static_cast<uint32_t>(max(127 - 14 + e, 1)) << 23);
+#pragma unroll
+        for (int h = 0; h < D / 64; ++h) {
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const __nv_bfloat162* b = reinterpret_cast<const __nv_bfloat162*>(&raw[2 * h + i]);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const float2 f = __bfloat1622float2(b[k]);
+              qa[4 * h + 2 * i + (k >> 1)][2 * (k & 1) + x] = f16x2(f.x * up, f.y * up);
+            }
+          }
+        }
+        m[x] = -INFINITY;
+        l[x] = 0.f;
+        last[x] = cc.len - a.T + r % a.T;
+      }
+#pragma unroll
+      for (int j = 0; j < NT; ++j) o[j][0] = o[j][1] = o[j][2] = o[j][3] = 0.f;
+      vref = 0.f;
+    }
+
+    // S = Q K^T of 64 keys
+    float s[8][4];
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      const uint32_t slot = consume();
+#pragma unroll
+      for (int nt = 0; nt < 2; ++nt) {
+        float (&acc)[4] = s[2 * c + nt];
+        acc[0] = acc[1] = acc[2] = acc[3] = 0.f;
+#pragma unroll
+        for (int h = 0; h < D / 64; ++h) {
+          const uint4 w = lds128(slot + k_off<D>(8 * nt + g, t + 4 * h));
+          const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            mma16816(acc, qa[4 * h + i], codes_to_f16x2(static_cast<uint16_t>(ww[i])),
+                     codes_to_f16x2(static_cast<uint16_t>(ww[i] >> 16)));
+        }
+        const float2 ks = lds_f2(slot + kChunk * D + 4 * (8 * nt + 2 * t));
+        acc[0] *= ks.x * rf[0];
+        acc[1] *= ks.y * rf[0];
+        acc[2] *= ks.x * rf[1];
+        acc[3] *= ks.y * rf[1];
+      }
+      __syncwarp();
+      produce(false);
+    }
+
+    // mask: only tiles that reach past what some row sees
+    const int key0 = cc.tile * kTile;
+    const bool edge = key0 + kTile > cc.len - a.T + 1;
+    if (edge) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const int k = key0 + 8 * j + 2 * t;
+        if (k > last[0]) s[j][0] = -INFINITY;
+        if (k + 1 > last[0]) s[j][1] = -INFINITY;
+        if (k > last[1]) s[j][2] = -INFINITY;
+        if (k + 1 > last[1]) s[j][3] = -INFINITY;
+      }
+    }
+    float alpha[2], inv[2], back[2];
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
+      float mt = s[0][2 * x];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) mt = fmaxf(mt, fmaxf(s[j][2 * x], s[j][2 * x + 1]));
+      mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, 1));
+      mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, 2));
+      const float mn = fmaxf(m[x], mt);
+      const float ref = mn == -INFINITY ? 0.f : mn;
+      alpha[x] = ex2(m[x] - ref);
+      m[x] = mn;
+      float sum = 0.f;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        s[j][2 * x] = ex2(s[j][2 * x] - ref);
+        s[j][2 * x + 1] = ex2(s[j][2 * x + 1] - ref);
+        sum += s[j][2 * x] + s[j][2 * x + 1];
+      }
+      l[x] = l[x] * alpha[x] + sum;
+      if (kQuant) {  // the tile's largest p is that of its largest score
+        const float amax = ex2(mt - ref);
+        const TileScale ts = tile_scale(amax < kTinyP ? 0.f : amax);
+        inv[x] = ts.inv;
+        back[x] = ts.scale;
+      }
+    }
+    if (__any_sync(0xffffffffu, alpha[0] != 1.f || alpha[1] != 1.f)) {
+#pragma unroll
+      for (int j = 0; j < NT; ++j) {
+        o[j][0] *= alpha[0];
+        o[j][1] *= alpha[0];
+        o[j][2] *= alpha[1];
+        o[j][3] *= alpha[1];
+      }
+    }
+
+    // O += P V
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      const uint32_t slot = consume();
+      float2 vs[2];
+      vs[0] = lds_f2(slot + kChunk * D + 8 * t);
+      vs[1] = lds_f2(slot + kChunk * D + 32 + 8 * t);
+      float vmax = fmaxf(fmaxf(vs[0].x, vs[0].y), fmaxf(vs[1].x, vs[1].y));
+      vmax = fmaxf(vmax, __shfl_xor_sync(0xffffffffu, vmax, 1));
+      vmax = fmaxf(vmax, __shfl_xor_sync(0xffffffffu, vmax, 2));
+      if (vmax > vref) {  // a power of two above every scale so far; o is kept divided by it
+        const int e = min(max(static_cast<int>(__float_as_uint(vmax) >> 23) - 126, -100), 126);
+        const float nref = __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
+        const float f = vref / nref;
+        vref = nref;
+#pragma unroll
+        for (int j = 0; j < NT; ++j) {
+          o[j][0] *= f;
+          o[j][1] *= f;
+          o[j][2] *= f;
+          o[j][3] *= f;
+        }
+      }
+      const float unit = vref > 0.f ? kPTop / vref : 0.f;
+      uint32_t pa[4];
+#pragma unroll
+      for (int nt = 0; nt < 2; ++nt) {
+        const float fx = vs[nt].x * unit, fy = vs[nt].y * unit;
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          float p0 = s[2 * c + nt][2 * x], p1 = s[2 * c + nt][2 * x + 1];
+          if (kQuant) {
+            const float2 y = mul_rn_f32x2(make_float2(p0, p1), make_float2(inv[x], inv[x]));
+            const float2 d = mul_rn_f32x2(e4m3x2_decode(e4m3x2_rn_satfinite(y.x, y.y)),
+                                          make_float2(back[x], back[x]));
+            p0 = d.x;
+            p1 = d.y;
+          }
+          p0 *= fx;
+          p1 *= fy;
+          if (edge) {  // 0 x NaN: a key that the row does not see may hold anything
+            const int k = key0 + kChunk * c + 8 * nt + 2 * t;
+            if (k > last[x]) p0 = 0.f;
+            if (k + 1 > last[x]) p1 = 0.f;
+          }
+          pa[2 * nt + x] = f16x2(p0, p1);
+        }
+      }
+      if constexpr (D == 128) {
+        const uint4 v0 = lds128(slot + v_off<D>(2 * t, g)), v1 = lds128(slot + v_off<D>(2 * t + 1, g));
+        const uint4 v2 = lds128(slot + v_off<D>(2 * t + 8, g)), v3 = lds128(slot + v_off<D>(2 * t + 9, g));
+        const uint32_t w0[4] = {v0.x, v0.y, v0.z, v0.w}, w1[4] = {v1.x, v1.y, v1.z, v1.w};
+        const uint32_t w2[4] = {v2.x, v2.y, v2.z, v2.w}, w3[4] = {v3.x, v3.y, v3.z, v3.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const uint32_t a0 = __byte_perm(w0[i], w1[i], 0x5140), a1 = __byte_perm(w0[i], w1[i], 0x7362);
+          const uint32_t b0 = __byte_perm(w2[i], w3[i], 0x5140), b1 = __byte_perm(w2[i], w3[i], 0x7362);
+          mma16816(o[4 * i], pa, codes_to_f16x2(static_cast<uint16_t>(a0)), codes_to_f16x2(static_cast<uint16_t>(b0)));
+          mma16816(o[4 * i + 1], pa, codes_to_f16x2(static_cast<uint16_t>(a0 >> 16)), codes_to_f16x2(static_cast<uint16_t>(b0 >> 16)));
+          mma16816(o[4 * i + 2], pa, codes_to_f16x2(static_cast<uint16_t>(a1)), codes_to_f16x2(static_cast<uint16_t>(b1)));
+          mma16816(o[4 * i + 3], pa, codes_to_f16x2(static_cast<uint16_t>(a1 >> 16)), codes_to_f16x2(static_cast<uint16_t>(b1 >> 16)));
+        }
+      } else {
+        const uint32_t half8 = (g & 1) << 3;
+        const uint2 v0 = lds64(slot + v_off<D>(2 * t, g >> 1) + half8);
+        const uint2 v1 = lds64(slot + v_off<D>(2 * t + 1, g >> 1) + half8);
+        const uint2 v2 = lds64(slot + v_off<D>(2 * t + 8, g >> 1) + half8);
+        const uint2 v3 = lds64(slot + v_off<D>(2 * t + 9, g >> 1) + half8);
+        const uint32_t w0[2] = {v0.x, v0.y}, w1[2] = {v1.x, v1.y}, w2[2] = {v2.x, v2.y}, w3[2] = {v3.x, v3.y};
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const uint32_t a0 = __byte_perm(w0[i], w1[i], 0x5140), a1 = __byte_perm(w0[i], w1[i], 0x7362);
+          const uint32_t b0 = __byte_perm(w2[i], w3[i], 0x5140), b1 = __byte_perm(w2[i], w3[i], 0x7362);
+          mma16816(o[4 * i], pa, codes_to_f16x2(static_cast<uint16_t>(a0)), codes_to_f16x2(static_cast<uint16_t>(b0)));
+          mma16816(o[4 * i + 1], pa, codes_to_f16x2(static_cast<uint16_t>(a0 >> 16)), codes_to_f16x2(static_cast<uint16_t>(b0 >> 16)));
+          mma16816(o[4 * i + 2], pa, codes_to_f16x2(static_cast<uint16_t>(a1)), codes_to_f16x2(static_cast<uint16_t>(b1)));
+          mma16816(o[4 * i + 3], pa, codes_to_f16x2(static_cast<uint16_t>(a1 >> 16)), codes_to_f16x2(static_cast<uint16_t>(b1 >> 16)));
+        }
+      }
+      __syncwarp();
+      produce(false);
+    }
+
+    const bool ends = cc.tile + 1 == cc.tiles;
+    if (ends || u + 1 == u1) {  // the segment's end
+      begun = false;
+      const float unit = vref * (1.f / kPTop);
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        l[x] += __shfl_xor_sync(0xffffffffu, l[x], 1);
+        l[x] += __shfl_xor_sync(0xffffffffu, l[x], 2);
+      }
+      if (first_tile == 0 && ends) {  // the whole item: its output
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          const int r = cc.mt * kRows + g + 8 * x;
+          if (r >= p.R) continue;
+          const size_t row = (static_cast<size_t>(cc.b) * a.Hkv + cc.h) * p.R + r;
+          const bool none = l[x] == 0.f;
+          const float f = none ? 0.f : unit / l[x];
+          // columns 2t and 2t + 1 of n-tile j are channels NT (2t) + j and NT (2t + 1) + j
+          uint32_t w[NT];
+#pragma unroll
+          for (int y = 0; y < 2; ++y)
+#pragma unroll
+            for (int j = 0; j < NT / 2; ++j) {
+              const float lo = none ? 0.f : o[2 * j][2 * x + y] * f;
+              const float hi = none ? 0.f : o[2 * j + 1][2 * x + y] * f;
+              const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+              w[y * NT / 2 + j] = *reinterpret_cast<const uint32_t*>(&v);
+            }
+          uint4* dst = reinterpret_cast<uint4*>(a.o + row * D + 2 * NT * t);
+#pragma unroll
+          for (int j = 0; j < NT / 4; ++j)
+            dst[j] = make_uint4(w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
+          if (t == 0 && a.lse != nullptr) a.lse[row] = none ? -INFINITY : m[x] + log2f(l[x]);
+        }
+      } else {
+        const bool head = first_tile != 0;
+        Partial<D>& part = ws->part[id][head ? 0 : 1];
+        if (lane == 0) {
+          if (head) {
+            ws->meta[id].head = item_of(p, cc);
+            ws->meta[id].head_done = ends;
+          } else {
+            ws->meta[id].tail = item_of(p, cc);
+          }
+        }
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          const int r = g + 8 * x;
+          if (cc.mt * kRows + r >= p.R) continue;
+          if (t == 0) *reinterpret_cast<float2*>(part.ml[r]) = make_float2(m[x], l[x]);
+#pragma unroll
+          for (int y = 0; y < 2; ++y)
+#pragma unroll
+            for (int j = 0; j < NT / 4; ++j)
+              *reinterpret_cast<float4*>(&part.o[r][NT * (2 * t + y) + 4 * j]) =
+                  make_float4(o[4 * j][2 * x + y] * unit, o[4 * j + 1][2 * x + y] * unit,
+                              o[4 * j + 2][2 * x + y] * unit, o[4 * j + 3][2 * x + y] * unit);
+        }
+      }
+    }
+    advance(p, cc);
+  }
+  cp_wait<0>();
+}
+
+// Adds the partials of the items that ranges cut: block w takes the item that worker w's range
+// begins and does not end (if there is one), one warp per row, D / 32 channels per lane, in worker
+// order.
+template <int D>
+__global__ void __launch_bounds__(32 * kRows) decode_merge_kernel(const Params p) {
+  constexpr int V = D / 32;
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // the partials are complete
+  const Workspace<D>* ws = static_cast<const Workspace<D>*>(p.a.ws);
+  const int w = blockIdx.x, lane = threadIdx.x & 31, r = threadIdx.x >> 5;
+  const int workers = ws->workers;
+  if (w >= workers) return;
+  const int item = ws->meta[w].tail;
+  if (item < 0) return;
+  const int mt = item % p.mtiles;
+  if (mt * kRows + r >= p.R) return;
+  const Partial<D>* part = &ws->part[w][1];
+  float m = part->ml[r][0], l = part->ml[r][1];
+  float acc[V];
+#pragma unroll
+  for (int i = 0; i < V; ++i) acc[i] = part->o[r][V * lane + i];
+  for (int x = w + 1; x < workers; ++x) {
+    part = &ws->part[x][0];
+    const float m2 = part->ml[r][0], l2 = part->ml[r][1];
+    const float mn = fmaxf(m, m2);
+    const float ref = mn == -INFINITY ? 0.f : mn;
+    const float f = ex2(m - ref), f2 = ex2(m2 - ref);
+    m = mn;
+    l = l * f + l2 * f2;
+#pragma unroll
+    for (int i = 0; i < V; ++i) acc[i] = acc[i] * f + part->o[r][V * lane + i] * f2;
+    if (ws->meta[x].head_done) break;
+  }
+  const size_t row = static_cast<size_t>(item / p.mtiles) * p.R + mt * kRows + r;
+  const bool none = l == 0.f;
+  const float f = none ? 0.f : 1.f / l;
+  uint32_t out[V / 2];
+#pragma unroll
+  for (int i = 0; i < V / 2; ++i) {
+    const __nv_bfloat162 v = __floats2bfloat162_rn(none ? 0.f : acc[2 * i] * f, none ? 0.f : acc[2 * i + 1] * f);
+    out[i] = *reinterpret_cast<const uint32_t*>(&v);
+  }
+  uint16_t* dst = p.a.o + row * D + V * lane;
+  if constexpr (V == 4)
+    *reinterpret_cast<uint2*>(dst) = make_uint2(out[0], out[1]);
+  else
+    *reinterpret_cast<uint32_t*>(dst) = out[0];
+  if (lane == 0 && p.a.lse != nullptr) p.a.lse[row] = none ? -INFINITY : m + log2f(l);
+}
+
+template <int D, bool kQuant>
+cudaError_t run(const Params& p, int ctas, cudaStream_t s) {
+  const size_t smem = Cfg<D>::kSmem + sizeof(int) * (p.a.B + 1);
+  cudaError_t e = cudaFuncSetAttribute(decode_kernel<D, kQuant>,
+                                       cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       static_cast<int>(smem));
+  if (e != cudaSuccess) return e;
+  decode_kernel<D, kQuant><<<ctas, 32 * kWarps, smem, s>>>(p);
+  e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(ctas * kWarps);
+  cfg.blockDim = dim3(32 * kRows);
+  cfg.stream = s;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, decode_merge_kernel<D>, p);
+}
+
+}  // namespace
+
+size_t decode_workspace_bytes(int D) {
+  return D == 64 ? sizeof(Workspace<64>) : sizeof(Workspace<128>);
+}
+
+cudaError_t launch_decode(const DecodeArgs& a, int D, int num_sms, cudaStream_t s) {
+  Params p;
+  p.a = a;
+  p.R = a.Hq / a.Hkv * a.T;
+  p.mtiles = (p.R + kRows - 1) / kRows;
+  // one CTA per SM, fewer when the table cannot hold a unit for each
+  const long long cap = static_cast<long long>(a.max_pages) << a.page_shift;
+  const long long units = static_cast<long long>(a.B) * a.Hkv * p.mtiles * ((cap + kTile - 1) / kTile);  // >= 1
+  int ctas = num_sms < kMaxCtas ? num_sms : kMaxCtas;
+  if (units < ctas) ctas = static_cast<int>(units);
+  if (D == 64) return a.quant ? run<64, true>(p, ctas, s) : run<64, false>(p, ctas, s);
+  return a.quant ? run<128, true>(p, ctas, s) : run<128, false>(p, ctas, s);
+}
+
+}  // namespace qat

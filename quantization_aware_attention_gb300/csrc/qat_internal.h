@@ -155,7 +155,80 @@ struct BwdArgs {
   int page_bwd;     // 1: dV from quantized P and Delta from the O passed (O_q)
 };
 
+// Bits of the device error word: a bounded wait expired; a page index or a sequence length that
+// the cache or its table cannot hold.
+constexpr unsigned int kErrTimeout = 1u;
+constexpr unsigned int kErrBadPage = 2u;
+
+// One of the two tensors of the norm + rotation pass ([B, H, N, D] by element strides; D
+// innermost).  H = 0: absent.
+struct NormRopeTensor {
+  const uint16_t* x;
+  long long sb, sh, sn;
+  const uint16_t* dy;  // backward only
+  long long dy_sb, dy_sh, dy_sn;
+  uint16_t* y;         // forward: contiguous output; backward: dx with the strides below
+  long long y_sb, y_sh, y_sn;
+  const void* w;       // [D] or null: no norm
+  void* dw;            // [D] or null
+  int H;
+};
+
+struct NormRopeArgs {
+  NormRopeTensor q, k;
+  const int* positions;
+  long long pos_sb;
+  const unsigned long long* phases;  // [R / 2]
+  int B, N, R, interleaved, w_bf16;
+  long long tokens;                  // B * N
+  float amplitude, eps;
+  float* part;                       // backward: [blocks][D]
+  // work split, filled in by the launcher
+  int heads_per_part, q_parts, parts, q_blocks;
+};
+
+// Most blocks of the backward of the norm + rotation (its workspace holds D sums for each).
+constexpr int kNormRopeBwdBlocks = 608;  // 152 SMs x 4
+
+// Append to and read from the FP8 cache.
+struct KvCacheArgs {
+  const uint16_t *k, *v;             // append: [B, H, N, D] by element strides
+  long long k_sb, k_sh, k_sn, v_sb, v_sh, v_sn;
+  uint16_t *k_out, *v_out;           // read: contiguous [B, H, N, D]
+  uint8_t *k_codes, *v_codes;        // [pages, H, page, D]
+  float *k_scales, *v_scales;        // [pages, H, page]
+  const int* table;                  // [B, max_pages]
+  const int* seq_lens;               // [B]
+  const int* new_lens;               // append: [B] or null
+  unsigned int* err;
+  int B, H, N, begin, num_pages, page_shift, max_pages;
+};
+
+// The attention of a few new tokens over the FP8 cache.
+struct DecodeArgs {
+  const uint16_t* q;                 // [B, Hq, T, D]
+  const uint8_t *k_codes, *v_codes;
+  const float *k_scales, *v_scales;
+  const int* table;
+  const int* seq_lens;
+  uint16_t* o;                       // [B, Hq, T, D]
+  float* lse;                        // [B, Hq, T] or null
+  void* ws;
+  unsigned int* err;
+  int B, Hq, Hkv, T, num_pages, page_shift, max_pages, quant;
+  float qk_scale;                    // sm_scale * log2(e)
+};
+
+constexpr int kDecodeMaxBatch = 4096;  // the kernel keeps the batch's prefix sums in shared memory
+constexpr int kDecodeMaxTokens = 16;
+size_t decode_workspace_bytes(int D);
+
 // Kernel launchers (return cudaGetLastError() after the launches).
+cudaError_t launch_norm_rope(NormRopeArgs a, int D, int num_sms, cudaStream_t s);
+cudaError_t launch_norm_rope_bwd(NormRopeArgs a, int D, int num_sms, cudaStream_t s);
+cudaError_t launch_kv_append(const KvCacheArgs& a, int D, cudaStream_t s);
+cudaError_t launch_kv_read(const KvCacheArgs& a, int D, cudaStream_t s);
+cudaError_t launch_decode(const DecodeArgs& a, int D, int num_sms, cudaStream_t s);
 cudaError_t launch_fwd_tc(const FwdArgs& a, unsigned int* err, int num_sms, cudaStream_t s);
 // prep + dK/dV + dQ kernels
 cudaError_t launch_bwd_tc(const BwdArgs& a, unsigned int* err, int num_sms, cudaStream_t s);
