@@ -357,7 +357,8 @@ QAT_API qat_status_t qat_qk_norm_rope_bwd(
  *   contiguous, bf16_RN(fl32(code scale)); zeros behind a sequence's end; NaN on a page outside
  *   the cache.
  * Errors: QAT_ERR_INVALID_ARG (null or misaligned pointer, bad size, stride or D),
- *   QAT_ERR_UNSUPPORTED (another page size; max_pages * page_size above 2^30), QAT_ERR_CUDA.
+ *   QAT_ERR_UNSUPPORTED (another page size; max_pages * page_size above 2^30, or a cache of
+ *   more than 2^32 - 296 rows), QAT_ERR_CUDA.
  */
 QAT_API qat_status_t qat_kv_cache_append(const void* k, const long long* k_strides, const void* v,
                                          const long long* v_strides, void* k_codes, void* v_codes,

@@ -8,7 +8,7 @@
 //
 // What bounds it: the cache is read once, 2 (D + 4) bytes per key and KV head, and every byte
 // meets at most 16 query rows, so HBM does.  The kernel is built around keeping loads in flight:
-// every warp is its own worker with its own ring of 16-key slots filled by cp.async, no barrier
+// every warp is its own worker with its own ring of K and V tiles filled by cp.async, no barrier
 // between warps, and all G = Hq / Hkv heads that share a KV head (times T tokens) are rows of one
 // 16-row tile, so that the cache is read once for all of them.
 //
@@ -39,23 +39,26 @@
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
+#include <type_traits>
+
 namespace qat {
 namespace {
 
 constexpr int kWarps = 8;
 constexpr int kTile = 64;    // keys per unit
-constexpr int kChunk = 16;   // keys per slot
+constexpr int kChunk = 16;   // keys that certainly share a page
 constexpr int kRows = 16;    // query rows per item
 constexpr int kMaxCtas = 152;
 constexpr int kWorkers = kMaxCtas * kWarps;
 constexpr float kTinyP = 7.888609052210118e-31f;  // 2^-100: a tile below it counts as zero (448 / amax
                                                   // must stay finite)
 constexpr float kPTop = 16384.f;  // P x value scale / bound is at most this
+constexpr uint32_t kNoPage = 0xffffffffu, kBadPage = 0xfffffffeu;
 
 template <int D>
 struct Cfg {
-  static constexpr int kSlots = D == 128 ? 12 : 24;
-  static constexpr int kSlotBytes = kChunk * D + 4 * kChunk;  // codes, then scales
+  static constexpr int kSlots = D == 128 ? 3 : 6;             // K or V of one tile each
+  static constexpr int kSlotBytes = kTile * D + 4 * kTile;    // codes, then scales
   static constexpr int kRing = kSlots * kSlotBytes;
   static constexpr int kSmem = kWarps * kRing;  // then B + 1 prefix sums
 };
@@ -111,7 +114,10 @@ __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], 
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-// 16 bytes into shared memory, the first `bytes` from global memory and zeros behind them.
+// 16 bytes into shared memory; with `bytes`, that many from global memory and zeros behind them.
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, int bytes) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes)
                : "memory");
@@ -138,7 +144,7 @@ __device__ __forceinline__ float2 lds_f2(uint32_t a) {
   return make_float2(__uint_as_float(v.x), __uint_as_float(v.y));
 }
 
-// Byte offset of 16-byte chunk c of row r in a slot of K or V codes.
+// Byte offset of 16-byte chunk c of row r in 16 rows of K or V codes.
 template <int D>
 __device__ __forceinline__ uint32_t k_off(int r, int c) {
   return D == 128 ? r * 128 + ((c ^ ((r & 1) << 2)) << 4) : r * 64 + (c << 4);
@@ -178,6 +184,69 @@ __device__ __forceinline__ void advance(const Params& p, Cursor& c) {
 
 __device__ __forceinline__ int item_of(const Params& p, const Cursor& c) {
   return (c.b * p.a.Hkv + c.h) * p.mtiles + c.mt;
+}
+
+// The item's query rows g and g + 8 as f16 times a power of two (exact for all that matters), in the
+// order of the K fragments, and what their scores are to be multiplied by.
+template <int D>
+__device__ __forceinline__ void load_rows(const Params& p, const Cursor& c, int g, int t,
+                                          uint32_t (&qa)[D / 16][4], float (&rf)[2]) {
+#pragma unroll
+  for (int x = 0; x < 2; ++x) {
+    const int r = c.mt * kRows + g + 8 * x;
+    uint4 raw[D / 32];
+#pragma unroll
+    for (int i = 0; i < D / 32; ++i) raw[i] = make_uint4(0u, 0u, 0u, 0u);
+    if (r < p.R) {
+      const uint4* src = reinterpret_cast<const uint4*>(
+          p.a.q + ((static_cast<size_t>(c.b) * p.a.Hkv + c.h) * p.R + r) * D);
+#pragma unroll
+      for (int h = 0; h < D / 64; ++h) {
+        raw[2 * h] = __ldg(src + 8 * h + 2 * t);
+        raw[2 * h + 1] = __ldg(src + 8 * h + 2 * t + 1);
+      }
+    }
+    float amax = 0.f;
+#pragma unroll
+    for (int i = 0; i < D / 32; ++i) {
+      const __nv_bfloat162* b = reinterpret_cast<const __nv_bfloat162*>(&raw[i]);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const float2 f = __bfloat1622float2(b[k]);
+        amax = fmaxf(amax, fmaxf(fabsf(f.x), fabsf(f.y)));
+      }
+    }
+    amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+    amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
+    // amax in [2^e, 2^(e+1)) goes to [2^14, 2^15)
+    int e = static_cast<int>(__float_as_uint(amax) >> 23) - 127;
+    e = min(max(e, -100), 126);
+    const float up = __uint_as_float(static_cast<uint32_t>(127 + 14 - e) << 23);
+    rf[x] = fmaxf(p.a.qk_scale * __uint_as_float(static_cast<uint32_t>(127 - 14 + e) << 23),
+                  1.1754943508222875e-38f);  // not zero: it multiplies -inf
+#pragma unroll
+    for (int h = 0; h < D / 64; ++h) {
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const __nv_bfloat162* b = reinterpret_cast<const __nv_bfloat162*>(&raw[2 * h + i]);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const float2 f = __bfloat1622float2(b[k]);
+          qa[4 * h + 2 * i + (k >> 1)][2 * (k & 1) + x] = f16x2(f.x * up, f.y * up);
+        }
+      }
+    }
+  }
+}
+
+template <int NT>
+__device__ __forceinline__ void scale_rows(float (&o)[NT][4], float f0, float f1) {
+#pragma unroll
+  for (int j = 0; j < NT; ++j) {
+    const float2 a = mul_rn_f32x2(make_float2(o[j][0], o[j][1]), make_float2(f0, f0));
+    const float2 b = mul_rn_f32x2(make_float2(o[j][2], o[j][3]), make_float2(f1, f1));
+    o[j][0] = a.x; o[j][1] = a.y; o[j][2] = b.x; o[j][3] = b.y;
+  }
 }
 
 template <int D, bool kQuant>
@@ -247,66 +316,93 @@ __global__ void __launch_bounds__(32 * kWarps, 1) decode_kernel(const Params p) 
     cc.h = u / p.mtiles;
   }
   Cursor pc = cc;  // what is loaded next
-  int pu = u0, ps = 0;
-  int pages = -1;  // lane l: the page of 16-key chunk 32 (tile / 8) + l
+  int pu = u0;
+  uint32_t rows_of = kNoPage;  // lane l: cache row where 16-key chunk 32 (tile / 8) + l begins
+  bool all_good = false;       // no chunk of those lies on a bad page
   const uint32_t ring = sm100::smem_addr(smem) + warp * C::kRing;
   uint32_t pslot = 0, cslot = 0;
+  // The lane's part of every copy: bytes 16 lane.. of each 512-byte run, by their swizzled places.
+  const uint32_t k_dst = k_off<D>(lane / (D / 16), lane % (D / 16));
+  const uint32_t v_dst0 = v_off<D>(lane / (D / 16), lane % (D / 16));
+  const uint32_t v_dst1 = v_off<D>(lane / (D / 16) + 512 / D, lane % (D / 16)) - 512;
 
-  // Issues the next slot's copies (or none, at the end) as one group.
-  auto produce = [&](bool fresh) {
+  // Issues the copies of the next K (or V) tile as one group; an empty group at the end.
+  auto produce = [&](auto is_v, bool fresh) {
+    constexpr bool kV = decltype(is_v)::value;
     if (pu < u1) {
-      if (ps == 0 && (fresh || (pc.tile & 7) == 0)) {
+      if (!kV && (fresh || (pc.tile & 7) == 0)) {
         const int pos = ((pc.tile & ~7) * 4 + lane) * kChunk;
-        pages = -2;
+        rows_of = kNoPage;
         if (pos < pc.len) {
-          pages = __ldg(a.table + static_cast<long long>(pc.b) * a.max_pages + (pos >> a.page_shift));
-          if (pages < 0 || pages >= a.num_pages) {
+          const int page = __ldg(a.table + static_cast<long long>(pc.b) * a.max_pages + (pos >> a.page_shift));
+          rows_of = kBadPage;
+          if (page >= 0 && page < a.num_pages)
+            rows_of = ((static_cast<uint32_t>(page) * a.Hkv + pc.h) << a.page_shift) +
+                      (pos & ((1 << a.page_shift) - 1));
+          else
             atomicOr(a.err, kErrBadPage);
-            pages = -1;
+        }
+        all_good = !__any_sync(0xffffffffu, rows_of == kBadPage);
+      }
+      const uint8_t* codes = (kV ? a.v_codes : a.k_codes) + 16 * lane;
+      const float* scales = kV ? a.v_scales : a.k_scales;
+      const uint32_t dst = ring + pslot * C::kSlotBytes;
+      const int first = (pc.tile & 7) * 4;
+      const uint32_t sc_row = __shfl_sync(0xffffffffu, rows_of, first + (lane >> 2 & 3)) + 4 * (lane & 3);
+      const uint32_t sc_dst = dst + kTile * D + 16 * lane;
+      const int left = pc.len - pc.tile * kTile;  // the sequence's keys from the tile's first on
+      if (left >= kTile && all_good) {
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          const uint8_t* src = codes + static_cast<size_t>(__shfl_sync(0xffffffffu, rows_of, first + c)) * D;
+#pragma unroll
+          for (int i = 0; i < D / 32; ++i) {
+            const uint32_t off = kV ? ((i & 1) ? v_dst1 : v_dst0) : k_dst;
+            cp_async16(dst + off + c * kChunk * D + i * 512, src + i * 512);
+          }
+        }
+        if (lane < 16) cp_async16(sc_dst, scales + sc_row);
+      } else {  // zeros behind the end, and for bad pages zeros with scale NaN
+#pragma unroll 1
+        for (int c = 0; c < 4; ++c) {
+          const uint32_t row = __shfl_sync(0xffffffffu, rows_of, first + c);
+          const int n = row < kBadPage ? left - c * kChunk : 0;
+          const uint8_t* src = codes + (row < kBadPage ? static_cast<size_t>(row) * D : 0);
+#pragma unroll 1
+          for (int i = 0; i < D / 32; ++i) {
+            const uint32_t off = kV ? ((i & 1) ? v_dst1 : v_dst0) : k_dst;
+            const int r = lane / (D / 16) + i * (512 / D);
+            cp_async16(dst + off + c * kChunk * D + i * 512, r < n ? src + i * 512 : codes, r < n ? 16 : 0);
+          }
+        }
+        if (lane < 16) {
+          const uint32_t row = sc_row - 4 * (lane & 3);
+          if (row == kBadPage) {
+            asm volatile("st.shared.v4.u32 [%0], {%1,%1,%1,%1};" ::"r"(sc_dst), "r"(0x7fc00000u) : "memory");
+          } else {
+            const int n = row == kNoPage ? 0 : min(max(left - 4 * lane, 0), 4);
+            cp_async16(sc_dst, n > 0 ? scales + sc_row : scales, 4 * n);
           }
         }
       }
-      const int c = ps & 3;
-      const bool val = ps >= 4;
-      const int page = __shfl_sync(0xffffffffu, pages, (pc.tile & 7) * 4 + c);
-      const int row0 = pc.tile * kTile + c * kChunk;
-      const int rows = page >= 0 ? min(kChunk, pc.len - row0) : 0;
-      const size_t at = ((static_cast<size_t>(max(page, 0)) * a.Hkv + pc.h) << a.page_shift) +
-                        (row0 & ((1 << a.page_shift) - 1));
-      const uint8_t* src = (val ? a.v_codes : a.k_codes) + at * D;
-      const uint32_t dst = ring + pslot * C::kSlotBytes;
-#pragma unroll
-      for (int i = 0; i < D / 32; ++i) {
-        const int idx = lane + 32 * i;
-        const int r = idx / (D / 16), ch = idx % (D / 16);
-        cp_async16(dst + (val ? v_off<D>(r, ch) : k_off<D>(r, ch)), src + idx * 16, r < rows ? 16 : 0);
-      }
-      if (lane < 4) {
-        const float* sc = (val ? a.v_scales : a.k_scales) + at + 4 * lane;
-        const uint32_t d = dst + kChunk * D + 16 * lane;
-        if (page == -1) {  // no such page: its keys have no value
-          const uint32_t nan = 0x7fc00000u;
-          asm volatile("st.shared.v4.u32 [%0], {%1,%1,%1,%1};" ::"r"(d), "r"(nan) : "memory");
-        } else {
-          cp_async16(d, sc, 4 * min(max(rows - 4 * lane, 0), 4));
-        }
-      }
       pslot = pslot + 1 == C::kSlots ? 0 : pslot + 1;
-      if (++ps == 8) {
-        ps = 0;
+      if (kV) {
         ++pu;
         advance(p, pc);
       }
     }
     cp_commit();
   };
-  produce(true);
+  using K = std::false_type;
+  using V = std::true_type;
 #pragma unroll 1
-  for (int i = 1; i < C::kSlots - 1; ++i) produce(false);
+  for (int i = 0; i < C::kSlots; ++i) {
+    if (i & 1) produce(V{}, false); else produce(K{}, i == 0);
+  }
 
-  // Waits for the next slot; returns its address.
+  // Waits for the oldest slot; returns its address.
   auto consume = [&]() {
-    cp_wait<C::kSlots - 2>();
+    cp_wait<C::kSlots - 1>();
     __syncwarp();
     const uint32_t s = ring + cslot * C::kSlotBytes;
     cslot = cslot + 1 == C::kSlots ? 0 : cslot + 1;
@@ -327,86 +423,53 @@ __global__ void __launch_bounds__(32 * kWarps, 1) decode_kernel(const Params p) 
     if (!begun) {
       begun = true;
       first_tile = cc.tile;
-      // the item's query rows g and g + 8 as f16 times a power of two
+      load_rows<D>(p, cc, g, t, qa, rf);
 #pragma unroll
       for (int x = 0; x < 2; ++x) {
-        const int r = cc.mt * kRows + g + 8 * x;
-        uint4 raw[D / 32];
-#pragma unroll
-        for (int i = 0; i < D / 32; ++i) raw[i] = make_uint4(0u, 0u, 0u, 0u);
-        if (r < p.R) {
-          const uint4* src = reinterpret_cast<const uint4*>(
-              a.q + ((static_cast<size_t>(cc.b) * a.Hkv + cc.h) * p.R + r) * D);
-#pragma unroll
-          for (int h = 0; h < D / 64; ++h) {
-            raw[2 * h] = __ldg(src + 8 * h + 2 * t);
-            raw[2 * h + 1] = __ldg(src + 8 * h + 2 * t + 1);
-          }
-        }
-        float amax = 0.f;
-#pragma unroll
-        for (int i = 0; i < D / 32; ++i) {
-          const __nv_bfloat162* b = reinterpret_cast<const __nv_bfloat162*>(&raw[i]);
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const float2 f = __bfloat1622float2(b[k]);
-            amax = fmaxf(amax, fmaxf(fabsf(f.x), fabsf(f.y)));
-          }
-        }
-        amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
-        amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
-        // amax in [2^e, 2^(e+1)) goes to [2^14, 2^15)
-        int e = static_cast<int>(__float_as_uint(amax) >> 23) - 127;
-        e = min(max(e, -100), 126);
-        const float up = __uint_as_float(static_cast<uint32_t>(127 + 14 - e) << 23);
-        rf[x] = a.qk_scale * __uint_as_float(static_cast<uint32_t>(max(127 - 14 + e, 1)) << 23);
-#pragma unroll
-        for (int h = 0; h < D / 64; ++h) {
-#pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            const __nv_bfloat162* b = reinterpret_cast<const __nv_bfloat162*>(&raw[2 * h + i]);
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              const float2 f = __bfloat1622float2(b[k]);
-              qa[4 * h + 2 * i + (k >> 1)][2 * (k & 1) + x] = f16x2(f.x * up, f.y * up);
-            }
-          }
-        }
         m[x] = -INFINITY;
         l[x] = 0.f;
-        last[x] = cc.len - a.T + r % a.T;
+        last[x] = cc.len - a.T + (cc.mt * kRows + g + 8 * x) % a.T;
       }
 #pragma unroll
       for (int j = 0; j < NT; ++j) o[j][0] = o[j][1] = o[j][2] = o[j][3] = 0.f;
       vref = 0.f;
     }
 
-    // S = Q K^T of 64 keys
+    // S = Q K^T of 64 keys, times the keys' scales (and, below, the rows')
     float s[8][4];
-#pragma unroll
-    for (int c = 0; c < 4; ++c) {
+    {
       const uint32_t slot = consume();
 #pragma unroll
-      for (int nt = 0; nt < 2; ++nt) {
-        float (&acc)[4] = s[2 * c + nt];
-        acc[0] = acc[1] = acc[2] = acc[3] = 0.f;
+      for (int c = 0; c < 2; ++c) {  // 32 keys: four independent chains of products
+#pragma unroll
+        for (int nt = 0; nt < 4; ++nt)
+          s[4 * c + nt][0] = s[4 * c + nt][1] = s[4 * c + nt][2] = s[4 * c + nt][3] = 0.f;
 #pragma unroll
         for (int h = 0; h < D / 64; ++h) {
-          const uint4 w = lds128(slot + k_off<D>(8 * nt + g, t + 4 * h));
-          const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
+          uint32_t w[4][4];
+#pragma unroll
+          for (int nt = 0; nt < 4; ++nt) {
+            const uint4 x = lds128(slot + (4 * c + nt) * 8 * D + k_off<D>(g, t + 4 * h));
+            w[nt][0] = x.x; w[nt][1] = x.y; w[nt][2] = x.z; w[nt][3] = x.w;
+          }
 #pragma unroll
           for (int i = 0; i < 4; ++i)
-            mma16816(acc, qa[4 * h + i], codes_to_f16x2(static_cast<uint16_t>(ww[i])),
-                     codes_to_f16x2(static_cast<uint16_t>(ww[i] >> 16)));
+#pragma unroll
+            for (int nt = 0; nt < 4; ++nt)
+              mma16816(s[4 * c + nt], qa[4 * h + i], codes_to_f16x2(static_cast<uint16_t>(w[nt][i])),
+                       codes_to_f16x2(static_cast<uint16_t>(w[nt][i] >> 16)));
         }
-        const float2 ks = lds_f2(slot + kChunk * D + 4 * (8 * nt + 2 * t));
-        acc[0] *= ks.x * rf[0];
-        acc[1] *= ks.y * rf[0];
-        acc[2] *= ks.x * rf[1];
-        acc[3] *= ks.y * rf[1];
+#pragma unroll
+        for (int nt = 0; nt < 4; ++nt) {
+          float (&acc)[4] = s[4 * c + nt];
+          const float2 ks = lds_f2(slot + kTile * D + 4 * (8 * (4 * c + nt) + 2 * t));
+          const float2 y0 = mul_rn_f32x2(make_float2(acc[0], acc[1]), ks);
+          const float2 y1 = mul_rn_f32x2(make_float2(acc[2], acc[3]), ks);
+          acc[0] = y0.x; acc[1] = y0.y; acc[2] = y1.x; acc[3] = y1.y;
+        }
       }
       __syncwarp();
-      produce(false);
+      if constexpr (C::kSlots & 1) produce(V{}, false); else produce(K{}, false);
     }
 
     // mask: only tiles that reach past what some row sees
@@ -430,108 +493,92 @@ __global__ void __launch_bounds__(32 * kWarps, 1) decode_kernel(const Params p) 
       for (int j = 0; j < 8; ++j) mt = fmaxf(mt, fmaxf(s[j][2 * x], s[j][2 * x + 1]));
       mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, 1));
       mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, 2));
-      const float mn = fmaxf(m[x], mt);
+      const float mn = fmaxf(m[x], mt * rf[x]);
       const float ref = mn == -INFINITY ? 0.f : mn;
       alpha[x] = ex2(m[x] - ref);
       m[x] = mn;
-      float sum = 0.f;
+      const float2 r2 = make_float2(rf[x], rf[x]), n2 = make_float2(-ref, -ref);
+      float2 sum = make_float2(0.f, 0.f);
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        s[j][2 * x] = ex2(s[j][2 * x] - ref);
-        s[j][2 * x + 1] = ex2(s[j][2 * x + 1] - ref);
-        sum += s[j][2 * x] + s[j][2 * x + 1];
+        const float2 e = fma_rn_f32x2(make_float2(s[j][2 * x], s[j][2 * x + 1]), r2, n2);
+        const float2 pp = make_float2(ex2(e.x), ex2(e.y));
+        s[j][2 * x] = pp.x;
+        s[j][2 * x + 1] = pp.y;
+        sum = add_rn_f32x2(sum, pp);
       }
-      l[x] = l[x] * alpha[x] + sum;
+      l[x] = l[x] * alpha[x] + (sum.x + sum.y);
       if (kQuant) {  // the tile's largest p is that of its largest score
-        const float amax = ex2(mt - ref);
+        const float amax = ex2(__fmaf_rn(mt, rf[x], -ref));
         const TileScale ts = tile_scale(amax < kTinyP ? 0.f : amax);
         inv[x] = ts.inv;
         back[x] = ts.scale;
       }
     }
-    if (__any_sync(0xffffffffu, alpha[0] != 1.f || alpha[1] != 1.f)) {
-#pragma unroll
-      for (int j = 0; j < NT; ++j) {
-        o[j][0] *= alpha[0];
-        o[j][1] *= alpha[0];
-        o[j][2] *= alpha[1];
-        o[j][3] *= alpha[1];
-      }
-    }
+    if (__any_sync(0xffffffffu, alpha[0] != 1.f || alpha[1] != 1.f)) scale_rows<NT>(o, alpha[0], alpha[1]);
 
     // O += P V
-#pragma unroll
-    for (int c = 0; c < 4; ++c) {
+    {
       const uint32_t slot = consume();
-      float2 vs[2];
-      vs[0] = lds_f2(slot + kChunk * D + 8 * t);
-      vs[1] = lds_f2(slot + kChunk * D + 32 + 8 * t);
-      float vmax = fmaxf(fmaxf(vs[0].x, vs[0].y), fmaxf(vs[1].x, vs[1].y));
+      const uint32_t sc = slot + kTile * D + 8 * t;
+      float vmax = 0.f;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const float2 v = lds_f2(sc + 32 * j);
+        vmax = fmaxf(vmax, fmaxf(v.x, v.y));
+      }
       vmax = fmaxf(vmax, __shfl_xor_sync(0xffffffffu, vmax, 1));
       vmax = fmaxf(vmax, __shfl_xor_sync(0xffffffffu, vmax, 2));
       if (vmax > vref) {  // a power of two above every scale so far; o is kept divided by it
         const int e = min(max(static_cast<int>(__float_as_uint(vmax) >> 23) - 126, -100), 126);
         const float nref = __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
-        const float f = vref / nref;
+        scale_rows<NT>(o, vref / nref, vref / nref);
         vref = nref;
-#pragma unroll
-        for (int j = 0; j < NT; ++j) {
-          o[j][0] *= f;
-          o[j][1] *= f;
-          o[j][2] *= f;
-          o[j][3] *= f;
-        }
       }
       const float unit = vref > 0.f ? kPTop / vref : 0.f;
-      uint32_t pa[4];
 #pragma unroll
-      for (int nt = 0; nt < 2; ++nt) {
-        const float fx = vs[nt].x * unit, fy = vs[nt].y * unit;
+      for (int c = 0; c < 4; ++c) {
+        uint32_t pa[4];
 #pragma unroll
-        for (int x = 0; x < 2; ++x) {
-          float p0 = s[2 * c + nt][2 * x], p1 = s[2 * c + nt][2 * x + 1];
-          if (kQuant) {
-            const float2 y = mul_rn_f32x2(make_float2(p0, p1), make_float2(inv[x], inv[x]));
-            const float2 d = mul_rn_f32x2(e4m3x2_decode(e4m3x2_rn_satfinite(y.x, y.y)),
-                                          make_float2(back[x], back[x]));
-            p0 = d.x;
-            p1 = d.y;
+        for (int nt = 0; nt < 2; ++nt) {
+          const int j = 2 * c + nt;
+          const float2 f = mul_rn_f32x2(lds_f2(sc + 32 * j), make_float2(unit, unit));
+#pragma unroll
+          for (int x = 0; x < 2; ++x) {
+            float2 w = make_float2(s[j][2 * x], s[j][2 * x + 1]);
+            if (kQuant) {
+              const float2 y = mul_rn_f32x2(w, make_float2(inv[x], inv[x]));
+              w = mul_rn_f32x2(e4m3x2_decode(e4m3x2_rn_satfinite(y.x, y.y)), make_float2(back[x], back[x]));
+            }
+            w = mul_rn_f32x2(w, f);
+            if (edge) {  // 0 x NaN: a key that the row does not see may hold anything
+              const int k = key0 + 8 * j + 2 * t;
+              if (k > last[x]) w.x = 0.f;
+              if (k + 1 > last[x]) w.y = 0.f;
+            }
+            pa[2 * nt + x] = f16x2(w.x, w.y);
           }
-          p0 *= fx;
-          p1 *= fy;
-          if (edge) {  // 0 x NaN: a key that the row does not see may hold anything
-            const int k = key0 + kChunk * c + 8 * nt + 2 * t;
-            if (k > last[x]) p0 = 0.f;
-            if (k + 1 > last[x]) p1 = 0.f;
+        }
+        const uint32_t base = slot + c * kChunk * D;
+        constexpr int W = D / 32;  // words of a lane's run of a row: NT codes
+        uint32_t w[4][W];
+        if constexpr (D == 128) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const uint4 v = lds128(base + v_off<D>(2 * t + (i & 1) + 8 * (i >> 1), g));
+            w[i][0] = v.x; w[i][1] = v.y; w[i][2] = v.z; w[i][3] = v.w;
           }
-          pa[2 * nt + x] = f16x2(p0, p1);
-        }
-      }
-      if constexpr (D == 128) {
-        const uint4 v0 = lds128(slot + v_off<D>(2 * t, g)), v1 = lds128(slot + v_off<D>(2 * t + 1, g));
-        const uint4 v2 = lds128(slot + v_off<D>(2 * t + 8, g)), v3 = lds128(slot + v_off<D>(2 * t + 9, g));
-        const uint32_t w0[4] = {v0.x, v0.y, v0.z, v0.w}, w1[4] = {v1.x, v1.y, v1.z, v1.w};
-        const uint32_t w2[4] = {v2.x, v2.y, v2.z, v2.w}, w3[4] = {v3.x, v3.y, v3.z, v3.w};
+        } else {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const uint32_t a0 = __byte_perm(w0[i], w1[i], 0x5140), a1 = __byte_perm(w0[i], w1[i], 0x7362);
-          const uint32_t b0 = __byte_perm(w2[i], w3[i], 0x5140), b1 = __byte_perm(w2[i], w3[i], 0x7362);
-          mma16816(o[4 * i], pa, codes_to_f16x2(static_cast<uint16_t>(a0)), codes_to_f16x2(static_cast<uint16_t>(b0)));
-          mma16816(o[4 * i + 1], pa, codes_to_f16x2(static_cast<uint16_t>(a0 >> 16)), codes_to_f16x2(static_cast<uint16_t>(b0 >> 16)));
-          mma16816(o[4 * i + 2], pa, codes_to_f16x2(static_cast<uint16_t>(a1)), codes_to_f16x2(static_cast<uint16_t>(b1)));
-          mma16816(o[4 * i + 3], pa, codes_to_f16x2(static_cast<uint16_t>(a1 >> 16)), codes_to_f16x2(static_cast<uint16_t>(b1 >> 16)));
+          for (int i = 0; i < 4; ++i) {
+            const uint2 v = lds64(base + v_off<D>(2 * t + (i & 1) + 8 * (i >> 1), g >> 1) + ((g & 1) << 3));
+            w[i][0] = v.x; w[i][1] = v.y;
+          }
         }
-      } else {
-        const uint32_t half8 = (g & 1) << 3;
-        const uint2 v0 = lds64(slot + v_off<D>(2 * t, g >> 1) + half8);
-        const uint2 v1 = lds64(slot + v_off<D>(2 * t + 1, g >> 1) + half8);
-        const uint2 v2 = lds64(slot + v_off<D>(2 * t + 8, g >> 1) + half8);
-        const uint2 v3 = lds64(slot + v_off<D>(2 * t + 9, g >> 1) + half8);
-        const uint32_t w0[2] = {v0.x, v0.y}, w1[2] = {v1.x, v1.y}, w2[2] = {v2.x, v2.y}, w3[2] = {v3.x, v3.y};
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const uint32_t a0 = __byte_perm(w0[i], w1[i], 0x5140), a1 = __byte_perm(w0[i], w1[i], 0x7362);
-          const uint32_t b0 = __byte_perm(w2[i], w3[i], 0x5140), b1 = __byte_perm(w2[i], w3[i], 0x7362);
+        for (int i = 0; i < W; ++i) {  // bytes of two keys interleaved, four channels
+          const uint32_t a0 = __byte_perm(w[0][i], w[1][i], 0x5140), a1 = __byte_perm(w[0][i], w[1][i], 0x7362);
+          const uint32_t b0 = __byte_perm(w[2][i], w[3][i], 0x5140), b1 = __byte_perm(w[2][i], w[3][i], 0x7362);
           mma16816(o[4 * i], pa, codes_to_f16x2(static_cast<uint16_t>(a0)), codes_to_f16x2(static_cast<uint16_t>(b0)));
           mma16816(o[4 * i + 1], pa, codes_to_f16x2(static_cast<uint16_t>(a0 >> 16)), codes_to_f16x2(static_cast<uint16_t>(b0 >> 16)));
           mma16816(o[4 * i + 2], pa, codes_to_f16x2(static_cast<uint16_t>(a1)), codes_to_f16x2(static_cast<uint16_t>(b1)));
@@ -539,7 +586,7 @@ __global__ void __launch_bounds__(32 * kWarps, 1) decode_kernel(const Params p) 
         }
       }
       __syncwarp();
-      produce(false);
+      if constexpr (C::kSlots & 1) produce(K{}, false); else produce(V{}, false);
     }
 
     const bool ends = cc.tile + 1 == cc.tiles;

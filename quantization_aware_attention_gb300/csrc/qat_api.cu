@@ -440,6 +440,8 @@ qat_status_t check_cache_sizes(int H, int D, int num_pages, int page_size, int m
   if (H < 1 || (D != 64 && D != 128) || num_pages < 1 || max_pages < 1) return QAT_ERR_INVALID_ARG;
   if (page_shift(page_size) < 0) return QAT_ERR_UNSUPPORTED;
   if (static_cast<long long>(max_pages) * page_size > (1ll << 30)) return QAT_ERR_UNSUPPORTED;
+  // rows are numbered in 32 bits (2^32 rows of 64 channels are 550 GB of codes)
+  if (static_cast<double>(num_pages) * H * page_size > 4294967000.0) return QAT_ERR_UNSUPPORTED;
   return QAT_OK;
 }
 
