@@ -58,6 +58,13 @@ QUANT_P_FP8E4M3_ROW_TILE64 = 1
 QUANT_P_FP8E4M3_ROW_TILE64_PAGE_BWD = 2
 
 
+_OK = Status.OK
+
+
+def _status(code: int) -> Status:
+    return _OK if code == 0 else Status(code)
+
+
 class QatError(RuntimeError):
     def __init__(self, status: int, what: str = ""):
         self.status = Status(status)
@@ -136,10 +143,18 @@ def _ptr(x) -> int | None:
     return x.data_ptr()
 
 
+_raw_stream = None
+
+
 def _stream(s) -> int | None:
     if s is None:
+        global _raw_stream
         import torch
-        return torch.cuda.current_stream().cuda_stream
+        if _raw_stream is None:  # the handle without the Stream object around it, where torch has it
+            torch.cuda.current_stream()
+            _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
+                                  lambda device: torch.cuda.current_stream(device).cuda_stream)
+        return _raw_stream(torch.cuda.current_device())
     if isinstance(s, int):
         return s
     return s.cuda_stream
@@ -239,7 +254,7 @@ def _s3(strides):
 def qat_qk_norm_rope(q, q_strides, k, k_strides, q_out, k_out, positions, position_stride, phases,
                      q_weight, k_weight, weight_bf16, B, Hq, Hk, N, D, rotary_dim, interleaved,
                      amplitude, eps, stream=None) -> Status:
-    return Status(lib().qat_qk_norm_rope(
+    return _status(lib().qat_qk_norm_rope(
         _ptr(q), _s3(q_strides), _ptr(k), _s3(k_strides), _ptr(q_out), _ptr(k_out), _ptr(positions),
         position_stride, _ptr(phases), _ptr(q_weight), _ptr(k_weight), int(weight_bf16), B, Hq, Hk, N,
         D, rotary_dim, interleaved, amplitude, eps, _stream(stream)))
@@ -254,7 +269,7 @@ def qat_qk_norm_rope_bwd(q, q_strides, k, k_strides, dq_out, dq_out_strides, dk_
                          dq_strides, dk, dk_strides, dq_weight, dk_weight, B, Hq, Hk, N, D, rotary_dim,
                          interleaved, amplitude, eps, workspace, workspace_bytes,
                          stream=None) -> Status:
-    return Status(lib().qat_qk_norm_rope_bwd(
+    return _status(lib().qat_qk_norm_rope_bwd(
         _ptr(q), _s3(q_strides), _ptr(k), _s3(k_strides), _ptr(dq_out), _s3(dq_out_strides),
         _ptr(dk_out), _s3(dk_out_strides), _ptr(positions), position_stride, _ptr(phases),
         _ptr(q_weight), _ptr(k_weight), int(weight_bf16), _ptr(dq), _s3(dq_strides), _ptr(dk),
@@ -265,7 +280,7 @@ def qat_qk_norm_rope_bwd(q, q_strides, k, k_strides, dq_out, dq_out_strides, dk_
 def qat_kv_cache_append(k, k_strides, v, v_strides, k_codes, v_codes, k_scales, v_scales, block_table,
                         seq_lens, new_lens, B, H, N, D, num_pages, page_size, max_pages,
                         stream=None) -> Status:
-    return Status(lib().qat_kv_cache_append(
+    return _status(lib().qat_kv_cache_append(
         _ptr(k), _s3(k_strides), _ptr(v), _s3(v_strides), _ptr(k_codes), _ptr(v_codes),
         _ptr(k_scales), _ptr(v_scales), _ptr(block_table), _ptr(seq_lens), _ptr(new_lens), B, H, N, D,
         num_pages, page_size, max_pages, _stream(stream)))
@@ -273,7 +288,7 @@ def qat_kv_cache_append(k, k_strides, v, v_strides, k_codes, v_codes, k_scales, 
 
 def qat_kv_cache_read(k_codes, v_codes, k_scales, v_scales, block_table, seq_lens, k_out, v_out, B, H,
                       begin, N, D, num_pages, page_size, max_pages, stream=None) -> Status:
-    return Status(lib().qat_kv_cache_read(
+    return _status(lib().qat_kv_cache_read(
         _ptr(k_codes), _ptr(v_codes), _ptr(k_scales), _ptr(v_scales), _ptr(block_table),
         _ptr(seq_lens), _ptr(k_out), _ptr(v_out), B, H, begin, N, D, num_pages, page_size, max_pages,
         _stream(stream)))
@@ -286,7 +301,7 @@ def qat_attn_decode_workspace_bytes(D) -> int:
 def qat_attn_decode(q, k_codes, v_codes, k_scales, v_scales, block_table, seq_lens, o, lse, B, Hq, Hkv,
                     T, D, num_pages, page_size, max_pages, sm_scale, quant_mode, workspace,
                     workspace_bytes, stream=None) -> Status:
-    return Status(lib().qat_attn_decode(
+    return _status(lib().qat_attn_decode(
         _ptr(q), _ptr(k_codes), _ptr(v_codes), _ptr(k_scales), _ptr(v_scales), _ptr(block_table),
         _ptr(seq_lens), _ptr(o), _ptr(lse), B, Hq, Hkv, T, D, num_pages, page_size, max_pages,
         float(sm_scale), int(quant_mode), _ptr(workspace), workspace_bytes, _stream(stream)))

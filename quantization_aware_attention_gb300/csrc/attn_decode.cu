@@ -16,7 +16,8 @@
 // key -- are cut into equal contiguous ranges, one per warp, whatever the sequences' lengths.  An
 // (sequence, head, row tile) item inside one range is finished there; an item cut by a range
 // boundary leaves unnormalized fp32 partials with their m and l in the workspace, which
-// decode_merge_kernel adds in worker order (no atomics: the same lengths give the same bits).
+// decode_merge_kernel adds in an order that the lengths alone decide (no atomics: the same lengths
+// give the same bits).
 //
 // Products: mma.sync m16n8k16 with f16 operands and fp32 sums.  E4M3 codes are exact in f16, and
 // become f16 in registers (one conversion per two codes), so the scale of a key multiplies its
@@ -65,10 +66,8 @@ struct Cfg {
 
 // Workspace: what each worker's range cut, then the partials.
 struct WorkerMeta {
-  int head;       // item whose beginning lies in an earlier range, or -1
-  int head_done;  // that item ends in this range
-  int tail;       // item that begins in this range and ends in a later one, or -1
-  int pad;
+  int tail;  // item that begins in this range and ends in a later one, or -1
+  int last;  // the worker in whose range it ends
 };
 template <int D>
 struct Partial {
@@ -78,7 +77,7 @@ struct Partial {
 template <int D>
 struct Workspace {
   int workers;
-  int pad[3];
+  int pad[31];
   WorkerMeta meta[kWorkers];
   Partial<D> part[kWorkers][2];  // [0] head, [1] tail
 };
@@ -294,6 +293,8 @@ __global__ void __launch_bounds__(32 * kWarps, 1) decode_kernel(const Params p) 
   const int per_cta = min(kWarps, (W + static_cast<int>(gridDim.x) - 1) / static_cast<int>(gridDim.x));
   const int workers = min(W, per_cta * static_cast<int>(gridDim.x));
   if (blockIdx.x == 0 && tid == 0) ws->workers = workers;
+  // the merge kernel's blocks may be brought up; they wait for this grid's end
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if (warp >= per_cta) return;
   const int id = blockIdx.x * per_cta + warp;
   if (id >= workers) return;
@@ -416,7 +417,7 @@ __global__ void __launch_bounds__(32 * kWarps, 1) decode_kernel(const Params p) 
   float m[2], l[2], rf[2], vref = 0.f;
   int last[2];                 // the newest key each of the lane's two rows sees
   bool begun = false;
-  if (lane == 0) ws->meta[id] = WorkerMeta{-1, 0, -1, 0};
+  if (lane == 0) ws->meta[id] = WorkerMeta{-1, -1};
   int first_tile = cc.tile;    // of the current segment
 
   for (int u = u0; u < u1; ++u) {
@@ -626,13 +627,9 @@ __global__ void __launch_bounds__(32 * kWarps, 1) decode_kernel(const Params p) 
       } else {
         const bool head = first_tile != 0;
         Partial<D>& part = ws->part[id][head ? 0 : 1];
-        if (lane == 0) {
-          if (head) {
-            ws->meta[id].head = item_of(p, cc);
-            ws->meta[id].head_done = ends;
-          } else {
-            ws->meta[id].tail = item_of(p, cc);
-          }
+        if (!head && lane == 0) {
+          const long long end = u - cc.tile + cc.tiles;  // the unit behind the item
+          ws->meta[id] = WorkerMeta{item_of(p, cc), static_cast<int>((end * workers - 1) / W)};
         }
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
@@ -654,45 +651,74 @@ __global__ void __launch_bounds__(32 * kWarps, 1) decode_kernel(const Params p) 
   cp_wait<0>();
 }
 
-// Adds the partials of the items that ranges cut: block w takes the item that worker w's range
-// begins and does not end (if there is one), one warp per row, D / 32 channels per lane, in worker
-// order.
-template <int D>
-__global__ void __launch_bounds__(32 * kRows) decode_merge_kernel(const Params p) {
-  constexpr int V = D / 32;
-  asm volatile("griddepcontrol.wait;" ::: "memory");  // the partials are complete
-  const Workspace<D>* ws = static_cast<const Workspace<D>*>(p.a.ws);
-  const int w = blockIdx.x, lane = threadIdx.x & 31, r = threadIdx.x >> 5;
-  const int workers = ws->workers;
-  if (w >= workers) return;
-  const int item = ws->meta[w].tail;
-  if (item < 0) return;
-  const int mt = item % p.mtiles;
-  if (mt * kRows + r >= p.R) return;
-  const Partial<D>* part = &ws->part[w][1];
-  float m = part->ml[r][0], l = part->ml[r][1];
-  float acc[V];
+// A row of partials being added up: V channels per lane, and the row's m and l.
+template <int V>
+struct Sum {
+  float m, l, acc[V];
+  __device__ __forceinline__ void clear() {
+    m = -INFINITY;
+    l = 0.f;
 #pragma unroll
-  for (int i = 0; i < V; ++i) acc[i] = part->o[r][V * lane + i];
-  for (int x = w + 1; x < workers; ++x) {
-    part = &ws->part[x][0];
-    const float m2 = part->ml[r][0], l2 = part->ml[r][1];
+    for (int i = 0; i < V; ++i) acc[i] = 0.f;
+  }
+  __device__ __forceinline__ void add(float m2, float l2, const float (&o2)[V]) {
     const float mn = fmaxf(m, m2);
     const float ref = mn == -INFINITY ? 0.f : mn;
     const float f = ex2(m - ref), f2 = ex2(m2 - ref);
     m = mn;
     l = l * f + l2 * f2;
 #pragma unroll
-    for (int i = 0; i < V; ++i) acc[i] = acc[i] * f + part->o[r][V * lane + i] * f2;
-    if (ws->meta[x].head_done) break;
+    for (int i = 0; i < V; ++i) acc[i] = acc[i] * f + o2[i] * f2;
   }
-  const size_t row = static_cast<size_t>(item / p.mtiles) * p.R + mt * kRows + r;
-  const bool none = l == 0.f;
-  const float f = none ? 0.f : 1.f / l;
+};
+
+template <int V>
+__device__ __forceinline__ void load_v(float (&x)[V], const float* src) {
+  if constexpr (V == 4) {
+    const float4 t = __ldcg(reinterpret_cast<const float4*>(src));
+    x[0] = t.x; x[1] = t.y; x[2] = t.z; x[3] = t.w;
+  } else {
+    const float2 t = __ldcg(reinterpret_cast<const float2*>(src));
+    x[0] = t.x; x[1] = t.y;
+  }
+}
+
+// Adds partials first, first + step, ... up to n of the chain that begins with worker w's tail, four
+// loads ahead.
+template <int D>
+__device__ __forceinline__ void add_chain(const Workspace<D>* ws, int w, int first, int step, int n,
+                                          int r, int lane, Sum<D / 32>& sum) {
+  constexpr int V = D / 32;
+  for (int i = first; i < n; i += 4 * step) {
+    float x[4][V];
+    float2 ml[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int c = i + k * step;
+      if (c < n) {
+        const Partial<D>* part = &ws->part[w + c][c == 0 ? 1 : 0];
+        ml[k] = __ldcg(reinterpret_cast<const float2*>(part->ml[r]));
+        load_v<V>(x[k], part->o[r] + V * lane);
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      if (i + k * step < n) sum.add(ml[k].x, ml[k].y, x[k]);
+  }
+}
+
+template <int D>
+__device__ __forceinline__ void store_row(const Params& p, int item, int r, int lane,
+                                          const Sum<D / 32>& s) {
+  constexpr int V = D / 32;
+  const size_t row = static_cast<size_t>(item / p.mtiles) * p.R + item % p.mtiles * kRows + r;
+  const bool none = s.l == 0.f;
+  const float f = none ? 0.f : 1.f / s.l;
   uint32_t out[V / 2];
 #pragma unroll
   for (int i = 0; i < V / 2; ++i) {
-    const __nv_bfloat162 v = __floats2bfloat162_rn(none ? 0.f : acc[2 * i] * f, none ? 0.f : acc[2 * i + 1] * f);
+    const __nv_bfloat162 v = __floats2bfloat162_rn(none ? 0.f : s.acc[2 * i] * f,
+                                                   none ? 0.f : s.acc[2 * i + 1] * f);
     out[i] = *reinterpret_cast<const uint32_t*>(&v);
   }
   uint16_t* dst = p.a.o + row * D + V * lane;
@@ -700,7 +726,61 @@ __global__ void __launch_bounds__(32 * kRows) decode_merge_kernel(const Params p
     *reinterpret_cast<uint2*>(dst) = make_uint2(out[0], out[1]);
   else
     *reinterpret_cast<uint32_t*>(dst) = out[0];
-  if (lane == 0 && p.a.lse != nullptr) p.a.lse[row] = none ? -INFINITY : m + log2f(l);
+  if (lane == 0 && p.a.lse != nullptr) p.a.lse[row] = none ? -INFINITY : s.m + log2f(s.l);
+}
+
+// Adds the partials of the items that ranges cut.  Block (x, r) takes row r of the items that the
+// ranges of workers 8 x .. 8 x + 7 begin and do not end: one warp each, or all eight warps together
+// where an item's chain of partials is long.
+template <int D>
+__global__ void __launch_bounds__(32 * kWarps) decode_merge_kernel(const Params p) {
+  constexpr int V = D / 32;
+  constexpr int kShort = 16;
+  __shared__ float acc[kWarps][D], ml[kWarps][2];
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // the partials are complete
+  const Workspace<D>* ws = static_cast<const Workspace<D>*>(p.a.ws);
+  const int w0 = blockIdx.x * kWarps, r = blockIdx.y;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int workers = ws->workers;
+  if (w0 >= workers) return;
+  WorkerMeta mine = {-1, -1};
+  if (lane < kWarps && w0 + lane < workers) mine = ws->meta[w0 + lane];
+  const bool cut = mine.tail >= 0 && mine.tail % p.mtiles * kRows + r < p.R;
+  const int n = cut ? mine.last - (w0 + lane) + 1 : 0;
+  Sum<V> sum;
+  {
+    const int len = __shfl_sync(0xffffffffu, n, warp), item = __shfl_sync(0xffffffffu, mine.tail, warp);
+    if (len > 0 && len <= kShort) {
+      sum.clear();
+      add_chain<D>(ws, w0 + warp, 0, 1, len, r, lane, sum);
+      store_row<D>(p, item, r, lane, sum);
+    }
+  }
+  unsigned rest = __ballot_sync(0xffffffffu, n > kShort);  // the same in every warp
+  while (rest != 0) {
+    const int k = __ffs(rest) - 1;
+    rest &= rest - 1;
+    sum.clear();
+    add_chain<D>(ws, w0 + k, warp, kWarps, __shfl_sync(0xffffffffu, n, k), r, lane, sum);
+#pragma unroll
+    for (int i = 0; i < V; ++i) acc[warp][V * lane + i] = sum.acc[i];
+    if (lane == 0) {
+      ml[warp][0] = sum.m;
+      ml[warp][1] = sum.l;
+    }
+    __syncthreads();
+    const int item = __shfl_sync(0xffffffffu, mine.tail, k);
+    if (warp == 0) {
+      for (int x = 1; x < kWarps; ++x) {
+        float o2[V];
+#pragma unroll
+        for (int i = 0; i < V; ++i) o2[i] = acc[x][V * lane + i];
+        sum.add(ml[x][0], ml[x][1], o2);
+      }
+      store_row<D>(p, item, r, lane, sum);
+    }
+    __syncthreads();
+  }
 }
 
 template <int D, bool kQuant>
@@ -714,8 +794,8 @@ cudaError_t run(const Params& p, int ctas, cudaStream_t s) {
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(ctas * kWarps);
-  cfg.blockDim = dim3(32 * kRows);
+  cfg.gridDim = dim3(ctas, p.R < kRows ? p.R : kRows);
+  cfg.blockDim = dim3(32 * kWarps);
   cfg.stream = s;
   cudaLaunchAttribute at[1];
   at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;

@@ -87,9 +87,17 @@ class RopePlan:
             raise ValueError("device must be a CUDA device (this library has no CPU path)")
 
 
-def _rows(t, name, device, B=None, N=None, D=None, H=None):
-    """A bf16 [B, H, N, D] tensor the kernels can read in place (D innermost, rows on 16-byte
-    boundaries)."""
+def rows_strides(t, name, device, shape):
+    """The element strides {b, h, n} of a bf16 [B, H, N, D] tensor that the kernels can read in place
+    (D innermost, rows on 16-byte boundaries), None when it is contiguous.  ``shape`` is what it has
+    to be, or None."""
+    if (isinstance(t, torch.Tensor) and t.dtype is torch.bfloat16 and t.device == device
+            and (t.shape == shape or (shape is None and t.dim() == 4)) and not t.data_ptr() & 15):
+        if t.is_contiguous():
+            return None
+        b, h, n, d = t.stride()
+        if d == 1 and not (b | h | n) & 7:
+            return b, h, n
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if not t.is_cuda or t.device != device:
@@ -98,53 +106,52 @@ def _rows(t, name, device, B=None, N=None, D=None, H=None):
         raise ValueError(f"{name} must be torch.bfloat16, got {t.dtype}")
     if t.dim() != 4:
         raise ValueError(f"{name} must be [B, H, N, D], got shape {tuple(t.shape)}")
-    s = t.shape
-    if (B is not None and (s[0] != B or s[2] != N or s[3] != D)) or (H is not None and s[1] != H):
-        raise ValueError(f"{name} has shape {tuple(s)}, expected "
-                         f"{(B, 'H' if H is None else H, N, D)}")
-    if not _readable(t):
+    if shape is not None and t.shape != shape:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if not readable(t):
         raise ValueError(f"{name} must have D innermost and rows on 16-byte boundaries, got strides "
                          f"{t.stride()}")
+    return t.stride()[:3]
 
 
-def _readable(t) -> bool:
+def readable(t) -> bool:
+    """Whether the kernels can read t [B, H, N, D] in place."""
+    if t.data_ptr() & 15:
+        return False
     if t.is_contiguous():
-        return t.data_ptr() % 16 == 0
+        return True
     st, s = t.stride(), t.shape
-    return ((st[3] == 1 or s[3] == 1) and t.data_ptr() % 16 == 0
-            and all(n <= 1 or x % 8 == 0 for n, x in zip(s[:3], st[:3])))
-
-
-def _strides(t):
-    return None if t.is_contiguous() else t.stride()[:3]
+    return st[3] == 1 and all(n <= 1 or x % 8 == 0 for n, x in zip(s[:3], st[:3]))
 
 
 def _operands(q, k, positions, rope, q_weight, k_weight):
-    """Checks them; returns the C call's leading arguments in common (after the tensors)."""
+    """Checks them; returns (device, q's strides, k's, B, Hq, Hk, N, D, the positions' stride)."""
     if not isinstance(q, torch.Tensor) or not q.is_cuda:
         raise ValueError("q must be a CUDA tensor (this library has no CPU path)")
     dev = q.device
-    _rows(q, "q", dev)
+    qs = rows_strides(q, "q", dev, None)
     B, Hq, N, D = q.shape
-    if D not in (64, 128):
+    if D != 64 and D != 128:
         raise ValueError(f"the head dimension must be 64 or 128, got {D}")
-    Hk = 0
+    Hk, ks = 0, None
     if k is not None:
-        _rows(k, "k", dev, B, N, D)
-        Hk = k.shape[1]
+        Hk = k.shape[1] if isinstance(k, torch.Tensor) and k.dim() == 4 else -1
+        ks = rows_strides(k, "k", dev, (B, Hk, N, D))
         if (q_weight is None) != (k_weight is None):
             raise ValueError("q_weight and k_weight go together")
     elif k_weight is not None:
         raise ValueError("k_weight without k")
-    for name, w in (("q_weight", q_weight), ("k_weight", k_weight)):
-        if w is None:
-            continue
-        if not isinstance(w, torch.Tensor) or w.device != dev:
-            raise ValueError(f"{name} must be a tensor on {dev}")
-        if w.dtype not in (torch.float32, torch.bfloat16) or w.dtype != q_weight.dtype:
-            raise ValueError("the weights must both be torch.float32 or torch.bfloat16")
-        if w.dim() != 1 or w.shape[0] != D or not w.is_contiguous() or w.data_ptr() % 16:
-            raise ValueError(f"{name} must be contiguous [{D}] on a 16-byte boundary")
+    if q_weight is not None:
+        wtype = q_weight.dtype if isinstance(q_weight, torch.Tensor) else None
+        for name, w in (("q_weight", q_weight), ("k_weight", k_weight)):
+            if w is None:
+                continue
+            if not isinstance(w, torch.Tensor) or w.device != dev:
+                raise ValueError(f"{name} must be a tensor on {dev}")
+            if w.dtype is not wtype or (wtype is not torch.float32 and wtype is not torch.bfloat16):
+                raise ValueError("the weights must both be torch.float32 or torch.bfloat16")
+            if w.shape != (D,) or not w.is_contiguous() or w.data_ptr() & 15:
+                raise ValueError(f"{name} must be contiguous [{D}] on a 16-byte boundary")
     pos_stride = 0
     if rope is None:
         if positions is not None:
@@ -158,34 +165,34 @@ def _operands(q, k, positions, rope, q_weight, k_weight):
             raise ValueError(f"rotary_dim {rope.rotary_dim} exceeds the head dimension {D}")
         if not isinstance(positions, torch.Tensor) or positions.device != dev:
             raise ValueError(f"positions must be a tensor on {dev}")
-        if positions.dtype != torch.int32:
+        if positions.dtype is not torch.int32:
             raise ValueError(f"positions must be torch.int32, got {positions.dtype}")
-        shape = tuple(positions.shape)
-        if shape not in ((N,), (B, N)):
-            raise ValueError(f"positions has shape {shape}, expected {(N,)} or {(B, N)}")
+        if positions.shape == (B, N):
+            if B > 1:
+                pos_stride = positions.stride(0)
+        elif positions.shape != (N,):
+            raise ValueError(f"positions has shape {tuple(positions.shape)}, expected {(N,)} or "
+                             f"{(B, N)}")
         if N > 1 and positions.stride(-1) != 1:
             raise ValueError("positions must be contiguous along the tokens")
-        if len(shape) == 2 and B > 1:
-            pos_stride = positions.stride(0)
-    return B, Hq, Hk, N, D, pos_stride
+    return dev, qs, ks, B, Hq, Hk, N, D, pos_stride
 
 
 def _tail(rope):
     if rope is None:
-        return 0, 0, 1.0
-    return rope.rotary_dim, int(rope.layout == "interleaved"), rope.amplitude
+        return None, 0, 0, 1.0
+    return rope.phases, rope.rotary_dim, 1 if rope.layout == "interleaved" else 0, rope.amplitude
 
 
 def _forward(q, k, positions, rope, q_weight, k_weight, eps):
-    B, Hq, Hk, N, D, pos_stride = _operands(q, k, positions, rope, q_weight, k_weight)
-    R, inter, amp = _tail(rope)
-    q_out = torch.empty((B, Hq, N, D), dtype=torch.bfloat16, device=q.device)
-    k_out = None if k is None else torch.empty((B, Hk, N, D), dtype=torch.bfloat16, device=q.device)
-    with device_guard(q.device):
+    dev, qs, ks, B, Hq, Hk, N, D, pos_stride = _operands(q, k, positions, rope, q_weight, k_weight)
+    phases, R, inter, amp = _tail(rope)
+    q_out = torch.empty((B, Hq, N, D), dtype=torch.bfloat16, device=dev)
+    k_out = None if k is None else torch.empty((B, Hk, N, D), dtype=torch.bfloat16, device=dev)
+    with device_guard(dev):
         st = capi.qat_qk_norm_rope(
-            q, _strides(q), k, None if k is None else _strides(k), q_out, k_out, positions, pos_stride,
-            None if rope is None else rope.phases, q_weight, k_weight,
-            q_weight is not None and q_weight.dtype == torch.bfloat16, B, Hq, Hk, N, D, R, inter, amp,
+            q, qs, k, ks, q_out, k_out, positions, pos_stride, phases, q_weight, k_weight,
+            q_weight is not None and q_weight.dtype is torch.bfloat16, B, Hq, Hk, N, D, R, inter, amp,
             eps)
     _raise(st, "qat_qk_norm_rope")
     return q_out, k_out
@@ -195,38 +202,35 @@ def qat_qk_norm_rope_backward(q, k, positions, rope, q_weight, k_weight, dq_out,
                               eps: float = 1e-6, workspace: torch.Tensor | None = None):
     """Gradients (dq, dk, dq_weight, dk_weight) of ``qat_qk_norm_rope`` at its inputs, given those of
     its outputs; None for what is absent.  dq and dk have the inputs' order in memory."""
-    B, Hq, Hk, N, D, pos_stride = _operands(q, k, positions, rope, q_weight, k_weight)
-    R, inter, amp = _tail(rope)
-    _rows(dq_out, "dq_out", q.device, B, N, D, Hq)
+    dev, qs, ks, B, Hq, Hk, N, D, pos_stride = _operands(q, k, positions, rope, q_weight, k_weight)
+    phases, R, inter, amp = _tail(rope)
+    gqs = rows_strides(dq_out, "dq_out", dev, (B, Hq, N, D))
     if (k is None) != (dk_out is None):
         raise ValueError("dk_out goes together with k")
-    if k is not None:
-        _rows(dk_out, "dk_out", q.device, B, N, D, Hk)
+    gks = None if k is None else rows_strides(dk_out, "dk_out", dev, (B, Hk, N, D))
 
-    def grad_of(x):
-        if x is None:
-            return None
-        if x.stride(2) > x.stride(1):  # heads inner, as a projection writes them
-            return torch.empty((B, N, x.shape[1], D), dtype=x.dtype, device=x.device).transpose(1, 2)
-        return torch.empty(x.shape, dtype=x.dtype, device=x.device)
+    def grad_of(x, strides, H):
+        if strides is not None and strides[2] > strides[1]:  # heads inner, as a projection writes them
+            g = torch.empty((B, N, H, D), dtype=torch.bfloat16, device=dev)
+            return g.transpose(1, 2), (N * H * D, D, H * D)
+        return torch.empty((B, H, N, D), dtype=torch.bfloat16, device=dev), None
 
-    dq, dk = grad_of(q), grad_of(k)
-    dwq = None if q_weight is None else torch.empty_like(q_weight)
-    dwk = None if k_weight is None else torch.empty_like(k_weight)
-    if workspace is None and q_weight is not None:
-        workspace = torch.empty(capi.qat_qk_norm_rope_bwd_workspace_bytes(D), dtype=torch.uint8,
-                                device=q.device)
-
-    def st(x):
-        return None if x is None else _strides(x)
-
-    with device_guard(q.device):
+    dq, dqs = grad_of(q, qs, Hq)
+    dk, dks = (None, None) if k is None else grad_of(k, ks, Hk)
+    dwq = dwk = None
+    ws_bytes = 0
+    if q_weight is not None:
+        dwq = torch.empty_like(q_weight)
+        dwk = None if k is None else torch.empty_like(k_weight)
+        if workspace is None:
+            workspace = torch.empty(capi.qat_qk_norm_rope_bwd_workspace_bytes(D), dtype=torch.uint8,
+                                    device=dev)
+        ws_bytes = workspace.numel()
+    with device_guard(dev):
         status = capi.qat_qk_norm_rope_bwd(
-            q, st(q), k, st(k), dq_out, st(dq_out), dk_out, st(dk_out), positions, pos_stride,
-            None if rope is None else rope.phases, q_weight, k_weight,
-            q_weight is not None and q_weight.dtype == torch.bfloat16, dq, st(dq), dk, st(dk), dwq, dwk,
-            B, Hq, Hk, N, D, R, inter, amp, eps, workspace,
-            0 if workspace is None else workspace.numel())
+            q, qs, k, ks, dq_out, gqs, dk_out, gks, positions, pos_stride, phases, q_weight, k_weight,
+            q_weight is not None and q_weight.dtype is torch.bfloat16, dq, dqs, dk, dks, dwq, dwk, B,
+            Hq, Hk, N, D, R, inter, amp, eps, workspace, ws_bytes)
     _raise(status, "qat_qk_norm_rope_bwd")
     return dq, dk, dwq, dwk
 
@@ -248,7 +252,7 @@ class QKNormRope(torch.autograd.Function):
         q, k, positions, q_weight, k_weight = ctx.saved_tensors
 
         def ready(d):
-            return d if d is None or _readable(d) else d.contiguous()
+            return d if d is None or readable(d) else d.contiguous()
 
         dq, dk, dwq, dwk = qat_qk_norm_rope_backward(q, k, positions, ctx.rope, q_weight, k_weight,
                                                      ready(dq_out), ready(dk_out), ctx.eps)
@@ -268,9 +272,8 @@ def qat_qk_norm_rope(q, k=None, positions=None, rope: RopePlan | None = None, q_
     fused projection, ``x.view(B, N, H, D).transpose(1, 2)``, is read in place.  Differentiable in q,
     k and the weights; the gradients are deterministic."""
     check = _check_enabled(check)
-    grad = torch.is_grad_enabled() and any(
-        t is not None and t.requires_grad for t in (q, k, q_weight, k_weight))
-    if grad:
+    if torch.is_grad_enabled() and any(
+            isinstance(t, torch.Tensor) and t.requires_grad for t in (q, k, q_weight, k_weight)):
         out = QKNormRope.apply(q, k, positions, rope, q_weight, k_weight, eps, check)
     else:
         out = _forward(q, k, positions, rope, q_weight, k_weight, eps)
