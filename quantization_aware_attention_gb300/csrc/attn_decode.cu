@@ -19,20 +19,23 @@
 // decode_merge_kernel adds in an order that the lengths alone decide (no atomics: the same lengths
 // give the same bits).
 //
-// Products: mma.sync m16n8k16 with f16 operands and fp32 sums.  E4M3 codes are exact in f16, and
-// become f16 in registers (one conversion per two codes), so the scale of a key multiplies its
-// column of S, and the scale of a value its column of P.  q (bf16) is brought into f16 by a power
-// of two per row, which is exact for every element above 2^-32 of the row's largest.  P times the
-// value's scale is rounded to f16 (2^-11 relative; relative to a running power-of-two bound of the
-// scales, so that it neither overflows nor loses small weights: the largest is near 2^14, the
-// smallest kept whole 2^-28 of it).  With 16 rows at most these products need a tenth of the
-// tensor rate, and operands come from registers, so the 128-row tcgen05 tile would be mostly empty
-// rows; the memory pipeline is what has to be fed.
+// Products: mma.sync m16n8k16 with f16 operands and fp32 sums, the cache as the 16-row operand and
+// the query rows as the 8 columns (one column tile for up to 8 rows, else two): S^T = K Q^T and
+// O^T = V^T P^T.  E4M3 codes are exact in f16, and become f16 in registers (one conversion per two
+// codes), so the scale of a key multiplies its row of S^T, and the scale of a value its row of P^T.
+// q (bf16) is brought into f16 by a power of two per row, which is exact for every element above 2^-32
+// of the row's largest.  P times the value's scale is rounded to f16 (2^-11 relative; relative to a
+// running power-of-two bound of the scales, so that it neither overflows nor loses small weights: the
+// largest is near 2^14, the smallest kept whole 2^-28 of it).  With so few rows these products need a
+// tenth of the tensor rate, and a 128-row tcgen05 tile would want the codes of V transposed and P in
+// 8 bits with a scale per key; the memory pipeline is what has to be fed.
 //
-// Operand layout: the order of d in Q K^T and of the output columns in P V is free, so each lane
-// takes 16-byte runs of a row: for K chunk t + 4 h of key g (k-step s of the run: bytes 4 s..4 s + 3),
-// for V chunk g of keys 2t, 2t + 1, 2t + 8, 2t + 9, whose bytes are interleaved by key with prmt.
-// Chunks are XOR-swizzled by row so that these reads are free of bank conflicts.
+// Operand layout: the order of d in Q K^T and of the output rows in V^T P^T is free, so each lane
+// (g = lane / 4, t = lane % 4) takes 16-byte runs of a row: for K chunk t + 4 h of keys g and g + 8
+// (k-step s of the run: bytes 4 s .. 4 s + 3), for V the g-th eighth of keys 2t, 2t + 1, 2t + 8, 2t + 9,
+// whose bytes are interleaved by key with prmt.  Chunks are XOR-swizzled by row so that these reads are
+// free of bank conflicts.  P^T leaves the softmax with a key per lane and becomes the product's operand
+// by movmatrix.
 #include "qat_internal.h"
 #include "qat_quant.cuh"
 #include "sm100.cuh"
@@ -45,23 +48,27 @@
 namespace qat {
 namespace {
 
-constexpr int kWarps = 8;
 constexpr int kTile = 64;    // keys per unit
+constexpr int kHalf = 32;    // keys per ring slot
 constexpr int kChunk = 16;   // keys that certainly share a page
-constexpr int kRows = 16;    // query rows per item
+constexpr int kRows = 16;    // query rows per item at most
 constexpr int kMaxCtas = 152;
-constexpr int kWorkers = kMaxCtas * kWarps;
+constexpr int kMaxWarps = 12;
+constexpr int kWorkers = kMaxCtas * kMaxWarps;
 constexpr float kTinyP = 7.888609052210118e-31f;  // 2^-100: a tile below it counts as zero (448 / amax
                                                   // must stay finite)
 constexpr float kPTop = 16384.f;  // P x value scale / bound is at most this
 constexpr uint32_t kNoPage = 0xffffffffu, kBadPage = 0xfffffffeu;
 
-template <int D>
+// NR: column tiles of 8 query rows per item, 1 or 2.  One tile needs half the registers, which
+// makes room for half as many warps again.
+template <int D, int NR>
 struct Cfg {
-  static constexpr int kSlots = D == 128 ? 3 : 6;             // K or V of one tile each
-  static constexpr int kSlotBytes = kTile * D + 4 * kTile;    // codes, then scales
+  static constexpr int kWarps = NR == 1 ? 12 : 8;
+  static constexpr int kSlots = D == 128 ? (NR == 1 ? 4 : 6) : (NR == 1 ? 6 : 10);
+  static constexpr int kSlotBytes = kHalf * D + 8 * kHalf;  // codes; in K slots the scales of K and V
   static constexpr int kRing = kSlots * kSlotBytes;
-  static constexpr int kSmem = kWarps * kRing;  // then B + 1 prefix sums
+  static constexpr int kSmem = kWarps * kRing;  // then the warps' sums and B + 1 prefix sums
 };
 
 // Workspace: what each worker's range cut, then the partials.
@@ -84,7 +91,7 @@ struct Workspace {
 
 struct Params {
   DecodeArgs a;
-  int R, mtiles;  // rows of a KV head (Hq / Hkv heads x T tokens), row tiles
+  int R, rows, mtiles;  // rows of a KV head (Hq / Hkv heads x T tokens), of an item; items of a head
 };
 
 __device__ __forceinline__ float ex2(float x) {
@@ -102,6 +109,13 @@ __device__ __forceinline__ uint32_t codes_to_f16x2(uint16_t c) {
   uint32_t h2;
   asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h2) : "h"(c));
   return h2;
+}
+
+// Transposes an 8 x 8 matrix of 16-bit elements, row g's elements 2t and 2t + 1 in lane 4 g + t.
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
+  uint32_t y;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
 }
 
 __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
@@ -138,9 +152,10 @@ __device__ __forceinline__ uint2 lds64(uint32_t a) {
   asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a) : "memory");
   return v;
 }
-__device__ __forceinline__ float2 lds_f2(uint32_t a) {
-  const uint2 v = lds64(a);
-  return make_float2(__uint_as_float(v.x), __uint_as_float(v.y));
+__device__ __forceinline__ float lds_f(uint32_t a) {
+  float v;
+  asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(a) : "memory");
+  return v;
 }
 
 // Byte offset of 16-byte chunk c of row r in 16 rows of K or V codes.
@@ -185,14 +200,14 @@ __device__ __forceinline__ int item_of(const Params& p, const Cursor& c) {
   return (c.b * p.a.Hkv + c.h) * p.mtiles + c.mt;
 }
 
-// The item's query rows g and g + 8 as f16 times a power of two (exact for all that matters), in the
-// order of the K fragments, and what their scores are to be multiplied by.
-template <int D>
+// The item's query rows 8 n + g as f16 times a power of two (exact for all that matters), in the order
+// of the K fragments; rf: what the scores of rows 8 n + 2t and 8 n + 2t + 1 are to be multiplied by.
+template <int D, int NR>
 __device__ __forceinline__ void load_rows(const Params& p, const Cursor& c, int g, int t,
-                                          uint32_t (&qa)[D / 16][4], float (&rf)[2]) {
+                                          uint32_t (&qb)[NR][D / 16][2], float2 (&rf)[NR]) {
 #pragma unroll
-  for (int x = 0; x < 2; ++x) {
-    const int r = c.mt * kRows + g + 8 * x;
+  for (int n = 0; n < NR; ++n) {
+    const int r = c.mt * p.rows + g + 8 * n;
     uint4 raw[D / 32];
 #pragma unroll
     for (int i = 0; i < D / 32; ++i) raw[i] = make_uint4(0u, 0u, 0u, 0u);
@@ -221,8 +236,9 @@ __device__ __forceinline__ void load_rows(const Params& p, const Cursor& c, int 
     int e = static_cast<int>(__float_as_uint(amax) >> 23) - 127;
     e = min(max(e, -100), 126);
     const float up = __uint_as_float(static_cast<uint32_t>(127 + 14 - e) << 23);
-    rf[x] = fmaxf(p.a.qk_scale * __uint_as_float(static_cast<uint32_t>(127 - 14 + e) << 23),
-                  1.1754943508222875e-38f);  // not zero: it multiplies -inf
+    const float down = fmaxf(p.a.qk_scale * __uint_as_float(static_cast<uint32_t>(127 - 14 + e) << 23),
+                             1.1754943508222875e-38f);  // not zero: it multiplies -inf
+    rf[n] = make_float2(__shfl_sync(0xffffffffu, down, 8 * t), __shfl_sync(0xffffffffu, down, 8 * t + 4));
 #pragma unroll
     for (int h = 0; h < D / 64; ++h) {
 #pragma unroll
@@ -231,29 +247,44 @@ __device__ __forceinline__ void load_rows(const Params& p, const Cursor& c, int 
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
           const float2 f = __bfloat1622float2(b[k]);
-          qa[4 * h + 2 * i + (k >> 1)][2 * (k & 1) + x] = f16x2(f.x * up, f.y * up);
+          qb[n][4 * h + 2 * i + (k >> 1)][k & 1] = f16x2(f.x * up, f.y * up);
         }
       }
     }
   }
 }
 
-template <int NT>
-__device__ __forceinline__ void scale_rows(float (&o)[NT][4], float f0, float f1) {
+template <int MT>
+__device__ __forceinline__ void scale_rows(float (&o)[MT][4], float2 f) {
 #pragma unroll
-  for (int j = 0; j < NT; ++j) {
-    const float2 a = mul_rn_f32x2(make_float2(o[j][0], o[j][1]), make_float2(f0, f0));
-    const float2 b = mul_rn_f32x2(make_float2(o[j][2], o[j][3]), make_float2(f1, f1));
+  for (int j = 0; j < MT; ++j) {
+    const float2 a = mul_rn_f32x2(make_float2(o[j][0], o[j][1]), f);
+    const float2 b = mul_rn_f32x2(make_float2(o[j][2], o[j][3]), f);
     o[j][0] = a.x; o[j][1] = a.y; o[j][2] = b.x; o[j][3] = b.y;
   }
 }
 
-template <int D, bool kQuant>
-__global__ void __launch_bounds__(32 * kWarps, 1) decode_kernel(const Params p) {
-  using C = Cfg<D>;
-  extern __shared__ __align__(16) uint8_t smem[];
-  int* prefix = reinterpret_cast<int*>(smem + C::kSmem);
-  __shared__ int warp_sum[kWarps];
+// Over the lanes that share t.
+__device__ __forceinline__ float max_over_g(float x) {
+  x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
+  x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
+  return fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
+}
+__device__ __forceinline__ float sum_over_g(float x) {
+  x += __shfl_xor_sync(0xffffffffu, x, 4);
+  x += __shfl_xor_sync(0xffffffffu, x, 8);
+  return x + __shfl_xor_sync(0xffffffffu, x, 16);
+}
+
+template <int D, int NR, bool kQuant>
+__global__ void __launch_bounds__(32 * Cfg<D, NR>::kWarps, 1) decode_kernel(const Params p) {
+  using C = Cfg<D, NR>;
+  constexpr int kThreads = 32 * C::kWarps;
+  // No static shared memory: it would shift the ring, and cp.async fetches a sector twice when two
+  // 16-byte pieces of it do not go to one 32-byte aligned place (B64 ragged: 122 against 100 us).
+  extern __shared__ __align__(1024) uint8_t smem[];
+  int* warp_sum = reinterpret_cast<int*>(smem + C::kSmem);
+  int* prefix = warp_sum + C::kWarps;
   const DecodeArgs& a = p.a;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int g = lane >> 2, t = lane & 3;
@@ -261,7 +292,7 @@ __global__ void __launch_bounds__(32 * kWarps, 1) decode_kernel(const Params p) 
   // prefix[b] = units before sequence b
   const int per_seq = a.Hkv * p.mtiles;
   {
-    const int chunk = (a.B + 32 * kWarps - 1) / (32 * kWarps);
+    const int chunk = (a.B + kThreads - 1) / kThreads;
     const int b0 = min(tid * chunk, a.B), b1 = min(b0 + chunk, a.B);
     int sum = 0;
     for (int b = b0; b < b1; ++b) {
@@ -284,13 +315,13 @@ __global__ void __launch_bounds__(32 * kWarps, 1) decode_kernel(const Params p) 
       prefix[b] = base;
       base += tiles_of(clamp_len(a, __ldg(a.seq_lens + b))) * per_seq;
     }
-    if (tid == 32 * kWarps - 1) prefix[a.B] = base;
+    if (tid == kThreads - 1) prefix[a.B] = base;
     __syncthreads();
   }
   const int W = prefix[a.B];
   Workspace<D>* ws = static_cast<Workspace<D>*>(a.ws);
   // workers: as few warps per CTA as give every worker a unit, spread over the CTAs
-  const int per_cta = min(kWarps, (W + static_cast<int>(gridDim.x) - 1) / static_cast<int>(gridDim.x));
+  const int per_cta = min(C::kWarps, (W + static_cast<int>(gridDim.x) - 1) / static_cast<int>(gridDim.x));
   const int workers = min(W, per_cta * static_cast<int>(gridDim.x));
   if (blockIdx.x == 0 && tid == 0) ws->workers = workers;
   // the merge kernel's blocks may be brought up; they wait for this grid's end
@@ -327,11 +358,13 @@ __global__ void __launch_bounds__(32 * kWarps, 1) decode_kernel(const Params p) 
   const uint32_t v_dst0 = v_off<D>(lane / (D / 16), lane % (D / 16));
   const uint32_t v_dst1 = v_off<D>(lane / (D / 16) + 512 / D, lane % (D / 16)) - 512;
 
-  // Issues the copies of the next K (or V) tile as one group; an empty group at the end.
-  auto produce = [&](auto is_v, bool fresh) {
-    constexpr bool kV = decltype(is_v)::value;
+  // Issues the copies of the next slot -- sub 0, 1: the halves of K, with the scales of K and V; 2, 3:
+  // those of V -- as one group; an empty group at the end.
+  auto produce = [&](auto which, bool fresh) {
+    constexpr int sub = decltype(which)::value;
+    constexpr bool kV = sub >= 2;
     if (pu < u1) {
-      if (!kV && (fresh || (pc.tile & 7) == 0)) {
+      if (sub == 0 && (fresh || (pc.tile & 7) == 0)) {
         const int pos = ((pc.tile & ~7) * 4 + lane) * kChunk;
         rows_of = kNoPage;
         if (pos < pc.len) {
@@ -346,29 +379,32 @@ __global__ void __launch_bounds__(32 * kWarps, 1) decode_kernel(const Params p) 
         all_good = !__any_sync(0xffffffffu, rows_of == kBadPage);
       }
       const uint8_t* codes = (kV ? a.v_codes : a.k_codes) + 16 * lane;
-      const float* scales = kV ? a.v_scales : a.k_scales;
       const uint32_t dst = ring + pslot * C::kSlotBytes;
-      const int first = (pc.tile & 7) * 4;
-      const uint32_t sc_row = __shfl_sync(0xffffffffu, rows_of, first + (lane >> 2 & 3)) + 4 * (lane & 3);
-      const uint32_t sc_dst = dst + kTile * D + 16 * lane;
-      const int left = pc.len - pc.tile * kTile;  // the sequence's keys from the tile's first on
-      if (left >= kTile && all_good) {
+      const int first = (pc.tile & 7) * 4 + 2 * (sub & 1);
+      const int left = pc.len - pc.tile * kTile - kHalf * (sub & 1);  // keys from the half's first on
+      const uint32_t row[2] = {__shfl_sync(0xffffffffu, rows_of, first),
+                               __shfl_sync(0xffffffffu, rows_of, first + 1)};
+      // lanes 0-7: the scales of K, 8-15: of V, four keys each
+      const float* scales = (lane & 8) ? a.v_scales : a.k_scales;
+      const uint32_t sc_row = (lane & 4) ? row[1] : row[0];
+      const uint32_t sc_dst = dst + kHalf * D + 16 * lane;
+      if (left >= kHalf && all_good) {
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          const uint8_t* src = codes + static_cast<size_t>(__shfl_sync(0xffffffffu, rows_of, first + c)) * D;
+        for (int c = 0; c < 2; ++c) {
+          const uint8_t* src = codes + static_cast<size_t>(row[c]) * D;
 #pragma unroll
           for (int i = 0; i < D / 32; ++i) {
             const uint32_t off = kV ? ((i & 1) ? v_dst1 : v_dst0) : k_dst;
             cp_async16(dst + off + c * kChunk * D + i * 512, src + i * 512);
           }
         }
-        if (lane < 16) cp_async16(sc_dst, scales + sc_row);
+        if (!kV && lane < 16) cp_async16(sc_dst, scales + sc_row + 4 * (lane & 3));
       } else {  // zeros behind the end, and for bad pages zeros with scale NaN
 #pragma unroll 1
-        for (int c = 0; c < 4; ++c) {
-          const uint32_t row = __shfl_sync(0xffffffffu, rows_of, first + c);
-          const int n = row < kBadPage ? left - c * kChunk : 0;
-          const uint8_t* src = codes + (row < kBadPage ? static_cast<size_t>(row) * D : 0);
+        for (int c = 0; c < 2; ++c) {
+          const uint32_t rc = c ? row[1] : row[0];
+          const int n = rc < kBadPage ? left - c * kChunk : 0;
+          const uint8_t* src = codes + (rc < kBadPage ? static_cast<size_t>(rc) * D : 0);
 #pragma unroll 1
           for (int i = 0; i < D / 32; ++i) {
             const uint32_t off = kV ? ((i & 1) ? v_dst1 : v_dst0) : k_dst;
@@ -376,29 +412,33 @@ __global__ void __launch_bounds__(32 * kWarps, 1) decode_kernel(const Params p) 
             cp_async16(dst + off + c * kChunk * D + i * 512, r < n ? src + i * 512 : codes, r < n ? 16 : 0);
           }
         }
-        if (lane < 16) {
-          const uint32_t row = sc_row - 4 * (lane & 3);
-          if (row == kBadPage) {
+        if (!kV && lane < 16) {
+          if (sc_row == kBadPage) {
             asm volatile("st.shared.v4.u32 [%0], {%1,%1,%1,%1};" ::"r"(sc_dst), "r"(0x7fc00000u) : "memory");
           } else {
-            const int n = row == kNoPage ? 0 : min(max(left - 4 * lane, 0), 4);
-            cp_async16(sc_dst, n > 0 ? scales + sc_row : scales, 4 * n);
+            const int n = sc_row == kNoPage ? 0 : min(max(left - 4 * (lane & 7), 0), 4);
+            cp_async16(sc_dst, n > 0 ? scales + sc_row + 4 * (lane & 3) : scales, 4 * n);
           }
         }
       }
       pslot = pslot + 1 == C::kSlots ? 0 : pslot + 1;
-      if (kV) {
+      if (sub == 3) {
         ++pu;
         advance(p, pc);
       }
     }
     cp_commit();
   };
-  using K = std::false_type;
-  using V = std::true_type;
-#pragma unroll 1
-  for (int i = 0; i < C::kSlots; ++i) {
-    if (i & 1) produce(V{}, false); else produce(K{}, i == 0);
+#define QAT_SUB(i) std::integral_constant<int, (i) & 3>{}
+#pragma unroll
+  for (int i = 0; i < C::kSlots; i += 2) {
+    if (i & 2) {
+      produce(QAT_SUB(2), false);
+      produce(QAT_SUB(3), false);
+    } else {
+      produce(QAT_SUB(0), i == 0);
+      produce(QAT_SUB(1), false);
+    }
   }
 
   // Waits for the oldest slot; returns its address.
@@ -410,12 +450,13 @@ __global__ void __launch_bounds__(32 * kWarps, 1) decode_kernel(const Params p) 
     return s;
   };
 
-  constexpr int KS = D / 16;   // k-steps of Q K^T
-  constexpr int NT = D / 8;    // n-tiles of P V
-  uint32_t qa[KS][4];
-  float o[NT][4];
-  float m[2], l[2], rf[2], vref = 0.f;
-  int last[2];                 // the newest key each of the lane's two rows sees
+  constexpr int KS = D / 16;   // k-steps of K Q^T
+  constexpr int MT = D / 16;   // row tiles of V^T P^T; a lane's channels are (D / 8) g + 0 .. D / 8 - 1
+  uint32_t qb[NR][KS][2];
+  float o[NR][MT][4];
+  float2 m[NR], l[NR], rf[NR];  // of rows 8 n + 2t and 8 n + 2t + 1
+  int last[NR][2];              // the newest key each of those rows sees
+  float vref = 0.f;
   bool begun = false;
   if (lane == 0) ws->meta[id] = WorkerMeta{-1, -1};
   int first_tile = cc.tile;    // of the current segment
@@ -424,230 +465,244 @@ __global__ void __launch_bounds__(32 * kWarps, 1) decode_kernel(const Params p) 
     if (!begun) {
       begun = true;
       first_tile = cc.tile;
-      load_rows<D>(p, cc, g, t, qa, rf);
+      load_rows<D, NR>(p, cc, g, t, qb, rf);
 #pragma unroll
-      for (int x = 0; x < 2; ++x) {
-        m[x] = -INFINITY;
-        l[x] = 0.f;
-        last[x] = cc.len - a.T + (cc.mt * kRows + g + 8 * x) % a.T;
+      for (int n = 0; n < NR; ++n) {
+        m[n] = make_float2(-INFINITY, -INFINITY);
+        l[n] = make_float2(0.f, 0.f);
+#pragma unroll
+        for (int y = 0; y < 2; ++y)
+          last[n][y] = cc.len - a.T + (cc.mt * p.rows + 8 * n + 2 * t + y) % a.T;
+#pragma unroll
+        for (int j = 0; j < MT; ++j) o[n][j][0] = o[n][j][1] = o[n][j][2] = o[n][j][3] = 0.f;
       }
-#pragma unroll
-      for (int j = 0; j < NT; ++j) o[j][0] = o[j][1] = o[j][2] = o[j][3] = 0.f;
       vref = 0.f;
     }
 
-    // S = Q K^T of 64 keys, times the keys' scales (and, below, the rows')
-    float s[8][4];
-    {
+    // S^T = K Q^T of 64 keys, times the keys' scales (and, below, the rows'): chunk c's values are
+    // keys g and g + 8 of rows 2t, 2t + 1
+    float s[NR][4][4];
+    float vs[4][2];  // the values' scales of those keys
+#pragma unroll
+    for (int hf = 0; hf < 2; ++hf) {
       const uint32_t slot = consume();
 #pragma unroll
-      for (int c = 0; c < 2; ++c) {  // 32 keys: four independent chains of products
+      for (int n = 0; n < NR; ++n)
 #pragma unroll
-        for (int nt = 0; nt < 4; ++nt)
-          s[4 * c + nt][0] = s[4 * c + nt][1] = s[4 * c + nt][2] = s[4 * c + nt][3] = 0.f;
+        for (int c = 0; c < 2; ++c)
+          s[n][2 * hf + c][0] = s[n][2 * hf + c][1] = s[n][2 * hf + c][2] = s[n][2 * hf + c][3] = 0.f;
 #pragma unroll
-        for (int h = 0; h < D / 64; ++h) {
-          uint32_t w[4][4];
+      for (int h = 0; h < D / 64; ++h) {
+        uint32_t w[4][4];
 #pragma unroll
-          for (int nt = 0; nt < 4; ++nt) {
-            const uint4 x = lds128(slot + (4 * c + nt) * 8 * D + k_off<D>(g, t + 4 * h));
-            w[nt][0] = x.x; w[nt][1] = x.y; w[nt][2] = x.z; w[nt][3] = x.w;
+        for (int k = 0; k < 4; ++k) {
+          const uint4 x = lds128(slot + 8 * k * D + k_off<D>(g, t + 4 * h));
+          w[k][0] = x.x; w[k][1] = x.y; w[k][2] = x.z; w[k][3] = x.w;
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            const uint32_t ka[4] = {codes_to_f16x2(static_cast<uint16_t>(w[2 * c][i])),
+                                    codes_to_f16x2(static_cast<uint16_t>(w[2 * c + 1][i])),
+                                    codes_to_f16x2(static_cast<uint16_t>(w[2 * c][i] >> 16)),
+                                    codes_to_f16x2(static_cast<uint16_t>(w[2 * c + 1][i] >> 16))};
+#pragma unroll
+            for (int n = 0; n < NR; ++n)
+              mma16816(s[n][2 * hf + c], ka, qb[n][4 * h + i][0], qb[n][4 * h + i][1]);
           }
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-#pragma unroll
-            for (int nt = 0; nt < 4; ++nt)
-              mma16816(s[4 * c + nt], qa[4 * h + i], codes_to_f16x2(static_cast<uint16_t>(w[nt][i])),
-                       codes_to_f16x2(static_cast<uint16_t>(w[nt][i] >> 16)));
-        }
-#pragma unroll
-        for (int nt = 0; nt < 4; ++nt) {
-          float (&acc)[4] = s[4 * c + nt];
-          const float2 ks = lds_f2(slot + kTile * D + 4 * (8 * (4 * c + nt) + 2 * t));
-          const float2 y0 = mul_rn_f32x2(make_float2(acc[0], acc[1]), ks);
-          const float2 y1 = mul_rn_f32x2(make_float2(acc[2], acc[3]), ks);
-          acc[0] = y0.x; acc[1] = y0.y; acc[2] = y1.x; acc[3] = y1.y;
-        }
       }
+#pragma unroll
+      for (int c = 0; c < 2; ++c)
+#pragma unroll
+        for (int y = 0; y < 2; ++y) {
+          const uint32_t at = slot + kHalf * D + 4 * (16 * c + 8 * y + g);
+          const float ks = lds_f(at);
+          vs[2 * hf + c][y] = lds_f(at + 4 * kHalf);
+#pragma unroll
+          for (int n = 0; n < NR; ++n) {
+            float* x = s[n][2 * hf + c] + 2 * y;
+            const float2 z = mul_rn_f32x2(make_float2(x[0], x[1]), make_float2(ks, ks));
+            x[0] = z.x;
+            x[1] = z.y;
+          }
+        }
       __syncwarp();
-      if constexpr (C::kSlots & 1) produce(V{}, false); else produce(K{}, false);
+      if (hf == 0) produce(QAT_SUB(C::kSlots), false); else produce(QAT_SUB(1 + C::kSlots), false);
     }
 
     // mask: only tiles that reach past what some row sees
-    const int key0 = cc.tile * kTile;
-    const bool edge = key0 + kTile > cc.len - a.T + 1;
+    const int key0 = cc.tile * kTile + g;
+    const bool edge = (cc.tile + 1) * kTile > cc.len - a.T + 1;
     if (edge) {
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const int k = key0 + 8 * j + 2 * t;
-        if (k > last[0]) s[j][0] = -INFINITY;
-        if (k + 1 > last[0]) s[j][1] = -INFINITY;
-        if (k > last[1]) s[j][2] = -INFINITY;
-        if (k + 1 > last[1]) s[j][3] = -INFINITY;
-      }
+      for (int n = 0; n < NR; ++n)
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            if (key0 + 16 * c + 8 * (i >> 1) > last[n][i & 1]) s[n][c][i] = -INFINITY;
     }
-    float alpha[2], inv[2], back[2];
-#pragma unroll
-    for (int x = 0; x < 2; ++x) {
-      float mt = s[0][2 * x];
-#pragma unroll
-      for (int j = 0; j < 8; ++j) mt = fmaxf(mt, fmaxf(s[j][2 * x], s[j][2 * x + 1]));
-      mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, 1));
-      mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, 2));
-      const float mn = fmaxf(m[x], mt * rf[x]);
-      const float ref = mn == -INFINITY ? 0.f : mn;
-      alpha[x] = ex2(m[x] - ref);
-      m[x] = mn;
-      const float2 r2 = make_float2(rf[x], rf[x]), n2 = make_float2(-ref, -ref);
-      float2 sum = make_float2(0.f, 0.f);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const float2 e = fma_rn_f32x2(make_float2(s[j][2 * x], s[j][2 * x + 1]), r2, n2);
-        const float2 pp = make_float2(ex2(e.x), ex2(e.y));
-        s[j][2 * x] = pp.x;
-        s[j][2 * x + 1] = pp.y;
-        sum = add_rn_f32x2(sum, pp);
-      }
-      l[x] = l[x] * alpha[x] + (sum.x + sum.y);
-      if (kQuant) {  // the tile's largest p is that of its largest score
-        const float amax = ex2(__fmaf_rn(mt, rf[x], -ref));
-        const TileScale ts = tile_scale(amax < kTinyP ? 0.f : amax);
-        inv[x] = ts.inv;
-        back[x] = ts.scale;
-      }
-    }
-    if (__any_sync(0xffffffffu, alpha[0] != 1.f || alpha[1] != 1.f)) scale_rows<NT>(o, alpha[0], alpha[1]);
 
-    // O += P V
-    {
-      const uint32_t slot = consume();
-      const uint32_t sc = slot + kTile * D + 8 * t;
-      float vmax = 0.f;
+    // a power of two above every value's scale so far; o is kept divided by it
+    float vmax = 0.f;
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const float2 v = lds_f2(sc + 32 * j);
-        vmax = fmaxf(vmax, fmaxf(v.x, v.y));
-      }
-      vmax = fmaxf(vmax, __shfl_xor_sync(0xffffffffu, vmax, 1));
-      vmax = fmaxf(vmax, __shfl_xor_sync(0xffffffffu, vmax, 2));
-      if (vmax > vref) {  // a power of two above every scale so far; o is kept divided by it
-        const int e = min(max(static_cast<int>(__float_as_uint(vmax) >> 23) - 126, -100), 126);
-        const float nref = __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
-        scale_rows<NT>(o, vref / nref, vref / nref);
-        vref = nref;
-      }
-      const float unit = vref > 0.f ? kPTop / vref : 0.f;
+    for (int c = 0; c < 4; ++c) vmax = fmaxf(vmax, fmaxf(vs[c][0], vs[c][1]));
+    vmax = max_over_g(vmax);
+    float grow = 1.f;
+    if (vmax > vref) {
+      const int e = min(max(static_cast<int>(__float_as_uint(vmax) >> 23) - 126, -100), 126);
+      const float nref = __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
+      grow = vref / nref;
+      vref = nref;
+    }
+    const float unit = vref > 0.f ? kPTop / vref : 0.f;
+
+    uint32_t pb[NR][4][2];
+#pragma unroll
+    for (int n = 0; n < NR; ++n) {
+      float2 mt = make_float2(s[n][0][0], s[n][0][1]);
 #pragma unroll
       for (int c = 0; c < 4; ++c) {
-        uint32_t pa[4];
+        mt.x = fmaxf(mt.x, fmaxf(s[n][c][0], s[n][c][2]));
+        mt.y = fmaxf(mt.y, fmaxf(s[n][c][1], s[n][c][3]));
+      }
+      mt.x = max_over_g(mt.x);
+      mt.y = max_over_g(mt.y);
+      const float2 mn = make_float2(fmaxf(m[n].x, mt.x * rf[n].x), fmaxf(m[n].y, mt.y * rf[n].y));
+      const float2 neg = make_float2(mn.x == -INFINITY ? 0.f : -mn.x, mn.y == -INFINITY ? 0.f : -mn.y);
+      const float2 alpha = make_float2(ex2(m[n].x + neg.x), ex2(m[n].y + neg.y));
+      m[n] = mn;
+      float2 sum = make_float2(0.f, 0.f);
 #pragma unroll
-        for (int nt = 0; nt < 2; ++nt) {
-          const int j = 2 * c + nt;
-          const float2 f = mul_rn_f32x2(lds_f2(sc + 32 * j), make_float2(unit, unit));
+      for (int c = 0; c < 4; ++c)
 #pragma unroll
-          for (int x = 0; x < 2; ++x) {
-            float2 w = make_float2(s[j][2 * x], s[j][2 * x + 1]);
-            if (kQuant) {
-              const float2 y = mul_rn_f32x2(w, make_float2(inv[x], inv[x]));
-              w = mul_rn_f32x2(e4m3x2_decode(e4m3x2_rn_satfinite(y.x, y.y)), make_float2(back[x], back[x]));
-            }
-            w = mul_rn_f32x2(w, f);
-            if (edge) {  // 0 x NaN: a key that the row does not see may hold anything
-              const int k = key0 + 8 * j + 2 * t;
-              if (k > last[x]) w.x = 0.f;
-              if (k + 1 > last[x]) w.y = 0.f;
-            }
-            pa[2 * nt + x] = f16x2(w.x, w.y);
-          }
+        for (int y = 0; y < 2; ++y) {
+          float* x = s[n][c] + 2 * y;
+          const float2 e = fma_rn_f32x2(make_float2(x[0], x[1]), rf[n], neg);
+          x[0] = ex2(e.x);
+          x[1] = ex2(e.y);
+          sum = add_rn_f32x2(sum, make_float2(x[0], x[1]));
         }
-        const uint32_t base = slot + c * kChunk * D;
-        constexpr int W = D / 32;  // words of a lane's run of a row: NT codes
-        uint32_t w[4][W];
-        if constexpr (D == 128) {
+      l[n] = fma_rn_f32x2(l[n], alpha, sum);
+      float2 inv, back;
+      if (kQuant) {  // the tile's largest p is that of its largest score
+        const float2 e = fma_rn_f32x2(mt, rf[n], neg);
+        const float ax = ex2(e.x), ay = ex2(e.y);
+        const TileScale tx = tile_scale(ax < kTinyP ? 0.f : ax), ty = tile_scale(ay < kTinyP ? 0.f : ay);
+        inv = make_float2(tx.inv, ty.inv);
+        back = make_float2(tx.scale, ty.scale);
+      }
+      const float2 f = make_float2(alpha.x * grow, alpha.y * grow);
+      if (__any_sync(0xffffffffu, f.x != 1.f || f.y != 1.f)) scale_rows<MT>(o[n], f);
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const uint4 v = lds128(base + v_off<D>(2 * t + (i & 1) + 8 * (i >> 1), g));
-            w[i][0] = v.x; w[i][1] = v.y; w[i][2] = v.z; w[i][3] = v.w;
+      for (int c = 0; c < 4; ++c)
+#pragma unroll
+        for (int y = 0; y < 2; ++y) {
+          float2 w = make_float2(s[n][c][2 * y], s[n][c][2 * y + 1]);
+          if (kQuant) {
+            const float2 q = mul_rn_f32x2(w, inv);
+            w = mul_rn_f32x2(e4m3x2_decode(e4m3x2_rn_satfinite(q.x, q.y)), back);
           }
-        } else {
+          const float v = vs[c][y] * unit;
+          w = mul_rn_f32x2(w, make_float2(v, v));
+          if (edge) {  // 0 x NaN: a key that the row does not see may hold anything
+            if (key0 + 16 * c + 8 * y > last[n][0]) w.x = 0.f;
+            if (key0 + 16 * c + 8 * y > last[n][1]) w.y = 0.f;
+          }
+          pb[n][c][y] = transpose8x8(f16x2(w.x, w.y));
+        }
+    }
+
+    // O^T += V^T P^T
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const uint2 v = lds64(base + v_off<D>(2 * t + (i & 1) + 8 * (i >> 1), g >> 1) + ((g & 1) << 3));
+    for (int hf = 0; hf < 2; ++hf) {
+      const uint32_t slot = consume();
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        const uint32_t base = slot + c * kChunk * D;
+        constexpr int W = D / 32;  // words of a lane's run of a row
+        uint32_t w[4][W];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int r = 2 * t + (i & 1) + 8 * (i >> 1);
+          if constexpr (D == 128) {
+            const uint4 v = lds128(base + v_off<D>(r, g));
+            w[i][0] = v.x; w[i][1] = v.y; w[i][2] = v.z; w[i][3] = v.w;
+          } else {
+            const uint2 v = lds64(base + v_off<D>(r, g >> 1) + ((g & 1) << 3));
             w[i][0] = v.x; w[i][1] = v.y;
           }
         }
 #pragma unroll
-        for (int i = 0; i < W; ++i) {  // bytes of two keys interleaved, four channels
-          const uint32_t a0 = __byte_perm(w[0][i], w[1][i], 0x5140), a1 = __byte_perm(w[0][i], w[1][i], 0x7362);
-          const uint32_t b0 = __byte_perm(w[2][i], w[3][i], 0x5140), b1 = __byte_perm(w[2][i], w[3][i], 0x7362);
-          mma16816(o[4 * i], pa, codes_to_f16x2(static_cast<uint16_t>(a0)), codes_to_f16x2(static_cast<uint16_t>(b0)));
-          mma16816(o[4 * i + 1], pa, codes_to_f16x2(static_cast<uint16_t>(a0 >> 16)), codes_to_f16x2(static_cast<uint16_t>(b0 >> 16)));
-          mma16816(o[4 * i + 2], pa, codes_to_f16x2(static_cast<uint16_t>(a1)), codes_to_f16x2(static_cast<uint16_t>(b1)));
-          mma16816(o[4 * i + 3], pa, codes_to_f16x2(static_cast<uint16_t>(a1 >> 16)), codes_to_f16x2(static_cast<uint16_t>(b1 >> 16)));
-        }
+        for (int i = 0; i < W; ++i)
+#pragma unroll
+          for (int z = 0; z < 2; ++z) {  // bytes of two keys interleaved, two channels
+            const uint32_t x = __byte_perm(w[0][i], w[1][i], z ? 0x7362 : 0x5140);
+            const uint32_t y = __byte_perm(w[2][i], w[3][i], z ? 0x7362 : 0x5140);
+            const uint32_t va[4] = {codes_to_f16x2(static_cast<uint16_t>(x)),
+                                    codes_to_f16x2(static_cast<uint16_t>(x >> 16)),
+                                    codes_to_f16x2(static_cast<uint16_t>(y)),
+                                    codes_to_f16x2(static_cast<uint16_t>(y >> 16))};
+#pragma unroll
+            for (int n = 0; n < NR; ++n)
+              mma16816(o[n][2 * i + z], va, pb[n][2 * hf + c][0], pb[n][2 * hf + c][1]);
+          }
       }
       __syncwarp();
-      if constexpr (C::kSlots & 1) produce(K{}, false); else produce(V{}, false);
+      if (hf == 0) produce(QAT_SUB(2 + C::kSlots), false); else produce(QAT_SUB(3 + C::kSlots), false);
     }
 
     const bool ends = cc.tile + 1 == cc.tiles;
     if (ends || u + 1 == u1) {  // the segment's end
       begun = false;
-      const float unit = vref * (1.f / kPTop);
-#pragma unroll
-      for (int x = 0; x < 2; ++x) {
-        l[x] += __shfl_xor_sync(0xffffffffu, l[x], 1);
-        l[x] += __shfl_xor_sync(0xffffffffu, l[x], 2);
+      const bool head = first_tile != 0;
+      const bool whole = !head && ends;
+      if (!whole && !head && lane == 0) {
+        const long long end = u - cc.tile + cc.tiles;  // the unit behind the item
+        ws->meta[id] = WorkerMeta{item_of(p, cc), static_cast<int>((end * workers - 1) / W)};
       }
-      if (first_tile == 0 && ends) {  // the whole item: its output
+      const float scale = vref * (1.f / kPTop);
 #pragma unroll
-        for (int x = 0; x < 2; ++x) {
-          const int r = cc.mt * kRows + g + 8 * x;
-          if (r >= p.R) continue;
-          const size_t row = (static_cast<size_t>(cc.b) * a.Hkv + cc.h) * p.R + r;
-          const bool none = l[x] == 0.f;
-          const float f = none ? 0.f : unit / l[x];
-          // columns 2t and 2t + 1 of n-tile j are channels NT (2t) + j and NT (2t + 1) + j
-          uint32_t w[NT];
+      for (int n = 0; n < NR; ++n) {
+        l[n].x = sum_over_g(l[n].x);
+        l[n].y = sum_over_g(l[n].y);
 #pragma unroll
-          for (int y = 0; y < 2; ++y)
+        for (int y = 0; y < 2; ++y) {
+          const int r = 8 * n + 2 * t + y;
+          if (cc.mt * p.rows + r >= p.R) continue;
+          const float lr = y ? l[n].y : l[n].x, mr = y ? m[n].y : m[n].x;
+          if (whole) {  // the item's output
+            const size_t row = (static_cast<size_t>(cc.b) * a.Hkv + cc.h) * p.R + cc.mt * p.rows + r;
+            const bool none = lr == 0.f;
+            const float f = none ? 0.f : scale / lr;
+            uint32_t w[MT];
 #pragma unroll
-            for (int j = 0; j < NT / 2; ++j) {
-              const float lo = none ? 0.f : o[2 * j][2 * x + y] * f;
-              const float hi = none ? 0.f : o[2 * j + 1][2 * x + y] * f;
-              const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
-              w[y * NT / 2 + j] = *reinterpret_cast<const uint32_t*>(&v);
+            for (int j = 0; j < MT; ++j) {
+              const __nv_bfloat162 v = __floats2bfloat162_rn(none ? 0.f : o[n][j][y] * f,
+                                                             none ? 0.f : o[n][j][2 + y] * f);
+              w[j] = *reinterpret_cast<const uint32_t*>(&v);
             }
-          uint4* dst = reinterpret_cast<uint4*>(a.o + row * D + 2 * NT * t);
+            uint4* dst = reinterpret_cast<uint4*>(a.o + row * D + D / 8 * g);
 #pragma unroll
-          for (int j = 0; j < NT / 4; ++j)
-            dst[j] = make_uint4(w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
-          if (t == 0 && a.lse != nullptr) a.lse[row] = none ? -INFINITY : m[x] + log2f(l[x]);
-        }
-      } else {
-        const bool head = first_tile != 0;
-        Partial<D>& part = ws->part[id][head ? 0 : 1];
-        if (!head && lane == 0) {
-          const long long end = u - cc.tile + cc.tiles;  // the unit behind the item
-          ws->meta[id] = WorkerMeta{item_of(p, cc), static_cast<int>((end * workers - 1) / W)};
-        }
+            for (int j = 0; j < MT / 4; ++j)
+              dst[j] = make_uint4(w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
+            if (g == 0 && a.lse != nullptr) a.lse[row] = none ? -INFINITY : mr + log2f(lr);
+          } else {
+            Partial<D>& part = ws->part[id][head ? 0 : 1];
+            if (g == 0) *reinterpret_cast<float2*>(part.ml[r]) = make_float2(mr, lr);
 #pragma unroll
-        for (int x = 0; x < 2; ++x) {
-          const int r = g + 8 * x;
-          if (cc.mt * kRows + r >= p.R) continue;
-          if (t == 0) *reinterpret_cast<float2*>(part.ml[r]) = make_float2(m[x], l[x]);
-#pragma unroll
-          for (int y = 0; y < 2; ++y)
-#pragma unroll
-            for (int j = 0; j < NT / 4; ++j)
-              *reinterpret_cast<float4*>(&part.o[r][NT * (2 * t + y) + 4 * j]) =
-                  make_float4(o[4 * j][2 * x + y] * unit, o[4 * j + 1][2 * x + y] * unit,
-                              o[4 * j + 2][2 * x + y] * unit, o[4 * j + 3][2 * x + y] * unit);
+            for (int j = 0; j < MT / 2; ++j)
+              *reinterpret_cast<float4*>(&part.o[r][D / 8 * g + 4 * j]) =
+                  make_float4(o[n][2 * j][y] * scale, o[n][2 * j][2 + y] * scale,
+                              o[n][2 * j + 1][y] * scale, o[n][2 * j + 1][2 + y] * scale);
+          }
         }
       }
     }
     advance(p, cc);
   }
+#undef QAT_SUB
   cp_wait<0>();
 }
 
@@ -711,7 +766,7 @@ template <int D>
 __device__ __forceinline__ void store_row(const Params& p, int item, int r, int lane,
                                           const Sum<D / 32>& s) {
   constexpr int V = D / 32;
-  const size_t row = static_cast<size_t>(item / p.mtiles) * p.R + item % p.mtiles * kRows + r;
+  const size_t row = static_cast<size_t>(item / p.mtiles) * p.R + item % p.mtiles * p.rows + r;
   const bool none = s.l == 0.f;
   const float f = none ? 0.f : 1.f / s.l;
   uint32_t out[V / 2];
@@ -732,20 +787,22 @@ __device__ __forceinline__ void store_row(const Params& p, int item, int r, int 
 // Adds the partials of the items that ranges cut.  Block (x, r) takes row r of the items that the
 // ranges of workers 8 x .. 8 x + 7 begin and do not end: one warp each, or all eight warps together
 // where an item's chain of partials is long.
+constexpr int kMergeWarps = 8;
+
 template <int D>
-__global__ void __launch_bounds__(32 * kWarps) decode_merge_kernel(const Params p) {
+__global__ void __launch_bounds__(32 * kMergeWarps) decode_merge_kernel(const Params p) {
   constexpr int V = D / 32;
   constexpr int kShort = 16;
-  __shared__ float acc[kWarps][D], ml[kWarps][2];
+  __shared__ float acc[kMergeWarps][D], ml[kMergeWarps][2];
   asm volatile("griddepcontrol.wait;" ::: "memory");  // the partials are complete
   const Workspace<D>* ws = static_cast<const Workspace<D>*>(p.a.ws);
-  const int w0 = blockIdx.x * kWarps, r = blockIdx.y;
+  const int w0 = blockIdx.x * kMergeWarps, r = blockIdx.y;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int workers = ws->workers;
   if (w0 >= workers) return;
   WorkerMeta mine = {-1, -1};
-  if (lane < kWarps && w0 + lane < workers) mine = ws->meta[w0 + lane];
-  const bool cut = mine.tail >= 0 && mine.tail % p.mtiles * kRows + r < p.R;
+  if (lane < kMergeWarps && w0 + lane < workers) mine = ws->meta[w0 + lane];
+  const bool cut = mine.tail >= 0 && mine.tail % p.mtiles * p.rows + r < p.R;
   const int n = cut ? mine.last - (w0 + lane) + 1 : 0;
   Sum<V> sum;
   {
@@ -761,7 +818,7 @@ __global__ void __launch_bounds__(32 * kWarps) decode_merge_kernel(const Params 
     const int k = __ffs(rest) - 1;
     rest &= rest - 1;
     sum.clear();
-    add_chain<D>(ws, w0 + k, warp, kWarps, __shfl_sync(0xffffffffu, n, k), r, lane, sum);
+    add_chain<D>(ws, w0 + k, warp, kMergeWarps, __shfl_sync(0xffffffffu, n, k), r, lane, sum);
 #pragma unroll
     for (int i = 0; i < V; ++i) acc[warp][V * lane + i] = sum.acc[i];
     if (lane == 0) {
@@ -771,7 +828,7 @@ __global__ void __launch_bounds__(32 * kWarps) decode_merge_kernel(const Params 
     __syncthreads();
     const int item = __shfl_sync(0xffffffffu, mine.tail, k);
     if (warp == 0) {
-      for (int x = 1; x < kWarps; ++x) {
+      for (int x = 1; x < kMergeWarps; ++x) {
         float o2[V];
 #pragma unroll
         for (int i = 0; i < V; ++i) o2[i] = acc[x][V * lane + i];
@@ -783,19 +840,21 @@ __global__ void __launch_bounds__(32 * kWarps) decode_merge_kernel(const Params 
   }
 }
 
-template <int D, bool kQuant>
+template <int D, int NR, bool kQuant>
 cudaError_t run(const Params& p, int ctas, cudaStream_t s) {
-  const size_t smem = Cfg<D>::kSmem + sizeof(int) * (p.a.B + 1);
-  cudaError_t e = cudaFuncSetAttribute(decode_kernel<D, kQuant>,
+  using C = Cfg<D, NR>;
+  const size_t smem = C::kSmem + sizeof(int) * (C::kWarps + p.a.B + 1);
+  cudaError_t e = cudaFuncSetAttribute(decode_kernel<D, NR, kQuant>,
                                        cudaFuncAttributeMaxDynamicSharedMemorySize,
                                        static_cast<int>(smem));
   if (e != cudaSuccess) return e;
-  decode_kernel<D, kQuant><<<ctas, 32 * kWarps, smem, s>>>(p);
+  decode_kernel<D, NR, kQuant><<<ctas, 32 * C::kWarps, smem, s>>>(p);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(ctas, p.R < kRows ? p.R : kRows);
-  cfg.blockDim = dim3(32 * kWarps);
+  const int most = ctas * C::kWarps;
+  cfg.gridDim = dim3((most + kMergeWarps - 1) / kMergeWarps, p.R < p.rows ? p.R : p.rows);
+  cfg.blockDim = dim3(32 * kMergeWarps);
   cfg.stream = s;
   cudaLaunchAttribute at[1];
   at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -815,14 +874,19 @@ cudaError_t launch_decode(const DecodeArgs& a, int D, int num_sms, cudaStream_t 
   Params p;
   p.a = a;
   p.R = a.Hq / a.Hkv * a.T;
-  p.mtiles = (p.R + kRows - 1) / kRows;
+  p.rows = p.R <= 8 ? 8 : kRows;
+  p.mtiles = (p.R + p.rows - 1) / p.rows;
   // one CTA per SM, fewer when the table cannot hold a unit for each
   const long long cap = static_cast<long long>(a.max_pages) << a.page_shift;
   const long long units = static_cast<long long>(a.B) * a.Hkv * p.mtiles * ((cap + kTile - 1) / kTile);  // >= 1
   int ctas = num_sms < kMaxCtas ? num_sms : kMaxCtas;
   if (units < ctas) ctas = static_cast<int>(units);
-  if (D == 64) return a.quant ? run<64, true>(p, ctas, s) : run<64, false>(p, ctas, s);
-  return a.quant ? run<128, true>(p, ctas, s) : run<128, false>(p, ctas, s);
+  if (p.rows == 8) {
+    if (D == 64) return a.quant ? run<64, 1, true>(p, ctas, s) : run<64, 1, false>(p, ctas, s);
+    return a.quant ? run<128, 1, true>(p, ctas, s) : run<128, 1, false>(p, ctas, s);
+  }
+  if (D == 64) return a.quant ? run<64, 2, true>(p, ctas, s) : run<64, 2, false>(p, ctas, s);
+  return a.quant ? run<128, 2, true>(p, ctas, s) : run<128, 2, false>(p, ctas, s);
 }
 
 }  // namespace qat
