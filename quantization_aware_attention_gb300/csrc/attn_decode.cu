@@ -53,7 +53,7 @@ constexpr int kHalf = 32;    // keys per ring slot
 constexpr int kChunk = 16;   // keys that certainly share a page
 constexpr int kRows = 16;    // query rows per item at most
 constexpr int kMaxCtas = 152;
-constexpr int kMaxWarps = 12;
+constexpr int kMaxWarps = 16;
 constexpr int kWorkers = kMaxCtas * kMaxWarps;
 constexpr float kTinyP = 7.888609052210118e-31f;  // 2^-100: a tile below it counts as zero (448 / amax
                                                   // must stay finite)
@@ -61,11 +61,11 @@ constexpr float kPTop = 16384.f;  // P x value scale / bound is at most this
 constexpr uint32_t kNoPage = 0xffffffffu, kBadPage = 0xfffffffeu;
 
 // NR: column tiles of 8 query rows per item, 1 or 2.  One tile needs half the registers, which
-// makes room for half as many warps again.
+// makes room for more warps (B64 ragged, D = 128: 104 us with 12, 108 with 16 warps of fewer slots).
 template <int D, int NR>
 struct Cfg {
-  static constexpr int kWarps = NR == 1 ? 12 : 8;
-  static constexpr int kSlots = D == 128 ? (NR == 1 ? 4 : 6) : (NR == 1 ? 6 : 10);
+  static constexpr int kWarps = NR == 1 ? (D == 128 ? 12 : 16) : 8;
+  static constexpr int kSlots = D == 128 ? (NR == 1 ? 4 : 6) : (NR == 1 ? 5 : 10);
   static constexpr int kSlotBytes = kHalf * D + 8 * kHalf;  // codes; in K slots the scales of K and V
   static constexpr int kRing = kSlots * kSlotBytes;
   static constexpr int kSmem = kWarps * kRing;  // then the warps' sums and B + 1 prefix sums
@@ -431,14 +431,11 @@ __global__ void __launch_bounds__(32 * Cfg<D, NR>::kWarps, 1) decode_kernel(cons
   };
 #define QAT_SUB(i) std::integral_constant<int, (i) & 3>{}
 #pragma unroll
-  for (int i = 0; i < C::kSlots; i += 2) {
-    if (i & 2) {
-      produce(QAT_SUB(2), false);
-      produce(QAT_SUB(3), false);
-    } else {
-      produce(QAT_SUB(0), i == 0);
-      produce(QAT_SUB(1), false);
-    }
+  for (int i = 0; i < C::kSlots; ++i) {
+    if ((i & 3) == 0) produce(QAT_SUB(0), i == 0);
+    if ((i & 3) == 1) produce(QAT_SUB(1), false);
+    if ((i & 3) == 2) produce(QAT_SUB(2), false);
+    if ((i & 3) == 3) produce(QAT_SUB(3), false);
   }
 
   // Waits for the oldest slot; returns its address.
@@ -798,10 +795,22 @@ __global__ void __launch_bounds__(32 * kMergeWarps) decode_merge_kernel(const Pa
   const Workspace<D>* ws = static_cast<const Workspace<D>*>(p.a.ws);
   const int w0 = blockIdx.x * kMergeWarps, r = blockIdx.y;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int workers = ws->workers;
+  // one round trip: the count, the chains' ends and the first partials of this warp's chain, which
+  // mean nothing (and are not used) where there is no chain
+  const int workers = __ldcg(&ws->workers);
+  int2 raw = make_int2(-1, -1);
+  if (lane < kMergeWarps) raw = __ldcg(reinterpret_cast<const int2*>(&ws->meta[w0 + lane]));
+  float x0[2][V];
+  float2 ml0[2];
+#pragma unroll
+  for (int c = 0; c < 2; ++c) {
+    const Partial<D>* part = &ws->part[min(w0 + warp + c, kWorkers - 1)][c == 0 ? 1 : 0];
+    ml0[c] = __ldcg(reinterpret_cast<const float2*>(part->ml[r]));
+    load_v<V>(x0[c], part->o[r] + V * lane);
+  }
   if (w0 >= workers) return;
   WorkerMeta mine = {-1, -1};
-  if (lane < kMergeWarps && w0 + lane < workers) mine = ws->meta[w0 + lane];
+  if (w0 + lane < workers) mine = WorkerMeta{raw.x, raw.y};
   const bool cut = mine.tail >= 0 && mine.tail % p.mtiles * p.rows + r < p.R;
   const int n = cut ? mine.last - (w0 + lane) + 1 : 0;
   Sum<V> sum;
@@ -809,7 +818,9 @@ __global__ void __launch_bounds__(32 * kMergeWarps) decode_merge_kernel(const Pa
     const int len = __shfl_sync(0xffffffffu, n, warp), item = __shfl_sync(0xffffffffu, mine.tail, warp);
     if (len > 0 && len <= kShort) {
       sum.clear();
-      add_chain<D>(ws, w0 + warp, 0, 1, len, r, lane, sum);
+      sum.add(ml0[0].x, ml0[0].y, x0[0]);
+      sum.add(ml0[1].x, ml0[1].y, x0[1]);  // a chain has two partials at least
+      add_chain<D>(ws, w0 + warp, 2, 1, len, r, lane, sum);
       store_row<D>(p, item, r, lane, sum);
     }
   }
@@ -841,7 +852,7 @@ __global__ void __launch_bounds__(32 * kMergeWarps) decode_merge_kernel(const Pa
 }
 
 template <int D, int NR, bool kQuant>
-cudaError_t run(const Params& p, int ctas, cudaStream_t s) {
+cudaError_t run(const Params& p, int ctas, long long units, cudaStream_t s) {
   using C = Cfg<D, NR>;
   const size_t smem = C::kSmem + sizeof(int) * (C::kWarps + p.a.B + 1);
   cudaError_t e = cudaFuncSetAttribute(decode_kernel<D, NR, kQuant>,
@@ -852,7 +863,7 @@ cudaError_t run(const Params& p, int ctas, cudaStream_t s) {
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
-  const int most = ctas * C::kWarps;
+  const int most = static_cast<int>(units < ctas * C::kWarps ? units : ctas * C::kWarps);
   cfg.gridDim = dim3((most + kMergeWarps - 1) / kMergeWarps, p.R < p.rows ? p.R : p.rows);
   cfg.blockDim = dim3(32 * kMergeWarps);
   cfg.stream = s;
@@ -882,11 +893,11 @@ cudaError_t launch_decode(const DecodeArgs& a, int D, int num_sms, cudaStream_t 
   int ctas = num_sms < kMaxCtas ? num_sms : kMaxCtas;
   if (units < ctas) ctas = static_cast<int>(units);
   if (p.rows == 8) {
-    if (D == 64) return a.quant ? run<64, 1, true>(p, ctas, s) : run<64, 1, false>(p, ctas, s);
-    return a.quant ? run<128, 1, true>(p, ctas, s) : run<128, 1, false>(p, ctas, s);
+    if (D == 64) return a.quant ? run<64, 1, true>(p, ctas, units, s) : run<64, 1, false>(p, ctas, units, s);
+    return a.quant ? run<128, 1, true>(p, ctas, units, s) : run<128, 1, false>(p, ctas, units, s);
   }
-  if (D == 64) return a.quant ? run<64, 2, true>(p, ctas, s) : run<64, 2, false>(p, ctas, s);
-  return a.quant ? run<128, 2, true>(p, ctas, s) : run<128, 2, false>(p, ctas, s);
+  if (D == 64) return a.quant ? run<64, 2, true>(p, ctas, units, s) : run<64, 2, false>(p, ctas, units, s);
+  return a.quant ? run<128, 2, true>(p, ctas, units, s) : run<128, 2, false>(p, ctas, units, s);
 }
 
 }  // namespace qat
