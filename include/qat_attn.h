@@ -386,13 +386,14 @@ QAT_API qat_status_t qat_kv_cache_read(const void* k_codes, const void* v_codes,
  *   A row that sees no key (position < 0) gets o = 0 and lse = -inf.
  *   Only keys that a row sees can reach its output: what lies behind the sequence's end in its last
  *   page, or in newer tokens' rows, may be anything the append can have stored, NaN rows included.
- *   workspace  at least qat_attn_decode_workspace_bytes(D) bytes, 256-byte aligned; contents ignored
- *            on entry, unspecified on exit.  Two calls that may overlap need two workspaces.
+ *   workspace  at least qat_attn_decode_workspace_bytes(Hq, Hkv, T, D) bytes (0 for invalid sizes),
+ *            256-byte aligned; contents ignored on entry, unspecified on exit.  Two calls that may
+ *            overlap need two workspaces.
  *   The work is split by the lengths on the device; the same lengths give the same bits.
  * Errors: as the cache's entries, QAT_ERR_UNSUPPORTED also for T or B above the limits or more than
  *   2^31 64-key tiles; QAT_ERR_WORKSPACE.  Pages outside the cache give NaN rows (see above).
  */
-QAT_API size_t qat_attn_decode_workspace_bytes(int D);
+QAT_API size_t qat_attn_decode_workspace_bytes(int Hq, int Hkv, int T, int D);
 QAT_API qat_status_t qat_attn_decode(const void* q, const void* k_codes, const void* v_codes,
                                      const float* k_scales, const float* v_scales,
                                      const int* block_table, const int* seq_lens, void* o,

@@ -142,7 +142,7 @@ def qat_attention_decode(q, cache: KVCache, block_table, seq_lens, sm_scale: flo
     its own.  Hq is a multiple of the cache's heads (consecutive query heads share one); T is at most
     16.  Returns o bf16 [B, Hq, T, D], and with ``return_lse`` the base-2 log-sum-exp fp32 [B, Hq, T].
     A row that sees no key gives o = 0, lse = -inf.  ``workspace``: uint8, at least
-    ``capi.qat_attn_decode_workspace_bytes(D)`` bytes, for one call at a time; allocated if None."""
+    ``capi.qat_attn_decode_workspace_bytes(Hq, cache.heads, T, D)`` bytes, for one call at a time; allocated if None."""
     if not isinstance(cache, KVCache):
         raise TypeError("cache must be a KVCache")
     B, max_pages = cache._tables(block_table, seq_lens)
@@ -155,7 +155,8 @@ def qat_attention_decode(q, cache: KVCache, block_table, seq_lens, sm_scale: flo
     if Hq < 1 or Hq % cache.heads:
         raise ValueError(f"{Hq} query heads do not share the cache's {cache.heads} evenly")
     if workspace is None:
-        workspace = torch.empty(capi.qat_attn_decode_workspace_bytes(D), dtype=torch.uint8, device=dev)
+        workspace = torch.empty(max(capi.qat_attn_decode_workspace_bytes(Hq, cache.heads, T, D), 256),
+                                dtype=torch.uint8, device=dev)
     elif not isinstance(workspace, torch.Tensor) or workspace.device != dev or (
             workspace.dtype != torch.uint8 or not workspace.is_contiguous()):
         raise ValueError(f"workspace must be a contiguous uint8 tensor on {dev}")

@@ -127,7 +127,7 @@ def lib() -> ctypes.CDLL:
         L.qat_kv_cache_append.restype = _i
         L.qat_kv_cache_read.argtypes = [_vp] * 8 + [_i] * 8 + [_vp]
         L.qat_kv_cache_read.restype = _i
-        L.qat_attn_decode_workspace_bytes.argtypes = [_i]
+        L.qat_attn_decode_workspace_bytes.argtypes = [_i] * 4
         L.qat_attn_decode_workspace_bytes.restype = _sz
         L.qat_attn_decode.argtypes = [_vp] * 9 + [_i] * 8 + [_f, _i, _vp, _sz, _vp]
         L.qat_attn_decode.restype = _i
@@ -294,8 +294,8 @@ def qat_kv_cache_read(k_codes, v_codes, k_scales, v_scales, block_table, seq_len
         _stream(stream)))
 
 
-def qat_attn_decode_workspace_bytes(D) -> int:
-    return int(lib().qat_attn_decode_workspace_bytes(D))
+def qat_attn_decode_workspace_bytes(Hq, Hkv, T, D) -> int:
+    return int(lib().qat_attn_decode_workspace_bytes(Hq, Hkv, T, D))
 
 
 def qat_attn_decode(q, k_codes, v_codes, k_scales, v_scales, block_table, seq_lens, o, lse, B, Hq, Hkv,

@@ -71,28 +71,35 @@ struct Cfg {
   static constexpr int kSmem = kWarps * kRing;  // then the warps' sums and B + 1 prefix sums
 };
 
-// Workspace: what each worker's range cut, then the partials.
+// Workspace: the header, what each worker's range cut, then the partials: two per worker, [0] of the
+// item its range ends or passes through ("head"), [1] of the item it begins and does not end ("tail"),
+// each rows x D sums and rows x (m, l).
+struct Header {
+  int workers;
+  int pad[31];
+};
 struct WorkerMeta {
   int tail;  // item that begins in this range and ends in a later one, or -1
   int last;  // the worker in whose range it ends
 };
-template <int D>
-struct Partial {
-  float o[kRows][D];
-  float ml[kRows][2];
-};
-template <int D>
-struct Workspace {
-  int workers;
-  int pad[31];
-  WorkerMeta meta[kWorkers];
-  Partial<D> part[kWorkers][2];  // [0] head, [1] tail
-};
+constexpr size_t kPartsAt = sizeof(Header) + kWorkers * sizeof(WorkerMeta);
+static_assert(kPartsAt % 16 == 0, "partials are read 16 bytes at a time");
 
 struct Params {
   DecodeArgs a;
   int R, rows, mtiles;  // rows of a KV head (Hq / Hkv heads x T tokens), of an item; items of a head
+  int prows;            // rows of a partial
 };
+
+__device__ __forceinline__ Header* header_of(const Params& p) { return static_cast<Header*>(p.a.ws); }
+__device__ __forceinline__ WorkerMeta* meta_of(const Params& p) {
+  return reinterpret_cast<WorkerMeta*>(static_cast<char*>(p.a.ws) + sizeof(Header));
+}
+template <int D>
+__device__ __forceinline__ float* partial_of(const Params& p, int worker, int which) {
+  return reinterpret_cast<float*>(static_cast<char*>(p.a.ws) + kPartsAt) +
+         (static_cast<size_t>(worker) * 2 + which) * p.prows * (D + 2);
+}
 
 __device__ __forceinline__ float ex2(float x) {
   float y;
@@ -319,11 +326,10 @@ __global__ void __launch_bounds__(32 * Cfg<D, NR>::kWarps, 1) decode_kernel(cons
     __syncthreads();
   }
   const int W = prefix[a.B];
-  Workspace<D>* ws = static_cast<Workspace<D>*>(a.ws);
   // workers: as few warps per CTA as give every worker a unit, spread over the CTAs
   const int per_cta = min(C::kWarps, (W + static_cast<int>(gridDim.x) - 1) / static_cast<int>(gridDim.x));
   const int workers = min(W, per_cta * static_cast<int>(gridDim.x));
-  if (blockIdx.x == 0 && tid == 0) ws->workers = workers;
+  if (blockIdx.x == 0 && tid == 0) header_of(p)->workers = workers;
   // the merge kernel's blocks may be brought up; they wait for this grid's end
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if (warp >= per_cta) return;
@@ -455,7 +461,7 @@ __global__ void __launch_bounds__(32 * Cfg<D, NR>::kWarps, 1) decode_kernel(cons
   int last[NR][2];              // the newest key each of those rows sees
   float vref = 0.f;
   bool begun = false;
-  if (lane == 0) ws->meta[id] = WorkerMeta{-1, -1};
+  if (lane == 0) meta_of(p)[id] = WorkerMeta{-1, -1};
   int first_tile = cc.tile;    // of the current segment
 
   for (int u = u0; u < u1; ++u) {
@@ -657,7 +663,7 @@ __global__ void __launch_bounds__(32 * Cfg<D, NR>::kWarps, 1) decode_kernel(cons
       const bool whole = !head && ends;
       if (!whole && !head && lane == 0) {
         const long long end = u - cc.tile + cc.tiles;  // the unit behind the item
-        ws->meta[id] = WorkerMeta{item_of(p, cc), static_cast<int>((end * workers - 1) / W)};
+        meta_of(p)[id] = WorkerMeta{item_of(p, cc), static_cast<int>((end * workers - 1) / W)};
       }
       const float scale = vref * (1.f / kPTop);
 #pragma unroll
@@ -686,11 +692,11 @@ __global__ void __launch_bounds__(32 * Cfg<D, NR>::kWarps, 1) decode_kernel(cons
               dst[j] = make_uint4(w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
             if (g == 0 && a.lse != nullptr) a.lse[row] = none ? -INFINITY : mr + log2f(lr);
           } else {
-            Partial<D>& part = ws->part[id][head ? 0 : 1];
-            if (g == 0) *reinterpret_cast<float2*>(part.ml[r]) = make_float2(mr, lr);
+            float* part = partial_of<D>(p, id, head ? 0 : 1);
+            if (g == 0) *reinterpret_cast<float2*>(part + p.prows * D + 2 * r) = make_float2(mr, lr);
 #pragma unroll
             for (int j = 0; j < MT / 2; ++j)
-              *reinterpret_cast<float4*>(&part.o[r][D / 8 * g + 4 * j]) =
+              *reinterpret_cast<float4*>(part + r * D + D / 8 * g + 4 * j) =
                   make_float4(o[n][2 * j][y] * scale, o[n][2 * j][2 + y] * scale,
                               o[n][2 * j + 1][y] * scale, o[n][2 * j + 1][2 + y] * scale);
           }
@@ -735,23 +741,27 @@ __device__ __forceinline__ void load_v(float (&x)[V], const float* src) {
   }
 }
 
+// Row r of worker w's partial `which`.
+template <int D>
+__device__ __forceinline__ void load_partial(const Params& p, int w, int which, int r, int lane, float2& ml,
+                                             float (&x)[D / 32]) {
+  const float* part = partial_of<D>(p, w, which);
+  ml = __ldcg(reinterpret_cast<const float2*>(part + p.prows * D + 2 * r));
+  load_v<D / 32>(x, part + r * D + D / 32 * lane);
+}
+
 // Adds partials first, first + step, ... up to n of the chain that begins with worker w's tail, four
 // loads ahead.
 template <int D>
-__device__ __forceinline__ void add_chain(const Workspace<D>* ws, int w, int first, int step, int n,
-                                          int r, int lane, Sum<D / 32>& sum) {
-  constexpr int V = D / 32;
+__device__ __forceinline__ void add_chain(const Params& p, int w, int first, int step, int n, int r,
+                                          int lane, Sum<D / 32>& sum) {
   for (int i = first; i < n; i += 4 * step) {
-    float x[4][V];
+    float x[4][D / 32];
     float2 ml[4];
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
       const int c = i + k * step;
-      if (c < n) {
-        const Partial<D>* part = &ws->part[w + c][c == 0 ? 1 : 0];
-        ml[k] = __ldcg(reinterpret_cast<const float2*>(part->ml[r]));
-        load_v<V>(x[k], part->o[r] + V * lane);
-      }
+      if (c < n) load_partial<D>(p, w + c, c == 0 ? 1 : 0, r, lane, ml[k], x[k]);
     }
 #pragma unroll
     for (int k = 0; k < 4; ++k)
@@ -792,22 +802,12 @@ __global__ void __launch_bounds__(32 * kMergeWarps) decode_merge_kernel(const Pa
   constexpr int kShort = 16;
   __shared__ float acc[kMergeWarps][D], ml[kMergeWarps][2];
   asm volatile("griddepcontrol.wait;" ::: "memory");  // the partials are complete
-  const Workspace<D>* ws = static_cast<const Workspace<D>*>(p.a.ws);
   const int w0 = blockIdx.x * kMergeWarps, r = blockIdx.y;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  // one round trip: the count, the chains' ends and the first partials of this warp's chain, which
-  // mean nothing (and are not used) where there is no chain
-  const int workers = __ldcg(&ws->workers);
+  // one round trip: the count and the chains' ends, which mean nothing beyond the count
+  const int workers = __ldcg(&header_of(p)->workers);
   int2 raw = make_int2(-1, -1);
-  if (lane < kMergeWarps) raw = __ldcg(reinterpret_cast<const int2*>(&ws->meta[w0 + lane]));
-  float x0[2][V];
-  float2 ml0[2];
-#pragma unroll
-  for (int c = 0; c < 2; ++c) {
-    const Partial<D>* part = &ws->part[min(w0 + warp + c, kWorkers - 1)][c == 0 ? 1 : 0];
-    ml0[c] = __ldcg(reinterpret_cast<const float2*>(part->ml[r]));
-    load_v<V>(x0[c], part->o[r] + V * lane);
-  }
+  if (lane < kMergeWarps) raw = __ldcg(reinterpret_cast<const int2*>(meta_of(p) + w0 + lane));
   if (w0 >= workers) return;
   WorkerMeta mine = {-1, -1};
   if (w0 + lane < workers) mine = WorkerMeta{raw.x, raw.y};
@@ -818,9 +818,7 @@ __global__ void __launch_bounds__(32 * kMergeWarps) decode_merge_kernel(const Pa
     const int len = __shfl_sync(0xffffffffu, n, warp), item = __shfl_sync(0xffffffffu, mine.tail, warp);
     if (len > 0 && len <= kShort) {
       sum.clear();
-      sum.add(ml0[0].x, ml0[0].y, x0[0]);
-      sum.add(ml0[1].x, ml0[1].y, x0[1]);  // a chain has two partials at least
-      add_chain<D>(ws, w0 + warp, 2, 1, len, r, lane, sum);
+      add_chain<D>(p, w0 + warp, 0, 1, len, r, lane, sum);
       store_row<D>(p, item, r, lane, sum);
     }
   }
@@ -829,7 +827,7 @@ __global__ void __launch_bounds__(32 * kMergeWarps) decode_merge_kernel(const Pa
     const int k = __ffs(rest) - 1;
     rest &= rest - 1;
     sum.clear();
-    add_chain<D>(ws, w0 + k, warp, kMergeWarps, __shfl_sync(0xffffffffu, n, k), r, lane, sum);
+    add_chain<D>(p, w0 + k, warp, kMergeWarps, __shfl_sync(0xffffffffu, n, k), r, lane, sum);
 #pragma unroll
     for (int i = 0; i < V; ++i) acc[warp][V * lane + i] = sum.acc[i];
     if (lane == 0) {
@@ -877,8 +875,13 @@ cudaError_t run(const Params& p, int ctas, long long units, cudaStream_t s) {
 
 }  // namespace
 
-size_t decode_workspace_bytes(int D) {
-  return D == 64 ? sizeof(Workspace<64>) : sizeof(Workspace<128>);
+namespace {
+// Rows of a partial, even so that partials stay 16-byte aligned.
+int partial_rows(int R) { return R >= kRows ? kRows : (R + 1) / 2 * 2; }
+}  // namespace
+
+size_t decode_workspace_bytes(int R, int D) {
+  return kPartsAt + static_cast<size_t>(kWorkers) * 2 * partial_rows(R) * (D + 2) * sizeof(float);
 }
 
 cudaError_t launch_decode(const DecodeArgs& a, int D, int num_sms, cudaStream_t s) {
@@ -887,6 +890,7 @@ cudaError_t launch_decode(const DecodeArgs& a, int D, int num_sms, cudaStream_t 
   p.R = a.Hq / a.Hkv * a.T;
   p.rows = p.R <= 8 ? 8 : kRows;
   p.mtiles = (p.R + p.rows - 1) / p.rows;
+  p.prows = partial_rows(p.R);
   // one CTA per SM, fewer when the table cannot hold a unit for each
   const long long cap = static_cast<long long>(a.max_pages) << a.page_shift;
   const long long units = static_cast<long long>(a.B) * a.Hkv * p.mtiles * ((cap + kTile - 1) / kTile);  // >= 1

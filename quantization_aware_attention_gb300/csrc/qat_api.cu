@@ -618,8 +618,12 @@ qat_status_t qat_kv_cache_read(const void* k_codes, const void* v_codes, const f
   return from_cuda(e);
 }
 
-size_t qat_attn_decode_workspace_bytes(int D) {
-  return D == 64 || D == 128 ? qat::decode_workspace_bytes(D) : 0;
+size_t qat_attn_decode_workspace_bytes(int Hq, int Hkv, int T, int D) {
+  if ((D != 64 && D != 128) || Hkv < 1 || Hq < 1 || Hq % Hkv != 0 || T < 0 ||
+      T > qat::kDecodeMaxTokens)
+    return 0;
+  const long long R = static_cast<long long>(Hq / Hkv) * T;
+  return qat::decode_workspace_bytes(static_cast<int>(R < 16 ? R : 16), D);
 }
 
 qat_status_t qat_attn_decode(const void* q, const void* k_codes, const void* v_codes,
@@ -646,7 +650,7 @@ qat_status_t qat_attn_decode(const void* q, const void* k_codes, const void* v_c
     return QAT_ERR_INVALID_ARG;
   if (q == nullptr || o == nullptr || !aligned16(q) || !aligned16(o)) return QAT_ERR_INVALID_ARG;
   if (lse != nullptr && (reinterpret_cast<uintptr_t>(lse) & 3u) != 0) return QAT_ERR_INVALID_ARG;
-  if (workspace == nullptr || workspace_bytes < qat_attn_decode_workspace_bytes(D))
+  if (workspace == nullptr || workspace_bytes < qat_attn_decode_workspace_bytes(Hq, Hkv, T, D))
     return QAT_ERR_WORKSPACE;
   if ((reinterpret_cast<uintptr_t>(workspace) & (kAlign - 1)) != 0) return QAT_ERR_INVALID_ARG;
   qat::DecodeArgs a = {};

@@ -221,7 +221,7 @@ struct DecodeArgs {
 
 constexpr int kDecodeMaxBatch = 4096;  // the kernel keeps the batch's prefix sums in shared memory
 constexpr int kDecodeMaxTokens = 16;
-size_t decode_workspace_bytes(int D);
+size_t decode_workspace_bytes(int R, int D);  // R = Hq / Hkv * T
 
 // Kernel launchers (return cudaGetLastError() after the launches).
 cudaError_t launch_norm_rope(NormRopeArgs a, int D, int num_sms, cudaStream_t s);

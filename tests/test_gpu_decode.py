@@ -118,6 +118,55 @@ def test_long_sequence():
     _check(q, lens, 2, 64, cache, table, codes, scales, 1)
 
 
+@pytest.mark.parametrize("D,Hq,Hkv,T", [(64, 16, 8, 1), (128, 8, 8, 1), (64, 24, 8, 3), (128, 16, 4, 4)])
+def test_batch_of_long_sequences(D, Hq, Hkv, T):
+    """Many tiles for every warp, items cut anywhere, one item cut many times: every row right, the same
+    bits in every run and in every replay of a captured call, with a workspace that holds anything."""
+    B, page = 24, 64
+    rng = np.random.default_rng(6)
+    lens = [int(x) for x in rng.integers(4000, 9000, B)]
+    lens[3], lens[7] = 65000, 1
+    if Hkv == 4:
+        lens = [2 * n for n in lens]
+    per = [(n + page - 1) // page for n in lens]
+    pages = sum(per)
+    order = rng.permutation(pages).astype(np.int32)
+    table = np.zeros((B, max(per)), np.int32)
+    at = 0
+    for b, n in enumerate(per):
+        table[b, :n] = order[at:at + n]
+        at += n
+    g = torch.Generator(device="cuda").manual_seed(3)
+    codes = [(torch.randn(pages, Hkv, page, D, generator=g, device="cuda") * 100).clamp(-448, 448).to(
+        torch.float8_e4m3fn) for _ in range(2)]
+    scales = [torch.rand(pages, Hkv, page, generator=g, device="cuda") * 0.02 + 0.002 for _ in range(2)]
+    cache = KVCache(codes[0], codes[1], scales[0], scales[1])
+    q = dev_bf16(normal_bf16(77, (B, Hq, T, D)))
+    args = (q, cache, _i32(table), _i32(lens))
+    o, lse = qat_attention_decode(*args, return_lse=True, check=True)
+    for b, h in ((0, 0), (3, Hkv - 1), (7, 1), (B - 1, Hkv - 1), (11, 2)):
+        n = lens[b]
+        t = torch.from_numpy(table[b, :per[b]]).cuda().long()
+        k, v = (so.dequant(c[t][:, h].reshape(-1, D)[:n].view(torch.uint8).cpu().numpy(),
+                           s[t][:, h].reshape(-1)[:n].cpu().numpy()) for c, s in zip(codes, scales))
+        for hq in range(h * (Hq // Hkv), (h + 1) * (Hq // Hkv)):
+            w, wl, tol, ltol = so.decode_head(host_f64(q[b, hq]), k, v, n - T + np.arange(T), D ** -0.5, 1)
+            assert (np.abs(host_f64(o[b, hq]) - w) <= tol).all()
+            assert (np.abs(host_f64(lse[b, hq]) - wl)[np.isfinite(wl)] <= ltol[np.isfinite(wl)]).all()
+    ws = torch.randint(0, 256, (capi.qat_attn_decode_workspace_bytes(Hq, Hkv, T, D),), dtype=torch.uint8,
+                       device="cuda")
+    for _ in range(3):
+        again = qat_attention_decode(*args, return_lse=True, workspace=ws)
+        assert torch.equal(o, again[0]) and torch.equal(lse, again[1])
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = qat_attention_decode(*args, workspace=ws)
+    for _ in range(4):
+        out.zero_()
+        graph.replay()
+        assert torch.equal(out, o)
+
+
 @pytest.mark.parametrize("quant", [0, 1])
 def test_peaked_scores_and_scales(quant):
     """Scores hundreds apart (tiles that underflow, the maximum rising tile by tile) and rows of V whose

@@ -81,8 +81,11 @@ def test_norm_rope_bwd_validation(kw, want):
 def test_workspace_sizes():
     assert capi.qat_qk_norm_rope_bwd_workspace_bytes(96) == 0
     assert capi.qat_qk_norm_rope_bwd_workspace_bytes(128) % 256 == 0
-    assert capi.qat_attn_decode_workspace_bytes(96) == 0
-    assert capi.qat_attn_decode_workspace_bytes(64) > 0
+    for bad in ((8, 2, 1, 96), (8, 3, 1, 64), (8, 0, 1, 64), (0, 1, 1, 64), (8, 2, -1, 64), (8, 2, 17, 64)):
+        assert capi.qat_attn_decode_workspace_bytes(*bad) == 0
+    # grows with the rows that share a KV head, up to 16
+    sizes = [capi.qat_attn_decode_workspace_bytes(hq, 2, 1, 64) for hq in (2, 8, 16, 32, 64)]
+    assert sizes[0] < sizes[1] < sizes[2] < sizes[3] == sizes[4]
 
 
 APPEND = dict(k=A, k_strides=None, v=A, v_strides=None, k_codes=A, v_codes=A, k_scales=A, v_scales=A,
