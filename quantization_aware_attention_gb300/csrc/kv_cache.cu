@@ -46,42 +46,40 @@ __device__ __forceinline__ int seq_len(const KvCacheArgs& p, int b) {
   return static_cast<int>(cap);
 }
 
+// max(|a|, |b|) of two bf16 pairs, NaN if either is.
+__device__ __forceinline__ uint32_t absmax_bf16x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a & 0x7fff7fffu), "r"(b & 0x7fff7fffu));
+  return r;
+}
+
+// amax is the largest magnitude itself, so it is taken on the bf16 bits; a NaN stays one, and an
+// infinity is one's own.
 template <int D>
 __device__ __forceinline__ void quant_store(const uint4 (&raw)[2], uint8_t* code, float* scale,
                                             size_t row, int j, bool in) {
   constexpr int L = D / 16;
-  float v[16];
-  float amax = 0.f;
-  bool bad = false;
+  const uint32_t x[8] = {raw[0].x, raw[0].y, raw[0].z, raw[0].w, raw[1].x, raw[1].y, raw[1].z, raw[1].w};
+  uint32_t mx = absmax_bf16x2(x[0], x[1]);
 #pragma unroll
-  for (int k = 0; k < 2; ++k) {
-    const __nv_bfloat162* h = reinterpret_cast<const __nv_bfloat162*>(&raw[k]);
+  for (int i = 2; i < 8; ++i) mx = absmax_bf16x2(mx, x[i]);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float2 f = __bfloat1622float2(h[i]);
-      v[8 * k + 2 * i] = f.x;
-      v[8 * k + 2 * i + 1] = f.y;
-    }
-  }
-#pragma unroll
-  for (int i = 0; i < 16; ++i) {
-    const float a = fabsf(v[i]);
-    amax = fmaxf(amax, a);
-    bad |= !(a <= 3.4028234663852886e38f);
-  }
-  if (bad) amax = __int_as_float(0x7f800000);
-#pragma unroll
-  for (int o = L / 2; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-  bad = amax > 3.4028234663852886e38f;
+  for (int o = L / 2; o > 0; o >>= 1) mx = absmax_bf16x2(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+  mx = absmax_bf16x2(mx, mx >> 16);
+  const float amax = __uint_as_float(mx << 16);
+  const bool bad = !(amax <= 3.4028234663852886e38f);
   const TileScale ts = tile_scale(bad || amax < kTinyRow ? 0.f : amax);
+  if (!in) return;
   uint32_t w[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const float2 x = mul_rn_f32x2(make_float2(v[4 * i], v[4 * i + 1]), make_float2(ts.inv, ts.inv));
-    const float2 y = mul_rn_f32x2(make_float2(v[4 * i + 2], v[4 * i + 3]), make_float2(ts.inv, ts.inv));
-    w[i] = e4m3x2_rn_satfinite(x.x, x.y) | static_cast<uint32_t>(e4m3x2_rn_satfinite(y.x, y.y)) << 16;
+    const uint32_t u = x[2 * i], v = x[2 * i + 1];
+    const float2 p = mul_rn_f32x2(make_float2(__uint_as_float(u << 16), __uint_as_float(u & 0xffff0000u)),
+                                  make_float2(ts.inv, ts.inv));
+    const float2 q = mul_rn_f32x2(make_float2(__uint_as_float(v << 16), __uint_as_float(v & 0xffff0000u)),
+                                  make_float2(ts.inv, ts.inv));
+    w[i] = e4m3x2_rn_satfinite(p.x, p.y) | static_cast<uint32_t>(e4m3x2_rn_satfinite(q.x, q.y)) << 16;
   }
-  if (!in) return;
   *reinterpret_cast<uint4*>(code + row * D + 16 * j) =
       bad ? make_uint4(0u, 0u, 0u, 0u) : make_uint4(w[0], w[1], w[2], w[3]);
   if (j == 0) scale[row] = bad ? __int_as_float(0x7fc00000) : ts.scale;
@@ -91,12 +89,12 @@ template <int D>
 __global__ void __launch_bounds__(kThreads) kv_append_kernel(const KvCacheArgs p) {
   constexpr int L = D / 16;
   const int j = threadIdx.x % L;
-  const long long row = (static_cast<long long>(blockIdx.x) * kThreads + threadIdx.x) / L;
-  const long long rows = static_cast<long long>(p.B) * p.H * p.N;
-  bool in = row < rows;
-  const int n = static_cast<int>(in ? row % p.N : 0);
-  const int bh = static_cast<int>(in ? row / p.N : 0);
-  const int b = bh / p.H, h = bh - b * p.H;
+  // at most 2^31 rows: 32-bit divisions
+  const unsigned row = blockIdx.x * (kThreads / L) + threadIdx.x / L;
+  bool in = row < static_cast<unsigned long long>(p.B) * p.H * p.N;
+  const unsigned bh = row / static_cast<unsigned>(p.N);
+  const int n = static_cast<int>(row - bh * p.N), b = static_cast<int>(bh / static_cast<unsigned>(p.H));
+  const int h = static_cast<int>(bh - static_cast<unsigned>(b) * p.H);
   uint4 rk[2], rv[2];
   rk[0] = rk[1] = rv[0] = rv[1] = make_uint4(0u, 0u, 0u, 0u);
   size_t at = 0;
@@ -124,6 +122,7 @@ __global__ void __launch_bounds__(kThreads) kv_append_kernel(const KvCacheArgs p
       }
     }
   }
+  if (!__any_sync(0xffffffffu, in)) return;  // padding
   quant_store<D>(rk, p.k_codes, p.k_scales, at, j, in);
   quant_store<D>(rv, p.v_codes, p.v_scales, at, j, in);
 }
@@ -147,12 +146,11 @@ template <int D>
 __global__ void __launch_bounds__(kThreads) kv_read_kernel(const KvCacheArgs p) {
   constexpr int L = D / 16;
   const int j = threadIdx.x % L;
-  const long long row = (static_cast<long long>(blockIdx.x) * kThreads + threadIdx.x) / L;
-  const long long rows = static_cast<long long>(p.B) * p.H * p.N;
-  if (row >= rows) return;
-  const int n = static_cast<int>(row % p.N);
-  const int bh = static_cast<int>(row / p.N);
-  const int b = bh / p.H, h = bh - b * p.H;
+  const unsigned row = blockIdx.x * (kThreads / L) + threadIdx.x / L;
+  if (row >= static_cast<unsigned long long>(p.B) * p.H * p.N) return;
+  const unsigned bh = row / static_cast<unsigned>(p.N);
+  const int n = static_cast<int>(row - bh * p.N), b = static_cast<int>(bh / static_cast<unsigned>(p.H));
+  const int h = static_cast<int>(bh - static_cast<unsigned>(b) * p.H);
   const long long pos = static_cast<long long>(p.begin) + n;
   uint4 ck = make_uint4(0u, 0u, 0u, 0u), cv = ck;
   float sk = 0.f, sv = 0.f;
@@ -168,8 +166,8 @@ __global__ void __launch_bounds__(kThreads) kv_read_kernel(const KvCacheArgs p) 
       sk = sv = __int_as_float(0x7fc00000);  // no page: the row reads as NaN
     }
   }
-  dequant_store(ck, sk, p.k_out + row * D + 16 * j);
-  dequant_store(cv, sv, p.v_out + row * D + 16 * j);
+  dequant_store(ck, sk, p.k_out + static_cast<size_t>(row) * D + 16 * j);
+  dequant_store(cv, sv, p.v_out + static_cast<size_t>(row) * D + 16 * j);
 }
 
 inline unsigned blocks_of(const KvCacheArgs& a, int D) {

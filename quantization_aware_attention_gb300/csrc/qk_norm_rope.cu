@@ -16,12 +16,18 @@
 // become an angle in [-pi, pi), where the hardware sine and cosine are within 2^-20 absolute;
 // the outputs round to bf16 (2^-9 relative).
 //
-// Work split.  D / 16 lanes hold one row, 16 channels each as two 16-byte chunks chosen so
-// that both halves of every pair are in one lane; a warp holds 4 rows (D = 128) or 8 (D = 64)
-// of one token, computes the token's angles once and walks the heads of its part.  A block's
-// 8 warps take 8 consecutive tokens, so that in the head-major output a block writes 2 KB
+// Work split.  D / 16 lanes hold one row, 16 channels each as two 16-byte chunks chosen so that both
+// halves of every pair are in one lane; a warp holds 4 rows (D = 128) or 8 (D = 64) of one token,
+// computes the token's angles once and walks the heads of its part, a trip of 4 or 8 heads at a time.
+// A block's 8 warps take 8 consecutive tokens, so that in the head-major output a block writes 2 KB
 // (D = 128) runs.
+//
+// What bounds both directions is HBM; what it takes is bytes in flight.  The rows of the next trips are
+// on their way by cp.async, each lane's own 16-byte pieces into its own place in shared memory: no
+// registers, no barriers.  Arithmetic is in packed fp32 pairs.
 #include "qat_internal.h"
+#include "qat_quant.cuh"
+#include "sm100.cuh"
 
 #include <cuda_bf16.h>
 
@@ -29,33 +35,60 @@ namespace qat {
 namespace {
 
 constexpr int kWarps = 8;
-constexpr int kPer = 16;                        // channels per lane
+constexpr int kPer = 16;        // channels per lane
+constexpr int kFwdStages = 4;   // trips in flight and in hand
+constexpr int kBwdStages = 3;
 constexpr float kTurnToRad = 1.4629180792671596e-09f;  // 2 pi / 2^32
 
-struct Row16 {
-  uint4 a, b;
+// A lane's 16 channels as 8 pairs (a, b), packed two by two: in the half layout a is chunk `a` and b
+// chunk `b`; interleaved, the first four pairs are chunk `a`, the others chunk `b`.
+struct Chan {
+  float2 a[4], b[4];
 };
 
-__device__ __forceinline__ void unpack8(const uint4& u, float* f) {
-  const __nv_bfloat162* h = reinterpret_cast<const __nv_bfloat162*>(&u);
+__device__ __forceinline__ float2 bf16x2_to_f32x2(uint32_t u) {
+  return make_float2(__uint_as_float(u << 16), __uint_as_float(u & 0xffff0000u));
+}
+__device__ __forceinline__ uint32_t f32x2_to_bf16x2(float lo, float hi) {
+  const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
+
+template <bool kInter>
+__device__ __forceinline__ void unpack(const uint4& ra, const uint4& rb, Chan& v) {
+  const uint32_t x[8] = {ra.x, ra.y, ra.z, ra.w, rb.x, rb.y, rb.z, rb.w};
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const float2 t = __bfloat1622float2(h[i]);
-    f[2 * i] = t.x;
-    f[2 * i + 1] = t.y;
+    if constexpr (kInter) {
+      const float2 p = bf16x2_to_f32x2(x[2 * i]), q = bf16x2_to_f32x2(x[2 * i + 1]);
+      v.a[i] = make_float2(p.x, q.x);
+      v.b[i] = make_float2(p.y, q.y);
+    } else {
+      v.a[i] = bf16x2_to_f32x2(x[i]);
+      v.b[i] = bf16x2_to_f32x2(x[4 + i]);
+    }
   }
 }
 
-__device__ __forceinline__ uint4 pack8(const float* f) {
-  uint4 u;
-  __nv_bfloat162* h = reinterpret_cast<__nv_bfloat162*>(&u);
+template <bool kInter>
+__device__ __forceinline__ void store(uint4* row, int ca, int cb, const Chan& v) {
+  uint32_t x[8];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) h[i] = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
-  return u;
+  for (int i = 0; i < 4; ++i) {
+    if constexpr (kInter) {
+      x[2 * i] = f32x2_to_bf16x2(v.a[i].x, v.b[i].x);
+      x[2 * i + 1] = f32x2_to_bf16x2(v.a[i].y, v.b[i].y);
+    } else {
+      x[i] = f32x2_to_bf16x2(v.a[i].x, v.a[i].y);
+      x[4 + i] = f32x2_to_bf16x2(v.b[i].x, v.b[i].y);
+    }
+  }
+  row[ca] = make_uint4(x[0], x[1], x[2], x[3]);
+  row[cb] = make_uint4(x[4], x[5], x[6], x[7]);
 }
 
-// The lane's two 8-channel chunks, whether each is rotated, and the pair index of each
-// chunk's first pair.
+// The lane's two 8-channel chunks, whether each is rotated, and the pair index of each chunk's first
+// pair.
 template <int D, bool kInter>
 struct LaneMap {
   int ca, cb;
@@ -73,50 +106,54 @@ struct LaneMap {
     } else {
       const int half = R / 16;  // chunks per half of the rotated part
       rot_a = rot_b = j < half;
-      ca = rot_a ? j : 2 * j;   // the other chunks in order: R / 8 + 2 (j - half)
-      cb = rot_a ? j + half : 2 * j + 1;
-      pair_a = pair_b = 8 * j;
+      ca = rot_a ? j : half + j;  // the other chunks, R / 8 .. D / 8 - 1, in two runs of lanes
+      cb = rot_a ? j + half : L + j;
+      pair_a = 8 * j;
+      pair_b = 8 * j + 4;
     }
+  }
+  // channel of pair e's member a (b: the next one, or the one of chunk b)
+  __device__ __forceinline__ int channel(int e, bool b) const {
+    if (kInter) return 8 * (e < 4 ? ca : cb) + 2 * (e & 3) + (b ? 1 : 0);
+    return 8 * (b ? cb : ca) + e;
   }
 };
 
-// The eight (cos, sin) pairs of the lane at a position, times the amplitude; unset for
-// chunks that are not rotated.
+// The lane's eight (cos, sin) pairs at a position, times the amplitude; unset for chunks that are not
+// rotated.
 template <bool kInter, class Map>
-__device__ __forceinline__ void lane_angles(const Map& m, const unsigned long long* phases,
-                                            int pos, float amplitude, float (&c)[8],
-                                            float (&s)[8]) {
+__device__ __forceinline__ void lane_angles(const Map& m, const unsigned long long* phases, int pos,
+                                            float amplitude, float2 (&c)[4], float2 (&s)[4]) {
+  float cs[8], sn[8];
 #pragma unroll
   for (int e = 0; e < 8; ++e) {
-    const bool rot = (kInter && e >= 4) ? m.rot_b : m.rot_a;
-    c[e] = s[e] = 0.f;
-    if (rot) {
-      const int i = kInter ? (e < 4 ? m.pair_a + e : m.pair_b + e - 4) : m.pair_a + e;
+    cs[e] = sn[e] = 0.f;
+    if (e < 4 ? m.rot_a : m.rot_b) {
       const unsigned long long turn =
-          static_cast<unsigned long long>(static_cast<long long>(pos)) * __ldg(phases + i);
+          static_cast<unsigned long long>(static_cast<long long>(pos)) *
+          __ldg(phases + (e < 4 ? m.pair_a + e : m.pair_b + e - 4));
       const float ang = static_cast<float>(static_cast<int>(turn >> 32)) * kTurnToRad;
-      float sn, cs;
-      __sincosf(ang, &sn, &cs);
-      c[e] = cs * amplitude;
-      s[e] = sn * amplitude;
+      __sincosf(ang, &sn[e], &cs[e]);
     }
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    c[i] = make_float2(cs[2 * i] * amplitude, cs[2 * i + 1] * amplitude);
+    s[i] = make_float2(sn[2 * i] * amplitude, sn[2 * i + 1] * amplitude);
   }
 }
 
-// v: the lane's 16 channels (chunk a, then chunk b), rotated in place by +angle (kBack: by
-// -angle, the transpose).
-// Channels that are not rotated are left alone, not multiplied by (1, 0): an infinity would
-// make its neighbour NaN.
-template <bool kInter, bool kBack, class Map>
-__device__ __forceinline__ void rotate16(const Map& m, float (&v)[16], const float (&c)[8],
-                                         const float (&s)[8]) {
+// v rotated in place by +angle (kBack: by -angle, the transpose).  Channels that are not rotated are
+// left alone, not multiplied by (1, 0): an infinity would make its neighbour NaN.
+template <bool kBack, class Map>
+__device__ __forceinline__ void rotate(const Map& m, Chan& v, const float2 (&c)[4], const float2 (&s)[4]) {
 #pragma unroll
-  for (int e = 0; e < 8; ++e) {
-    const int ia = kInter ? 2 * e : e, ib = kInter ? 2 * e + 1 : e + 8;
-    if (!((kInter && e >= 4) ? m.rot_b : m.rot_a)) continue;
-    const float a = v[ia], b = v[ib], sn = kBack ? -s[e] : s[e];
-    v[ia] = a * c[e] - b * sn;
-    v[ib] = a * sn + b * c[e];
+  for (int i = 0; i < 4; ++i) {
+    if (!(i < 2 ? m.rot_a : m.rot_b)) continue;
+    const float2 a = v.a[i], b = v.b[i];
+    const float2 minus = make_float2(-s[i].x, -s[i].y);
+    v.a[i] = fma_rn_f32x2(a, c[i], mul_rn_f32x2(b, kBack ? s[i] : minus));
+    v.b[i] = fma_rn_f32x2(b, c[i], mul_rn_f32x2(a, kBack ? minus : s[i]));
   }
 }
 
@@ -127,82 +164,109 @@ __device__ __forceinline__ float row_sum(float x) {
   return x;
 }
 
-__device__ __forceinline__ void load_weight8(const void* w, int bf16, int ch, float* f) {
-  if (bf16) {
-    unpack8(__ldg(reinterpret_cast<const uint4*>(w) + ch), f);
-  } else {
-    const float4 x = __ldg(reinterpret_cast<const float4*>(w) + 2 * ch);
-    const float4 y = __ldg(reinterpret_cast<const float4*>(w) + 2 * ch + 1);
-    f[0] = x.x; f[1] = x.y; f[2] = x.z; f[3] = x.w;
-    f[4] = y.x; f[5] = y.y; f[6] = y.z; f[7] = y.w;
+// sum_e x_e y_e over the lane's channels
+__device__ __forceinline__ float dot16(const Chan& x, const Chan& y) {
+  float2 s = mul_rn_f32x2(x.a[0], y.a[0]), t = mul_rn_f32x2(x.b[0], y.b[0]);
+#pragma unroll
+  for (int i = 1; i < 4; ++i) {
+    s = fma_rn_f32x2(x.a[i], y.a[i], s);
+    t = fma_rn_f32x2(x.b[i], y.b[i], t);
+  }
+  s = add_rn_f32x2(s, t);
+  return s.x + s.y;
+}
+
+template <bool kInter, class Map>
+__device__ __forceinline__ void load_weight(const Map& m, const void* w, int bf16, Chan& v) {
+  float* a = reinterpret_cast<float*>(v.a);
+  float* b = reinterpret_cast<float*>(v.b);
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    const int i = m.channel(e, false), j = m.channel(e, true);
+    a[e] = bf16 ? __bfloat162float(__ldg(static_cast<const __nv_bfloat16*>(w) + i)) : __ldg(static_cast<const float*>(w) + i);
+    b[e] = bf16 ? __bfloat162float(__ldg(static_cast<const __nv_bfloat16*>(w) + j)) : __ldg(static_cast<const float*>(w) + j);
   }
 }
 
-// Where block `part` of a token's heads lies: parts [0, nq) are the query heads, the rest the
-// key heads, `hpp` heads each.
-struct Part {
-  bool key;
-  int h0, h1;
-};
-
-__device__ __forceinline__ Part part_of(const NormRopeArgs& p, int part) {
-  Part r;
-  r.key = part >= p.q_parts;
-  r.h0 = (r.key ? part - p.q_parts : part) * p.heads_per_part;
-  r.h1 = min(r.h0 + p.heads_per_part, r.key ? p.k.H : p.q.H);
-  return r;
+// The lane's own 16 bytes from global memory into its own place; zeros (and no access) when !in.
+__device__ __forceinline__ void fetch16(uint32_t dst, const uint4* src, bool in) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(in ? 16 : 0)
+               : "memory");
+}
+__device__ __forceinline__ void fetch_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void fetch_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ uint4 lds128(uint32_t a) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a) : "memory");
+  return v;
 }
 
+__device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
+
 template <int D, bool kInter>
-__global__ void __launch_bounds__(32 * kWarps) norm_rope_kernel(const NormRopeArgs p) {
+__global__ void __launch_bounds__(32 * kWarps, 4) norm_rope_kernel(const NormRopeArgs p) {
   constexpr int L = D / kPer;    // lanes per row
-  constexpr int RW = 32 / L;     // rows per warp
+  constexpr int RW = 32 / L;     // rows per warp and trip
+  __shared__ uint4 ring[kWarps][kFwdStages][2][32];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int part = blockIdx.x % p.parts;
-  const long long tok = static_cast<long long>(blockIdx.x / p.parts) * kWarps + warp;
-  if (tok >= p.tokens) return;
-  const int b = static_cast<int>(tok / p.N), n = static_cast<int>(tok - static_cast<long long>(b) * p.N);
-  const Part pt = part_of(p, part);
-  const NormRopeTensor& t = pt.key ? p.k : p.q;
+  // parts [0, q_parts) are the query heads, the rest the key heads, heads_per_part each
+  const int part = static_cast<int>(blockIdx.x % static_cast<unsigned>(p.parts));
+  const unsigned tok = blockIdx.x / static_cast<unsigned>(p.parts) * kWarps + warp;
+  if (tok >= static_cast<unsigned long long>(p.tokens)) return;
+  const unsigned b = tok / static_cast<unsigned>(p.N), n = tok - b * static_cast<unsigned>(p.N);
+  const bool key = part >= p.q_parts;
+  const NormRopeTensor& t = key ? p.k : p.q;
+  const int h0 = (key ? part - p.q_parts : part) * p.heads_per_part;
+  const int h1 = min(h0 + p.heads_per_part, t.H);
   const LaneMap<D, kInter> m(lane % L, p.R);
   const int sub = lane / L;
 
-  float w[16];
-  if (t.w != nullptr) {
-    load_weight8(t.w, p.w_bf16, m.ca, w);
-    load_weight8(t.w, p.w_bf16, m.cb, w + 8);
-  }
-  float c[8], s[8];
+  const uint16_t* src = t.x + b * t.sb + n * t.sn;
+  const uint32_t mine = sm100::smem_addr(&ring[warp][0][0][lane]);
+  int hf = h0 + sub;  // head fetched next
+  uint32_t fs = 0;
+  auto fetch = [&]() {
+    if (hf - sub < h1) {
+      const uint4* row = reinterpret_cast<const uint4*>(src + min(hf, h1 - 1) * t.sh);
+      fetch16(mine + fs * 1024, row + m.ca, hf < h1);
+      fetch16(mine + fs * 1024 + 512, row + m.cb, hf < h1);
+      hf += RW;
+      fs = fs + 1 == kFwdStages ? 0 : fs + 1;
+    }
+    fetch_commit();
+  };
+#pragma unroll
+  for (int i = 0; i < kFwdStages - 1; ++i) fetch();
+
+  Chan w;
+  if (t.w != nullptr) load_weight<kInter>(m, t.w, p.w_bf16, w);
+  float2 c[4], s[4];
   const int pos = p.R > 0 ? __ldg(p.positions + b * p.pos_sb + n) : 0;
   lane_angles<kInter>(m, p.phases, pos, p.amplitude, c, s);
 
-  const uint16_t* src = t.x + b * t.sb + n * t.sn;
   uint16_t* dst = t.y + (static_cast<long long>(b) * t.H * p.N + n) * D;
-  for (int h = pt.h0 + sub; h - sub < pt.h1; h += RW) {
-    const bool in = h < pt.h1;
-    float v[16];
-    uint4 ra = make_uint4(0u, 0u, 0u, 0u), rb = ra;
-    if (in) {
-      const uint16_t* row = src + h * t.sh;
-      ra = __ldg(reinterpret_cast<const uint4*>(row) + m.ca);
-      rb = __ldg(reinterpret_cast<const uint4*>(row) + m.cb);
-    }
-    unpack8(ra, v);
-    unpack8(rb, v + 8);
+  uint32_t us = 0;
+  for (int h = h0 + sub; h - sub < h1; h += RW) {
+    fetch();
+    fetch_wait<kFwdStages - 1>();
+    Chan v;
+    unpack<kInter>(lds128(mine + us * 1024), lds128(mine + us * 1024 + 512), v);
+    us = us + 1 == kFwdStages ? 0 : us + 1;
     if (t.w != nullptr) {
-      float ss = 0.f;
+      const float2 r = both(rsqrtf(row_sum<L>(dot16(v, v)) * (1.f / D) + p.eps));
 #pragma unroll
-      for (int i = 0; i < 16; ++i) ss += v[i] * v[i];
-      const float r = rsqrtf(row_sum<L>(ss) * (1.f / D) + p.eps);
-#pragma unroll
-      for (int i = 0; i < 16; ++i) v[i] = v[i] * r * w[i];
+      for (int i = 0; i < 4; ++i) {
+        v.a[i] = mul_rn_f32x2(mul_rn_f32x2(v.a[i], r), w.a[i]);
+        v.b[i] = mul_rn_f32x2(mul_rn_f32x2(v.b[i], r), w.b[i]);
+      }
     }
-    rotate16<kInter, false>(m, v, c, s);
-    if (in) {
-      uint4* out = reinterpret_cast<uint4*>(dst + static_cast<long long>(h) * p.N * D);
-      out[m.ca] = pack8(v);
-      out[m.cb] = pack8(v + 8);
-    }
+    rotate<false>(m, v, c, s);
+    if (h < h1)
+      store<kInter>(reinterpret_cast<uint4*>(dst + static_cast<long long>(h) * p.N * D), m.ca, m.cb, v);
   }
 }
 
@@ -211,94 +275,129 @@ __global__ void __launch_bounds__(32 * kWarps) norm_rope_kernel(const NormRopeAr
 // the block's sum goes to its own row of the workspace, which norm_rope_dw_kernel adds in
 // block order.  No atomics: the same sizes give the same bits.
 template <int D, bool kInter>
-__global__ void __launch_bounds__(32 * kWarps) norm_rope_bwd_kernel(const NormRopeArgs p) {
+__global__ void __launch_bounds__(32 * kWarps, 2) norm_rope_bwd_kernel(const NormRopeArgs p) {
   constexpr int L = D / kPer;
   constexpr int RW = 32 / L;
-  __shared__ float red[kWarps][D];
+  __shared__ uint4 ring[kWarps][kBwdStages][4][32];  // x and dy; then the warps' weight gradients
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const bool key = blockIdx.x >= static_cast<unsigned>(p.q_blocks);
   const NormRopeTensor& t = key ? p.k : p.q;
   const int blk = key ? blockIdx.x - p.q_blocks : blockIdx.x;
   const int blocks = key ? gridDim.x - p.q_blocks : p.q_blocks;
-  const int parts = key ? p.parts - p.q_parts : p.q_parts;
+  const unsigned parts = key ? p.parts - p.q_parts : p.q_parts;
   const long long items = (p.tokens + kWarps - 1) / kWarps * parts;
   const LaneMap<D, kInter> m(lane % L, p.R);
   const int sub = lane / L;
+  const bool norm = t.w != nullptr;
 
-  float w[16], dw[16];
+  // The fetches run ahead over the warp's trips: their item, token and head.
+  const uint32_t mine = sm100::smem_addr(&ring[warp][0][0][lane]);
+  long long fi = blk;
+  const uint16_t *fx = nullptr, *fg = nullptr;
+  int fh = 0, fh1 = 0;  // heads fetched next, and the part's end; fh = fh1: the next item
+  uint32_t fs = 0;
+  auto locate = [&](long long it, unsigned& b, unsigned& n, int& h0, int& h1) {
+    const unsigned group = static_cast<unsigned>(it / parts), part = static_cast<unsigned>(it - static_cast<long long>(group) * parts);
+    const unsigned long long tok = static_cast<unsigned long long>(group) * kWarps + warp;
+    if (tok >= static_cast<unsigned long long>(p.tokens)) return false;
+    b = static_cast<unsigned>(tok) / static_cast<unsigned>(p.N);
+    n = static_cast<unsigned>(tok) - b * static_cast<unsigned>(p.N);
+    h0 = part * p.heads_per_part;
+    h1 = min(h0 + p.heads_per_part, t.H);
+    return true;
+  };
+  auto fetch = [&]() {
+    while (fh >= fh1 && fi < items) {  // on to the next item that this warp has a token of
+      unsigned b, n;
+      if (locate(fi, b, n, fh, fh1)) {
+        fx = t.x + b * t.sb + n * t.sn;
+        fg = t.dy + b * t.dy_sb + n * t.dy_sn;
+      }
+      fi += blocks;
+    }
+    if (fh < fh1) {
+      const int h = fh + sub;
+      const bool in = h < fh1;
+      const uint32_t at = mine + fs * 2048;
+      const uint4* g = reinterpret_cast<const uint4*>(fg + min(h, fh1 - 1) * t.dy_sh);
+      fetch16(at, g + m.ca, in);
+      fetch16(at + 512, g + m.cb, in);
+      if (norm) {
+        const uint4* x = reinterpret_cast<const uint4*>(fx + min(h, fh1 - 1) * t.sh);
+        fetch16(at + 1024, x + m.ca, in);
+        fetch16(at + 1536, x + m.cb, in);
+      }
+      fh += RW;
+      fs = fs + 1 == kBwdStages ? 0 : fs + 1;
+    }
+    fetch_commit();
+  };
 #pragma unroll
-  for (int i = 0; i < 16; ++i) dw[i] = 0.f;
-  if (t.w != nullptr) {
-    load_weight8(t.w, p.w_bf16, m.ca, w);
-    load_weight8(t.w, p.w_bf16, m.cb, w + 8);
-  }
+  for (int i = 0; i < kBwdStages - 1; ++i) fetch();
+
+  Chan w, dw;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) dw.a[i] = dw.b[i] = both(0.f);
+  if (norm) load_weight<kInter>(m, t.w, p.w_bf16, w);
+  uint32_t us = 0;
   for (long long it = blk; it < items; it += blocks) {
-    const int part = static_cast<int>(it % parts);
-    const long long tok = it / parts * kWarps + warp;
-    if (tok >= p.tokens) continue;
-    const int b = static_cast<int>(tok / p.N), n = static_cast<int>(tok - static_cast<long long>(b) * p.N);
-    const int h0 = part * p.heads_per_part, h1 = min(h0 + p.heads_per_part, t.H);
-    float c[8], s[8];
+    unsigned b, n;
+    int h0, h1;
+    if (!locate(it, b, n, h0, h1)) continue;
+    float2 c[4], s[4];
     const int pos = p.R > 0 ? __ldg(p.positions + b * p.pos_sb + n) : 0;
     lane_angles<kInter>(m, p.phases, pos, p.amplitude, c, s);
-    const uint16_t* xs = t.x + b * t.sb + n * t.sn;
-    const uint16_t* gs = t.dy + b * t.dy_sb + n * t.dy_sn;
     uint16_t* ds = t.y + b * t.y_sb + n * t.y_sn;
     for (int h = h0 + sub; h - sub < h1; h += RW) {
-      const bool in = h < h1;
-      float g[16];
-      uint4 ga = make_uint4(0u, 0u, 0u, 0u), gb = ga, xa = ga, xb = ga;
-      if (in) {
-        const uint16_t* grow = gs + h * t.dy_sh;
-        ga = __ldg(reinterpret_cast<const uint4*>(grow) + m.ca);
-        gb = __ldg(reinterpret_cast<const uint4*>(grow) + m.cb);
-        if (t.w != nullptr) {
-          const uint16_t* row = xs + h * t.sh;
-          xa = __ldg(reinterpret_cast<const uint4*>(row) + m.ca);
-          xb = __ldg(reinterpret_cast<const uint4*>(row) + m.cb);
+      fetch();
+      fetch_wait<kBwdStages - 1>();
+      const uint32_t at = mine + us * 2048;
+      us = us + 1 == kBwdStages ? 0 : us + 1;
+      Chan g;
+      unpack<kInter>(lds128(at), lds128(at + 512), g);
+      rotate<true>(m, g, c, s);
+      if (norm) {
+        Chan x;
+        unpack<kInter>(lds128(at + 1024), lds128(at + 1536), x);
+        const float r = rsqrtf(row_sum<L>(dot16(x, x)) * (1.f / D) + p.eps);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {  // x: the normed channel
+          x.a[i] = mul_rn_f32x2(x.a[i], both(r));
+          x.b[i] = mul_rn_f32x2(x.b[i], both(r));
+          dw.a[i] = fma_rn_f32x2(g.a[i], x.a[i], dw.a[i]);
+          dw.b[i] = fma_rn_f32x2(g.b[i], x.b[i], dw.b[i]);
+          g.a[i] = mul_rn_f32x2(g.a[i], w.a[i]);
+          g.b[i] = mul_rn_f32x2(g.b[i], w.b[i]);
+        }
+        const float2 dot = both(-row_sum<L>(dot16(g, x)) * (1.f / D));
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          g.a[i] = mul_rn_f32x2(fma_rn_f32x2(x.a[i], dot, g.a[i]), both(r));
+          g.b[i] = mul_rn_f32x2(fma_rn_f32x2(x.b[i], dot, g.b[i]), both(r));
         }
       }
-      unpack8(ga, g);
-      unpack8(gb, g + 8);
-      rotate16<kInter, true>(m, g, c, s);
-      if (t.w != nullptr) {
-        float x[16];
-        unpack8(xa, x);
-        unpack8(xb, x + 8);
-        float ss = 0.f;
-#pragma unroll
-        for (int i = 0; i < 16; ++i) ss += x[i] * x[i];
-        const float r = rsqrtf(row_sum<L>(ss) * (1.f / D) + p.eps);
-        float dot = 0.f;
-#pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          x[i] *= r;                 // the normed channel
-          dw[i] += g[i] * x[i];
-          g[i] *= w[i];
-          dot += g[i] * x[i];
-        }
-        dot = row_sum<L>(dot) * (1.f / D);
-#pragma unroll
-        for (int i = 0; i < 16; ++i) g[i] = r * (g[i] - x[i] * dot);
-      }
-      if (in) {
-        uint4* out = reinterpret_cast<uint4*>(ds + h * t.y_sh);
-        out[m.ca] = pack8(g);
-        out[m.cb] = pack8(g + 8);
-      }
+      if (h < h1) store<kInter>(reinterpret_cast<uint4*>(ds + h * t.y_sh), m.ca, m.cb, g);
     }
   }
-  if (t.w == nullptr) return;
+  if (!norm) return;
+  fetch_wait<0>();
+  float* va = reinterpret_cast<float*>(dw.a);
+  float* vb = reinterpret_cast<float*>(dw.b);
 #pragma unroll
-  for (int i = 0; i < 16; ++i) {
+  for (int e = 0; e < 8; ++e) {
 #pragma unroll
-    for (int o = L; o < 32; o <<= 1) dw[i] += __shfl_xor_sync(0xffffffffu, dw[i], o);
+    for (int o = L; o < 32; o <<= 1) {
+      va[e] += __shfl_xor_sync(0xffffffffu, va[e], o);
+      vb[e] += __shfl_xor_sync(0xffffffffu, vb[e], o);
+    }
   }
+  __syncthreads();  // the ring is free
+  float(*red)[D] = reinterpret_cast<float(*)[D]>(&ring[0][0][0][0]);
   if (sub == 0) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      red[warp][8 * m.ca + i] = dw[i];
-      red[warp][8 * m.cb + i] = dw[8 + i];
+    for (int e = 0; e < 8; ++e) {
+      red[warp][m.channel(e, false)] = va[e];
+      red[warp][m.channel(e, true)] = vb[e];
     }
   }
   __syncthreads();
@@ -334,15 +433,18 @@ __global__ void __launch_bounds__(D * 8) norm_rope_dw_kernel(const NormRopeArgs 
   }
 }
 
-// Heads per part: one trip of a warp over its rows while that leaves the GPU short of warps,
-// more (up to 8 trips, so that a token's angles are shared) when tokens abound.
+// Heads per part: one trip of a warp over its rows while that leaves the GPU short of warps, more (up to
+// 16 trips, so that a token's angles are shared and fetches run ahead) when tokens abound, in parts of
+// about the same size.
 void choose_parts(NormRopeArgs& a, int D, int num_sms) {
   const int rows_per_trip = 32 / (D / kPer);
   const long long trips = a.tokens * ((a.q.H + a.k.H + rows_per_trip - 1) / rows_per_trip);
   long long per = trips / (static_cast<long long>(num_sms) * 64);
-  if (per < 1) per = 1;
-  if (per > 8) per = 8;
-  a.heads_per_part = static_cast<int>(per) * rows_per_trip;
+  per = per < 1 ? 1 : per > 16 ? 16 : per;
+  const int most = a.q.H > a.k.H ? a.q.H : a.k.H;
+  const int parts = static_cast<int>((most + per * rows_per_trip - 1) / (per * rows_per_trip));
+  a.heads_per_part = parts == 0 ? rows_per_trip
+                                : ((most + parts - 1) / parts + rows_per_trip - 1) / rows_per_trip * rows_per_trip;
   a.q_parts = (a.q.H + a.heads_per_part - 1) / a.heads_per_part;
   a.parts = a.q_parts + (a.k.H + a.heads_per_part - 1) / a.heads_per_part;
 }
