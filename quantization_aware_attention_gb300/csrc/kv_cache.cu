@@ -11,10 +11,11 @@
 // Layout: codes [page][head][slot][D] bytes, scales [page][head][slot] fp32; position i of
 // sequence b is slot i % page_size of page table[b][i / page_size].
 //
-// Both kernels move every byte once: D / 16 lanes hold one row, 16 channels each (32 bytes of
-// bf16, 16 bytes of codes), so a warp covers 4 (D = 128) or 8 (D = 64) rows, consecutive tokens
-// of one head, which are consecutive in a page.  Keys and values of a row are handled by the same
-// lanes, which keeps four 16-byte loads in flight each.
+// Both kernels move every byte once: D / 16 lanes hold one row, so a warp covers 4 (D = 128) or 8
+// (D = 64) rows, consecutive tokens of one head, which are consecutive in a page.  Lane j takes
+// channels 8 j .. 8 j + 7 and the same of the row's second half, so that every load and store of a row
+// is one run of whole sectors: 16 bytes a lane of bf16, 8 bytes of codes.  Keys and values of a row are
+// handled by the same lanes, which keeps four loads in flight each.
 #include "qat_internal.h"
 #include "qat_quant.cuh"
 #include "sm100.cuh"
@@ -53,36 +54,37 @@ __device__ __forceinline__ uint32_t absmax_bf16x2(uint32_t a, uint32_t b) {
   return r;
 }
 
-// amax is the largest magnitude itself, so it is taken on the bf16 bits; a NaN stays one, and an
-// infinity is one's own.
-template <int D>
-__device__ __forceinline__ void quant_store(const uint4 (&raw)[2], uint8_t* code, float* scale,
-                                            size_t row, int j, bool in) {
-  constexpr int L = D / 16;
+// The row's largest magnitude: it is a bf16 value itself, so it is taken on the bits.  A NaN stays one.
+template <int L>
+__device__ __forceinline__ float row_amax(const uint4 (&raw)[2]) {
   const uint32_t x[8] = {raw[0].x, raw[0].y, raw[0].z, raw[0].w, raw[1].x, raw[1].y, raw[1].z, raw[1].w};
   uint32_t mx = absmax_bf16x2(x[0], x[1]);
 #pragma unroll
   for (int i = 2; i < 8; ++i) mx = absmax_bf16x2(mx, x[i]);
 #pragma unroll
   for (int o = L / 2; o > 0; o >>= 1) mx = absmax_bf16x2(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-  mx = absmax_bf16x2(mx, mx >> 16);
-  const float amax = __uint_as_float(mx << 16);
-  const bool bad = !(amax <= 3.4028234663852886e38f);
-  const TileScale ts = tile_scale(bad || amax < kTinyRow ? 0.f : amax);
-  if (!in) return;
-  uint32_t w[4];
+  return __uint_as_float(absmax_bf16x2(mx, mx >> 16) << 16);
+}
+
+__device__ __forceinline__ uint2 quant8(const uint4& raw, float inv) {
+  const uint32_t x[4] = {raw.x, raw.y, raw.z, raw.w};
+  uint32_t c[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const uint32_t u = x[2 * i], v = x[2 * i + 1];
-    const float2 p = mul_rn_f32x2(make_float2(__uint_as_float(u << 16), __uint_as_float(u & 0xffff0000u)),
-                                  make_float2(ts.inv, ts.inv));
-    const float2 q = mul_rn_f32x2(make_float2(__uint_as_float(v << 16), __uint_as_float(v & 0xffff0000u)),
-                                  make_float2(ts.inv, ts.inv));
-    w[i] = e4m3x2_rn_satfinite(p.x, p.y) | static_cast<uint32_t>(e4m3x2_rn_satfinite(q.x, q.y)) << 16;
+    const float2 y = mul_rn_f32x2(make_float2(__uint_as_float(x[i] << 16), __uint_as_float(x[i] & 0xffff0000u)),
+                                  make_float2(inv, inv));
+    c[i] = e4m3x2_rn_satfinite(y.x, y.y);
   }
-  *reinterpret_cast<uint4*>(code + row * D + 16 * j) =
-      bad ? make_uint4(0u, 0u, 0u, 0u) : make_uint4(w[0], w[1], w[2], w[3]);
-  if (j == 0) scale[row] = bad ? __int_as_float(0x7fc00000) : ts.scale;
+  return make_uint2(c[0] | c[1] << 16, c[2] | c[3] << 16);
+}
+
+template <int D>
+__device__ __forceinline__ void store_codes(uint8_t* code, size_t row, int j, const uint4 (&raw)[2],
+                                            float inv, bool bad) {
+  const uint2 lo = quant8(raw[0], inv), hi = quant8(raw[1], inv), none = make_uint2(0u, 0u);
+  uint2* dst = reinterpret_cast<uint2*>(code + row * D);
+  dst[j] = bad ? none : lo;
+  dst[j + D / 16] = bad ? none : hi;
 }
 
 template <int D>
@@ -104,10 +106,10 @@ __global__ void __launch_bounds__(kThreads) kv_append_kernel(const KvCacheArgs p
     if (in) {
       const uint4* k = reinterpret_cast<const uint4*>(p.k + b * p.k_sb + h * p.k_sh + n * p.k_sn);
       const uint4* v = reinterpret_cast<const uint4*>(p.v + b * p.v_sb + h * p.v_sh + n * p.v_sn);
-      rk[0] = __ldg(k + 2 * j);
-      rk[1] = __ldg(k + 2 * j + 1);
-      rv[0] = __ldg(v + 2 * j);
-      rv[1] = __ldg(v + 2 * j + 1);
+      rk[0] = __ldg(k + j);
+      rk[1] = __ldg(k + L + j);
+      rv[0] = __ldg(v + j);
+      rv[1] = __ldg(v + L + j);
       // the count's tokens are the sequence's last
       const int len = __ldg(p.seq_lens + b);
       const long long pos = static_cast<long long>(len) - count + n;
@@ -123,23 +125,34 @@ __global__ void __launch_bounds__(kThreads) kv_append_kernel(const KvCacheArgs p
     }
   }
   if (!__any_sync(0xffffffffu, in)) return;  // padding
-  quant_store<D>(rk, p.k_codes, p.k_scales, at, j, in);
-  quant_store<D>(rv, p.v_codes, p.v_scales, at, j, in);
+  const float ak = row_amax<L>(rk), av = row_amax<L>(rv);
+  const bool bad_k = !(ak <= 3.4028234663852886e38f), bad_v = !(av <= 3.4028234663852886e38f);
+  // the row's four divisions, 448 / amax and amax / 448 of K and V, one to a lane
+  const float am = (j & 2) ? av : ak;
+  const bool zero = !(am >= kTinyRow) || ((j & 2) ? bad_v : bad_k);
+  const float q = zero ? 0.f : ((j & 1) ? __fdiv_rn(am, kE4M3Max) : __fdiv_rn(kE4M3Max, am));
+  const int first = (threadIdx.x & 31) - j;
+  const float inv_k = __shfl_sync(0xffffffffu, q, first), inv_v = __shfl_sync(0xffffffffu, q, first + 2);
+  if (!in) return;
+  store_codes<D>(p.k_codes, at, j, rk, inv_k, bad_k);
+  store_codes<D>(p.v_codes, at, j, rv, inv_v, bad_v);
+  const float nan = __int_as_float(0x7fc00000);
+  if (j == 1) p.k_scales[at] = bad_k ? nan : q;
+  if (j == 3) p.v_scales[at] = bad_v ? nan : q;
 }
 
-__device__ __forceinline__ void dequant_store(const uint4& codes, float scale, uint16_t* dst) {
-  const uint32_t c[4] = {codes.x, codes.y, codes.z, codes.w};
-  uint32_t w[8];
+// Eight codes to bf16.
+__device__ __forceinline__ uint4 dequant8(const uint2& c, float scale) {
+  const uint16_t x[4] = {static_cast<uint16_t>(c.x), static_cast<uint16_t>(c.x >> 16),
+                         static_cast<uint16_t>(c.y), static_cast<uint16_t>(c.y >> 16)};
+  uint32_t w[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const float2 lo = mul_rn_f32x2(e4m3x2_decode(static_cast<uint16_t>(c[i])), make_float2(scale, scale));
-    const float2 hi = mul_rn_f32x2(e4m3x2_decode(static_cast<uint16_t>(c[i] >> 16)), make_float2(scale, scale));
-    const __nv_bfloat162 a = __floats2bfloat162_rn(lo.x, lo.y), b = __floats2bfloat162_rn(hi.x, hi.y);
-    w[2 * i] = *reinterpret_cast<const uint32_t*>(&a);
-    w[2 * i + 1] = *reinterpret_cast<const uint32_t*>(&b);
+    const float2 v = mul_rn_f32x2(e4m3x2_decode(x[i]), make_float2(scale, scale));
+    const __nv_bfloat162 h = __floats2bfloat162_rn(v.x, v.y);
+    w[i] = *reinterpret_cast<const uint32_t*>(&h);
   }
-  reinterpret_cast<uint4*>(dst)[0] = make_uint4(w[0], w[1], w[2], w[3]);
-  reinterpret_cast<uint4*>(dst)[1] = make_uint4(w[4], w[5], w[6], w[7]);
+  return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
 template <int D>
@@ -152,22 +165,31 @@ __global__ void __launch_bounds__(kThreads) kv_read_kernel(const KvCacheArgs p) 
   const int n = static_cast<int>(row - bh * p.N), b = static_cast<int>(bh / static_cast<unsigned>(p.H));
   const int h = static_cast<int>(bh - static_cast<unsigned>(b) * p.H);
   const long long pos = static_cast<long long>(p.begin) + n;
-  uint4 ck = make_uint4(0u, 0u, 0u, 0u), cv = ck;
+  uint2 ck[2], cv[2];
+  ck[0] = ck[1] = cv[0] = cv[1] = make_uint2(0u, 0u);
   float sk = 0.f, sv = 0.f;
   if (pos < seq_len(p, b)) {
     int page, slot;
     if (find_slot(p, b, static_cast<int>(pos), page, slot)) {
       const size_t at = ((static_cast<size_t>(page) * p.H + h) << p.page_shift) + slot;
-      ck = __ldg(reinterpret_cast<const uint4*>(p.k_codes + at * D) + j);
-      cv = __ldg(reinterpret_cast<const uint4*>(p.v_codes + at * D) + j);
+      const uint2* k = reinterpret_cast<const uint2*>(p.k_codes + at * D) + j;
+      const uint2* v = reinterpret_cast<const uint2*>(p.v_codes + at * D) + j;
+      ck[0] = __ldg(k);
+      ck[1] = __ldg(k + L);
+      cv[0] = __ldg(v);
+      cv[1] = __ldg(v + L);
       sk = __ldg(p.k_scales + at);
       sv = __ldg(p.v_scales + at);
     } else {
       sk = sv = __int_as_float(0x7fc00000);  // no page: the row reads as NaN
     }
   }
-  dequant_store(ck, sk, p.k_out + static_cast<size_t>(row) * D + 16 * j);
-  dequant_store(cv, sv, p.v_out + static_cast<size_t>(row) * D + 16 * j);
+  uint4* ko = reinterpret_cast<uint4*>(p.k_out + static_cast<size_t>(row) * D) + j;
+  uint4* vo = reinterpret_cast<uint4*>(p.v_out + static_cast<size_t>(row) * D) + j;
+  ko[0] = dequant8(ck[0], sk);
+  ko[L] = dequant8(ck[1], sk);
+  vo[0] = dequant8(cv[0], sv);
+  vo[L] = dequant8(cv[1], sv);
 }
 
 inline unsigned blocks_of(const KvCacheArgs& a, int D) {
