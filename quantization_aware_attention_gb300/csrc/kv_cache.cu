@@ -47,10 +47,10 @@ __device__ __forceinline__ int seq_len(const KvCacheArgs& p, int b) {
   return static_cast<int>(cap);
 }
 
-// max(|a|, |b|) of two bf16 pairs, NaN if either is.
+// max(|a|, |b|) of two bf16 pairs up to the signs, NaN if either is.
 __device__ __forceinline__ uint32_t absmax_bf16x2(uint32_t a, uint32_t b) {
   uint32_t r;
-  asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a & 0x7fff7fffu), "r"(b & 0x7fff7fffu));
+  asm("max.NaN.xorsign.abs.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
   return r;
 }
 
@@ -63,7 +63,7 @@ __device__ __forceinline__ float row_amax(const uint4 (&raw)[2]) {
   for (int i = 2; i < 8; ++i) mx = absmax_bf16x2(mx, x[i]);
 #pragma unroll
   for (int o = L / 2; o > 0; o >>= 1) mx = absmax_bf16x2(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-  return __uint_as_float(absmax_bf16x2(mx, mx >> 16) << 16);
+  return __uint_as_float((absmax_bf16x2(mx, mx >> 16) & 0x7fffu) << 16);
 }
 
 __device__ __forceinline__ uint2 quant8(const uint4& raw, float inv) {
@@ -88,14 +88,13 @@ __device__ __forceinline__ void store_codes(uint8_t* code, size_t row, int j, co
 }
 
 template <int D>
-__global__ void __launch_bounds__(kThreads) kv_append_kernel(const KvCacheArgs p) {
+__global__ void __launch_bounds__(kThreads, 8) kv_append_kernel(const KvCacheArgs p) {
   constexpr int L = D / 16;
   const int j = threadIdx.x % L;
-  // at most 2^31 rows: 32-bit divisions
   const unsigned row = blockIdx.x * (kThreads / L) + threadIdx.x / L;
   bool in = row < static_cast<unsigned long long>(p.B) * p.H * p.N;
-  const unsigned bh = row / static_cast<unsigned>(p.N);
-  const int n = static_cast<int>(row - bh * p.N), b = static_cast<int>(bh / static_cast<unsigned>(p.H));
+  const unsigned bh = p.by_n(row);
+  const int n = static_cast<int>(row - bh * p.N), b = static_cast<int>(p.by_h(bh));
   const int h = static_cast<int>(bh - static_cast<unsigned>(b) * p.H);
   uint4 rk[2], rv[2];
   rk[0] = rk[1] = rv[0] = rv[1] = make_uint4(0u, 0u, 0u, 0u);
@@ -161,8 +160,8 @@ __global__ void __launch_bounds__(kThreads) kv_read_kernel(const KvCacheArgs p) 
   const int j = threadIdx.x % L;
   const unsigned row = blockIdx.x * (kThreads / L) + threadIdx.x / L;
   if (row >= static_cast<unsigned long long>(p.B) * p.H * p.N) return;
-  const unsigned bh = row / static_cast<unsigned>(p.N);
-  const int n = static_cast<int>(row - bh * p.N), b = static_cast<int>(bh / static_cast<unsigned>(p.H));
+  const unsigned bh = p.by_n(row);
+  const int n = static_cast<int>(row - bh * p.N), b = static_cast<int>(p.by_h(bh));
   const int h = static_cast<int>(bh - static_cast<unsigned>(b) * p.H);
   const long long pos = static_cast<long long>(p.begin) + n;
   uint2 ck[2], cv[2];

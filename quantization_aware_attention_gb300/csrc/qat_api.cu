@@ -575,6 +575,8 @@ qat_status_t qat_kv_cache_append(const void* k, const long long* k_strides, cons
   a.seq_lens = seq_lens;
   a.new_lens = new_lens;
   a.B = B; a.H = H; a.N = N;
+  a.by_n = qat::FastDiv(N);
+  a.by_h = qat::FastDiv(H);
   a.num_pages = num_pages;
   a.page_shift = page_shift(page_size);
   a.max_pages = max_pages;
@@ -608,6 +610,8 @@ qat_status_t qat_kv_cache_read(const void* k_codes, const void* v_codes, const f
   a.k_out = static_cast<uint16_t*>(k_out);
   a.v_out = static_cast<uint16_t*>(v_out);
   a.B = B; a.H = H; a.N = N;
+  a.by_n = qat::FastDiv(N);
+  a.by_h = qat::FastDiv(H);
   a.begin = begin;
   a.num_pages = num_pages;
   a.page_shift = page_shift(page_size);

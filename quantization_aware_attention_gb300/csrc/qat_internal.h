@@ -190,6 +190,23 @@ struct NormRopeArgs {
 // Most blocks of the backward of the norm + rotation (its workspace holds D sums for each).
 constexpr int kNormRopeBwdBlocks = 608;  // 152 SMs x 4
 
+// Division of x < 2^31 by a divisor known on the host: with s = ceil(log2 d) and
+// m = ceil(2^(31 + s) / d) < 2^32, x / d = floor(x m / 2^(31 + s)), as x m / 2^(31 + s) exceeds x / d by
+// x / 2^(31 + s) < 1 / d at most.
+struct FastDiv {
+  unsigned m, s;
+  FastDiv() = default;
+  explicit FastDiv(unsigned d) : m(0), s(0) {
+    while ((1ull << s) < d) ++s;
+    m = static_cast<unsigned>(((1ull << (31 + s)) + d - 1) / d);
+  }
+#ifdef __CUDACC__
+  __device__ __forceinline__ unsigned operator()(unsigned x) const {
+    return static_cast<unsigned>((static_cast<unsigned long long>(x) * m) >> 31 >> s);
+  }
+#endif
+};
+
 // Append to and read from the FP8 cache.
 struct KvCacheArgs {
   const uint16_t *k, *v;             // append: [B, H, N, D] by element strides
@@ -202,6 +219,7 @@ struct KvCacheArgs {
   const int* new_lens;               // append: [B] or null
   unsigned int* err;
   int B, H, N, begin, num_pages, page_shift, max_pages;
+  FastDiv by_n, by_h;
 };
 
 // The attention of a few new tokens over the FP8 cache.
