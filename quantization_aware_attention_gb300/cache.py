@@ -32,6 +32,12 @@ def _index(t, name, device, shape):
                      f"{tuple(t.shape)}")
 
 
+def _no_gradient(name, *tensors):
+    if torch.is_grad_enabled() and any(t.requires_grad for t in tensors):
+        raise ValueError(f"{name} has no backward: call it under torch.no_grad(), or with tensors that "
+                         "do not require gradients")
+
+
 class KVCache:
     """Pages of keys and values: ``k`` and ``v`` are torch.float8_e4m3fn [pages, H, page_size, D],
     ``k_scale`` and ``v_scale`` fp32 [pages, H, page_size]; a row's value is its codes times its
@@ -65,9 +71,15 @@ class KVCache:
             if tuple(t.shape) != shape or not t.is_contiguous() or t.data_ptr() % 16:
                 raise ValueError(f"{name} must be contiguous {shape} on a 16-byte boundary, got shape "
                                  f"{tuple(t.shape)}")
-        self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
+        self._k, self._v, self._k_scale, self._v_scale = k, v, k_scale, v_scale
         self.num_pages, self.heads, self.page_size, self.D = pages, H, page, D
         self.device = k.device
+
+    # the tensors the sizes above were checked against
+    k = property(lambda self: self._k)
+    v = property(lambda self: self._v)
+    k_scale = property(lambda self: self._k_scale)
+    v_scale = property(lambda self: self._v_scale)
 
     @classmethod
     def empty(cls, num_pages: int, heads: int, page_size: int, D: int, device="cuda") -> "KVCache":
@@ -102,11 +114,12 @@ class KVCache:
         shape = (B, self.heads, N, self.D)
         ks = rows_strides(k, "k", self.device, shape)
         vs = rows_strides(v, "v", self.device, shape)
+        _no_gradient("append", k, v)
         if new_lens is not None:
             _index(new_lens, "new_lens", self.device, (B,))
         with device_guard(self.device):
             st = capi.qat_kv_cache_append(
-                k, ks, v, vs, self.k, self.v, self.k_scale, self.v_scale, block_table, seq_lens,
+                k, ks, v, vs, self._k, self._v, self._k_scale, self._v_scale, block_table, seq_lens,
                 new_lens, B, self.heads, N, self.D, self.num_pages, self.page_size, max_pages)
             _raise(st, "qat_kv_cache_append")
             if _check_enabled(check):
@@ -125,7 +138,7 @@ class KVCache:
         k_out = torch.empty(shape, dtype=torch.bfloat16, device=self.device)
         v_out = torch.empty(shape, dtype=torch.bfloat16, device=self.device)
         with device_guard(self.device):
-            st = capi.qat_kv_cache_read(self.k, self.v, self.k_scale, self.v_scale, block_table,
+            st = capi.qat_kv_cache_read(self._k, self._v, self._k_scale, self._v_scale, block_table,
                                         seq_lens, k_out, v_out, B, self.heads, begin, length, self.D,
                                         self.num_pages, self.page_size, max_pages)
             _raise(st, "qat_kv_cache_read")
@@ -152,6 +165,7 @@ def qat_attention_decode(q, cache: KVCache, block_table, seq_lens, sm_scale: flo
     Hq, T, D = q.shape[1:]
     if q.shape[0] != B or D != cache.D:
         raise ValueError(f"q has shape {tuple(q.shape)}, expected ({B}, Hq, T, {cache.D})")
+    _no_gradient("qat_attention_decode", q)
     if Hq < 1 or Hq % cache.heads:
         raise ValueError(f"{Hq} query heads do not share the cache's {cache.heads} evenly")
     if workspace is None:
@@ -164,7 +178,7 @@ def qat_attention_decode(q, cache: KVCache, block_table, seq_lens, sm_scale: flo
     lse = torch.empty((B, Hq, T), dtype=torch.float32, device=dev) if return_lse else None
     with device_guard(dev):
         st = capi.qat_attn_decode(
-            q, cache.k, cache.v, cache.k_scale, cache.v_scale, block_table, seq_lens, o, lse, B, Hq,
+            q, cache._k, cache._v, cache._k_scale, cache._v_scale, block_table, seq_lens, o, lse, B, Hq,
             cache.heads, T, D, cache.num_pages, cache.page_size, max_pages,
             D ** -0.5 if sm_scale is None else sm_scale, quant_mode, workspace, workspace.numel())
         _raise(st, "qat_attn_decode")

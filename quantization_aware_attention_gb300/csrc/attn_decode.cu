@@ -187,12 +187,15 @@ __device__ __forceinline__ int clamp_len(const DecodeArgs& a, int len) {
 }
 __device__ __forceinline__ int tiles_of(int len) { return len > 0 ? (len + kTile - 1) / kTile : 1; }
 
-__device__ __forceinline__ void enter_seq(const DecodeArgs& a, Cursor& c) {
-  c.len = c.b < a.B ? clamp_len(a, __ldg(a.seq_lens + c.b)) : 0;
-  c.tiles = tiles_of(c.len);
+// Tiles as the prefix sums have them: the cut and every index hold together even if a length changes
+// under the kernel.
+__device__ __forceinline__ void enter_seq(const Params& p, const int* prefix, Cursor& c) {
+  if (c.b >= p.a.B) return;  // behind the last: not looked at again
+  c.tiles = static_cast<unsigned>(prefix[c.b + 1] - prefix[c.b]) / static_cast<unsigned>(p.a.Hkv * p.mtiles);
+  c.len = min(clamp_len(p.a, __ldg(p.a.seq_lens + c.b)), c.tiles * kTile);
 }
 
-__device__ __forceinline__ void advance(const Params& p, Cursor& c) {
+__device__ __forceinline__ void advance(const Params& p, const int* prefix, Cursor& c) {
   if (++c.tile < c.tiles) return;
   c.tile = 0;
   if (++c.mt < p.mtiles) return;
@@ -200,7 +203,7 @@ __device__ __forceinline__ void advance(const Params& p, Cursor& c) {
   if (++c.h < p.a.Hkv) return;
   c.h = 0;
   ++c.b;
-  enter_seq(p.a, c);
+  enter_seq(p, prefix, c);
 }
 
 __device__ __forceinline__ int item_of(const Params& p, const Cursor& c) {
@@ -306,7 +309,8 @@ __global__ void __launch_bounds__(32 * Cfg<D, NR>::kWarps, 1) decode_kernel(cons
       const int len = __ldg(a.seq_lens + b);
       const int ok = clamp_len(a, len);
       if (len > ok) atomicOr(a.err, kErrBadPage);
-      sum += tiles_of(ok) * per_seq;
+      prefix[b] = tiles_of(ok) * per_seq;
+      sum += prefix[b];
     }
     int inc = sum;
 #pragma unroll
@@ -319,8 +323,9 @@ __global__ void __launch_bounds__(32 * Cfg<D, NR>::kWarps, 1) decode_kernel(cons
     int base = inc - sum;
     for (int w = 0; w < warp; ++w) base += warp_sum[w];
     for (int b = b0; b < b1; ++b) {
+      const int units = prefix[b];
       prefix[b] = base;
-      base += tiles_of(clamp_len(a, __ldg(a.seq_lens + b))) * per_seq;
+      base += units;
     }
     if (tid == kThreads - 1) prefix[a.B] = base;
     __syncthreads();
@@ -346,7 +351,7 @@ __global__ void __launch_bounds__(32 * Cfg<D, NR>::kWarps, 1) decode_kernel(cons
       if (prefix[mid] <= u0) lo = mid; else hi = mid;
     }
     cc.b = lo;
-    enter_seq(a, cc);
+    enter_seq(p, prefix, cc);
     int u = u0 - prefix[lo];
     cc.tile = u % cc.tiles;
     u /= cc.tiles;
@@ -430,7 +435,7 @@ __global__ void __launch_bounds__(32 * Cfg<D, NR>::kWarps, 1) decode_kernel(cons
       pslot = pslot + 1 == C::kSlots ? 0 : pslot + 1;
       if (sub == 3) {
         ++pu;
-        advance(p, pc);
+        advance(p, prefix, pc);
       }
     }
     cp_commit();
@@ -703,7 +708,7 @@ __global__ void __launch_bounds__(32 * Cfg<D, NR>::kWarps, 1) decode_kernel(cons
         }
       }
     }
-    advance(p, cc);
+    advance(p, prefix, cc);
   }
 #undef QAT_SUB
   cp_wait<0>();

@@ -636,7 +636,7 @@ qat_status_t qat_attn_decode(const void* q, const void* k_codes, const void* v_c
                              int T, int D, int num_pages, int page_size, int max_pages,
                              float sm_scale, int quant_mode, void* workspace,
                              size_t workspace_bytes, void* stream) {
-  if (B < 0 || Hq < 1 || T < 0 || !(sm_scale > 0.f) || !isfinite(sm_scale))
+  if (B < 0 || Hq < 1 || T < 0 || !(sm_scale > 0.f) || !isfinite(sm_scale * kLog2e))
     return QAT_ERR_INVALID_ARG;
   if (quant_mode != QAT_QUANT_NONE && quant_mode != QAT_QUANT_P_FP8E4M3_ROW_TILE64)
     return QAT_ERR_INVALID_ARG;

@@ -15,7 +15,7 @@ import torch
 from torch.autograd.function import once_differentiable
 
 from . import capi
-from .attention import _raise, check_device_status, _check_enabled, device_guard
+from .attention import _raise, device_guard
 
 
 class RopePlan:
@@ -184,8 +184,8 @@ def _tail(rope):
     return rope.phases, rope.rotary_dim, 1 if rope.layout == "interleaved" else 0, rope.amplitude
 
 
-def _forward(q, k, positions, rope, q_weight, k_weight, eps):
-    dev, qs, ks, B, Hq, Hk, N, D, pos_stride = _operands(q, k, positions, rope, q_weight, k_weight)
+def _forward(ops, q, k, positions, rope, q_weight, k_weight, eps):
+    dev, qs, ks, B, Hq, Hk, N, D, pos_stride = ops
     phases, R, inter, amp = _tail(rope)
     q_out = torch.empty((B, Hq, N, D), dtype=torch.bfloat16, device=dev)
     k_out = None if k is None else torch.empty((B, Hk, N, D), dtype=torch.bfloat16, device=dev)
@@ -198,25 +198,20 @@ def _forward(q, k, positions, rope, q_weight, k_weight, eps):
     return q_out, k_out
 
 
-def qat_qk_norm_rope_backward(q, k, positions, rope, q_weight, k_weight, dq_out, dk_out,
-                              eps: float = 1e-6, workspace: torch.Tensor | None = None):
-    """Gradients (dq, dk, dq_weight, dk_weight) of ``qat_qk_norm_rope`` at its inputs, given those of
-    its outputs; None for what is absent.  dq and dk have the inputs' order in memory."""
-    dev, qs, ks, B, Hq, Hk, N, D, pos_stride = _operands(q, k, positions, rope, q_weight, k_weight)
+def _backward(ops, q, k, positions, rope, q_weight, k_weight, dq_out, dk_out, eps, workspace=None):
+    dev, qs, ks, B, Hq, Hk, N, D, pos_stride = ops
     phases, R, inter, amp = _tail(rope)
     gqs = rows_strides(dq_out, "dq_out", dev, (B, Hq, N, D))
-    if (k is None) != (dk_out is None):
-        raise ValueError("dk_out goes together with k")
     gks = None if k is None else rows_strides(dk_out, "dk_out", dev, (B, Hk, N, D))
 
-    def grad_of(x, strides, H):
+    def grad_of(strides, H):
         if strides is not None and strides[2] > strides[1]:  # heads inner, as a projection writes them
             g = torch.empty((B, N, H, D), dtype=torch.bfloat16, device=dev)
             return g.transpose(1, 2), (N * H * D, D, H * D)
         return torch.empty((B, H, N, D), dtype=torch.bfloat16, device=dev), None
 
-    dq, dqs = grad_of(q, qs, Hq)
-    dk, dks = (None, None) if k is None else grad_of(k, ks, Hk)
+    dq, dqs = grad_of(qs, Hq)
+    dk, dks = (None, None) if k is None else grad_of(ks, Hk)
     dwq = dwk = None
     ws_bytes = 0
     if q_weight is not None:
@@ -235,34 +230,47 @@ def qat_qk_norm_rope_backward(q, k, positions, rope, q_weight, k_weight, dq_out,
     return dq, dk, dwq, dwk
 
 
+def qat_qk_norm_rope_backward(q, k, positions, rope, q_weight, k_weight, dq_out, dk_out,
+                              eps: float = 1e-6, workspace: torch.Tensor | None = None):
+    """Gradients (dq, dk, dq_weight, dk_weight) of ``qat_qk_norm_rope`` at its inputs, given those of
+    its outputs; None for what is absent.  dq and dk have the inputs' order in memory.  ``workspace``:
+    uint8, at least ``capi.qat_qk_norm_rope_bwd_workspace_bytes(D)`` bytes, allocated if None."""
+    ops = _operands(q, k, positions, rope, q_weight, k_weight)
+    if (k is None) != (dk_out is None):
+        raise ValueError("dk_out goes together with k")
+    if workspace is not None and (workspace.device != ops[0] or workspace.dtype != torch.uint8
+                                  or not workspace.is_contiguous()):
+        raise ValueError(f"workspace must be a contiguous uint8 tensor on {ops[0]}")
+    return _backward(ops, q, k, positions, rope, q_weight, k_weight, dq_out, dk_out, eps, workspace)
+
+
 class QKNormRope(torch.autograd.Function):
     """Forward returns the normed and rotated q (and k); nothing but the inputs is saved, the
     backward recomputes the norm."""
 
     @staticmethod
-    def forward(ctx, q, k, positions, rope, q_weight, k_weight, eps, check):
+    def forward(ctx, q, k, positions, rope, q_weight, k_weight, eps):
+        ops = _operands(q, k, positions, rope, q_weight, k_weight)
         ctx.save_for_backward(q, k, positions, q_weight, k_weight)
-        ctx.rope, ctx.eps, ctx.check = rope, eps, check
-        out = _forward(q, k, positions, rope, q_weight, k_weight, eps)
+        ctx.rest = ops, rope, eps
+        out = _forward(ops, q, k, positions, rope, q_weight, k_weight, eps)
         return out[0] if k is None else out
 
     @staticmethod
     @once_differentiable
     def backward(ctx, dq_out, dk_out=None):
         q, k, positions, q_weight, k_weight = ctx.saved_tensors
-
-        def ready(d):
-            return d if d is None or readable(d) else d.contiguous()
-
-        dq, dk, dwq, dwk = qat_qk_norm_rope_backward(q, k, positions, ctx.rope, q_weight, k_weight,
-                                                     ready(dq_out), ready(dk_out), ctx.eps)
-        if ctx.check:
-            check_device_status("qat_qk_norm_rope_bwd")
-        return dq, dk, None, None, dwq, dwk, None, None
+        ops, rope, eps = ctx.rest
+        if not readable(dq_out):
+            dq_out = dq_out.contiguous()
+        if dk_out is not None and not readable(dk_out):
+            dk_out = dk_out.contiguous()
+        dq, dk, dwq, dwk = _backward(ops, q, k, positions, rope, q_weight, k_weight, dq_out, dk_out, eps)
+        return dq, dk, None, None, dwq, dwk, None
 
 
 def qat_qk_norm_rope(q, k=None, positions=None, rope: RopePlan | None = None, q_weight=None,
-                     k_weight=None, eps: float = 1e-6, check: bool | None = None):
+                     k_weight=None, eps: float = 1e-6):
     """Per-head RMS norm (with ``q_weight`` / ``k_weight``, [D] fp32 or bf16) and rotary positions
     (with ``rope`` and int32 ``positions``, [N] or [B, N]) of q [B, Hq, N, D] and k [B, Hk, N, D]
     (or None), bf16; either step may be left out.  Returns (q, k) contiguous [B, H, N, D], what
@@ -271,14 +279,12 @@ def qat_qk_norm_rope(q, k=None, positions=None, rope: RopePlan | None = None, q_
     The inputs may have any strides with D innermost and rows on 16-byte boundaries: a slice of a
     fused projection, ``x.view(B, N, H, D).transpose(1, 2)``, is read in place.  Differentiable in q,
     k and the weights; the gradients are deterministic."""
-    check = _check_enabled(check)
     if torch.is_grad_enabled() and any(
             isinstance(t, torch.Tensor) and t.requires_grad for t in (q, k, q_weight, k_weight)):
-        out = QKNormRope.apply(q, k, positions, rope, q_weight, k_weight, eps, check)
+        out = QKNormRope.apply(q, k, positions, rope, q_weight, k_weight, eps)
     else:
-        out = _forward(q, k, positions, rope, q_weight, k_weight, eps)
+        ops = _operands(q, k, positions, rope, q_weight, k_weight)
+        out = _forward(ops, q, k, positions, rope, q_weight, k_weight, eps)
         if k is None:
             out = out[0]
-    if check:
-        check_device_status("qat_qk_norm_rope")
     return out

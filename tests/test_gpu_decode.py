@@ -75,7 +75,7 @@ def _check(q, lens, Hkv, page, cache, table, codes, scales, quant, sm_scale=None
                 assert (err <= tol).all(), (b, hq, float((err / np.maximum(tol, 1e-300)).max()))
                 seen = np.isfinite(wl)
                 assert np.array_equal(np.isneginf(fl[b, hq]), ~seen)
-                assert (np.abs(fl[b, hq] - wl)[seen] <= ltol[seen]).all()
+                assert (np.abs(fl[b, hq][seen] - wl[seen]) <= ltol[seen]).all()
     return o, lse
 
 
@@ -109,6 +109,22 @@ def test_many_sequences():
     cache, table, codes, scales = _cache(lens, 1, 64, 16, 3)
     q = dev_bf16(normal_bf16(9, (700, 3, 1, 64)))
     _check(q, lens, 1, 16, cache, table, codes, scales, 1)
+
+
+def test_largest_batch():
+    """4096 sequences, the most a call takes; one more is refused."""
+    lens = [int(x) for x in np.random.default_rng(8).integers(0, 40, 4096)]
+    cache, table, codes, scales = _cache(lens, 1, 64, 16, 3)
+    q = dev_bf16(normal_bf16(9, (4096, 1, 1, 64)))
+    o = qat_attention_decode(q, cache, _i32(table), _i32(lens), check=True)
+    for b in (0, 1, 2047, 4094, 4095):
+        k, v = (_sequence(c, s, table, b, 0, lens[b], 16) for c, s in zip(codes, scales))
+        w, _, tol, _ = so.decode_head(host_f64(q[b, 0]), k, v, np.array([lens[b] - 1]), 0.125, 1)
+        assert (np.abs(host_f64(o[b, 0]) - w) <= tol).all()
+    with pytest.raises(QatError) as e:
+        qat_attention_decode(dev_bf16(normal_bf16(9, (4097, 1, 1, 64))), cache,
+                             _i32(np.zeros((4097, 1), np.int32)), _i32([0] * 4097))
+    assert e.value.status == Status.UNSUPPORTED
 
 
 def test_long_sequence():
@@ -152,7 +168,8 @@ def test_batch_of_long_sequences(D, Hq, Hkv, T):
         for hq in range(h * (Hq // Hkv), (h + 1) * (Hq // Hkv)):
             w, wl, tol, ltol = so.decode_head(host_f64(q[b, hq]), k, v, n - T + np.arange(T), D ** -0.5, 1)
             assert (np.abs(host_f64(o[b, hq]) - w) <= tol).all()
-            assert (np.abs(host_f64(lse[b, hq]) - wl)[np.isfinite(wl)] <= ltol[np.isfinite(wl)]).all()
+            seen = np.isfinite(wl)
+            assert (np.abs(host_f64(lse[b, hq])[seen] - wl[seen]) <= ltol[seen]).all()
     ws = torch.randint(0, 256, (capi.qat_attn_decode_workspace_bytes(Hq, Hkv, T, D),), dtype=torch.uint8,
                        device="cuda")
     for _ in range(3):
