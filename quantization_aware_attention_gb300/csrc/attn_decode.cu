@@ -796,43 +796,61 @@ __device__ __forceinline__ void store_row(const Params& p, int item, int r, int 
   if (lane == 0 && p.a.lse != nullptr) p.a.lse[row] = none ? -INFINITY : s.m + log2f(s.l);
 }
 
-// Adds the partials of the items that ranges cut.  Block (x, r) takes row r of the items that the
-// ranges of workers 8 x .. 8 x + 7 begin and do not end: one warp each, or all eight warps together
-// where an item's chain of partials is long.
-constexpr int kMergeWarps = 8;
+// Adds the partials of the items that ranges cut.  Block (x, r) takes row r
+//   kFew = false: of the items that ranges of workers 8 x .. 8 x + 7 begin and do not end, 8 warps: one
+//     each, or all together where an item's chain of partials is long;
+//   kFew = true: of item x, 32 warps, where the items are so few that every chain is long (one sequence
+//     of 131072 keys, one KV head, 8 query heads: 50 us in all without, 28 with it).
+constexpr int kMergeSpan = 8;
 
-template <int D>
-__global__ void __launch_bounds__(32 * kMergeWarps) decode_merge_kernel(const Params p) {
+template <int D, bool kFew>
+__global__ void __launch_bounds__(kFew ? 1024 : 256) decode_merge_kernel(const Params p) {
   constexpr int V = D / 32;
+  constexpr int W = kFew ? 32 : 8;
   constexpr int kShort = 16;
-  __shared__ float acc[kMergeWarps][D], ml[kMergeWarps][2];
+  __shared__ float acc[W][D], ml[W][2];
+  __shared__ WorkerMeta found;
+  const int r = blockIdx.y, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (kFew && threadIdx.x == 0) found = WorkerMeta{-1, -1};
   asm volatile("griddepcontrol.wait;" ::: "memory");  // the partials are complete
-  const int w0 = blockIdx.x * kMergeWarps, r = blockIdx.y;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  // one round trip: the count and the chains' ends, which mean nothing beyond the count
   const int workers = __ldcg(&header_of(p)->workers);
-  int2 raw = make_int2(-1, -1);
-  if (lane < kMergeWarps) raw = __ldcg(reinterpret_cast<const int2*>(meta_of(p) + w0 + lane));
-  if (w0 >= workers) return;
-  WorkerMeta mine = {-1, -1};
-  if (w0 + lane < workers) mine = WorkerMeta{raw.x, raw.y};
-  const bool cut = mine.tail >= 0 && mine.tail % p.mtiles * p.rows + r < p.R;
-  const int n = cut ? mine.last - (w0 + lane) + 1 : 0;
-  Sum<V> sum;
-  {
-    const int len = __shfl_sync(0xffffffffu, n, warp), item = __shfl_sync(0xffffffffu, mine.tail, warp);
+  // lane k: the chain of the block's k-th worker's item, if its range cuts one
+  int w = 0, n = 0, item = 0;
+  if constexpr (kFew) {
+    __syncthreads();
+    for (int i = threadIdx.x; i < workers; i += 1024) {
+      const int2 raw = __ldcg(reinterpret_cast<const int2*>(meta_of(p) + i));
+      if (raw.x == static_cast<int>(blockIdx.x)) found = WorkerMeta{i, raw.y};  // one of them at most
+    }
+    __syncthreads();
+    item = blockIdx.x;
+    w = found.tail;
+    if (lane == 0 && w >= 0 && item % p.mtiles * p.rows + r < p.R) n = found.last - w + 1;
+  } else {
+    const int w0 = blockIdx.x * kMergeSpan;
+    int2 raw = make_int2(-1, -1);  // means nothing beyond the count
+    if (lane < kMergeSpan) raw = __ldcg(reinterpret_cast<const int2*>(meta_of(p) + w0 + lane));
+    if (w0 >= workers) return;
+    item = raw.x;
+    w = w0 + lane;
+    if (lane < kMergeSpan && w < workers && item >= 0 && item % p.mtiles * p.rows + r < p.R)
+      n = raw.y - w + 1;
+    const int len = __shfl_sync(0xffffffffu, n, warp), it = __shfl_sync(0xffffffffu, item, warp);
     if (len > 0 && len <= kShort) {
+      Sum<V> sum;
       sum.clear();
       add_chain<D>(p, w0 + warp, 0, 1, len, r, lane, sum);
-      store_row<D>(p, item, r, lane, sum);
+      store_row<D>(p, it, r, lane, sum);
     }
   }
-  unsigned rest = __ballot_sync(0xffffffffu, n > kShort);  // the same in every warp
+  unsigned rest = __ballot_sync(0xffffffffu, n > (kFew ? 0 : kShort));  // the same in every warp
   while (rest != 0) {
     const int k = __ffs(rest) - 1;
     rest &= rest - 1;
+    const int len = __shfl_sync(0xffffffffu, n, k);
+    Sum<V> sum;
     sum.clear();
-    add_chain<D>(p, w0 + k, warp, kMergeWarps, __shfl_sync(0xffffffffu, n, k), r, lane, sum);
+    add_chain<D>(p, __shfl_sync(0xffffffffu, w, k), warp, W, len, r, lane, sum);
 #pragma unroll
     for (int i = 0; i < V; ++i) acc[warp][V * lane + i] = sum.acc[i];
     if (lane == 0) {
@@ -840,15 +858,28 @@ __global__ void __launch_bounds__(32 * kMergeWarps) decode_merge_kernel(const Pa
       ml[warp][1] = sum.l;
     }
     __syncthreads();
-    const int item = __shfl_sync(0xffffffffu, mine.tail, k);
-    if (warp == 0) {
-      for (int x = 1; x < kMergeWarps; ++x) {
-        float o2[V];
+    const int it = __shfl_sync(0xffffffffu, item, k);
+    if (warp == 0) {  // lane x weighs warp x's sums; then every lane adds its channels of all
+      const bool mine = lane < W;
+      const float m = mine ? ml[lane][0] : -INFINITY;
+      float top = m;
 #pragma unroll
-        for (int i = 0; i < V; ++i) o2[i] = acc[x][V * lane + i];
-        sum.add(ml[x][0], ml[x][1], o2);
+      for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+      const float f = mine ? ex2(m - (top == -INFINITY ? 0.f : top)) : 0.f;
+      float l = mine ? ml[lane][1] * f : 0.f;
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+      sum.m = top;
+      sum.l = l;
+#pragma unroll
+      for (int i = 0; i < V; ++i) sum.acc[i] = 0.f;
+#pragma unroll 8
+      for (int x = 0; x < W; ++x) {
+        const float fx = __shfl_sync(0xffffffffu, f, x);
+#pragma unroll
+        for (int i = 0; i < V; ++i) sum.acc[i] = fmaf(acc[x][V * lane + i], fx, sum.acc[i]);
       }
-      store_row<D>(p, item, r, lane, sum);
+      store_row<D>(p, it, r, lane, sum);
     }
     __syncthreads();
   }
@@ -867,15 +898,19 @@ cudaError_t run(const Params& p, int ctas, long long units, cudaStream_t s) {
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   const int most = static_cast<int>(units < ctas * C::kWarps ? units : ctas * C::kWarps);
-  cfg.gridDim = dim3((most + kMergeWarps - 1) / kMergeWarps, p.R < p.rows ? p.R : p.rows);
-  cfg.blockDim = dim3(32 * kMergeWarps);
+  const long long items = static_cast<long long>(p.a.B) * p.a.Hkv * p.mtiles;
+  const bool few = items * 32 <= most;
+  cfg.gridDim = dim3(few ? static_cast<unsigned>(items) : (most + kMergeSpan - 1) / kMergeSpan,
+                     p.R < p.rows ? p.R : p.rows);
+  cfg.blockDim = dim3(few ? 1024 : 256);
   cfg.stream = s;
   cudaLaunchAttribute at[1];
   at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   at[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = at;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, decode_merge_kernel<D>, p);
+  return few ? cudaLaunchKernelEx(&cfg, decode_merge_kernel<D, true>, p)
+             : cudaLaunchKernelEx(&cfg, decode_merge_kernel<D, false>, p);
 }
 
 }  // namespace
