@@ -391,7 +391,7 @@ QAT_API qat_status_t qat_kv_cache_read(const void* k_codes, const void* v_codes,
  *            overlap need two workspaces.
  *   The work is split by the lengths on the device; the same lengths give the same bits.
  * Errors: as the cache's entries, QAT_ERR_UNSUPPORTED also for T or B above the limits or more than
- *   2^31 64-key tiles; QAT_ERR_WORKSPACE.  Pages outside the cache give NaN rows (see above).
+ *   2^30 64-key tiles; QAT_ERR_WORKSPACE.  Pages outside the cache give NaN rows (see above).
  */
 QAT_API size_t qat_attn_decode_workspace_bytes(int Hq, int Hkv, int T, int D);
 QAT_API qat_status_t qat_attn_decode(const void* q, const void* k_codes, const void* v_codes,

@@ -12,12 +12,14 @@
 // between warps, and all G = Hq / Hkv heads that share a KV head (times T tokens) are rows of one
 // 16-row tile, so that the cache is read once for all of them.
 //
-// Work split (stream-K): the batch's units -- 64-key tiles, ordered by sequence, KV head, row tile,
-// key -- are cut into equal contiguous ranges, one per warp, whatever the sequences' lengths.  An
-// (sequence, head, row tile) item inside one range is finished there; an item cut by a range
-// boundary leaves unnormalized fp32 partials with their m and l in the workspace, which
-// decode_merge_kernel adds in an order that the lengths alone decide (no atomics: the same lengths
-// give the same bits).
+// Work split (stream-K).  The batch's units -- 64-key tiles, ordered by sequence, KV head, row tile,
+// key, and one more at the head of every (sequence, head, row tile) item for what an item costs beside its
+// tiles -- are cut into equal contiguous ranges, one per warp, whatever the sequences' lengths.  (Without
+// the item's unit, warps that got many short sequences ended last: 64 sequences of 129 to 8192 keys, 3
+// tokens, 64 channels, 104 against 87 us.)  An item inside one range is finished there; an item cut by a
+// range boundary leaves unnormalized fp32 partials with their m and l in the workspace, which
+// decode_merge_kernel adds in an order that the lengths alone decide (no atomics: the same lengths give
+// the same bits).
 //
 // Products: mma.sync m16n8k16 with f16 operands and fp32 sums, the cache as the 16-row operand and
 // the query rows as the 8 columns (one column tile for up to 8 rows, else two): S^T = K Q^T and
@@ -195,8 +197,11 @@ __device__ __forceinline__ void enter_seq(const Params& p, const int* prefix, Cu
   c.len = min(clamp_len(p.a, __ldg(p.a.seq_lens + c.b)), c.tiles * kTile);
 }
 
-__device__ __forceinline__ void advance(const Params& p, const int* prefix, Cursor& c) {
+// The next tile; u: its unit.
+__device__ __forceinline__ void advance(const Params& p, const int* prefix, int extra, Cursor& c, int& u) {
+  ++u;
   if (++c.tile < c.tiles) return;
+  u += extra;
   c.tile = 0;
   if (++c.mt < p.mtiles) return;
   c.mt = 0;
@@ -330,33 +335,37 @@ __global__ void __launch_bounds__(32 * Cfg<D, NR>::kWarps, 1) decode_kernel(cons
     if (tid == kThreads - 1) prefix[a.B] = base;
     __syncthreads();
   }
-  const int W = prefix[a.B];
-  // workers: as few warps per CTA as give every worker a unit, spread over the CTAs
-  const int per_cta = min(C::kWarps, (W + static_cast<int>(gridDim.x) - 1) / static_cast<int>(gridDim.x));
-  const int workers = min(W, per_cta * static_cast<int>(gridDim.x));
+  const int tiles = prefix[a.B];
+  // workers: as few warps per CTA as give every worker a tile, spread over the CTAs
+  const int per_cta = min(C::kWarps, (tiles + static_cast<int>(gridDim.x) - 1) / static_cast<int>(gridDim.x));
+  const int workers = min(tiles, per_cta * static_cast<int>(gridDim.x));
   if (blockIdx.x == 0 && tid == 0) header_of(p)->workers = workers;
   // the merge kernel's blocks may be brought up; they wait for this grid's end
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if (warp >= per_cta) return;
   const int id = blockIdx.x * per_cta + warp;
   if (id >= workers) return;
-  const int u0 = static_cast<int>(static_cast<long long>(W) * id / workers);
+  // an item's own unit, where ranges are long enough that each holds a tile all the same
+  const int extra = tiles / 4 >= workers ? 1 : 0;
+  const int W = tiles + extra * a.B * per_seq;
+  int u0 = static_cast<int>(static_cast<long long>(W) * id / workers);
   const int u1 = static_cast<int>(static_cast<long long>(W) * (id + 1) / workers);
 
   Cursor cc;  // what is computed next
   {
-    int lo = 0, hi = a.B;  // the last b with prefix[b] <= u0
+    int lo = 0, hi = a.B;  // the last b whose units begin at u0 or before
     while (hi - lo > 1) {
       const int mid = (lo + hi) >> 1;
-      if (prefix[mid] <= u0) lo = mid; else hi = mid;
+      if (prefix[mid] + extra * mid * per_seq <= u0) lo = mid; else hi = mid;
     }
     cc.b = lo;
     enter_seq(p, prefix, cc);
-    int u = u0 - prefix[lo];
-    cc.tile = u % cc.tiles;
-    u /= cc.tiles;
-    cc.mt = u % p.mtiles;
-    cc.h = u / p.mtiles;
+    const int u = u0 - (prefix[lo] + extra * lo * per_seq);
+    const int item = u / (cc.tiles + extra), in = u - item * (cc.tiles + extra);
+    cc.tile = max(in - extra, 0);
+    if (in < extra) ++u0;  // to the item's first tile
+    cc.mt = item % p.mtiles;
+    cc.h = item / p.mtiles;
   }
   Cursor pc = cc;  // what is loaded next
   int pu = u0;
@@ -434,8 +443,7 @@ __global__ void __launch_bounds__(32 * Cfg<D, NR>::kWarps, 1) decode_kernel(cons
       }
       pslot = pslot + 1 == C::kSlots ? 0 : pslot + 1;
       if (sub == 3) {
-        ++pu;
-        advance(p, prefix, pc);
+        advance(p, prefix, extra, pc, pu);
       }
     }
     cp_commit();
@@ -469,7 +477,7 @@ __global__ void __launch_bounds__(32 * Cfg<D, NR>::kWarps, 1) decode_kernel(cons
   if (lane == 0) meta_of(p)[id] = WorkerMeta{-1, -1};
   int first_tile = cc.tile;    // of the current segment
 
-  for (int u = u0; u < u1; ++u) {
+  for (int u = u0; u < u1;) {
     if (!begun) {
       begun = true;
       first_tile = cc.tile;
@@ -662,7 +670,7 @@ __global__ void __launch_bounds__(32 * Cfg<D, NR>::kWarps, 1) decode_kernel(cons
     }
 
     const bool ends = cc.tile + 1 == cc.tiles;
-    if (ends || u + 1 == u1) {  // the segment's end
+    if (ends || u + 1 >= u1) {  // the segment's end
       begun = false;
       const bool head = first_tile != 0;
       const bool whole = !head && ends;
@@ -708,7 +716,7 @@ __global__ void __launch_bounds__(32 * Cfg<D, NR>::kWarps, 1) decode_kernel(cons
         }
       }
     }
-    advance(p, prefix, cc);
+    advance(p, prefix, extra, cc, u);
   }
 #undef QAT_SUB
   cp_wait<0>();

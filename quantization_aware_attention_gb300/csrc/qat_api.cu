@@ -648,7 +648,7 @@ qat_status_t qat_attn_decode(const void* q, const void* k_codes, const void* v_c
   if (rows > kMaxRows || static_cast<long long>(B) * Hkv > kMaxRows) return QAT_ERR_UNSUPPORTED;
   const long long units = (static_cast<long long>(max_pages) * page_size + 63) / 64;
   const double all = static_cast<double>(units) * B * Hkv * static_cast<double>((rows + 15) / 16);
-  if (all > static_cast<double>(kMaxRows)) return QAT_ERR_UNSUPPORTED;
+  if (all > 1073741823.0) return QAT_ERR_UNSUPPORTED;
   if (B == 0 || T == 0) return QAT_OK;
   if (!cache_pointers_ok(k_codes, v_codes, k_scales, v_scales, block_table, seq_lens))
     return QAT_ERR_INVALID_ARG;
