@@ -8,6 +8,8 @@ read on the device, so every call can be captured into a CUDA graph and replayed
 
 from __future__ import annotations
 
+import functools
+
 import torch
 
 from . import capi
@@ -30,6 +32,11 @@ def _index(t, name, device, shape):
         raise ValueError(f"{name} must be torch.int32, got {t.dtype}")
     raise ValueError(f"{name} must be contiguous with shape {tuple(shape)} (-1: any), got "
                      f"{tuple(t.shape)}")
+
+
+@functools.lru_cache(maxsize=64)
+def _workspace_bytes(Hq, heads, T, D):
+    return max(capi.qat_attn_decode_workspace_bytes(Hq, heads, T, D), 256)
 
 
 def _no_gradient(name, *tensors):
@@ -169,8 +176,7 @@ def qat_attention_decode(q, cache: KVCache, block_table, seq_lens, sm_scale: flo
     if Hq < 1 or Hq % cache.heads:
         raise ValueError(f"{Hq} query heads do not share the cache's {cache.heads} evenly")
     if workspace is None:
-        workspace = torch.empty(max(capi.qat_attn_decode_workspace_bytes(Hq, cache.heads, T, D), 256),
-                                dtype=torch.uint8, device=dev)
+        workspace = torch.empty(_workspace_bytes(Hq, cache.heads, T, D), dtype=torch.uint8, device=dev)
     elif not isinstance(workspace, torch.Tensor) or workspace.device != dev or (
             workspace.dtype != torch.uint8 or not workspace.is_contiguous()):
         raise ValueError(f"workspace must be a contiguous uint8 tensor on {dev}")
