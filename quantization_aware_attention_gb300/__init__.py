@@ -12,5 +12,5 @@ from .capi import (QUANT_NONE, QUANT_P_FP8E4M3_ROW_TILE64,  # noqa: F401
 from .attention import (QATAttention, attention, check_device_status,  # noqa: F401
                         qat_attention_backward, qat_attention_forward, qat_prepare_qkv,
                         qat_subtract_mean)
-from .rope import QKNormRope, RopePlan, qat_qk_norm_rope, qat_qk_norm_rope_backward  # noqa: F401
+from .rope import RopePlan, qat_qk_norm_rope, qat_qk_norm_rope_backward  # noqa: F401
 from .cache import KVCache, qat_attention_decode  # noqa: F401

@@ -11,7 +11,6 @@ _attention.forward saves q, k, v, O and M).
 
 from __future__ import annotations
 
-import contextlib
 import math
 import os
 
@@ -55,16 +54,6 @@ def _check_enabled(check: bool | None) -> bool:
     if check is not None:
         return bool(check)
     return os.environ.get("QAT_CHECK_STATUS", "0") == "1"
-
-
-_no_guard = contextlib.nullcontext()
-
-
-def device_guard(device: torch.device):
-    """Makes ``device`` current for a call; nothing to do, and nothing paid, when it is."""
-    if device.index == torch.cuda.current_device():
-        return _no_guard
-    return torch.cuda.device(device)
 
 
 def check_device_status(what: str = "QAT attention") -> None:

@@ -1,4 +1,5 @@
-"""Builds the in-tree C-ABI library ``libqat_attn.so`` for sm_103a with nvcc.
+"""Builds the in-tree C-ABI library ``libqat_attn.so`` for sm_103a with nvcc, and the torch extension
+``_qat_torch`` (host code over that library) with the host compiler.
 
 Translation units are compiled in parallel, then linked with ``nvcc -shared``; the CUDA
 runtime is linked statically.  An object is rebuilt when its source or any header of
@@ -19,6 +20,8 @@ CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 OBJDIR = os.path.join(HERE, "_build_tmp")
 LIB_PATH = os.path.join(HERE, "libqat_attn.so")
+EXT_PATH = os.path.join(HERE, "_qat_torch.so")
+EXT_SOURCE = "torch_ops.cpp"
 
 SOURCES = ["qat_api.cu", "attn_fwd_sm100.cu", "attn_bwd_sm100.cu", "attn_bwd_dq_sm100.cu",
            "quant_debug.cu", "qat_noalloc.cu", "qkv_quant.cu", "attn_merge.cu", "debug_wait.cu",
@@ -59,13 +62,60 @@ def _compile(src: str, extra: list[str], verbose: bool) -> str:
     return obj
 
 
+def _compile_ext(verbose: bool) -> str:
+    """The torch extension's object, compiled against the installed torch's headers."""
+    import sysconfig
+
+    import torch
+
+    obj = os.path.join(OBJDIR, f"torch_ops-{torch.__version__}.o")
+    src = os.path.join(CSRC, EXT_SOURCE)
+    newest = max(os.path.getmtime(src), os.path.getmtime(os.path.join(INCLUDE, "qat_attn.h")))
+    if os.path.exists(obj) and os.path.getmtime(obj) >= newest:
+        return obj
+    base = os.path.join(os.path.dirname(torch.__file__), "include")
+    cuda = os.path.join(os.path.dirname(os.path.dirname(_nvcc())), "include")
+    cmd = [shutil.which("g++") or "c++", "-c", src, "-o", obj, "-O2", "-std=c++17", "-fPIC",
+           "-fvisibility=hidden", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           "-I", INCLUDE]
+    for path in (base, os.path.join(base, "torch", "csrc", "api", "include"),
+                 sysconfig.get_paths()["include"], cuda):
+        cmd += ["-isystem", path]
+    _run(cmd, EXT_SOURCE, verbose)
+    return obj
+
+
+def _link_ext(obj: str, verbose: bool) -> None:
+    import torch
+
+    if os.path.exists(EXT_PATH) and os.path.getmtime(EXT_PATH) >= os.path.getmtime(obj):
+        return
+    lib = os.path.join(os.path.dirname(torch.__file__), "lib")
+    tmp = EXT_PATH + ".tmp"
+    _run([shutil.which("g++") or "c++", "-shared", obj, "-o", tmp, "-L", HERE, "-l:libqat_attn.so",
+          "-L", lib, "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch", "-ltorch_python",
+          "-Wl,-rpath,$ORIGIN", f"-Wl,-rpath,{lib}"], "_qat_torch", verbose)
+    os.replace(tmp, EXT_PATH)
+
+
+def _run(cmd: list[str], what: str, verbose: bool) -> None:
+    if verbose:
+        print(" ".join(cmd), flush=True)
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"building {what} failed:\n{r.stdout}\n{r.stderr}")
+
+
 def build(verbose: bool = False, ptxas_verbose: bool = False) -> str:
-    """Compile every CUDA source and link ``libqat_attn.so``; returns its path."""
+    """Compile every source and link ``libqat_attn.so`` and the torch extension; returns the library's
+    path."""
     os.makedirs(OBJDIR, exist_ok=True)
     extra = ["-Xptxas", "-v"] if ptxas_verbose else []
-    workers = min(len(SOURCES), os.cpu_count() or 1)
+    workers = min(len(SOURCES) + 1, os.cpu_count() or 1)
     with concurrent.futures.ThreadPoolExecutor(max_workers=workers) as ex:
+        ext = ex.submit(_compile_ext, verbose or ptxas_verbose)
         objs = list(ex.map(lambda s: _compile(s, extra, verbose or ptxas_verbose), SOURCES))
+        ext_obj = ext.result()
     newest = max(os.path.getmtime(o) for o in objs)
     if not os.path.exists(LIB_PATH) or os.path.getmtime(LIB_PATH) < newest:
         tmp = LIB_PATH + ".tmp"
@@ -74,6 +124,7 @@ def build(verbose: bool = False, ptxas_verbose: bool = False) -> str:
         if r.returncode != 0:
             raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
         os.replace(tmp, LIB_PATH)
+    _link_ext(ext_obj, verbose or ptxas_verbose)
     return LIB_PATH
 
 

@@ -8,41 +8,9 @@ read on the device, so every call can be captured into a CUDA graph and replayed
 
 from __future__ import annotations
 
-import functools
-
 import torch
 
 from . import capi
-from .attention import _raise, check_device_status, _check_enabled, device_guard
-from .rope import rows_strides
-
-
-def _index(t, name, device, shape):
-    """An int32 tensor of that shape (-1: any size), contiguous, on the device."""
-    if (isinstance(t, torch.Tensor) and t.dtype is torch.int32 and t.device == device
-            and t.dim() == len(shape) and t.is_contiguous()):
-        for n, want in zip(t.shape, shape):
-            if want >= 0 and n != want:
-                break
-        else:
-            return
-    if not isinstance(t, torch.Tensor) or t.device != device:
-        raise ValueError(f"{name} must be a tensor on {device}")
-    if t.dtype != torch.int32:
-        raise ValueError(f"{name} must be torch.int32, got {t.dtype}")
-    raise ValueError(f"{name} must be contiguous with shape {tuple(shape)} (-1: any), got "
-                     f"{tuple(t.shape)}")
-
-
-@functools.lru_cache(maxsize=64)
-def _workspace_bytes(Hq, heads, T, D):
-    return max(capi.qat_attn_decode_workspace_bytes(Hq, heads, T, D), 256)
-
-
-def _no_gradient(name, *tensors):
-    if torch.is_grad_enabled() and any(t.requires_grad for t in tensors):
-        raise ValueError(f"{name} has no backward: call it under torch.no_grad(), or with tensors that "
-                         "do not require gradients")
 
 
 class KVCache:
@@ -101,57 +69,20 @@ class KVCache:
 
         return cls(codes(), codes(), scales(), scales())
 
-    def _tables(self, block_table, seq_lens):
-        """(number of sequences, pages of a table row)."""
-        _index(seq_lens, "seq_lens", self.device, (-1,))
-        B = seq_lens.shape[0]
-        _index(block_table, "block_table", self.device, (B, -1))
-        pages = block_table.shape[1]
-        if pages < 1:
-            raise ValueError("block_table has no pages")
-        return B, pages
-
     def append(self, k, v, block_table, seq_lens, new_lens=None, check: bool | None = None) -> None:
         """Quantizes new keys and values, bf16 [B, H, N, D] with any strides that have D innermost,
         into their pages.  ``seq_lens`` are the lengths after the append: row n of sequence b goes to
         position seq_lens[b] - N + n, or, with int32 ``new_lens`` [B], to seq_lens[b] - new_lens[b] + n
         for its first new_lens[b] rows (the others are padding).  No two rows may go to one slot."""
-        B, max_pages = self._tables(block_table, seq_lens)
-        N = k.shape[2] if isinstance(k, torch.Tensor) and k.dim() == 4 else -1
-        shape = (B, self.heads, N, self.D)
-        ks = rows_strides(k, "k", self.device, shape)
-        vs = rows_strides(v, "v", self.device, shape)
-        _no_gradient("append", k, v)
-        if new_lens is not None:
-            _index(new_lens, "new_lens", self.device, (B,))
-        with device_guard(self.device):
-            st = capi.qat_kv_cache_append(
-                k, ks, v, vs, self._k, self._v, self._k_scale, self._v_scale, block_table, seq_lens,
-                new_lens, B, self.heads, N, self.D, self.num_pages, self.page_size, max_pages)
-            _raise(st, "qat_kv_cache_append")
-            if _check_enabled(check):
-                check_device_status("qat_kv_cache_append")
+        capi.torch_ops().kv_append(self._k, self._v, self._k_scale, self._v_scale, k, v, block_table,
+                                   seq_lens, new_lens, check)
 
     def read(self, block_table, seq_lens, begin: int = 0, length: int | None = None,
              check: bool | None = None):
         """(k, v) of positions [begin, begin + length), bf16 [B, H, length, D] contiguous, zeros behind
         a sequence's end.  Without ``length``: all that the block table can hold."""
-        B, max_pages = self._tables(block_table, seq_lens)
-        if begin < 0 or (length is not None and length < 0):
-            raise ValueError("begin and length must not be negative")
-        if length is None:
-            length = max(max_pages * self.page_size - begin, 0)
-        shape = (B, self.heads, length, self.D)
-        k_out = torch.empty(shape, dtype=torch.bfloat16, device=self.device)
-        v_out = torch.empty(shape, dtype=torch.bfloat16, device=self.device)
-        with device_guard(self.device):
-            st = capi.qat_kv_cache_read(self._k, self._v, self._k_scale, self._v_scale, block_table,
-                                        seq_lens, k_out, v_out, B, self.heads, begin, length, self.D,
-                                        self.num_pages, self.page_size, max_pages)
-            _raise(st, "qat_kv_cache_read")
-            if _check_enabled(check):
-                check_device_status("qat_kv_cache_read")
-        return k_out, v_out
+        return capi.torch_ops().kv_read(self._k, self._v, self._k_scale, self._v_scale, block_table,
+                                        seq_lens, begin, length, check)
 
 
 def qat_attention_decode(q, cache: KVCache, block_table, seq_lens, sm_scale: float | None = None,
@@ -162,32 +93,9 @@ def qat_attention_decode(q, cache: KVCache, block_table, seq_lens, sm_scale: flo
     its own.  Hq is a multiple of the cache's heads (consecutive query heads share one); T is at most
     16.  Returns o bf16 [B, Hq, T, D], and with ``return_lse`` the base-2 log-sum-exp fp32 [B, Hq, T].
     A row that sees no key gives o = 0, lse = -inf.  ``workspace``: uint8, at least
-    ``capi.qat_attn_decode_workspace_bytes(Hq, cache.heads, T, D)`` bytes, for one call at a time; allocated if None."""
+    ``capi.qat_attn_decode_workspace_bytes(Hq, cache.heads, T, D)`` bytes, for one call at a time;
+    allocated if None."""
     if not isinstance(cache, KVCache):
         raise TypeError("cache must be a KVCache")
-    B, max_pages = cache._tables(block_table, seq_lens)
-    dev = cache.device
-    if rows_strides(q, "q", dev, None) is not None:
-        raise ValueError("q must be contiguous")
-    Hq, T, D = q.shape[1:]
-    if q.shape[0] != B or D != cache.D:
-        raise ValueError(f"q has shape {tuple(q.shape)}, expected ({B}, Hq, T, {cache.D})")
-    _no_gradient("qat_attention_decode", q)
-    if Hq < 1 or Hq % cache.heads:
-        raise ValueError(f"{Hq} query heads do not share the cache's {cache.heads} evenly")
-    if workspace is None:
-        workspace = torch.empty(_workspace_bytes(Hq, cache.heads, T, D), dtype=torch.uint8, device=dev)
-    elif not isinstance(workspace, torch.Tensor) or workspace.device != dev or (
-            workspace.dtype != torch.uint8 or not workspace.is_contiguous()):
-        raise ValueError(f"workspace must be a contiguous uint8 tensor on {dev}")
-    o = torch.empty_like(q)
-    lse = torch.empty((B, Hq, T), dtype=torch.float32, device=dev) if return_lse else None
-    with device_guard(dev):
-        st = capi.qat_attn_decode(
-            q, cache._k, cache._v, cache._k_scale, cache._v_scale, block_table, seq_lens, o, lse, B, Hq,
-            cache.heads, T, D, cache.num_pages, cache.page_size, max_pages,
-            D ** -0.5 if sm_scale is None else sm_scale, quant_mode, workspace, workspace.numel())
-        _raise(st, "qat_attn_decode")
-        if _check_enabled(check):
-            check_device_status("qat_attn_decode")
-    return (o, lse) if return_lse else o
+    return capi.torch_ops().decode(cache._k, cache._v, cache._k_scale, cache._v_scale, q, block_table,
+                                   seq_lens, sm_scale, quant_mode, return_lse, workspace, check)

@@ -135,6 +135,23 @@ def lib() -> ctypes.CDLL:
     return _lib
 
 
+_ops = None
+
+
+def torch_ops():
+    """The torch extension over the library (loaded once).  Raises if it has not been built."""
+    global _ops
+    if _ops is None:
+        lib()
+        try:
+            from . import _qat_torch
+        except ImportError as e:
+            raise RuntimeError("the torch extension is missing or does not load: build it first "
+                               f"(python -m quantization_aware_attention_gb300.build): {e}") from e
+        _ops = _qat_torch
+    return _ops
+
+
 def _ptr(x) -> int | None:
     if x is None:
         return None

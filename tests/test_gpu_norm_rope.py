@@ -150,6 +150,21 @@ def test_empty_sizes():
         assert dq.shape == q.shape and (dw == 0).all()
 
 
+def test_no_second_derivative():
+    q, _, _, _ = _make(1, 2, 1, 3, 64, 41)
+    q = q.detach().requires_grad_(True)
+    out = qat_qk_norm_rope(q, None, q_weight=torch.ones(64, device="cuda"))
+    with pytest.raises(RuntimeError, match="second derivative"):
+        torch.autograd.grad(out.float().square().sum(), q, create_graph=True)
+
+
+def test_a_tensor_of_no_key_heads():
+    q, _, fq, _ = _make(2, 3, 1, 5, 64, 42)
+    k = torch.empty(2, 0, 5, 64, dtype=torch.bfloat16, device="cuda")
+    a, b = qat_qk_norm_rope(q, k)
+    assert torch.equal(a, q) and b.shape == k.shape
+
+
 def _backward_case(B, Hq, Hk, N, D, R, layout, wtype, amplitude=1.0, inner=True):
     q, k, fq, fk = _make(B, Hq, Hk, N, D, 300 + N, inner)
     ws, fws = _weights(D, 9, wtype)
