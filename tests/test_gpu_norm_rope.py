@@ -277,3 +277,42 @@ def test_refusals(change):
     with pytest.raises((ValueError, TypeError)):
         qat_qk_norm_rope(**args)
     check_device_status()
+
+
+def test_captured_forward_and_backward():
+    """Forward and backward in one graph, through the functions and through autograd; replays follow new
+    inputs, and give the eager call's bits."""
+    q, k, fq, fk, ws, fws, rope, pos, g, fg = _backward_case(2, 6, 2, 37, 64, 64, "half", torch.float32)
+    dpos = torch.from_numpy(pos).cuda()
+    q, k = q.contiguous(), k.contiguous()
+
+    def run():
+        leaves = [t.detach().requires_grad_(True) for t in (q, k, *ws)]
+        out = qat_qk_norm_rope(leaves[0], leaves[1], dpos, rope, leaves[2], leaves[3])
+        grads = torch.autograd.grad(out, leaves, g)
+        return [t.detach() for t in out] + list(grads) + list(
+            qat_qk_norm_rope_backward(q, k, dpos, rope, *ws, *g))
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        run()  # loads the kernels
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        captured = run()
+    for seed in (1, 2):
+        new = dev_bf16(normal_bf16(seed, tuple(q.shape)))
+        q.copy_(new)
+        dpos.add_(seed)
+        graph.replay()
+        for a, b in zip(captured, run()):
+            assert torch.equal(a, b)
+    for a, b in zip(captured[2:6], captured[6:]):
+        assert torch.equal(a, b)
+
+
+def test_sizes_beyond_32_bits_are_refused():
+    x = torch.zeros(1, 1, 1, 64, dtype=torch.bfloat16, device="cuda")
+    with pytest.raises(ValueError, match="too large"):
+        qat_qk_norm_rope(x.expand(1, 1, 2 ** 32 + 1, 64))
