@@ -172,6 +172,7 @@ struct NormRopeTensor {
   const void* w;       // [D] or null: no norm
   void* dw;            // [D] or null
   int H;
+  int log_tokens;      // a warp holds rows of 2^log_tokens tokens at once; filled in by the launcher
 };
 
 struct NormRopeArgs {

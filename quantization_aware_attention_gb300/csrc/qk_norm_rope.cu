@@ -19,8 +19,9 @@
 // Work split.  D / 16 lanes hold one row, 16 channels each as two 16-byte chunks chosen so that both
 // halves of every pair are in one lane; a warp holds 4 rows (D = 128) or 8 (D = 64) of one token,
 // computes the token's angles once and walks the heads of its part, a trip of 4 or 8 heads at a time.
-// A block's 8 warps take 8 consecutive tokens, so that in the head-major output a block writes 2 KB
-// (D = 128) runs.
+// Of a tensor with half as many heads or fewer it takes 2, 4 or 8 tokens at once instead of leaving
+// lanes idle.  A block's 8 warps take consecutive tokens, so that in the head-major output a block
+// writes 2 KB (D = 128) runs.
 //
 // What bounds both directions is HBM; what it takes is bytes in flight.  The rows of the next trips are
 // on their way by cp.async, each lane's own 16-byte pieces into its own place in shared memory: no
@@ -207,23 +208,43 @@ __device__ __forceinline__ uint4 lds128(uint32_t a) {
 
 __device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
 
-template <int D, bool kInter>
+// kFew: a tensor has so few heads that a warp's rows are of several of its tokens.  (A variant, as the
+// lanes' own tokens cost registers: B1 H40+40 N32768 D128 takes 203 us with them, 198 without.)
+template <int D, bool kInter, bool kFew>
 __global__ void __launch_bounds__(32 * kWarps, 4) norm_rope_kernel(const NormRopeArgs p) {
   constexpr int L = D / kPer;    // lanes per row
   constexpr int RW = 32 / L;     // rows per warp and trip
   __shared__ uint4 ring[kWarps][kFwdStages][2][32];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  // parts [0, q_parts) are the query heads, the rest the key heads, heads_per_part each
-  const int part = static_cast<int>(blockIdx.x % static_cast<unsigned>(p.parts));
-  const unsigned tok = blockIdx.x / static_cast<unsigned>(p.parts) * kWarps + warp;
-  if (tok >= static_cast<unsigned long long>(p.tokens)) return;
-  const unsigned b = tok / static_cast<unsigned>(p.N), n = tok - b * static_cast<unsigned>(p.N);
-  const bool key = part >= p.q_parts;
+  bool key;
+  unsigned group, part;  // of the tokens; of the tensor's heads, heads_per_part each
+  if constexpr (kFew) {  // blocks [0, q_blocks) are the queries', the rest the keys'
+    key = blockIdx.x >= static_cast<unsigned>(p.q_blocks);
+    const unsigned blk = key ? blockIdx.x - p.q_blocks : blockIdx.x, parts = key ? p.parts - p.q_parts : p.q_parts;
+    group = blk / parts;
+    part = blk - group * parts;
+  } else {  // the parts of both for the same tokens, one after the other
+    group = blockIdx.x / static_cast<unsigned>(p.parts);
+    part = blockIdx.x - group * static_cast<unsigned>(p.parts);
+    key = part >= static_cast<unsigned>(p.q_parts);
+    if (key) part -= p.q_parts;
+  }
   const NormRopeTensor& t = key ? p.k : p.q;
-  const int h0 = (key ? part - p.q_parts : part) * p.heads_per_part;
-  const int h1 = min(h0 + p.heads_per_part, t.H);
+  const int log_tokens = kFew ? t.log_tokens : 0;
+  const unsigned long long first = (static_cast<unsigned long long>(group) * kWarps + warp) << log_tokens;
+  if (first >= static_cast<unsigned long long>(p.tokens)) return;
+  const int heads = RW >> log_tokens;  // heads of a trip
+  const int sub = lane / L % heads;
+  unsigned tok = static_cast<unsigned>(first);
+  const int h0 = static_cast<int>(part) * p.heads_per_part, h1 = min(h0 + p.heads_per_part, t.H);
+  int lim = h1;  // the lane's rows end at lim
+  if constexpr (kFew) {
+    const unsigned left = static_cast<unsigned>(p.tokens - 1) - tok, ahead = lane / L / heads;
+    if (ahead > left) lim = 0;
+    tok += min(ahead, left);
+  }
+  const unsigned b = tok / static_cast<unsigned>(p.N), n = tok - b * static_cast<unsigned>(p.N);
   const LaneMap<D, kInter> m(lane % L, p.R);
-  const int sub = lane / L;
 
   const uint16_t* src = t.x + b * t.sb + n * t.sn;
   const uint32_t mine = sm100::smem_addr(&ring[warp][0][0][lane]);
@@ -232,9 +253,9 @@ __global__ void __launch_bounds__(32 * kWarps, 4) norm_rope_kernel(const NormRop
   auto fetch = [&]() {
     if (hf - sub < h1) {
       const uint4* row = reinterpret_cast<const uint4*>(src + min(hf, h1 - 1) * t.sh);
-      fetch16(mine + fs * 1024, row + m.ca, hf < h1);
-      fetch16(mine + fs * 1024 + 512, row + m.cb, hf < h1);
-      hf += RW;
+      fetch16(mine + fs * 1024, row + m.ca, hf < lim);
+      fetch16(mine + fs * 1024 + 512, row + m.cb, hf < lim);
+      hf += heads;
       fs = fs + 1 == kFwdStages ? 0 : fs + 1;
     }
     fetch_commit();
@@ -250,7 +271,7 @@ __global__ void __launch_bounds__(32 * kWarps, 4) norm_rope_kernel(const NormRop
 
   uint16_t* dst = t.y + (static_cast<long long>(b) * t.H * p.N + n) * D;
   uint32_t us = 0;
-  for (int h = h0 + sub; h - sub < h1; h += RW) {
+  for (int h = h0 + sub; h - sub < h1; h += heads) {
     fetch();
     fetch_wait<kFwdStages - 1>();
     Chan v;
@@ -265,12 +286,12 @@ __global__ void __launch_bounds__(32 * kWarps, 4) norm_rope_kernel(const NormRop
       }
     }
     rotate<false>(m, v, c, s);
-    if (h < h1)
+    if (h < lim)
       store<kInter>(reinterpret_cast<uint4*>(dst + static_cast<long long>(h) * p.N * D), m.ca, m.cb, v);
   }
 }
 
-// Backward.  Persistent: block k of a tensor's `blocks` walks (8-token group, head part) items
+// Backward.  Persistent: block k of a tensor's `blocks` walks (token group, head part) items
 // k, k + blocks, ...; each lane keeps the weight gradient of its 16 channels in registers and
 // the block's sum goes to its own row of the workspace, which norm_rope_dw_kernel adds in
 // block order.  No atomics: the same sizes give the same bits.
@@ -285,9 +306,10 @@ __global__ void __launch_bounds__(32 * kWarps, 2) norm_rope_bwd_kernel(const Nor
   const int blk = key ? blockIdx.x - p.q_blocks : blockIdx.x;
   const int blocks = key ? gridDim.x - p.q_blocks : p.q_blocks;
   const unsigned parts = key ? p.parts - p.q_parts : p.q_parts;
-  const long long items = (p.tokens + kWarps - 1) / kWarps * parts;
+  const long long items = (p.tokens + (kWarps << t.log_tokens) - 1) / (kWarps << t.log_tokens) * parts;
   const LaneMap<D, kInter> m(lane % L, p.R);
-  const int sub = lane / L;
+  const int heads = RW >> t.log_tokens;  // heads of a trip
+  const int sub = lane / L % heads;
   const bool norm = t.w != nullptr;
 
   // The fetches run ahead over the warp's trips: their item, token and head.
@@ -295,13 +317,18 @@ __global__ void __launch_bounds__(32 * kWarps, 2) norm_rope_bwd_kernel(const Nor
   long long fi = blk;
   const uint16_t *fx = nullptr, *fg = nullptr;
   int fh = 0, fh1 = 0;  // heads fetched next, and the part's end; fh = fh1: the next item
+  bool fthere = false;
   uint32_t fs = 0;
-  auto locate = [&](long long it, unsigned& b, unsigned& n, int& h0, int& h1) {
+  // the lane's token of an item and whether there is one; false: the warp has none
+  auto locate = [&](long long it, bool& there, unsigned& b, unsigned& n, int& h0, int& h1) {
     const unsigned group = static_cast<unsigned>(it / parts), part = static_cast<unsigned>(it - static_cast<long long>(group) * parts);
-    const unsigned long long tok = static_cast<unsigned long long>(group) * kWarps + warp;
-    if (tok >= static_cast<unsigned long long>(p.tokens)) return false;
-    b = static_cast<unsigned>(tok) / static_cast<unsigned>(p.N);
-    n = static_cast<unsigned>(tok) - b * static_cast<unsigned>(p.N);
+    const unsigned long long first = (static_cast<unsigned long long>(group) * kWarps + warp) << t.log_tokens;
+    if (first >= static_cast<unsigned long long>(p.tokens)) return false;
+    const unsigned last = static_cast<unsigned>(p.tokens - 1);
+    there = first + lane / L / heads <= last;
+    const unsigned tok = there ? static_cast<unsigned>(first) + lane / L / heads : last;
+    b = tok / static_cast<unsigned>(p.N);
+    n = tok - b * static_cast<unsigned>(p.N);
     h0 = part * p.heads_per_part;
     h1 = min(h0 + p.heads_per_part, t.H);
     return true;
@@ -309,7 +336,7 @@ __global__ void __launch_bounds__(32 * kWarps, 2) norm_rope_bwd_kernel(const Nor
   auto fetch = [&]() {
     while (fh >= fh1 && fi < items) {  // on to the next item that this warp has a token of
       unsigned b, n;
-      if (locate(fi, b, n, fh, fh1)) {
+      if (locate(fi, fthere, b, n, fh, fh1)) {
         fx = t.x + b * t.sb + n * t.sn;
         fg = t.dy + b * t.dy_sb + n * t.dy_sn;
       }
@@ -317,7 +344,7 @@ __global__ void __launch_bounds__(32 * kWarps, 2) norm_rope_bwd_kernel(const Nor
     }
     if (fh < fh1) {
       const int h = fh + sub;
-      const bool in = h < fh1;
+      const bool in = fthere && h < fh1;
       const uint32_t at = mine + fs * 2048;
       const uint4* g = reinterpret_cast<const uint4*>(fg + min(h, fh1 - 1) * t.dy_sh);
       fetch16(at, g + m.ca, in);
@@ -327,7 +354,7 @@ __global__ void __launch_bounds__(32 * kWarps, 2) norm_rope_bwd_kernel(const Nor
         fetch16(at + 1024, x + m.ca, in);
         fetch16(at + 1536, x + m.cb, in);
       }
-      fh += RW;
+      fh += heads;
       fs = fs + 1 == kBwdStages ? 0 : fs + 1;
     }
     fetch_commit();
@@ -343,12 +370,13 @@ __global__ void __launch_bounds__(32 * kWarps, 2) norm_rope_bwd_kernel(const Nor
   for (long long it = blk; it < items; it += blocks) {
     unsigned b, n;
     int h0, h1;
-    if (!locate(it, b, n, h0, h1)) continue;
+    bool there;
+    if (!locate(it, there, b, n, h0, h1)) continue;
     float2 c[4], s[4];
     const int pos = p.R > 0 ? __ldg(p.positions + b * p.pos_sb + n) : 0;
     lane_angles<kInter>(m, p.phases, pos, p.amplitude, c, s);
     uint16_t* ds = t.y + b * t.y_sb + n * t.y_sn;
-    for (int h = h0 + sub; h - sub < h1; h += RW) {
+    for (int h = h0 + sub; h - sub < h1; h += heads) {
       fetch();
       fetch_wait<kBwdStages - 1>();
       const uint32_t at = mine + us * 2048;
@@ -376,7 +404,7 @@ __global__ void __launch_bounds__(32 * kWarps, 2) norm_rope_bwd_kernel(const Nor
           g.b[i] = mul_rn_f32x2(fma_rn_f32x2(x.b[i], dot, g.b[i]), both(r));
         }
       }
-      if (h < h1) store<kInter>(reinterpret_cast<uint4*>(ds + h * t.y_sh), m.ca, m.cb, g);
+      if (there && h < h1) store<kInter>(reinterpret_cast<uint4*>(ds + h * t.y_sh), m.ca, m.cb, g);
     }
   }
   if (!norm) return;
@@ -393,7 +421,7 @@ __global__ void __launch_bounds__(32 * kWarps, 2) norm_rope_bwd_kernel(const Nor
   }
   __syncthreads();  // the ring is free
   float(*red)[D] = reinterpret_cast<float(*)[D]>(&ring[0][0][0][0]);
-  if (sub == 0) {
+  if (lane < L) {
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
       red[warp][m.channel(e, false)] = va[e];
@@ -447,14 +475,22 @@ void choose_parts(NormRopeArgs& a, int D, int num_sms) {
                                 : ((most + parts - 1) / parts + rows_per_trip - 1) / rows_per_trip * rows_per_trip;
   a.q_parts = (a.q.H + a.heads_per_part - 1) / a.heads_per_part;
   a.parts = a.q_parts + (a.k.H + a.heads_per_part - 1) / a.heads_per_part;
+  for (NormRopeTensor* t : {&a.q, &a.k}) {
+    t->log_tokens = 0;
+    while (t->H > 0 && t->H << (t->log_tokens + 1) <= rows_per_trip) ++t->log_tokens;
+  }
+}
+
+long long token_groups(const NormRopeArgs& a, const NormRopeTensor& t) {
+  return (a.tokens + (kWarps << t.log_tokens) - 1) / (kWarps << t.log_tokens);
 }
 
 template <int D>
 cudaError_t run_fwd(const NormRopeArgs& a, unsigned grid, cudaStream_t s) {
-  if (a.interleaved)
-    norm_rope_kernel<D, true><<<grid, 32 * kWarps, 0, s>>>(a);
-  else
-    norm_rope_kernel<D, false><<<grid, 32 * kWarps, 0, s>>>(a);
+  const bool few = a.q.log_tokens + a.k.log_tokens > 0;
+  auto kernel = a.interleaved ? (few ? norm_rope_kernel<D, true, true> : norm_rope_kernel<D, true, false>)
+                              : (few ? norm_rope_kernel<D, false, true> : norm_rope_kernel<D, false, false>);
+  kernel<<<grid, 32 * kWarps, 0, s>>>(a);
   return cudaGetLastError();
 }
 
@@ -475,8 +511,10 @@ cudaError_t run_bwd(const NormRopeArgs& a, int k_blocks, cudaStream_t s) {
 
 cudaError_t launch_norm_rope(NormRopeArgs a, int D, int num_sms, cudaStream_t s) {
   choose_parts(a, D, num_sms);
-  const long long grid = (a.tokens + kWarps - 1) / kWarps * a.parts;
+  const long long q_blocks = token_groups(a, a.q) * a.q_parts;
+  const long long grid = q_blocks + token_groups(a, a.k) * (a.parts - a.q_parts);
   if (grid > 2147483647LL) return cudaErrorInvalidConfiguration;
+  a.q_blocks = static_cast<int>(q_blocks);
   return D == 64 ? run_fwd<64>(a, static_cast<unsigned>(grid), s)
                  : run_fwd<128>(a, static_cast<unsigned>(grid), s);
 }
@@ -484,16 +522,15 @@ cudaError_t launch_norm_rope(NormRopeArgs a, int D, int num_sms, cudaStream_t s)
 cudaError_t launch_norm_rope_bwd(NormRopeArgs a, int D, int num_sms, cudaStream_t s) {
   choose_parts(a, D, num_sms);
   // the blocks are shared out in proportion to the heads, at least one for a tensor that is there
-  const long long groups = (a.tokens + kWarps - 1) / kWarps;
   const int H = a.q.H + a.k.H;
-  auto share = [&](int heads, int parts) {
-    if (heads == 0) return 0;
-    long long n = static_cast<long long>(kNormRopeBwdBlocks - 1) * heads / H;
-    if (n > groups * parts) n = groups * parts;
+  auto share = [&](const NormRopeTensor& t, int parts) {
+    if (t.H == 0) return 0;
+    long long n = static_cast<long long>(kNormRopeBwdBlocks - 1) * t.H / H;
+    if (n > token_groups(a, t) * parts) n = token_groups(a, t) * parts;
     return static_cast<int>(n < 1 ? 1 : n);
   };
-  a.q_blocks = share(a.q.H, a.q_parts);
-  const int k_blocks = share(a.k.H, a.parts - a.q_parts);
+  a.q_blocks = share(a.q, a.q_parts);
+  const int k_blocks = share(a.k, a.parts - a.q_parts);
   return D == 64 ? run_bwd<64>(a, k_blocks, s) : run_bwd<128>(a, k_blocks, s);
 }
 

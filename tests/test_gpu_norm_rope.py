@@ -207,6 +207,28 @@ def test_backward(layout, B, Hq, Hk, N, D, R, wtype):
         assert torch.equal(a, b)
 
 
+# Few heads: a warp's rows are then of 2, 4 or 8 tokens (D = 64: 8 rows, D = 128: 4), a different number
+# for the queries than for the keys, and the last warp's tokens end among its rows.
+@pytest.mark.parametrize("layout", ["half", "interleaved"])
+@pytest.mark.parametrize("B,Hq,Hk,N,D,R", [
+    (1, 1, 1, 5, 64, 64), (3, 3, 1, 43, 64, 16), (2, 4, 2, 65, 64, 32), (1, 5, 4, 130, 64, 64),
+    (1, 1, 1, 3, 128, 128), (5, 3, 1, 21, 128, 64), (2, 2, 2, 4001, 128, 128), (1, 3, 0, 63, 128, 128),
+])
+def test_few_heads(layout, B, Hq, Hk, N, D, R):
+    q, k, fq, fk, ws, fws, rope, pos, g, fg = _backward_case(B, Hq, Hk, N, D, R, layout, torch.float32)
+    dpos = torch.from_numpy(pos).cuda()
+    out = qat_qk_norm_rope(q, k if Hk else None, dpos, rope, ws[0], ws[1] if Hk else None)
+    if Hk == 0:  # the queries alone, not a pair
+        out = (out, None)
+    dq, dk, dwq, dwk = qat_qk_norm_rope_backward(q, k if Hk else None, dpos, rope, ws[0], ws[1] if Hk else None,
+                                                 g[0], g[1] if Hk else None)
+    for got, x, w, dy, fdy, dx, dw in ((out[0], fq, fws[0], g[0], fg[0], dq, dwq),
+                                       (out[1], fk, fws[1], g[1], fg[1], dk, dwk))[:2 if Hk else 1]:
+        want = so.norm_rope(x, w, pos, rope.frequencies, layout, rope.amplitude)
+        _near(got, want, _forward_slack(x, w, rope.amplitude))
+        _check_grads(x, w, fdy, pos, rope, dx, dw)
+
+
 def test_backward_against_differences():
     """<dy, y> moves with an input as its gradient says, by the kernel's own forward: the step is large
     enough that bf16 roundings of y (2^-9 of each, random) average out over the 2^18 elements."""
