@@ -6,6 +6,7 @@
 // host spends on them is what they cost; in Python it was two to three times as much (a decode call on one
 // sequence 28 us, a training pass of the norm + rotation through autograd 310).
 #include <torch/csrc/autograd/custom_function.h>
+#include <torch/csrc/autograd/variable.h>
 #include <torch/csrc/utils/pybind.h>
 
 #include <ATen/ATen.h>
@@ -17,6 +18,7 @@
 #include <cmath>
 #include <cstdint>
 #include <cstdlib>
+#include <initializer_list>
 #include <optional>
 #include <tuple>
 
@@ -300,6 +302,26 @@ struct NormRope : torch::autograd::Function<NormRope> {
   }
 };
 
+// A leaf keeps one accumulation node as long as any graph that ends in it lives, on the stream that was
+// current when the first of them was made.  If that is the default stream, a backward under capture would
+// have the default stream wait for the capturing one, which ends the capture and may end the process.
+void check_capture(std::initializer_list<const Tensor*> leaves, const at::Device& dev) {
+  const c10::cuda::CUDAStream now = c10::cuda::getCurrentCUDAStream(dev.index());
+  const c10::cuda::CUDAStream none = c10::cuda::getDefaultCUDAStream(dev.index());
+  if (now == none) return;  // the default stream is never captured
+  cudaStreamCaptureStatus status = cudaStreamCaptureStatusNone;
+  if (cudaStreamIsCapturing(now.stream(), &status) != cudaSuccess || status == cudaStreamCaptureStatusNone) return;
+  for (const Tensor* t : leaves) {
+    if (!t->defined() || !t->requires_grad() || !t->is_leaf()) continue;
+    const auto node = torch::autograd::impl::try_get_grad_accumulator(*t);
+    if (node == nullptr) continue;
+    const auto on = node->stream();
+    TORCH_CHECK_VALUE(!on.has_value() || *on != none.unwrap(),
+                      "a graph that ends in one of these leaves was made on the default stream and is still "
+                      "alive: drop its outputs before capturing a backward, or make it on another stream");
+  }
+}
+
 py::object norm_rope(const Tensor& q, const OptTensor& k_, const OptTensor& positions_, const OptTensor& phases_,
                      const OptTensor& wq_, const OptTensor& wk_, int64_t rotary_dim, bool interleaved,
                      double amplitude, double eps) {
@@ -308,6 +330,8 @@ py::object norm_rope(const Tensor& q, const OptTensor& k_, const OptTensor& posi
   const auto needs = [](const Tensor& t) { return t.defined() && t.requires_grad(); };
   variable_list out;
   if (at::GradMode::is_enabled() && (needs(q) || needs(k) || needs(wq) || needs(wk))) {
+    on_cuda(q, "q");
+    check_capture({&q, &k, &wq, &wk}, q.device());
     out = NormRope::apply(q, k_, positions_, phases_, wq_, wk_, rotary_dim, interleaved, amplitude, eps);
   } else {
     const RopeArgs a{static_cast<int>(rotary_dim), interleaved, amplitude, eps};

@@ -334,6 +334,38 @@ def test_captured_forward_and_backward():
         assert torch.equal(a, b)
 
 
+def test_a_capture_beside_a_living_eager_graph_of_the_leaves_is_refused():
+    """The leaves' accumulation nodes belong to the default stream while the eager graph lives; with it
+    gone, or made on another stream, the same capture goes through.  Only the forward is called here where
+    the call has to be refused."""
+    q, k, fq, fk, ws, fws, rope, pos, g, fg = _backward_case(1, 2, 1, 9, 64, 64, "half", torch.float32)
+    dpos = torch.from_numpy(pos).cuda()
+    leaves = [t.contiguous().detach().requires_grad_(True) for t in (q, k, *ws)]
+
+    def forward():
+        return qat_qk_norm_rope(leaves[0], leaves[1], dpos, rope, leaves[2], leaves[3])
+
+    eager = forward()
+    want = torch.autograd.grad(eager, leaves, g, retain_graph=True)
+    torch.cuda.synchronize()
+    with pytest.raises(ValueError, match="default stream"):
+        with torch.cuda.graph(torch.cuda.CUDAGraph()):
+            forward()
+    torch.cuda.synchronize()
+    del eager
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        torch.autograd.grad(forward(), leaves, g)
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = torch.autograd.grad(forward(), leaves, g)
+    graph.replay()
+    for a, b in zip(want, got):
+        assert torch.equal(a, b)
+
+
 def test_sizes_beyond_32_bits_are_refused():
     x = torch.zeros(1, 1, 1, 64, dtype=torch.bfloat16, device="cuda")
     with pytest.raises(ValueError, match="too large"):
