@@ -9,8 +9,15 @@
 // What bounds it: the cache is read once, 2 (D + 4) bytes per key and KV head, and every byte
 // meets at most 16 query rows, so HBM does.  The kernel is built around keeping loads in flight:
 // every warp is its own worker with its own ring of K and V tiles filled by cp.async, no barrier
-// between warps, and all G = Hq / Hkv heads that share a KV head (times T tokens) are rows of one
-// 16-row tile, so that the cache is read once for all of them.
+// between warps, and all G = Hq / Hkv heads that share a KV head (times T tokens) are rows of one item
+// of 8 or 16 rows, so that the cache is read once for all of them (once for each 16 beyond that).
+// Measured, D = 128, 8 KV heads, one token, quantized:
+//   32 query heads, 64 sequences of 129 to 8192 keys    99 us, 5.7 TB/s of codes and scales
+//   40 query heads, 2 sequences of 250001 and 262144   173 us, 6.2 TB/s
+//   32 query heads, one sequence of 1537 keys          9.5 us: two launches and their chains of loads
+// What is left of the first is that the SMs differ by 15 percent in bandwidth: equal ranges end 10 us
+// apart.  (Ranges handed out in pieces end together, but every piece cuts an item, and adding the
+// partials took what that gained.)
 //
 // Work split (stream-K).  The batch's units -- 64-key tiles, ordered by sequence, KV head, row tile,
 // key, and one more at the head of every (sequence, head, row tile) item for what an item costs beside its
@@ -63,7 +70,7 @@ constexpr float kPTop = 16384.f;  // P x value scale / bound is at most this
 constexpr uint32_t kNoPage = 0xffffffffu, kBadPage = 0xfffffffeu;
 
 // NR: column tiles of 8 query rows per item, 1 or 2.  One tile needs half the registers, which
-// makes room for more warps (B64 ragged, D = 128: 104 us with 12, 108 with 16 warps of fewer slots).
+// makes room for more warps (64 ragged sequences, D = 128: 16 warps of 3 slots take 4 percent longer than 12 of 4).
 template <int D, int NR>
 struct Cfg {
   static constexpr int kWarps = NR == 1 ? (D == 128 ? 12 : 16) : 8;
@@ -296,7 +303,7 @@ __global__ void __launch_bounds__(32 * Cfg<D, NR>::kWarps, 1) decode_kernel(cons
   using C = Cfg<D, NR>;
   constexpr int kThreads = 32 * C::kWarps;
   // No static shared memory: it would shift the ring, and cp.async fetches a sector twice when two
-  // 16-byte pieces of it do not go to one 32-byte aligned place (B64 ragged: 122 against 100 us).
+  // 16-byte pieces of it do not go to one 32-byte aligned place (64 ragged sequences: 122 against 100 us).
   extern __shared__ __align__(1024) uint8_t smem[];
   int* warp_sum = reinterpret_cast<int*>(smem + C::kSmem);
   int* prefix = warp_sum + C::kWarps;
