@@ -201,7 +201,7 @@ __device__ __forceinline__ int tiles_of(int len) { return len > 0 ? (len + kTile
 __device__ __forceinline__ void enter_seq(const Params& p, const int* prefix, Cursor& c) {
   if (c.b >= p.a.B) return;  // behind the last: not looked at again
   c.tiles = static_cast<unsigned>(prefix[c.b + 1] - prefix[c.b]) / static_cast<unsigned>(p.a.Hkv * p.mtiles);
-  c.len = min(clamp_len(p.a, __ldg(p.a.seq_lens + c.b)), c.tiles * kTile);
+  c.len = min(clamp_len(p.a, p.a.seq_lens[c.b]), c.tiles * kTile);
 }
 
 // The next tile; u: its unit.
@@ -238,8 +238,8 @@ __device__ __forceinline__ void load_rows(const Params& p, const Cursor& c, int 
           p.a.q + ((static_cast<size_t>(c.b) * p.a.Hkv + c.h) * p.R + r) * D);
 #pragma unroll
       for (int h = 0; h < D / 64; ++h) {
-        raw[2 * h] = __ldg(src + 8 * h + 2 * t);
-        raw[2 * h + 1] = __ldg(src + 8 * h + 2 * t + 1);
+        raw[2 * h] = src[8 * h + 2 * t];
+        raw[2 * h + 1] = src[8 * h + 2 * t + 1];
       }
     }
     float amax = 0.f;
@@ -310,6 +310,7 @@ __global__ void __launch_bounds__(32 * Cfg<D, NR>::kWarps, 1) decode_kernel(cons
   const DecodeArgs& a = p.a;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int g = lane >> 2, t = lane & 3;
+  after_previous();
 
   // prefix[b] = units before sequence b
   const int per_seq = a.Hkv * p.mtiles;
@@ -318,7 +319,7 @@ __global__ void __launch_bounds__(32 * Cfg<D, NR>::kWarps, 1) decode_kernel(cons
     const int b0 = min(tid * chunk, a.B), b1 = min(b0 + chunk, a.B);
     int sum = 0;
     for (int b = b0; b < b1; ++b) {
-      const int len = __ldg(a.seq_lens + b);
+      const int len = a.seq_lens[b];
       const int ok = clamp_len(a, len);
       if (len > ok) atomicOr(a.err, kErrBadPage);
       prefix[b] = tiles_of(ok) * per_seq;
@@ -347,8 +348,6 @@ __global__ void __launch_bounds__(32 * Cfg<D, NR>::kWarps, 1) decode_kernel(cons
   const int per_cta = min(C::kWarps, (tiles + static_cast<int>(gridDim.x) - 1) / static_cast<int>(gridDim.x));
   const int workers = min(tiles, per_cta * static_cast<int>(gridDim.x));
   if (blockIdx.x == 0 && tid == 0) header_of(p)->workers = workers;
-  // the merge kernel's blocks may be brought up; they wait for this grid's end
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if (warp >= per_cta) return;
   const int id = blockIdx.x * per_cta + warp;
   if (id >= workers) return;
@@ -395,7 +394,7 @@ __global__ void __launch_bounds__(32 * Cfg<D, NR>::kWarps, 1) decode_kernel(cons
         const int pos = ((pc.tile & ~7) * 4 + lane) * kChunk;
         rows_of = kNoPage;
         if (pos < pc.len) {
-          const int page = __ldg(a.table + static_cast<long long>(pc.b) * a.max_pages + (pos >> a.page_shift));
+          const int page = a.table[static_cast<long long>(pc.b) * a.max_pages + (pos >> a.page_shift)];
           rows_of = kBadPage;
           if (page >= 0 && page < a.num_pages)
             rows_of = ((static_cast<uint32_t>(page) * a.Hkv + pc.h) << a.page_shift) +
@@ -827,7 +826,7 @@ __global__ void __launch_bounds__(kFew ? 1024 : 256) decode_merge_kernel(const P
   __shared__ WorkerMeta found;
   const int r = blockIdx.y, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (kFew && threadIdx.x == 0) found = WorkerMeta{-1, -1};
-  asm volatile("griddepcontrol.wait;" ::: "memory");  // the partials are complete
+  after_previous();  // the partials are complete
   const int workers = __ldcg(&header_of(p)->workers);
   // lane k: the chain of the block's k-th worker's item, if its range cuts one
   int w = 0, n = 0, item = 0;
@@ -908,24 +907,15 @@ cudaError_t run(const Params& p, int ctas, long long units, cudaStream_t s) {
                                        cudaFuncAttributeMaxDynamicSharedMemorySize,
                                        static_cast<int>(smem));
   if (e != cudaSuccess) return e;
-  decode_kernel<D, NR, kQuant><<<ctas, 32 * C::kWarps, smem, s>>>(p);
-  e = cudaGetLastError();
+  e = launch_early(decode_kernel<D, NR, kQuant>, ctas, 32 * C::kWarps, smem, s, p);
   if (e != cudaSuccess) return e;
-  cudaLaunchConfig_t cfg = {};
   const int most = static_cast<int>(units < ctas * C::kWarps ? units : ctas * C::kWarps);
   const long long items = static_cast<long long>(p.a.B) * p.a.Hkv * p.mtiles;
   const bool few = items * 32 <= most;
-  cfg.gridDim = dim3(few ? static_cast<unsigned>(items) : (most + kMergeSpan - 1) / kMergeSpan,
-                     p.R < p.rows ? p.R : p.rows);
-  cfg.blockDim = dim3(few ? 1024 : 256);
-  cfg.stream = s;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = at;
-  cfg.numAttrs = 1;
-  return few ? cudaLaunchKernelEx(&cfg, decode_merge_kernel<D, true>, p)
-             : cudaLaunchKernelEx(&cfg, decode_merge_kernel<D, false>, p);
+  const dim3 grid(few ? static_cast<unsigned>(items) : (most + kMergeSpan - 1) / kMergeSpan,
+                  p.R < p.rows ? p.R : p.rows);
+  return few ? launch_early(decode_merge_kernel<D, true>, grid, 1024, 0, s, p)
+             : launch_early(decode_merge_kernel<D, false>, grid, 256, 0, s, p);
 }
 
 }  // namespace

@@ -35,7 +35,7 @@ constexpr float kTinyRow = 7.703719777548943e-34f;  // 2^-110
 // The page of a position and its place in it; false when the table's entry lies outside the
 // cache (reported in the device error word).
 __device__ __forceinline__ bool find_slot(const KvCacheArgs& p, int b, int pos, int& page, int& slot) {
-  page = __ldg(p.table + static_cast<long long>(b) * p.max_pages + (pos >> p.page_shift));
+  page = p.table[static_cast<long long>(b) * p.max_pages + (pos >> p.page_shift)];
   slot = pos & ((1 << p.page_shift) - 1);
   if (page >= 0 && page < p.num_pages) return true;
   atomicOr(p.err, kErrBadPage);
@@ -44,7 +44,7 @@ __device__ __forceinline__ bool find_slot(const KvCacheArgs& p, int b, int pos, 
 
 // A sequence's length as the table can hold it.
 __device__ __forceinline__ int seq_len(const KvCacheArgs& p, int b) {
-  const int len = __ldg(p.seq_lens + b);
+  const int len = p.seq_lens[b];
   const long long cap = static_cast<long long>(p.max_pages) << p.page_shift;
   if (len <= cap) return max(len, 0);
   atomicOr(p.err, kErrBadPage);
@@ -96,6 +96,7 @@ __global__ void __launch_bounds__(kThreads, 8) kv_append_kernel(const KvCacheArg
   constexpr int L = D / 16;
   const int j = threadIdx.x % L;
   const unsigned row = blockIdx.x * (kThreads / L) + threadIdx.x / L;
+  after_previous();
   bool in = row < static_cast<unsigned long long>(p.B) * p.H * p.N;
   const unsigned bh = p.by_n(row);
   const int n = static_cast<int>(row - bh * p.N), b = static_cast<int>(p.by_h(bh));
@@ -104,17 +105,17 @@ __global__ void __launch_bounds__(kThreads, 8) kv_append_kernel(const KvCacheArg
   rk[0] = rk[1] = rv[0] = rv[1] = make_uint4(0u, 0u, 0u, 0u);
   size_t at = 0;
   if (in) {
-    const int count = p.new_lens != nullptr ? min(__ldg(p.new_lens + b), p.N) : p.N;
+    const int count = p.new_lens != nullptr ? min(p.new_lens[b], p.N) : p.N;
     in = n < count;
     if (in) {
       const uint4* k = reinterpret_cast<const uint4*>(p.k + b * p.k_sb + h * p.k_sh + n * p.k_sn);
       const uint4* v = reinterpret_cast<const uint4*>(p.v + b * p.v_sb + h * p.v_sh + n * p.v_sn);
-      rk[0] = __ldg(k + j);
-      rk[1] = __ldg(k + L + j);
-      rv[0] = __ldg(v + j);
-      rv[1] = __ldg(v + L + j);
+      rk[0] = k[j];
+      rk[1] = k[L + j];
+      rv[0] = v[j];
+      rv[1] = v[L + j];
       // the count's tokens are the sequence's last
-      const int len = __ldg(p.seq_lens + b);
+      const int len = p.seq_lens[b];
       const long long pos = static_cast<long long>(len) - count + n;
       const long long cap = static_cast<long long>(p.max_pages) << p.page_shift;
       if (pos < 0 || pos >= cap) {
@@ -163,6 +164,7 @@ __global__ void __launch_bounds__(kThreads) kv_read_kernel(const KvCacheArgs p) 
   constexpr int L = D / 16;
   const int j = threadIdx.x % L;
   const unsigned row = blockIdx.x * (kThreads / L) + threadIdx.x / L;
+  after_previous();
   if (row >= static_cast<unsigned long long>(p.B) * p.H * p.N) return;
   const unsigned bh = p.by_n(row);
   const int n = static_cast<int>(row - bh * p.N), b = static_cast<int>(p.by_h(bh));
@@ -177,12 +179,12 @@ __global__ void __launch_bounds__(kThreads) kv_read_kernel(const KvCacheArgs p) 
       const size_t at = ((static_cast<size_t>(page) * p.H + h) << p.page_shift) + slot;
       const uint2* k = reinterpret_cast<const uint2*>(p.k_codes + at * D) + j;
       const uint2* v = reinterpret_cast<const uint2*>(p.v_codes + at * D) + j;
-      ck[0] = __ldg(k);
-      ck[1] = __ldg(k + L);
-      cv[0] = __ldg(v);
-      cv[1] = __ldg(v + L);
-      sk = __ldg(p.k_scales + at);
-      sv = __ldg(p.v_scales + at);
+      ck[0] = k[0];
+      ck[1] = k[L];
+      cv[0] = v[0];
+      cv[1] = v[L];
+      sk = p.k_scales[at];
+      sv = p.v_scales[at];
     } else {
       sk = sv = __int_as_float(0x7fc00000);  // no page: the row reads as NaN
     }
@@ -203,19 +205,11 @@ inline unsigned blocks_of(const KvCacheArgs& a, int D) {
 }  // namespace
 
 cudaError_t launch_kv_append(const KvCacheArgs& a, int D, cudaStream_t s) {
-  if (D == 64)
-    kv_append_kernel<64><<<blocks_of(a, D), kThreads, 0, s>>>(a);
-  else
-    kv_append_kernel<128><<<blocks_of(a, D), kThreads, 0, s>>>(a);
-  return cudaGetLastError();
+  return launch_early(D == 64 ? kv_append_kernel<64> : kv_append_kernel<128>, blocks_of(a, D), kThreads, 0, s, a);
 }
 
 cudaError_t launch_kv_read(const KvCacheArgs& a, int D, cudaStream_t s) {
-  if (D == 64)
-    kv_read_kernel<64><<<blocks_of(a, D), kThreads, 0, s>>>(a);
-  else
-    kv_read_kernel<128><<<blocks_of(a, D), kThreads, 0, s>>>(a);
-  return cudaGetLastError();
+  return launch_early(D == 64 ? kv_read_kernel<64> : kv_read_kernel<128>, blocks_of(a, D), kThreads, 0, s, a);
 }
 
 }  // namespace qat

@@ -242,6 +242,33 @@ constexpr int kDecodeMaxBatch = 4096;  // the kernel keeps the batch's prefix su
 constexpr int kDecodeMaxTokens = 16;
 size_t decode_workspace_bytes(int R, int D);  // R = Hq / Hkv * T
 
+#ifdef __CUDACC__
+// Launches a kernel that may be brought up while the stream's previous kernel still runs: it begins with
+// after_previous(), which waits for that kernel's end and memory, and lets the next one be brought up in
+// turn.  In a serving step's chain of kernels of a few microseconds that hides a launch each.
+// Such a kernel reads its inputs by plain or L2 loads: the read-only path may only be used for what does not
+// change between the kernel's start, which is before the wait, and its end.
+template <class... Par, class... Arg>
+cudaError_t launch_early(void (*kernel)(Par...), dim3 grid, dim3 block, size_t smem, cudaStream_t s,
+                         const Arg&... arg) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = block;
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, arg...);
+}
+__device__ __forceinline__ void after_previous() {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+#endif
+
 // Kernel launchers (return cudaGetLastError() after the launches).
 cudaError_t launch_norm_rope(NormRopeArgs a, int D, int num_sms, cudaStream_t s);
 cudaError_t launch_norm_rope_bwd(NormRopeArgs a, int D, int num_sms, cudaStream_t s);

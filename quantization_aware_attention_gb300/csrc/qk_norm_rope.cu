@@ -137,7 +137,7 @@ __device__ __forceinline__ void lane_angles(const Map& m, const unsigned long lo
     if (e < 4 ? m.rot_a : m.rot_b) {
       const unsigned long long turn =
           static_cast<unsigned long long>(static_cast<long long>(pos)) *
-          __ldg(phases + (e < 4 ? m.pair_a + e : m.pair_b + e - 4));
+          phases[e < 4 ? m.pair_a + e : m.pair_b + e - 4];
       const float ang = static_cast<float>(static_cast<int>(turn >> 32)) * kTurnToRad;
       __sincosf(ang, &sn[e], &cs[e]);
     }
@@ -189,8 +189,8 @@ __device__ __forceinline__ void load_weight(const Map& m, const void* w, int bf1
 #pragma unroll
   for (int e = 0; e < 8; ++e) {
     const int i = m.channel(e, false), j = m.channel(e, true);
-    a[e] = bf16 ? __bfloat162float(__ldg(static_cast<const __nv_bfloat16*>(w) + i)) : __ldg(static_cast<const float*>(w) + i);
-    b[e] = bf16 ? __bfloat162float(__ldg(static_cast<const __nv_bfloat16*>(w) + j)) : __ldg(static_cast<const float*>(w) + j);
+    a[e] = bf16 ? __bfloat162float(static_cast<const __nv_bfloat16*>(w)[i]) : static_cast<const float*>(w)[i];
+    b[e] = bf16 ? __bfloat162float(static_cast<const __nv_bfloat16*>(w)[j]) : static_cast<const float*>(w)[j];
   }
 }
 
@@ -221,6 +221,7 @@ __global__ void __launch_bounds__(32 * kWarps, 4) norm_rope_kernel(const NormRop
   constexpr int RW = 32 / L;     // rows per warp and trip
   __shared__ uint4 ring[kWarps][kFwdStages][2][32];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  after_previous();
   bool key;
   unsigned group, part;  // of the tokens; of the tensor's heads, heads_per_part each
   if constexpr (kFew) {  // blocks [0, q_blocks) are the queries', the rest the keys'
@@ -271,7 +272,7 @@ __global__ void __launch_bounds__(32 * kWarps, 4) norm_rope_kernel(const NormRop
   Chan w;
   if (t.w != nullptr) load_weight<kInter>(m, t.w, p.w_bf16, w);
   float2 c[4], s[4];
-  const int pos = p.R > 0 ? __ldg(p.positions + b * p.pos_sb + n) : 0;
+  const int pos = p.R > 0 ? p.positions[b * p.pos_sb + n] : 0;
   lane_angles<kInter>(m, p.phases, pos, p.amplitude, c, s);
 
   uint16_t* dst = t.y + (static_cast<long long>(b) * t.H * p.N + n) * D;
@@ -316,8 +317,7 @@ __global__ void __launch_bounds__(32 * kWarps, 2) norm_rope_bwd_kernel(const Nor
   const int heads = RW >> t.log_tokens;  // heads of a trip
   const int sub = lane / L % heads;
   const bool norm = t.w != nullptr;
-  // the weights' kernel may be brought up; it waits for this grid's end
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  after_previous();
 
   // The fetches run ahead over the warp's trips: their item, token and head.
   const uint32_t mine = sm100::smem_addr(&ring[warp][0][0][lane]);
@@ -380,7 +380,7 @@ __global__ void __launch_bounds__(32 * kWarps, 2) norm_rope_bwd_kernel(const Nor
     bool there;
     if (!locate(it, there, b, n, h0, h1)) continue;
     float2 c[4], s[4];
-    const int pos = p.R > 0 ? __ldg(p.positions + b * p.pos_sb + n) : 0;
+    const int pos = p.R > 0 ? p.positions[b * p.pos_sb + n] : 0;
     lane_angles<kInter>(m, p.phases, pos, p.amplitude, c, s);
     uint16_t* ds = t.y + b * t.y_sb + n * t.y_sn;
     for (int h = h0 + sub; h - sub < h1; h += heads) {
@@ -453,7 +453,7 @@ __global__ void __launch_bounds__(1024) norm_rope_dw_kernel(const NormRopeArgs p
   void* out = key ? p.k.dw : p.q.dw;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, d = blockIdx.x * 32 + lane;
   const float* src = p.part + (key ? static_cast<size_t>(p.q_blocks) * D : 0) + d;
-  asm volatile("griddepcontrol.wait;" ::: "memory");  // the blocks' sums are complete
+  after_previous();  // the blocks' sums are complete
   float sum = 0.f;
 #pragma unroll 8
   for (int i = warp; i < blocks; i += 32) sum += __ldcg(src + static_cast<size_t>(i) * D);
@@ -498,29 +498,16 @@ cudaError_t run_fwd(const NormRopeArgs& a, unsigned grid, cudaStream_t s) {
   const bool few = a.q.log_tokens + a.k.log_tokens > 0;
   auto kernel = a.interleaved ? (few ? norm_rope_kernel<D, true, true> : norm_rope_kernel<D, true, false>)
                               : (few ? norm_rope_kernel<D, false, true> : norm_rope_kernel<D, false, false>);
-  kernel<<<grid, 32 * kWarps, 0, s>>>(a);
-  return cudaGetLastError();
+  return launch_early(kernel, grid, 32 * kWarps, 0, s, a);
 }
 
 template <int D>
 cudaError_t run_bwd(const NormRopeArgs& a, int k_blocks, cudaStream_t s) {
   const unsigned grid = static_cast<unsigned>(a.q_blocks + k_blocks);
-  if (a.interleaved)
-    norm_rope_bwd_kernel<D, true><<<grid, 32 * kWarps, 0, s>>>(a);
-  else
-    norm_rope_bwd_kernel<D, false><<<grid, 32 * kWarps, 0, s>>>(a);
-  cudaError_t e = cudaGetLastError();
+  const cudaError_t e = launch_early(a.interleaved ? norm_rope_bwd_kernel<D, true> : norm_rope_bwd_kernel<D, false>,
+                                     grid, 32 * kWarps, 0, s, a);
   if (e != cudaSuccess || (a.q.w == nullptr && a.k.w == nullptr)) return e;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(D / 32, 2);
-  cfg.blockDim = dim3(1024);
-  cfg.stream = s;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = at;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, norm_rope_dw_kernel, a, k_blocks, D);
+  return launch_early(norm_rope_dw_kernel, dim3(D / 32, 2), 1024, 0, s, a, k_blocks, D);
 }
 
 }  // namespace

@@ -10,7 +10,8 @@ from oracle import qat_oracle as orc
 from oracle import serving_oracle as so
 from quantization_aware_attention_gb300 import (QUANT_NONE, KVCache, RopePlan, attention,
                                                 check_device_status, qat_attention_decode,
-                                                qat_attention_forward, qat_qk_norm_rope)
+                                                qat_attention_forward, qat_qk_norm_rope,
+                                                qat_qk_norm_rope_backward)
 from quantization_aware_attention_gb300 import build as qbuild
 from quantization_aware_attention_gb300 import capi
 from quantization_aware_attention_gb300.inputs import normal_bf16
@@ -225,3 +226,59 @@ def test_calls_without_a_backward_say_so():
     with torch.no_grad():
         assert s.step(x, _i32([[0]] * B), _i32([1] * B)).shape == (B, HQ, 1, D)
     assert capi.qat_attn_device_status() == capi.Status.OK
+
+
+@pytest.mark.parametrize("captured", [False, True])
+def test_a_chain_of_calls_in_flight(captured):
+    """Forty steps of one stream, each call's inputs the ones before it have just written -- lengths and
+    positions included -- and the scratch memory used again by the next: queued without a pause, they give
+    the bits that they give one at a time."""
+    def steps(s, x, lens, wait):
+        pos = torch.empty(B, 1, dtype=torch.int32, device="cuda")
+        outs = []
+        for _ in range(40):
+            torch.add(lens, 0, out=pos[:, 0])
+            lens.add_(1)
+            o = s.step(x, pos, lens)
+            kr, vr = s.cache.read(s.table, lens, length=64)
+            x = torch.cat([o.transpose(1, 2), kr[:, :, 5:6].transpose(1, 2), vr[:, :, 5:6].transpose(1, 2)], 2)
+            g = qat_qk_norm_rope_backward(x[:, :, :HQ].transpose(1, 2), None, pos, s.rope, s.wq, None, o, None)
+            x = torch.cat([g[0].transpose(1, 2), x[:, :, HQ:]], 2)
+            s.wq.copy_(1 + g[2].tanh() / 4)
+            outs += [o, kr, vr, *[t for t in g if t is not None]]
+            if wait:
+                torch.cuda.synchronize()
+        return outs
+
+    runs = []
+    for wait in (True, False):
+        s = Server()
+        for t in (s.cache.k, s.cache.v):
+            t.view(torch.uint8).zero_()
+        for t in (s.cache.k_scale, s.cache.v_scale):
+            t.zero_()
+        x, lens = _x(1, 500), _i32([0, 11, 3])
+        if captured and not wait:
+            first = (s.wq.clone(), lens.clone())
+            side = torch.cuda.Stream()
+            side.wait_stream(torch.cuda.current_stream())
+            with torch.cuda.stream(side):
+                steps(s, x, lens.clone(), False)
+            torch.cuda.current_stream().wait_stream(side)
+            graph = torch.cuda.CUDAGraph()
+            with torch.cuda.graph(graph):
+                outs = steps(s, x, lens, False)
+            for t in (s.cache.k, s.cache.v):
+                t.view(torch.uint8).zero_()
+            for t in (s.cache.k_scale, s.cache.v_scale):
+                t.zero_()
+            s.wq.copy_(first[0])
+            lens.copy_(first[1])
+            graph.replay()
+        else:
+            outs = steps(s, x, lens, wait)
+        torch.cuda.synchronize()
+        runs.append([t.clone() for t in outs])
+    for i, (a, b) in enumerate(zip(*runs)):
+        assert torch.equal(a.view(torch.uint8), b.view(torch.uint8)), i
+    check_device_status()
