@@ -80,29 +80,32 @@ struct Cfg {
   static constexpr int kSmem = kWarps * kRing;  // then the warps' sums and B + 1 prefix sums
 };
 
-// Workspace: the header, what each worker's range cut, then the partials: two per worker, [0] of the
-// item its range ends or passes through ("head"), [1] of the item it begins and does not end ("tail"),
-// each rows x D sums and rows x (m, l).
+// Workspace: the header, the chains, then the partials: two per worker, [0] of the item its range ends or
+// passes through ("head"), [1] of the item it begins and does not end ("tail"), each rows x D sums and
+// rows x (m, l).  An item that ranges cut leaves a chain of partials: the tail of the worker in whose range
+// it begins, then the heads of the following workers.  Chains are listed by item where there are at most as
+// many items as workers (Params::by_item), else by the worker they begin with.
 struct Header {
   int workers;
   int pad[31];
 };
-struct WorkerMeta {
-  int tail;  // item that begins in this range and ends in a later one, or -1
-  int last;  // the worker in whose range it ends
+struct Chain {
+  int key;   // by item: the first worker; by worker: the item; -1: none
+  int last;  // the worker in whose range the item ends
 };
-constexpr size_t kPartsAt = sizeof(Header) + kWorkers * sizeof(WorkerMeta);
+constexpr size_t kPartsAt = sizeof(Header) + kWorkers * sizeof(Chain);
 static_assert(kPartsAt % 16 == 0, "partials are read 16 bytes at a time");
 
 struct Params {
   DecodeArgs a;
   int R, rows, mtiles;  // rows of a KV head (Hq / Hkv heads x T tokens), of an item; items of a head
   int prows;            // rows of a partial
+  int by_item;
 };
 
 __device__ __forceinline__ Header* header_of(const Params& p) { return static_cast<Header*>(p.a.ws); }
-__device__ __forceinline__ WorkerMeta* meta_of(const Params& p) {
-  return reinterpret_cast<WorkerMeta*>(static_cast<char*>(p.a.ws) + sizeof(Header));
+__device__ __forceinline__ Chain* chains_of(const Params& p) {
+  return reinterpret_cast<Chain*>(static_cast<char*>(p.a.ws) + sizeof(Header));
 }
 template <int D>
 __device__ __forceinline__ float* partial_of(const Params& p, int worker, int which) {
@@ -344,8 +347,10 @@ __global__ void __launch_bounds__(32 * Cfg<D, NR>::kWarps, 1) decode_kernel(cons
     __syncthreads();
   }
   const int tiles = prefix[a.B];
-  // workers: as few warps per CTA as give every worker a tile, spread over the CTAs
-  const int per_cta = min(C::kWarps, (tiles + static_cast<int>(gridDim.x) - 1) / static_cast<int>(gridDim.x));
+  // workers: as few warps of every CTA as keep the most tiles that one has
+  const int ctas = static_cast<int>(gridDim.x);
+  const int deep = (tiles + ctas * C::kWarps - 1) / (ctas * C::kWarps);
+  const int per_cta = (tiles + ctas * deep - 1) / (ctas * deep);
   const int workers = min(tiles, per_cta * static_cast<int>(gridDim.x));
   if (blockIdx.x == 0 && tid == 0) header_of(p)->workers = workers;
   if (warp >= per_cta) return;
@@ -480,7 +485,7 @@ __global__ void __launch_bounds__(32 * Cfg<D, NR>::kWarps, 1) decode_kernel(cons
   int last[NR][2];              // the newest key each of those rows sees
   float vref = 0.f;
   bool begun = false;
-  if (lane == 0) meta_of(p)[id] = WorkerMeta{-1, -1};
+  if (lane == 0 && !p.by_item) chains_of(p)[id] = Chain{-1, -1};
   int first_tile = cc.tile;    // of the current segment
 
   for (int u = u0; u < u1;) {
@@ -680,9 +685,14 @@ __global__ void __launch_bounds__(32 * Cfg<D, NR>::kWarps, 1) decode_kernel(cons
       begun = false;
       const bool head = first_tile != 0;
       const bool whole = !head && ends;
-      if (!whole && !head && lane == 0) {
+      if (!head && lane == 0) {
         const long long end = u - cc.tile + cc.tiles;  // the unit behind the item
-        meta_of(p)[id] = WorkerMeta{item_of(p, cc), static_cast<int>((end * workers - 1) / W)};
+        const int item = item_of(p, cc);
+        if (whole) {
+          if (p.by_item) chains_of(p)[item] = Chain{-1, -1};
+        } else {
+          chains_of(p)[p.by_item ? item : id] = Chain{p.by_item ? id : item, static_cast<int>((end * workers - 1) / W)};
+        }
       }
       const float scale = vref * (1.f / kPTop);
 #pragma unroll
@@ -738,14 +748,24 @@ struct Sum {
 #pragma unroll
     for (int i = 0; i < V; ++i) acc[i] = 0.f;
   }
-  __device__ __forceinline__ void add(float m2, float l2, const float (&o2)[V]) {
-    const float mn = fmaxf(m, m2);
-    const float ref = mn == -INFINITY ? 0.f : mn;
-    const float f = ex2(m - ref), f2 = ex2(m2 - ref);
-    m = mn;
-    l = l * f + l2 * f2;
+  template <int N>
+  __device__ __forceinline__ void add(const float2 (&ml)[N], const float (&x)[N][V]) {
+    float top = m;
 #pragma unroll
-    for (int i = 0; i < V; ++i) acc[i] = acc[i] * f + o2[i] * f2;
+    for (int k = 0; k < N; ++k) top = fmaxf(top, ml[k].x);
+    const float ref = top == -INFINITY ? 0.f : top;
+    const float f = ex2(m - ref);
+    m = top;
+    l *= f;
+#pragma unroll
+    for (int i = 0; i < V; ++i) acc[i] *= f;
+#pragma unroll
+    for (int k = 0; k < N; ++k) {
+      const float fk = ex2(ml[k].x - ref);
+      l = fmaf(ml[k].y, fk, l);
+#pragma unroll
+      for (int i = 0; i < V; ++i) acc[i] = fmaf(x[k][i], fk, acc[i]);
+    }
   }
 };
 
@@ -769,22 +789,28 @@ __device__ __forceinline__ void load_partial(const Params& p, int w, int which, 
   load_v<D / 32>(x, part + r * D + D / 32 * lane);
 }
 
-// Adds partials first, first + step, ... up to n of the chain that begins with worker w's tail, four
-// loads ahead.
-template <int D>
+// Adds partials first, first + step, ... up to n of the chain that begins with worker w's tail, kAhead
+// loads in flight: none is conditional (behind the end the last one is loaded again and counts as nothing),
+// or each would be waited for before the next.
+template <int D, int kAhead>
 __device__ __forceinline__ void add_chain(const Params& p, int w, int first, int step, int n, int r,
                                           int lane, Sum<D / 32>& sum) {
-  for (int i = first; i < n; i += 4 * step) {
-    float x[4][D / 32];
-    float2 ml[4];
+  for (int i = first; i < n; i += kAhead * step) {
+    float x[kAhead][D / 32];
+    float2 ml[kAhead];
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const int c = i + k * step;
-      if (c < n) load_partial<D>(p, w + c, c == 0 ? 1 : 0, r, lane, ml[k], x[k]);
+    for (int k = 0; k < kAhead; ++k) {
+      const int c = min(i + k * step, n - 1);
+      load_partial<D>(p, w + c, c == 0 ? 1 : 0, r, lane, ml[k], x[k]);
     }
 #pragma unroll
-    for (int k = 0; k < 4; ++k)
-      if (i + k * step < n) sum.add(ml[k].x, ml[k].y, x[k]);
+    for (int k = 1; k < kAhead; ++k) {
+      if (i + k * step < n) continue;
+      ml[k] = make_float2(-INFINITY, 0.f);
+#pragma unroll
+      for (int j = 0; j < D / 32; ++j) x[k][j] = 0.f;
+    }
+    sum.add(ml, x);
   }
 }
 
@@ -810,112 +836,170 @@ __device__ __forceinline__ void store_row(const Params& p, int item, int r, int 
   if (lane == 0 && p.a.lse != nullptr) p.a.lse[row] = none ? -INFINITY : s.m + log2f(s.l);
 }
 
-// Adds the partials of the items that ranges cut.  Block (x, r) takes row r
-//   kFew = false: of the items that ranges of workers 8 x .. 8 x + 7 begin and do not end, 8 warps: one
-//     each, or all together where an item's chain of partials is long;
-//   kFew = true: of item x, 32 warps, where the items are so few that every chain is long (one sequence
-//     of 131072 keys, one KV head, 8 query heads: 50 us in all without, 28 with it).
-constexpr int kMergeSpan = 8;
+// A value into the same shared memory variable of the cluster's first block.
+__device__ __forceinline__ void store_first(float* dst, float x) {
+  uint32_t at;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(at) : "r"(sm100::smem_addr(dst)));
+  asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(at), "f"(x) : "memory");
+}
 
-template <int D, bool kFew>
-__global__ void __launch_bounds__(kFew ? 1024 : 256) decode_merge_kernel(const Params p) {
+// The kN sums in acc and ml as one: lane x weighs the x-th, then every lane adds its channels of all.
+template <int D, int kN>
+__device__ __forceinline__ void add_all(const float (*acc)[D], const float (*ml)[2], int lane, Sum<D / 32>& sum) {
   constexpr int V = D / 32;
-  constexpr int W = kFew ? 32 : 8;
-  constexpr int kShort = 16;
-  __shared__ float acc[W][D], ml[W][2];
-  __shared__ WorkerMeta found;
-  const int r = blockIdx.y, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  if (kFew && threadIdx.x == 0) found = WorkerMeta{-1, -1};
-  after_previous();  // the partials are complete
-  const int workers = __ldcg(&header_of(p)->workers);
-  // lane k: the chain of the block's k-th worker's item, if its range cuts one
-  int w = 0, n = 0, item = 0;
-  if constexpr (kFew) {
-    __syncthreads();
-    for (int i = threadIdx.x; i < workers; i += 1024) {
-      const int2 raw = __ldcg(reinterpret_cast<const int2*>(meta_of(p) + i));
-      if (raw.x == static_cast<int>(blockIdx.x)) found = WorkerMeta{i, raw.y};  // one of them at most
-    }
-    __syncthreads();
-    item = blockIdx.x;
-    w = found.tail;
-    if (lane == 0 && w >= 0 && item % p.mtiles * p.rows + r < p.R) n = found.last - w + 1;
-  } else {
-    const int w0 = blockIdx.x * kMergeSpan;
-    int2 raw = make_int2(-1, -1);  // means nothing beyond the count
-    if (lane < kMergeSpan) raw = __ldcg(reinterpret_cast<const int2*>(meta_of(p) + w0 + lane));
-    if (w0 >= workers) return;
-    item = raw.x;
-    w = w0 + lane;
-    if (lane < kMergeSpan && w < workers && item >= 0 && item % p.mtiles * p.rows + r < p.R)
-      n = raw.y - w + 1;
-    const int len = __shfl_sync(0xffffffffu, n, warp), it = __shfl_sync(0xffffffffu, item, warp);
-    if (len > 0 && len <= kShort) {
-      Sum<V> sum;
-      sum.clear();
-      add_chain<D>(p, w0 + warp, 0, 1, len, r, lane, sum);
-      store_row<D>(p, it, r, lane, sum);
-    }
+  const float m = lane < kN ? ml[lane][0] : -INFINITY;
+  float top = m;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+  const float f = lane < kN ? ex2(m - (top == -INFINITY ? 0.f : top)) : 0.f;
+  float l = lane < kN ? ml[lane][1] * f : 0.f;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+  sum.m = top;
+  sum.l = l;
+#pragma unroll
+  for (int i = 0; i < V; ++i) sum.acc[i] = 0.f;
+#pragma unroll
+  for (int y = 0; y < kN; ++y) {
+    const float fy = __shfl_sync(0xffffffffu, f, y);
+#pragma unroll
+    for (int i = 0; i < V; ++i) sum.acc[i] = fmaf(acc[y][V * lane + i], fy, sum.acc[i]);
   }
-  unsigned rest = __ballot_sync(0xffffffffu, n > (kFew ? 0 : kShort));  // the same in every warp
+}
+
+// Adds up row r = blockIdx.y of 8 chains, a warp for each; all 8 warps for one after the other where few of
+// the block's are long.
+constexpr int kEachWarps = 8, kEachAhead = 8;
+constexpr int kMergeCtas = 8;  // blocks of a cluster at most
+
+// Row r of the chain at place x of the list: its first worker, length (0: none) and item.
+__device__ __forceinline__ void find_chain(const Params& p, int x, int r, int& w, int& n, int& item) {
+  const int workers = __ldcg(&header_of(p)->workers);
+  w = n = item = 0;
+  if (x >= (p.by_item ? p.a.B * p.a.Hkv * p.mtiles : kWorkers)) return;
+  const int2 raw = __ldcg(reinterpret_cast<const int2*>(chains_of(p) + x));
+  item = p.by_item ? x : raw.x;
+  w = p.by_item ? raw.x : x;
+  if (raw.x >= 0 && (p.by_item || x < workers) && item % p.mtiles * p.rows + r < p.R) n = raw.y - w + 1;
+}
+
+// A chain's partials by all the block's warps, into sum of warp 0.
+template <int D, int kWarps, int kAhead>
+__device__ __forceinline__ void add_by_block(const Params& p, int w, int first, int step, int n, int r, int warp,
+                                             int lane, float (*acc)[D], float (*ml)[2], Sum<D / 32>& sum) {
+  sum.clear();
+  add_chain<D, kAhead>(p, w, first, step, n, r, lane, sum);
+#pragma unroll
+  for (int i = 0; i < D / 32; ++i) acc[warp][D / 32 * lane + i] = sum.acc[i];
+  if (lane == 0) {
+    ml[warp][0] = sum.m;
+    ml[warp][1] = sum.l;
+  }
+  __syncthreads();
+  if (warp == 0) add_all<D, kWarps>(acc, ml, lane, sum);
+}
+
+template <int D>
+__global__ void __launch_bounds__(32 * kEachWarps) merge_each_kernel(const Params p) {
+  __shared__ float acc[kEachWarps][D], ml[kEachWarps][2];
+  const int r = blockIdx.y, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  after_previous();  // the partials are complete
+  int w, n, item;    // lane k: the block's k-th chain
+  find_chain(p, blockIdx.x * kEachWarps + min(lane, kEachWarps - 1), r, w, n, item);
+  if (lane >= kEachWarps) n = 0;
+  // A round of loads takes 1 us, and a chain that all warps share 2 us: a warp takes up to two rounds, and
+  // one more for every chain of the block beyond that.
+  const int most = kEachAhead * (2 + __popc(__ballot_sync(0xffffffffu, n > 2 * kEachAhead)));
+  const int len = __shfl_sync(0xffffffffu, n, warp);
+  const int first = __shfl_sync(0xffffffffu, w, warp), it = __shfl_sync(0xffffffffu, item, warp);
+  Sum<D / 32> sum;
+  if (len > 0 && len <= most) {
+    sum.clear();
+    add_chain<D, kEachAhead>(p, first, 0, 1, len, r, lane, sum);
+    store_row<D>(p, it, r, lane, sum);
+  }
+  unsigned rest = __ballot_sync(0xffffffffu, n > most);  // the same in every warp
   while (rest != 0) {
     const int k = __ffs(rest) - 1;
     rest &= rest - 1;
-    const int len = __shfl_sync(0xffffffffu, n, k);
-    Sum<V> sum;
-    sum.clear();
-    add_chain<D>(p, __shfl_sync(0xffffffffu, w, k), warp, W, len, r, lane, sum);
-#pragma unroll
-    for (int i = 0; i < V; ++i) acc[warp][V * lane + i] = sum.acc[i];
-    if (lane == 0) {
-      ml[warp][0] = sum.m;
-      ml[warp][1] = sum.l;
-    }
-    __syncthreads();
-    const int it = __shfl_sync(0xffffffffu, item, k);
-    if (warp == 0) {  // lane x weighs warp x's sums; then every lane adds its channels of all
-      const bool mine = lane < W;
-      const float m = mine ? ml[lane][0] : -INFINITY;
-      float top = m;
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-      const float f = mine ? ex2(m - (top == -INFINITY ? 0.f : top)) : 0.f;
-      float l = mine ? ml[lane][1] * f : 0.f;
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
-      sum.m = top;
-      sum.l = l;
-#pragma unroll
-      for (int i = 0; i < V; ++i) sum.acc[i] = 0.f;
-#pragma unroll 8
-      for (int x = 0; x < W; ++x) {
-        const float fx = __shfl_sync(0xffffffffu, f, x);
-#pragma unroll
-        for (int i = 0; i < V; ++i) sum.acc[i] = fmaf(acc[x][V * lane + i], fx, sum.acc[i]);
-      }
-      store_row<D>(p, it, r, lane, sum);
-    }
+    add_by_block<D, kEachWarps, kEachAhead>(p, __shfl_sync(0xffffffffu, w, k), warp, kEachWarps,
+                                            __shfl_sync(0xffffffffu, n, k), r, warp, lane, acc, ml, sum);
+    if (warp == 0) store_row<D>(p, __shfl_sync(0xffffffffu, item, k), r, lane, sum);
     __syncthreads();
   }
 }
 
+// Adds up row r = blockIdx.y of one chain: by a block, or by a cluster of `ctas` blocks whose sums the first
+// adds up in its shared memory.
+template <int D, int kWarps>
+__global__ void __launch_bounds__(32 * kWarps, 32 / kWarps) merge_long_kernel(const Params p, int ctas) {
+  constexpr int V = D / 32;
+  __shared__ float acc[kWarps][D], ml[kWarps][2], all_acc[kMergeCtas][D], all_ml[kMergeCtas][2];
+  const int r = blockIdx.y, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int x = blockIdx.x / static_cast<unsigned>(ctas), rank = blockIdx.x - x * ctas;
+  if (ctas > 1) {  // the cluster's blocks have all started before one writes to another
+    asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
+    asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
+  }
+  after_previous();  // the partials are complete
+  int w, n, item;
+  find_chain(p, x, r, w, n, item);
+  if (n == 0) return;  // in every block of the cluster
+  Sum<V> sum;
+  add_by_block<D, kWarps, 64 / kWarps>(p, w, rank * kWarps + warp, kWarps * ctas, n, r, warp, lane, acc, ml, sum);
+  if (ctas > 1) {
+    if (warp == 0) {
+#pragma unroll
+      for (int i = 0; i < V; ++i) store_first(&all_acc[rank][V * lane + i], sum.acc[i]);
+      if (lane == 0) {
+        store_first(&all_ml[rank][0], sum.m);
+        store_first(&all_ml[rank][1], sum.l);
+      }
+      __syncwarp();
+    }
+    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+    if (rank != 0) return;
+    if (warp == 0) {
+      for (int k = ctas; k < kMergeCtas; ++k) {  // blocks that are not there
+        if (lane == 0) {
+          all_ml[k][0] = -INFINITY;
+          all_ml[k][1] = 0.f;
+        }
+#pragma unroll
+        for (int i = 0; i < V; ++i) all_acc[k][V * lane + i] = 0.f;
+      }
+      __syncwarp();
+      add_all<D, kMergeCtas>(all_acc, all_ml, lane, sum);
+    }
+  }
+  if (warp == 0) store_row<D>(p, item, r, lane, sum);
+}
+
 template <int D, int NR, bool kQuant>
-cudaError_t run(const Params& p, int ctas, long long units, cudaStream_t s) {
+cudaError_t run(Params p, int ctas, long long units, cudaStream_t s) {
   using C = Cfg<D, NR>;
   const size_t smem = C::kSmem + sizeof(int) * (C::kWarps + p.a.B + 1);
+  const int most = static_cast<int>(units < ctas * C::kWarps ? units : ctas * C::kWarps);  // workers
+  const long long items = static_cast<long long>(p.a.B) * p.a.Hkv * p.mtiles;
+  p.by_item = items <= most;
   cudaError_t e = cudaFuncSetAttribute(decode_kernel<D, NR, kQuant>,
                                        cudaFuncAttributeMaxDynamicSharedMemorySize,
                                        static_cast<int>(smem));
   if (e != cudaSuccess) return e;
   e = launch_early(decode_kernel<D, NR, kQuant>, ctas, 32 * C::kWarps, smem, s, p);
   if (e != cudaSuccess) return e;
-  const int most = static_cast<int>(units < ctas * C::kWarps ? units : ctas * C::kWarps);
-  const long long items = static_cast<long long>(p.a.B) * p.a.Hkv * p.mtiles;
-  const bool few = items * 32 <= most;
-  const dim3 grid(few ? static_cast<unsigned>(items) : (most + kMergeSpan - 1) / kMergeSpan,
-                  p.R < p.rows ? p.R : p.rows);
-  return few ? launch_early(decode_merge_kernel<D, true>, grid, 1024, 0, s, p)
-             : launch_early(decode_merge_kernel<D, false>, grid, 256, 0, s, p);
+  // How many warps add up a chain depends on the partials that an item leaves on average.  Where all chains
+  // fit the GPU at two blocks of 16 warps an SM, more blocks share a chain while each has 128 partials.
+  const int chains = p.by_item ? static_cast<int>(items) : most, rows = p.R < p.rows ? p.R : p.rows;
+  if (items * 16 > most)
+    return launch_early(merge_each_kernel<D>, dim3((chains + kEachWarps - 1) / kEachWarps, rows), 32 * kEachWarps, 0,
+                        s, p);
+  const int room = 2 * ctas;
+  if (chains * rows > room) return launch_early(merge_long_kernel<D, 8>, dim3(chains, rows), 256, 0, s, p, 1);
+  int n = 1;
+  while (n < kMergeCtas && chains * rows * 2 * n <= room && items * 128 * n < most) n *= 2;
+  return launch_cluster(n, merge_long_kernel<D, 16>, dim3(chains * n, rows), 512, 0, s, p, n);
 }
 
 }  // namespace

@@ -247,21 +247,30 @@ size_t decode_workspace_bytes(int R, int D);  // R = Hq / Hkv * T
 // after_previous(), which waits for that kernel's end and memory, and lets the next one be brought up in
 // turn.  In a serving step's chain of kernels of a few microseconds that hides a launch each.
 // Such a kernel reads its inputs by plain or L2 loads: the read-only path may only be used for what does not
-// change between the kernel's start, which is before the wait, and its end.
+// change between the kernel's start, which is before the wait, and its end.  launch_cluster: with clusters of
+// n blocks along x.
 template <class... Par, class... Arg>
-cudaError_t launch_early(void (*kernel)(Par...), dim3 grid, dim3 block, size_t smem, cudaStream_t s,
-                         const Arg&... arg) {
+cudaError_t launch_cluster(int n, void (*kernel)(Par...), dim3 grid, dim3 block, size_t smem, cudaStream_t s,
+                           const Arg&... arg) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = grid;
   cfg.blockDim = block;
   cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
-  cudaLaunchAttribute at[1];
+  cudaLaunchAttribute at[2];
   at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   at[0].val.programmaticStreamSerializationAllowed = 1;
+  at[1].id = cudaLaunchAttributeClusterDimension;
+  at[1].val.clusterDim.x = n;
+  at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
   cfg.attrs = at;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = n > 1 ? 2 : 1;
   return cudaLaunchKernelEx(&cfg, kernel, arg...);
+}
+template <class... Par, class... Arg>
+cudaError_t launch_early(void (*kernel)(Par...), dim3 grid, dim3 block, size_t smem, cudaStream_t s,
+                         const Arg&... arg) {
+  return launch_cluster(1, kernel, grid, block, smem, s, arg...);
 }
 __device__ __forceinline__ void after_previous() {
   asm volatile("griddepcontrol.wait;" ::: "memory");
