@@ -73,8 +73,8 @@ constexpr uint32_t kNoPage = 0xffffffffu, kBadPage = 0xfffffffeu;
 // makes room for more warps (64 ragged sequences, D = 128: 16 warps of 3 slots take 4 percent longer than 12 of 4).
 template <int D, int NR>
 struct Cfg {
-  static constexpr int kWarps = NR == 1 ? (D == 128 ? 12 : 16) : 8;
-  static constexpr int kSlots = D == 128 ? (NR == 1 ? 4 : 6) : (NR == 1 ? 5 : 10);
+  static constexpr int kWarps = NR == 1 ? (D == 128 ? 12 : 16) : (D == 128 ? 8 : 12);
+  static constexpr int kSlots = D == 128 ? (NR == 1 ? 4 : 6) : (NR == 1 ? 5 : 7);
   static constexpr int kSlotBytes = kHalf * D + 8 * kHalf;  // codes; in K slots the scales of K and V
   static constexpr int kRing = kSlots * kSlotBytes;
   static constexpr int kSmem = kWarps * kRing;  // then the warps' sums and B + 1 prefix sums
@@ -585,7 +585,7 @@ __global__ void __launch_bounds__(32 * Cfg<D, NR>::kWarps, 1) decode_kernel(cons
     }
     const float unit = vref > 0.f ? kPTop / vref : 0.f;
 
-    uint32_t pb[NR][4][2];
+    float amax[NR][2];  // the tile's largest p of the lane's rows
 #pragma unroll
     for (int n = 0; n < NR; ++n) {
       float2 mt = make_float2(s[n][0][0], s[n][0][1]);
@@ -612,16 +612,32 @@ __global__ void __launch_bounds__(32 * Cfg<D, NR>::kWarps, 1) decode_kernel(cons
           sum = add_rn_f32x2(sum, make_float2(x[0], x[1]));
         }
       l[n] = fma_rn_f32x2(l[n], alpha, sum);
-      float2 inv, back;
-      if (kQuant) {  // the tile's largest p is that of its largest score
+      if (kQuant) {  // that of the largest score
         const float2 e = fma_rn_f32x2(mt, rf[n], neg);
-        const float ax = ex2(e.x), ay = ex2(e.y);
-        const TileScale tx = tile_scale(ax < kTinyP ? 0.f : ax), ty = tile_scale(ay < kTinyP ? 0.f : ay);
-        inv = make_float2(tx.inv, ty.inv);
-        back = make_float2(tx.scale, ty.scale);
+        amax[n][0] = ex2(e.x);
+        amax[n][1] = ex2(e.y);
       }
       const float2 f = make_float2(alpha.x * grow, alpha.y * grow);
       if (__any_sync(0xffffffffu, f.x != 1.f || f.y != 1.f)) scale_rows<MT>(o[n], f);
+    }
+    // The rows' scales, 448 / amax and amax / 448: the lanes that share t hold the same rows, so each does
+    // one of the divisions (g = 4 n + 2 y + which) and the results go round.
+    float quot = 0.f;
+    if (kQuant) {
+      float x = (g & 2) ? amax[0][1] : amax[0][0];
+      if (NR == 2 && (g & 4)) x = (g & 2) ? amax[NR - 1][1] : amax[NR - 1][0];
+      if (!(x < kTinyP)) quot = __fdiv_rn((g & 1) ? x : kE4M3Max, (g & 1) ? kE4M3Max : x);
+    }
+    uint32_t pb[NR][4][2];
+#pragma unroll
+    for (int n = 0; n < NR; ++n) {
+      float2 inv, back;
+      if (kQuant) {
+        inv.x = __shfl_sync(0xffffffffu, quot, 16 * n + t);
+        back.x = __shfl_sync(0xffffffffu, quot, 16 * n + 4 + t);
+        inv.y = __shfl_sync(0xffffffffu, quot, 16 * n + 8 + t);
+        back.y = __shfl_sync(0xffffffffu, quot, 16 * n + 12 + t);
+      }
 #pragma unroll
       for (int c = 0; c < 4; ++c)
 #pragma unroll
