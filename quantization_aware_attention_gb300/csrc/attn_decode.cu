@@ -359,8 +359,10 @@ __global__ void __launch_bounds__(32 * Cfg<D, NR>::kWarps, 1) decode_kernel(cons
   // an item's own unit, where ranges are long enough that each holds a tile all the same
   const int extra = tiles / 4 >= workers ? 1 : 0;
   const int W = tiles + extra * a.B * per_seq;
-  int u0 = static_cast<int>(static_cast<long long>(W) * id / workers);
-  const int u1 = static_cast<int>(static_cast<long long>(W) * (id + 1) / workers);
+  // u0 = floor(W id / workers), u1 the next one's, by 32-bit divisions: W = each workers + over
+  const unsigned each = static_cast<unsigned>(W) / workers, over = W - each * workers;  // over id < kWorkers^2
+  int u0 = each * id + over * id / workers;
+  const int u1 = each * (id + 1) + over * (id + 1) / workers;
 
   Cursor cc;  // what is computed next
   {
