@@ -134,6 +134,33 @@ def test_long_sequence():
     _check(q, lens, 2, 64, cache, table, codes, scales, 1)
 
 
+@pytest.mark.parametrize("lens,Hq,Hkv,T,D", [
+    ([20011], 4, 1, 1, 64),                         # one item: some blocks share its partials
+    ([131071], 3, 1, 1, 128),                       # many
+    ([70000, 5, 0, 300], 8, 1, 2, 64),              # beside items that are whole
+    ([2900 + 17 * i for i in range(40)], 8, 1, 1, 64),   # more rows than fit at once
+    ([3000] + [1 + i % 60 for i in range(199)], 2, 1, 1, 64),    # one long chain among short ones
+    ([9000 + i for i in range(24)], 4, 4, 1, 64),   # long chains of every warp
+    ([1100] * 12, 1, 1, 1, 128),
+])
+def test_cut_items(lens, Hq, Hkv, T, D):
+    """What ranges leave of the items they cut, added up by a warp, a block or several blocks: every row
+    right, the same bits again, and a NaN in one sequence's keys in that sequence's rows alone."""
+    cache, table, codes, scales = _cache(lens, Hkv, D, 64, 23)
+    q = dev_bf16(normal_bf16(12, (len(lens), Hq, T, D)))
+    o, lse = _check(q, lens, Hkv, 64, cache, table, codes, scales, 1, heads=[Hkv - 1])
+    args = (q, cache, _i32(table), _i32(lens))
+    again = qat_attention_decode(*args, return_lse=True)
+    assert torch.equal(o, again[0]) and torch.equal(lse, again[1])
+    at = lens[0] // 3
+    cache.k_scale[int(table[0, at // 64]), 0, at % 64] = float("nan")
+    bad, bad_lse = qat_attention_decode(*args, return_lse=True, check=True)
+    rows = Hq // Hkv
+    assert torch.isnan(bad[0, :rows]).all() and torch.isnan(bad_lse[0, :rows]).all()
+    assert torch.equal(bad[1:], o[1:]) and torch.equal(bad_lse[1:], lse[1:])
+    assert torch.equal(bad[0, rows:], o[0, rows:]) and torch.equal(bad_lse[0, rows:], lse[0, rows:])
+
+
 @pytest.mark.parametrize("D,Hq,Hkv,T", [(64, 16, 8, 1), (128, 8, 8, 1), (64, 24, 8, 3), (128, 16, 4, 4)])
 def test_batch_of_long_sequences(D, Hq, Hkv, T):
     """Many tiles for every warp, items cut anywhere, one item cut many times: every row right, the same
