@@ -93,7 +93,7 @@ def _link_ext(obj: str, verbose: bool) -> None:
     lib = os.path.join(os.path.dirname(torch.__file__), "lib")
     tmp = EXT_PATH + ".tmp"
     _run([shutil.which("g++") or "c++", "-shared", obj, "-o", tmp, "-L", HERE, "-l:libqat_attn.so",
-          "-L", lib, "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch", "-ltorch_python",
+          "-L", lib, "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_cuda", "-ltorch", "-ltorch_python",
           "-Wl,-rpath,$ORIGIN", f"-Wl,-rpath,{lib}"], "_qat_torch", verbose)
     os.replace(tmp, EXT_PATH)
 

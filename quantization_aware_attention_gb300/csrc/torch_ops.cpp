@@ -10,6 +10,7 @@
 #include <torch/csrc/utils/pybind.h>
 
 #include <ATen/ATen.h>
+#include <ATen/cuda/EmptyTensor.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 
@@ -114,6 +115,12 @@ const int* index_ptr(const Tensor& t, const char* name, const at::Device& dev, i
   return t.const_data_ptr<int>();
 }
 
+// An uninitialized tensor from the caching allocator.  Not by way of the dispatcher, which would take as long
+// as the rest of such a call's checks.
+Tensor new_tensor(at::IntArrayRef sizes, at::ScalarType type, const at::Device& dev) {
+  return at::detail::empty_cuda(sizes, type, dev, std::nullopt);
+}
+
 void no_gradient(const char* what, const Tensor& t) {
   TORCH_CHECK_VALUE(!(at::GradMode::is_enabled() && t.requires_grad()), what,
                     " has no backward: call it under torch.no_grad(), or with tensors that do not require "
@@ -121,7 +128,7 @@ void no_gradient(const char* what, const Tensor& t) {
 }
 
 Tensor workspace_or_new(const OptTensor& ws, int64_t bytes, const at::Device& dev) {
-  if (!ws.has_value()) return at::empty({bytes}, at::TensorOptions(at::kByte).device(dev));
+  if (!ws.has_value()) return new_tensor({bytes}, at::kByte, dev);
   TORCH_CHECK_VALUE(ws->device() == dev && ws->scalar_type() == at::kByte && ws->is_contiguous(),
                     "workspace must be a contiguous uint8 tensor on ", dev);
   return *ws;
@@ -195,11 +202,10 @@ NormRopeShape check_norm_rope(const Tensor& q, const Tensor& k, const Tensor& po
 variable_list norm_rope_forward(const NormRopeShape& s, const Tensor& positions, const Tensor& phases,
                                 const Tensor& wq, const Tensor& wk, const RopeArgs& a) {
   const c10::cuda::CUDAGuard guard(s.dev);
-  const auto opt = at::TensorOptions(at::kBFloat16).device(s.dev);
   variable_list out;
   out.reserve(2);
-  out.push_back(at::empty({s.B, s.Hq, s.N, s.D}, opt));
-  if (s.has_k) out.push_back(at::empty({s.B, s.Hk, s.N, s.D}, opt));
+  out.push_back(new_tensor({s.B, s.Hq, s.N, s.D}, at::kBFloat16, s.dev));
+  if (s.has_k) out.push_back(new_tensor({s.B, s.Hk, s.N, s.D}, at::kBFloat16, s.dev));
   ok(qat_qk_norm_rope(s.q.ptr, s.q.strides(), s.k.ptr, s.k.strides(), out[0].mutable_data_ptr(),
                       out.size() > 1 ? out[1].mutable_data_ptr() : nullptr,
                       static_cast<const int*>(ptr_or_null(positions)), s.pos_stride,
@@ -214,17 +220,16 @@ variable_list norm_rope_forward(const NormRopeShape& s, const Tensor& positions,
 
 // dx in the input's order in memory: heads inner where a projection wrote them so.
 Tensor grad_like(const Rows& x, const NormRopeShape& s, int64_t H, Rows* out) {
-  const auto opt = at::TensorOptions(at::kBFloat16).device(s.dev);
   out->dense = true;
   Tensor g;
   if (!x.dense && x.s[2] > x.s[1]) {
-    g = at::empty({s.B, s.N, H, s.D}, opt).transpose(1, 2);
+    g = new_tensor({s.B, s.N, H, s.D}, at::kBFloat16, s.dev).transpose(1, 2);
     out->dense = false;
     out->s[0] = s.N * H * s.D;
     out->s[1] = s.D;
     out->s[2] = H * s.D;
   } else {
-    g = at::empty({s.B, H, s.N, s.D}, opt);
+    g = new_tensor({s.B, H, s.N, s.D}, at::kBFloat16, s.dev);
   }
   out->ptr = g.mutable_data_ptr();
   return g;
@@ -246,8 +251,8 @@ std::array<Tensor, 4> norm_rope_backward(const NormRopeShape& s, const Tensor& p
   }
   Tensor ws;
   if (wq.defined()) {
-    out[2] = at::empty_like(wq);
-    if (s.has_k) out[3] = at::empty_like(wk);
+    out[2] = new_tensor({s.D}, wq.scalar_type(), s.dev);
+    if (s.has_k) out[3] = new_tensor({s.D}, wk.scalar_type(), s.dev);
     ws = workspace_or_new(workspace, static_cast<int64_t>(qat_qk_norm_rope_bwd_workspace_bytes(static_cast<int>(s.D))),
                           s.dev);
   }
@@ -418,8 +423,7 @@ std::tuple<Tensor, Tensor> kv_read(const Tensor& ck, const Tensor& cv, const Ten
   const int64_t N = length.has_value() ? *length : std::max<int64_t>(c.max_pages * c.page - begin, 0);
   TORCH_CHECK_VALUE(N <= INT32_MAX, "length is too large");
   const c10::cuda::CUDAGuard guard(c.dev);
-  const auto opt = at::TensorOptions(at::kBFloat16).device(c.dev);
-  Tensor k = at::empty({c.B, c.H, N, c.D}, opt), v = at::empty({c.B, c.H, N, c.D}, opt);
+  Tensor k = new_tensor({c.B, c.H, N, c.D}, at::kBFloat16, c.dev), v = new_tensor(k.sizes(), at::kBFloat16, c.dev);
   ok(qat_kv_cache_read(c.k, c.v, c.ks, c.vs, c.table, c.lens, k.mutable_data_ptr(), v.mutable_data_ptr(),
                        static_cast<int>(c.B), static_cast<int>(c.H), static_cast<int>(begin), static_cast<int>(N),
                        static_cast<int>(c.D), static_cast<int>(c.pages), static_cast<int>(c.page),
@@ -443,8 +447,8 @@ py::object decode(const Tensor& ck, const Tensor& cv, const Tensor& cks, const T
                                                        static_cast<int>(std::min<int64_t>(T, 1 << 20)),
                                                        static_cast<int>(c.D));
   const Tensor ws = workspace_or_new(workspace, std::max<int64_t>(static_cast<int64_t>(bytes), 256), c.dev);
-  Tensor o = at::empty(q.sizes(), at::TensorOptions(at::kBFloat16).device(c.dev)), lse;
-  if (return_lse) lse = at::empty({c.B, Hq, T}, at::TensorOptions(at::kFloat).device(c.dev));
+  Tensor o = new_tensor(q.sizes(), at::kBFloat16, c.dev), lse;
+  if (return_lse) lse = new_tensor({c.B, Hq, T}, at::kFloat, c.dev);
   ok(qat_attn_decode(q.const_data_ptr(), c.k, c.v, c.ks, c.vs, c.table, c.lens, o.mutable_data_ptr(),
                      return_lse ? lse.mutable_data_ptr<float>() : nullptr, static_cast<int>(c.B),
                      static_cast<int>(Hq), static_cast<int>(c.H), static_cast<int>(T), static_cast<int>(c.D),
