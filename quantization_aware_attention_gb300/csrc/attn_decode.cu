@@ -11,10 +11,14 @@
 // every warp is its own worker with its own ring of K and V tiles filled by cp.async, no barrier
 // between warps, and all G = Hq / Hkv heads that share a KV head (times T tokens) are rows of one item
 // of 8 or 16 rows, so that the cache is read once for all of them (once for each 16 beyond that).
-// Measured, D = 128, 8 KV heads, one token, quantized:
-//   32 query heads, 64 sequences of 129 to 8192 keys    99 us, 5.7 TB/s of codes and scales
-//   40 query heads, 2 sequences of 250001 and 262144   173 us, 6.2 TB/s
-//   32 query heads, one sequence of 1537 keys          9.5 us: two launches and their chains of loads
+// Measured, 8 KV heads, quantized:
+//   D 128, 32 query heads, 1 token, 64 sequences of 129 to 8192 keys     97 us, 5.8 TB/s of codes and scales
+//   D 128, 40 query heads, 1 token, 2 sequences of 250001 and 262144    171 us, 6.3 TB/s
+//   D 64,  32 query heads, 3 tokens, 64 sequences of 129 to 8192         69 us, 4.2 TB/s: issue and latency
+//   D 128, 32 query heads, 1 token, one sequence of 1537 keys            10 us: two launches and their chains
+//                                                                        of loads (prefix sums 1.1 us, table
+//                                                                        and first copies 2.3, data 2 to 4,
+//                                                                        end to merge 1, merge 2.5 to 4)
 // What is left of the first is that the SMs differ by 15 percent in bandwidth: equal ranges end 10 us
 // apart.  (Ranges handed out in pieces end together, but every piece cuts an item, and adding the
 // partials took what that gained.)

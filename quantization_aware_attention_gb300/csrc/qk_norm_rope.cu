@@ -26,10 +26,10 @@
 // What bounds both directions is HBM; what it takes is bytes in flight.  The rows of the next trips are
 // on their way by cp.async, each lane's own 16-byte pieces into its own place in shared memory: no
 // registers, no barriers.  Arithmetic is in packed fp32 pairs.  Measured, D = 128, full rotation, norms:
-//   B1 H40+40 N32768   forward 198 us, 6.8 TB/s of the 4 bytes a channel read and written
-//   B4 H32+32 N8192    forward 159 us, 6.8 TB/s; backward 237 us, 6.8 TB/s of 6 bytes a channel
-//   B1 H32+8 N2048     forward 11.0 us, backward 20.7; B16 N1 2.7 us
-// With few heads (D = 64, 3+1 heads, 200000 tokens: 77 us, 2.7 TB/s) the sines and cosines of a token are
+//   B1 H40+40 N32768   forward 197 us, 6.8 TB/s of the 4 bytes a channel read and written
+//   B4 H32+32 N8192    forward 158 us, 6.8 TB/s; backward 236 us, 6.8 TB/s of 6 bytes a channel
+//   B1 H32+8 N2048     forward 10.3 us, backward 20; B16 N1 2.4 us
+// With few heads (D = 64, 3+1 heads, 200000 tokens: 71 us, 2.9 TB/s) the sines and cosines of a token are
 // shared by few rows and bound it.
 #include "qat_internal.h"
 #include "qat_quant.cuh"
@@ -297,8 +297,8 @@ __global__ void __launch_bounds__(32 * kWarps, 4) norm_rope_kernel(const NormRop
   }
 }
 
-// Backward.  Persistent, so that the weights' gradients leave each block once: block k of a tensor's `blocks` walks (token group, head part) items
-// k, k + blocks, ...; each lane keeps the weight gradient of its 16 channels in registers and
+// Backward.  Persistent, so that the weights' gradients leave each block once: block k of a tensor's
+// `blocks` walks (token group, head part) items k, k + blocks, ...; each lane keeps the weight gradient of its 16 channels in registers and
 // the block's sum goes to its own row of the workspace, which norm_rope_dw_kernel adds in
 // block order.  No atomics: the same sizes give the same bits.
 template <int D, bool kInter>
