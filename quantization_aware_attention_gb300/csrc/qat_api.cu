@@ -71,6 +71,7 @@ constexpr size_t kAlign = 256;
 // With QAT_VERBOSE=1 in the environment, CUDA errors are also printed to stderr.
 qat_status_t from_cuda(cudaError_t e) {
   if (e == cudaSuccess) return QAT_OK;
+  cudaGetLastError();  // reported here: not left for a later call's check of its launch
   static const bool verbose = [] {
     const char* v = getenv("QAT_VERBOSE");
     return v != nullptr && v[0] == '1';

@@ -152,6 +152,13 @@ def test_cut_items(lens, Hq, Hkv, T, D):
     args = (q, cache, _i32(table), _i32(lens))
     again = qat_attention_decode(*args, return_lse=True)
     assert torch.equal(o, again[0]) and torch.equal(lse, again[1])
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        again = qat_attention_decode(*args, return_lse=True)
+    for _ in range(2):
+        again[0].zero_()
+        graph.replay()
+        assert torch.equal(o, again[0]) and torch.equal(lse, again[1])
     at = lens[0] // 3
     cache.k_scale[int(table[0, at // 64]), 0, at % 64] = float("nan")
     bad, bad_lse = qat_attention_decode(*args, return_lse=True, check=True)

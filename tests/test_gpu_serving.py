@@ -282,3 +282,58 @@ def test_a_chain_of_calls_in_flight(captured):
     for i, (a, b) in enumerate(zip(*runs)):
         assert torch.equal(a.view(torch.uint8), b.view(torch.uint8)), i
     check_device_status()
+
+
+@pytest.mark.parametrize("captured", [False, True])
+def test_calls_that_alternate_between_streams(captured):
+    """Every call on the other stream than the one before, ordered by events alone, the workspace shared:
+    the bits of one stream."""
+    def steps(s, x, lens, streams, ws):
+        pos = torch.empty(B, 1, dtype=torch.int32, device="cuda")
+        keep, turn = [], 0
+
+        def on(f):
+            nonlocal turn
+            turn += 1
+            a, b = streams[turn % 2], streams[(turn + 1) % 2]
+            a.wait_stream(b)
+            with torch.cuda.stream(a):
+                out = f()
+            keep.append(out)  # alive until the end: no memory is handed on
+            return out
+
+        for _ in range(25):
+            on(lambda: torch.add(lens, 0, out=pos[:, 0]))
+            on(lambda: lens.add_(1))
+            q, k, v = on(lambda: s.qkv(x, pos))
+            on(lambda: s.cache.append(k, v, s.table, lens))
+            o = on(lambda: qat_attention_decode(q, s.cache, s.table, lens, workspace=ws))
+            kr, vr = on(lambda: s.cache.read(s.table, lens, length=48))
+            x = on(lambda: torch.cat([o, kr[:, :, 3:4], vr[:, :, 3:4]], 1).transpose(1, 2).contiguous())
+        streams[0].wait_stream(streams[1])
+        return [t for out in keep for t in (out if isinstance(out, tuple) else (out,)) if t is not None]
+
+    ws = torch.empty(capi.qat_attn_decode_workspace_bytes(HQ, HKV, 1, D), dtype=torch.uint8, device="cuda")
+    runs = []
+    for two in (False, True):
+        s = Server()
+        for t in (s.cache.k, s.cache.v):
+            t.view(torch.uint8).zero_()
+        for t in (s.cache.k_scale, s.cache.v_scale):
+            t.zero_()
+        x, lens = _x(1, 501), _i32([2, 30, 0])
+        main = torch.cuda.current_stream()
+        if captured and two:
+            torch.cuda.synchronize()
+            graph = torch.cuda.CUDAGraph()
+            with torch.cuda.graph(graph):
+                main = torch.cuda.current_stream()
+                outs = steps(s, x, lens, (main, torch.cuda.Stream()), ws)
+            graph.replay()
+        else:
+            outs = steps(s, x, lens, (main, torch.cuda.Stream() if two else main), ws)
+        torch.cuda.synchronize()
+        runs.append([t.clone() for t in outs])
+    for i, (a, b) in enumerate(zip(*runs)):
+        assert torch.equal(a.view(torch.uint8), b.view(torch.uint8)), i
+    check_device_status()
