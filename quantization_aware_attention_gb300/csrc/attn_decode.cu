@@ -75,9 +75,11 @@ constexpr uint32_t kNoPage = 0xffffffffu, kBadPage = 0xfffffffeu;
 
 // NR: column tiles of 8 query rows per item, 1 or 2.  One tile needs half the registers, which
 // makes room for more warps (64 ragged sequences, D = 128: 16 warps of 3 slots take 4 percent longer than 12 of 4).
+constexpr int warps_of(int D, int NR) { return NR == 1 ? (D == 128 ? 12 : 16) : (D == 128 ? 8 : 12); }
+
 template <int D, int NR>
 struct Cfg {
-  static constexpr int kWarps = NR == 1 ? (D == 128 ? 12 : 16) : (D == 128 ? 8 : 12);
+  static constexpr int kWarps = warps_of(D, NR);
   static constexpr int kSlots = D == 128 ? (NR == 1 ? 4 : 6) : (NR == 1 ? 5 : 7);
   static constexpr int kSlotBytes = kHalf * D + 8 * kHalf;  // codes; in K slots the scales of K and V
   static constexpr int kRing = kSlots * kSlotBytes;
@@ -898,11 +900,15 @@ constexpr int kMergeCtas = 8;  // blocks of a cluster at most
 __device__ __forceinline__ void find_chain(const Params& p, int x, int r, int& w, int& n, int& item) {
   const int workers = __ldcg(&header_of(p)->workers);
   w = n = item = 0;
-  if (x >= (p.by_item ? p.a.B * p.a.Hkv * p.mtiles : kWorkers)) return;
+  const int items = p.a.B * p.a.Hkv * p.mtiles;
+  if (x >= (p.by_item ? items : kWorkers)) return;
   const int2 raw = __ldcg(reinterpret_cast<const int2*>(chains_of(p) + x));
   item = p.by_item ? x : raw.x;
   w = p.by_item ? raw.x : x;
-  if (raw.x >= 0 && (p.by_item || x < workers) && item % p.mtiles * p.rows + r < p.R) n = raw.y - w + 1;
+  // (bounds: an entry beyond the workers' count means nothing, and none may lead outside the workspace)
+  if (raw.x >= 0 && item < items && w < workers && raw.y > w && raw.y < workers &&
+      item % p.mtiles * p.rows + r < p.R)
+    n = raw.y - w + 1;
 }
 
 // A chain's partials by all the block's warps, into sum of warp 0.
@@ -1032,7 +1038,8 @@ int partial_rows(int R) { return R >= kRows ? kRows : (R + 1) / 2 * 2; }
 }  // namespace
 
 size_t decode_workspace_bytes(int R, int D) {
-  return kPartsAt + static_cast<size_t>(kWorkers) * 2 * partial_rows(R) * (D + 2) * sizeof(float);
+  return kPartsAt + static_cast<size_t>(kMaxCtas) * warps_of(D, R <= 8 ? 1 : 2) * 2 * partial_rows(R) * (D + 2) *
+                         sizeof(float);
 }
 
 cudaError_t launch_decode(const DecodeArgs& a, int D, int num_sms, cudaStream_t s) {
