@@ -8,7 +8,8 @@
 //
 // What bounds it: the cache is read once, 2 (D + 4) bytes per key and KV head, and every byte
 // meets at most 16 query rows, so HBM does.  The kernel is built around keeping loads in flight:
-// every warp is its own worker with its own ring of K and V tiles filled by cp.async, no barrier
+// every warp is its own worker with its own place for a tile's K and V, filled by cp.async, each again
+// as soon as it is used (smaller pieces, more of them in flight, took 1 to 7 percent longer); no barrier
 // between warps, and all G = Hq / Hkv heads that share a KV head (times T tokens) are rows of one item
 // of 8 or 16 rows, so that the cache is read once for all of them (once for each 16 beyond that).
 // Measured, 8 KV heads, quantized:
@@ -62,7 +63,6 @@ namespace qat {
 namespace {
 
 constexpr int kTile = 64;    // keys per unit
-constexpr int kHalf = 32;    // keys per ring slot
 constexpr int kChunk = 16;   // keys that certainly share a page
 constexpr int kRows = 16;    // query rows per item at most
 constexpr int kMaxCtas = 152;
@@ -74,15 +74,15 @@ constexpr float kPTop = 16384.f;  // P x value scale / bound is at most this
 constexpr uint32_t kNoPage = 0xffffffffu, kBadPage = 0xfffffffeu;
 
 // NR: column tiles of 8 query rows per item, 1 or 2.  One tile needs half the registers, which
-// makes room for more warps (64 ragged sequences, D = 128: 16 warps of 3 slots take 4 percent longer than 12 of 4).
+// makes room for more warps (64 ragged sequences, D = 128: 16 warps take 4 percent longer than 12; 16 rows of
+// 128 channels with 12 warps and the query rows in shared memory 11 percent longer than 8).
 constexpr int warps_of(int D, int NR) { return NR == 1 ? (D == 128 ? 12 : 16) : (D == 128 ? 8 : 12); }
 
 template <int D, int NR>
 struct Cfg {
   static constexpr int kWarps = warps_of(D, NR);
-  static constexpr int kSlots = D == 128 ? (NR == 1 ? 4 : 6) : (NR == 1 ? 5 : 7);
-  static constexpr int kSlotBytes = kHalf * D + 8 * kHalf;  // codes; in K slots the scales of K and V
-  static constexpr int kRing = kSlots * kSlotBytes;
+  static constexpr int kVAt = kTile * D + 8 * kTile;  // a ring: K codes, the scales of K and V; V codes
+  static constexpr int kRing = kVAt + kTile * D;
   static constexpr int kSmem = kWarps * kRing;  // then the warps' sums and B + 1 prefix sums
 };
 
@@ -391,19 +391,17 @@ __global__ void __launch_bounds__(32 * Cfg<D, NR>::kWarps, 1) decode_kernel(cons
   uint32_t rows_of = kNoPage;  // lane l: cache row where 16-key chunk 32 (tile / 8) + l begins
   bool all_good = false;       // no chunk of those lies on a bad page
   const uint32_t ring = sm100::smem_addr(smem) + warp * C::kRing;
-  uint32_t pslot = 0, cslot = 0;
   // The lane's part of every copy: bytes 16 lane.. of each 512-byte run, by their swizzled places.
   const uint32_t k_dst = k_off<D>(lane / (D / 16), lane % (D / 16));
   const uint32_t v_dst0 = v_off<D>(lane / (D / 16), lane % (D / 16));
   const uint32_t v_dst1 = v_off<D>(lane / (D / 16) + 512 / D, lane % (D / 16)) - 512;
 
-  // Issues the copies of the next slot -- sub 0, 1: the halves of K, with the scales of K and V; 2, 3:
-  // those of V -- as one group; an empty group at the end.
+  // Issues the copies of the next tile's K, with the scales of both, or V as one group; an empty group at the
+  // end.
   auto produce = [&](auto which, bool fresh) {
-    constexpr int sub = decltype(which)::value;
-    constexpr bool kV = sub >= 2;
+    constexpr bool kV = decltype(which)::value;
     if (pu < u1) {
-      if (sub == 0 && (fresh || (pc.tile & 7) == 0)) {
+      if (!kV && (fresh || (pc.tile & 7) == 0)) {
         const int pos = ((pc.tile & ~7) * 4 + lane) * kChunk;
         rows_of = kNoPage;
         if (pos < pc.len) {
@@ -418,30 +416,28 @@ __global__ void __launch_bounds__(32 * Cfg<D, NR>::kWarps, 1) decode_kernel(cons
         all_good = !__any_sync(0xffffffffu, rows_of == kBadPage);
       }
       const uint8_t* codes = (kV ? a.v_codes : a.k_codes) + 16 * lane;
-      const uint32_t dst = ring + pslot * C::kSlotBytes;
-      const int first = (pc.tile & 7) * 4 + 2 * (sub & 1);
-      const int left = pc.len - pc.tile * kTile - kHalf * (sub & 1);  // keys from the half's first on
-      const uint32_t row[2] = {__shfl_sync(0xffffffffu, rows_of, first),
-                               __shfl_sync(0xffffffffu, rows_of, first + 1)};
-      // lanes 0-7: the scales of K, 8-15: of V, four keys each
-      const float* scales = (lane & 8) ? a.v_scales : a.k_scales;
-      const uint32_t sc_row = (lane & 4) ? row[1] : row[0];
-      const uint32_t sc_dst = dst + kHalf * D + 16 * lane;
-      if (left >= kHalf && all_good) {
+      const uint32_t dst = ring + (kV ? C::kVAt : 0);
+      const int first = (pc.tile & 7) * (kTile / kChunk);
+      const int left = pc.len - pc.tile * kTile;  // keys from the tile's first on
+      // lanes 0-15: the scales of K, 16-31: of V, four keys each
+      const float* scales = (lane & 16) ? a.v_scales : a.k_scales;
+      const uint32_t sc_row = kV ? 0 : __shfl_sync(0xffffffffu, rows_of, first + ((lane & 15) >> 2));
+      const uint32_t sc_dst = dst + kTile * D + 16 * lane;
+      if (left >= kTile && all_good) {
 #pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          const uint8_t* src = codes + static_cast<size_t>(row[c]) * D;
+        for (int c = 0; c < kTile / kChunk; ++c) {
+          const uint8_t* src = codes + static_cast<size_t>(__shfl_sync(0xffffffffu, rows_of, first + c)) * D;
 #pragma unroll
           for (int i = 0; i < D / 32; ++i) {
             const uint32_t off = kV ? ((i & 1) ? v_dst1 : v_dst0) : k_dst;
             cp_async16(dst + off + c * kChunk * D + i * 512, src + i * 512);
           }
         }
-        if (!kV && lane < 16) cp_async16(sc_dst, scales + sc_row + 4 * (lane & 3));
+        if (!kV) cp_async16(sc_dst, scales + sc_row + 4 * (lane & 3));
       } else {  // zeros behind the end, and for bad pages zeros with scale NaN
 #pragma unroll 1
-        for (int c = 0; c < 2; ++c) {
-          const uint32_t rc = c ? row[1] : row[0];
+        for (int c = 0; c < kTile / kChunk; ++c) {
+          const uint32_t rc = __shfl_sync(0xffffffffu, rows_of, first + c);
           const int n = rc < kBadPage ? left - c * kChunk : 0;
           const uint8_t* src = codes + (rc < kBadPage ? static_cast<size_t>(rc) * D : 0);
 #pragma unroll 1
@@ -451,39 +447,23 @@ __global__ void __launch_bounds__(32 * Cfg<D, NR>::kWarps, 1) decode_kernel(cons
             cp_async16(dst + off + c * kChunk * D + i * 512, r < n ? src + i * 512 : codes, r < n ? 16 : 0);
           }
         }
-        if (!kV && lane < 16) {
+        if (!kV) {
           if (sc_row == kBadPage) {
             asm volatile("st.shared.v4.u32 [%0], {%1,%1,%1,%1};" ::"r"(sc_dst), "r"(0x7fc00000u) : "memory");
           } else {
-            const int n = sc_row == kNoPage ? 0 : min(max(left - 4 * (lane & 7), 0), 4);
+            const int n = sc_row == kNoPage ? 0 : min(max(left - 4 * (lane & 15), 0), 4);
             cp_async16(sc_dst, n > 0 ? scales + sc_row + 4 * (lane & 3) : scales, 4 * n);
           }
         }
       }
-      pslot = pslot + 1 == C::kSlots ? 0 : pslot + 1;
-      if (sub == 3) {
-        advance(p, prefix, extra, pc, pu);
-      }
+      if (kV) advance(p, prefix, extra, pc, pu);
     }
     cp_commit();
   };
-#define QAT_SUB(i) std::integral_constant<int, (i) & 3>{}
-#pragma unroll
-  for (int i = 0; i < C::kSlots; ++i) {
-    if ((i & 3) == 0) produce(QAT_SUB(0), i == 0);
-    if ((i & 3) == 1) produce(QAT_SUB(1), false);
-    if ((i & 3) == 2) produce(QAT_SUB(2), false);
-    if ((i & 3) == 3) produce(QAT_SUB(3), false);
-  }
-
-  // Waits for the oldest slot; returns its address.
-  auto consume = [&]() {
-    cp_wait<C::kSlots - 1>();
-    __syncwarp();
-    const uint32_t s = ring + cslot * C::kSlotBytes;
-    cslot = cslot + 1 == C::kSlots ? 0 : cslot + 1;
-    return s;
-  };
+  constexpr std::integral_constant<bool, false> kKeys{};
+  constexpr std::integral_constant<bool, true> kValues{};
+  produce(kKeys, true);
+  produce(kValues, false);
 
   constexpr int KS = D / 16;   // k-steps of K Q^T
   constexpr int MT = D / 16;   // row tiles of V^T P^T; a lane's channels are (D / 8) g + 0 .. D / 8 - 1
@@ -518,9 +498,11 @@ __global__ void __launch_bounds__(32 * Cfg<D, NR>::kWarps, 1) decode_kernel(cons
     // keys g and g + 8 of rows 2t, 2t + 1
     float s[NR][4][4];
     float vs[4][2];  // the values' scales of those keys
+    cp_wait<1>();
+    __syncwarp();
 #pragma unroll
     for (int hf = 0; hf < 2; ++hf) {
-      const uint32_t slot = consume();
+      const uint32_t slot = ring + hf * (kTile / 2) * D;
 #pragma unroll
       for (int n = 0; n < NR; ++n)
 #pragma unroll
@@ -551,9 +533,9 @@ __global__ void __launch_bounds__(32 * Cfg<D, NR>::kWarps, 1) decode_kernel(cons
       for (int c = 0; c < 2; ++c)
 #pragma unroll
         for (int y = 0; y < 2; ++y) {
-          const uint32_t at = slot + kHalf * D + 4 * (16 * c + 8 * y + g);
+          const uint32_t at = ring + kTile * D + 4 * (32 * hf + 16 * c + 8 * y + g);
           const float ks = lds_f(at);
-          vs[2 * hf + c][y] = lds_f(at + 4 * kHalf);
+          vs[2 * hf + c][y] = lds_f(at + 4 * kTile);
 #pragma unroll
           for (int n = 0; n < NR; ++n) {
             float* x = s[n][2 * hf + c] + 2 * y;
@@ -562,9 +544,9 @@ __global__ void __launch_bounds__(32 * Cfg<D, NR>::kWarps, 1) decode_kernel(cons
             x[1] = z.y;
           }
         }
-      __syncwarp();
-      if (hf == 0) produce(QAT_SUB(C::kSlots), false); else produce(QAT_SUB(1 + C::kSlots), false);
     }
+    __syncwarp();
+    produce(kKeys, false);
 
     // mask: only tiles that reach past what some row sees
     const int key0 = cc.tile * kTile + g;
@@ -666,9 +648,11 @@ __global__ void __launch_bounds__(32 * Cfg<D, NR>::kWarps, 1) decode_kernel(cons
     }
 
     // O^T += V^T P^T
+    cp_wait<1>();
+    __syncwarp();
 #pragma unroll
     for (int hf = 0; hf < 2; ++hf) {
-      const uint32_t slot = consume();
+      const uint32_t slot = ring + C::kVAt + hf * (kTile / 2) * D;
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
         const uint32_t base = slot + c * kChunk * D;
@@ -700,9 +684,9 @@ __global__ void __launch_bounds__(32 * Cfg<D, NR>::kWarps, 1) decode_kernel(cons
               mma16816(o[n][2 * i + z], va, pb[n][2 * hf + c][0], pb[n][2 * hf + c][1]);
           }
       }
-      __syncwarp();
-      if (hf == 0) produce(QAT_SUB(2 + C::kSlots), false); else produce(QAT_SUB(3 + C::kSlots), false);
     }
+    __syncwarp();
+    produce(kValues, false);
 
     const bool ends = cc.tile + 1 == cc.tiles;
     if (ends || u + 1 >= u1) {  // the segment's end
@@ -758,7 +742,6 @@ __global__ void __launch_bounds__(32 * Cfg<D, NR>::kWarps, 1) decode_kernel(cons
     }
     advance(p, prefix, extra, cc, u);
   }
-#undef QAT_SUB
   cp_wait<0>();
 }
 
