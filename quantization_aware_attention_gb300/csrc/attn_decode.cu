@@ -13,10 +13,10 @@
 // between warps, and all G = Hq / Hkv heads that share a KV head (times T tokens) are rows of one item
 // of 8 or 16 rows, so that the cache is read once for all of them (once for each 16 beyond that).
 // Measured, 8 KV heads, quantized:
-//   D 128, 32 query heads, 1 token, 64 sequences of 129 to 8192 keys     97 us, 5.8 TB/s of codes and scales
+//   D 128, 32 query heads, 1 token, 64 sequences of 129 to 8192 keys     96 us, 5.9 TB/s of codes and scales
 //   D 128, 40 query heads, 1 token, 2 sequences of 250001 and 262144    171 us, 6.3 TB/s
-//   D 64,  32 query heads, 3 tokens, 64 sequences of 129 to 8192         69 us, 4.2 TB/s: issue and latency
-//   D 128, 32 query heads, 1 token, one sequence of 1537 keys            10 us: two launches and their chains
+//   D 64,  32 query heads, 3 tokens, 64 sequences of 129 to 8192         64 us, 4.6 TB/s: issue and latency
+//   D 128, 32 query heads, 1 token, one sequence of 1537 keys           9.4 us: two launches and their chains
 //                                                                        of loads (prefix sums 1.1 us, table
 //                                                                        and first copies 2.3, data 2 to 4,
 //                                                                        end to merge 1, merge 2.5 to 4)
@@ -30,7 +30,7 @@
 // the item's unit, warps that got many short sequences ended last: 64 sequences of 129 to 8192 keys, 3
 // tokens, 64 channels, 104 against 87 us.)  An item inside one range is finished there; an item cut by a
 // range boundary leaves unnormalized fp32 partials with their m and l in the workspace, which
-// decode_merge_kernel adds in an order that the lengths alone decide (no atomics: the same lengths give
+// the merge kernels add in an order that the lengths alone decide (no atomics: the same lengths give
 // the same bits).
 //
 // Products: mma.sync m16n8k16 with f16 operands and fp32 sums, the cache as the 16-row operand and
