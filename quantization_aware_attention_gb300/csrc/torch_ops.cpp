@@ -5,7 +5,9 @@
 // These calls are made once per layer and decoding step, on a few microseconds of GPU work, so what the
 // host spends on them is what they cost; in Python it was two to three times as much (a decode call on one
 // sequence 28 us, a training pass of the norm + rotation through autograd 310).
+#include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/custom_function.h>
+#include <torch/csrc/autograd/python_variable.h>
 #include <torch/csrc/autograd/variable.h>
 #include <torch/csrc/utils/pybind.h>
 
@@ -461,12 +463,125 @@ py::object decode(const Tensor& ck, const Tensor& cv, const Tensor& cks, const T
   return py::cast(o);
 }
 
+// ------------------------------------------------------------------------------- Python
+
+// The arguments of a call, in order.  (Read here and not by generated casters, which take 1 us for a call of
+// a dozen, as long as the checks.)
+class Args {
+ public:
+  Args(PyObject* const* a, Py_ssize_t n, Py_ssize_t want) : a_(a) {
+    TORCH_CHECK_TYPE(n == want, "expected ", want, " arguments, got ", n);
+  }
+  const Tensor& tensor() {
+    PyObject* o = *a_++;
+    TORCH_CHECK_TYPE(THPVariable_Check(o), "expected a tensor, got ", Py_TYPE(o)->tp_name);
+    return THPVariable_Unpack(o);
+  }
+  OptTensor optional_tensor() {
+    if (none()) return std::nullopt;
+    return tensor();
+  }
+  int64_t integer() {
+    const long long x = PyLong_AsLongLong(*a_++);
+    if (x == -1 && PyErr_Occurred()) throw py::error_already_set();
+    return x;
+  }
+  std::optional<int64_t> optional_integer() {
+    if (none()) return std::nullopt;
+    return integer();
+  }
+  double real() {
+    const double x = PyFloat_AsDouble(*a_++);
+    if (x == -1.0 && PyErr_Occurred()) throw py::error_already_set();
+    return x;
+  }
+  std::optional<double> optional_real() {
+    if (none()) return std::nullopt;
+    return real();
+  }
+  bool boolean() {
+    const int x = PyObject_IsTrue(*a_++);
+    if (x < 0) throw py::error_already_set();
+    return x != 0;
+  }
+  std::optional<bool> optional_boolean() {
+    if (none()) return std::nullopt;
+    return boolean();
+  }
+
+ private:
+  bool none() {
+    if (*a_ != Py_None) return false;
+    ++a_;
+    return true;
+  }
+  PyObject* const* a_;
+};
+
+PyObject* py_norm_rope(PyObject*, PyObject* const* args, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  Args a(args, n, 10);
+  const Tensor& q = a.tensor();
+  const OptTensor k = a.optional_tensor(), positions = a.optional_tensor(), phases = a.optional_tensor(),
+                  wq = a.optional_tensor(), wk = a.optional_tensor();
+  const int64_t rotary_dim = a.integer();
+  const bool interleaved = a.boolean();
+  const double amplitude = a.real(), eps = a.real();
+  return norm_rope(q, k, positions, phases, wq, wk, rotary_dim, interleaved, amplitude, eps).release().ptr();
+  END_HANDLE_TH_ERRORS
+}
+
+PyObject* py_kv_append(PyObject*, PyObject* const* args, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  Args a(args, n, 10);
+  const Tensor &ck = a.tensor(), &cv = a.tensor(), &cks = a.tensor(), &cvs = a.tensor(), &k = a.tensor(),
+               &v = a.tensor(), &table = a.tensor(), &lens = a.tensor();
+  const OptTensor new_lens = a.optional_tensor();
+  kv_append(ck, cv, cks, cvs, k, v, table, lens, new_lens, a.optional_boolean());
+  Py_RETURN_NONE;
+  END_HANDLE_TH_ERRORS
+}
+
+PyObject* py_kv_read(PyObject*, PyObject* const* args, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  Args a(args, n, 9);
+  const Tensor &ck = a.tensor(), &cv = a.tensor(), &cks = a.tensor(), &cvs = a.tensor(), &table = a.tensor(),
+               &lens = a.tensor();
+  const int64_t begin = a.integer();
+  const std::optional<int64_t> length = a.optional_integer();
+  const auto out = kv_read(ck, cv, cks, cvs, table, lens, begin, length, a.optional_boolean());
+  return py::make_tuple(std::get<0>(out), std::get<1>(out)).release().ptr();
+  END_HANDLE_TH_ERRORS
+}
+
+PyObject* py_decode(PyObject*, PyObject* const* args, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  Args a(args, n, 12);
+  const Tensor &ck = a.tensor(), &cv = a.tensor(), &cks = a.tensor(), &cvs = a.tensor(), &q = a.tensor(),
+               &table = a.tensor(), &lens = a.tensor();
+  const std::optional<double> sm_scale = a.optional_real();
+  const int64_t quant_mode = a.integer();
+  TORCH_CHECK_VALUE(quant_mode >= INT32_MIN && quant_mode <= INT32_MAX, "quant_mode ", quant_mode);
+  const bool return_lse = a.boolean();
+  const OptTensor workspace = a.optional_tensor();
+  return decode(ck, cv, cks, cvs, q, table, lens, sm_scale, static_cast<int>(quant_mode), return_lse, workspace,
+                a.optional_boolean())
+      .release()
+      .ptr();
+  END_HANDLE_TH_ERRORS
+}
+
+template <PyObject* (*f)(PyObject*, PyObject* const*, Py_ssize_t)>
+PyMethodDef method(const char* name) {
+  return {name, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(f)), METH_FASTCALL, nullptr};
+}
+
 }  // namespace
 
 PYBIND11_MODULE(_qat_torch, m) {
-  m.def("norm_rope", &norm_rope);
   m.def("norm_rope_bwd", &norm_rope_bwd);
-  m.def("kv_append", &kv_append);
-  m.def("kv_read", &kv_read);
-  m.def("decode", &decode);
+  static PyMethodDef methods[] = {method<py_norm_rope>("norm_rope"), method<py_kv_append>("kv_append"),
+                                  method<py_kv_read>("kv_read"), method<py_decode>("decode"),
+                                  {nullptr, nullptr, 0, nullptr}};
+  if (PyModule_AddFunctions(m.ptr(), methods) != 0) throw py::error_already_set();
 }
