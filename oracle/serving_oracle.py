@@ -89,8 +89,8 @@ def decode_head(q, k, v, positions, sm_scale, quant):
       scores    fp32 products and sums: 2^-19 of sum_d |q_d k_d| sm_scale log2 e, plus 2^-20 for exp2
                 and the row sum, both relative to p
       codes     one E4M3 step where 448 p / amax lies that near to the middle between two codes
-      weights   f16: half a step, 2^-11 relative; absolute 2^-38 of the largest value of V below its
-                normal range
+      weights   f16: half a step, 2^-11 relative; below its normal range absolute 2^-38 of the row's own
+                largest weight, p times the largest |v| of a key
       output    bf16: half a step, 2^-8 relative; fp32 sum over n keys: 2^-20 of sum p |v|."""
     T, D = q.shape
     n = k.shape[0]
@@ -124,6 +124,6 @@ def decode_head(q, k, v, positions, sm_scale, quant):
         o[t] = p @ vv / l
         mass = p @ np.abs(vv) / l
         tol[t] = (2.0 ** -8 * np.abs(o[t]) + (2.0 ** -11 + 4 * eps_p + 2.0 ** -20) * mass
-                  + flips @ np.abs(vv) / l + n * 2.0 ** -38 * np.abs(vv).max(initial=0.0) / l)
+                  + flips @ np.abs(vv) / l + n * 2.0 ** -38 * (p * np.abs(vv).max(-1, initial=0.0)).max() / l)
         lse_tol[t] = LOG2E * 2 * eps_p + 2.0 ** -22 * abs(lse[t])
     return o, lse, tol, lse_tol

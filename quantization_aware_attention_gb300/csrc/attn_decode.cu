@@ -15,7 +15,7 @@
 // Measured, 8 KV heads, quantized:
 //   D 128, 32 query heads, 1 token, 64 sequences of 129 to 8192 keys     96 us, 5.9 TB/s of codes and scales
 //   D 128, 40 query heads, 1 token, 2 sequences of 250001 and 262144    171 us, 6.3 TB/s
-//   D 64,  32 query heads, 3 tokens, 64 sequences of 129 to 8192         64 us, 4.6 TB/s: issue and latency
+//   D 64,  32 query heads, 3 tokens, 64 sequences of 129 to 8192         65 us, 4.5 TB/s: issue and latency
 //   D 128, 32 query heads, 1 token, one sequence of 1537 keys           9.4 us: two launches and their chains
 //                                                                        of loads (prefix sums 1.1 us, table
 //                                                                        and first copies 2.3, data 2 to 4,
@@ -38,9 +38,9 @@
 // O^T = V^T P^T.  E4M3 codes are exact in f16, and become f16 in registers (one conversion per two
 // codes), so the scale of a key multiplies its row of S^T, and the scale of a value its row of P^T.
 // q (bf16) is brought into f16 by a power of two per row, which is exact for every element above 2^-32
-// of the row's largest.  P times the value's scale is rounded to f16 (2^-11 relative; relative to a
-// running power-of-two bound of the scales, so that it neither overflows nor loses small weights: the
-// largest is near 2^14, the smallest kept whole 2^-28 of it).  With so few rows these products need a
+// of the row's largest.  The weights, P times the values' scales, are rounded to f16: by 2^-11 of
+// themselves, as each row's are multiplied by a power of two that follows its largest weight so far
+// (to about 2^14; what is below 2^-28 of the row's largest is off by 2^-39 of it).  With so few rows these products need a
 // tenth of the tensor rate, and a 128-row tcgen05 tile would want the codes of V transposed and P in
 // 8 bits with a scale per key; the memory pipeline is what has to be fed.
 //
@@ -70,7 +70,8 @@ constexpr int kMaxWarps = 16;
 constexpr int kWorkers = kMaxCtas * kMaxWarps;
 constexpr float kTinyP = 7.888609052210118e-31f;  // 2^-100: a tile below it counts as zero (448 / amax
                                                   // must stay finite)
-constexpr float kPTop = 16384.f;  // P x value scale / bound is at most this
+constexpr float kPTop = 16384.f;  // the largest weight as an f16 operand
+constexpr uint32_t kPTopAt = (127u + 127u + 14u) << 23;  // minus a power of two's bits: those of kPTop over it
 constexpr uint32_t kNoPage = 0xffffffffu, kBadPage = 0xfffffffeu;
 
 // NR: column tiles of 8 query rows per item, 1 or 2.  One tile needs half the registers, which
@@ -307,6 +308,27 @@ __device__ __forceinline__ float sum_over_g(float x) {
   return x + __shfl_xor_sync(0xffffffffu, x, 16);
 }
 
+// Two maxima of values >= 0 over the lanes that share t, to 8 bits (rounded towards zero).
+__device__ __forceinline__ float2 max_over_g(float2 v) {
+  uint32_t x = __byte_perm(__float_as_uint(v.x), __float_as_uint(v.y), 0x7632);
+#pragma unroll
+  for (int o = 4; o < 32; o <<= 1) {
+    const uint32_t y = __shfl_xor_sync(0xffffffffu, x, o);
+    asm("max.bf16x2 %0, %0, %1;" : "+r"(x) : "r"(y));
+  }
+  return make_float2(__uint_as_float(x << 16), __uint_as_float(x & 0xffff0000u));
+}
+
+// The bits of the power of two above x >= 0, of 2^-112 .. 2^126 (kPTop over it is a normal number).
+__device__ __forceinline__ uint32_t pow2_above(float x) {
+  return min(max((__float_as_uint(x) & 0x7f800000u) + 0x00800000u, 15u << 23), 253u << 23);
+}
+// a / b of two such powers, as far as fp32 reaches.
+__device__ __forceinline__ float pow2_ratio(uint32_t a, uint32_t b) {
+  const int r = static_cast<int>(a - b) + (127 << 23);
+  return __uint_as_float(static_cast<uint32_t>(min(max(r, 1 << 23), 254 << 23)));
+}
+
 template <int D, int NR, bool kQuant>
 __global__ void __launch_bounds__(32 * Cfg<D, NR>::kWarps, 1) decode_kernel(const Params p) {
   using C = Cfg<D, NR>;
@@ -471,7 +493,7 @@ __global__ void __launch_bounds__(32 * Cfg<D, NR>::kWarps, 1) decode_kernel(cons
   float o[NR][MT][4];
   float2 m[NR], l[NR], rf[NR];  // of rows 8 n + 2t and 8 n + 2t + 1
   int last[NR][2];              // the newest key each of those rows sees
-  float vref = 0.f;
+  float2 bound[NR];             // the rows' largest weights so far, as m is
   bool begun = false;
   if (lane == 0 && !p.by_item) chains_of(p)[id] = Chain{-1, -1};
   int first_tile = cc.tile;    // of the current segment
@@ -484,14 +506,13 @@ __global__ void __launch_bounds__(32 * Cfg<D, NR>::kWarps, 1) decode_kernel(cons
 #pragma unroll
       for (int n = 0; n < NR; ++n) {
         m[n] = make_float2(-INFINITY, -INFINITY);
-        l[n] = make_float2(0.f, 0.f);
+        l[n] = bound[n] = make_float2(0.f, 0.f);
 #pragma unroll
         for (int y = 0; y < 2; ++y)
           last[n][y] = cc.len - a.T + (cc.mt * p.rows + 8 * n + 2 * t + y) % a.T;
 #pragma unroll
         for (int j = 0; j < MT; ++j) o[n][j][0] = o[n][j][1] = o[n][j][2] = o[n][j][3] = 0.f;
       }
-      vref = 0.f;
     }
 
     // S^T = K Q^T of 64 keys, times the keys' scales (and, below, the rows'): chunk c's values are
@@ -561,21 +582,8 @@ __global__ void __launch_bounds__(32 * Cfg<D, NR>::kWarps, 1) decode_kernel(cons
             if (key0 + 16 * c + 8 * (i >> 1) > last[n][i & 1]) s[n][c][i] = -INFINITY;
     }
 
-    // a power of two above every value's scale so far; o is kept divided by it
-    float vmax = 0.f;
-#pragma unroll
-    for (int c = 0; c < 4; ++c) vmax = fmaxf(vmax, fmaxf(vs[c][0], vs[c][1]));
-    vmax = max_over_g(vmax);
-    float grow = 1.f;
-    if (vmax > vref) {
-      const int e = min(max(static_cast<int>(__float_as_uint(vmax) >> 23) - 126, -100), 126);
-      const float nref = __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
-      grow = vref / nref;
-      vref = nref;
-    }
-    const float unit = vref > 0.f ? kPTop / vref : 0.f;
-
     float amax[NR][2];  // the tile's largest p of the lane's rows
+    float2 alpha[NR];
 #pragma unroll
     for (int n = 0; n < NR; ++n) {
       float2 mt = make_float2(s[n][0][0], s[n][0][1]);
@@ -588,7 +596,7 @@ __global__ void __launch_bounds__(32 * Cfg<D, NR>::kWarps, 1) decode_kernel(cons
       mt.y = max_over_g(mt.y);
       const float2 mn = make_float2(fmaxf(m[n].x, mt.x * rf[n].x), fmaxf(m[n].y, mt.y * rf[n].y));
       const float2 neg = make_float2(mn.x == -INFINITY ? 0.f : -mn.x, mn.y == -INFINITY ? 0.f : -mn.y);
-      const float2 alpha = make_float2(ex2(m[n].x + neg.x), ex2(m[n].y + neg.y));
+      alpha[n] = make_float2(ex2(m[n].x + neg.x), ex2(m[n].y + neg.y));
       m[n] = mn;
       float2 sum = make_float2(0.f, 0.f);
 #pragma unroll
@@ -601,14 +609,12 @@ __global__ void __launch_bounds__(32 * Cfg<D, NR>::kWarps, 1) decode_kernel(cons
           x[1] = ex2(e.y);
           sum = add_rn_f32x2(sum, make_float2(x[0], x[1]));
         }
-      l[n] = fma_rn_f32x2(l[n], alpha, sum);
+      l[n] = fma_rn_f32x2(l[n], alpha[n], sum);
       if (kQuant) {  // that of the largest score
         const float2 e = fma_rn_f32x2(mt, rf[n], neg);
         amax[n][0] = ex2(e.x);
         amax[n][1] = ex2(e.y);
       }
-      const float2 f = make_float2(alpha.x * grow, alpha.y * grow);
-      if (__any_sync(0xffffffffu, f.x != 1.f || f.y != 1.f)) scale_rows<MT>(o[n], f);
     }
     // The rows' scales, 448 / amax and amax / 448: the lanes that share t hold the same rows, so each does
     // one of the divisions (g = 4 n + 2 y + which) and the results go round.
@@ -618,6 +624,9 @@ __global__ void __launch_bounds__(32 * Cfg<D, NR>::kWarps, 1) decode_kernel(cons
       if (NR == 2 && (g & 4)) x = (g & 2) ? amax[NR - 1][1] : amax[NR - 1][0];
       if (!(x < kTinyP)) quot = __fdiv_rn((g & 1) ? x : kE4M3Max, (g & 1) ? kE4M3Max : x);
     }
+    // The weights, P times the values' scales, and as f16 operands: each row's are multiplied by a power of two
+    // that takes the largest so far to 2^13 .. 2^14, and its sums with them.  A weight that the row does not see,
+    // or that is nothing beside the others, counts for nothing there, whatever the value's scale.
     uint32_t pb[NR][4][2];
 #pragma unroll
     for (int n = 0; n < NR; ++n) {
@@ -628,21 +637,40 @@ __global__ void __launch_bounds__(32 * Cfg<D, NR>::kWarps, 1) decode_kernel(cons
         inv.y = __shfl_sync(0xffffffffu, quot, 16 * n + 8 + t);
         back.y = __shfl_sync(0xffffffffu, quot, 16 * n + 12 + t);
       }
+      float2 top = make_float2(0.f, 0.f);
 #pragma unroll
       for (int c = 0; c < 4; ++c)
 #pragma unroll
         for (int y = 0; y < 2; ++y) {
-          float2 w = make_float2(s[n][c][2 * y], s[n][c][2 * y + 1]);
+          float* x = s[n][c] + 2 * y;
+          float2 w = make_float2(x[0], x[1]);
           if (kQuant) {
             const float2 q = mul_rn_f32x2(w, inv);
             w = mul_rn_f32x2(e4m3x2_decode(e4m3x2_rn_satfinite(q.x, q.y)), back);
           }
-          const float v = vs[c][y] * unit;
-          w = mul_rn_f32x2(w, make_float2(v, v));
+          w = mul_rn_f32x2(w, make_float2(vs[c][y], vs[c][y]));
           if (edge) {  // 0 x NaN: a key that the row does not see may hold anything
             if (key0 + 16 * c + 8 * y > last[n][0]) w.x = 0.f;
             if (key0 + 16 * c + 8 * y > last[n][1]) w.y = 0.f;
           }
+          x[0] = w.x;
+          x[1] = w.y;
+          top.x = fmaxf(top.x, w.x);
+          top.y = fmaxf(top.y, w.y);
+        }
+      top = max_over_g(top);
+      const float2 old = bound[n];
+      bound[n] = make_float2(fmaxf(old.x * alpha[n].x, top.x), fmaxf(old.y * alpha[n].y, top.y));
+      const uint32_t ex = pow2_above(bound[n].x), ey = pow2_above(bound[n].y);
+      const float2 f = make_float2(alpha[n].x * pow2_ratio(pow2_above(old.x), ex),
+                                   alpha[n].y * pow2_ratio(pow2_above(old.y), ey));
+      if (__any_sync(0xffffffffu, f.x != 1.f || f.y != 1.f)) scale_rows<MT>(o[n], f);
+      const float2 unit = make_float2(__uint_as_float(kPTopAt - ex), __uint_as_float(kPTopAt - ey));
+#pragma unroll
+      for (int c = 0; c < 4; ++c)
+#pragma unroll
+        for (int y = 0; y < 2; ++y) {
+          const float2 w = mul_rn_f32x2(make_float2(s[n][c][2 * y], s[n][c][2 * y + 1]), unit);
           pb[n][c][y] = transpose8x8(f16x2(w.x, w.y));
         }
     }
@@ -702,7 +730,6 @@ __global__ void __launch_bounds__(32 * Cfg<D, NR>::kWarps, 1) decode_kernel(cons
           chains_of(p)[p.by_item ? item : id] = Chain{p.by_item ? id : item, static_cast<int>((end * workers - 1) / W)};
         }
       }
-      const float scale = vref * (1.f / kPTop);
 #pragma unroll
       for (int n = 0; n < NR; ++n) {
         l[n].x = sum_over_g(l[n].x);
@@ -712,6 +739,7 @@ __global__ void __launch_bounds__(32 * Cfg<D, NR>::kWarps, 1) decode_kernel(cons
           const int r = 8 * n + 2 * t + y;
           if (cc.mt * p.rows + r >= p.R) continue;
           const float lr = y ? l[n].y : l[n].x, mr = y ? m[n].y : m[n].x;
+          const float scale = __uint_as_float(pow2_above(y ? bound[n].y : bound[n].x)) * (1.f / kPTop);
           if (whole) {  // the item's output
             const size_t row = (static_cast<size_t>(cc.b) * a.Hkv + cc.h) * p.R + cc.mt * p.rows + r;
             const bool none = lr == 0.f;
