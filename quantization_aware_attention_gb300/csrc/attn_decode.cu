@@ -1018,15 +1018,18 @@ __global__ void __launch_bounds__(32 * kWarps, 32 / kWarps) merge_long_kernel(co
 template <int D, int NR, bool kQuant>
 cudaError_t run(Params p, int ctas, long long units, cudaStream_t s) {
   using C = Cfg<D, NR>;
-  const size_t smem = C::kSmem + sizeof(int) * (C::kWarps + p.a.B + 1);
+  const auto bytes = [](int B) { return C::kSmem + sizeof(int) * (C::kWarps + B + 1); };
   const int most = static_cast<int>(units < ctas * C::kWarps ? units : ctas * C::kWarps);  // workers
   const long long items = static_cast<long long>(p.a.B) * p.a.Hkv * p.mtiles;
   p.by_item = items <= most;
+  // The limit is that of the largest batch in every call: it is the kernel's, and another thread's call may
+  // come between this one's limit and its launch.
+  static_assert(bytes(kDecodeMaxBatch) <= 227 * 1024, "the batch's prefix sums fit beside the rings");
   cudaError_t e = cudaFuncSetAttribute(decode_kernel<D, NR, kQuant>,
                                        cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       static_cast<int>(smem));
+                                       static_cast<int>(bytes(kDecodeMaxBatch)));
   if (e != cudaSuccess) return e;
-  e = launch_early(decode_kernel<D, NR, kQuant>, ctas, 32 * C::kWarps, smem, s, p);
+  e = launch_early(decode_kernel<D, NR, kQuant>, ctas, 32 * C::kWarps, bytes(p.a.B), s, p);
   if (e != cudaSuccess) return e;
   // How many warps add up a chain depends on the partials that an item leaves on average.  Where all chains
   // fit the GPU at two blocks of 16 warps an SM, more blocks share a chain while each has 128 partials.
