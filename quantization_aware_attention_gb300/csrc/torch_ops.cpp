@@ -251,9 +251,19 @@ std::array<Tensor, 4> norm_rope_backward(const NormRopeShape& s, const Tensor& p
     out[1] = grad_like(s.k, s, s.Hk, &dk);
   }
   Tensor ws;
+  void *dwq = nullptr, *dwk = nullptr;
   if (wq.defined()) {
-    out[2] = new_tensor({s.D}, wq.scalar_type(), s.dev);
-    if (s.has_k) out[3] = new_tensor({s.D}, wk.scalar_type(), s.dev);
+    // of a tensor without heads the weight's gradient is zero (the entry takes none for it)
+    const auto weight_grad = [&](const Tensor& w, int64_t H, void** dw) {
+      Tensor g = new_tensor({s.D}, w.scalar_type(), s.dev);
+      if (H > 0)
+        *dw = g.mutable_data_ptr();
+      else
+        g.zero_();
+      return g;
+    };
+    out[2] = weight_grad(wq, s.Hq, &dwq);
+    if (s.has_k) out[3] = weight_grad(wk, s.Hk, &dwk);
     ws = workspace_or_new(workspace, static_cast<int64_t>(qat_qk_norm_rope_bwd_workspace_bytes(static_cast<int>(s.D))),
                           s.dev);
   }
@@ -261,8 +271,7 @@ std::array<Tensor, 4> norm_rope_backward(const NormRopeShape& s, const Tensor& p
          s.q.ptr, s.q.strides(), s.k.ptr, s.k.strides(), gq.ptr, gq.strides(), gk.ptr, gk.strides(),
          static_cast<const int*>(ptr_or_null(positions)), s.pos_stride,
          static_cast<const unsigned long long*>(ptr_or_null(phases)), ptr_or_null(wq), ptr_or_null(wk), s.w_bf16,
-         dq.ptr, dq.strides(), dk.ptr, dk.strides(), out[2].defined() ? out[2].mutable_data_ptr() : nullptr,
-         out[3].defined() ? out[3].mutable_data_ptr() : nullptr, static_cast<int>(s.B), static_cast<int>(s.Hq),
+         dq.ptr, dq.strides(), dk.ptr, dk.strides(), dwq, dwk, static_cast<int>(s.B), static_cast<int>(s.Hq),
          static_cast<int>(s.Hk), static_cast<int>(s.N), static_cast<int>(s.D), a.rotary_dim, a.interleaved,
          static_cast<float>(a.amplitude), static_cast<float>(a.eps), ws.defined() ? ws.mutable_data_ptr() : nullptr,
          ws.defined() ? static_cast<size_t>(ws.numel()) : 0, stream_of(s.dev)),

@@ -7,10 +7,14 @@ import numpy as np
 import pytest
 import torch
 
-from quantization_aware_attention_gb300 import KVCache
+from quantization_aware_attention_gb300 import (KVCache, RopePlan, qat_qk_norm_rope,
+                                                qat_qk_norm_rope_backward)
 from quantization_aware_attention_gb300 import build as qbuild
 from quantization_aware_attention_gb300 import capi
 from quantization_aware_attention_gb300.capi import Status
+from quantization_aware_attention_gb300.inputs import normal_bf16
+
+from gpu_util import dev_bf16
 
 pytestmark = pytest.mark.gpu
 
@@ -61,3 +65,27 @@ def test_decode_from_threads_with_different_batches():
     torch.cuda.synchronize()
     assert not bad, (len(bad), bad[:3])
     assert all((c[7] == 0).all() for c in calls)
+
+
+@pytest.mark.parametrize("Hq,Hk", [(3, 0), (0, 2), (0, 0)])
+@pytest.mark.parametrize("wtype", [torch.float32, torch.bfloat16])
+def test_gradients_where_a_tensor_has_no_heads(Hq, Hk, wtype):
+    """Both weights given, one tensor (or each) without heads: its weight's gradient is zero, the other's what
+    it is alone."""
+    D, rope = 64, RopePlan(32)
+    q, k = (dev_bf16(normal_bf16(80 + h, (2, 3, 5, D)))[:, :h] for h in (Hq, Hk))
+    g = [dev_bf16(normal_bf16(90 + h, (2, 3, 5, D)))[:, :h] for h in (Hq, Hk)]
+    w = [torch.linspace(0.5, 1.5, D, device="cuda").to(wtype).requires_grad_(True) for _ in range(2)]
+    pos = _i32(range(5))
+    leaves = [q.detach().requires_grad_(True), k.detach().requires_grad_(True), *w]
+    out = qat_qk_norm_rope(leaves[0], leaves[1], pos, rope, *w)
+    grads = torch.autograd.grad(out, leaves, g)
+    direct = qat_qk_norm_rope_backward(q, k, pos, rope, *(t.detach() for t in w), *g)
+    for x, y, leaf in zip(grads, direct, leaves):
+        assert x.shape == leaf.shape and x.dtype == leaf.dtype and torch.equal(x, y)
+    for i, (t, h) in enumerate(((q, Hq), (k, Hk))):
+        if h == 0:
+            assert (grads[2 + i] == 0).all()
+        else:
+            alone = qat_qk_norm_rope_backward(t, None, pos, rope, w[i].detach(), None, g[i], None)
+            assert torch.equal(alone[0], grads[i]) and torch.equal(alone[2], grads[2 + i])
