@@ -128,6 +128,12 @@ void no_gradient(const char* what, const Tensor& t) {
                     "gradients");
 }
 
+// Forward-mode derivatives would be dropped: the direct calls look at requires_grad alone.
+void no_tangent(const char* what, std::initializer_list<const Tensor*> in) {
+  for (const Tensor* t : in)
+    TORCH_CHECK_VALUE(!t->defined() || !t->_fw_grad(0).defined(), what, " has no forward-mode derivative");
+}
+
 Tensor workspace_or_new(const OptTensor& ws, int64_t bytes, const at::Device& dev) {
   if (!ws.has_value()) return new_tensor({bytes}, at::kByte, dev);
   TORCH_CHECK_VALUE(ws->device() == dev && ws->scalar_type() == at::kByte && ws->is_contiguous(),
@@ -308,6 +314,7 @@ struct NormRope : torch::autograd::Function<NormRope> {
                      ctx->saved_data["eps"].toDouble()};
     const NormRopeShape s = check_norm_rope(v[0], v[1], v[2], v[3], v[4], v[5], a);
     for (Tensor& g : grads) {
+      no_tangent("qat_qk_norm_rope_backward", {&g});
       Rows r;
       if (!readable(g, &r)) g = g.contiguous();
     }
@@ -342,6 +349,7 @@ py::object norm_rope(const Tensor& q, const OptTensor& k_, const OptTensor& posi
                      double amplitude, double eps) {
   const Tensor k = or_undefined(k_), positions = or_undefined(positions_), phases = or_undefined(phases_);
   const Tensor wq = or_undefined(wq_), wk = or_undefined(wk_);
+  no_tangent("qat_qk_norm_rope", {&q, &k, &wq, &wk});
   const auto needs = [](const Tensor& t) { return t.defined() && t.requires_grad(); };
   variable_list out;
   if (at::GradMode::is_enabled() && (needs(q) || needs(k) || needs(wq) || needs(wk))) {
@@ -363,9 +371,11 @@ std::tuple<OptTensor, OptTensor, OptTensor, OptTensor> norm_rope_bwd(
   const Tensor k = or_undefined(k_), positions = or_undefined(positions_), phases = or_undefined(phases_);
   const Tensor wq = or_undefined(wq_), wk = or_undefined(wk_);
   TORCH_CHECK_VALUE(k.defined() == dk_out.has_value(), "dk_out goes together with k");
+  const Tensor dk = or_undefined(dk_out);
+  no_tangent("qat_qk_norm_rope_backward", {&q, &k, &wq, &wk, &dq_out, &dk});
   const RopeArgs a{static_cast<int>(rotary_dim), interleaved, amplitude, eps};
   auto d = norm_rope_backward(check_norm_rope(q, k, positions, phases, wq, wk, a), positions, phases, wq, wk, dq_out,
-                              or_undefined(dk_out), a, workspace);
+                              dk, a, workspace);
   const auto opt = [](const Tensor& t) { return t.defined() ? OptTensor(t) : std::nullopt; };
   return {d[0], opt(d[1]), opt(d[2]), opt(d[3])};
 }
@@ -393,6 +403,7 @@ Cache cache_of(const Tensor& k, const Tensor& v, const Tensor& ks, const Tensor&
     TORCH_CHECK_VALUE(t->device() == dev && t->scalar_type() == at::kFloat && t->is_contiguous() &&
                           t->sizes() == k.sizes().slice(0, 3) && aligned16(*t),
                       "the cache's scales must be contiguous torch.float32 [pages, H, page_size]");
+  no_tangent("the cache", {&ks, &vs});
   Cache c{dev, k.size(0), k.size(1), k.size(2), k.size(3), 0, 0, k.mutable_data_ptr(), v.mutable_data_ptr(),
           ks.mutable_data_ptr<float>(), vs.mutable_data_ptr<float>(), nullptr, nullptr};
   c.lens = index_ptr(lens, "seq_lens", dev, -1, -2);
@@ -414,6 +425,7 @@ void kv_append(const Tensor& ck, const Tensor& cv, const Tensor& cks, const Tens
   const Rows rv = rows(v, "v", c.dev, {c.B, c.H, N, c.D});
   no_gradient("append", k);
   no_gradient("append", v);
+  no_tangent("append", {&k, &v});
   const int* nl = new_lens.has_value() ? index_ptr(*new_lens, "new_lens", c.dev, c.B, -2) : nullptr;
   const c10::cuda::CUDAGuard guard(c.dev);
   ok(qat_kv_cache_append(rk.ptr, rk.strides(), rv.ptr, rv.strides(), c.k, c.v, c.ks, c.vs, c.table, c.lens, nl,
@@ -450,6 +462,7 @@ py::object decode(const Tensor& ck, const Tensor& cv, const Tensor& cks, const T
   const Rows rq = rows(q, "q", c.dev, {c.B, -1, -1, c.D});
   TORCH_CHECK_VALUE(rq.dense, "q must be contiguous");
   no_gradient("qat_attention_decode", q);
+  no_tangent("qat_attention_decode", {&q});
   const int64_t Hq = q.size(1), T = q.size(2);
   TORCH_CHECK_VALUE(Hq >= 1 && Hq % c.H == 0, Hq, " query heads do not share the cache's ", c.H, " evenly");
   const c10::cuda::CUDAGuard guard(c.dev);

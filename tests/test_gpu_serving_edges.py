@@ -1,4 +1,5 @@
-"""Calls at the edges of what the norm + rotation, the cache and decoding take."""
+"""Calls at the edges of what the norm + rotation, the cache and decoding take: several host threads, tensors
+without heads, derivatives that are not there."""
 
 import sys
 import threading
@@ -6,8 +7,9 @@ import threading
 import numpy as np
 import pytest
 import torch
+import torch.autograd.forward_ad as fwad
 
-from quantization_aware_attention_gb300 import (KVCache, RopePlan, qat_qk_norm_rope,
+from quantization_aware_attention_gb300 import (KVCache, RopePlan, qat_attention_decode, qat_qk_norm_rope,
                                                 qat_qk_norm_rope_backward)
 from quantization_aware_attention_gb300 import build as qbuild
 from quantization_aware_attention_gb300 import capi
@@ -89,3 +91,49 @@ def test_gradients_where_a_tensor_has_no_heads(Hq, Hk, wtype):
         else:
             alone = qat_qk_norm_rope_backward(t, None, pos, rope, w[i].detach(), None, g[i], None)
             assert torch.equal(alone[0], grads[i]) and torch.equal(alone[2], grads[2 + i])
+
+
+def test_forward_mode_derivatives_are_refused():
+    """A tangent that a call would drop is an error, on tensors that need gradients and on others."""
+    q, k = (dev_bf16(normal_bf16(70 + h, (2, h, 5, 64))) for h in (4, 2))
+    w = [torch.ones(64, device="cuda") for _ in range(2)]
+    pos, table, lens = _i32(range(5)), _i32([[0], [1]]), _i32([5, 5])
+    cache = KVCache.empty(2, 2, 16, 64)
+    cache.append(k, k, table, lens)
+    args = [q, k, *w]
+    for needs in (False, True):
+        for i in range(4):
+            with fwad.dual_level():
+                a = [t.detach().requires_grad_(needs) for t in args]
+                a[i] = fwad.make_dual(a[i], torch.ones_like(a[i]))
+                with pytest.raises((ValueError, RuntimeError), match="forward-mode|jvp"):
+                    qat_qk_norm_rope(a[0], a[1], pos, RopePlan(64), a[2], a[3])
+    with fwad.dual_level():
+        dual = fwad.make_dual(k, torch.ones_like(k))
+        for call in (lambda: cache.append(dual, k, table, lens), lambda: cache.append(k, dual, table, lens),
+                     lambda: qat_attention_decode(fwad.make_dual(q, torch.ones_like(q)), cache, table, lens),
+                     lambda: qat_qk_norm_rope_backward(q, k, pos, RopePlan(64), *w, q, dual)):
+            with pytest.raises(ValueError, match="forward-mode"):
+                call()
+        leaf = q.detach().requires_grad_(True)
+        out = qat_qk_norm_rope(leaf, q_weight=w[0])
+        with pytest.raises(ValueError, match="forward-mode"):  # forward over reverse
+            torch.autograd.grad(out, leaf, fwad.make_dual(q, torch.ones_like(q)))
+        scaled = KVCache(cache.k, cache.v, fwad.make_dual(cache.k_scale, torch.ones_like(cache.k_scale)),
+                         cache.v_scale)
+        with pytest.raises(ValueError, match="forward-mode"):
+            scaled.read(table, lens)
+    # and the same calls without a tangent go through
+    assert len(qat_qk_norm_rope(q, k, pos, RopePlan(64), *w)) == 2
+    assert qat_attention_decode(q, cache, table, lens, check=True).shape == q.shape
+
+
+def test_function_transforms_are_refused():
+    """torch.func's wrapped tensors have no memory of their own: an error, not a result without the transform."""
+    q = dev_bf16(normal_bf16(75, (3, 2, 4, 5, 64)))
+    w = torch.ones(64, device="cuda")
+    for call in (lambda: torch.func.vmap(lambda x: qat_qk_norm_rope(x, q_weight=w))(q),
+                 lambda: torch.func.grad(lambda x: qat_qk_norm_rope(x, q_weight=w).float().sum())(q[0]),
+                 lambda: torch.func.jvp(lambda x: qat_qk_norm_rope(x, q_weight=w), (q[0],), (q[0],))):
+        with pytest.raises((ValueError, RuntimeError)):
+            call()
