@@ -63,6 +63,12 @@ void check_status(std::optional<bool> check, const at::Device& dev, const char* 
   if (*check) ok(qat_attn_device_status(stream_of(dev)), what);
 }
 
+// A wrapper (a fake or distributed tensor, a subclass around other tensors) has sizes and a device but no
+// memory of its own; its null pointer would read as an argument that was left out.
+void with_memory(const Tensor& t, const char* name) {
+  TORCH_CHECK_VALUE(t.numel() == 0 || t.const_data_ptr() != nullptr, name, " has no memory of its own");
+}
+
 void on_cuda(const Tensor& t, const char* name) {
   TORCH_CHECK_VALUE(t.is_cuda(), name, " must be a CUDA tensor (this library has no CPU path)");
 }
@@ -101,6 +107,7 @@ Rows rows(const Tensor& t, const char* name, const at::Device& dev, std::array<i
                       at::IntArrayRef(shape.data(), 4), " (-1: any)");
     TORCH_CHECK_VALUE(t.size(i) <= INT32_MAX, name, " is too large: ", t.sizes());
   }
+  with_memory(t, name);
   Rows r;
   TORCH_CHECK_VALUE(readable(t, &r), name, " must have D innermost and rows on 16-byte boundaries, got strides ",
                     t.strides());
@@ -114,6 +121,7 @@ const int* index_ptr(const Tensor& t, const char* name, const at::Device& dev, i
   TORCH_CHECK_VALUE(t.dim() == dims && t.is_contiguous() && (n < 0 || t.size(0) == n), name,
                     " must be contiguous with ", dims, " dimension(s)", n < 0 ? "" : ", one row a sequence",
                     ", got shape ", t.sizes());
+  with_memory(t, name);
   return t.const_data_ptr<int>();
 }
 
@@ -138,6 +146,7 @@ Tensor workspace_or_new(const OptTensor& ws, int64_t bytes, const at::Device& de
   if (!ws.has_value()) return new_tensor({bytes}, at::kByte, dev);
   TORCH_CHECK_VALUE(ws->device() == dev && ws->scalar_type() == at::kByte && ws->is_contiguous(),
                     "workspace must be a contiguous uint8 tensor on ", dev);
+  with_memory(*ws, "workspace");
   return *ws;
 }
 
@@ -184,6 +193,7 @@ NormRopeShape check_norm_rope(const Tensor& q, const Tensor& k, const Tensor& po
                       "the weights must both be torch.float32 or torch.bfloat16");
     TORCH_CHECK_VALUE(w->dim() == 1 && w->size(0) == s.D && w->is_contiguous() && aligned16(*w),
                       "a weight must be contiguous [", s.D, "] on a 16-byte boundary, got shape ", w->sizes());
+    with_memory(*w, "a weight");
   }
   s.w_bf16 = wq.defined() && wq.scalar_type() == at::kBFloat16;
   if (!phases.defined()) {
@@ -194,8 +204,10 @@ NormRopeShape check_norm_rope(const Tensor& q, const Tensor& k, const Tensor& po
   TORCH_CHECK_VALUE(phases.scalar_type() == at::kLong && phases.is_contiguous() &&
                         phases.numel() == a.rotary_dim / 2,
                     "the RopePlan's phases must be contiguous int64 [rotary_dim / 2]");
+  with_memory(phases, "the RopePlan");
   TORCH_CHECK_VALUE(a.rotary_dim <= s.D, "rotary_dim ", a.rotary_dim, " exceeds the head dimension ", s.D);
   TORCH_CHECK_VALUE(positions.defined() && positions.device() == s.dev, "positions must be a tensor on ", s.dev);
+  with_memory(positions, "positions");
   TORCH_CHECK_VALUE(positions.scalar_type() == at::kInt, "positions must be torch.int32, got ",
                     positions.scalar_type());
   const auto ps = positions.sizes();
@@ -404,6 +416,7 @@ Cache cache_of(const Tensor& k, const Tensor& v, const Tensor& ks, const Tensor&
                           t->sizes() == k.sizes().slice(0, 3) && aligned16(*t),
                       "the cache's scales must be contiguous torch.float32 [pages, H, page_size]");
   no_tangent("the cache", {&ks, &vs});
+  for (const Tensor* t : {&k, &v, &ks, &vs}) with_memory(*t, "the cache");
   Cache c{dev, k.size(0), k.size(1), k.size(2), k.size(3), 0, 0, k.mutable_data_ptr(), v.mutable_data_ptr(),
           ks.mutable_data_ptr<float>(), vs.mutable_data_ptr<float>(), nullptr, nullptr};
   c.lens = index_ptr(lens, "seq_lens", dev, -1, -2);

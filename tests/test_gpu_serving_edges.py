@@ -137,3 +137,34 @@ def test_function_transforms_are_refused():
                  lambda: torch.func.jvp(lambda x: qat_qk_norm_rope(x, q_weight=w), (q[0],), (q[0],))):
         with pytest.raises((ValueError, RuntimeError)):
             call()
+
+
+class _Wrapper(torch.Tensor):
+    """Sizes and a device, no memory."""
+
+    @staticmethod
+    def __new__(cls, like):
+        return torch.Tensor._make_wrapper_subclass(cls, like.shape, dtype=like.dtype, device=like.device)
+
+    @classmethod
+    def __torch_dispatch__(cls, func, types, args=(), kwargs=None):
+        raise NotImplementedError(str(func))
+
+
+def test_tensors_without_memory_are_refused():
+    """Optional arguments among them: they are not taken for absent."""
+    q, k = (dev_bf16(normal_bf16(76 + h, (2, h, 5, 64))) for h in (4, 2))
+    w, pos, table, lens = torch.ones(64, device="cuda"), _i32(range(5)), _i32([[0], [1]]), _i32([5, 5])
+    cache = KVCache.empty(2, 2, 16, 64)
+    rope = RopePlan(64)
+    for call in (lambda: qat_qk_norm_rope(q, k, pos, rope, _Wrapper(w), _Wrapper(w)),
+                 lambda: qat_qk_norm_rope(q, k, _Wrapper(pos), rope, w, w),
+                 lambda: qat_qk_norm_rope(q, _Wrapper(k), pos, rope, w, w),
+                 lambda: qat_qk_norm_rope_backward(q, k, pos, rope, w, w, q, _Wrapper(k)),
+                 lambda: cache.append(k, k, table, lens, _Wrapper(lens)),
+                 lambda: cache.append(k, k, _Wrapper(table), lens),
+                 lambda: qat_attention_decode(q, cache, table, lens,
+                                              workspace=_Wrapper(torch.empty(1 << 20, dtype=torch.uint8,
+                                                                             device="cuda")))):
+        with pytest.raises(ValueError, match="memory"):
+            call()

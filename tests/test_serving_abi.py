@@ -183,3 +183,30 @@ def test_host_tensors_are_refused():
         KVCache(f8, f8, s, s)
     with pytest.raises(TypeError):
         qat_attention_decode(x, None, None, None)
+
+
+class _Wrapper(torch.Tensor):
+    """Sizes and a device, no memory."""
+
+    @staticmethod
+    def __new__(cls, shape, dtype):
+        return torch.Tensor._make_wrapper_subclass(cls, shape, dtype=dtype, device="cuda:0")
+
+    @classmethod
+    def __torch_dispatch__(cls, func, types, args=(), kwargs=None):
+        raise NotImplementedError(str(func))
+
+
+def test_tensors_without_memory_are_refused():
+    x = _Wrapper((2, 3, 5, 64), torch.bfloat16)
+    with pytest.raises(ValueError, match="memory"):
+        qat_qk_norm_rope(x)
+    f8, s = _Wrapper((2, 3, 16, 64), torch.float8_e4m3fn), _Wrapper((2, 3, 16), torch.float32)
+    cache = KVCache(f8, f8, s, s)
+    table, lens = _Wrapper((2, 1), torch.int32), _Wrapper((2,), torch.int32)
+    with pytest.raises(ValueError, match="memory"):
+        qat_attention_decode(x, cache, table, lens)
+    with pytest.raises(ValueError, match="memory"):
+        cache.append(x, x, table, lens)
+    with pytest.raises(ValueError, match="memory"):
+        cache.read(table, lens)
