@@ -7,6 +7,7 @@
 // sequence 28 us, a training pass of the norm + rotation through autograd 310).
 #include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/custom_function.h>
+#include <torch/csrc/autograd/graph_task.h>
 #include <torch/csrc/autograd/python_variable.h>
 #include <torch/csrc/autograd/variable.h>
 #include <torch/csrc/utils/pybind.h>
@@ -24,6 +25,8 @@
 #include <initializer_list>
 #include <optional>
 #include <tuple>
+#include <unordered_set>
+#include <vector>
 
 #include "qat_attn.h"
 
@@ -299,6 +302,66 @@ std::array<Tensor, 4> norm_rope_backward(const NormRopeShape& s, const Tensor& p
 
 Tensor or_undefined(const OptTensor& t) { return t.has_value() ? *t : Tensor(); }
 
+// A backward step under capture must not pass gradients to a node of the default stream: torch would have that
+// stream wait for the capturing one, which ends the capture and may end the process.  A node's stream is the one
+// that was current when it was made, and a leaf keeps one accumulation node as long as any graph that ends in it
+// lives.
+bool on_default_stream(torch::autograd::Node& node, const c10::Stream& none) {
+  const auto on = node.stream();
+  return on.has_value() && *on == none;
+}
+
+constexpr const char* kOnDefault =
+    " was made on the default stream and is still alive: drop its outputs before capturing a backward, or make it "
+    "on another stream";
+
+// Whether the current stream is being captured, and the device's default stream (never captured itself).
+std::optional<c10::Stream> default_beside_capture(const at::Device& dev) {
+  const c10::cuda::CUDAStream now = c10::cuda::getCurrentCUDAStream(dev.index());
+  const c10::cuda::CUDAStream none = c10::cuda::getDefaultCUDAStream(dev.index());
+  if (now == none) return std::nullopt;
+  cudaStreamCaptureStatus status = cudaStreamCaptureStatusNone;
+  if (cudaStreamIsCapturing(now.stream(), &status) != cudaSuccess || status == cudaStreamCaptureStatusNone)
+    return std::nullopt;
+  return none.unwrap();
+}
+
+// The forward looks at the leaves that it is given itself.
+void check_capture(std::initializer_list<const Tensor*> leaves, const at::Device& dev) {
+  const auto none = default_beside_capture(dev);
+  if (!none.has_value()) return;
+  for (const Tensor* t : leaves) {
+    if (!t->defined() || !t->requires_grad() || !t->is_leaf()) continue;
+    const auto node = torch::autograd::impl::try_get_grad_accumulator(*t);
+    TORCH_CHECK_VALUE(node == nullptr || !on_default_stream(*node, *none), "a graph that ends in one of these leaves",
+                      kOnDefault);
+  }
+}
+
+// The backward at all that lies before it -- a projection and its leaves -- as far as this pass will run it.
+void check_capture_before(const at::Device& dev) {
+  const auto none = default_beside_capture(dev);
+  const auto self = torch::autograd::get_current_node();
+  if (!none.has_value() || self == nullptr) return;
+  const auto* plan = torch::autograd::get_current_graph_task_exec_info();  // empty: everything runs
+  std::vector<torch::autograd::Node*> todo{self.get()};
+  std::unordered_set<torch::autograd::Node*> seen;
+  while (!todo.empty()) {
+    torch::autograd::Node* at = todo.back();
+    todo.pop_back();
+    for (const auto& edge : at->next_edges()) {
+      torch::autograd::Node* node = edge.function.get();
+      if (node == nullptr || !seen.insert(node).second) continue;
+      if (plan != nullptr && !plan->empty()) {
+        const auto it = plan->find(node);
+        if (it == plan->end() || !it->second.should_execute()) continue;
+      }
+      TORCH_CHECK_VALUE(!on_default_stream(*node, *none), "a graph that this backward passes through", kOnDefault);
+      todo.push_back(node);
+    }
+  }
+}
+
 // Forward returns the normed and rotated q (and k); nothing but the inputs is saved, the backward
 // recomputes the norm.
 struct NormRope : torch::autograd::Function<NormRope> {
@@ -325,6 +388,7 @@ struct NormRope : torch::autograd::Function<NormRope> {
                      ctx->saved_data["interleaved"].toBool(), ctx->saved_data["amplitude"].toDouble(),
                      ctx->saved_data["eps"].toDouble()};
     const NormRopeShape s = check_norm_rope(v[0], v[1], v[2], v[3], v[4], v[5], a);
+    check_capture_before(s.dev);
     for (Tensor& g : grads) {
       no_tangent("qat_qk_norm_rope_backward", {&g});
       Rows r;
@@ -335,26 +399,6 @@ struct NormRope : torch::autograd::Function<NormRope> {
     return {d[0], d[1], Tensor(), Tensor(), d[2], d[3], Tensor(), Tensor(), Tensor(), Tensor()};
   }
 };
-
-// A leaf keeps one accumulation node as long as any graph that ends in it lives, on the stream that was
-// current when the first of them was made.  If that is the default stream, a backward under capture would
-// have the default stream wait for the capturing one, which ends the capture and may end the process.
-void check_capture(std::initializer_list<const Tensor*> leaves, const at::Device& dev) {
-  const c10::cuda::CUDAStream now = c10::cuda::getCurrentCUDAStream(dev.index());
-  const c10::cuda::CUDAStream none = c10::cuda::getDefaultCUDAStream(dev.index());
-  if (now == none) return;  // the default stream is never captured
-  cudaStreamCaptureStatus status = cudaStreamCaptureStatusNone;
-  if (cudaStreamIsCapturing(now.stream(), &status) != cudaSuccess || status == cudaStreamCaptureStatusNone) return;
-  for (const Tensor* t : leaves) {
-    if (!t->defined() || !t->requires_grad() || !t->is_leaf()) continue;
-    const auto node = torch::autograd::impl::try_get_grad_accumulator(*t);
-    if (node == nullptr) continue;
-    const auto on = node->stream();
-    TORCH_CHECK_VALUE(!on.has_value() || *on != none.unwrap(),
-                      "a graph that ends in one of these leaves was made on the default stream and is still "
-                      "alive: drop its outputs before capturing a backward, or make it on another stream");
-  }
-}
 
 py::object norm_rope(const Tensor& q, const OptTensor& k_, const OptTensor& positions_, const OptTensor& phases_,
                      const OptTensor& wq_, const OptTensor& wk_, int64_t rotary_dim, bool interleaved,

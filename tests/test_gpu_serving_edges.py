@@ -1,6 +1,7 @@
 """Calls at the edges of what the norm + rotation, the cache and decoding take: several host threads, tensors
-without heads, derivatives that are not there."""
+without heads, derivatives that are not there, wrappers, a captured backward."""
 
+import gc
 import sys
 import threading
 
@@ -168,3 +169,48 @@ def test_tensors_without_memory_are_refused():
                                                                              device="cuda")))):
         with pytest.raises(ValueError, match="memory"):
             call()
+
+
+@pytest.mark.parametrize("alive", ["projection", "input"])
+def test_a_captured_backward_beside_a_living_eager_graph_of_a_projection(alive):
+    """q and k are slices of a projection, whose weight's accumulation node (or the projection itself) belongs to
+    the default stream: the captured backward is refused before gradients leave the operator.  With the eager graph
+    gone, or where the backward ends before it, the same capture goes through with the eager call's bits."""
+    H, D, N = 2, 64, 9
+    gen = torch.Generator(device="cuda").manual_seed(1)
+    h = torch.randn(1, N, 128, generator=gen, device="cuda").bfloat16()
+    big = (torch.randn(128, 2 * H * D, generator=gen, device="cuda") / 12).bfloat16().requires_grad_(True)
+    w = torch.ones(D, device="cuda", requires_grad=True)
+    pos, rope = _i32(range(N)), RopePlan(D)
+    g = [torch.randn(1, H, N, D, generator=gen, device="cuda").bfloat16() for _ in range(2)]
+
+    def project():
+        return (h @ big).view(1, N, 2 * H, D).transpose(1, 2)
+
+    def forward(x):
+        return qat_qk_norm_rope(x[:, :H], x[:, H:], pos, rope, w, w)
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        want = torch.autograd.grad(forward(project()), (big, w), g)  # and loads the kernels
+    torch.cuda.current_stream().wait_stream(side)
+    eager = project()
+    torch.cuda.synchronize()
+    with pytest.raises(ValueError, match="default stream"):
+        with torch.cuda.graph(torch.cuda.CUDAGraph()):
+            out = forward(project() if alive == "projection" else eager)
+            torch.autograd.grad(out, (big, w), g)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):  # the weight of the norm alone: nothing goes further
+        got = torch.autograd.grad(forward(project()), w, g)
+    graph.replay()
+    assert torch.equal(got[0], want[1])
+    del eager, out
+    gc.collect()  # the refused call's frames
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = torch.autograd.grad(forward(project()), (big, w), g)
+    graph.replay()
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
