@@ -10,9 +10,12 @@ from __future__ import annotations
 
 import concurrent.futures
 import glob
+import hashlib
+import importlib.util
 import os
 import shutil
 import subprocess
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
@@ -62,13 +65,20 @@ def _compile(src: str, extra: list[str], verbose: bool) -> str:
     return obj
 
 
-def _compile_ext(verbose: bool) -> str:
-    """The torch extension's object, compiled against the installed torch's headers."""
-    import sysconfig
-
+def _ext_key() -> str:
+    """What the extension is compiled and linked against: torch's version and place, and the interpreter."""
     import torch
 
-    obj = os.path.join(OBJDIR, f"torch_ops-{torch.__version__}.o")
+    where = os.path.dirname(torch.__file__) + sysconfig.get_paths()["include"]
+    return (f"{torch.__version__}-{sysconfig.get_config_var('SOABI')}-"
+            f"{hashlib.sha256(where.encode()).hexdigest()[:12]}")
+
+
+def _compile_ext(verbose: bool) -> str:
+    """The torch extension's object, compiled against the installed torch's headers."""
+    import torch
+
+    obj = os.path.join(OBJDIR, f"torch_ops-{_ext_key()}.o")
     src = os.path.join(CSRC, EXT_SOURCE)
     newest = max(os.path.getmtime(src), os.path.getmtime(os.path.join(INCLUDE, "qat_attn.h")))
     if os.path.exists(obj) and os.path.getmtime(obj) >= newest:
@@ -88,14 +98,25 @@ def _compile_ext(verbose: bool) -> str:
 def _link_ext(obj: str, verbose: bool) -> None:
     import torch
 
-    if os.path.exists(EXT_PATH) and os.path.getmtime(EXT_PATH) >= os.path.getmtime(obj):
+    # the object that the extension was linked from: another torch's is newer or older as it happens
+    stamp = os.path.join(OBJDIR, "_qat_torch.linked")
+    linked = ""
+    if os.path.exists(stamp):
+        with open(stamp) as f:
+            linked = f.read()
+    if (linked == os.path.basename(obj) and os.path.exists(EXT_PATH)
+            and os.path.getmtime(EXT_PATH) >= os.path.getmtime(obj)):
         return
     lib = os.path.join(os.path.dirname(torch.__file__), "lib")
     tmp = EXT_PATH + ".tmp"
     _run([shutil.which("g++") or "c++", "-shared", obj, "-o", tmp, "-L", HERE, "-l:libqat_attn.so",
           "-L", lib, "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_cuda", "-ltorch", "-ltorch_python",
           "-Wl,-rpath,$ORIGIN", f"-Wl,-rpath,{lib}"], "_qat_torch", verbose)
+    if os.path.exists(stamp):
+        os.remove(stamp)
     os.replace(tmp, EXT_PATH)
+    with open(stamp, "w") as f:
+        f.write(os.path.basename(obj))
 
 
 def _run(cmd: list[str], what: str, verbose: bool) -> None:
@@ -107,15 +128,16 @@ def _run(cmd: list[str], what: str, verbose: bool) -> None:
 
 
 def build(verbose: bool = False, ptxas_verbose: bool = False) -> str:
-    """Compile every source and link ``libqat_attn.so`` and the torch extension; returns the library's
-    path."""
+    """Compile every source and link ``libqat_attn.so``, then the torch extension, for which torch must be
+    installed (without it the library is built alone); returns the library's path."""
     os.makedirs(OBJDIR, exist_ok=True)
     extra = ["-Xptxas", "-v"] if ptxas_verbose else []
     workers = min(len(SOURCES) + 1, os.cpu_count() or 1)
     with concurrent.futures.ThreadPoolExecutor(max_workers=workers) as ex:
-        ext = ex.submit(_compile_ext, verbose or ptxas_verbose)
+        ext = None
+        if importlib.util.find_spec("torch") is not None:
+            ext = ex.submit(_compile_ext, verbose or ptxas_verbose)
         objs = list(ex.map(lambda s: _compile(s, extra, verbose or ptxas_verbose), SOURCES))
-        ext_obj = ext.result()
     newest = max(os.path.getmtime(o) for o in objs)
     if not os.path.exists(LIB_PATH) or os.path.getmtime(LIB_PATH) < newest:
         tmp = LIB_PATH + ".tmp"
@@ -124,7 +146,8 @@ def build(verbose: bool = False, ptxas_verbose: bool = False) -> str:
         if r.returncode != 0:
             raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
         os.replace(tmp, LIB_PATH)
-    _link_ext(ext_obj, verbose or ptxas_verbose)
+    if ext is not None:  # the library stands by itself, whatever becomes of the extension
+        _link_ext(ext.result(), verbose or ptxas_verbose)
     return LIB_PATH
 
 
