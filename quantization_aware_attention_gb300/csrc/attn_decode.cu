@@ -233,10 +233,15 @@ __device__ __forceinline__ int item_of(const Params& p, const Cursor& c) {
 }
 
 // The item's query rows 8 n + g as f16 times a power of two (exact for all that matters), in the order
-// of the K fragments; rf: what the scores of rows 8 n + 2t and 8 n + 2t + 1 are to be multiplied by.
+// of the K fragments; rf: what the scores of rows 8 n + 2t and 8 n + 2t + 1 are to be multiplied by, with the
+// keys' scales times `less`.  Sums of 2^31 times a key's scale leave fp32 for keys above 2^105, so the scales
+// are taken 2^-32 times and rf 2^32 times as large, unless a row's is above 2^64 (then scores of such keys do
+// not fit fp32 themselves).  What that rounds of the least scales is below 2^-20 of a score.
 template <int D, int NR>
 __device__ __forceinline__ void load_rows(const Params& p, const Cursor& c, int g, int t,
-                                          uint32_t (&qb)[NR][D / 16][2], float2 (&rf)[NR]) {
+                                          uint32_t (&qb)[NR][D / 16][2], float2 (&rf)[NR], float& less) {
+  int ex[NR];
+  bool far = false;
 #pragma unroll
   for (int n = 0; n < NR; ++n) {
     const int r = c.mt * p.rows + g + 8 * n;
@@ -268,9 +273,8 @@ __device__ __forceinline__ void load_rows(const Params& p, const Cursor& c, int 
     int e = static_cast<int>(__float_as_uint(amax) >> 23) - 127;
     e = min(max(e, -100), 126);
     const float up = __uint_as_float(static_cast<uint32_t>(127 + 14 - e) << 23);
-    const float down = fmaxf(p.a.qk_scale * __uint_as_float(static_cast<uint32_t>(127 - 14 + e) << 23),
-                             1.1754943508222875e-38f);  // not zero: it multiplies -inf
-    rf[n] = make_float2(__shfl_sync(0xffffffffu, down, 8 * t), __shfl_sync(0xffffffffu, down, 8 * t + 4));
+    ex[n] = e - 14;
+    far |= !(ldexpf(p.a.qk_scale, ex[n]) < 18446744073709551616.f);
 #pragma unroll
     for (int h = 0; h < D / 64; ++h) {
 #pragma unroll
@@ -283,6 +287,14 @@ __device__ __forceinline__ void load_rows(const Params& p, const Cursor& c, int 
         }
       }
     }
+  }
+  far = __any_sync(0xffffffffu, far);
+  less = far ? 1.f : 2.3283064365386963e-10f;
+#pragma unroll
+  for (int n = 0; n < NR; ++n) {
+    const float down = fmaxf(ldexpf(p.a.qk_scale, ex[n] + (far ? 0 : 32)),
+                             1.1754943508222875e-38f);  // not zero: it multiplies -inf
+    rf[n] = make_float2(__shfl_sync(0xffffffffu, down, 8 * t), __shfl_sync(0xffffffffu, down, 8 * t + 4));
   }
 }
 
@@ -492,6 +504,7 @@ __global__ void __launch_bounds__(32 * Cfg<D, NR>::kWarps, 1) decode_kernel(cons
   uint32_t qb[NR][KS][2];
   float o[NR][MT][4];
   float2 m[NR], l[NR], rf[NR];  // of rows 8 n + 2t and 8 n + 2t + 1
+  float less = 1.f;
   int last[NR][2];              // the newest key each of those rows sees
   float2 bound[NR];             // the rows' largest weights so far, as m is
   bool begun = false;
@@ -502,7 +515,7 @@ __global__ void __launch_bounds__(32 * Cfg<D, NR>::kWarps, 1) decode_kernel(cons
     if (!begun) {
       begun = true;
       first_tile = cc.tile;
-      load_rows<D, NR>(p, cc, g, t, qb, rf);
+      load_rows<D, NR>(p, cc, g, t, qb, rf, less);
 #pragma unroll
       for (int n = 0; n < NR; ++n) {
         m[n] = make_float2(-INFINITY, -INFINITY);
@@ -555,7 +568,7 @@ __global__ void __launch_bounds__(32 * Cfg<D, NR>::kWarps, 1) decode_kernel(cons
 #pragma unroll
         for (int y = 0; y < 2; ++y) {
           const uint32_t at = ring + kTile * D + 4 * (32 * hf + 16 * c + 8 * y + g);
-          const float ks = lds_f(at);
+          const float ks = lds_f(at) * less;
           vs[2 * hf + c][y] = lds_f(at + 4 * kTile);
 #pragma unroll
           for (int n = 0; n < NR; ++n) {

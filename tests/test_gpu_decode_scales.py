@@ -118,3 +118,21 @@ def _spread(name, n, rng):
 @pytest.mark.parametrize("quant", [0, 1])
 def test_values_of_little_weight(name, D, Hq, T, copies, quant):
     _check(_case(*_spread(name, 300, np.random.default_rng(2)), D, Hq, T, copies, 6), quant)
+
+
+@pytest.mark.parametrize("D,Hq,T", SHAPES)
+@pytest.mark.parametrize("keys,queries,sm_scale", [
+    (2.0 ** 122, 2.0 ** -90, 2.0 ** -32), (2.0 ** 122, 1.0, 2.0 ** -122), (2.0 ** 60, 2.0 ** -60, 1.0),
+    (2.0 ** -100, 2.0 ** 100, 1.0), (2.0 ** -100, 1.0, 2.0 ** 100), (2.0 ** 20, 2.0 ** 80, 2.0 ** -100),
+    (2.0 ** 100, 2.0 ** -80, 2.0 ** -20),
+])
+@pytest.mark.parametrize("quant", [0, 1])
+def test_keys_of_extreme_magnitude(D, Hq, T, keys, queries, sm_scale, quant):
+    """Scores of ordinary size from keys, queries and a scale that are not: the same bits as from ordinary ones,
+    as all are powers of two times those."""
+    rng = np.random.default_rng(3)
+    q, cache, table, lens, _, _ = _case(rng.standard_normal(300), np.ones(300), D, Hq, T, 1, 7)
+    want = qat_attention_decode(q, cache, table, lens, 1.0, quant, return_lse=True)
+    cache.k_scale.mul_(keys)
+    got = qat_attention_decode(q * queries, cache, table, lens, sm_scale, quant, return_lse=True, check=True)
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
