@@ -389,7 +389,9 @@ QAT_API qat_status_t qat_kv_cache_read(const void* k_codes, const void* v_codes,
  *   workspace  at least qat_attn_decode_workspace_bytes(Hq, Hkv, T, D) bytes (0 for invalid sizes),
  *            256-byte aligned; contents ignored on entry, unspecified on exit.  Two calls that may
  *            overlap need two workspaces.
- *   The work is split by the lengths on the device; the same lengths give the same bits.
+ *   The work is split by the lengths on the device, and the partials of a row are added in an order that
+ *   also depends on max_pages: the same sizes, max_pages and lengths give the same bits on the same GPU
+ *   type; another max_pages may round the sums differently.
  * Errors: as the cache's entries, QAT_ERR_UNSUPPORTED also for T or B above the limits or more than
  *   2^30 64-key tiles; QAT_ERR_WORKSPACE.  Pages outside the cache give NaN rows (see above).
  */

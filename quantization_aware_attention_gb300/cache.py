@@ -92,7 +92,8 @@ def qat_attention_decode(q, cache: KVCache, block_table, seq_lens, sm_scale: flo
     their own keys and values already: token t is position seq_lens[b] - T + t and sees the keys up to
     its own.  Hq is a multiple of the cache's heads (consecutive query heads share one); T is at most
     16.  Returns o bf16 [B, Hq, T, D], and with ``return_lse`` the base-2 log-sum-exp fp32 [B, Hq, T].
-    A row that sees no key gives o = 0, lse = -inf.  ``workspace``: uint8, at least
+    A row that sees no key gives o = 0, lse = -inf.  The same shapes and lengths give the same bits; a
+    block table of another width may round differently.  ``workspace``: uint8, at least
     ``capi.qat_attn_decode_workspace_bytes(Hq, cache.heads, T, D)`` bytes, for one call at a time;
     allocated if None."""
     if not isinstance(cache, KVCache):

@@ -30,8 +30,8 @@
 // the item's unit, warps that got many short sequences ended last: 64 sequences of 129 to 8192 keys, 3
 // tokens, 64 channels, 104 against 87 us.)  An item inside one range is finished there; an item cut by a
 // range boundary leaves unnormalized fp32 partials with their m and l in the workspace, which
-// the merge kernels add in an order that the lengths alone decide (no atomics: the same lengths give
-// the same bits).
+// the merge kernels add in an order that the sizes, the table's width and the lengths decide (no atomics: the
+// same ones give the same bits; the width bounds the lengths on the host, which chooses the merge by it).
 //
 // Products: mma.sync m16n8k16 with f16 operands and fp32 sums, the cache as the 16-row operand and
 // the query rows as the 8 columns (one column tile for up to 8 rows, else two): S^T = K Q^T and

@@ -1,5 +1,5 @@
 """Calls at the edges of what the norm + rotation, the cache and decoding take: several host threads, tensors
-without heads, derivatives that are not there, wrappers, a captured backward."""
+without heads, derivatives that are not there, wrappers, a captured backward, wide tables."""
 
 import gc
 import sys
@@ -10,6 +10,7 @@ import pytest
 import torch
 import torch.autograd.forward_ad as fwad
 
+from oracle import serving_oracle as so
 from quantization_aware_attention_gb300 import (KVCache, RopePlan, qat_attention_decode, qat_qk_norm_rope,
                                                 qat_qk_norm_rope_backward)
 from quantization_aware_attention_gb300 import build as qbuild
@@ -17,7 +18,7 @@ from quantization_aware_attention_gb300 import capi
 from quantization_aware_attention_gb300.capi import Status
 from quantization_aware_attention_gb300.inputs import normal_bf16
 
-from gpu_util import dev_bf16
+from gpu_util import dev_bf16, host_f64
 
 pytestmark = pytest.mark.gpu
 
@@ -214,3 +215,29 @@ def test_a_captured_backward_beside_a_living_eager_graph_of_a_projection(alive):
         got = torch.autograd.grad(forward(project()), (big, w), g)
     graph.replay()
     assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
+@pytest.mark.parametrize("n,Hkv,T", [(500, 8, 1), (1100, 2, 2), (3000, 1, 3)])
+def test_the_same_lengths_in_tables_of_different_widths(n, Hkv, T):
+    """A block table that could hold far longer sequences changes the order in which partials are added, and no
+    more: every width gives rows within the oracle's tolerance, and its own bits again; entries behind the
+    sequence's end are never followed."""
+    D, G, page = 64, 4, 16
+    per = -(-n // page)
+    k, v = (dev_bf16(normal_bf16(60 + i, (1, Hkv, n, D))) for i in range(2))
+    q = dev_bf16(normal_bf16(62, (1, Hkv * G, T, D)))
+    cache = KVCache.empty(per, Hkv, page, D)
+    narrow = torch.randperm(per, device="cuda", dtype=torch.int32)[None]
+    cache.append(k, v, narrow, _i32([n]), check=True)
+    kk, vv = (so.dequant(*so.quant_row(host_f64(x)[0])) for x in (k, v))
+    for width in (per, 4 * per, 8192):
+        table = torch.full((1, width), -1, dtype=torch.int32, device="cuda")
+        table[:, :per] = narrow
+        o, lse = qat_attention_decode(q, cache, table, _i32([n]), return_lse=True, check=True)
+        for h in range(Hkv * G):
+            w, wl, tol, ltol = so.decode_head(host_f64(q)[0, h], kk[h // G], vv[h // G], n - T + np.arange(T),
+                                              D ** -0.5, 1)
+            assert (np.abs(host_f64(o)[0, h] - w) <= tol).all()
+            assert (np.abs(host_f64(lse)[0, h] - wl) <= ltol).all()
+        again = qat_attention_decode(q, cache, table, _i32([n]), return_lse=True)
+        assert torch.equal(o, again[0]) and torch.equal(lse, again[1])
