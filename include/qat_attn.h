@@ -297,7 +297,7 @@ QAT_API qat_status_t qat_subtract_mean(const void* x, const float* mean, void* o
  *   q_weight, k_weight  [D] fp32, or bf16 with weight_bf16 = 1 (device, 16-byte aligned):
  *            z = x rsqrt(mean_d x_d^2 + eps) weight.  Both NULL: no norm, z = x.
  *   eps      finite, > 0.
- * Everything is computed in fp32 and rounded once, on the store.
+ * Everything is computed in fp32 (sine and cosine to 2^-20) and rounded once, on the store.
  * Errors: QAT_ERR_INVALID_ARG, QAT_ERR_CUDA.
  */
 QAT_API qat_status_t qat_qk_norm_rope(
@@ -311,8 +311,8 @@ QAT_API qat_status_t qat_qk_norm_rope(
  * qat_qk_norm_rope_bwd -- the gradients of qat_qk_norm_rope.
  *   dq_out, dk_out  bf16 [B, H, N, D] with strides as above: gradients of its outputs
  *   dq, dk     bf16 [B, H, N, D] OUT, with strides as above (no two elements may share memory)
- *   dq_weight, dk_weight  [D] OUT in the weights' type, or NULL.  Summed in a fixed order: the
- *            same sizes give the same bits.
+ *   dq_weight, dk_weight  [D] OUT in the weights' type, or NULL.  Summed in fp32 in a fixed order:
+ *            the same sizes give the same bits on the same GPU type.
  *   workspace  at least qat_qk_norm_rope_bwd_workspace_bytes(D) bytes, 256-byte aligned; not
  *            used without weights.
  *   Other arguments as in the forward.  No rows (B, N, or both Hq and Hk zero): the weights'
@@ -381,8 +381,12 @@ QAT_API qat_status_t qat_kv_cache_read(const void* k_codes, const void* v_codes,
  *   o        bf16 [B, Hq, T, D] OUT
  *   lse      fp32 [B, Hq, T] OUT or NULL: base-2 log-sum-exp, as in qat_attn_fwd
  *   quant_mode  QAT_QUANT_NONE or QAT_QUANT_P_FP8E4M3_ROW_TILE64 (the forward's rule, with tiles of
- *            64 absolute positions; a tile whose largest p is below 2^-100 of the row's counts as
+ *            64 absolute positions; a tile whose largest p is below 2^-100 of the row's may count as
  *            zeros)
+ *   Roundings: each weight, p (quantized or not) times its value's scale, is an f16 operand of the product
+ *            with V, off by up to 2^-11 of itself, or by 2^-38 of the row's largest weight if that is more;
+ *            an element of q below 2^-32 of its row's largest loses bits; scores and sums are fp32, and
+ *            have to fit it.
  *   A row that sees no key (position < 0) gets o = 0 and lse = -inf.
  *   Only keys that a row sees can reach its output: what lies behind the sequence's end in its last
  *   page, or in newer tokens' rows, may be anything the append can have stored, NaN rows included.

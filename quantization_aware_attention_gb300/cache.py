@@ -73,7 +73,8 @@ class KVCache:
         """Quantizes new keys and values, bf16 [B, H, N, D] with any strides that have D innermost,
         into their pages.  ``seq_lens`` are the lengths after the append: row n of sequence b goes to
         position seq_lens[b] - N + n, or, with int32 ``new_lens`` [B], to seq_lens[b] - new_lens[b] + n
-        for its first new_lens[b] rows (the others are padding).  No two rows may go to one slot."""
+        for its first new_lens[b] rows (the others are padding; a new_lens above N counts as N).  Rows
+        whose position would be negative are dropped.  No two rows may go to one slot."""
         capi.torch_ops().kv_append(self._k, self._v, self._k_scale, self._v_scale, k, v, block_table,
                                    seq_lens, new_lens, check)
 

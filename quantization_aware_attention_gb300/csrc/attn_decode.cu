@@ -12,10 +12,12 @@
 // as soon as it is used (smaller pieces, more of them in flight, took 1 to 7 percent longer); no barrier
 // between warps, and all G = Hq / Hkv heads that share a KV head (times T tokens) are rows of one item
 // of 8 or 16 rows, so that the cache is read once for all of them (once for each 16 beyond that).
-// Measured, 8 KV heads, quantized:
-//   D 128, 32 query heads, 1 token, 64 sequences of 129 to 8192 keys     96 us, 5.9 TB/s of codes and scales
-//   D 128, 40 query heads, 1 token, 2 sequences of 250001 and 262144    171 us, 6.3 TB/s
+// Measured, 8 KV heads, quantized, in a captured graph:
+//   D 128, 32 query heads, 1 token, 64 sequences of 129 to 8192 keys     95 us, 5.9 TB/s of codes and scales
+//   D 128, 40 query heads, 1 token, 2 sequences of 250001 and 262144    169 us, 6.4 TB/s
 //   D 64,  32 query heads, 3 tokens, 64 sequences of 129 to 8192         65 us, 4.5 TB/s: issue and latency
+//                                                                        (its 168 registers spill 4 bytes,
+//                                                                        56 where P is not quantized)
 //   D 128, 32 query heads, 1 token, one sequence of 1537 keys           9.4 us: two launches and their chains
 //                                                                        of loads (prefix sums 1.1 us, table
 //                                                                        and first copies 2.3, data 2 to 4,
@@ -40,9 +42,11 @@
 // q (bf16) is brought into f16 by a power of two per row, which is exact for every element above 2^-32
 // of the row's largest.  The weights, P times the values' scales, are rounded to f16: by 2^-11 of
 // themselves, as each row's are multiplied by a power of two that follows its largest weight so far
-// (to about 2^14; what is below 2^-28 of the row's largest is off by 2^-39 of it).  With so few rows these products need a
-// tenth of the tensor rate, and a 128-row tcgen05 tile would want the codes of V transposed and P in
-// 8 bits with a scale per key; the memory pipeline is what has to be fed.
+// (to about 2^14; what is below 2^-28 of the row's largest is off by 2^-39 of it).  Following each row's weights
+// costs nothing where HBM bounds and 1 to 2 percent where issue does, against one bound for all scales of a
+// tile, which lost the weights of rows that do not see, or hardly weigh, a value 2^28 times as large.
+// With so few rows these products need a tenth of the tensor rate, and a 128-row tcgen05 tile would want the
+// codes of V transposed and P in 8 bits with a scale per key; the memory pipeline is what has to be fed.
 //
 // Operand layout: the order of d in Q K^T and of the output rows in V^T P^T is free, so each lane
 // (g = lane / 4, t = lane % 4) takes 16-byte runs of a row: for K chunk t + 4 h of keys g and g + 8

@@ -16,7 +16,7 @@
 // channels 8 j .. 8 j + 7 and the same of the row's second half, so that every load and store of a row
 // is one run of whole sectors: 16 bytes a lane of bf16, 8 bytes of codes.  Keys and values of a row are
 // handled by the same lanes, which keeps four loads in flight each.  HBM bounds both.  Measured, D = 128:
-//   append  8 sequences' prompts of 1000 to 8192 tokens, 8 heads   35.5 us, 6.4 TB/s
+//   append  8 sequences' prompts of 1000 to 8192 tokens, 8 heads   36.3 us, 6.3 TB/s
 //   read    6 sequences' prefixes of 9000 to 32768 tokens, 8 heads  158 us, 6.8 TB/s
 //   append of one token to each of 64 sequences                     2.1 us: a launch and its chain of loads
 // (Tiles of 8 tokens by 4 or 8 heads, which read a token's heads as one run, made append 5 percent slower.)

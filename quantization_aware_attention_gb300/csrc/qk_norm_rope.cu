@@ -14,7 +14,7 @@
 // reduction that 32-bit angles lose (at position 10^6 an fp32 angle is off by 0.06 rad)
 // costs two integer multiplies, and no table of cosines is read.  The fraction's top 32 bits
 // become an angle in [-pi, pi), where the hardware sine and cosine are within 2^-20 absolute;
-// the outputs round to bf16 (2^-9 relative).
+// the outputs round to bf16 (by up to 2^-8 of themselves).
 //
 // Work split.  D / 16 lanes hold one row, 16 channels each as two 16-byte chunks chosen so that both
 // halves of every pair are in one lane; a warp holds 4 rows (D = 128) or 8 (D = 64) of one token,
@@ -28,9 +28,13 @@
 // registers, no barriers.  Arithmetic is in packed fp32 pairs.  Measured, D = 128, full rotation, norms:
 //   B1 H40+40 N32768   forward 197 us, 6.8 TB/s of the 4 bytes a channel read and written
 //   B4 H32+32 N8192    forward 158 us, 6.8 TB/s; backward 236 us, 6.8 TB/s of 6 bytes a channel
-//   B1 H32+8 N2048     forward 10.3 us, backward 20; B16 N1 2.4 us
-// With few heads (D = 64, 3+1 heads, 200000 tokens: 71 us, 2.9 TB/s) the sines and cosines of a token are
-// shared by few rows and bound it.
+//   B1 H32+8 N2048     forward 10.6 us, backward 20; B16 N1 2.4 us
+// Few heads (D = 64, 3+1 heads, 200000 tokens): forward 71 us, 2.9 TB/s, 61 without the rotation as without the
+// norm.  A warp makes one trip of 8 rows and ends: 520 instructions with its start, angles and weights, 74 percent
+// of the issue slots.  Backward 112 us, 88 without norm and weights.
+// Backward of small sizes (B1 H32+8 N2048): 20 us, 12 without norm and weights; what the sums' second launch,
+// each block's start and its sums take of the rest has not been told apart.
+// The forward is held to 64 registers, for four blocks an SM, and spills 4 to 40 bytes a thread.
 #include "qat_internal.h"
 #include "qat_quant.cuh"
 #include "sm100.cuh"

@@ -4,7 +4,7 @@
 //
 // These calls are made once per layer and decoding step, on a few microseconds of GPU work, so what the
 // host spends on them is what they cost; in Python it was two to three times as much (a decode call on one
-// sequence 28 us, a training pass of the norm + rotation through autograd 310).
+// sequence 28 us, a training pass of the norm + rotation through autograd 300).
 #include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/custom_function.h>
 #include <torch/csrc/autograd/graph_task.h>

@@ -104,10 +104,10 @@ def qat_qk_norm_rope(q, k=None, positions=None, rope: RopePlan | None = None, q_
 
     The inputs may have any strides with D innermost and rows on 16-byte boundaries: a slice of a
     fused projection, ``x.view(B, N, H, D).transpose(1, 2)``, is read in place.  Differentiable in q,
-    k and the weights (once: there is no second derivative); the gradients are deterministic, those of
-    q and k in the inputs' order in memory.  Nothing but the inputs is saved for the backward.  Forward and
-    backward can be captured into a CUDA graph; while a graph of the same leaves made on the default stream
-    lives, that is refused."""
+    k and the weights (once: there is no second derivative, and no forward-mode one); the gradients are
+    deterministic, those of q and k in the inputs' order in memory.  Nothing but the inputs is saved for the
+    backward.  Forward and backward can be captured into a CUDA graph; while a graph made on the default
+    stream lives that ends in the same leaves, or that the backward passes through, that is refused."""
     phases, rotary_dim, interleaved, amplitude = _plan(rope)
     return capi.torch_ops().norm_rope(q, k, positions, phases, q_weight, k_weight, rotary_dim,
                                       interleaved, amplitude, eps)
