@@ -408,6 +408,96 @@ QAT_API qat_status_t qat_attn_decode(const void* q, const void* k_codes, const v
                                      int quant_mode, void* workspace, size_t workspace_bytes,
                                      void* stream);
 
+/*
+ * qat_attn_fwd_window, qat_attn_bwd_window -- qat_attn_fwd and qat_attn_bwd, causal, with a sliding window and
+ * sinks: query i sees key j if j <= i and (j > i - window or j < sinks).  No counterpart on the pages.
+ *   N        queries and keys;  N <= 2^30
+ *   window   >= 1; the query's own key counts, so 1 leaves it alone (and the sinks); N or more: no window
+ *   sinks    >= 0, the first keys, which every later query goes on seeing
+ *   k_mean   fp32 [D] or NULL, as in qat_attn_bwd_smooth_k
+ *   everything else as in qat_attn_fwd and qat_attn_bwd with Nq = Nkv = N and causal 1.  Tiles of the
+ *   quantization are the same absolute 64 keys; a tile's amax is that of the keys that the row sees.
+ *   The work follows the pairs that are seen, in blocks of 128 x 128.  The sums of dK and dV of sinks may be cut
+ *   into pieces, kept in the workspace and added in order; results are deterministic.
+ *   Values of keys (queries) that share a 128-block with seen ones are multiplied by zero: they must be finite.
+ * Errors: as qat_attn_fwd and qat_attn_bwd; QAT_ERR_INVALID_ARG also for window < 1 or sinks < 0,
+ *   QAT_ERR_UNSUPPORTED for N > 2^30.
+ */
+QAT_API qat_status_t qat_attn_fwd_window(const void* q, const void* k, const void* v, void* o_q, void* o_hp,
+                                         float* lse, int B, int H, int N, int D, float sm_scale, int window,
+                                         int sinks, int quant_mode, void* stream);
+QAT_API size_t qat_attn_bwd_window_workspace_bytes(int B, int H, int N, int D, int window, int sinks);
+QAT_API qat_status_t qat_attn_bwd_window(const void* q, const void* k, const void* v, const void* o_hp,
+                                         const float* lse, const void* dO, void* dq, void* dk, void* dv,
+                                         const float* k_mean, int B, int H, int N, int D, float sm_scale, int window,
+                                         int sinks, int quant_mode, void* workspace, size_t workspace_bytes,
+                                         void* stream);
+
+/*
+ * qat_attn_decode_window -- qat_attn_decode with a sliding window and sinks, by absolute positions: the token
+ *   at position i sees key j if j <= i and (j > i - window or j < sinks).  window >= 1, sinks >= 0.
+ *   What no token sees is not read, and pages that hold nothing else are not looked up: their entries in the
+ *   block table may be anything.  Everything else as qat_attn_decode, its workspace included.
+ */
+QAT_API qat_status_t qat_attn_decode_window(const void* q, const void* k_codes, const void* v_codes,
+                                            const float* k_scales, const float* v_scales, const int* block_table,
+                                            const int* seq_lens, void* o, float* lse, int B, int Hq, int Hkv, int T,
+                                            int D, int num_pages, int page_size, int max_pages, float sm_scale,
+                                            int window, int sinks, int quant_mode, void* workspace,
+                                            size_t workspace_bytes, void* stream);
+
+/*
+ * qat_attn_tree -- attention of each sequence's last T tokens, a drafted tree, over the FP8 cache.
+ *   q        bf16 [B, Hq, T, D]: token t of sequence b lies in slot seq_lens[b] - T + t of the cache
+ *   tree     u64: bit s of tree[b tree_stride + t] says that token t sees token s (itself included, where its own
+ *            bit is set); bits from T on, and of slots before the sequence's first, are ignored.  A tree_stride of
+ *            0 gives all sequences one tree.  Every token sees the whole text before the tree.
+ *   T        1 .. 64 (0: nothing to do)
+ *   window   0: none (then sinks is 0); else a key j before the tree also needs j > i - window or
+ *            j < sinks, with i = seq_lens[b] - T + popcount(mask) - 1, the token's position by its depth; tokens
+ *            of the tree are seen by their bits alone
+ *   everything else as qat_attn_decode; workspace of qat_attn_tree_workspace_bytes(Hq, Hkv, T, D) bytes.
+ */
+QAT_API size_t qat_attn_tree_workspace_bytes(int Hq, int Hkv, int T, int D);
+QAT_API qat_status_t qat_attn_tree(const void* q, const void* k_codes, const void* v_codes, const float* k_scales,
+                                   const float* v_scales, const int* block_table, const int* seq_lens,
+                                   const unsigned long long* tree, long long tree_stride, void* o, float* lse, int B,
+                                   int Hq, int Hkv, int T, int D, int num_pages, int page_size, int max_pages,
+                                   float sm_scale, int window, int sinks, int quant_mode, void* workspace,
+                                   size_t workspace_bytes, void* stream);
+
+/*
+ * qat_draft_tree -- masks and positions of drafted trees from the tokens' parents.
+ *   parents   int32, sequence b's T from parents + b parents_stride (stride 0: one tree for all): the token that t
+ *             continues, which comes before it, or -1 for the text.  Anything else marks t as padding, and
+ *             what continues it too.
+ *   seq_lens  int32 [B], lengths with the T tokens, as for the cache's entries
+ *   tree      u64 [B, T] OUT: bit t and the bits of t's ancestors; 0 for padding
+ *   positions int32 [B, T] OUT: seq_lens[b] - T + popcount(tree) - 1 (padding: the text's last)
+ *   T         at most 64
+ * Errors: QAT_ERR_INVALID_ARG, QAT_ERR_UNSUPPORTED (T > 64), QAT_ERR_CUDA.
+ */
+QAT_API qat_status_t qat_draft_tree(const int* parents, long long parents_stride, const int* seq_lens,
+                                    unsigned long long* tree, int* positions, int B, int T, void* stream);
+
+/*
+ * qat_kv_cache_keep -- after drafted tokens were checked: moves the accepted ones' rows behind the text.
+ *   seq_lens  lengths with the T drafted tokens;  path int32 [B, L]: drafted token path[b][i] becomes the i-th
+ *             after the text, for i < path_lens[b] (above L counts as L, below 0 as 0)
+ *   new_lens  int32 [B] OUT: seq_lens[b] - T + kept, not below 0; must not be seq_lens or path_lens
+ *   Rows move as if all were read before one is written: any order, and a token may be named twice.  Rows to or
+ *   from positions before 0 are left out.  Every other slot of the cache stays as it was, the kept tokens' old ones
+ *   included where nothing else moves there.  A path entry outside [0, T), and rows on pages outside the cache,
+ *   are not moved and reported by qat_attn_device_status (QAT_ERR_BAD_PAGE).  Pages that take a row must not be
+ *   shared between sequences.
+ *   T <= 64, L <= T.
+ * Errors: as the cache's entries; QAT_ERR_UNSUPPORTED also for T > 64 or L > T.
+ */
+QAT_API qat_status_t qat_kv_cache_keep(void* k_codes, void* v_codes, float* k_scales, float* v_scales,
+                                       const int* block_table, const int* seq_lens, const int* path,
+                                       const int* path_lens, int* new_lens, int B, int H, int T, int L, int D,
+                                       int num_pages, int page_size, int max_pages, void* stream);
+
 /* Static, human-readable name of a status code (never NULL). */
 QAT_API const char* qat_status_string(qat_status_t status);
 

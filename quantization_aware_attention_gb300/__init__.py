@@ -13,4 +13,5 @@ from .attention import (QATAttention, attention, check_device_status,  # noqa: F
                         qat_attention_backward, qat_attention_forward, qat_prepare_qkv,
                         qat_subtract_mean)
 from .rope import RopePlan, qat_qk_norm_rope, qat_qk_norm_rope_backward  # noqa: F401
-from .cache import KVCache, qat_attention_decode  # noqa: F401
+from .cache import (KVCache, qat_attention_decode, qat_attention_tree,  # noqa: F401
+                    qat_draft_tree)

@@ -12,6 +12,7 @@ _attention.forward saves q, k, v, O and M).
 from __future__ import annotations
 
 import math
+import operator
 import os
 
 import torch
@@ -63,17 +64,39 @@ def check_device_status(what: str = "QAT attention") -> None:
     _raise(capi.qat_attn_device_status(), what)
 
 
+def _window(causal, window, sinks):
+    """(window, sinks) as the library takes them, or None without a window."""
+    if window is None:
+        if sinks != 0:
+            raise ValueError("sinks go together with a window")
+        return None
+    window, sinks = operator.index(window), operator.index(sinks)
+    if window < 1 or sinks < 0:
+        raise ValueError(f"window must be at least 1 and sinks at least 0, got {window} and {sinks}")
+    if not causal:
+        raise ValueError("a window is one of causal attention: pass causal=True")
+    return min(window, 1 << 30), min(sinks, 1 << 30)
+
+
 def qat_attention_forward(q, k, v, causal: bool = False, sm_scale: float | None = None,
-                          quant_mode: int = capi.QUANT_P_FP8E4M3_ROW_TILE64):
-    """Returns (o_q, o_hp, lse): bf16 [B,H,Nq,D], bf16 [B,H,Nq,D], fp32 [B,H,Nq] (base 2)."""
+                          quant_mode: int = capi.QUANT_P_FP8E4M3_ROW_TILE64, window: int | None = None,
+                          sinks: int = 0):
+    """Returns (o_q, o_hp, lse): bf16 [B,H,Nq,D], bf16 [B,H,Nq,D], fp32 [B,H,Nq] (base 2).  ``window`` and
+    ``sinks``: see ``attention``."""
+    win = _window(causal, window, sinks)
     B, H, Nq, Nkv, D = _dims(q, k, v)
     sm_scale = 1.0 / math.sqrt(D) if sm_scale is None else float(sm_scale)
     o_q = torch.empty_like(q)
     o_hp = torch.empty_like(q)
     lse = torch.empty((B, H, Nq), dtype=torch.float32, device=q.device)
+    if win is not None and Nq != Nkv:
+        raise ValueError(f"a window needs as many keys as queries, got {Nkv} and {Nq}")
     with torch.cuda.device(q.device):
-        st = capi.qat_attn_fwd(q, k, v, o_q, o_hp, lse, B, H, Nq, Nkv, D, sm_scale,
-                               int(causal), quant_mode)
+        if win is not None:
+            st = capi.qat_attn_fwd_window(q, k, v, o_q, o_hp, lse, B, H, Nq, D, sm_scale, *win, quant_mode)
+        else:
+            st = capi.qat_attn_fwd(q, k, v, o_q, o_hp, lse, B, H, Nq, Nkv, D, sm_scale,
+                                   int(causal), quant_mode)
     _raise(st, "qat_attn_fwd")
     return o_q, o_hp, lse
 
@@ -82,11 +105,13 @@ def qat_attention_backward(q, k, v, o_hp, lse, do, causal: bool = False,
                            sm_scale: float | None = None,
                            quant_mode: int = capi.QUANT_P_FP8E4M3_ROW_TILE64,
                            workspace: torch.Tensor | None = None,
-                           k_mean: torch.Tensor | None = None):
+                           k_mean: torch.Tensor | None = None, window: int | None = None,
+                           sinks: int = 0):
     """Returns (dq, dk, dv) of L = <dO, O_hp> (straight-through estimator; quant_mode 2:
     the page's backward, with the forward's O_q passed as ``o_hp``).  With ``k_mean``
     (fp32 [D], smooth_k's channel mean; k is the smoothed key) dQ gets the page's
-    SMOOTH_K term."""
+    SMOOTH_K term.  ``window`` and ``sinks`` as in the forward."""
+    win = _window(causal, window, sinks)
     B, H, Nq, Nkv, D = _dims(q, k, v)
     _check(o_hp, "o_hp", (B, H, Nq, D))
     _check(do, "do", (B, H, Nq, D))
@@ -94,14 +119,22 @@ def qat_attention_backward(q, k, v, o_hp, lse, do, causal: bool = False,
     if k_mean is not None:
         _check(k_mean, "k_mean", (D,), torch.float32)
     sm_scale = 1.0 / math.sqrt(D) if sm_scale is None else float(sm_scale)
-    ws_bytes = capi.qat_attn_bwd_workspace_bytes(B, H, Nq, Nkv, D)
+    if win is not None and Nq != Nkv:
+        raise ValueError(f"a window needs as many keys as queries, got {Nkv} and {Nq}")
+    if win is not None:
+        ws_bytes = capi.qat_attn_bwd_window_workspace_bytes(B, H, Nq, D, *win)
+    else:
+        ws_bytes = capi.qat_attn_bwd_workspace_bytes(B, H, Nq, Nkv, D)
     if workspace is None:
         workspace = torch.empty(max(ws_bytes, 256), dtype=torch.uint8, device=q.device)
     dq = torch.empty_like(q)
     dk = torch.empty_like(k)
     dv = torch.empty_like(v)
     with torch.cuda.device(q.device):
-        if k_mean is None:
+        if win is not None:
+            st = capi.qat_attn_bwd_window(q, k, v, o_hp, lse, do, dq, dk, dv, k_mean, B, H, Nq, D, sm_scale, *win,
+                                          quant_mode, workspace, workspace.numel())
+        elif k_mean is None:
             st = capi.qat_attn_bwd(q, k, v, o_hp, lse, do, dq, dk, dv, B, H, Nq, Nkv, D,
                                    sm_scale, int(causal), quant_mode, workspace,
                                    workspace.numel())
@@ -150,7 +183,7 @@ class QATAttention(torch.autograd.Function):
     @staticmethod
     def forward(ctx, q, k, v, causal=False, sm_scale=None,
                 quant_mode=capi.QUANT_P_FP8E4M3_ROW_TILE64, qkv_quant=False, smooth_k=False,
-                use_qat_qkv_backward=True, check=None):
+                use_qat_qkv_backward=True, check=None, window=None, sinks=0):
         k_mean = None
         q_bwd, k_bwd, v_bwd = q, k, v
         if qkv_quant:  # attention runs on fake-quantized inputs; gradients pass straight
@@ -165,7 +198,7 @@ class QATAttention(torch.autograd.Function):
         elif not use_qat_qkv_backward:
             raise ValueError("use_qat_qkv_backward=False applies only together with qkv_quant")
         ctx.check = _check_enabled(check)
-        o_q, o_hp, lse = qat_attention_forward(q, k, v, causal, sm_scale, quant_mode)
+        o_q, o_hp, lse = qat_attention_forward(q, k, v, causal, sm_scale, quant_mode, window, sinks)
         if ctx.check:
             check_device_status("qat_attn_fwd")
         # the page's backward variant forms Delta from O_q, the straight-through one from O_hp
@@ -173,6 +206,7 @@ class QATAttention(torch.autograd.Function):
         saved = (q_bwd, k_bwd, v_bwd, o_bwd, lse) + ((k_mean,) if k_mean is not None else ())
         ctx.save_for_backward(*saved)
         ctx.causal, ctx.sm_scale, ctx.quant_mode = causal, sm_scale, quant_mode
+        ctx.window, ctx.sinks = window, sinks
         return o_q
 
     @staticmethod
@@ -180,16 +214,17 @@ class QATAttention(torch.autograd.Function):
         q, k, v, o_bwd, lse, *rest = ctx.saved_tensors
         k_mean = rest[0] if rest else None
         dq, dk, dv = qat_attention_backward(q, k, v, o_bwd, lse, do.contiguous(), ctx.causal,
-                                            ctx.sm_scale, ctx.quant_mode, k_mean=k_mean)
+                                            ctx.sm_scale, ctx.quant_mode, k_mean=k_mean,
+                                            window=ctx.window, sinks=ctx.sinks)
         if ctx.check:
             check_device_status("qat_attn_bwd")
-        return dq, dk, dv, None, None, None, None, None, None, None
+        return dq, dk, dv, None, None, None, None, None, None, None, None, None
 
 
 def attention(q, k, v, causal: bool = False, sm_scale: float | None = None,
               quant_mode: int = capi.QUANT_P_FP8E4M3_ROW_TILE64, qkv_quant: bool = False,
               smooth_k: bool = False, use_qat_qkv_backward: bool = True,
-              check: bool | None = None):
+              check: bool | None = None, window: int | None = None, sinks: int = 0):
     """QAT attention: the quantized output O_q, differentiable (straight-through; the
     page's own backward with quant_mode 2).
 
@@ -199,6 +234,9 @@ def attention(q, k, v, causal: bool = False, sm_scale: float | None = None,
     the unquantized q, k - k_mean and v, as the page's option of that name does.
     check=True (or QAT_CHECK_STATUS=1 in the environment) synchronizes after the forward
     and the backward and raises QatError if a kernel's bounded wait expired, so that a
-    call cut short is never consumed silently."""
+    call cut short is never consumed silently.
+    window (causal only): query i sees key j if j <= i and (j > i - window or j < sinks), a
+    sliding window beside which the first ``sinks`` keys stay visible; forward and backward
+    take work in proportion to what is seen."""
     return QATAttention.apply(q, k, v, causal, sm_scale, quant_mode, qkv_quant, smooth_k,
-                              use_qat_qkv_backward, check)
+                              use_qat_qkv_backward, check, window, sinks)

@@ -86,9 +86,21 @@ class KVCache:
                                         seq_lens, begin, length, check)
 
 
+    def keep(self, block_table, seq_lens, drafted: int, path, path_lens, check: bool | None = None):
+        """After the last ``drafted`` tokens of each sequence were checked: moves the accepted ones' rows behind
+        the text before them.  ``path`` (int32 [B, L], L <= drafted <= 64) names drafted tokens in their order in
+        the text, the first ``path_lens[b]`` (int32 [B]) of them accepted.  Returns the new lengths, int32
+        [B]: seq_lens - drafted + accepted, not below 0.  Rows move as if all were read before one is written; every
+        other slot stays as it was.  Entries outside [0, drafted) are not moved and reported as bad
+        pages are."""
+        return capi.torch_ops().kv_keep(self._k, self._v, self._k_scale, self._v_scale, block_table, seq_lens,
+                                        drafted, path, path_lens, check)
+
+
 def qat_attention_decode(q, cache: KVCache, block_table, seq_lens, sm_scale: float | None = None,
                          quant_mode: int = capi.QUANT_P_FP8E4M3_ROW_TILE64, return_lse: bool = False,
-                         workspace: torch.Tensor | None = None, check: bool | None = None):
+                         workspace: torch.Tensor | None = None, check: bool | None = None,
+                         window: int | None = None, sinks: int = 0):
     """Attention of each sequence's last T tokens, q bf16 [B, Hq, T, D], over the cache, which holds
     their own keys and values already: token t is position seq_lens[b] - T + t and sees the keys up to
     its own.  Hq is a multiple of the cache's heads (consecutive query heads share one); T is at most
@@ -96,8 +108,41 @@ def qat_attention_decode(q, cache: KVCache, block_table, seq_lens, sm_scale: flo
     A row that sees no key gives o = 0, lse = -inf.  The same shapes and lengths give the same bits; a
     block table of another width may round differently.  ``workspace``: uint8, at least
     ``capi.qat_attn_decode_workspace_bytes(Hq, cache.heads, T, D)`` bytes, for one call at a time;
-    allocated if None."""
+    allocated if None.  ``window``: the token at position i sees only keys j > i - window, and the
+    first ``sinks`` keys; nothing else is read, and block table entries of pages that no token sees may be
+    anything."""
     if not isinstance(cache, KVCache):
         raise TypeError("cache must be a KVCache")
     return capi.torch_ops().decode(cache._k, cache._v, cache._k_scale, cache._v_scale, q, block_table,
-                                   seq_lens, sm_scale, quant_mode, return_lse, workspace, check)
+                                   seq_lens, None, sm_scale, quant_mode, return_lse, workspace, check, window,
+                                   sinks)
+
+
+def qat_attention_tree(q, cache: KVCache, block_table, seq_lens, tree, sm_scale: float | None = None,
+                       quant_mode: int = capi.QUANT_P_FP8E4M3_ROW_TILE64, return_lse: bool = False,
+                       workspace: torch.Tensor | None = None, check: bool | None = None,
+                       window: int | None = None, sinks: int = 0):
+    """Attention of a tree of drafted tokens, q bf16 [B, Hq, T, D] with T up to 64, over the cache: the last T
+    slots of each sequence hold their keys and values (appended as they come, seq_lens with them), and
+    ``tree`` (int64 [B, T], or [T] for all sequences; from ``qat_draft_tree``) says which of them each token sees:
+    bit s of tree[b, t] for token s.  Every token sees the whole text before the tree; with ``window``, only keys
+    j > i - window of it, and the first ``sinks``, i being the token's position by its depth, seq_lens[b] - T +
+    popcount - 1 (the tree itself is seen by its bits alone).  Everything else as
+    ``qat_attention_decode``; the workspace has ``capi.qat_attn_tree_workspace_bytes(Hq, cache.heads, T, D)``
+    bytes."""
+    if not isinstance(cache, KVCache):
+        raise TypeError("cache must be a KVCache")
+    if not isinstance(tree, torch.Tensor):
+        raise TypeError("tree must be a torch.Tensor")
+    return capi.torch_ops().decode(cache._k, cache._v, cache._k_scale, cache._v_scale, q, block_table,
+                                   seq_lens, tree, sm_scale, quant_mode, return_lse, workspace, check, window,
+                                   sinks)
+
+
+def qat_draft_tree(parents, seq_lens):
+    """(tree, positions) of drafted trees: ``parents`` int32 [B, T] or [T], T up to 64, names for each token the
+    earlier one that it continues, -1 for the text (anything else: padding, as is what continues it).  tree
+    int64 [B, T] holds each token's own bit and its ancestors' (0 for padding), for ``qat_attention_tree``;
+    positions int32 [B, T] are seq_lens - T + depth, for ``qat_qk_norm_rope``.  ``seq_lens`` (int32 [B]) count the
+    T tokens, as for the cache."""
+    return capi.torch_ops().draft_tree(parents, seq_lens)

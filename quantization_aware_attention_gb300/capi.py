@@ -40,6 +40,14 @@ EXPORTED = (
     "qat_kv_cache_read",
     "qat_attn_decode_workspace_bytes",
     "qat_attn_decode",
+    "qat_attn_fwd_window",
+    "qat_attn_bwd_window_workspace_bytes",
+    "qat_attn_bwd_window",
+    "qat_attn_decode_window",
+    "qat_attn_tree_workspace_bytes",
+    "qat_attn_tree",
+    "qat_draft_tree",
+    "qat_kv_cache_keep",
 )
 
 
@@ -131,6 +139,22 @@ def lib() -> ctypes.CDLL:
         L.qat_attn_decode_workspace_bytes.restype = _sz
         L.qat_attn_decode.argtypes = [_vp] * 9 + [_i] * 8 + [_f, _i, _vp, _sz, _vp]
         L.qat_attn_decode.restype = _i
+        L.qat_attn_fwd_window.argtypes = [_vp] * 6 + [_i] * 4 + [_f, _i, _i, _i, _vp]
+        L.qat_attn_fwd_window.restype = _i
+        L.qat_attn_bwd_window_workspace_bytes.argtypes = [_i] * 6
+        L.qat_attn_bwd_window_workspace_bytes.restype = _sz
+        L.qat_attn_bwd_window.argtypes = [_vp] * 10 + [_i] * 4 + [_f, _i, _i, _i, _vp, _sz, _vp]
+        L.qat_attn_bwd_window.restype = _i
+        L.qat_attn_decode_window.argtypes = [_vp] * 9 + [_i] * 8 + [_f, _i, _i, _i, _vp, _sz, _vp]
+        L.qat_attn_decode_window.restype = _i
+        L.qat_attn_tree_workspace_bytes.argtypes = [_i] * 4
+        L.qat_attn_tree_workspace_bytes.restype = _sz
+        L.qat_attn_tree.argtypes = [_vp] * 8 + [_ll] + [_vp] * 2 + [_i] * 8 + [_f, _i, _i, _i, _vp, _sz, _vp]
+        L.qat_attn_tree.restype = _i
+        L.qat_draft_tree.argtypes = [_vp, _ll] + [_vp] * 3 + [_i] * 2 + [_vp]
+        L.qat_draft_tree.restype = _i
+        L.qat_kv_cache_keep.argtypes = [_vp] * 9 + [_i] * 8 + [_vp]
+        L.qat_kv_cache_keep.restype = _i
         _lib = L
     return _lib
 
@@ -322,3 +346,57 @@ def qat_attn_decode(q, k_codes, v_codes, k_scales, v_scales, block_table, seq_le
         _ptr(q), _ptr(k_codes), _ptr(v_codes), _ptr(k_scales), _ptr(v_scales), _ptr(block_table),
         _ptr(seq_lens), _ptr(o), _ptr(lse), B, Hq, Hkv, T, D, num_pages, page_size, max_pages,
         float(sm_scale), int(quant_mode), _ptr(workspace), workspace_bytes, _stream(stream)))
+
+
+def qat_attn_fwd_window(q, k, v, o_q, o_hp, lse, B, H, N, D, sm_scale, window, sinks, quant_mode,
+                        stream=None) -> Status:
+    return _status(lib().qat_attn_fwd_window(_ptr(q), _ptr(k), _ptr(v), _ptr(o_q), _ptr(o_hp), _ptr(lse), B, H,
+                                             N, D, float(sm_scale), int(window), int(sinks), int(quant_mode),
+                                             _stream(stream)))
+
+
+def qat_attn_bwd_window_workspace_bytes(B, H, N, D, window, sinks) -> int:
+    return int(lib().qat_attn_bwd_window_workspace_bytes(B, H, N, D, window, sinks))
+
+
+def qat_attn_bwd_window(q, k, v, o_hp, lse, dO, dq, dk, dv, k_mean, B, H, N, D, sm_scale, window, sinks,
+                        quant_mode, workspace, workspace_bytes, stream=None) -> Status:
+    return _status(lib().qat_attn_bwd_window(
+        _ptr(q), _ptr(k), _ptr(v), _ptr(o_hp), _ptr(lse), _ptr(dO), _ptr(dq), _ptr(dk), _ptr(dv), _ptr(k_mean), B,
+        H, N, D, float(sm_scale), int(window), int(sinks), int(quant_mode), _ptr(workspace), int(workspace_bytes),
+        _stream(stream)))
+
+
+def qat_attn_decode_window(q, k_codes, v_codes, k_scales, v_scales, block_table, seq_lens, o, lse, B, Hq, Hkv, T, D,
+                           num_pages, page_size, max_pages, sm_scale, window, sinks, quant_mode, workspace,
+                           workspace_bytes, stream=None) -> Status:
+    return _status(lib().qat_attn_decode_window(
+        _ptr(q), _ptr(k_codes), _ptr(v_codes), _ptr(k_scales), _ptr(v_scales), _ptr(block_table), _ptr(seq_lens),
+        _ptr(o), _ptr(lse), B, Hq, Hkv, T, D, num_pages, page_size, max_pages, float(sm_scale), int(window),
+        int(sinks), int(quant_mode), _ptr(workspace), workspace_bytes, _stream(stream)))
+
+
+def qat_attn_tree_workspace_bytes(Hq, Hkv, T, D) -> int:
+    return int(lib().qat_attn_tree_workspace_bytes(Hq, Hkv, T, D))
+
+
+def qat_attn_tree(q, k_codes, v_codes, k_scales, v_scales, block_table, seq_lens, tree, tree_stride, o, lse, B, Hq,
+                  Hkv, T, D, num_pages, page_size, max_pages, sm_scale, window, sinks, quant_mode, workspace,
+                  workspace_bytes, stream=None) -> Status:
+    return _status(lib().qat_attn_tree(
+        _ptr(q), _ptr(k_codes), _ptr(v_codes), _ptr(k_scales), _ptr(v_scales), _ptr(block_table), _ptr(seq_lens),
+        _ptr(tree), int(tree_stride), _ptr(o), _ptr(lse), B, Hq, Hkv, T, D, num_pages, page_size, max_pages,
+        float(sm_scale), int(window), int(sinks), int(quant_mode), _ptr(workspace), workspace_bytes,
+        _stream(stream)))
+
+
+def qat_draft_tree(parents, parents_stride, seq_lens, tree, positions, B, T, stream=None) -> Status:
+    return _status(lib().qat_draft_tree(_ptr(parents), int(parents_stride), _ptr(seq_lens), _ptr(tree),
+                                        _ptr(positions), B, T, _stream(stream)))
+
+
+def qat_kv_cache_keep(k_codes, v_codes, k_scales, v_scales, block_table, seq_lens, path, path_lens, new_lens, B, H,
+                      T, L, D, num_pages, page_size, max_pages, stream=None) -> Status:
+    return _status(lib().qat_kv_cache_keep(
+        _ptr(k_codes), _ptr(v_codes), _ptr(k_scales), _ptr(v_scales), _ptr(block_table), _ptr(seq_lens), _ptr(path),
+        _ptr(path_lens), _ptr(new_lens), B, H, T, L, D, num_pages, page_size, max_pages, _stream(stream)))

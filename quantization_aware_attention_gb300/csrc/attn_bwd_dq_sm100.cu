@@ -89,9 +89,16 @@ struct DqParams {
   int hgroup;   // heads per group of the causal order (causal_head_group)
 };
 
+// kWin (sliding windows with sinks, causal): J is the number of key blocks that the rows' windows and the
+// sinks lie in.
+template <bool kWin>
 __device__ __forceinline__ void dq_item(int idx, const DqParams& p, int& bh, int& mt, int& J) {
   const int BH = p.a.B * p.a.H;
-  if (p.a.causal) {  // longest first (late query blocks see the most keys), heads in groups
+  if constexpr (kWin) {
+    bh = idx / p.mtiles;
+    mt = idx - bh * p.mtiles;
+    J = WindowBlocks(mt, p.a.window, p.a.sinks).count;
+  } else if (p.a.causal) {  // longest first (late query blocks see the most keys), heads in groups
     int cls;
     causal_item(idx, BH, p.mtiles, p.hgroup, bh, cls);
     mt = p.mtiles - 1 - cls;
@@ -130,7 +137,7 @@ __device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
 // sub-partition's 16K registers, so a 352-thread CTA cannot launch with more.
 // kSmooth: a k_mean is passed (the SMOOTH_K term); a separate instance, so that the
 // hot loop of the plain backward carries no row-sum register or add.
-template <int D, bool kSmooth>
+template <int D, bool kSmooth, bool kWin>
 __global__ void __launch_bounds__(384, 1)
     attn_bwd_dq_kernel(const __grid_constant__ CUtensorMap tmK,
                        const __grid_constant__ CUtensorMap tmV,
@@ -175,7 +182,7 @@ __global__ void __launch_bounds__(384, 1)
       bool ok = true;
       for (int idx = blockIdx.x; idx < p.items && ok; idx += gridDim.x, ++it) {
         int bh, mt, J;
-        dq_item(idx, p, bh, mt, J);
+        dq_item<kWin>(idx, p, bh, mt, J);
         // the item's dO waits for the previous item's last dP; its first K and V tiles
         // only for ring stages, so they go first and the item's first S can follow the
         // previous item's last one without waiting for that dP
@@ -188,14 +195,16 @@ __global__ void __launch_bounds__(384, 1)
           // the next item's dO tile into L2 (each dO tile is read once, so from DRAM)
           if (idx + static_cast<int>(gridDim.x) < p.items) {
             int nbh, nmt, nJ;
-            dq_item(idx + gridDim.x, p, nbh, nmt, nJ);
+            dq_item<kWin>(idx + gridDim.x, p, nbh, nmt, nJ);
             for (int c = 0; c < C::kChunks; ++c)
               tma_prefetch_l2_3d(&tmDO, 64 * c, nmt * kBlk, nbh);
           }
           return true;
         };
+        const WindowBlocks win(mt, p.a.window, p.a.sinks);
         for (int j = 0; j < J && ok; ++j) {
           if (j == 1 && !(ok = load_do())) break;
+          const int jb = kWin ? win.at(j) : j;
           {
             const uint32_t st = kc % kKStages, use = kc / kKStages;
             ok = mbar_wait(bar(Q_K_EMPTY + st), (use & 1) ^ 1, abort_flag, p.err);
@@ -203,7 +212,7 @@ __global__ void __launch_bounds__(384, 1)
             mbar_arrive_expect_tx(bar(Q_K_FULL + st), C::kTileBytes);
             for (int c = 0; c < C::kChunks; ++c)
               tma_load_3d(base + C::kOffK + st * C::kTileBytes + c * C::kChunkBytes, &tmK,
-                          bar(Q_K_FULL + st), 64 * c, j * kBlk, bh);
+                          bar(Q_K_FULL + st), 64 * c, jb * kBlk, bh);
             ++kc;
           }
           {
@@ -213,7 +222,7 @@ __global__ void __launch_bounds__(384, 1)
             mbar_arrive_expect_tx(bar(Q_V_FULL + st), C::kTileBytes);
             for (int c = 0; c < C::kChunks; ++c)
               tma_load_3d(base + C::kOffV + st * C::kTileBytes + c * C::kChunkBytes, &tmV,
-                          bar(Q_V_FULL + st), 64 * c, j * kBlk, bh);
+                          bar(Q_V_FULL + st), 64 * c, jb * kBlk, bh);
             ++vc;
           }
         }
@@ -276,7 +285,7 @@ __global__ void __launch_bounds__(384, 1)
       // blocks and its completion overlaps a whole block of their work.
       for (int idx = blockIdx.x; idx < p.items && ok; idx += gridDim.x, ++it) {
         int bh, mt, J;
-        dq_item(idx, p, bh, mt, J);
+        dq_item<kWin>(idx, p, bh, mt, J);
         ok = w(bar(Q_QR_FULL), it & 1) && issue_s(kc, bc, J == 1);
         for (int j = 0; j < J && ok; ++j) {
           if (j + 1 < J && !(ok = issue_s(kc + j + 1, bc + j + 1, j + 2 == J))) break;
@@ -302,7 +311,7 @@ __global__ void __launch_bounds__(384, 1)
       const uint32_t sdo = base + C::kOffDO;
       for (int idx = blockIdx.x; idx < p.items && ok; idx += gridDim.x, ++it) {
         int bh, mt, J;
-        dq_item(idx, p, bh, mt, J);
+        dq_item<kWin>(idx, p, bh, mt, J);
         ok = w(bar(Q_DO_FULL), it & 1);
         for (int j = 0; j < J && ok; ++j, ++vc, ++bc) {
           // dP overwrites dP of block bc - 1: wait until the compute warps have read it
@@ -389,12 +398,12 @@ __global__ void __launch_bounds__(384, 1)
     };
     if (static_cast<int>(blockIdx.x) < p.items) {
       int bh, mt, J;
-      dq_item(blockIdx.x, p, bh, mt, J);
+      dq_item<kWin>(blockIdx.x, p, bh, mt, J);
       load_next(bh, mt);
     }
     for (int idx = blockIdx.x; idx < p.items && ok; idx += gridDim.x, ++it) {
       int bh, mt, J;
-      dq_item(idx, p, bh, mt, J);
+      dq_item<kWin>(idx, p, bh, mt, J);
       const int row = mt * kBlk + r;
       const float lse_r = lse_n;
       const float delta_r = delta_n;
@@ -402,7 +411,7 @@ __global__ void __launch_bounds__(384, 1)
       {  // the next item's Q half-row, lse and Delta, read during this item, into L2 now
         if (nidx < p.items) {
           int nbh, nmt, nJ;
-          dq_item(nidx, p, nbh, nmt, nJ);
+          dq_item<kWin>(nidx, p, nbh, nmt, nJ);
           const int nrow = nmt * kBlk + r;
           const size_t nprow = static_cast<size_t>(nbh) * p.nq_pad + nrow;
           if (nrow < p.a.Nq)
@@ -414,6 +423,7 @@ __global__ void __launch_bounds__(384, 1)
       // dS of block c (keys [64h, 64h + 64)) -> TMEM dS columns [32h, 32h + 32), once dQ
       // of block c - 1 has read the buffer.  dS_c is held in registers and written after
       // P of block c + 1 has been computed, so dQ_{c-1} has a block's time to complete.
+      const WindowBlocks win(mt, p.a.window, p.a.sinks);
       uint32_t pk[32];
       float rs = 0.f;                                  // sum of this thread's fp32 dS
       auto write_ds = [&](uint32_t c) -> bool {
@@ -444,8 +454,16 @@ __global__ void __launch_bounds__(384, 1)
         }
         // keys past Nkv, and keys after the row on the causal diagonal: P = 0 (a
         // warp-uniform pass over the few blocks that have such keys)
-        const int key0 = j * kBlk + 64 * h;
-        if (key0 + 64 > p.a.Nkv || (p.a.causal && j == mt)) {
+        const int jb = kWin ? win.at(j) : j;
+        const int key0 = jb * kBlk + 64 * h;
+        if constexpr (kWin) {  // and keys before the row's window, but for the sinks
+          if (jb == mt || (jb * kBlk < mt * kBlk + kBlk - p.a.window && jb * kBlk + kBlk > p.a.sinks)) {
+            const int lim = min(p.a.Nkv - 1, row), low = row - p.a.window;
+#pragma unroll
+            for (int i = 0; i < 64; ++i)
+              if (key0 + i > lim || (key0 + i <= low && key0 + i >= p.a.sinks)) pr[i] = 0u;
+          }
+        } else if (key0 + 64 > p.a.Nkv || (p.a.causal && j == mt)) {
           const int lim = p.a.causal ? min(p.a.Nkv - 1, row) : p.a.Nkv - 1;
 #pragma unroll
           for (int i = 0; i < 64; ++i)
@@ -481,7 +499,7 @@ __global__ void __launch_bounds__(384, 1)
         if (!(ok = wwait(bar(Q_QR_EMPTY), it & 1))) break;
         tc_fence_after();
         int nbh, nmt, nJ;
-        dq_item(nidx, p, nbh, nmt, nJ);
+        dq_item<kWin>(nidx, p, nbh, nmt, nJ);
         load_next(nbh, nmt);
       }
       // ---- epilogue: group h stores dQ columns [hD/2, (h+1)D/2) of its row
@@ -553,7 +571,8 @@ cudaError_t launch_bwd_dq_d(const BwdArgs& a, unsigned int* err, int num_sms, cu
   if (!make_bf16_map_3d(&mk, a.k, D, a.Nkv, BH) || !make_bf16_map_3d(&mv, a.v, D, a.Nkv, BH) ||
       !make_bf16_map_3d(&mdo, a.dO, D, a.Nq, BH))
     return cudaErrorInvalidValue;
-  auto kern = a.k_mean != nullptr ? attn_bwd_dq_kernel<D, true> : attn_bwd_dq_kernel<D, false>;
+  auto kern = a.window > 0 ? (a.k_mean != nullptr ? attn_bwd_dq_kernel<D, true, true> : attn_bwd_dq_kernel<D, false, true>)
+                           : (a.k_mean != nullptr ? attn_bwd_dq_kernel<D, true, false> : attn_bwd_dq_kernel<D, false, false>);
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                        static_cast<int>(C::kSmemBytes));
   if (e != cudaSuccess) return e;

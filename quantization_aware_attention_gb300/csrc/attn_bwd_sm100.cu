@@ -125,6 +125,8 @@ __device__ __forceinline__ int sk_start(int work, int c, int G) {
 // or the range end.  (The two are separate kernel instances: with the range arithmetic
 // in it, the one-CTA-per-item loop kept its item values out of the uniform registers
 // and ran 5% slower.)
+// kWin (sliding windows with sinks, causal): the items are the pieces of the sinks' key blocks, the longest,
+// then the other key blocks, each with the query blocks whose windows reach it.
 template <bool kSK>
 __device__ __forceinline__ int bwd_first(const BwdTcParams& p) {
   if constexpr (kSK) return sk_start(p.work, blockIdx.x, gridDim.x);
@@ -137,11 +139,30 @@ __device__ __forceinline__ int bwd_end(const BwdTcParams& p) {
   else return p.items;
 }
 
-template <bool kSK>
+template <bool kSK, bool kWin>
 __device__ __forceinline__ BwdItem bwd_item(int idx, const BwdTcParams& p) {
   BwdItem t;
   t.slot = -1;
-  if constexpr (!kSK) {
+  if constexpr (kWin) {
+    const int blocks = (p.a.sinks + kBlk - 1) / kBlk, n = p.a.sink_pieces;
+    const int pieces = p.a.B * p.a.H * blocks * n;
+    t.rot = 0;
+    if (idx < pieces) {
+      t.kb = idx % blocks;  // the blocks of one head's piece share its queries in L2
+      const int x = idx / blocks;
+      t.bh = x / n;
+      const int i = x - t.bh * n, M = p.mtiles - t.kb;
+      t.q0 = t.kb + static_cast<int>(static_cast<long long>(M) * i / n);
+      t.count = t.kb + static_cast<int>(static_cast<long long>(M) * (i + 1) / n) - t.q0;
+      if (n > 1) t.slot = (t.bh * blocks + t.kb) * n + i;
+    } else {
+      const int x = idx - pieces, rest = p.ktiles - blocks;
+      t.bh = x / rest;
+      t.kb = blocks + (x - t.bh * rest);
+      t.q0 = t.kb;
+      t.count = min(p.mtiles - 1, (t.kb * kBlk + kBlk - 2 + p.a.window) / kBlk) - t.kb + 1;
+    }
+  } else if constexpr (!kSK) {
     if (p.a.causal) {  // longest first (small key blocks see the most queries), heads in groups
       causal_item(idx, p.a.B * p.a.H, p.ktiles, p.hgroup, t.bh, t.kb);
       t.q0 = t.kb;
@@ -203,7 +224,7 @@ __device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
 
 // Bounds of 384 threads cap registers at 168 per thread: with 11 warps, three share a
 // sub-partition's 16K registers, so a 352-thread CTA cannot launch with more.
-template <int D, bool kSK>
+template <int D, bool kSK, bool kWin>
 __global__ void __launch_bounds__(384, 1)
     attn_bwd_dkdv_kernel(const __grid_constant__ CUtensorMap tmQ,
                          const __grid_constant__ CUtensorMap tmK,
@@ -274,7 +295,7 @@ __global__ void __launch_bounds__(384, 1)
         return true;
       };
       for (int idx = bwd_first<kSK>(p), end = bwd_end<kSK>(p), nx; idx < end && ok; idx = nx, ++it) {
-        const BwdItem t = bwd_item<kSK>(idx, p);
+        const BwdItem t = bwd_item<kSK, kWin>(idx, p);
         nx = bwd_step<kSK>(idx, t);
         const int bh = t.bh, kb = t.kb, count = t.count;
         ok = mbar_wait(bar(B_KV_EMPTY), (it & 1) ^ 1, abort_flag, p.err);
@@ -352,7 +373,7 @@ __global__ void __launch_bounds__(384, 1)
       };
       ok = w(bar(B_ONES_FULL), 0);
       for (int idx = bwd_first<kSK>(p), end = bwd_end<kSK>(p), nx; idx < end && ok; idx = nx, ++it) {
-        const BwdItem t = bwd_item<kSK>(idx, p);
+        const BwdItem t = bwd_item<kSK, kWin>(idx, p);
         nx = bwd_step<kSK>(idx, t);
         const int count = t.count;
         ok = w(bar(B_KV_FULL), it & 1) && wait_q(qc);
@@ -420,7 +441,7 @@ __global__ void __launch_bounds__(384, 1)
       };
       ok = w(bar(B_ONES_FULL), 0);
       for (int idx = bwd_first<kSK>(p), end = bwd_end<kSK>(p), nx; idx < end && ok; idx = nx, ++it) {
-        const BwdItem t = bwd_item<kSK>(idx, p);
+        const BwdItem t = bwd_item<kSK, kWin>(idx, p);
         nx = bwd_step<kSK>(idx, t);
         const int count = t.count;
         ok = w(bar(B_KV_FULL), it & 1) && wait_do(qc);
@@ -466,6 +487,12 @@ __global__ void __launch_bounds__(384, 1)
       const bool okw = mbar_wait(b_, par, abort_flag, p.err);
       return __all_sync(0xffffffffu, okw) != 0;
     };
+    // kWin: whether some query of block blk lies behind the window of some key of block kb, and the last query
+    // that sees this thread's key
+    auto behind = [&](int blk, int kb) {
+      return kWin && blk * kBlk + kBlk > kb * kBlk + p.a.window && kb * kBlk + kBlk > p.a.sinks;
+    };
+    auto newest = [&](int key) { return key < p.a.sinks ? 0x7fffffff : key + p.a.window - 1; };
     uint32_t Pp[32];                                  // P^T of the current block, bf16 pairs
     // this thread's row of P^T (64 queries, bf16 pairs) over its S^T columns [64h, 64h+32):
     // the A operand of the dV MMA
@@ -482,7 +509,9 @@ __global__ void __launch_bounds__(384, 1)
     auto p_phase = [&](uint32_t c, int blk, int kb, bool key_ok, int key) -> bool {
       if (!wwait(bar(B_S_FULL), c & 1)) return false;
       tc_fence_after();
-      const bool diag = p.a.causal && blk == kb;
+      const bool diag = (kWin || p.a.causal) && blk == kb;
+      const bool far = behind(blk, kb);
+      const int until = kWin ? newest(key) : 0;
       const int qh = blk * kBlk + 64 * h;             // first query of this thread's columns
       {
         uint32_t sr[64];
@@ -498,11 +527,11 @@ __global__ void __launch_bounds__(384, 1)
         }
         // keys past Nkv (whole rows) and queries before the key on the causal diagonal
         // get P = 0; a separate pass, taken only by the few rows and blocks that need it
-        if (__any_sync(0xffffffffu, !key_ok) || diag) {
+        if (__any_sync(0xffffffffu, !key_ok) || diag || far) {
 #pragma unroll
           for (int i = 0; i < 32; ++i) {
-            const bool m0 = !key_ok || (diag && qh + 2 * i < key);
-            const bool m1 = !key_ok || (diag && qh + 2 * i + 1 < key);
+            const bool m0 = !key_ok || (diag && qh + 2 * i < key) || (far && qh + 2 * i > until);
+            const bool m1 = !key_ok || (diag && qh + 2 * i + 1 < key) || (far && qh + 2 * i + 1 > until);
             Pp[i] &= (m0 ? 0xffff0000u : 0xffffffffu) & (m1 ? 0x0000ffffu : 0xffffffffu);
           }
         }
@@ -520,7 +549,9 @@ __global__ void __launch_bounds__(384, 1)
     auto p_phase_page = [&](uint32_t c, int blk, int kb, bool key_ok, int key) -> bool {
       if (!wwait(bar(B_S_FULL), c & 1)) return false;
       tc_fence_after();
-      const bool diag = p.a.causal && blk == kb;
+      const bool diag = (kWin || p.a.causal) && blk == kb;
+      const bool far = behind(blk, kb);
+      const int until = kWin ? newest(key) : 0;
       const int qh = blk * kBlk + 64 * h;
       uint32_t pf[64];                                 // P^T of this row, fp32 bits
       tmem_ld32(tbase + lrow + C::kTmemS + 64 * h, *reinterpret_cast<uint32_t(*)[32]>(&pf[0]));
@@ -533,10 +564,10 @@ __global__ void __launch_bounds__(384, 1)
         pf[i] = __float_as_uint(ex2f(x.x));
         pf[i + 1] = __float_as_uint(ex2f(x.y));
       }
-      if (__any_sync(0xffffffffu, !key_ok) || diag) {
+      if (__any_sync(0xffffffffu, !key_ok) || diag || far) {
 #pragma unroll
         for (int i = 0; i < 64; ++i)
-          if (!key_ok || (diag && qh + i < key)) pf[i] = 0u;
+          if (!key_ok || (diag && qh + i < key) || (far && qh + i > until)) pf[i] = 0u;
       }
 #pragma unroll
       for (int i = 0; i < 64; i += 2)
@@ -607,7 +638,7 @@ __global__ void __launch_bounds__(384, 1)
     int it = 0;
     bool ok = true;
     for (int idx = bwd_first<kSK>(p), end = bwd_end<kSK>(p), nx; idx < end && ok; idx = nx, ++it) {
-      const BwdItem t = bwd_item<kSK>(idx, p);
+      const BwdItem t = bwd_item<kSK, kWin>(idx, p);
       nx = bwd_step<kSK>(idx, t);
       const int bh = t.bh, kb = t.kb, count = t.count;
       const int key = kb * kBlk + r;
@@ -633,7 +664,7 @@ __global__ void __launch_bounds__(384, 1)
       const float scale = h ? p.a.sm_scale : 1.0f;
       // a segment of a cut item stores its fp32 partial sums (dK unscaled) in its slot;
       // bwd_segment_sum_kernel adds an item's segments in order and converts
-      float* part = kSK && t.slot >= 0
+      float* part = (kSK || kWin) && t.slot >= 0
                         ? p.a.part + ((static_cast<size_t>(t.slot) * 2 + h) * kBlk + r) * D
                         : nullptr;
 #pragma unroll 1
@@ -791,6 +822,34 @@ __global__ void __launch_bounds__(256) bwd_segment_sum_kernel(const float4* __re
   }
 }
 
+// The sinks' key blocks: adds the pieces' fp32 sums of block blockIdx.x in order, and stores bf16 dV and dK
+// (x sm_scale).
+template <int D>
+__global__ void __launch_bounds__(256) bwd_sink_sum_kernel(const float4* __restrict__ part, int blocks, int n,
+                                                           int Nkv, float sm_scale, uint2* dv, uint2* dk) {
+  constexpr int kD4 = D / 4;
+  const int kb = blockIdx.x % blocks;
+  const long long bh = blockIdx.x / blocks;
+  const int rows = min(kBlk, Nkv - kb * kBlk);
+  for (int i = blockIdx.y * blockDim.x + threadIdx.x; i < 2 * kBlk * kD4; i += gridDim.y * blockDim.x) {
+    const int t = i / (kBlk * kD4);                    // 0: dV, 1: dK
+    const int row = (i / kD4) % kBlk, c4 = i % kD4;
+    if (row >= rows) continue;
+    const float4* src = part + ((static_cast<long long>(blockIdx.x) * n * 2 + t) * kBlk + row) * kD4 + c4;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int k = 0; k < n; ++k) {
+      const float4 x = src[static_cast<long long>(k) * 2 * kBlk * kD4];
+      acc.x += x.x;
+      acc.y += x.y;
+      acc.z += x.z;
+      acc.w += x.w;
+    }
+    const float sc = t ? sm_scale : 1.0f;
+    (t ? dk : dv)[(bh * Nkv + kb * kBlk + row) * kD4 + c4] =
+        make_uint2(pack_bf16x2(acc.x * sc, acc.y * sc), pack_bf16x2(acc.z * sc, acc.w * sc));
+  }
+}
+
 template <int D>
 cudaError_t launch_bwd_tc_d(const BwdArgs& a, unsigned int* err, int num_sms, cudaStream_t s) {
   using C = BwdTc<D>;
@@ -803,6 +862,8 @@ cudaError_t launch_bwd_tc_d(const BwdArgs& a, unsigned int* err, int num_sms, cu
   p.items = BH * p.ktiles;
   // stream-K: at most the CTAs the workspace has slots for, each with >= 4 units
   const long long work = static_cast<long long>(p.items) * p.mtiles;
+  const int sink_blocks = (a.sinks + kBlk - 1) / kBlk;
+  if (a.window > 0) p.items += BH * sink_blocks * (a.sink_pieces - 1);
   int G = a.causal || a.part == nullptr ? 0 : a.sk_ctas;
   if (G > num_sms) G = num_sms;
   if (G > kMaxSkCtas) G = kMaxSkCtas;  // the fix-up's shared slot table
@@ -827,7 +888,9 @@ cudaError_t launch_bwd_tc_d(const BwdArgs& a, unsigned int* err, int num_sms, cu
       !make_ext_map_3d(&mqx, a.lse_ext, p.nq_pad, BH) ||
       !make_ext_map_3d(&mdx, a.d_ext, p.nq_pad, BH) || !make_ext_map_3d(&mones, a.ones, 128, 1))
     return cudaErrorInvalidValue;
-  auto kern = p.streamk ? attn_bwd_dkdv_kernel<D, true> : attn_bwd_dkdv_kernel<D, false>;
+  auto kern = a.window > 0 ? attn_bwd_dkdv_kernel<D, false, true>
+              : p.streamk  ? attn_bwd_dkdv_kernel<D, true, false>
+                           : attn_bwd_dkdv_kernel<D, false, false>;
   e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
                            static_cast<int>(C::kSmemBytes));
   if (e != cudaSuccess) return e;
@@ -838,6 +901,13 @@ cudaError_t launch_bwd_tc_d(const BwdArgs& a, unsigned int* err, int num_sms, cu
   if (p.streamk) {
     bwd_segment_sum_kernel<D><<<dim3(p.items, 2 * kBlk * (D / 4) / 512), 256, 0, s>>>(
         reinterpret_cast<const float4*>(a.part), p.work, G, p.mtiles, p.ktiles, a.Nkv, a.sm_scale,
+        reinterpret_cast<uint2*>(a.dv), reinterpret_cast<uint2*>(a.dk));
+    e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+  }
+  if (a.window > 0 && sink_blocks > 0 && a.sink_pieces > 1) {
+    bwd_sink_sum_kernel<D><<<dim3(BH * sink_blocks, 2 * kBlk * (D / 4) / 512), 256, 0, s>>>(
+        reinterpret_cast<const float4*>(a.part), sink_blocks, a.sink_pieces, a.Nkv, a.sm_scale,
         reinterpret_cast<uint2*>(a.dv), reinterpret_cast<uint2*>(a.dk));
     e = cudaGetLastError();
     if (e != cudaSuccess) return e;

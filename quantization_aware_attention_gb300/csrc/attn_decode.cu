@@ -199,10 +199,30 @@ __device__ __forceinline__ uint32_t v_off(int r, int c) {
   return (r >> 1) * 128 + (((((r & 1) << 2) | c) ^ (((r >> 1) & 3) << 1)) << 4);
 }
 
-// A place in the batch's list of units.
+// What the rows may see of the keys before their own: everything, or a window and the sinks; or (the last T
+// tokens being a drafted tree) also those of the T that their masks name.
+enum { kAll = 0, kWindow = 1, kTree = 2 };
+
+// A place in the batch's list of units.  Where windows leave a gap between the sinks and the keys of the first
+// row's window, the gap's whole tiles are not units: `tile` counts the others.
 struct Cursor {
   int b, h, mt, tile, tiles, len;
+  int gap_at, gap, low;  // tiles from gap_at on lie `gap` further; no row sees keys before `low` but sinks
 };
+
+template <int kMask>
+__device__ __forceinline__ int place_of(const Cursor& c, int tile) {
+  return kMask != kAll && tile >= c.gap_at ? tile + c.gap : tile;
+}
+
+template <int kMask>
+__device__ __forceinline__ void find_gap(const DecodeArgs& a, int len, Cursor& c) {
+  c.gap_at = c.gap = c.low = 0;
+  if (kMask == kAll || a.window == 0) return;
+  c.low = max(len - a.T - a.window, 0);  // one early: a drafted token without ancestors has the position before
+  c.gap_at = (min(a.sinks, len) + kTile - 1) / kTile;
+  c.gap = max(c.low / kTile - c.gap_at, 0);
+}
 
 __device__ __forceinline__ int clamp_len(const DecodeArgs& a, int len) {
   const long long cap = static_cast<long long>(a.max_pages) << a.page_shift;
@@ -212,13 +232,17 @@ __device__ __forceinline__ int tiles_of(int len) { return len > 0 ? (len + kTile
 
 // Tiles as the prefix sums have them: the cut and every index hold together even if a length changes
 // under the kernel.
+template <int kMask>
 __device__ __forceinline__ void enter_seq(const Params& p, const int* prefix, Cursor& c) {
   if (c.b >= p.a.B) return;  // behind the last: not looked at again
   c.tiles = static_cast<unsigned>(prefix[c.b + 1] - prefix[c.b]) / static_cast<unsigned>(p.a.Hkv * p.mtiles);
-  c.len = min(clamp_len(p.a, p.a.seq_lens[c.b]), c.tiles * kTile);
+  c.len = clamp_len(p.a, p.a.seq_lens[c.b]);
+  find_gap<kMask>(p.a, c.len, c);
+  c.len = min(c.len, (c.tiles + c.gap) * kTile);
 }
 
 // The next tile; u: its unit.
+template <int kMask>
 __device__ __forceinline__ void advance(const Params& p, const int* prefix, int extra, Cursor& c, int& u) {
   ++u;
   if (++c.tile < c.tiles) return;
@@ -229,7 +253,11 @@ __device__ __forceinline__ void advance(const Params& p, const int* prefix, int 
   if (++c.h < p.a.Hkv) return;
   c.h = 0;
   ++c.b;
-  enter_seq(p, prefix, c);
+  enter_seq<kMask>(p, prefix, c);
+}
+
+__device__ __forceinline__ unsigned long long mask_of(const DecodeArgs& a, int b, int token) {
+  return a.tree[b * a.tree_sb + token];
 }
 
 __device__ __forceinline__ int item_of(const Params& p, const Cursor& c) {
@@ -345,7 +373,7 @@ __device__ __forceinline__ float pow2_ratio(uint32_t a, uint32_t b) {
   return __uint_as_float(static_cast<uint32_t>(min(max(r, 1 << 23), 254 << 23)));
 }
 
-template <int D, int NR, bool kQuant>
+template <int D, int NR, bool kQuant, int kMask>
 __global__ void __launch_bounds__(32 * Cfg<D, NR>::kWarps, 1) decode_kernel(const Params p) {
   using C = Cfg<D, NR>;
   constexpr int kThreads = 32 * C::kWarps;
@@ -369,7 +397,9 @@ __global__ void __launch_bounds__(32 * Cfg<D, NR>::kWarps, 1) decode_kernel(cons
       const int len = a.seq_lens[b];
       const int ok = clamp_len(a, len);
       if (len > ok) atomicOr(a.err, kErrBadPage);
-      prefix[b] = tiles_of(ok) * per_seq;
+      Cursor c;
+      find_gap<kMask>(a, ok, c);
+      prefix[b] = (tiles_of(ok) - c.gap) * per_seq;
       sum += prefix[b];
     }
     int inc = sum;
@@ -416,7 +446,7 @@ __global__ void __launch_bounds__(32 * Cfg<D, NR>::kWarps, 1) decode_kernel(cons
       if (prefix[mid] + extra * mid * per_seq <= u0) lo = mid; else hi = mid;
     }
     cc.b = lo;
-    enter_seq(p, prefix, cc);
+    enter_seq<kMask>(p, prefix, cc);
     const int u = u0 - (prefix[lo] + extra * lo * per_seq);
     const int item = u / (cc.tiles + extra), in = u - item * (cc.tiles + extra);
     cc.tile = max(in - extra, 0);
@@ -440,9 +470,12 @@ __global__ void __launch_bounds__(32 * Cfg<D, NR>::kWarps, 1) decode_kernel(cons
     constexpr bool kV = decltype(which)::value;
     if (pu < u1) {
       if (!kV && (fresh || (pc.tile & 7) == 0)) {
-        const int pos = ((pc.tile & ~7) * 4 + lane) * kChunk;
+        const int pos = kMask == kAll ? ((pc.tile & ~7) * 4 + lane) * kChunk
+                                      : place_of<kMask>(pc, (pc.tile & ~7) + (lane >> 2)) * kTile + (lane & 3) * kChunk;
+        // pages that hold nothing any row sees are not looked up: they may have been given back
+        const bool unseen = kMask != kAll && pos < pc.len && pos + kChunk <= pc.low && pos >= a.sinks;
         rows_of = kNoPage;
-        if (pos < pc.len) {
+        if (pos < pc.len && !unseen) {
           const int page = a.table[static_cast<long long>(pc.b) * a.max_pages + (pos >> a.page_shift)];
           rows_of = kBadPage;
           if (page >= 0 && page < a.num_pages)
@@ -451,12 +484,12 @@ __global__ void __launch_bounds__(32 * Cfg<D, NR>::kWarps, 1) decode_kernel(cons
           else
             atomicOr(a.err, kErrBadPage);
         }
-        all_good = !__any_sync(0xffffffffu, rows_of == kBadPage);
+        all_good = !__any_sync(0xffffffffu, rows_of == kBadPage || unseen);
       }
       const uint8_t* codes = (kV ? a.v_codes : a.k_codes) + 16 * lane;
       const uint32_t dst = ring + (kV ? C::kVAt : 0);
       const int first = (pc.tile & 7) * (kTile / kChunk);
-      const int left = pc.len - pc.tile * kTile;  // keys from the tile's first on
+      const int left = pc.len - place_of<kMask>(pc, pc.tile) * kTile;  // keys from the tile's first on
       // lanes 0-15: the scales of K, 16-31: of V, four keys each
       const float* scales = (lane & 16) ? a.v_scales : a.k_scales;
       const uint32_t sc_row = kV ? 0 : __shfl_sync(0xffffffffu, rows_of, first + ((lane & 15) >> 2));
@@ -494,7 +527,7 @@ __global__ void __launch_bounds__(32 * Cfg<D, NR>::kWarps, 1) decode_kernel(cons
           }
         }
       }
-      if (kV) advance(p, prefix, extra, pc, pu);
+      if (kV) advance<kMask>(p, prefix, extra, pc, pu);
     }
     cp_commit();
   };
@@ -509,7 +542,7 @@ __global__ void __launch_bounds__(32 * Cfg<D, NR>::kWarps, 1) decode_kernel(cons
   float o[NR][MT][4];
   float2 m[NR], l[NR], rf[NR];  // of rows 8 n + 2t and 8 n + 2t + 1
   float less = 1.f;
-  int last[NR][2];              // the newest key each of those rows sees
+  int last[NR][2];              // the newest key each of those rows sees (a drafted token's own position)
   float2 bound[NR];             // the rows' largest weights so far, as m is
   bool begun = false;
   if (lane == 0 && !p.by_item) chains_of(p)[id] = Chain{-1, -1};
@@ -525,8 +558,10 @@ __global__ void __launch_bounds__(32 * Cfg<D, NR>::kWarps, 1) decode_kernel(cons
         m[n] = make_float2(-INFINITY, -INFINITY);
         l[n] = bound[n] = make_float2(0.f, 0.f);
 #pragma unroll
-        for (int y = 0; y < 2; ++y)
-          last[n][y] = cc.len - a.T + (cc.mt * p.rows + 8 * n + 2 * t + y) % a.T;
+        for (int y = 0; y < 2; ++y) {
+          const int token = (cc.mt * p.rows + 8 * n + 2 * t + y) % a.T;
+          last[n][y] = cc.len - a.T + (kMask == kTree ? __popcll(mask_of(a, cc.b, token)) - 1 : token);
+        }
 #pragma unroll
         for (int j = 0; j < MT; ++j) o[n][j][0] = o[n][j][1] = o[n][j][2] = o[n][j][3] = 0.f;
       }
@@ -587,16 +622,40 @@ __global__ void __launch_bounds__(32 * Cfg<D, NR>::kWarps, 1) decode_kernel(cons
     produce(kKeys, false);
 
     // mask: only tiles that reach past what some row sees
-    const int key0 = cc.tile * kTile + g;
-    const bool edge = (cc.tile + 1) * kTile > cc.len - a.T + 1;
+    const int here = place_of<kMask>(cc, cc.tile), key0 = here * kTile + g, base = cc.len - a.T;
+    // what hides keys at the sequence's end, and before the windows
+    const bool recent = (here + 1) * kTile > base + (kMask == kTree ? 0 : 1);
+    const bool old = kMask != kAll && a.window > 0 && here * kTile < cc.len - a.window &&
+                     (here + 1) * kTile > a.sinks;
+    const bool edge = recent || old;
+    uint32_t hid[NR];  // kMask: bit 4 c + i of s[n][c][i]
     if (edge) {
 #pragma unroll
-      for (int n = 0; n < NR; ++n)
+      for (int n = 0; n < NR; ++n) {
+        unsigned long long bits[2] = {0ull, 0ull};
+        if (kMask == kTree && recent) {
+#pragma unroll
+          for (int y = 0; y < 2; ++y) bits[y] = mask_of(a, cc.b, (cc.mt * p.rows + 8 * n + 2 * t + y) % a.T);
+        }
+        hid[n] = 0u;
 #pragma unroll
         for (int c = 0; c < 4; ++c)
 #pragma unroll
-          for (int i = 0; i < 4; ++i)
-            if (key0 + 16 * c + 8 * (i >> 1) > last[n][i & 1]) s[n][c][i] = -INFINITY;
+          for (int i = 0; i < 4; ++i) {
+            const int key = key0 + 16 * c + 8 * (i >> 1);
+            bool h = key > last[n][i & 1];
+            if (kMask == kTree) {
+              const int place = key - base;  // among the drafted tokens
+              h = place >= 0 && (place >= a.T || !(bits[i & 1] >> (place & 63) & 1ull));
+            }
+            if (kMask != kAll && a.window > 0 && (kMask == kWindow || key < base))
+              h |= key <= last[n][i & 1] - a.window && key >= a.sinks;
+            if (h) {
+              s[n][c][i] = -INFINITY;
+              if (kMask != kAll) hid[n] |= 1u << (4 * c + i);
+            }
+          }
+      }
     }
 
     float amax[NR][2];  // the tile's largest p of the lane's rows
@@ -667,8 +726,9 @@ __global__ void __launch_bounds__(32 * Cfg<D, NR>::kWarps, 1) decode_kernel(cons
           }
           w = mul_rn_f32x2(w, make_float2(vs[c][y], vs[c][y]));
           if (edge) {  // 0 x NaN: a key that the row does not see may hold anything
-            if (key0 + 16 * c + 8 * y > last[n][0]) w.x = 0.f;
-            if (key0 + 16 * c + 8 * y > last[n][1]) w.y = 0.f;
+            if (kMask == kAll ? key0 + 16 * c + 8 * y > last[n][0] : (hid[n] >> (4 * c + 2 * y) & 1u) != 0) w.x = 0.f;
+            if (kMask == kAll ? key0 + 16 * c + 8 * y > last[n][1] : (hid[n] >> (4 * c + 2 * y + 1) & 1u) != 0)
+              w.y = 0.f;
           }
           x[0] = w.x;
           x[1] = w.y;
@@ -785,7 +845,7 @@ __global__ void __launch_bounds__(32 * Cfg<D, NR>::kWarps, 1) decode_kernel(cons
         }
       }
     }
-    advance(p, prefix, extra, cc, u);
+    advance<kMask>(p, prefix, extra, cc, u);
   }
   cp_wait<0>();
 }
@@ -1032,7 +1092,7 @@ __global__ void __launch_bounds__(32 * kWarps, 32 / kWarps) merge_long_kernel(co
   if (warp == 0) store_row<D>(p, item, r, lane, sum);
 }
 
-template <int D, int NR, bool kQuant>
+template <int D, int NR, bool kQuant, int kMask>
 cudaError_t run(Params p, int ctas, long long units, cudaStream_t s) {
   using C = Cfg<D, NR>;
   const auto bytes = [](int B) { return C::kSmem + sizeof(int) * (C::kWarps + B + 1); };
@@ -1042,11 +1102,11 @@ cudaError_t run(Params p, int ctas, long long units, cudaStream_t s) {
   // The limit is that of the largest batch in every call: it is the kernel's, and another thread's call may
   // come between this one's limit and its launch.
   static_assert(bytes(kDecodeMaxBatch) <= 227 * 1024, "the batch's prefix sums fit beside the rings");
-  cudaError_t e = cudaFuncSetAttribute(decode_kernel<D, NR, kQuant>,
+  cudaError_t e = cudaFuncSetAttribute(decode_kernel<D, NR, kQuant, kMask>,
                                        cudaFuncAttributeMaxDynamicSharedMemorySize,
                                        static_cast<int>(bytes(kDecodeMaxBatch)));
   if (e != cudaSuccess) return e;
-  e = launch_early(decode_kernel<D, NR, kQuant>, ctas, 32 * C::kWarps, bytes(p.a.B), s, p);
+  e = launch_early(decode_kernel<D, NR, kQuant, kMask>, ctas, 32 * C::kWarps, bytes(p.a.B), s, p);
   if (e != cudaSuccess) return e;
   // How many warps add up a chain depends on the partials that an item leaves on average.  Where all chains
   // fit the GPU at two blocks of 16 warps an SM, more blocks share a chain while each has 128 partials.
@@ -1085,12 +1145,19 @@ cudaError_t launch_decode(const DecodeArgs& a, int D, int num_sms, cudaStream_t 
   const long long units = static_cast<long long>(a.B) * a.Hkv * p.mtiles * ((cap + kTile - 1) / kTile);  // >= 1
   int ctas = num_sms < kMaxCtas ? num_sms : kMaxCtas;
   if (units < ctas) ctas = static_cast<int>(units);
-  if (p.rows == 8) {
-    if (D == 64) return a.quant ? run<64, 1, true>(p, ctas, units, s) : run<64, 1, false>(p, ctas, units, s);
-    return a.quant ? run<128, 1, true>(p, ctas, units, s) : run<128, 1, false>(p, ctas, units, s);
-  }
-  if (D == 64) return a.quant ? run<64, 2, true>(p, ctas, units, s) : run<64, 2, false>(p, ctas, units, s);
-  return a.quant ? run<128, 2, true>(p, ctas, units, s) : run<128, 2, false>(p, ctas, units, s);
+  const auto by_mask = [&](auto d, auto nr, auto quant) {
+    constexpr int kD = decltype(d)::value, kNr = decltype(nr)::value;
+    constexpr bool kQ = decltype(quant)::value;
+    if (a.tree != nullptr) return run<kD, kNr, kQ, kTree>(p, ctas, units, s);
+    return a.window > 0 ? run<kD, kNr, kQ, kWindow>(p, ctas, units, s) : run<kD, kNr, kQ, kAll>(p, ctas, units, s);
+  };
+  const auto by_quant = [&](auto d, auto nr) {
+    return a.quant ? by_mask(d, nr, std::true_type{}) : by_mask(d, nr, std::false_type{});
+  };
+  const auto by_rows = [&](auto d) {
+    return p.rows == 8 ? by_quant(d, std::integral_constant<int, 1>{}) : by_quant(d, std::integral_constant<int, 2>{});
+  };
+  return D == 64 ? by_rows(std::integral_constant<int, 64>{}) : by_rows(std::integral_constant<int, 128>{});
 }
 
 }  // namespace qat

@@ -90,9 +90,10 @@ struct TcParams {
   int hgroup;   // heads per group of the causal order (causal_head_group)
 };
 
+template <bool kWin>
 __device__ __forceinline__ void item_coords(int idx, const TcParams& p, int& bh, int& mt) {
   const int BH = p.a.B * p.a.H;
-  if (p.a.causal) {  // longest rows first, heads in L2-sized groups
+  if (!kWin && p.a.causal) {  // longest rows first, heads in L2-sized groups
     int cls;
     causal_item(idx, BH, p.mtiles, p.hgroup, bh, cls);
     mt = p.mtiles - 1 - cls;
@@ -102,10 +103,25 @@ __device__ __forceinline__ void item_coords(int idx, const TcParams& p, int& bh,
   }
 }
 
+// The key blocks of an item, by step: 0 .. count - 1, or those of its rows' windows.
+template <bool kWin>
+struct KvBlocks;
+template <>
+struct KvBlocks<false> {
+  int count;
+  __device__ __forceinline__ KvBlocks(const TcParams& p, int mt);
+  __device__ __forceinline__ int at(int j) const { return j; }
+};
+template <>
+struct KvBlocks<true> : WindowBlocks {
+  __device__ __forceinline__ KvBlocks(const TcParams& p, int mt_) : WindowBlocks(mt_, p.a.window, p.a.sinks) {}
+};
+
 __device__ __forceinline__ int kv_tiles(const TcParams& p, int mt) {
   const int n = (p.a.Nkv + kBN - 1) / kBN;
   return p.a.causal ? min(n, mt + 1) : n;
 }
+__device__ __forceinline__ KvBlocks<false>::KvBlocks(const TcParams& p, int mt) : count(kv_tiles(p, mt)) {}
 
 __device__ __forceinline__ float fmax3(float a, float b, float c) {
   float d;
@@ -129,7 +145,9 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
 // kDefer: each item's epilogue waits for the next item's first block of P (short items,
 // see the softmax warps); a separate instance, since with the epilogue inside the block
 // loop long items ran 2-4% slower.
-template <int D, bool kDefer>
+// kWin: sliding windows with sinks (causal): an item takes the key blocks that its rows' windows and the
+// sinks lie in, masks those that an edge of a window crosses, and costs as much as they are.
+template <int D, bool kDefer, bool kWin>
 __global__ void __launch_bounds__(384, 1)
     attn_fwd_tc_kernel(const __grid_constant__ CUtensorMap tmQ,
                        const __grid_constant__ CUtensorMap tmK,
@@ -190,8 +208,9 @@ __global__ void __launch_bounds__(384, 1)
       bool ok = true;
       for (int idx = blockIdx.x; idx < p.items && ok; idx += gridDim.x, ++it) {
         int bh, mt;
-        item_coords(idx, p, bh, mt);
-        const int J = kv_tiles(p, mt);
+        item_coords<kWin>(idx, p, bh, mt);
+        const KvBlocks<kWin> kv(p, mt);
+        const int J = kv.count;
         ok = mbar_wait(bar(BAR_Q_EMPTY), (it & 1) ^ 1, abort_flag, p.err);
         if (!ok) break;
         ++qn;
@@ -203,7 +222,7 @@ __global__ void __launch_bounds__(384, 1)
         // load then waits only for the L2 when the Q buffer frees up
         if (idx + static_cast<int>(gridDim.x) < p.items) {
           int nbh, nmt;
-          item_coords(idx + gridDim.x, p, nbh, nmt);
+          item_coords<kWin>(idx + gridDim.x, p, nbh, nmt);
           for (int c = 0; c < C::kChunks; ++c) tma_prefetch_l2_3d(&tmQ, 64 * c, nmt * kBM, nbh);
         }
         for (int j = 0; j <= J && ok; ++j) {
@@ -214,7 +233,7 @@ __global__ void __launch_bounds__(384, 1)
             mbar_arrive_expect_tx(bar(BAR_K_FULL + st), C::kTileBytes);
             for (int c = 0; c < C::kChunks; ++c)
               tma_load_3d(base + C::kOffK + st * C::kTileBytes + c * C::kChunkBytes, &tmK,
-                          bar(BAR_K_FULL + st), 64 * c, j * kBN, bh);
+                          bar(BAR_K_FULL + st), 64 * c, kv.at(j) * kBN, bh);
             ++kc;
           }
           if (j >= 1) {  // V_{j-1}: one tile behind K, matching the MMA issue order
@@ -224,7 +243,7 @@ __global__ void __launch_bounds__(384, 1)
             mbar_arrive_expect_tx(bar(BAR_V_FULL + st), C::kTileBytes);
             for (int c = 0; c < C::kChunks; ++c)
               tma_load_3d(base + C::kOffV + st * C::kTileBytes + c * C::kChunkBytes, &tmV,
-                          bar(BAR_V_FULL + st), 64 * c, (j - 1) * kBN, bh);
+                          bar(BAR_V_FULL + st), 64 * c, kv.at(j - 1) * kBN, bh);
             ++vc;
           }
         }
@@ -246,8 +265,9 @@ __global__ void __launch_bounds__(384, 1)
       bool ok = true, issued = false;
       for (int idx = blockIdx.x; idx < p.items && ok; idx += gridDim.x, ++it) {
         int bh, mt;
-        item_coords(idx, p, bh, mt);
-        const int J = kv_tiles(p, mt);
+        item_coords<kWin>(idx, p, bh, mt);
+        const KvBlocks<kWin> kv(p, mt);
+        const int J = kv.count;
         ok = mbar_wait(bar(BAR_Q_FULL), it & 1, abort_flag, p.err);
         for (int j = 0; j < J && ok; ++j, ++kc, ++sc) {
           const uint32_t st = kc % kKStages;
@@ -286,8 +306,9 @@ __global__ void __launch_bounds__(384, 1)
       bool ok = true, issued = false;
       for (int idx = blockIdx.x; idx < p.items && ok; idx += gridDim.x, ++it) {
         int bh, mt;
-        item_coords(idx, p, bh, mt);
-        const int J = kv_tiles(p, mt);
+        item_coords<kWin>(idx, p, bh, mt);
+        const KvBlocks<kWin> kv(p, mt);
+        const int J = kv.count;
         for (int j = 0; j < J && ok; ++j, ++vc, ++pc) {
           const uint32_t b = pc & 1;
           // V first (it has almost always landed), then P from the softmax warps
@@ -436,8 +457,9 @@ __global__ void __launch_bounds__(384, 1)
     bool ok = true;
     for (int idx = blockIdx.x; idx < p.items && ok; idx += gridDim.x, ++it) {
       int bh, mt;
-      item_coords(idx, p, bh, mt);
-      const int J = kv_tiles(p, mt);
+      item_coords<kWin>(idx, p, bh, mt);
+      const KvBlocks<kWin> kv(p, mt);
+      const int J = kv.count;
       const int row = mt * kBM + r;
       float m_used = -INFINITY, l = 0.f;
       for (int j = 0; j < J && ok; ++j) {
@@ -451,8 +473,17 @@ __global__ void __launch_bounds__(384, 1)
         tmem_ld32(tS + 64 * h + 32, *reinterpret_cast<uint32_t(*)[32]>(&sr[32]));
         tmem_wait_ld();
         float* s = reinterpret_cast<float*>(sr);
-        const int key0 = j * kBN + 64 * h;
-        if (j * kBN + kBN > p.a.Nkv || (p.a.causal && j == mt)) {
+        const int jb = kv.at(j);
+        const int key0 = jb * kBN + 64 * h;
+        if constexpr (kWin) {
+          // the diagonal (and with it the end of the keys), and blocks where some row's window begins
+          if (jb == mt || (jb * kBN < mt * kBM + kBM - p.a.window && jb * kBN + kBN > p.a.sinks)) {
+            const int lim = min(p.a.Nkv - 1, row), low = row - p.a.window;
+#pragma unroll
+            for (int i = 0; i < 64; ++i)
+              if (key0 + i > lim || (key0 + i <= low && key0 + i >= p.a.sinks)) s[i] = -INFINITY;
+          }
+        } else if (jb * kBN + kBN > p.a.Nkv || (p.a.causal && jb == mt)) {
           const int lim = p.a.causal ? min(p.a.Nkv - 1, row) : p.a.Nkv - 1;
 #pragma unroll
           for (int i = 0; i < 64; ++i)
@@ -569,9 +600,12 @@ cudaError_t launch_fwd_tc_d(const FwdArgs& a, unsigned int* err, int num_sms, cu
   p.items = BH * p.mtiles;
   // a causal item streams its head's K and V blocks
   p.hgroup = causal_head_group(4ll * a.Nkv * D, BH);
-  // deferred epilogues for items of at most 8 key blocks (non-causal)
-  const bool defer = !a.causal && a.Nkv <= 8 * kBN;
-  auto kern = defer ? attn_fwd_tc_kernel<D, true> : attn_fwd_tc_kernel<D, false>;
+  // deferred epilogues for items of at most 8 key blocks (not for causal ones, whose lengths differ)
+  const bool win = a.window > 0;
+  const long long blocks = win ? (a.window + 254ll) / kBN + (a.sinks + kBN - 1) / kBN : (a.Nkv + kBN - 1) / kBN;
+  const bool defer = (win || !a.causal) && blocks <= 8;
+  auto kern = win ? (defer ? attn_fwd_tc_kernel<D, true, true> : attn_fwd_tc_kernel<D, false, true>)
+                  : (defer ? attn_fwd_tc_kernel<D, true, false> : attn_fwd_tc_kernel<D, false, false>);
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                        static_cast<int>(C::kSmemBytes));
   if (e != cudaSuccess) return e;

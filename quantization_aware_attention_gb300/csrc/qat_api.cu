@@ -67,6 +67,7 @@ using qat::kMaxRows;
 
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr size_t kAlign = 256;
+constexpr int kMostKeys = 1 << 30;  // positions of a sequence in the cache
 
 // With QAT_VERBOSE=1 in the environment, CUDA errors are also printed to stderr.
 qat_status_t from_cuda(cudaError_t e) {
@@ -97,9 +98,22 @@ const char* qat_status_string(qat_status_t status) {
   return "QAT_ERR_UNKNOWN: unknown status code";
 }
 
-qat_status_t qat_attn_fwd(const void* q, const void* k, const void* v, void* o_q, void* o_hp,
-                          float* lse, int B, int H, int Nq, int Nkv, int D, float sm_scale,
-                          int causal, int quant_mode, void* stream) {
+}  // extern "C"
+
+namespace {
+
+// A window's arguments as the kernels take them: both within the keys there are.
+qat_status_t window_args(int N, int window, int sinks, int* w, int* s) {
+  if (window < 1 || sinks < 0) return QAT_ERR_INVALID_ARG;
+  if (N > (1 << 30)) return QAT_ERR_UNSUPPORTED;  // positions plus a window are 32-bit sums
+  *w = window < N ? window : N;
+  *s = sinks < N ? sinks : N;
+  return QAT_OK;
+}
+
+qat_status_t fwd_impl(const void* q, const void* k, const void* v, void* o_q, void* o_hp, float* lse, int B, int H,
+                      int Nq, int Nkv, int D, float sm_scale, int causal, int window, int sinks, int quant_mode,
+                      void* stream) {
   bool empty = false;
   const qat_status_t st = check_sizes(B, H, Nq, Nkv, D, sm_scale, causal, quant_mode, &empty);
   if (st != QAT_OK || empty) return st;
@@ -117,6 +131,8 @@ qat_status_t qat_attn_fwd(const void* q, const void* k, const void* v, void* o_q
   a.sm_scale = sm_scale;
   a.qk_scale = sm_scale * kLog2e;
   a.causal = causal;
+  a.window = window;
+  a.sinks = sinks;
   a.quant = quant_mode != QAT_QUANT_NONE;
   a.kv_head_rows = Nkv;
   a.o_q_f32 = nullptr;
@@ -126,6 +142,25 @@ qat_status_t qat_attn_fwd(const void* q, const void* k, const void* v, void* o_q
   cudaError_t e = qat::device_context(&err, &num_sms);
   if (e == cudaSuccess) e = qat::launch_fwd_tc(a, err, num_sms, static_cast<cudaStream_t>(stream));
   return from_cuda(e);
+}
+
+}  // namespace
+
+extern "C" {
+
+qat_status_t qat_attn_fwd(const void* q, const void* k, const void* v, void* o_q, void* o_hp,
+                          float* lse, int B, int H, int Nq, int Nkv, int D, float sm_scale,
+                          int causal, int quant_mode, void* stream) {
+  return fwd_impl(q, k, v, o_q, o_hp, lse, B, H, Nq, Nkv, D, sm_scale, causal, 0, 0, quant_mode, stream);
+}
+
+qat_status_t qat_attn_fwd_window(const void* q, const void* k, const void* v, void* o_q, void* o_hp, float* lse,
+                                 int B, int H, int N, int D, float sm_scale, int window, int sinks, int quant_mode,
+                                 void* stream) {
+  int w = 0, s = 0;
+  const qat_status_t st = window_args(N, window, sinks, &w, &s);
+  if (st != QAT_OK) return st;
+  return fwd_impl(q, k, v, o_q, o_hp, lse, B, H, N, N, D, sm_scale, 1, w, s, quant_mode, stream);
 }
 
 qat_status_t qat_attn_fwd_chunk(const void* q, const void* k, const void* v, float* o_q,
@@ -153,6 +188,7 @@ qat_status_t qat_attn_fwd_chunk(const void* q, const void* k, const void* v, flo
   a.sm_scale = sm_scale;
   a.qk_scale = sm_scale * kLog2e;
   a.causal = 0;
+  a.window = a.sinks = 0;
   a.quant = quant_mode != QAT_QUANT_NONE;
   a.kv_head_rows = Nkv_total;
   a.o_q_f32 = o_q;
@@ -193,6 +229,14 @@ size_t qat_attn_bwd_workspace_bytes(int B, int H, int Nq, int Nkv, int D) {
   return qat::bwd_workspace_layout(B, H, Nq, Nkv, D, qat::bwd_stream_k_ctas(B, H, Nq, Nkv)).total;
 }
 
+size_t qat_attn_bwd_window_workspace_bytes(int B, int H, int N, int D, int window, int sinks) {
+  bool empty = false;
+  int w = 0, s = 0;
+  if (check_sizes(B, H, N, N, D, 1.0f, 1, 0, &empty) != QAT_OK || window_args(N, window, sinks, &w, &s) != QAT_OK)
+    return 0;
+  return qat::bwd_workspace_layout(B, H, N, N, D, 0).total + (empty ? 0 : qat::window_part_bytes(B, H, N, D, w, s));
+}
+
 }  // extern "C"
 
 namespace {
@@ -200,7 +244,7 @@ namespace {
 qat_status_t bwd_impl(const void* q, const void* k, const void* v, const void* o_hp,
                       const float* lse, const void* dO, void* dq, void* dk, void* dv,
                       const float* k_mean, int B, int H, int Nq, int Nkv, int D, float sm_scale,
-                      int causal, int quant_mode, void* workspace, size_t workspace_bytes,
+                      int causal, int window, int sinks, int quant_mode, void* workspace, size_t workspace_bytes,
                       void* stream) {
   bool empty = false;
   const qat_status_t st = check_sizes(B, H, Nq, Nkv, D, sm_scale, causal, quant_mode, &empty);
@@ -220,7 +264,8 @@ qat_status_t bwd_impl(const void* q, const void* k, const void* v, const void* o
     if (p == nullptr || !aligned16(p)) return QAT_ERR_INVALID_ARG;
   // the stream-K split of the dK/dV work runs only when the workspace also holds its
   // segment sums (qat_attn_bwd_workspace_bytes does; the no-alloc scratch may not)
-  const size_t need = qat::bwd_workspace_layout(B, H, Nq, Nkv, D, 0).total;
+  const size_t base = qat::bwd_workspace_layout(B, H, Nq, Nkv, D, 0).total;
+  const size_t need = base + (window > 0 ? qat::window_part_bytes(B, H, Nq, D, window, sinks) : 0);
   if (workspace == nullptr || workspace_bytes < need) return QAT_ERR_WORKSPACE;
   if ((reinterpret_cast<uintptr_t>(workspace) & (kAlign - 1)) != 0) return QAT_ERR_INVALID_ARG;
   int sk = causal ? 0 : qat::bwd_stream_k_ctas(B, H, Nq, Nkv);
@@ -243,7 +288,10 @@ qat_status_t bwd_impl(const void* q, const void* k, const void* v, const void* o
   a.lse_ext = reinterpret_cast<uint16_t*>(ws + wl.off_lse_ext);
   a.d_ext = reinterpret_cast<uint16_t*>(ws + wl.off_d_ext);
   a.ones = reinterpret_cast<uint16_t*>(ws + wl.off_ones);
-  a.part = sk > 0 ? reinterpret_cast<float*>(ws + wl.off_part) : nullptr;
+  a.part = sk > 0 || need > base ? reinterpret_cast<float*>(ws + wl.off_part) : nullptr;
+  a.window = window;
+  a.sinks = sinks;
+  a.sink_pieces = window > 0 ? qat::window_sink_pieces(B, H, Nq, window, sinks) : 1;
   a.k_mean = k_mean;
   a.sk_ctas = sk;
   a.B = B; a.H = H; a.Nq = Nq; a.Nkv = Nkv; a.D = D;
@@ -268,7 +316,19 @@ qat_status_t qat_attn_bwd(const void* q, const void* k, const void* v, const voi
                           int quant_mode, void* workspace, size_t workspace_bytes,
                           void* stream) {
   return bwd_impl(q, k, v, o_hp, lse, dO, dq, dk, dv, nullptr, B, H, Nq, Nkv, D, sm_scale,
-                  causal, quant_mode, workspace, workspace_bytes, stream);
+                  causal, 0, 0, quant_mode, workspace, workspace_bytes, stream);
+}
+
+qat_status_t qat_attn_bwd_window(const void* q, const void* k, const void* v, const void* o_hp, const float* lse,
+                                 const void* dO, void* dq, void* dk, void* dv, const float* k_mean, int B, int H,
+                                 int N, int D, float sm_scale, int window, int sinks, int quant_mode,
+                                 void* workspace, size_t workspace_bytes, void* stream) {
+  int w = 0, s = 0;
+  const qat_status_t st = window_args(N, window, sinks, &w, &s);
+  if (st != QAT_OK) return st;
+  if (k_mean != nullptr && !aligned16(k_mean)) return QAT_ERR_INVALID_ARG;
+  return bwd_impl(q, k, v, o_hp, lse, dO, dq, dk, dv, k_mean, B, H, N, N, D, sm_scale, 1, w, s, quant_mode,
+                  workspace, workspace_bytes, stream);
 }
 
 qat_status_t qat_attn_bwd_smooth_k(const void* q, const void* k, const void* v,
@@ -278,7 +338,7 @@ qat_status_t qat_attn_bwd_smooth_k(const void* q, const void* k, const void* v,
                                    void* workspace, size_t workspace_bytes, void* stream) {
   if (k_mean == nullptr || !aligned16(k_mean)) return QAT_ERR_INVALID_ARG;
   return bwd_impl(q, k, v, o_hp, lse, dO, dq, dk, dv, k_mean, B, H, Nq, Nkv, D, sm_scale,
-                  causal, quant_mode, workspace, workspace_bytes, stream);
+                  causal, 0, 0, quant_mode, workspace, workspace_bytes, stream);
 }
 
 qat_status_t qat_debug_set_wait_limit_us(int limit_us, void* stream) {
@@ -623,20 +683,23 @@ qat_status_t qat_kv_cache_read(const void* k_codes, const void* v_codes, const f
   return from_cuda(e);
 }
 
-size_t qat_attn_decode_workspace_bytes(int Hq, int Hkv, int T, int D) {
-  if ((D != 64 && D != 128) || Hkv < 1 || Hq < 1 || Hq % Hkv != 0 || T < 0 ||
-      T > qat::kDecodeMaxTokens)
-    return 0;
+}  // extern "C"
+
+namespace {
+
+size_t over_cache_workspace(int Hq, int Hkv, int T, int D, int most) {
+  if ((D != 64 && D != 128) || Hkv < 1 || Hq < 1 || Hq % Hkv != 0 || T < 0 || T > most) return 0;
   const long long R = static_cast<long long>(Hq / Hkv) * T;
   return qat::decode_workspace_bytes(static_cast<int>(R < 16 ? R : 16), D);
 }
 
-qat_status_t qat_attn_decode(const void* q, const void* k_codes, const void* v_codes,
-                             const float* k_scales, const float* v_scales, const int* block_table,
-                             const int* seq_lens, void* o, float* lse, int B, int Hq, int Hkv,
-                             int T, int D, int num_pages, int page_size, int max_pages,
-                             float sm_scale, int quant_mode, void* workspace,
-                             size_t workspace_bytes, void* stream) {
+// The attention of new tokens over the cache, `most` of them: decoding, with a window (0: none), or of a tree.
+qat_status_t over_cache(const void* q, const void* k_codes, const void* v_codes, const float* k_scales,
+                        const float* v_scales, const int* block_table, const int* seq_lens,
+                        const unsigned long long* tree, long long tree_stride, void* o, float* lse, int B, int Hq,
+                        int Hkv, int T, int most, int D, int num_pages, int page_size, int max_pages, float sm_scale,
+                        int window, int sinks, int quant_mode, void* workspace, size_t workspace_bytes,
+                        void* stream) {
   if (B < 0 || Hq < 1 || T < 0 || !(sm_scale > 0.f) || !isfinite(sm_scale * kLog2e))
     return QAT_ERR_INVALID_ARG;
   if (quant_mode != QAT_QUANT_NONE && quant_mode != QAT_QUANT_P_FP8E4M3_ROW_TILE64)
@@ -644,7 +707,7 @@ qat_status_t qat_attn_decode(const void* q, const void* k_codes, const void* v_c
   const qat_status_t st = check_cache_sizes(Hkv, D, num_pages, page_size, max_pages);
   if (st != QAT_OK) return st;
   if (Hq % Hkv != 0) return QAT_ERR_INVALID_ARG;
-  if (T > qat::kDecodeMaxTokens || B > qat::kDecodeMaxBatch) return QAT_ERR_UNSUPPORTED;
+  if (T > most || B > qat::kDecodeMaxBatch) return QAT_ERR_UNSUPPORTED;
   const long long rows = static_cast<long long>(Hq / Hkv) * T;
   if (rows > kMaxRows || static_cast<long long>(B) * Hkv > kMaxRows) return QAT_ERR_UNSUPPORTED;
   const long long units = (static_cast<long long>(max_pages) * page_size + 63) / 64;
@@ -655,8 +718,9 @@ qat_status_t qat_attn_decode(const void* q, const void* k_codes, const void* v_c
     return QAT_ERR_INVALID_ARG;
   if (q == nullptr || o == nullptr || !aligned16(q) || !aligned16(o)) return QAT_ERR_INVALID_ARG;
   if (lse != nullptr && (reinterpret_cast<uintptr_t>(lse) & 3u) != 0) return QAT_ERR_INVALID_ARG;
-  if (workspace == nullptr || workspace_bytes < qat_attn_decode_workspace_bytes(Hq, Hkv, T, D))
-    return QAT_ERR_WORKSPACE;
+  if (most == qat::kTreeMaxTokens && (tree == nullptr || (reinterpret_cast<uintptr_t>(tree) & 7u) != 0))
+    return QAT_ERR_INVALID_ARG;
+  if (workspace == nullptr || workspace_bytes < over_cache_workspace(Hq, Hkv, T, D, most)) return QAT_ERR_WORKSPACE;
   if ((reinterpret_cast<uintptr_t>(workspace) & (kAlign - 1)) != 0) return QAT_ERR_INVALID_ARG;
   qat::DecodeArgs a = {};
   a.q = static_cast<const uint16_t*>(q);
@@ -675,9 +739,107 @@ qat_status_t qat_attn_decode(const void* q, const void* k_codes, const void* v_c
   a.max_pages = max_pages;
   a.quant = quant_mode != QAT_QUANT_NONE;
   a.qk_scale = sm_scale * kLog2e;
+  a.window = window < kMostKeys ? window : kMostKeys;  // of 2^30 positions, so that sums stay 32-bit
+  a.sinks = sinks < kMostKeys ? sinks : kMostKeys;
+  a.tree = tree;
+  a.tree_sb = tree_stride;
   int num_sms = 0;
   cudaError_t e = qat::device_context(&a.err, &num_sms);
   if (e == cudaSuccess) e = qat::launch_decode(a, D, num_sms, static_cast<cudaStream_t>(stream));
+  return from_cuda(e);
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t qat_attn_decode_workspace_bytes(int Hq, int Hkv, int T, int D) {
+  return over_cache_workspace(Hq, Hkv, T, D, qat::kDecodeMaxTokens);
+}
+
+qat_status_t qat_attn_decode(const void* q, const void* k_codes, const void* v_codes,
+                             const float* k_scales, const float* v_scales, const int* block_table,
+                             const int* seq_lens, void* o, float* lse, int B, int Hq, int Hkv,
+                             int T, int D, int num_pages, int page_size, int max_pages,
+                             float sm_scale, int quant_mode, void* workspace,
+                             size_t workspace_bytes, void* stream) {
+  return over_cache(q, k_codes, v_codes, k_scales, v_scales, block_table, seq_lens, nullptr, 0, o, lse, B, Hq, Hkv,
+                    T, qat::kDecodeMaxTokens, D, num_pages, page_size, max_pages, sm_scale, 0, 0, quant_mode,
+                    workspace, workspace_bytes, stream);
+}
+
+qat_status_t qat_attn_decode_window(const void* q, const void* k_codes, const void* v_codes, const float* k_scales,
+                                    const float* v_scales, const int* block_table, const int* seq_lens, void* o,
+                                    float* lse, int B, int Hq, int Hkv, int T, int D, int num_pages, int page_size,
+                                    int max_pages, float sm_scale, int window, int sinks, int quant_mode,
+                                    void* workspace, size_t workspace_bytes, void* stream) {
+  if (window < 1 || sinks < 0) return QAT_ERR_INVALID_ARG;
+  return over_cache(q, k_codes, v_codes, k_scales, v_scales, block_table, seq_lens, nullptr, 0, o, lse, B, Hq, Hkv,
+                    T, qat::kDecodeMaxTokens, D, num_pages, page_size, max_pages, sm_scale, window, sinks,
+                    quant_mode, workspace, workspace_bytes, stream);
+}
+
+size_t qat_attn_tree_workspace_bytes(int Hq, int Hkv, int T, int D) {
+  return over_cache_workspace(Hq, Hkv, T, D, qat::kTreeMaxTokens);
+}
+
+qat_status_t qat_attn_tree(const void* q, const void* k_codes, const void* v_codes, const float* k_scales,
+                           const float* v_scales, const int* block_table, const int* seq_lens,
+                           const unsigned long long* tree, long long tree_stride, void* o, float* lse, int B, int Hq,
+                           int Hkv, int T, int D, int num_pages, int page_size, int max_pages, float sm_scale,
+                           int window, int sinks, int quant_mode, void* workspace, size_t workspace_bytes,
+                           void* stream) {
+  if (window < 0 || sinks < 0 || tree_stride < 0 || (window == 0 && sinks > 0)) return QAT_ERR_INVALID_ARG;
+  return over_cache(q, k_codes, v_codes, k_scales, v_scales, block_table, seq_lens, tree, tree_stride, o, lse, B, Hq,
+                    Hkv, T, qat::kTreeMaxTokens, D, num_pages, page_size, max_pages, sm_scale, window, sinks,
+                    quant_mode, workspace, workspace_bytes, stream);
+}
+
+qat_status_t qat_draft_tree(const int* parents, long long parents_stride, const int* seq_lens,
+                            unsigned long long* tree, int* positions, int B, int T, void* stream) {
+  if (B < 0 || T < 0 || parents_stride < 0) return QAT_ERR_INVALID_ARG;
+  if (T > qat::kTreeMaxTokens) return QAT_ERR_UNSUPPORTED;
+  if (static_cast<long long>(B) * T > kMaxRows) return QAT_ERR_INVALID_ARG;
+  if (B == 0 || T == 0) return QAT_OK;
+  for (const void* p : {static_cast<const void*>(parents), static_cast<const void*>(seq_lens),
+                        static_cast<const void*>(positions)})
+    if (p == nullptr || (reinterpret_cast<uintptr_t>(p) & 3u) != 0) return QAT_ERR_INVALID_ARG;
+  if (tree == nullptr || (reinterpret_cast<uintptr_t>(tree) & 7u) != 0) return QAT_ERR_INVALID_ARG;
+  const qat::DraftTreeArgs a = {parents, parents_stride, seq_lens, tree, positions, B, T};
+  return from_cuda(qat::launch_draft_tree(a, static_cast<cudaStream_t>(stream)));
+}
+
+qat_status_t qat_kv_cache_keep(void* k_codes, void* v_codes, float* k_scales, float* v_scales,
+                               const int* block_table, const int* seq_lens, const int* path, const int* path_lens,
+                               int* new_lens, int B, int H, int T, int L, int D, int num_pages, int page_size,
+                               int max_pages, void* stream) {
+  if (B < 0 || T < 0 || L < 0) return QAT_ERR_INVALID_ARG;
+  const qat_status_t st = check_cache_sizes(H, D, num_pages, page_size, max_pages);
+  if (st != QAT_OK) return st;
+  if (T > qat::kTreeMaxTokens || L > T) return QAT_ERR_UNSUPPORTED;
+  if (static_cast<long long>(B) * H > kMaxRows) return QAT_ERR_INVALID_ARG;
+  if (B == 0) return QAT_OK;
+  if (!cache_pointers_ok(k_codes, v_codes, k_scales, v_scales, block_table, seq_lens)) return QAT_ERR_INVALID_ARG;
+  for (const int* p : {path_lens, static_cast<const int*>(new_lens)})
+    if (p == nullptr || (reinterpret_cast<uintptr_t>(p) & 3u) != 0) return QAT_ERR_INVALID_ARG;
+  if (L > 0 && (path == nullptr || (reinterpret_cast<uintptr_t>(path) & 3u) != 0)) return QAT_ERR_INVALID_ARG;
+  qat::KvKeepArgs a = {};
+  a.k_codes = static_cast<uint8_t*>(k_codes);
+  a.v_codes = static_cast<uint8_t*>(v_codes);
+  a.k_scales = k_scales;
+  a.v_scales = v_scales;
+  a.table = block_table;
+  a.seq_lens = seq_lens;
+  a.path = path;
+  a.path_lens = path_lens;
+  a.new_lens = new_lens;
+  a.B = B; a.H = H; a.T = T; a.L = L;
+  a.num_pages = num_pages;
+  a.page_shift = page_shift(page_size);
+  a.max_pages = max_pages;
+  int num_sms = 0;
+  cudaError_t e = qat::device_context(&a.err, &num_sms);
+  if (e == cudaSuccess) e = qat::launch_kv_keep(a, D, static_cast<cudaStream_t>(stream));
   return from_cuda(e);
 }
 

@@ -124,6 +124,8 @@ struct FwdArgs {
   float qk_scale;  // sm_scale * log2(e)
   int causal;
   int quant;
+  int window, sinks;  // window > 0 (causal only): key j also needs j > i - window or j < sinks;
+                      // both at most Nkv
   int kv_head_rows;  // rows between consecutive heads in K/V memory (Nkv unless a chunk)
   float* o_q_f32;    // when set (with o_hp_f32), fp32 outputs replace the bf16 ones
   float* o_hp_f32;
@@ -145,15 +147,57 @@ struct BwdArgs {
   uint16_t* lse_ext;  // bf16 [B, H, Nq_pad, 16] (see BwdWorkspace)
   uint16_t* d_ext;    // bf16 [B, H, Nq_pad, 16]
   uint16_t* ones;     // bf16 [128, 16]
-  float* part;        // dK/dV segment sums (BwdWorkspace::off_part) when sk_ctas > 0
+  float* part;        // dK/dV segment sums (BwdWorkspace::off_part) when sk_ctas > 0, or of the
+                      // sinks' key blocks when sink_pieces > 1
   const float* k_mean;  // fp32 [D] or null: smooth_k's channel mean (dQ's SMOOTH_K term)
   int sk_ctas;        // 0, or the stream-K CTA bound of bwd_stream_k_ctas (non-causal)
   int B, H, Nq, Nkv, D;
   float sm_scale;
   float qk_scale;
   int causal;
+  int window, sinks;  // as FwdArgs
+  int sink_pieces;    // window_sink_pieces
   int page_bwd;     // 1: dV from quantized P and Delta from the O passed (O_q)
 };
+
+// Sliding windows.  A 128-row query block mt sees the key blocks first .. mt of its rows' windows, and the
+// sinks' blocks 0 .. sinks - 1 before them: `count` in all, taken from the diagonal down, so that every
+// row has seen a key (its own) after the first and its running maximum is finite from then on.
+struct WindowBlocks {
+  int first, mt, sinks, count;
+#ifdef __CUDACC__
+  __device__ __forceinline__ WindowBlocks(int mt_, int window, int sink_keys) : mt(mt_) {
+    first = max(mt * 128 + 1 - window, 0) >> 7;
+    sinks = min((sink_keys + 127) >> 7, first);
+    count = mt - first + 1 + sinks;
+  }
+  __device__ __forceinline__ int at(int j) const {
+    const int inside = mt - first + 1;
+    return j < inside ? mt - j : inside + sinks - 1 - j;
+  }
+#endif
+};
+
+// Key blocks of 128 that hold sinks, whose dK and dV sum over all later queries, not a window's: each is cut
+// into this many pieces of query blocks, whose fp32 sums one more kernel adds in order.  A piece has at most
+// a quarter of an SM's share of all the work (or 4 blocks), so that the sinks of one long sequence do not
+// outlast the windows; none is empty.
+inline int window_sink_pieces(int B, int H, int N, int window, int sinks) {
+  const double heads = static_cast<double>(B) * H;
+  const int M = (N + 127) / 128, blocks = (sinks + 127) / 128;
+  if (blocks == 0) return 1;
+  const int each = (window + 254) / 128 < M ? (window + 254) / 128 : M;  // query blocks that see a key block
+  const double share = heads * (static_cast<double>(blocks) * M + static_cast<double>(M - blocks) * each) / 152.0;
+  const double piece = share / 4.0 < 4.0 ? 4.0 : share / 4.0;
+  const int most = M - blocks + 1;
+  const int want = static_cast<int>(ceil(M / piece));
+  return want < 1 ? 1 : (want < most ? want : most);
+}
+inline size_t window_part_bytes(int B, int H, int N, int D, int window, int sinks) {
+  const int n = window_sink_pieces(B, H, N, window, sinks);
+  if (n <= 1) return 0;
+  return static_cast<size_t>(B) * H * ((sinks + 127) / 128) * n * 2 * 128 * D * sizeof(float);
+}
 
 // Bits of the device error word: a bounded wait expired; a page index or a sequence length that
 // the cache or its table cannot hold.
@@ -236,8 +280,35 @@ struct DecodeArgs {
   unsigned int* err;
   int B, Hq, Hkv, T, num_pages, page_shift, max_pages, quant;
   float qk_scale;                    // sm_scale * log2(e)
+  int window, sinks;                 // window 0: every key before a row's own; else as FwdArgs, by positions
+  const unsigned long long* tree;    // drafted tokens' masks, or null: sequence b's begin at tree + b tree_sb
+  long long tree_sb;
 };
 
+constexpr int kTreeMaxTokens = 64;     // bits of a mask
+
+// Masks and positions of drafted trees; sequence b's parents begin at parents + b parents_sb.
+struct DraftTreeArgs {
+  const int* parents;
+  long long parents_sb;
+  const int* seq_lens;
+  unsigned long long* tree;          // [B, T]
+  int* positions;                    // [B, T]
+  int B, T;
+};
+
+// The move of accepted drafted rows behind the text.
+struct KvKeepArgs {
+  uint8_t *k_codes, *v_codes;
+  float *k_scales, *v_scales;
+  const int* table;
+  const int* seq_lens;
+  const int* path;                   // [B, L]
+  const int* path_lens;              // [B]
+  int* new_lens;                     // [B]
+  unsigned int* err;
+  int B, H, T, L, num_pages, page_shift, max_pages;
+};
 constexpr int kDecodeMaxBatch = 4096;  // the kernel keeps the batch's prefix sums in shared memory
 constexpr int kDecodeMaxTokens = 16;
 size_t decode_workspace_bytes(int R, int D);  // R = Hq / Hkv * T
@@ -283,6 +354,8 @@ cudaError_t launch_norm_rope(NormRopeArgs a, int D, int num_sms, cudaStream_t s)
 cudaError_t launch_norm_rope_bwd(NormRopeArgs a, int D, int num_sms, cudaStream_t s);
 cudaError_t launch_kv_append(const KvCacheArgs& a, int D, cudaStream_t s);
 cudaError_t launch_kv_read(const KvCacheArgs& a, int D, cudaStream_t s);
+cudaError_t launch_draft_tree(const DraftTreeArgs& a, cudaStream_t s);
+cudaError_t launch_kv_keep(const KvKeepArgs& a, int D, cudaStream_t s);
 cudaError_t launch_decode(const DecodeArgs& a, int D, int num_sms, cudaStream_t s);
 cudaError_t launch_fwd_tc(const FwdArgs& a, unsigned int* err, int num_sms, cudaStream_t s);
 // prep + dK/dV + dQ kernels

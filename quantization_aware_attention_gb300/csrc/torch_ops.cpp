@@ -512,33 +512,113 @@ std::tuple<Tensor, Tensor> kv_read(const Tensor& ck, const Tensor& cv, const Ten
   return {k, v};
 }
 
+// Masks (parents) of a batch's trees: [B, T], or [T] for all sequences; the step from one to the next.
+int64_t tree_stride(const Tensor& t, const char* name, at::ScalarType type, const at::Device& dev, int64_t B,
+                    int64_t T) {
+  TORCH_CHECK_VALUE(t.device() == dev, name, " must be a tensor on ", dev, ", got ", t.device());
+  TORCH_CHECK_VALUE(t.scalar_type() == type, name, " must be torch.", type == at::kLong ? "int64" : "int32", ", got ",
+                    t.scalar_type());
+  const auto sz = t.sizes();
+  TORCH_CHECK_VALUE((sz.size() == 1 && sz[0] == T) || (sz.size() == 2 && sz[0] == B && sz[1] == T), name,
+                    " has shape ", sz, ", expected [", B, ", ", T, "] or [", T, "]");
+  TORCH_CHECK_VALUE(T <= 1 || t.stride(-1) == 1, name, " must be contiguous along the tokens");
+  with_memory(t, name);
+  return sz.size() == 2 && B > 1 ? t.stride(0) : 0;
+}
+
+// With a tree: the last T tokens are drafted ones.
 py::object decode(const Tensor& ck, const Tensor& cv, const Tensor& cks, const Tensor& cvs, const Tensor& q,
-                  const Tensor& table, const Tensor& lens, std::optional<double> sm_scale, int quant_mode,
-                  bool return_lse, const OptTensor& workspace, std::optional<bool> check) {
+                  const Tensor& table, const Tensor& lens, const OptTensor& tree, std::optional<double> sm_scale,
+                  int quant_mode, bool return_lse, const OptTensor& workspace, std::optional<bool> check,
+                  std::optional<int64_t> window, int64_t sinks) {
+  const char* what = tree.has_value() ? "qat_attention_tree" : "qat_attention_decode";
   const Cache c = cache_of(ck, cv, cks, cvs, table, lens);
   const Rows rq = rows(q, "q", c.dev, {c.B, -1, -1, c.D});
   TORCH_CHECK_VALUE(rq.dense, "q must be contiguous");
-  no_gradient("qat_attention_decode", q);
-  no_tangent("qat_attention_decode", {&q});
+  no_gradient(what, q);
+  no_tangent(what, {&q});
+  TORCH_CHECK_VALUE(window.has_value() || sinks == 0, "sinks go together with a window");
+  TORCH_CHECK_VALUE((!window.has_value() || *window >= 1) && sinks >= 0, "window must be at least 1 and sinks at "
+                    "least 0, got ", window.value_or(1), " and ", sinks);
   const int64_t Hq = q.size(1), T = q.size(2);
   TORCH_CHECK_VALUE(Hq >= 1 && Hq % c.H == 0, Hq, " query heads do not share the cache's ", c.H, " evenly");
+  const int64_t tree_sb = tree.has_value() ? tree_stride(*tree, "tree", at::kLong, c.dev, c.B, T) : 0;
+  const auto limited = [](int64_t x) { return static_cast<int>(std::min<int64_t>(x, INT32_MAX)); };
   const c10::cuda::CUDAGuard guard(c.dev);
-  const size_t bytes = qat_attn_decode_workspace_bytes(static_cast<int>(Hq), static_cast<int>(c.H),
-                                                       static_cast<int>(std::min<int64_t>(T, 1 << 20)),
-                                                       static_cast<int>(c.D));
+  const auto workspace_bytes = tree.has_value() ? qat_attn_tree_workspace_bytes : qat_attn_decode_workspace_bytes;
+  const size_t bytes = workspace_bytes(static_cast<int>(Hq), static_cast<int>(c.H),
+                                       static_cast<int>(std::min<int64_t>(T, 1 << 20)), static_cast<int>(c.D));
   const Tensor ws = workspace_or_new(workspace, std::max<int64_t>(static_cast<int64_t>(bytes), 256), c.dev);
   Tensor o = new_tensor(q.sizes(), at::kBFloat16, c.dev), lse;
   if (return_lse) lse = new_tensor({c.B, Hq, T}, at::kFloat, c.dev);
-  ok(qat_attn_decode(q.const_data_ptr(), c.k, c.v, c.ks, c.vs, c.table, c.lens, o.mutable_data_ptr(),
-                     return_lse ? lse.mutable_data_ptr<float>() : nullptr, static_cast<int>(c.B),
-                     static_cast<int>(Hq), static_cast<int>(c.H), static_cast<int>(T), static_cast<int>(c.D),
-                     static_cast<int>(c.pages), static_cast<int>(c.page), static_cast<int>(c.max_pages),
-                     static_cast<float>(sm_scale.has_value() ? *sm_scale : 1.0 / std::sqrt(static_cast<double>(c.D))),
-                     quant_mode, ws.mutable_data_ptr(), static_cast<size_t>(ws.numel()), stream_of(c.dev)),
-     "qat_attn_decode");
-  check_status(check, c.dev, "qat_attn_decode");
+  float* lse_ptr = return_lse ? lse.mutable_data_ptr<float>() : nullptr;
+  const int B = static_cast<int>(c.B), Hkv = static_cast<int>(c.H), D = static_cast<int>(c.D);
+  const int pages = static_cast<int>(c.pages), page = static_cast<int>(c.page);
+  const int max_pages = static_cast<int>(c.max_pages);
+  const float scale = static_cast<float>(sm_scale.has_value() ? *sm_scale : 1.0 / std::sqrt(static_cast<double>(c.D)));
+  const size_t ws_bytes = static_cast<size_t>(ws.numel());
+  if (tree.has_value()) {
+    what = "qat_attn_tree";
+    ok(qat_attn_tree(q.const_data_ptr(), c.k, c.v, c.ks, c.vs, c.table, c.lens,
+                     static_cast<const unsigned long long*>(tree->const_data_ptr()), tree_sb, o.mutable_data_ptr(),
+                     lse_ptr, B, static_cast<int>(Hq), Hkv, static_cast<int>(T), D, pages, page, max_pages, scale,
+                     limited(window.value_or(0)), limited(sinks), quant_mode, ws.mutable_data_ptr(), ws_bytes,
+                     stream_of(c.dev)),
+       what);
+  } else if (window.has_value()) {
+    what = "qat_attn_decode_window";
+    ok(qat_attn_decode_window(q.const_data_ptr(), c.k, c.v, c.ks, c.vs, c.table, c.lens, o.mutable_data_ptr(),
+                              lse_ptr, B, static_cast<int>(Hq), Hkv, static_cast<int>(T), D, pages, page, max_pages,
+                              scale, limited(*window), limited(sinks), quant_mode, ws.mutable_data_ptr(), ws_bytes,
+                              stream_of(c.dev)),
+       what);
+  } else {
+    what = "qat_attn_decode";
+    ok(qat_attn_decode(q.const_data_ptr(), c.k, c.v, c.ks, c.vs, c.table, c.lens, o.mutable_data_ptr(), lse_ptr, B,
+                       static_cast<int>(Hq), Hkv, static_cast<int>(T), D, pages, page, max_pages, scale, quant_mode,
+                       ws.mutable_data_ptr(), ws_bytes, stream_of(c.dev)),
+       what);
+  }
+  check_status(check, c.dev, what);
   if (return_lse) return py::make_tuple(o, lse);
   return py::cast(o);
+}
+
+std::tuple<Tensor, Tensor> draft_tree(const Tensor& parents, const Tensor& lens) {
+  on_cuda(parents, "parents");
+  const at::Device dev = parents.device();
+  const int* seq_lens = index_ptr(lens, "seq_lens", dev, -1, -2);
+  const int64_t B = lens.size(0), T = parents.dim() > 0 ? parents.size(-1) : 0;
+  const int64_t sb = tree_stride(parents, "parents", at::kInt, dev, B, T);
+  TORCH_CHECK_VALUE(T <= 64, "a tree has at most 64 tokens, got ", T);
+  TORCH_CHECK_VALUE(B <= INT32_MAX, "seq_lens is too large");
+  const c10::cuda::CUDAGuard guard(dev);
+  Tensor tree = new_tensor({B, T}, at::kLong, dev), positions = new_tensor({B, T}, at::kInt, dev);
+  ok(qat_draft_tree(parents.const_data_ptr<int>(), sb, seq_lens,
+                    static_cast<unsigned long long*>(tree.mutable_data_ptr()), positions.mutable_data_ptr<int>(),
+                    static_cast<int>(B), static_cast<int>(T), stream_of(dev)),
+     "qat_draft_tree");
+  return {tree, positions};
+}
+
+Tensor kv_keep(const Tensor& ck, const Tensor& cv, const Tensor& cks, const Tensor& cvs, const Tensor& table,
+               const Tensor& lens, int64_t T, const Tensor& path, const Tensor& path_lens,
+               std::optional<bool> check) {
+  const Cache c = cache_of(ck, cv, cks, cvs, table, lens);
+  const int* rows_of = index_ptr(path, "path", c.dev, c.B, -1);
+  const int64_t L = path.size(1);
+  const int* kept = index_ptr(path_lens, "path_lens", c.dev, c.B, -2);
+  TORCH_CHECK_VALUE(T >= 0 && T <= 64, "drafted must lie in 0 .. 64, got ", T);
+  TORCH_CHECK_VALUE(L <= T, "path has ", L, " places for ", T, " drafted tokens");
+  const c10::cuda::CUDAGuard guard(c.dev);
+  Tensor out = new_tensor({c.B}, at::kInt, c.dev);
+  ok(qat_kv_cache_keep(c.k, c.v, c.ks, c.vs, c.table, c.lens, rows_of, kept, out.mutable_data_ptr<int>(),
+                       static_cast<int>(c.B), static_cast<int>(c.H), static_cast<int>(T), static_cast<int>(L),
+                       static_cast<int>(c.D), static_cast<int>(c.pages), static_cast<int>(c.page),
+                       static_cast<int>(c.max_pages), stream_of(c.dev)),
+     "qat_kv_cache_keep");
+  check_status(check, c.dev, "qat_kv_cache_keep");
+  return out;
 }
 
 // ------------------------------------------------------------------------------- Python
@@ -634,16 +714,41 @@ PyObject* py_kv_read(PyObject*, PyObject* const* args, Py_ssize_t n) {
 
 PyObject* py_decode(PyObject*, PyObject* const* args, Py_ssize_t n) {
   HANDLE_TH_ERRORS
-  Args a(args, n, 12);
+  Args a(args, n, 15);
   const Tensor &ck = a.tensor(), &cv = a.tensor(), &cks = a.tensor(), &cvs = a.tensor(), &q = a.tensor(),
                &table = a.tensor(), &lens = a.tensor();
+  const OptTensor tree = a.optional_tensor();
   const std::optional<double> sm_scale = a.optional_real();
   const int64_t quant_mode = a.integer();
   TORCH_CHECK_VALUE(quant_mode >= INT32_MIN && quant_mode <= INT32_MAX, "quant_mode ", quant_mode);
   const bool return_lse = a.boolean();
   const OptTensor workspace = a.optional_tensor();
-  return decode(ck, cv, cks, cvs, q, table, lens, sm_scale, static_cast<int>(quant_mode), return_lse, workspace,
-                a.optional_boolean())
+  const std::optional<bool> check = a.optional_boolean();
+  const std::optional<int64_t> window = a.optional_integer();
+  return decode(ck, cv, cks, cvs, q, table, lens, tree, sm_scale, static_cast<int>(quant_mode), return_lse, workspace,
+                check, window, a.integer())
+      .release()
+      .ptr();
+  END_HANDLE_TH_ERRORS
+}
+
+PyObject* py_draft_tree(PyObject*, PyObject* const* args, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  Args a(args, n, 2);
+  const Tensor &parents = a.tensor(), &lens = a.tensor();
+  const auto out = draft_tree(parents, lens);
+  return py::make_tuple(std::get<0>(out), std::get<1>(out)).release().ptr();
+  END_HANDLE_TH_ERRORS
+}
+
+PyObject* py_kv_keep(PyObject*, PyObject* const* args, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  Args a(args, n, 10);
+  const Tensor &ck = a.tensor(), &cv = a.tensor(), &cks = a.tensor(), &cvs = a.tensor(), &table = a.tensor(),
+               &lens = a.tensor();
+  const int64_t drafted = a.integer();
+  const Tensor &path = a.tensor(), &path_lens = a.tensor();
+  return py::cast(kv_keep(ck, cv, cks, cvs, table, lens, drafted, path, path_lens, a.optional_boolean()))
       .release()
       .ptr();
   END_HANDLE_TH_ERRORS
@@ -660,6 +765,7 @@ PYBIND11_MODULE(_qat_torch, m) {
   m.def("norm_rope_bwd", &norm_rope_bwd);
   static PyMethodDef methods[] = {method<py_norm_rope>("norm_rope"), method<py_kv_append>("kv_append"),
                                   method<py_kv_read>("kv_read"), method<py_decode>("decode"),
+                                  method<py_draft_tree>("draft_tree"), method<py_kv_keep>("kv_keep"),
                                   {nullptr, nullptr, 0, nullptr}};
   if (PyModule_AddFunctions(m.ptr(), methods) != 0) throw py::error_already_set();
 }
