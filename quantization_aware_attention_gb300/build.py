@@ -28,7 +28,8 @@ EXT_SOURCE = "torch_ops.cpp"
 
 SOURCES = ["qat_api.cu", "attn_fwd_sm100.cu", "attn_bwd_sm100.cu", "attn_bwd_dq_sm100.cu",
            "quant_debug.cu", "qat_noalloc.cu", "qkv_quant.cu", "attn_merge.cu", "debug_wait.cu",
-           "qk_norm_rope.cu", "kv_cache.cu", "attn_decode.cu", "draft_tree.cu"]
+           "qk_norm_rope.cu", "kv_cache.cu", "attn_decode.cu",
+           "attn_tree_sm100.cu", "draft_tree.cu"]
 GENCODE = "-gencode=arch=compute_103a,code=sm_103a"
 NVCC_FLAGS = [GENCODE, "-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC",
               "-Xcompiler", "-fvisibility=hidden", "--expt-relaxed-constexpr",

@@ -1,0 +1,658 @@
+// attn_tree_sm100.cu -- attention of many rows a KV head over the FP8 cache (a drafted tree, the tokens of a window)
+// on the Blackwell tensor core: tcgen05 products with the queries as the 128-row operand.
+//
+// Per query row (head, token) and key j that it sees:
+//   s_j = sm_scale <q, k_j>,  k_j = code_j scale_j;  p_j = exp(s_j - m);  l = sum p_j
+//   quantized: per absolute 64-key tile amax = max p, p'_j = E4M3(p_j 448 / amax) amax / 448
+//   o = sum p'_j v_j / l;  lse = log2 sum exp(s_j).  A row that sees no key: o = 0, lse = -inf.
+#include "cache_split.cuh"
+#include "qat_internal.h"
+#include "qat_quant.cuh"
+#include "sm100.cuh"
+
+#include <cuda_bf16.h>
+
+#include <type_traits>
+
+namespace qat {
+namespace {
+
+using namespace sm100;
+
+constexpr int kStep = 128;     // keys of a step
+constexpr int kM = 128;        // query rows of an item
+constexpr int kThreads = 512;  // warp 0 producer, 1 products, 4-5 K and 6-7 V converters, 8-15 softmax
+constexpr int kStages = 3;     // steps whose codes are on their way or in shared memory
+constexpr int kScStages = 6;   // steps whose scales are
+constexpr float kRaise = 8.0f; // log2: the running maximum is raised when it is this far behind
+
+template <int D>
+struct Tc {
+  static constexpr int kChunks = D / 64;                // 128-byte column chunks of a bf16 row
+  static constexpr uint32_t kChunkBytes = kStep * 128;  // 128 rows x 64 columns
+  static constexpr uint32_t kTileBytes = kChunks * kChunkBytes;
+  static constexpr uint32_t kCodes = kStep * D;         // bytes of a step's codes of K, and of V
+  static constexpr uint32_t kOffQ = 0;
+  static constexpr uint32_t kOffK = kOffQ + kTileBytes;
+  static constexpr uint32_t kOffV = kOffK + kTileBytes;
+  static constexpr uint32_t kOffRing = kOffV + kTileBytes;        // codes: K, then V, of each stage
+  static constexpr uint32_t kOffSc = kOffRing + kStages * 2 * kCodes;  // scales: K, then V
+  static constexpr uint32_t kOffBar = kOffSc + kScStages * 8 * kStep;
+  static constexpr uint32_t kOffMisc = kOffBar + 320;
+  static constexpr uint32_t kOffX = kOffMisc + 64;                // row maxima [2][2][128], row sums [2][128]
+  static constexpr uint32_t kOffSum = kOffX + 3072;               // the warps' sums, then B + 1 prefix sums
+  static constexpr uint32_t kUsed = kOffSum + 4 * (kThreads / 32);
+  static constexpr uint32_t kTmemO = 256;
+};
+
+enum : uint32_t {
+  T_CODES = 0, T_CODES_FREE = T_CODES + kStages, T_SC = T_CODES_FREE + kStages, T_SC_FREE = T_SC + kScStages,
+  T_Q = T_SC_FREE + kScStages, T_Q_FREE, T_K, T_K_FREE, T_V, T_V_FREE, T_S, T_P = T_S + 2, T_O_DONE = T_P + 2,
+  T_O_LAST, T_O_FREE, T_DRAIN, T_X, T_COUNT = T_X + 4
+};
+static_assert(T_COUNT * 8 <= 320, "barrier block");
+
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+  const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
+
+// Copies `bytes` (a multiple of 16, both addresses on 16-byte boundaries) and completes them on `bar`.
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst), "l"(src),
+      "r"(bytes), "r"(bar)
+      : "memory");
+}
+__device__ __forceinline__ void fence_async() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+
+__device__ __forceinline__ uint4 lds16(uint32_t a) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a) : "memory");
+  return v;
+}
+__device__ __forceinline__ void sts16(uint32_t a, uint4 v) {
+  asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(a), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
+}
+
+// Four E4M3 codes (never NaN) to bf16, exactly: the code's exponent and fraction are those of a bf16 number
+// 2^120 times smaller, subnormal codes included.
+__device__ __forceinline__ uint2 codes_to_bf16x4(uint32_t x) {
+  const uint32_t lo = __byte_perm(x, 0, 0x1404), hi = __byte_perm(x, 0, 0x3424);
+  const uint32_t a = ((lo >> 4) & 0x07f007f0u) | (lo & 0x80008000u), b = ((hi >> 4) & 0x07f007f0u) | (hi & 0x80008000u);
+  const uint32_t up = 0x7b807b80u;  // 2^120
+  uint2 r;
+  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r.x) : "r"(a), "r"(up));
+  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r.y) : "r"(b), "r"(up));
+  return r;
+}
+
+// A worker's part of an item: `count` steps from the cursor's on.
+__device__ __forceinline__ int segment_steps(const Cursor& c, int u, int u1) { return min(c.tiles - c.tile, u1 - u); }
+
+// The cursor and unit behind a segment.
+__device__ __forceinline__ void leave(const Params& p, const int* prefix, int extra, int count, Cursor& c, int& u) {
+  u += count - 1;
+  c.tile += count - 1;
+  advance<kTree, kStep>(p, prefix, extra, c, u);
+}
+
+// What hides keys in the step at place `at`: the tree and the end, or the beginnings of windows.
+__device__ __forceinline__ bool at_edge(const DecodeArgs& a, const Cursor& c, int at) {
+  return (at + 1) * kStep > c.len - a.T ||
+         (a.window > 0 && at * kStep < c.len - a.window && (at + 1) * kStep > a.sinks);
+}
+
+// Ones in bits [from, to), both clamped to 0 .. 64.
+__device__ __forceinline__ unsigned long long ones(int from, int to) {
+  from = min(max(from, 0), 64);
+  to = min(max(to, 0), 64);
+  if (to <= from) return 0ull;
+  const unsigned long long upto = to == 64 ? ~0ull : (1ull << to) - 1;
+  return upto & ~((1ull << from) - 1);
+}
+
+// The keys of key0 .. key0 + 63 that a row does not see; mask: the tokens it sees; pos: its position.
+__device__ __forceinline__ unsigned long long hidden_keys(const DecodeArgs& a, int len, int key0, int pos,
+                                                          unsigned long long mask) {
+  const int base = len - a.T;
+  unsigned long long seen = ones(0, base - key0);
+  if (a.window > 0) seen &= ~ones(max(a.sinks - key0, 0), pos - a.window + 1 - key0);
+  if (a.T < 64) mask &= (1ull << a.T) - 1;
+  const int at = base - key0;  // where the first token's key lies
+  if (at >= 0)
+    seen |= at < 64 ? mask << at : 0ull;
+  else
+    seen |= at > -64 ? mask >> -at : 0ull;
+  return ~seen;
+}
+
+template <int D, bool kQuant>
+__global__ void __launch_bounds__(kThreads, 1) tree_kernel(const Params p) {
+  using C = Tc<D>;
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t raw = smem_addr(smem_raw), base = (raw + 1023u) & ~1023u;
+  uint8_t* gbase = smem_raw + (base - raw);
+  const uint32_t bars = base + C::kOffBar;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(gbase + C::kOffMisc);
+  volatile WaitCtl* ctl = reinterpret_cast<volatile WaitCtl*>(gbase + C::kOffMisc + 8);
+  int* warp_sum = reinterpret_cast<int*>(gbase + C::kOffSum);
+  int* prefix = warp_sum + kThreads / 32;
+  const auto bar = [&](uint32_t i) { return bars + 8u * i; };
+  const DecodeArgs& a = p.a;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+
+  if (tid == 0) {
+    wait_ctl_init(ctl, a.err);
+    for (int i = 0; i < kStages; ++i) {
+      mbar_init(bar(T_CODES + i), 1);
+      mbar_init(bar(T_CODES_FREE + i), 128);
+    }
+    for (int i = 0; i < kScStages; ++i) {
+      mbar_init(bar(T_SC + i), 1);
+      mbar_init(bar(T_SC_FREE + i), 256);
+    }
+    mbar_init(bar(T_Q), 256);
+    mbar_init(bar(T_Q_FREE), 1);
+    mbar_init(bar(T_K), 64);
+    mbar_init(bar(T_K_FREE), 1);
+    mbar_init(bar(T_V), 64);
+    mbar_init(bar(T_V_FREE), 1);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(bar(T_S + i), 1);
+      mbar_init(bar(T_P + i), 256);
+    }
+    mbar_init(bar(T_O_DONE), 1);
+    mbar_init(bar(T_O_LAST), 1);
+    mbar_init(bar(T_O_FREE), 256);
+    mbar_init(bar(T_DRAIN), 1);
+    for (int i = 0; i < 4; ++i) mbar_init(bar(T_X + i), 64);
+    fence_barrier_init();
+  }
+  if (warp == 1) {
+    tmem_alloc(smem_addr(tmem_slot), 512);
+    tmem_relinquish();
+  }
+  after_previous();
+
+  // prefix[b] = steps before sequence b
+  const int per_seq = a.Hkv * p.mtiles;
+  {
+    const int chunk = (a.B + kThreads - 1) / kThreads;
+    const int b0 = min(tid * chunk, a.B), b1 = min(b0 + chunk, a.B);
+    int sum = 0;
+    for (int b = b0; b < b1; ++b) {
+      const int len = a.seq_lens[b], fits = clamp_len(a, len);
+      if (len > fits) atomicOr(a.err, kErrBadPage);
+      Cursor c;
+      find_gap<kTree, kStep>(a, fits, c);
+      prefix[b] = (tiles_of<kStep>(fits) - c.gap) * per_seq;
+      sum += prefix[b];
+    }
+    int inc = sum;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int x = __shfl_up_sync(0xffffffffu, inc, o);
+      if (lane >= o) inc += x;
+    }
+    if (lane == 31) warp_sum[warp] = inc;
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    int before = inc - sum;
+    for (int w = 0; w < warp; ++w) before += warp_sum[w];
+    for (int b = b0; b < b1; ++b) {
+      const int units = prefix[b];
+      prefix[b] = before;
+      before += units;
+    }
+    if (tid == kThreads - 1) prefix[a.B] = before;
+    __syncthreads();
+  }
+  const uint32_t tbase = *tmem_slot;
+  const int steps = prefix[a.B], workers = min(steps, static_cast<int>(gridDim.x)), id = blockIdx.x;
+  if (id == 0 && tid == 0) header_of(p)->workers = workers;
+  // an item's own unit, where ranges are long enough that each holds a step all the same
+  const int extra = steps / 4 >= workers ? 1 : 0;
+  const int W = steps + extra * a.B * per_seq;
+  const unsigned each = static_cast<unsigned>(W) / workers, over = W - each * workers;
+  int u0 = 0, u1 = 0;
+  Cursor first = {};
+  if (id < workers) {
+    u0 = each * id + over * id / workers;
+    u1 = each * (id + 1) + over * (id + 1) / workers;
+    int lo = 0, hi = a.B;  // the last b whose units begin at u0 or before
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (prefix[mid] + extra * mid * per_seq <= u0) lo = mid; else hi = mid;
+    }
+    first.b = lo;
+    enter_seq<kTree, kStep>(p, prefix, first);
+    const int u = u0 - (prefix[lo] + extra * lo * per_seq);
+    const int item = u / (first.tiles + extra), in = u - item * (first.tiles + extra);
+    first.tile = max(in - extra, 0);
+    if (in < extra) ++u0;  // to the item's first step
+    first.mt = item % p.mtiles;
+    first.h = item / p.mtiles;
+  }
+  Cursor c = first;
+  int u = u0;
+  bool ok = true;
+  const auto wait = [&](uint32_t i, uint32_t parity) { return mbar_wait(bar(i), parity & 1, ctl, a.err); };
+  const auto wwait = [&](uint32_t i, uint32_t parity) {  // the same answer in every lane
+    return __all_sync(0xffffffffu, wait(i, parity)) != 0;
+  };
+
+  if (warp == 0) {
+    // ------------------------------------------------------------ producer
+    uint32_t n = 0;
+    uint32_t rows_of = kNoPage;  // lane l: cache row where chunk l of a group of 4 steps begins
+    bool fresh = true;
+    while (u < u1) {
+      if (fresh || (c.tile & 3) == 0) {
+        const int pos = place_of<kTree>(c, (c.tile & ~3) + (lane >> 3)) * kStep + (lane & 7) * kChunk;
+        // pages that hold nothing any row sees are not looked up: they may have been given back
+        const bool unseen = pos + kChunk <= c.low && pos >= a.sinks;
+        rows_of = kNoPage;
+        if (pos < c.len && !unseen) {
+          const int page = a.table[static_cast<long long>(c.b) * a.max_pages + (pos >> a.page_shift)];
+          rows_of = kBadPage;
+          if (page >= 0 && page < a.num_pages)
+            rows_of = ((static_cast<uint32_t>(page) * a.Hkv + c.h) << a.page_shift) + (pos & ((1 << a.page_shift) - 1));
+          else
+            atomicOr(a.err, kErrBadPage);
+        }
+        fresh = false;
+      }
+      const uint32_t st = n % kStages, sc = n % kScStages;
+      if (!(ok = wwait(T_CODES_FREE + st, (n / kStages & 1) ^ 1) && wwait(T_SC_FREE + sc, (n / kScStages & 1) ^ 1))) break;
+      const uint32_t rc = __shfl_sync(0xffffffffu, rows_of, (c.tile & 3) * 8 + (lane & 7));
+      const uint32_t there = __ballot_sync(0xffffffffu, rc < kBadPage) & 0xffu;
+      const uint32_t bad = __ballot_sync(0xffffffffu, rc == kBadPage) & 0xffu;
+      const uint32_t ring = base + C::kOffRing + st * 2 * C::kCodes, scales = base + C::kOffSc + sc * 8 * kStep;
+      for (uint32_t rest = ~there & 0xffu; rest != 0; rest &= rest - 1) {  // zeros; NaN scales for bad pages
+        const int k = __ffs(rest) - 1;
+        const uint32_t fill = (bad >> k & 1u) ? 0x7fc00000u : 0u;
+#pragma unroll
+        for (int i = 0; i < kChunk * D / 512; ++i) {
+          sts16(ring + k * kChunk * D + 512 * i + 16 * lane, make_uint4(0u, 0u, 0u, 0u));
+          sts16(ring + C::kCodes + k * kChunk * D + 512 * i + 16 * lane, make_uint4(0u, 0u, 0u, 0u));
+        }
+        if (lane < 8)  // lanes 0-3: K's, 4-7: V's
+          sts16(scales + (lane >> 2) * 4 * kStep + k * 4 * kChunk + 16 * (lane & 3), make_uint4(fill, fill, fill, fill));
+        fence_async();  // a later step's copies go there
+      }
+      __syncwarp();
+      if (lane == 0) {
+        const uint32_t chunks = __popc(there);
+        mbar_arrive_expect_tx(bar(T_CODES + st), chunks * 2 * kChunk * D);
+        mbar_arrive_expect_tx(bar(T_SC + sc), chunks * 2 * 4 * kChunk);
+      }
+      __syncwarp();
+      // lanes 0-7: the chunks' K, 8-15: V, 16-23: K's scales, 24-31: V's
+      if (rc < kBadPage) {
+        const int k = lane & 7;
+        if (lane < 16)
+          bulk_load(ring + (lane >> 3) * C::kCodes + k * kChunk * D,
+                    (lane < 8 ? a.k_codes : a.v_codes) + static_cast<size_t>(rc) * D, kChunk * D, bar(T_CODES + st));
+        else
+          bulk_load(scales + (lane >> 3 & 1) * 4 * kStep + k * 4 * kChunk, (lane < 24 ? a.k_scales : a.v_scales) + rc,
+                    4 * kChunk, bar(T_SC + sc));
+      }
+      ++n;
+      const int b = c.b, h = c.h;
+      advance<kTree, kStep>(p, prefix, extra, c, u);
+      fresh = c.b != b || c.h != h;
+    }
+    // every copy lands before the CTA exits
+    for (uint32_t i = n > kStages ? n - kStages : 0; i < n; ++i) mbar_wait_drain(bar(T_CODES + i % kStages), i / kStages & 1, a.err);
+    for (uint32_t i = n > kScStages ? n - kScStages : 0; i < n; ++i) mbar_wait_drain(bar(T_SC + i % kScStages), i / kScStages & 1, a.err);
+  } else if (warp == 1) {
+    // ------------------------------------------------------------ products
+    if (lane == 0) {
+      constexpr uint32_t idS = idesc_bf16_f32(kM, kStep, false), idO = idesc_bf16_f32(kM, D, true);
+      uint32_t n = 0, it = 0;
+      bool issued = false;
+      const auto issue_s = [&](uint32_t k, bool last) {  // S of step k, into the buffer that held P of step k - 2
+        if (!wait(T_K, k)) return false;
+        tc_fence_after();
+#pragma unroll
+        for (int ks = 0; ks < D / 16; ++ks) {
+          const uint32_t off = (ks >> 2) * C::kChunkBytes + (ks & 3) * 32;
+          mma_ss(tbase + (k & 1) * 128, smem_desc_sw128(base + C::kOffQ + off, 16, 1024),
+                 smem_desc_sw128(base + C::kOffK + off, 16, 1024), idS, ks > 0 ? 1u : 0u);
+        }
+        issued = true;
+        mma_commit(bar(T_K_FREE));
+        mma_commit(bar(T_S + (k & 1)));
+        if (last) mma_commit(bar(T_Q_FREE));
+        return true;
+      };
+      for (; u < u1 && ok; ++it) {
+        const int count = segment_steps(c, u, u1);
+        ok = wait(T_Q, it) && issue_s(n, count == 1);
+        for (int j = 0; j < count && ok; ++j, ++n) {
+          if (j + 1 < count && !(ok = issue_s(n + 1, j + 2 == count))) break;
+          if (!(ok = wait(T_V, n) && wait(T_P + (n & 1), n >> 1))) break;
+          if (j == 0 && !(ok = wait(T_O_FREE, it + 1))) break;
+          tc_fence_after();
+#pragma unroll
+          for (int ks = 0; ks < kStep / 16; ++ks)
+            mma_ts(tbase + C::kTmemO, tbase + (n & 1) * 128 + 8 * ks,
+                   smem_desc_sw128(base + C::kOffV + ks * 2048, C::kChunkBytes, 1024), idO, (j > 0 || ks > 0) ? 1u : 0u);
+          mma_commit(bar(T_V_FREE));
+          mma_commit(bar(T_O_DONE));
+          if (j + 1 == count) mma_commit(bar(T_O_LAST));
+        }
+        if (ok) leave(p, prefix, extra, count, c, u);
+      }
+      if (issued) {
+        mma_commit(bar(T_DRAIN));
+        mbar_wait_drain(bar(T_DRAIN), 0, a.err);
+      }
+    }
+  } else if (warp >= 4 && warp < 8) {
+    // ------------------------------------------------------------ codes to bf16 operands
+    // Warps 4 and 5 bring K's codes of each step into the 128-byte swizzled layout that the products read, 6
+    // and 7 V's.  Lane groups of a row's 16-byte pieces; the two 16-byte halves of what a piece becomes are
+    // written in the order that keeps eight lanes on different banks.
+    const bool value = warp >= 6;
+    const int t = tid & 63;
+    constexpr int kPieces = D / 16, kEach = kStep * kPieces / 64;
+    const uint32_t out = base + (value ? C::kOffV : C::kOffK);
+    for (uint32_t n = 0; u < u1; ++n) {
+      const int left = c.len - place_of<kTree>(c, c.tile) * kStep;
+      const uint32_t st = n % kStages, ring = base + C::kOffRing + st * 2 * C::kCodes + (value ? C::kCodes : 0);
+      if (!wait(T_CODES + st, n / kStages) || !wait(value ? T_V_FREE : T_K_FREE, n + 1)) break;
+#pragma unroll
+      for (int i0 = 0; i0 < kEach; i0 += 4) {
+        uint4 x[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) x[i] = lds16(ring + 16 * (t + 64 * (i0 + i)));
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int row = (t + 64 * (i0 + i)) / kPieces, piece = t % kPieces;
+          if (row >= left) x[i] = make_uint4(0u, 0u, 0u, 0u);  // behind the end: may hold anything
+          const uint2 w0 = codes_to_bf16x4(x[i].x), w1 = codes_to_bf16x4(x[i].y), w2 = codes_to_bf16x4(x[i].z),
+                      w3 = codes_to_bf16x4(x[i].w);
+          const uint4 lo = make_uint4(w0.x, w0.y, w1.x, w1.y), hi = make_uint4(w2.x, w2.y, w3.x, w3.y);
+          const uint32_t at = out + (piece >> 2) * C::kChunkBytes + row * 128, swz = row & 7, at0 = 2 * piece & 7;
+          const bool odd = piece & 4;
+          sts16(at + (((at0 + (odd ? 1 : 0)) ^ swz) << 4), odd ? hi : lo);
+          sts16(at + (((at0 + (odd ? 0 : 1)) ^ swz) << 4), odd ? lo : hi);
+        }
+      }
+      fence_async();
+      mbar_arrive(bar(value ? T_V : T_K));
+      mbar_arrive(bar(T_CODES_FREE + st));
+      advance<kTree, kStep>(p, prefix, extra, c, u);
+    }
+  } else if (warp >= 8) {
+    // ------------------------------------------------------------ softmax, two groups of four warps
+    // h = 0 has keys 0-63 of every row of S, h = 1 keys 64-127: a thread one row of one quantization tile.
+    const int h = (warp - 8) >> 2, quarter = warp & 3, r = 32 * quarter + lane;
+    const uint32_t lrow = (32u * quarter) << 16;
+    float* xmax = reinterpret_cast<float*>(gbase + C::kOffX);         // [2][2 h][128]
+    float* xsum = reinterpret_cast<float*>(gbase + C::kOffX + 2048);  // [2 h][128]
+    uint32_t xc = 0;
+    const auto exchange = [&]() {  // between the two threads of a row (and their warps)
+      tc_fence_before();
+      mbar_arrive(bar(T_X + quarter));
+      const bool w = wwait(T_X + quarter, xc);
+      ++xc;
+      tc_fence_after();
+      return w;
+    };
+    // This thread's row of the item at c: half h of it goes to shared memory times a power of two that takes its
+    // largest element to 1 .. 2 (times 2^-32, so that products with large scales stay finite, unless that takes
+    // rf out of range); scores are S scale_k rf.
+    unsigned long long mask = 0ull;
+    int pos = 0;
+    float rf = 0.f;
+    const auto load_q = [&](const Cursor& at) {
+      const int row = at.mt * kM + r;
+      uint4 x[D / 16];
+      float amax = 0.f;
+      const uint4* src = reinterpret_cast<const uint4*>(
+          a.q + ((static_cast<size_t>(at.b) * a.Hkv + at.h) * p.R + row) * D + (D / 2) * h);
+#pragma unroll
+      for (int i = 0; i < D / 16; ++i) x[i] = row < p.R ? src[i] : make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+      for (int i = 0; i < D / 16; ++i) {
+        const uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          amax = fmaxf(amax, fmaxf(fabsf(__uint_as_float(w[k] << 16)), fabsf(__uint_as_float(w[k] & 0xffff0000u))));
+      }
+      xsum[h * 128 + r] = amax;
+      if (!exchange()) return false;
+      amax = fmaxf(amax, xsum[(h ^ 1) * 128 + r]);
+      int e = static_cast<int>(__float_as_uint(amax) >> 23) - 127;
+      e = min(max(e, -100), 126);
+      const bool far = !(ldexpf(a.qk_scale, e) < 18446744073709551616.f);
+      const float up = __uint_as_float(static_cast<uint32_t>(127 - e) << 23), less = far ? 1.f : 2.3283064365386963e-10f;
+      rf = fmaxf(ldexpf(a.qk_scale, e + (far ? 0 : 32)), 1.1754943508222875e-38f);  // not zero: it multiplies -inf
+#pragma unroll
+      for (int i = 0; i < D / 16; ++i) {
+        uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          w[k] = pack_bf16(__uint_as_float(w[k] << 16) * up * less, __uint_as_float(w[k] & 0xffff0000u) * up * less);
+        const int piece = h * (D / 16) + i;  // of the row's D / 8
+        sts16(base + C::kOffQ + (piece >> 3) * C::kChunkBytes + r * 128 + (((piece & 7) ^ (r & 7)) << 4),
+              make_uint4(w[0], w[1], w[2], w[3]));
+      }
+      const int token = row % a.T;
+      mask = mask_of(a, at.b, token);
+      pos = at.len - a.T + __popcll(mask) - 1;
+      fence_async();
+      mbar_arrive(bar(T_Q));
+      return true;
+    };
+    if (warp == 8 && lane == 0 && id < kWorkers && !p.by_item) chains_of(p)[id] = Chain{-1, -1};
+    uint32_t n = 0, it = 0;
+    if (u < u1) ok = load_q(c);
+    for (; u < u1 && ok; ++it) {
+      const int count = segment_steps(c, u, u1);
+      float m = -INFINITY, l = 0.f;
+      for (int j = 0; j < count && ok; ++j, ++n) {
+        const uint32_t b = n & 1, sc = n % kScStages;
+        const uint32_t tS = tbase + lrow + b * 128;
+        if (!(ok = wwait(T_S + b, n >> 1) && wwait(T_SC + sc, n / kScStages))) break;
+        tc_fence_after();
+        uint32_t sr[64];
+        tmem_ld32(tS + 64 * h, *reinterpret_cast<uint32_t(*)[32]>(&sr[0]));
+        tmem_ld32(tS + 64 * h + 32, *reinterpret_cast<uint32_t(*)[32]>(&sr[32]));
+        tmem_wait_ld();
+        float* s = reinterpret_cast<float*>(sr);
+        const uint32_t ks = base + C::kOffSc + sc * 8 * kStep + 256 * h, vs = ks + 4 * kStep;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          const uint4 k = lds16(ks + 16 * i);
+          const float2 lo = mul_rn_f32x2(make_float2(s[4 * i], s[4 * i + 1]), make_float2(__uint_as_float(k.x), __uint_as_float(k.y)));
+          const float2 hi = mul_rn_f32x2(make_float2(s[4 * i + 2], s[4 * i + 3]), make_float2(__uint_as_float(k.z), __uint_as_float(k.w)));
+          s[4 * i] = lo.x; s[4 * i + 1] = lo.y; s[4 * i + 2] = hi.x; s[4 * i + 3] = hi.y;
+        }
+        const int at = place_of<kTree>(c, c.tile + j);
+        const bool edge = at_edge(a, c, at);
+        unsigned long long hid = 0ull;
+        if (edge) {
+          hid = hidden_keys(a, c.len, at * kStep + 64 * h, pos, mask);
+          const uint32_t h0 = static_cast<uint32_t>(hid), h1 = static_cast<uint32_t>(hid >> 32);
+#pragma unroll
+          for (int i = 0; i < 32; ++i) {
+            if (h0 >> i & 1u) s[i] = -INFINITY;
+            if (h1 >> i & 1u) s[32 + i] = -INFINITY;
+          }
+        }
+        float t = fmaxf(s[0], s[1]);
+#pragma unroll
+        for (int i = 2; i < 64; i += 2) t = fmaxf(t, fmaxf(s[i], s[i + 1]));
+        xmax[(n & 1) * 256 + h * 128 + r] = t;
+        if (!(ok = exchange())) break;  // and both groups have read S before either writes P over it
+        const float top = fmaxf(t, xmax[(n & 1) * 256 + (h ^ 1) * 128 + r]) * rf;
+        float alpha = 1.f;
+        bool raise = false;
+        if (top > m + kRaise) {
+          if (j > 0) {
+            raise = true;
+            alpha = ex2(m - top);
+          }
+          m = top;
+        }
+        const float neg = m == -INFINITY ? 0.f : -m;
+        float inv = 0.f, back = 0.f;
+        if (kQuant) {
+          const float amax = ex2(fmaf(t, rf, neg));
+          if (!(amax < kTinyP)) {
+            inv = __fdiv_rn(kE4M3Max, amax);
+            back = __fdiv_rn(amax, kE4M3Max);
+          }
+        }
+        l *= alpha;
+        float2 sum = make_float2(0.f, 0.f);
+        const uint32_t h0 = static_cast<uint32_t>(hid), h1 = static_cast<uint32_t>(hid >> 32);
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+          uint32_t pk[16];
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {  // four keys
+            const uint4 vv = lds16(vs + 128 * q + 16 * i);
+            const uint32_t v4[4] = {vv.x, vv.y, vv.z, vv.w};
+#pragma unroll
+            for (int y = 0; y < 2; ++y) {
+              const int k = 32 * q + 4 * i + 2 * y;
+              const float2 e = fma_rn_f32x2(make_float2(s[k], s[k + 1]), make_float2(rf, rf), make_float2(neg, neg));
+              float2 w = make_float2(ex2(e.x), ex2(e.y));
+              sum = add_rn_f32x2(sum, w);
+              if (kQuant) {
+                const float2 x = mul_rn_f32x2(w, make_float2(inv, inv));
+                w = mul_rn_f32x2(e4m3x2_decode(e4m3x2_rn_satfinite(x.x, x.y)), make_float2(back, back));
+              }
+              w = mul_rn_f32x2(w, make_float2(__uint_as_float(v4[2 * y]), __uint_as_float(v4[2 * y + 1])));
+              if (edge) {  // 0 x NaN: a key that the row does not see may hold anything
+                if ((q ? h1 : h0) >> (4 * i + 2 * y) & 1u) w.x = 0.f;
+                if ((q ? h1 : h0) >> (4 * i + 2 * y + 1) & 1u) w.y = 0.f;
+              }
+              pk[2 * i + y] = pack_bf16(w.x, w.y);
+            }
+          }
+          tmem_st16(tS + 32 * h + 16 * q, pk);
+        }
+        mbar_arrive(bar(T_SC_FREE + sc));
+        l += sum.x + sum.y;
+        tmem_wait_st();
+        if (__any_sync(0xffffffffu, raise)) {
+          // O holds every product so far before it is rescaled; each group takes half its columns
+          if (!(ok = wwait(T_O_DONE, n + 1))) break;
+          tc_fence_after();
+#pragma unroll 1
+          for (int k = 0; k < D / 64; ++k) {
+            uint32_t o[32];
+            tmem_ld32(tbase + lrow + C::kTmemO + (D / 2) * h + 32 * k, o);
+            tmem_wait_ld();
+#pragma unroll
+            for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
+            tmem_st32(tbase + lrow + C::kTmemO + (D / 2) * h + 32 * k, o);
+          }
+          tmem_wait_st();
+        }
+        tc_fence_before();
+        mbar_arrive(bar(T_P + b));
+      }
+      if (!ok) break;
+      // the segment's end: the next one's rows first, whose scores can follow while this one's sums are stored
+      const bool head = c.tile != 0, ends = c.tile + count == c.tiles, whole = !head && ends;
+      const int row0 = c.mt * kM, row = row0 + r, item = item_of(p, c), seq = c.b * a.Hkv + c.h;
+      if (!head && warp == 8 && lane == 0) {
+        const long long end = u - c.tile + c.tiles;  // the unit behind the item
+        if (whole) {
+          if (p.by_item) chains_of(p)[item] = Chain{-1, -1};
+        } else {
+          chains_of(p)[p.by_item ? item : id] = Chain{p.by_item ? id : item, static_cast<int>((end * workers - 1) / W)};
+        }
+      }
+      xsum[h * 128 + r] = l;
+      if (!(ok = exchange())) break;
+      const float lr = xsum[r] + xsum[128 + r];
+      leave(p, prefix, extra, count, c, u);
+      if (!(ok = exchange())) break;  // xsum has been read
+      if (u < u1 && !(ok = wwait(T_Q_FREE, it) && load_q(c))) break;
+      if (!(ok = wwait(T_O_LAST, it))) break;
+      tc_fence_after();
+      const bool none = lr == 0.f, in = row < p.R;
+      const float f = whole ? (none ? 0.f : 1.f / lr) : 1.f;
+      float* part = partial_of<D>(p, id, head ? 0 : 1);
+#pragma unroll 1
+      for (int k = 0; k < D / 64; ++k) {
+        uint32_t o[32];
+        tmem_ld32(tbase + lrow + C::kTmemO + (D / 2) * h + 32 * k, o);
+        tmem_wait_ld();
+        if (!in) continue;
+        if (whole) {
+          uint32_t w[16];
+#pragma unroll
+          for (int i = 0; i < 16; ++i)
+            w[i] = none ? 0u : pack_bf16(__uint_as_float(o[2 * i]) * f, __uint_as_float(o[2 * i + 1]) * f);
+          uint4* dst = reinterpret_cast<uint4*>(a.o + (static_cast<size_t>(seq) * p.R + row) * D + (D / 2) * h + 32 * k);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) dst[i] = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+        } else {
+          uint4* dst = reinterpret_cast<uint4*>(part + r * D + (D / 2) * h + 32 * k);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) dst[i] = make_uint4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+        }
+      }
+      tc_fence_before();
+      mbar_arrive(bar(T_O_FREE));
+      if (in && h == 0) {
+        if (!whole)
+          *reinterpret_cast<float2*>(part + p.prows * D + 2 * r) = make_float2(m, lr);
+        else if (a.lse != nullptr)
+          a.lse[static_cast<size_t>(seq) * p.R + row] = none ? -INFINITY : m + log2f(lr);
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 1) tmem_dealloc(tbase, 512);
+}
+
+template <int D, bool kQuant>
+cudaError_t run(Params p, int ctas, int most, cudaStream_t s) {
+  using C = Tc<D>;
+  // at least 116 KB, so that no two CTAs share an SM (each holds all 512 TMEM columns)
+  const auto bytes = [](int B) {
+    const size_t n = C::kUsed + 4 * (static_cast<size_t>(B) + 1) + 1024;
+    return n > 118784 ? n : 118784;
+  };
+  const long long items = static_cast<long long>(p.a.B) * p.a.Hkv * p.mtiles;
+  p.by_item = items <= most;
+  static_assert(C::kUsed + 4 * (kDecodeMaxBatch + 1) + 1024 <= 227 * 1024, "the batch's prefix sums fit");
+  cudaError_t e = cudaFuncSetAttribute(tree_kernel<D, kQuant>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       static_cast<int>(bytes(kDecodeMaxBatch)));
+  if (e != cudaSuccess) return e;
+  e = launch_early(tree_kernel<D, kQuant>, ctas, kThreads, bytes(p.a.B), s, p);
+  if (e != cudaSuccess) return e;
+  return launch_merge<D>(p, most, ctas, s);
+}
+
+}  // namespace
+
+cudaError_t launch_tree(const DecodeArgs& a, int D, int num_sms, cudaStream_t s) {
+  Params p;
+  p.a = a;
+  p.R = a.Hq / a.Hkv * a.T;
+  p.rows = kM;
+  p.mtiles = (p.R + kM - 1) / kM;
+  p.prows = p.R < kM ? (p.R + 1) / 2 * 2 : kM;
+  const long long cap = static_cast<long long>(a.max_pages) << a.page_shift;
+  const long long units = static_cast<long long>(a.B) * a.Hkv * p.mtiles * ((cap + kStep - 1) / kStep);
+  int ctas = num_sms < kMaxCtas ? num_sms : kMaxCtas;
+  if (units < ctas) ctas = static_cast<int>(units);
+  if (D == 64) return a.quant ? run<64, true>(p, ctas, ctas, s) : run<64, false>(p, ctas, ctas, s);
+  return a.quant ? run<128, true>(p, ctas, ctas, s) : run<128, false>(p, ctas, ctas, s);
+}
+
+}  // namespace qat

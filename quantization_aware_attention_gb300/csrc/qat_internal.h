@@ -356,6 +356,7 @@ cudaError_t launch_kv_append(const KvCacheArgs& a, int D, cudaStream_t s);
 cudaError_t launch_kv_read(const KvCacheArgs& a, int D, cudaStream_t s);
 cudaError_t launch_draft_tree(const DraftTreeArgs& a, cudaStream_t s);
 cudaError_t launch_kv_keep(const KvKeepArgs& a, int D, cudaStream_t s);
+cudaError_t launch_tree(const DecodeArgs& a, int D, int num_sms, cudaStream_t s);
 cudaError_t launch_decode(const DecodeArgs& a, int D, int num_sms, cudaStream_t s);
 cudaError_t launch_fwd_tc(const FwdArgs& a, unsigned int* err, int num_sms, cudaStream_t s);
 // prep + dK/dV + dQ kernels

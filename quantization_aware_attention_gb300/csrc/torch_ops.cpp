@@ -521,7 +521,7 @@ int64_t tree_stride(const Tensor& t, const char* name, at::ScalarType type, cons
   const auto sz = t.sizes();
   TORCH_CHECK_VALUE((sz.size() == 1 && sz[0] == T) || (sz.size() == 2 && sz[0] == B && sz[1] == T), name,
                     " has shape ", sz, ", expected [", B, ", ", T, "] or [", T, "]");
-  TORCH_CHECK_VALUE(T <= 1 || t.stride(-1) == 1, name, " must be contiguous along the tokens");
+  TORCH_CHECK_VALUE(T <= 1 || t.numel() == 0 || t.stride(-1) == 1, name, " must be contiguous along the tokens");
   with_memory(t, name);
   return sz.size() == 2 && B > 1 ? t.stride(0) : 0;
 }
