@@ -21,7 +21,7 @@ using namespace sm100;
 
 constexpr int kStep = 128;     // keys of a step
 constexpr int kM = 128;        // query rows of an item
-constexpr int kThreads = 512;  // warp 0 producer, 1 products, 4-5 K and 6-7 V converters, 8-15 softmax
+constexpr int kThreads = 512;  // warp 0 producer, 1 products, 4-7 converters, 8-15 softmax
 constexpr int kStages = 3;     // steps whose codes are on their way or in shared memory
 constexpr int kScStages = 6;   // steps whose scales are
 constexpr float kRaise = 8.0f; // log2: the running maximum is raised when it is this far behind
@@ -42,7 +42,7 @@ struct Tc {
   static constexpr uint32_t kOffX = kOffMisc + 64;                // row maxima [2][2][128], row sums [2][128]
   static constexpr uint32_t kOffSum = kOffX + 3072;               // the warps' sums, then B + 1 prefix sums
   static constexpr uint32_t kUsed = kOffSum + 4 * (kThreads / 32);
-  static constexpr uint32_t kTmemO = 256;
+  static constexpr uint32_t kTmemO = 256, kTmemP = 384;  // S at 0 and 128; P at 384 and 448
 };
 
 enum : uint32_t {
@@ -75,11 +75,19 @@ __device__ __forceinline__ void sts16(uint32_t a, uint4 v) {
   asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(a), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
 }
 
-// Four E4M3 codes (never NaN) to bf16, exactly: the code's exponent and fraction are those of a bf16 number
-// 2^120 times smaller, subnormal codes included.
+__device__ __forceinline__ float fmax3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+
+// Four E4M3 codes (never NaN) to bf16, exactly: four bits further up, the code's exponent and fraction are those of
+// a bf16 number 2^120 times smaller, subnormal codes included.  The bytes are spread with their signs.
 __device__ __forceinline__ uint2 codes_to_bf16x4(uint32_t x) {
-  const uint32_t lo = __byte_perm(x, 0, 0x1404), hi = __byte_perm(x, 0, 0x3424);
-  const uint32_t a = ((lo >> 4) & 0x07f007f0u) | (lo & 0x80008000u), b = ((hi >> 4) & 0x07f007f0u) | (hi & 0x80008000u);
+  uint32_t lo, hi;
+  asm("prmt.b32 %0, %1, 0, 0x9180;" : "=r"(lo) : "r"(x));
+  asm("prmt.b32 %0, %1, 0, 0xb3a2;" : "=r"(hi) : "r"(x));
+  const uint32_t a = (lo << 4) & 0x87f087f0u, b = (hi << 4) & 0x87f087f0u;
   const uint32_t up = 0x7b807b80u;  // 2^120
   uint2 r;
   asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r.x) : "r"(a), "r"(up));
@@ -154,9 +162,9 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const Params p) {
     }
     mbar_init(bar(T_Q), 256);
     mbar_init(bar(T_Q_FREE), 1);
-    mbar_init(bar(T_K), 64);
+    mbar_init(bar(T_K), 128);
     mbar_init(bar(T_K_FREE), 1);
-    mbar_init(bar(T_V), 64);
+    mbar_init(bar(T_V), 128);
     mbar_init(bar(T_V_FREE), 1);
     for (int i = 0; i < 2; ++i) {
       mbar_init(bar(T_S + i), 1);
@@ -313,7 +321,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const Params p) {
       constexpr uint32_t idS = idesc_bf16_f32(kM, kStep, false), idO = idesc_bf16_f32(kM, D, true);
       uint32_t n = 0, it = 0;
       bool issued = false;
-      const auto issue_s = [&](uint32_t k, bool last) {  // S of step k, into the buffer that held P of step k - 2
+      const auto issue_s = [&](uint32_t k, bool last) {  // S of step k, into the buffer whose step k - 2 P of that step tells to be read
         if (!wait(T_K, k)) return false;
         tc_fence_after();
 #pragma unroll
@@ -338,7 +346,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const Params p) {
           tc_fence_after();
 #pragma unroll
           for (int ks = 0; ks < kStep / 16; ++ks)
-            mma_ts(tbase + C::kTmemO, tbase + (n & 1) * 128 + 8 * ks,
+            mma_ts(tbase + C::kTmemO, tbase + C::kTmemP + (n & 1) * 64 + 8 * ks,
                    smem_desc_sw128(base + C::kOffV + ks * 2048, C::kChunkBytes, 1024), idO, (j > 0 || ks > 0) ? 1u : 0u);
           mma_commit(bar(T_V_FREE));
           mma_commit(bar(T_O_DONE));
@@ -353,39 +361,61 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const Params p) {
     }
   } else if (warp >= 4 && warp < 8) {
     // ------------------------------------------------------------ codes to bf16 operands
-    // Warps 4 and 5 bring K's codes of each step into the 128-byte swizzled layout that the products read, 6
-    // and 7 V's.  Lane groups of a row's 16-byte pieces; the two 16-byte halves of what a piece becomes are
-    // written in the order that keeps eight lanes on different banks.
-    const bool value = warp >= 6;
-    const int t = tid & 63;
-    constexpr int kPieces = D / 16, kEach = kStep * kPieces / 64;
-    const uint32_t out = base + (value ? C::kOffV : C::kOffK);
-    for (uint32_t n = 0; u < u1; ++n) {
-      const int left = c.len - place_of<kTree>(c, c.tile) * kStep;
-      const uint32_t st = n % kStages, ring = base + C::kOffRing + st * 2 * C::kCodes + (value ? C::kCodes : 0);
-      if (!wait(T_CODES + st, n / kStages) || !wait(value ? T_V_FREE : T_K_FREE, n + 1)) break;
+    // Each step's K and V from E4M3 codes into the 128-byte swizzled layout that the products read, K of the next step
+    // before V of this one.  A lane takes 16 codes at a time; groups of four lanes take the halves of two rows
+    // crosswise, so that eight lanes are on different banks both reading and writing.
+    const int t = tid & 127;
+    constexpr int kEach = kStep * (D / 16) / 128;  // 16-code pieces of a lane
+    const auto convert = [&](uint32_t ring, uint32_t out, int left) {
+#pragma unroll 1
+      for (int i0 = 0; i0 < kEach; i0 += 2) {
+        uint4 x[2];
+        int row[2];
+        uint32_t at[2];
 #pragma unroll
-      for (int i0 = 0; i0 < kEach; i0 += 4) {
-        uint4 x[4];
+        for (int i = 0; i < 2; ++i) {
+          const int g = t >> 2, odd = g & 1;
+          const int half = D == 64 ? 0 : odd ^ i;
+          row[i] = D == 64 ? g + 32 * (i0 + i) : g + 32 * (i0 >> 1);
+          const int piece = (t & 3) + 4 * half;  // of the row's D / 16
+          x[i] = lds16(ring + row[i] * D + 16 * piece);
+          at[i] = out + half * C::kChunkBytes + row[i] * 128 + (((2 * t & 6) ^ (row[i] & 7)) << 4);
+        }
+        if (left < kStep) {  // behind the end: may hold anything
 #pragma unroll
-        for (int i = 0; i < 4; ++i) x[i] = lds16(ring + 16 * (t + 64 * (i0 + i)));
+          for (int i = 0; i < 2; ++i)
+            if (row[i] >= left) x[i] = make_uint4(0u, 0u, 0u, 0u);
+        }
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int row = (t + 64 * (i0 + i)) / kPieces, piece = t % kPieces;
-          if (row >= left) x[i] = make_uint4(0u, 0u, 0u, 0u);  // behind the end: may hold anything
+        for (int i = 0; i < 2; ++i) {
           const uint2 w0 = codes_to_bf16x4(x[i].x), w1 = codes_to_bf16x4(x[i].y), w2 = codes_to_bf16x4(x[i].z),
                       w3 = codes_to_bf16x4(x[i].w);
-          const uint4 lo = make_uint4(w0.x, w0.y, w1.x, w1.y), hi = make_uint4(w2.x, w2.y, w3.x, w3.y);
-          const uint32_t at = out + (piece >> 2) * C::kChunkBytes + row * 128, swz = row & 7, at0 = 2 * piece & 7;
-          const bool odd = piece & 4;
-          sts16(at + (((at0 + (odd ? 1 : 0)) ^ swz) << 4), odd ? hi : lo);
-          sts16(at + (((at0 + (odd ? 0 : 1)) ^ swz) << 4), odd ? lo : hi);
+          sts16(at[i], make_uint4(w0.x, w0.y, w1.x, w1.y));
+          sts16(at[i] ^ 16, make_uint4(w2.x, w2.y, w3.x, w3.y));
         }
       }
       fence_async();
-      mbar_arrive(bar(value ? T_V : T_K));
-      mbar_arrive(bar(T_CODES_FREE + st));
+    };
+    const auto left_at = [&](const Cursor& x) { return x.len - place_of<kTree>(x, x.tile) * kStep; };
+    const auto do_k = [&](uint32_t n, int left) {
+      const uint32_t st = n % kStages;
+      if (!wait(T_CODES + st, n / kStages) || !wait(T_K_FREE, n + 1)) return false;
+      convert(base + C::kOffRing + st * 2 * C::kCodes, base + C::kOffK, left);
+      mbar_arrive(bar(T_K));
+      return true;
+    };
+    int left = 0;
+    if (u < u1) ok = do_k(0, left = left_at(c));
+    for (uint32_t n = 0; u < u1 && ok; ++n) {
       advance<kTree, kStep>(p, prefix, extra, c, u);
+      int next = 0;
+      if (u < u1 && !do_k(n + 1, next = left_at(c))) break;
+      const uint32_t st = n % kStages;
+      if (!wait(T_V_FREE, n + 1)) break;
+      convert(base + C::kOffRing + st * 2 * C::kCodes + C::kCodes, base + C::kOffV, left);
+      mbar_arrive(bar(T_V));
+      mbar_arrive(bar(T_CODES_FREE + st));
+      left = next;
     }
   } else if (warp >= 8) {
     // ------------------------------------------------------------ softmax, two groups of four warps
@@ -460,36 +490,42 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const Params p) {
         const uint32_t tS = tbase + lrow + b * 128;
         if (!(ok = wwait(T_S + b, n >> 1) && wwait(T_SC + sc, n / kScStages))) break;
         tc_fence_after();
-        uint32_t sr[64];
-        tmem_ld32(tS + 64 * h, *reinterpret_cast<uint32_t(*)[32]>(&sr[0]));
-        tmem_ld32(tS + 64 * h + 32, *reinterpret_cast<uint32_t(*)[32]>(&sr[32]));
-        tmem_wait_ld();
-        float* s = reinterpret_cast<float*>(sr);
         const uint32_t ks = base + C::kOffSc + sc * 8 * kStep + 256 * h, vs = ks + 4 * kStep;
-#pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          const uint4 k = lds16(ks + 16 * i);
-          const float2 lo = mul_rn_f32x2(make_float2(s[4 * i], s[4 * i + 1]), make_float2(__uint_as_float(k.x), __uint_as_float(k.y)));
-          const float2 hi = mul_rn_f32x2(make_float2(s[4 * i + 2], s[4 * i + 3]), make_float2(__uint_as_float(k.z), __uint_as_float(k.w)));
-          s[4 * i] = lo.x; s[4 * i + 1] = lo.y; s[4 * i + 2] = hi.x; s[4 * i + 3] = hi.y;
-        }
         const int at = place_of<kTree>(c, c.tile + j);
         const bool edge = at_edge(a, c, at);
         unsigned long long hid = 0ull;
-        if (edge) {
-          hid = hidden_keys(a, c.len, at * kStep + 64 * h, pos, mask);
-          const uint32_t h0 = static_cast<uint32_t>(hid), h1 = static_cast<uint32_t>(hid >> 32);
+        if (edge) hid = hidden_keys(a, c.len, at * kStep + 64 * h, pos, mask);
+        // the row's S times the keys' scales, 32 keys from 32 q on; it is read twice, which takes half the registers and
+        // instructions that keeping it does
+        const auto scores = [&](int q, uint32_t (&sr)[32]) {
+          tmem_ld32(tS + 64 * h + 32 * q, sr);
+          tmem_wait_ld();
+          float* s = reinterpret_cast<float*>(sr);
 #pragma unroll
-          for (int i = 0; i < 32; ++i) {
-            if (h0 >> i & 1u) s[i] = -INFINITY;
-            if (h1 >> i & 1u) s[32 + i] = -INFINITY;
+          for (int i = 0; i < 8; ++i) {
+            const uint4 k = lds16(ks + 128 * q + 16 * i);
+            const float2 lo = mul_rn_f32x2(make_float2(s[4 * i], s[4 * i + 1]), make_float2(__uint_as_float(k.x), __uint_as_float(k.y)));
+            const float2 hi = mul_rn_f32x2(make_float2(s[4 * i + 2], s[4 * i + 3]), make_float2(__uint_as_float(k.z), __uint_as_float(k.w)));
+            s[4 * i] = lo.x; s[4 * i + 1] = lo.y; s[4 * i + 2] = hi.x; s[4 * i + 3] = hi.y;
           }
-        }
-        float t = fmaxf(s[0], s[1]);
+          if (edge) {
+            const uint32_t hq = static_cast<uint32_t>(hid >> (32 * q));
 #pragma unroll
-        for (int i = 2; i < 64; i += 2) t = fmaxf(t, fmaxf(s[i], s[i + 1]));
+            for (int i = 0; i < 32; ++i)
+              if (hq >> i & 1u) s[i] = -INFINITY;
+          }
+        };
+        float t = -INFINITY;
+#pragma unroll 1
+        for (int q = 0; q < 2; ++q) {
+          uint32_t sr[32];
+          scores(q, sr);
+          const float* s = reinterpret_cast<const float*>(sr);
+#pragma unroll
+          for (int i = 0; i < 32; i += 2) t = fmax3(t, s[i], s[i + 1]);
+        }
         xmax[(n & 1) * 256 + h * 128 + r] = t;
-        if (!(ok = exchange())) break;  // and both groups have read S before either writes P over it
+        if (!(ok = exchange())) break;
         const float top = fmaxf(t, xmax[(n & 1) * 256 + (h ^ 1) * 128 + r]) * rf;
         float alpha = 1.f;
         bool raise = false;
@@ -511,17 +547,19 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const Params p) {
         }
         l *= alpha;
         float2 sum = make_float2(0.f, 0.f);
-        const uint32_t h0 = static_cast<uint32_t>(hid), h1 = static_cast<uint32_t>(hid >> 32);
-#pragma unroll
+#pragma unroll 1
         for (int q = 0; q < 2; ++q) {
-          uint32_t pk[16];
+          uint32_t sr[32], pk[16];
+          scores(q, sr);
+          const float* s = reinterpret_cast<const float*>(sr);
+          const uint32_t hq = static_cast<uint32_t>(hid >> (32 * q));
 #pragma unroll
           for (int i = 0; i < 8; ++i) {  // four keys
             const uint4 vv = lds16(vs + 128 * q + 16 * i);
             const uint32_t v4[4] = {vv.x, vv.y, vv.z, vv.w};
 #pragma unroll
             for (int y = 0; y < 2; ++y) {
-              const int k = 32 * q + 4 * i + 2 * y;
+              const int k = 4 * i + 2 * y;
               const float2 e = fma_rn_f32x2(make_float2(s[k], s[k + 1]), make_float2(rf, rf), make_float2(neg, neg));
               float2 w = make_float2(ex2(e.x), ex2(e.y));
               sum = add_rn_f32x2(sum, w);
@@ -530,14 +568,15 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const Params p) {
                 w = mul_rn_f32x2(e4m3x2_decode(e4m3x2_rn_satfinite(x.x, x.y)), make_float2(back, back));
               }
               w = mul_rn_f32x2(w, make_float2(__uint_as_float(v4[2 * y]), __uint_as_float(v4[2 * y + 1])));
-              if (edge) {  // 0 x NaN: a key that the row does not see may hold anything
-                if ((q ? h1 : h0) >> (4 * i + 2 * y) & 1u) w.x = 0.f;
-                if ((q ? h1 : h0) >> (4 * i + 2 * y + 1) & 1u) w.y = 0.f;
-              }
               pk[2 * i + y] = pack_bf16(w.x, w.y);
             }
           }
-          tmem_st16(tS + 32 * h + 16 * q, pk);
+          if (edge) {  // 0 x NaN: a key that the row does not see may hold anything
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+              pk[i] &= ((hq >> (2 * i) & 1u) ? 0u : 0xffffu) | ((hq >> (2 * i + 1) & 1u) ? 0u : 0xffff0000u);
+          }
+          tmem_st16(tbase + lrow + C::kTmemP + 64 * b + 32 * h + 16 * q, pk);
         }
         mbar_arrive(bar(T_SC_FREE + sc));
         l += sum.x + sum.y;
