@@ -39,16 +39,15 @@ struct Tc {
   static constexpr uint32_t kOffSc = kOffRing + kStages * 2 * kCodes;  // scales: K, then V
   static constexpr uint32_t kOffBar = kOffSc + kScStages * 8 * kStep;
   static constexpr uint32_t kOffMisc = kOffBar + 320;
-  static constexpr uint32_t kOffX = kOffMisc + 64;                // row maxima [2][2][128], row sums [2][128]
+  static constexpr uint32_t kOffX = kOffMisc + 64;                // the rows' largest |q|, m and l, [2 groups][128] each
   static constexpr uint32_t kOffSum = kOffX + 3072;               // the warps' sums, then B + 1 prefix sums
   static constexpr uint32_t kUsed = kOffSum + 4 * (kThreads / 32);
-  static constexpr uint32_t kTmemO = 256, kTmemP = 384;  // S at 0 and 128; P at 384 and 448
+  static constexpr uint32_t kTmemO = 256;  // S, then P, of even and odd steps at 0 and 128; their sums at kTmemO, + D
 };
 
 enum : uint32_t {
   T_CODES = 0, T_CODES_FREE = T_CODES + kStages, T_SC = T_CODES_FREE + kStages, T_SC_FREE = T_SC + kScStages,
-  T_Q = T_SC_FREE + kScStages, T_Q_FREE, T_K, T_K_FREE, T_V, T_V_FREE, T_S, T_P = T_S + 2, T_O_DONE = T_P + 2,
-  T_O_LAST, T_O_FREE, T_DRAIN, T_X, T_COUNT = T_X + 4
+  T_Q = T_SC_FREE + kScStages, T_Q_FREE, T_K, T_K_FREE, T_V, T_V_FREE, T_S, T_P = T_S + 2, T_O_LAST = T_P + 2, T_O_FREE, T_DRAIN, T_X, T_COUNT = T_X + 4
 };
 static_assert(T_COUNT * 8 <= 320, "barrier block");
 
@@ -63,6 +62,15 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_
       "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst), "l"(src),
       "r"(bytes), "r"(bar)
       : "memory");
+}
+// 32 lanes x 16 columns, as tmem_ld32.
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr));
 }
 __device__ __forceinline__ void fence_async() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 
@@ -158,7 +166,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const Params p) {
     }
     for (int i = 0; i < kScStages; ++i) {
       mbar_init(bar(T_SC + i), 1);
-      mbar_init(bar(T_SC_FREE + i), 256);
+      mbar_init(bar(T_SC_FREE + i), 128);
     }
     mbar_init(bar(T_Q), 256);
     mbar_init(bar(T_Q_FREE), 1);
@@ -168,9 +176,8 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const Params p) {
     mbar_init(bar(T_V_FREE), 1);
     for (int i = 0; i < 2; ++i) {
       mbar_init(bar(T_S + i), 1);
-      mbar_init(bar(T_P + i), 256);
+      mbar_init(bar(T_P + i), 128);
     }
-    mbar_init(bar(T_O_DONE), 1);
     mbar_init(bar(T_O_LAST), 1);
     mbar_init(bar(T_O_FREE), 256);
     mbar_init(bar(T_DRAIN), 1);
@@ -321,7 +328,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const Params p) {
       constexpr uint32_t idS = idesc_bf16_f32(kM, kStep, false), idO = idesc_bf16_f32(kM, D, true);
       uint32_t n = 0, it = 0;
       bool issued = false;
-      const auto issue_s = [&](uint32_t k, bool last) {  // S of step k, into the buffer whose step k - 2 P of that step tells to be read
+      const auto issue_s = [&](uint32_t k, bool last) {  // S of step k, over P of step k - 2, which its sums have read
         if (!wait(T_K, k)) return false;
         tc_fence_after();
 #pragma unroll
@@ -338,19 +345,18 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const Params p) {
       };
       for (; u < u1 && ok; ++it) {
         const int count = segment_steps(c, u, u1);
-        ok = wait(T_Q, it) && issue_s(n, count == 1);
+        ok = wait(T_Q, it) && issue_s(n, count == 1) && (count == 1 || issue_s(n + 1, count == 2));
         for (int j = 0; j < count && ok; ++j, ++n) {
-          if (j + 1 < count && !(ok = issue_s(n + 1, j + 2 == count))) break;
           if (!(ok = wait(T_V, n) && wait(T_P + (n & 1), n >> 1))) break;
           if (j == 0 && !(ok = wait(T_O_FREE, it + 1))) break;
           tc_fence_after();
 #pragma unroll
           for (int ks = 0; ks < kStep / 16; ++ks)
-            mma_ts(tbase + C::kTmemO, tbase + C::kTmemP + (n & 1) * 64 + 8 * ks,
-                   smem_desc_sw128(base + C::kOffV + ks * 2048, C::kChunkBytes, 1024), idO, (j > 0 || ks > 0) ? 1u : 0u);
+            mma_ts(tbase + C::kTmemO + (n & 1) * D, tbase + (n & 1) * 128 + 8 * ks,
+                   smem_desc_sw128(base + C::kOffV + ks * 2048, C::kChunkBytes, 1024), idO, (j > 1 || ks > 0) ? 1u : 0u);
           mma_commit(bar(T_V_FREE));
-          mma_commit(bar(T_O_DONE));
           if (j + 1 == count) mma_commit(bar(T_O_LAST));
+          if (j + 2 < count && !(ok = issue_s(n + 2, j + 3 == count))) break;
         }
         if (ok) leave(p, prefix, extra, count, c, u);
       }
@@ -419,11 +425,14 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const Params p) {
     }
   } else if (warp >= 8) {
     // ------------------------------------------------------------ softmax, two groups of four warps
-    // h = 0 has keys 0-63 of every row of S, h = 1 keys 64-127: a thread one row of one quantization tile.
+    // Group h takes every other step, a thread a row of its S, with a running maximum, a sum and an accumulator of its
+    // own, added up at a segment's end: no thread waits for another in between, and the two warps of a scheduler
+    // are at different places of a step.
     const int h = (warp - 8) >> 2, quarter = warp & 3, r = 32 * quarter + lane;
     const uint32_t lrow = (32u * quarter) << 16;
-    float* xmax = reinterpret_cast<float*>(gbase + C::kOffX);         // [2][2 h][128]
-    float* xsum = reinterpret_cast<float*>(gbase + C::kOffX + 2048);  // [2 h][128]
+    float* xq = reinterpret_cast<float*>(gbase + C::kOffX);  // [2 groups][128]
+    float* xm = xq + 256;
+    float* xl = xq + 512;
     uint32_t xc = 0;
     const auto exchange = [&]() {  // between the two threads of a row (and their warps)
       tc_fence_before();
@@ -454,9 +463,9 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const Params p) {
         for (int k = 0; k < 4; ++k)
           amax = fmaxf(amax, fmaxf(fabsf(__uint_as_float(w[k] << 16)), fabsf(__uint_as_float(w[k] & 0xffff0000u))));
       }
-      xsum[h * 128 + r] = amax;
+      xq[h * 128 + r] = amax;
       if (!exchange()) return false;
-      amax = fmaxf(amax, xsum[(h ^ 1) * 128 + r]);
+      amax = fmaxf(amax, xq[(h ^ 1) * 128 + r]);
       int e = static_cast<int>(__float_as_uint(amax) >> 23) - 127;
       e = min(max(e, -100), 126);
       const bool far = !(ldexpf(a.qk_scale, e) < 18446744073709551616.f);
@@ -480,25 +489,31 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const Params p) {
       return true;
     };
     if (warp == 8 && lane == 0 && id < kWorkers && !p.by_item) chains_of(p)[id] = Chain{-1, -1};
-    uint32_t n = 0, it = 0;
+    uint32_t first_n = 0, it = 0;  // the segment's first step
     if (u < u1) ok = load_q(c);
     for (; u < u1 && ok; ++it) {
       const int count = segment_steps(c, u, u1);
       float m = -INFINITY, l = 0.f;
-      for (int j = 0; j < count && ok; ++j, ++n) {
-        const uint32_t b = n & 1, sc = n % kScStages;
-        const uint32_t tS = tbase + lrow + b * 128;
-        if (!(ok = wwait(T_S + b, n >> 1) && wwait(T_SC + sc, n / kScStages))) break;
+      const uint32_t tS = tbase + lrow + 128 * h, tO = tbase + lrow + C::kTmemO + D * h;
+      const int j0 = (first_n & 1) ^ h;  // this group's first step of the segment
+      for (int j = j0; j < count && ok; j += 2) {
+        const uint32_t n = first_n + j, sc = n % kScStages;
+        if (!(ok = wwait(T_S + h, n >> 1) && wwait(T_SC + sc, n / kScStages))) break;
         tc_fence_after();
-        const uint32_t ks = base + C::kOffSc + sc * 8 * kStep + 256 * h, vs = ks + 4 * kStep;
+        const uint32_t ks = base + C::kOffSc + sc * 8 * kStep, vs = ks + 4 * kStep;
         const int at = place_of<kTree>(c, c.tile + j);
         const bool edge = at_edge(a, c, at);
-        unsigned long long hid = 0ull;
-        if (edge) hid = hidden_keys(a, c.len, at * kStep + 64 * h, pos, mask);
-        // the row's S times the keys' scales, 32 keys from 32 q on; it is read twice, which takes half the registers and
-        // instructions that keeping it does
-        const auto scores = [&](int q, uint32_t (&sr)[32]) {
-          tmem_ld32(tS + 64 * h + 32 * q, sr);
+        unsigned long long hid0 = 0ull, hid1 = 0ull;
+        if (edge) {
+          hid0 = hidden_keys(a, c.len, at * kStep, pos, mask);
+          hid1 = hidden_keys(a, c.len, at * kStep + 64, pos, mask);
+        }
+        // S times the keys' scales goes back to where it came from, 32 keys at a time; the largest of each tile
+        float t0 = -INFINITY, t1 = -INFINITY;
+#pragma unroll 1
+        for (int q = 0; q < 4; ++q) {
+          uint32_t sr[32];
+          tmem_ld32(tS + 32 * q, sr);
           tmem_wait_ld();
           float* s = reinterpret_cast<float*>(sr);
 #pragma unroll
@@ -509,50 +524,59 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const Params p) {
             s[4 * i] = lo.x; s[4 * i + 1] = lo.y; s[4 * i + 2] = hi.x; s[4 * i + 3] = hi.y;
           }
           if (edge) {
-            const uint32_t hq = static_cast<uint32_t>(hid >> (32 * q));
+            const uint32_t hq = static_cast<uint32_t>((q < 2 ? hid0 : hid1) >> (32 * (q & 1)));
 #pragma unroll
             for (int i = 0; i < 32; ++i)
               if (hq >> i & 1u) s[i] = -INFINITY;
           }
-        };
-        float t = -INFINITY;
-#pragma unroll 1
-        for (int q = 0; q < 2; ++q) {
-          uint32_t sr[32];
-          scores(q, sr);
-          const float* s = reinterpret_cast<const float*>(sr);
+          tmem_st32(tS + 32 * q, sr);
+          float t = fmaxf(s[0], s[1]);
 #pragma unroll
-          for (int i = 0; i < 32; i += 2) t = fmax3(t, s[i], s[i + 1]);
+          for (int i = 2; i < 32; i += 2) t = fmax3(t, s[i], s[i + 1]);
+          if (q < 2) t0 = fmaxf(t0, t); else t1 = fmaxf(t1, t);
         }
-        xmax[(n & 1) * 256 + h * 128 + r] = t;
-        if (!(ok = exchange())) break;
-        const float top = fmaxf(t, xmax[(n & 1) * 256 + (h ^ 1) * 128 + r]) * rf;
-        float alpha = 1.f;
-        bool raise = false;
-        if (top > m + kRaise) {
-          if (j > 0) {
-            raise = true;
+        tmem_wait_st();
+        const float top = fmaxf(t0, t1) * rf;
+        if (__any_sync(0xffffffffu, top > m + kRaise)) {
+          float alpha = 1.f;
+          if (top > m + kRaise) {
             alpha = ex2(m - top);
+            m = top;
           }
-          m = top;
+          l *= alpha;
+          if (j > j0) {  // S of this step is behind every product of this accumulator so far
+#pragma unroll 1
+            for (int k = 0; k < D / 32; ++k) {
+              uint32_t o[32];
+              tmem_ld32(tO + 32 * k, o);
+              tmem_wait_ld();
+#pragma unroll
+              for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
+              tmem_st32(tO + 32 * k, o);
+            }
+          }
         }
         const float neg = m == -INFINITY ? 0.f : -m;
-        float inv = 0.f, back = 0.f;
+        float inv0 = 0.f, back0 = 0.f, inv1 = 0.f, back1 = 0.f;
         if (kQuant) {
-          const float amax = ex2(fmaf(t, rf, neg));
-          if (!(amax < kTinyP)) {
-            inv = __fdiv_rn(kE4M3Max, amax);
-            back = __fdiv_rn(amax, kE4M3Max);
+          const float a0 = ex2(fmaf(t0, rf, neg)), a1 = ex2(fmaf(t1, rf, neg));
+          if (!(a0 < kTinyP)) {
+            inv0 = __fdiv_rn(kE4M3Max, a0);
+            back0 = __fdiv_rn(a0, kE4M3Max);
+          }
+          if (!(a1 < kTinyP)) {
+            inv1 = __fdiv_rn(kE4M3Max, a1);
+            back1 = __fdiv_rn(a1, kE4M3Max);
           }
         }
-        l *= alpha;
         float2 sum = make_float2(0.f, 0.f);
 #pragma unroll 1
-        for (int q = 0; q < 2; ++q) {
+        for (int q = 0; q < 4; ++q) {
           uint32_t sr[32], pk[16];
-          scores(q, sr);
+          tmem_ld32(tS + 32 * q, sr);
+          tmem_wait_ld();
           const float* s = reinterpret_cast<const float*>(sr);
-          const uint32_t hq = static_cast<uint32_t>(hid >> (32 * q));
+          const float inv = q < 2 ? inv0 : inv1, back = q < 2 ? back0 : back1;
 #pragma unroll
           for (int i = 0; i < 8; ++i) {  // four keys
             const uint4 vv = lds16(vs + 128 * q + 16 * i);
@@ -572,37 +596,23 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const Params p) {
             }
           }
           if (edge) {  // 0 x NaN: a key that the row does not see may hold anything
+            const uint32_t hq = static_cast<uint32_t>((q < 2 ? hid0 : hid1) >> (32 * (q & 1)));
 #pragma unroll
             for (int i = 0; i < 16; ++i)
               pk[i] &= ((hq >> (2 * i) & 1u) ? 0u : 0xffffu) | ((hq >> (2 * i + 1) & 1u) ? 0u : 0xffff0000u);
           }
-          tmem_st16(tbase + lrow + C::kTmemP + 64 * b + 32 * h + 16 * q, pk);
+          tmem_st16(tS + 16 * q, pk);  // over keys whose scores have been read
         }
         mbar_arrive(bar(T_SC_FREE + sc));
         l += sum.x + sum.y;
         tmem_wait_st();
-        if (__any_sync(0xffffffffu, raise)) {
-          // O holds every product so far before it is rescaled; each group takes half its columns
-          if (!(ok = wwait(T_O_DONE, n + 1))) break;
-          tc_fence_after();
-#pragma unroll 1
-          for (int k = 0; k < D / 64; ++k) {
-            uint32_t o[32];
-            tmem_ld32(tbase + lrow + C::kTmemO + (D / 2) * h + 32 * k, o);
-            tmem_wait_ld();
-#pragma unroll
-            for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
-            tmem_st32(tbase + lrow + C::kTmemO + (D / 2) * h + 32 * k, o);
-          }
-          tmem_wait_st();
-        }
         tc_fence_before();
-        mbar_arrive(bar(T_P + b));
+        mbar_arrive(bar(T_P + h));
       }
       if (!ok) break;
       // the segment's end: the next one's rows first, whose scores can follow while this one's sums are stored
       const bool head = c.tile != 0, ends = c.tile + count == c.tiles, whole = !head && ends;
-      const int row0 = c.mt * kM, row = row0 + r, item = item_of(p, c), seq = c.b * a.Hkv + c.h;
+      const int row = c.mt * kM + r, item = item_of(p, c), seq = c.b * a.Hkv + c.h;
       if (!head && warp == 8 && lane == 0) {
         const long long end = u - c.tile + c.tiles;  // the unit behind the item
         if (whole) {
@@ -611,44 +621,53 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const Params p) {
           chains_of(p)[p.by_item ? item : id] = Chain{p.by_item ? id : item, static_cast<int>((end * workers - 1) / W)};
         }
       }
-      xsum[h * 128 + r] = l;
+      xm[h * 128 + r] = m;
+      xl[h * 128 + r] = l;
       if (!(ok = exchange())) break;
-      const float lr = xsum[r] + xsum[128 + r];
+      const float m0 = xm[r], m1 = xm[128 + r], both = fmaxf(m0, m1), ref = both == -INFINITY ? 0.f : both;
+      const float w0 = ex2(m0 - ref), w1 = ex2(m1 - ref);
+      const float lr = fmaf(xl[r], w0, xl[128 + r] * w1);
+      const bool has0 = count > 1 || (first_n & 1) == 0, has1 = count > 1 || (first_n & 1) == 1;
       leave(p, prefix, extra, count, c, u);
-      if (!(ok = exchange())) break;  // xsum has been read
+      first_n += count;
       if (u < u1 && !(ok = wwait(T_Q_FREE, it) && load_q(c))) break;
       if (!(ok = wwait(T_O_LAST, it))) break;
       tc_fence_after();
       const bool none = lr == 0.f, in = row < p.R;
-      const float f = whole ? (none ? 0.f : 1.f / lr) : 1.f;
+      const float f = whole ? (none ? 0.f : 1.f / lr) : 1.f, f0 = w0 * f, f1 = w1 * f;
       float* part = partial_of<D>(p, id, head ? 0 : 1);
 #pragma unroll 1
-      for (int k = 0; k < D / 64; ++k) {
-        uint32_t o[32];
-        tmem_ld32(tbase + lrow + C::kTmemO + (D / 2) * h + 32 * k, o);
+      for (int k = 0; k < D / 32; ++k) {  // half of the channels, 16 at a time
+        uint32_t o0[16], o1[16];
+        const uint32_t from = tbase + lrow + C::kTmemO + (D / 2) * h + 16 * k;
+        tmem_ld16(from, o0);
+        tmem_ld16(from + D, o1);
         tmem_wait_ld();
         if (!in) continue;
+        float x[16];
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+          x[i] = (has0 ? __uint_as_float(o0[i]) * f0 : 0.f) + (has1 ? __uint_as_float(o1[i]) * f1 : 0.f);
         if (whole) {
-          uint32_t w[16];
+          uint32_t w[8];
 #pragma unroll
-          for (int i = 0; i < 16; ++i)
-            w[i] = none ? 0u : pack_bf16(__uint_as_float(o[2 * i]) * f, __uint_as_float(o[2 * i + 1]) * f);
-          uint4* dst = reinterpret_cast<uint4*>(a.o + (static_cast<size_t>(seq) * p.R + row) * D + (D / 2) * h + 32 * k);
-#pragma unroll
-          for (int i = 0; i < 4; ++i) dst[i] = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+          for (int i = 0; i < 8; ++i) w[i] = none ? 0u : pack_bf16(x[2 * i], x[2 * i + 1]);
+          uint4* dst = reinterpret_cast<uint4*>(a.o + (static_cast<size_t>(seq) * p.R + row) * D + (D / 2) * h + 16 * k);
+          dst[0] = make_uint4(w[0], w[1], w[2], w[3]);
+          dst[1] = make_uint4(w[4], w[5], w[6], w[7]);
         } else {
-          uint4* dst = reinterpret_cast<uint4*>(part + r * D + (D / 2) * h + 32 * k);
+          float4* dst = reinterpret_cast<float4*>(part + r * D + (D / 2) * h + 16 * k);
 #pragma unroll
-          for (int i = 0; i < 8; ++i) dst[i] = make_uint4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+          for (int i = 0; i < 4; ++i) dst[i] = make_float4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]);
         }
       }
       tc_fence_before();
       mbar_arrive(bar(T_O_FREE));
       if (in && h == 0) {
         if (!whole)
-          *reinterpret_cast<float2*>(part + p.prows * D + 2 * r) = make_float2(m, lr);
+          *reinterpret_cast<float2*>(part + p.prows * D + 2 * r) = make_float2(both, lr);
         else if (a.lse != nullptr)
-          a.lse[static_cast<size_t>(seq) * p.R + row] = none ? -INFINITY : m + log2f(lr);
+          a.lse[static_cast<size_t>(seq) * p.R + row] = none ? -INFINITY : both + log2f(lr);
       }
     }
   }
