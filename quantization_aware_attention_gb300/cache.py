@@ -127,8 +127,8 @@ def qat_attention_tree(q, cache: KVCache, block_table, seq_lens, tree, sm_scale:
     ``tree`` (int64 [B, T], or [T] for all sequences; from ``qat_draft_tree``) says which of them each token sees:
     bit s of tree[b, t] for token s.  Every token sees the whole text before the tree; with ``window``, only keys
     j > i - window of it, and the first ``sinks``, i being the token's position by its depth, seq_lens[b] - T +
-    popcount - 1 (the tree itself is seen by its bits alone).  Everything else as
-    ``qat_attention_decode``; the workspace has ``capi.qat_attn_tree_workspace_bytes(Hq, cache.heads, T, D)``
+    popcount - 1 (the tree itself is seen by its bits alone).  P's tiles are of 64 slots, so a drafted token's P may be
+    quantized in another tile than after ``KVCache.keep``.  Everything else as ``qat_attention_decode``; the workspace has ``capi.qat_attn_tree_workspace_bytes(Hq, cache.heads, T, D)``
     bytes."""
     if not isinstance(cache, KVCache):
         raise TypeError("cache must be a KVCache")

@@ -767,7 +767,11 @@ size_t decode_workspace_bytes(int R, int D) {
 }
 
 cudaError_t launch_decode(const DecodeArgs& a, int D, int num_sms, cudaStream_t s) {
-  if (a.tree != nullptr && a.Hq / a.Hkv * a.T > kRows) return launch_tree(a, D, num_sms, s);
+  // A tree's rows: items of 16 read the cache once each, the tensor core's 128 rows take the time of about 40 (D 128)
+  // or 64 (D 64) of those.  16 sequences of 8192 keys, 8 KV heads, us (items of 16 / tensor core):
+  //   D 128   20 rows  94 / 118   32 rows  95 / 120   64 rows 175 / 123   128 rows 326 / 134   256 rows 629 / 244
+  //   D 64    20 rows  61 / 108   32 rows  62 / 108   64 rows 111 / 110   128 rows 209 / 115   256 rows 403 / 212
+  if (a.tree != nullptr && a.Hq / a.Hkv * a.T > (D == 64 ? 64 : 32)) return launch_tree(a, D, num_sms, s);
   Params p;
   p.a = a;
   p.R = a.Hq / a.Hkv * a.T;
