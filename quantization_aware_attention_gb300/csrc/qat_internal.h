@@ -178,20 +178,24 @@ struct WindowBlocks {
 #endif
 };
 
-// Key blocks of 128 that hold sinks, whose dK and dV sum over all later queries, not a window's: each is cut
-// into this many pieces of query blocks, whose fp32 sums one more kernel adds in order.  A piece has at most
-// a quarter of an SM's share of all the work (or 4 blocks), so that the sinks of one long sequence do not
-// outlast the windows; none is empty.
+// Key blocks of 128 that hold sinks, whose dK and dV sum over all later queries, not a window's: where they are
+// few, each is cut into this many pieces of query blocks, whose fp32 sums one more kernel adds in order.  (Every
+// CTA gets as many items as the others: with pieces of a quarter of an SM's share of the work, 8 heads of 32768
+// tokens with windows of 4096 and 64 sinks took 15 percent longer than without sinks, of which there are 3.)
+// A piece has about as many query blocks as another key block's windows, or a sixteenth of an SM's share of the
+// work if that is more; none is empty, and their sums take at most 1216 slots (160 MB at D 128).
 inline int window_sink_pieces(int B, int H, int N, int window, int sinks) {
   const double heads = static_cast<double>(B) * H;
   const int M = (N + 127) / 128, blocks = (sinks + 127) / 128;
   if (blocks == 0) return 1;
   const int each = (window + 254) / 128 < M ? (window + 254) / 128 : M;  // query blocks that see a key block
+  if (heads * blocks >= 4 * 152) return 1;
   const double share = heads * (static_cast<double>(blocks) * M + static_cast<double>(M - blocks) * each) / 152.0;
-  const double piece = share / 4.0 < 4.0 ? 4.0 : share / 4.0;
-  const int most = M - blocks + 1;
-  const int want = static_cast<int>(ceil(M / piece));
-  return want < 1 ? 1 : (want < most ? want : most);
+  const double piece = share / 16.0 < each ? each : share / 16.0;
+  int most = static_cast<int>(1216 / (heads * blocks));
+  if (most > M - blocks + 1) most = M - blocks + 1;
+  const int want = static_cast<int>(ceil(M / (piece < 4.0 ? 4.0 : piece)));
+  return want < most ? want : most;
 }
 inline size_t window_part_bytes(int B, int H, int N, int D, int window, int sinks) {
   const int n = window_sink_pieces(B, H, N, window, sinks);
