@@ -414,6 +414,7 @@ QAT_API qat_status_t qat_attn_decode(const void* q, const void* k_codes, const v
  *   N        queries and keys;  N <= 2^30
  *   window   >= 1; the query's own key counts, so 1 leaves it alone (and the sinks); N or more: no window
  *   sinks    >= 0, the first keys, which every later query goes on seeing
+ *   o_hp     NULL where no backward will follow: O_q alone, by two products in place of three
  *   k_mean   fp32 [D] or NULL, as in qat_attn_bwd_smooth_k
  *   everything else as in qat_attn_fwd and qat_attn_bwd with Nq = Nkv = N and causal 1.  Tiles of the
  *   quantization are the same absolute 64 keys; a tile's amax is that of the keys that the row sees.

@@ -183,7 +183,7 @@ class QATAttention(torch.autograd.Function):
     @staticmethod
     def forward(ctx, q, k, v, causal=False, sm_scale=None,
                 quant_mode=capi.QUANT_P_FP8E4M3_ROW_TILE64, qkv_quant=False, smooth_k=False,
-                use_qat_qkv_backward=True, check=None, window=None, sinks=0):
+                use_qat_qkv_backward=True, check=None):
         k_mean = None
         q_bwd, k_bwd, v_bwd = q, k, v
         if qkv_quant:  # attention runs on fake-quantized inputs; gradients pass straight
@@ -198,7 +198,7 @@ class QATAttention(torch.autograd.Function):
         elif not use_qat_qkv_backward:
             raise ValueError("use_qat_qkv_backward=False applies only together with qkv_quant")
         ctx.check = _check_enabled(check)
-        o_q, o_hp, lse = qat_attention_forward(q, k, v, causal, sm_scale, quant_mode, window, sinks)
+        o_q, o_hp, lse = qat_attention_forward(q, k, v, causal, sm_scale, quant_mode)
         if ctx.check:
             check_device_status("qat_attn_fwd")
         # the page's backward variant forms Delta from O_q, the straight-through one from O_hp
@@ -206,7 +206,6 @@ class QATAttention(torch.autograd.Function):
         saved = (q_bwd, k_bwd, v_bwd, o_bwd, lse) + ((k_mean,) if k_mean is not None else ())
         ctx.save_for_backward(*saved)
         ctx.causal, ctx.sm_scale, ctx.quant_mode = causal, sm_scale, quant_mode
-        ctx.window, ctx.sinks = window, sinks
         return o_q
 
     @staticmethod
@@ -214,11 +213,30 @@ class QATAttention(torch.autograd.Function):
         q, k, v, o_bwd, lse, *rest = ctx.saved_tensors
         k_mean = rest[0] if rest else None
         dq, dk, dv = qat_attention_backward(q, k, v, o_bwd, lse, do.contiguous(), ctx.causal,
-                                            ctx.sm_scale, ctx.quant_mode, k_mean=k_mean,
-                                            window=ctx.window, sinks=ctx.sinks)
+                                            ctx.sm_scale, ctx.quant_mode, k_mean=k_mean)
         if ctx.check:
             check_device_status("qat_attn_bwd")
-        return dq, dk, dv, None, None, None, None, None, None, None, None, None
+        return dq, dk, dv, None, None, None, None, None, None, None
+
+
+def _window_attention(q, k, v, sm_scale, quant_mode, qkv_quant, smooth_k, use_qat_qkv_backward, check,
+                      window, sinks):
+    for t, name in ((q, "q"), (k, "k"), (v, "v")):
+        _check(t, name, q.shape if isinstance(q, torch.Tensor) else None)
+    by, back, k_mean = (None,) * 3, (None,) * 3, None
+    if qkv_quant:
+        with torch.no_grad():
+            *by, k_mean = qat_prepare_qkv(q, k, v, smooth_k)
+            if use_qat_qkv_backward:
+                back = by
+            elif k_mean is not None:
+                back = (None, qat_subtract_mean(k, k_mean), None)
+    elif smooth_k:
+        raise ValueError("smooth_k changes the result only together with qkv_quant")
+    elif not use_qat_qkv_backward:
+        raise ValueError("use_qat_qkv_backward=False applies only together with qkv_quant")
+    return capi.torch_ops().window_attention(q, k, v, *by, *back, k_mean, sm_scale, quant_mode, window, sinks,
+                                             check)
 
 
 def attention(q, k, v, causal: bool = False, sm_scale: float | None = None,
@@ -237,6 +255,13 @@ def attention(q, k, v, causal: bool = False, sm_scale: float | None = None,
     call cut short is never consumed silently.
     window (causal only): query i sees key j if j <= i and (j > i - window or j < sinks), a
     sliding window beside which the first ``sinks`` keys stay visible; forward and backward
-    take work in proportion to what is seen."""
+    take work in proportion to what is seen.  The same in all but what is seen, but that
+    without gradients O_hp is not computed, that second and forward-mode derivatives are
+    refused, and that a backward is refused under capture while a graph made on the default
+    stream lives that ends in the same leaves or that it passes through."""
+    win = _window(causal, window, sinks)
+    if win is not None:
+        return _window_attention(q, k, v, sm_scale, quant_mode, qkv_quant, smooth_k, use_qat_qkv_backward,
+                                 check, *win)
     return QATAttention.apply(q, k, v, causal, sm_scale, quant_mode, qkv_quant, smooth_k,
-                              use_qat_qkv_backward, check, window, sinks)
+                              use_qat_qkv_backward, check)

@@ -147,7 +147,8 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
 // loop long items ran 2-4% slower.
 // kWin: sliding windows with sinks (causal): an item takes the key blocks that its rows' windows and the
 // sinks lie in, masks those that an edge of a window crosses, and costs as much as they are.
-template <int D, bool kDefer, bool kWin>
+// kHp: the straight-through output O_hp too (else O_q alone, as for inference: a third of the products less).
+template <int D, bool kDefer, bool kWin, bool kHp>
 __global__ void __launch_bounds__(384, 1)
     attn_fwd_tc_kernel(const __grid_constant__ CUtensorMap tmQ,
                        const __grid_constant__ CUtensorMap tmK,
@@ -325,10 +326,12 @@ __global__ void __launch_bounds__(384, 1)
             const uint64_t dv = smem_desc_sw128(vbase + ks * 2048, C::kChunkBytes, 1024);
             mma_ts(tbase + C::kTmemOq, sP + 8 * ks, dv, idPV, (j > 0 || ks > 0) ? 1u : 0u);
           }
+          if constexpr (kHp) {
 #pragma unroll
-          for (int ks = 0; ks < kBN / 16; ++ks) {
-            const uint64_t dv = smem_desc_sw128(vbase + ks * 2048, C::kChunkBytes, 1024);
-            mma_ts(tbase + C::kTmemOhp, sP + 64 + 8 * ks, dv, idPV, (j > 0 || ks > 0) ? 1u : 0u);
+            for (int ks = 0; ks < kBN / 16; ++ks) {
+              const uint64_t dv = smem_desc_sw128(vbase + ks * 2048, C::kChunkBytes, 1024);
+              mma_ts(tbase + C::kTmemOhp, sP + 64 + 8 * ks, dv, idPV, (j > 0 || ks > 0) ? 1u : 0u);
+            }
           }
           issued = true;
           mma_commit(bar(BAR_V_EMPTY + st));
@@ -413,15 +416,15 @@ __global__ void __launch_bounds__(384, 1)
       const int wrow = e_mt * kBM + 32 * quarter;
       const int wvalid = min(32, p.a.Nq - wrow);
       const size_t orow0 = static_cast<size_t>(e_bh) * p.a.Nq + wrow;
-      const uint32_t tO = tbase + lrow + (h ? C::kTmemOhp : C::kTmemOq);
-      uint16_t* out = h ? p.a.o_hp : p.a.o_q;
+      const uint32_t tO = tbase + lrow + (kHp ? (h ? C::kTmemOhp : C::kTmemOq) : C::kTmemOq + D / 2 * h);
+      uint16_t* out = kHp ? (h ? p.a.o_hp : p.a.o_q) : p.a.o_q + D / 2 * h;
       float* out32 = h ? p.a.o_hp_f32 : p.a.o_q_f32;  // partial results stay fp32
 #pragma unroll 1
-      for (int c = 0; c < D / 32; ++c) {
+      for (int c = 0; c < (kHp ? D / 32 : D / 64); ++c) {
         uint32_t o[32];
         tmem_ld32(tO + 32 * c, o);
         tmem_wait_ld();
-        if (out32 != nullptr) {
+        if (kHp && out32 != nullptr) {
 #pragma unroll
           for (int half = 0; half < 2; ++half) {
             uint4 v[4];
@@ -531,19 +534,19 @@ __global__ void __launch_bounds__(384, 1)
             }
           }
           tmem_st16(tS + 32 * h + 16 * c, pq);
-          tmem_st16(tS + 64 + 32 * h + 16 * c, ph);
+          if constexpr (kHp) tmem_st16(tS + 64 + 32 * h + 16 * c, ph);
         }
         l += lsum.x + lsum.y;
         tmem_wait_st();
         if (__any_sync(0xffffffffu, resc)) {
           // O must hold every PV issued so far before it is rescaled; group h rescales
-          // O_q (h = 0) or O_hp (h = 1)
+          // O_q (h = 0) or O_hp (h = 1), or its half of O_q
           ok = wwait(bar(BAR_O_DONE), (pvc - 1) & 1);
           if (!ok) break;
           tc_fence_after();
-          const uint32_t tO = tbase + lrow + (h ? C::kTmemOhp : C::kTmemOq);
+          const uint32_t tO = tbase + lrow + (kHp ? (h ? C::kTmemOhp : C::kTmemOq) : C::kTmemOq + D / 2 * h);
 #pragma unroll 1
-          for (int c = 0; c < D / 32; ++c) {
+          for (int c = 0; c < (kHp ? D / 32 : D / 64); ++c) {
             uint32_t o[32];
             tmem_ld32(tO + 32 * c, o);
             tmem_wait_ld();
@@ -604,8 +607,11 @@ cudaError_t launch_fwd_tc_d(const FwdArgs& a, unsigned int* err, int num_sms, cu
   const bool win = a.window > 0;
   const long long blocks = win ? (a.window + 254ll) / kBN + (a.sinks + kBN - 1) / kBN : (a.Nkv + kBN - 1) / kBN;
   const bool defer = (win || !a.causal) && blocks <= 8;
-  auto kern = win ? (defer ? attn_fwd_tc_kernel<D, true, true> : attn_fwd_tc_kernel<D, false, true>)
-                  : (defer ? attn_fwd_tc_kernel<D, true, false> : attn_fwd_tc_kernel<D, false, false>);
+  auto kern = defer ? attn_fwd_tc_kernel<D, true, false, true> : attn_fwd_tc_kernel<D, false, false, true>;
+  if (win && a.o_hp != nullptr)
+    kern = defer ? attn_fwd_tc_kernel<D, true, true, true> : attn_fwd_tc_kernel<D, false, true, true>;
+  else if (win)
+    kern = defer ? attn_fwd_tc_kernel<D, true, true, false> : attn_fwd_tc_kernel<D, false, true, false>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                        static_cast<int>(C::kSmemBytes));
   if (e != cudaSuccess) return e;

@@ -117,9 +117,10 @@ qat_status_t fwd_impl(const void* q, const void* k, const void* v, void* o_q, vo
   bool empty = false;
   const qat_status_t st = check_sizes(B, H, Nq, Nkv, D, sm_scale, causal, quant_mode, &empty);
   if (st != QAT_OK || empty) return st;
-  const void* ptrs[] = {q, k, v, o_q, o_hp, lse};
+  const void* ptrs[] = {q, k, v, o_q, lse};
   for (const void* p : ptrs)
     if (p == nullptr || !aligned16(p)) return QAT_ERR_INVALID_ARG;
+  if (!aligned16(o_hp) || (o_hp == nullptr && window == 0)) return QAT_ERR_INVALID_ARG;
   qat::FwdArgs a;
   a.q = static_cast<const uint16_t*>(q);
   a.k = static_cast<const uint16_t*>(k);

@@ -436,6 +436,122 @@ std::tuple<OptTensor, OptTensor, OptTensor, OptTensor> norm_rope_bwd(
   return {d[0], opt(d[1]), opt(d[2]), opt(d[3])};
 }
 
+// ------------------------------------------------------------------------------- windowed attention
+
+// What the attention is called with beside its tensors.
+struct WindowArgs {
+  double sm_scale;
+  int quant_mode, window, sinks;
+  bool check;
+};
+
+// What the forward runs on, and the backward (both q, k, v by default), each q, k, v; smooth_k's mean or undefined.
+struct WindowTensors {
+  std::array<Tensor, 3> by, back;
+  Tensor k_mean;
+};
+
+void dense(const Tensor& t, const char* name, const at::Device& dev, at::IntArrayRef shape) {
+  TORCH_CHECK_VALUE(t.is_cuda() && t.device() == dev, name, " must be a CUDA tensor on ", dev, ", got ", t.device());
+  TORCH_CHECK_VALUE(t.scalar_type() == at::kBFloat16, name, " must be torch.bfloat16, got ", t.scalar_type());
+  TORCH_CHECK_VALUE(t.sizes() == shape, name, " has shape ", t.sizes(), ", expected ", shape);
+  TORCH_CHECK_VALUE(t.is_contiguous() && aligned16(t), name, " must be contiguous on a 16-byte boundary");
+  with_memory(t, name);
+}
+
+// {o_q, o_hp, lse}; without `hp` o_hp is undefined.
+std::array<Tensor, 3> window_forward(const Tensor& q, const Tensor& k, const Tensor& v, const WindowArgs& a, bool hp) {
+  on_cuda(q, "q");
+  const at::Device dev = q.device();
+  TORCH_CHECK_VALUE(q.dim() == 4, "q must be [B, H, N, D], got shape ", q.sizes());
+  for (int i = 0; i < 4; ++i) TORCH_CHECK_VALUE(q.size(i) <= INT32_MAX, "q is too large: ", q.sizes());
+  dense(q, "q", dev, q.sizes());
+  dense(k, "k", dev, q.sizes());
+  dense(v, "v", dev, q.sizes());
+  const int64_t B = q.size(0), H = q.size(1), N = q.size(2), D = q.size(3);
+  const c10::cuda::CUDAGuard guard(dev);
+  std::array<Tensor, 3> out{new_tensor(q.sizes(), at::kBFloat16, dev), Tensor(), new_tensor({B, H, N}, at::kFloat, dev)};
+  if (hp) out[1] = new_tensor(q.sizes(), at::kBFloat16, dev);
+  ok(qat_attn_fwd_window(q.const_data_ptr(), k.const_data_ptr(), v.const_data_ptr(), out[0].mutable_data_ptr(),
+                         hp ? out[1].mutable_data_ptr() : nullptr, out[2].mutable_data_ptr<float>(), static_cast<int>(B),
+                         static_cast<int>(H), static_cast<int>(N), static_cast<int>(D), static_cast<float>(a.sm_scale),
+                         a.window, a.sinks, a.quant_mode, stream_of(dev)),
+     "qat_attn_fwd_window");
+  check_status(a.check, dev, "qat_attn_fwd_window");
+  return out;
+}
+
+// The forward ran on the leaves or on what was made of them (fake-quantized copies); the backward goes through the
+// tensors it is given as if they were the leaves.
+struct WindowAttention : torch::autograd::Function<WindowAttention> {
+  static variable_list forward(AutogradContext* ctx, const Tensor& q, const Tensor& k, const Tensor& v,
+                               const WindowTensors& x, const WindowArgs& a) {
+    const auto out = window_forward(x.by[0], x.by[1], x.by[2], a, true);
+    // the page's backward variant forms Delta from O_q, the straight-through one from O_hp
+    const Tensor& o = a.quant_mode == QAT_QUANT_P_FP8E4M3_ROW_TILE64_PAGE_BWD ? out[0] : out[1];
+    ctx->save_for_backward({x.back[0], x.back[1], x.back[2], o, out[2], x.k_mean});
+    ctx->saved_data["sm_scale"] = a.sm_scale;
+    ctx->saved_data["quant_mode"] = static_cast<int64_t>(a.quant_mode);
+    ctx->saved_data["window"] = static_cast<int64_t>(a.window);
+    ctx->saved_data["sinks"] = static_cast<int64_t>(a.sinks);
+    ctx->saved_data["check"] = a.check;
+    return {out[0]};
+  }
+
+  static variable_list backward(AutogradContext* ctx, variable_list grads) {
+    TORCH_CHECK(!at::GradMode::is_enabled(), "windowed attention has no second derivative");
+    const variable_list t = ctx->get_saved_variables();
+    const at::Device dev = t[0].device();
+    check_capture_before(dev);
+    no_tangent("windowed attention's backward", {&grads[0]});
+    Tensor g = grads[0].contiguous();
+    if (!aligned16(g)) g = g.clone();
+    dense(g, "the gradient", dev, t[0].sizes());
+    const int B = static_cast<int>(t[0].size(0)), H = static_cast<int>(t[0].size(1)), N = static_cast<int>(t[0].size(2)),
+              D = static_cast<int>(t[0].size(3));
+    const int window = static_cast<int>(ctx->saved_data["window"].toInt()),
+              sinks = static_cast<int>(ctx->saved_data["sinks"].toInt());
+    const c10::cuda::CUDAGuard guard(dev);
+    const size_t bytes = qat_attn_bwd_window_workspace_bytes(B, H, N, D, window, sinks);
+    Tensor ws = new_tensor({std::max<int64_t>(static_cast<int64_t>(bytes), 256)}, at::kByte, dev);
+    variable_list d(3);
+    for (Tensor& x : d) x = new_tensor(t[0].sizes(), at::kBFloat16, dev);
+    ok(qat_attn_bwd_window(t[0].const_data_ptr(), t[1].const_data_ptr(), t[2].const_data_ptr(), t[3].const_data_ptr(),
+                           t[4].const_data_ptr<float>(), g.const_data_ptr(), d[0].mutable_data_ptr(),
+                           d[1].mutable_data_ptr(), d[2].mutable_data_ptr(),
+                           static_cast<const float*>(ptr_or_null(t[5])), B, H, N, D,
+                           static_cast<float>(ctx->saved_data["sm_scale"].toDouble()), window, sinks,
+                           static_cast<int>(ctx->saved_data["quant_mode"].toInt()), ws.mutable_data_ptr(),
+                           static_cast<size_t>(ws.numel()), stream_of(dev)),
+       "qat_attn_bwd_window");
+    check_status(ctx->saved_data["check"].toBool(), dev, "qat_attn_bwd_window");
+    return {d[0], d[1], d[2], Tensor(), Tensor()};
+  }
+};
+
+Tensor window_attention(const Tensor& q, const Tensor& k, const Tensor& v, const WindowTensors& x,
+                        std::optional<double> sm_scale, int64_t quant_mode, int64_t window, int64_t sinks, std::optional<bool> check) {
+  no_tangent("windowed attention", {&q, &k, &v});
+  TORCH_CHECK_VALUE(quant_mode >= 0 && quant_mode <= 2, "quant_mode ", quant_mode);
+  TORCH_CHECK_VALUE(window >= 1 && sinks >= 0, "window must be at least 1 and sinks at least 0, got ", window, " and ",
+                    sinks);
+  if (!check.has_value()) {
+    const char* env = std::getenv("QAT_CHECK_STATUS");
+    check = env != nullptr && env[0] == '1' && env[1] == 0;
+  }
+  const double scale = sm_scale.has_value() ? *sm_scale
+                       : q.dim() == 4       ? 1.0 / std::sqrt(static_cast<double>(std::max<int64_t>(q.size(3), 1)))
+                                            : 1.0;
+  window = std::min<int64_t>(window, 1 << 30);
+  sinks = std::min<int64_t>(sinks, 1 << 30);
+  const WindowArgs a{scale, static_cast<int>(quant_mode), static_cast<int>(window), static_cast<int>(sinks), *check};
+  if (!at::GradMode::is_enabled() || !(q.requires_grad() || k.requires_grad() || v.requires_grad()))
+    return window_forward(x.by[0], x.by[1], x.by[2], a, false)[0];
+  on_cuda(q, "q");
+  check_capture({&q, &k, &v}, q.device());
+  return WindowAttention::apply(q, k, v, x, a)[0];
+}
+
 // ------------------------------------------------------------------------------- cache
 
 struct Cache {
@@ -689,6 +805,25 @@ PyObject* py_norm_rope(PyObject*, PyObject* const* args, Py_ssize_t n) {
   END_HANDLE_TH_ERRORS
 }
 
+PyObject* py_window_attention(PyObject*, PyObject* const* args, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  Args a(args, n, 15);
+  const Tensor &q = a.tensor(), &k = a.tensor(), &v = a.tensor();
+  WindowTensors x;
+  for (auto* list : {&x.by, &x.back})
+    for (int i = 0; i < 3; ++i) {
+      const OptTensor t = a.optional_tensor();
+      (*list)[i] = t.has_value() ? *t : i == 0 ? q : i == 1 ? k : v;
+    }
+  x.k_mean = or_undefined(a.optional_tensor());
+  const std::optional<double> sm_scale = a.optional_real();
+  const int64_t quant_mode = a.integer(), window = a.integer(), sinks = a.integer();
+  return py::cast(window_attention(q, k, v, x, sm_scale, quant_mode, window, sinks, a.optional_boolean()))
+      .release()
+      .ptr();
+  END_HANDLE_TH_ERRORS
+}
+
 PyObject* py_kv_append(PyObject*, PyObject* const* args, Py_ssize_t n) {
   HANDLE_TH_ERRORS
   Args a(args, n, 10);
@@ -763,7 +898,7 @@ PyMethodDef method(const char* name) {
 
 PYBIND11_MODULE(_qat_torch, m) {
   m.def("norm_rope_bwd", &norm_rope_bwd);
-  static PyMethodDef methods[] = {method<py_norm_rope>("norm_rope"), method<py_kv_append>("kv_append"),
+  static PyMethodDef methods[] = {method<py_norm_rope>("norm_rope"), method<py_window_attention>("window_attention"), method<py_kv_append>("kv_append"),
                                   method<py_kv_read>("kv_read"), method<py_decode>("decode"),
                                   method<py_draft_tree>("draft_tree"), method<py_kv_keep>("kv_keep"),
                                   {nullptr, nullptr, 0, nullptr}};

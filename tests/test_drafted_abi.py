@@ -65,8 +65,10 @@ def test_backward_workspace():
     f = capi.qat_attn_bwd_window_workspace_bytes
     base = f(1, 8, 65536, 128, 512, 0)
     assert base > 0 and (f(1, 8, 65536, 128, 512, 4) - base) % (8 * 2 * 128 * 128 * 4) == 0
-    assert 8 <= (f(1, 8, 65536, 128, 512, 4) - base) // (8 * 2 * 128 * 128 * 4) <= 32
-    assert f(4, 32, 8192, 128, 1024, 4) == f(4, 32, 8192, 128, 1024, 0)  # enough work for all SMs
+    assert 8 <= (f(1, 8, 65536, 128, 512, 4) - base) // (8 * 2 * 128 * 128 * 4) <= 128
+    assert f(20, 32, 8192, 128, 1024, 4) == f(20, 32, 8192, 128, 1024, 0)  # enough heads for all SMs
+    for S in (1, 500, 4000, 8191):  # never more than 1216 pieces
+        assert f(1, 8, 8192, 64, 64, S) - f(1, 8, 8192, 64, 64, 0) <= 1216 * 2 * 128 * 64 * 4
     assert f(1, 1, 4096, 64, 128, 4096) == f(1, 1, 4096, 64, 128, 1 << 30)
     for bad in ((1, 1, 8, 64, 0, 0), (1, 1, 8, 64, 1, -1), (1, 1, 8, 96, 1, 0), (-1, 1, 8, 64, 1, 0)):
         assert f(*bad) == 0

@@ -207,3 +207,70 @@ def test_refusals():
     with pytest.raises(ValueError):
         attention(q[..., :32], k, v, causal=True, window=4)
     check_device_status()
+
+
+def test_without_gradients_the_output_is_the_same():
+    """A call without gradients leaves O_hp out (null through the C ABI); its output is the training forward's."""
+    for N, D, window, sinks in ((700, 128, 200, 4), (1500, 64, 1400, 0), (130, 128, 20, 1)):
+        _, (q, k, v, _) = _inputs(15, 1, 2, N, D)
+        o_q, _, lse = qat_attention_forward(q, k, v, True, window=window, sinks=sinks)
+        with torch.no_grad():
+            assert torch.equal(attention(q, k, v, causal=True, window=window, sinks=sinks, check=True), o_q)
+        o = torch.full_like(q, float("nan"))
+        stats = torch.empty_like(lse)
+        assert capi.qat_attn_fwd_window(q, k, v, o, None, stats, 1, 2, N, D, D ** -0.5, window, sinks, 1) == 0
+        assert torch.equal(o, o_q) and torch.equal(stats, lse)
+
+
+def test_derivatives_that_are_not_there():
+    """A second derivative, forward-mode derivatives, and a captured backward of leaves in which a graph of the default
+    stream ends (torch would wait for the capture on that stream) are refused."""
+    import torch.autograd.forward_ad as fwad
+    _, (q, k, v, do) = _inputs(16, 1, 1, 128, 64)
+    how = dict(causal=True, window=30, sinks=2)
+    leaves = [x.clone().requires_grad_(True) for x in (q, k, v)]
+    o = attention(*leaves, **how)
+    with pytest.raises(RuntimeError, match="second derivative"):
+        torch.autograd.grad(o, leaves, do, create_graph=True)
+    with fwad.dual_level():
+        with pytest.raises(ValueError, match="forward-mode"):
+            attention(fwad.make_dual(q, q), k, v, **how)
+    want = torch.autograd.grad(o, leaves, do, retain_graph=True)
+    side = torch.cuda.Stream()
+    graph = torch.cuda.CUDAGraph()
+    with pytest.raises(ValueError, match="default stream"):
+        with torch.cuda.graph(graph, stream=side):
+            attention(*leaves, **how)
+    del o, graph
+    torch.cuda.synchronize()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):  # warm, on the capturing stream
+        torch.autograd.grad(attention(*leaves, **how), leaves, do)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=side):
+        got = torch.autograd.grad(attention(*leaves, **how), leaves, do)
+    for _ in range(2):
+        for g in got:
+            g.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(g, w) for g, w in zip(got, want))
+
+
+def test_gradient_layouts():
+    """An upstream gradient that is broadcast, strided or off the 16-byte boundary."""
+    _, (q, k, v, do) = _inputs(17, 1, 2, 130, 64)
+    how = dict(causal=True, window=30, sinks=2)
+    leaves = [x.clone().requires_grad_(True) for x in (q, k, v)]
+    want = torch.autograd.grad(attention(*leaves, **how), leaves, do)
+    flat = torch.empty(do.numel() + 1, dtype=do.dtype, device="cuda")
+    off = flat[1:].view(do.shape)
+    off.copy_(do)
+    for g in (do.transpose(1, 2).contiguous().transpose(1, 2), off):
+        got = torch.autograd.grad(attention(*leaves, **how), leaves, g)
+        assert all(torch.equal(x, y) for x, y in zip(got, want))
+    ones = torch.autograd.grad(attention(*leaves, **how).sum(), leaves)
+    full = torch.autograd.grad(attention(*leaves, **how), leaves, torch.ones_like(do))
+    assert all(torch.equal(x, y) for x, y in zip(ones, full))
+    only_v = [q, k, v.clone().requires_grad_(True)]
+    assert torch.equal(torch.autograd.grad(attention(*only_v, **how), only_v[2:], do)[0], want[2])
