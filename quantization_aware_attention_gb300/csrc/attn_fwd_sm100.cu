@@ -603,10 +603,12 @@ cudaError_t launch_fwd_tc_d(const FwdArgs& a, unsigned int* err, int num_sms, cu
   p.items = BH * p.mtiles;
   // a causal item streams its head's K and V blocks
   p.hgroup = causal_head_group(4ll * a.Nkv * D, BH);
-  // deferred epilogues for items of at most 8 key blocks (not for causal ones, whose lengths differ)
+  // Deferred epilogues for items of at most 8 key blocks (not for causal ones, whose lengths differ).  With windows
+  // up to 5, and throughout where O_q is all (B4 H32 N8192 D128, us deferred / not, with and without O_hp: W 512
+  // 512 / 521 and 413 / 440, W 896 734 / 709 and 596 / 625, W 1024 S 4 878 / 834 and 716 / 746).
   const bool win = a.window > 0;
   const long long blocks = win ? (a.window + 254ll) / kBN + (a.sinks + kBN - 1) / kBN : (a.Nkv + kBN - 1) / kBN;
-  const bool defer = (win || !a.causal) && blocks <= 8;
+  const bool defer = win ? a.o_hp == nullptr || blocks <= 5 : !a.causal && blocks <= 8;
   auto kern = defer ? attn_fwd_tc_kernel<D, true, false, true> : attn_fwd_tc_kernel<D, false, false, true>;
   if (win && a.o_hp != nullptr)
     kern = defer ? attn_fwd_tc_kernel<D, true, true, true> : attn_fwd_tc_kernel<D, false, true, true>;
