@@ -18,10 +18,10 @@
 //   warp 0      TMA producer: per item K_0 and V_0, the item's dO tile (once the
 //               previous item's last dP has read the buffer), then the other K_j (4-stage
 //               ring) and V_j (2-stage ring), 128 rows x D in 128-byte-swizzled boxes.
-//   warp 1      TMEM owner; lane 0 issues, per block j, S_{j+1} then dQ_{j-1}:
+//   warp 1      TMEM owner; one lane issues, per block j, S_{j+1} then dQ_{j-1}:
 //                 S  = Q K^T      TS  (A = Q bf16 in TMEM, B = K_j K-major)   -> TMEM S
 //                 dQ += dS K      TS  (A = dS bf16 in TMEM, B = K_j MN-major) -> TMEM dQ
-//   warp 2      lane 0 issues dP = dO V^T (SS, A = dO K-major, B = V_j K-major) -> TMEM dP
+//   warp 2      one lane issues dP = dO V^T (SS, A = dO K-major, B = V_j K-major) -> TMEM dP
 //               as soon as the compute warps have read the previous dP.
 //               Two issuers let the dP stream run ahead independently of the S / dQ
 //               stream.  S, dP and dS each have their own TMEM columns, so no product
@@ -237,7 +237,7 @@ __global__ void __launch_bounds__(384, 1)
     }
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMA issuer A: S, dQ
-    if (lane == 0) {
+    if (elect_one()) {
       constexpr uint32_t idS = idesc_bf16_f32(kBlk, kBlk, false);  // S (B = K K-major)
       constexpr uint32_t idQ = idesc_bf16_f32(kBlk, D, true);      // dQ (B = K MN-major)
       uint32_t kc = 0, bc = 0;  // K tiles, blocks (global counts)
@@ -302,7 +302,7 @@ __global__ void __launch_bounds__(384, 1)
     }
   } else if (warp == 2) {
     // ------------------------------------------------------------ MMA issuer B: dP
-    if (lane == 0) {
+    if (elect_one()) {
       constexpr uint32_t idS = idesc_bf16_f32(kBlk, kBlk, false);
       uint32_t vc = 0, bc = 0;
       int it = 0;

@@ -24,7 +24,7 @@
 // attn_bwd_dkdv_kernel, 352 threads:
 //   warp 0      TMA producer: the ones tile once; K, V once per item; per 128-row query
 //               block Q with its lse_ext rows and dO with its d_ext rows (2 stages each).
-//   warps 1, 2  MMA issuers (lane 0 of each); warp 1 also owns TMEM:
+//   warps 1, 2  MMA issuers (one lane of each); warp 1 also owns TMEM:
 //                 warp 1:  dV  += P^T_b dO    TS  (A = P^T bf16 in TMEM [0,32) + [64,96),
 //                                                  B = dO MN-major), then
 //                          S^T_{b+1} = K Q^T  SS  -> TMEM [0,128)   (A = K, B = Q, K-major)
@@ -357,7 +357,7 @@ __global__ void __launch_bounds__(384, 1)
     }
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMA issuer A: S^T, dV
-    if (lane == 0) {
+    if (elect_one()) {
       constexpr uint32_t idSS = idesc_bf16_f32(kBlk, kBlk, false, false);  // S^T
       constexpr uint32_t idKM = idesc_bf16_f32(kBlk, D, true, false);      // dV
       const uint32_t sK = base + C::kOffK;
@@ -423,7 +423,7 @@ __global__ void __launch_bounds__(384, 1)
     }
   } else if (warp == 2) {
     // ------------------------------------------------------------ MMA issuer B: dK, dP^T
-    if (lane == 0) {
+    if (elect_one()) {
       constexpr uint32_t idSS = idesc_bf16_f32(kBlk, kBlk, false, false);  // dP^T
       constexpr uint32_t idKM = idesc_bf16_f32(kBlk, D, true, false);      // dK
       const uint32_t sV = base + C::kOffV;

@@ -330,7 +330,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const Params p) {
     for (uint32_t i = n > kScStages ? n - kScStages : 0; i < n; ++i) mbar_wait_drain(bar(T_SC + i % kScStages), i / kScStages & 1, a.err);
   } else if (warp == 1) {
     // ------------------------------------------------------------ products
-    if (lane == 0) {
+    if (elect_one()) {
       constexpr uint32_t idS = idesc_bf16_f32(kM, kStep, false), idO = idesc_bf16_f32(kM, D, true);
       uint32_t n = 0, it = 0;
       bool issued = false;
