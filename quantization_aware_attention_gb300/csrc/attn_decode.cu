@@ -531,7 +531,7 @@ __global__ void __launch_bounds__(32 * Cfg<D, NR>::kWarps, 1) decode_kernel(cons
             bool h = key > last[n][i & 1];
             if (kMask == kTree) {
               const int place = key - base;  // among the drafted tokens
-              h = place >= 0 && (place >= a.T || !(bits[i & 1] >> (place & 63) & 1ull));
+              h = place >= a.T || (place >= 0 && !(bits[i & 1] >> place & 1ull));
             }
             if (kMask != kAll && a.window > 0 && (kMask == kWindow || key < base))
               h |= key <= last[n][i & 1] - a.window && key >= a.sinks;

@@ -140,7 +140,6 @@ __device__ __forceinline__ unsigned long long hidden_keys(const DecodeArgs& a, i
   const int base = len - a.T;
   unsigned long long seen = ones(0, base - key0);
   if (a.window > 0) seen &= ~ones(max(a.sinks - key0, 0), pos - a.window + 1 - key0);
-  if (a.T < 64) mask &= (1ull << a.T) - 1;
   const int at = base - key0;  // where the first token's key lies
   if (at >= 0)
     seen |= at < 64 ? mask << at : 0ull;

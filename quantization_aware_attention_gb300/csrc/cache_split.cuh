@@ -27,7 +27,6 @@ constexpr float kPTop = 16384.f;  // the largest weight as an f16 operand
 constexpr uint32_t kPTopAt = (127u + 127u + 14u) << 23;  // minus a power of two's bits: those of kPTop over it
 constexpr uint32_t kNoPage = 0xffffffffu, kBadPage = 0xfffffffeu;
 
-
 // Workspace: the header, the chains, then the partials: two per worker, [0] of the item its range ends or
 // passes through ("head"), [1] of the item it begins and does not end ("tail"), each rows x D sums and
 // rows x (m, l).  An item that ranges cut leaves a chain of partials: the tail of the worker in whose range
@@ -87,7 +86,8 @@ template <int kMask, int kUnit = kTile>
 __device__ __forceinline__ void find_gap(const DecodeArgs& a, int len, Cursor& c) {
   c.gap_at = c.gap = c.low = 0;
   if (kMask == kAll || a.window == 0) return;
-  c.low = max(len - a.T - a.window, 0);  // one early: a drafted token without ancestors has the position before
+  // the first token's window; a drafted token with an empty mask has the position before it
+  c.low = max(len - a.T - a.window + (kMask == kTree ? 0 : 1), 0);
   c.gap_at = (min(a.sinks, len) + kUnit - 1) / kUnit;
   c.gap = max(c.low / kUnit - c.gap_at, 0);
 }
@@ -128,7 +128,7 @@ __device__ __forceinline__ void advance(const Params& p, const int* prefix, int 
 }
 
 __device__ __forceinline__ unsigned long long mask_of(const DecodeArgs& a, int b, int token) {
-  return a.tree[b * a.tree_sb + token];
+  return a.tree[b * a.tree_sb + token] & (~0ull >> (kTreeMaxTokens - a.T));  // bits from T on name no token
 }
 
 __device__ __forceinline__ int item_of(const Params& p, const Cursor& c) {

@@ -824,6 +824,7 @@ qat_status_t qat_kv_cache_keep(void* k_codes, void* v_codes, float* k_scales, fl
   for (const int* p : {path_lens, static_cast<const int*>(new_lens)})
     if (p == nullptr || (reinterpret_cast<uintptr_t>(p) & 3u) != 0) return QAT_ERR_INVALID_ARG;
   if (L > 0 && (path == nullptr || (reinterpret_cast<uintptr_t>(path) & 3u) != 0)) return QAT_ERR_INVALID_ARG;
+  if (new_lens == seq_lens || new_lens == path_lens) return QAT_ERR_INVALID_ARG;  // read by a sequence's other blocks
   qat::KvKeepArgs a = {};
   a.k_codes = static_cast<uint8_t*>(k_codes);
   a.v_codes = static_cast<uint8_t*>(v_codes);

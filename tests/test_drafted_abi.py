@@ -147,7 +147,7 @@ def test_draft_validation(kw, want):
     assert capi.qat_draft_tree(**{**DRAFT, **kw}) == want
 
 
-KEEP = dict(k_codes=A, v_codes=A, k_scales=A, v_scales=A, block_table=A, seq_lens=A, path=A, path_lens=A, new_lens=A,
+KEEP = dict(k_codes=A, v_codes=A, k_scales=A, v_scales=A, block_table=A, seq_lens=A, path=A, path_lens=A, new_lens=2 * A,
             B=2, H=2, T=8, L=4, D=64, num_pages=4, page_size=16, max_pages=2, stream=0)
 
 
@@ -162,6 +162,9 @@ KEEP = dict(k_codes=A, v_codes=A, k_scales=A, v_scales=A, block_table=A, seq_len
     (dict(new_lens=None), Status.INVALID_ARG),
     (dict(k_codes=A + 4), Status.INVALID_ARG),
     (dict(B=0, path=None), Status.OK),
+    # blocks of one sequence read what another writes the new length to
+    (dict(seq_lens=A + 64, new_lens=A + 64), Status.INVALID_ARG),
+    (dict(path_lens=A + 64, new_lens=A + 64), Status.INVALID_ARG),
 ])
 def test_keep_validation(kw, want):
     assert capi.qat_kv_cache_keep(**{**KEEP, **kw}) == want

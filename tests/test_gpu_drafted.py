@@ -153,6 +153,24 @@ def test_decode_window_bad_pages_and_lengths():
     assert (o == 0).all() and torch.isneginf(lse).all()
 
 
+@pytest.mark.parametrize("D,page,T,sinks", [(64, 16, 1, 0), (128, 16, 3, 16), (64, 32, 16, 33), (128, 256, 2, 0)])
+def test_windows_that_begin_with_a_page(D, page, T, sinks):
+    """The first token's window begins where a page does: the page before it is not looked up, the page itself is."""
+    first = 3 * page
+    window = 2 * page - T + 1
+    lens = [first + window + T - 1]
+    cache, table, _, _ = _cache(lens, 2, D, page, 9)
+    q = dev_bf16(normal_bf16(13, (1, 4, T, D)))
+    want = qat_attention_decode(q, cache, _i32(table), _i32(lens), window=window, sinks=sinks, check=True)
+    given = table.copy()
+    given[0, 2] = -1
+    got = qat_attention_decode(q, cache, _i32(given), _i32(lens), window=window, sinks=sinks, check=True)
+    assert torch.equal(got, want)
+    given[0, 3] = -1
+    got = qat_attention_decode(q, cache, _i32(given), _i32(lens), window=window, sinks=sinks)
+    assert capi.qat_attn_device_status() == Status.BAD_PAGE and torch.isnan(got[:, :, 0]).all()
+
+
 # ------------------------------------------------------------------ trees
 
 def _trees(rng, B, T, kind):
@@ -223,6 +241,20 @@ def test_tree_with_a_window(Hq, Hkv, T, D, window, sinks):
     o, lse = qat_attention_tree(q, cache, _i32(table), _i32(lens), _i64(masks), return_lse=True, check=True,
                                 window=window, sinks=sinks)
     _compare(o, lse, q, lens, seen_of, cache, page, (table, codes, scales), 1, _eps(Hq, Hkv, T, D))
+
+
+@pytest.mark.parametrize("Hq,T,D", [(2, 5, 64), (4, 40, 128)])
+def test_bits_of_no_token(Hq, T, D):
+    """Bits from T on are ignored: they name no token, and do not add to the depth that windows go by."""
+    lens, page = [300, 60], 16
+    masks = _trees(np.random.default_rng(T), 2, T, "tree")
+    more = [[m | (2 ** 64 - 2 ** T) for m in row] for row in masks]
+    cache, table, _, _ = _cache(lens, 1, D, page, 21)
+    q = dev_bf16(normal_bf16(41, (2, Hq, T, D)))
+    for how in ({}, dict(window=20, sinks=2)):
+        a, b = (qat_attention_tree(q, cache, _i32(table), _i32(lens), _i64(m), return_lse=True, check=True, **how)
+                for m in (masks, more))
+        assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
 
 
 @pytest.mark.parametrize("lens,Hq,Hkv,T,D", [
