@@ -647,3 +647,48 @@ def test_calls_on_two_streams():
     for i in range(2):
         for x, y in got[i]:
             assert torch.equal(x, want[i][0]) and torch.equal(y, want[i][1])
+
+
+@pytest.mark.parametrize("Hq,T", [(8, 4), (16, 16)])
+def test_offsets_beyond_32_bits(Hq, T):
+    """A cache whose codes pass 2^32 bytes, the sequences on its last pages: the bits of a small cache's results."""
+    lens, Hkv, D, page, B = [300, 77], 8, 128, 128, 2
+    small, table, _, _ = _cache(lens, Hkv, D, page, 5)
+    n, pages = small.k.shape[0], (1 << 32) // (Hkv * page * D) + 40
+    big = KVCache.empty(pages, Hkv, page, D)
+    for x, y in ((big.k, small.k), (big.v, small.v)):
+        x.view(torch.uint8)[pages - n:] = y.view(torch.uint8)
+    for x, y in ((big.k_scale, small.k_scale), (big.v_scale, small.v_scale)):
+        x[pages - n:] = y
+    q = dev_bf16(normal_bf16(12, (B, Hq, T, D)))
+    tree = _i64(_trees(np.random.default_rng(T), 1, T, "tree")[0])
+    path, kept = _i32(np.stack([np.arange(1, T, 2)] * B)), _i32([T // 2] * B)
+    got = []
+    for cache, at in ((small, 0), (big, pages - n)):
+        given = _i32(table + at)
+        got.append((qat_attention_tree(q, cache, given, _i32(lens), tree, check=True),
+                    qat_attention_decode(q, cache, given, _i32(lens), window=100, sinks=4, check=True),
+                    cache.keep(given, _i32(lens), T, path, kept, check=True)))
+    assert all(torch.equal(x, y) for x, y in zip(*got))
+    assert torch.equal(big.k.view(torch.uint8)[pages - n:], small.k.view(torch.uint8))
+    assert torch.equal(big.v_scale[pages - n:].view(torch.int32), small.v_scale.view(torch.int32))
+
+
+def test_expired_waits_of_the_wide_kernel():
+    """With the waits' limit at nothing the kernel gives up at a wait, lets its copies and products complete, reports it
+    and returns; the next call gives what the first gave."""
+    lens, D, page, T, Hq = [20000, 300, 9000], 128, 64, 32, 8
+    cache, table, _, _ = _cache(lens, 1, D, page, 4)
+    q = dev_bf16(normal_bf16(10, (3, Hq, T, D)))
+    args = (q, cache, _i32(table), _i32(lens), _i64(_trees(np.random.default_rng(4), 3, T, "tree")))
+    want = qat_attention_tree(*args, check=True)
+    assert capi.qat_debug_set_wait_limit_us(0) == Status.OK
+    try:
+        with pytest.raises(QatError) as e:
+            for _ in range(5):
+                qat_attention_tree(*args, check=True)
+        assert e.value.status == Status.TIMEOUT
+    finally:
+        assert capi.qat_debug_set_wait_limit_us(4000000) == Status.OK
+        capi.qat_attn_device_status()
+    assert torch.equal(qat_attention_tree(*args, check=True), want)

@@ -274,3 +274,52 @@ def test_gradient_layouts():
     assert all(torch.equal(x, y) for x, y in zip(ones, full))
     only_v = [q, k, v.clone().requires_grad_(True)]
     assert torch.equal(torch.autograd.grad(attention(*only_v, **how), only_v[2:], do)[0], want[2])
+
+
+def test_offsets_beyond_32_bits():
+    """Tensors of more than 2^31 elements: the last head's results are those of a call with that head alone."""
+    H, N, D, window, sinks = 136, 131072, 128, 200, 4
+    x = torch.empty((1, H, N, D), dtype=torch.bfloat16, device="cuda").normal_(generator=torch.Generator("cuda").manual_seed(3))
+    how = dict(window=window, sinks=sinks)
+    o_q, o_hp, lse = qat_attention_forward(x, x, x, True, **how)
+    last = x[:, -1:].contiguous()
+    want = qat_attention_forward(last, last, last, True, **how)
+    for got, w in zip((o_q, o_hp, lse), want):
+        assert torch.equal(got[:, -1:], w)
+    del o_q
+    grads = qat_attention_backward(x, x, x, o_hp, lse, x, True, **how)
+    alone = qat_attention_backward(last, last, last, want[1], want[2], last, True, **how)
+    assert torch.equal(grads[0][:, -1:], alone[0])
+    keys = slice((sinks + 127) // 128 * 128, None)  # the sinks' own sums are cut into other pieces
+    for got, w in zip(grads[1:], alone[1:]):
+        assert torch.equal(got[:, -1:, keys], w[:, :, keys])
+        assert rel_l2(host_f64(got[:, -1:, :sinks]), host_f64(w[:, :, :sinks])) <= TOL_Q
+    check_device_status()
+
+
+def test_scale():
+    f, t = _inputs(18, 1, 1, 300, 64)
+    heads = [(0, 0)]
+    _check(_run(t, 50, 3, sm=0.3), _want(f, 0.3, do_.window_seen(range(300), 300, 50, 3), heads), heads)
+
+
+def test_expired_waits():
+    """With the waits' limit at nothing forward and backward give up, report it, and the next calls are whole."""
+    _, t = _inputs(19, 1, 8, 2048, 128)
+    want = _run(t, 700, 4)
+    q, k, v, do = t
+    assert capi.qat_debug_set_wait_limit_us(0) == 0
+    try:
+        with pytest.raises(QatError):
+            for _ in range(5):
+                attention(q, k, v, causal=True, window=700, sinks=4, check=True)
+        seen = False
+        for _ in range(5):
+            qat_attention_backward(q, k, v, want["o_hp"], want["lse"], do, True, window=700, sinks=4)
+            seen |= capi.qat_attn_device_status() == capi.Status.TIMEOUT
+        assert seen
+    finally:
+        assert capi.qat_debug_set_wait_limit_us(4000000) == 0
+        capi.qat_attn_device_status()
+    got = _run(t, 700, 4)
+    assert all(torch.equal(got[n], want[n]) for n in want)
