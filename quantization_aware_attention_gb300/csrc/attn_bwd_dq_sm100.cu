@@ -458,10 +458,10 @@ __global__ void __launch_bounds__(384, 1)
         const int key0 = jb * kBlk + 64 * h;
         if constexpr (kWin) {  // and keys before the row's window, but for the sinks
           if (jb == mt || (jb * kBlk < mt * kBlk + kBlk - p.a.window && jb * kBlk + kBlk > p.a.sinks)) {
-            const int lim = min(p.a.Nkv - 1, row), low = row - p.a.window;
+            const unsigned long long seen = window_seen(row, key0, p.a.window, p.a.sinks, p.a.Nkv);
 #pragma unroll
             for (int i = 0; i < 64; ++i)
-              if (key0 + i > lim || (key0 + i <= low && key0 + i >= p.a.sinks)) pr[i] = 0u;
+              if (!(seen >> i & 1)) pr[i] = 0u;
           }
         } else if (key0 + 64 > p.a.Nkv || (p.a.causal && j == mt)) {
           const int lim = p.a.causal ? min(p.a.Nkv - 1, row) : p.a.Nkv - 1;

@@ -498,13 +498,17 @@ __global__ void __launch_bounds__(384, 1)
       const bool okw = mbar_wait(b_, par, abort_flag, p.err);
       return __all_sync(0xffffffffu, okw) != 0;
     };
-    // kWin: whether some query of block blk lies behind the window of some key of block kb, and the last query
-    // that sees this thread's key
+    // kWin: whether some query of block blk lies behind the window of some key of block kb; the queries qh .. qh + 63
+    // that see this thread's key
     auto behind = [&](int blk, int kb) {
       return kWin && blk * kBlk + kBlk > kb * kBlk + p.a.window && kb * kBlk + kBlk > p.a.sinks;
     };
-    auto newest = [&](int key) { return key < p.a.sinks ? 0x7fffffff : key + p.a.window - 1; };
-    uint32_t Pp[32];                                  // P^T of the current block, bf16 pairs
+    auto seen_by = [&](int qh, int key, bool key_ok) {
+      return key_ok ? ones(key - qh, key < p.a.sinks ? 64 : key + p.a.window - qh) : 0ull;
+    };
+    // P^T of the current block, bf16 pairs.  kWin: fp32, for dS of fp32 P (dK's relative error 2.5e-3 in place of
+    // 3.0e-3, with the 160 registers that are there and in the same time).
+    uint32_t Pp[kWin ? 64 : 32];
     // this thread's row of P^T (64 queries, bf16 pairs) over its S^T columns [64h, 64h+32):
     // the A operand of the dV MMA
     auto store_pt = [&](const uint32_t (&v)[32]) -> bool {
@@ -521,10 +525,29 @@ __global__ void __launch_bounds__(384, 1)
       if (!wwait(bar(B_S_FULL), c & 1)) return false;
       tc_fence_after();
       const bool diag = (kWin || p.a.causal) && blk == kb;
-      const bool far = behind(blk, kb);
-      const int until = kWin ? newest(key) : 0;
       const int qh = blk * kBlk + 64 * h;             // first query of this thread's columns
-      {
+      if constexpr (kWin) {
+        tmem_ld32(tbase + lrow + C::kTmemS + 64 * h, *reinterpret_cast<uint32_t(*)[32]>(&Pp[0]));
+        tmem_ld32(tbase + lrow + C::kTmemS + 64 * h + 32, *reinterpret_cast<uint32_t(*)[32]>(&Pp[32]));
+        tmem_wait_ld();
+        uint32_t pb[32];
+#pragma unroll
+        for (int i = 0; i < 64; i += 2) {           // TMEM holds S^T - lse / qk_scale
+          const float2 x = mul_rn_f32x2(make_float2(__uint_as_float(Pp[i]), __uint_as_float(Pp[i + 1])),
+                                        make_float2(qk, qk));
+          Pp[i] = __float_as_uint(ex2f(x.x));
+          Pp[i + 1] = __float_as_uint(ex2f(x.y));
+        }
+        if (__any_sync(0xffffffffu, !key_ok) || diag || behind(blk, kb)) {
+          const unsigned long long seen = seen_by(qh, key, key_ok);
+#pragma unroll
+          for (int i = 0; i < 64; ++i)
+            if (!(seen >> i & 1)) Pp[i] = 0u;
+        }
+#pragma unroll
+        for (int i = 0; i < 64; i += 2) pb[i / 2] = pack_bf16x2(__uint_as_float(Pp[i]), __uint_as_float(Pp[i + 1]));
+        return store_pt(pb);
+      } else {
         uint32_t sr[64];
         tmem_ld32(tbase + lrow + C::kTmemS + 64 * h, *reinterpret_cast<uint32_t(*)[32]>(&sr[0]));
         tmem_ld32(tbase + lrow + C::kTmemS + 64 * h + 32,
@@ -538,16 +561,16 @@ __global__ void __launch_bounds__(384, 1)
         }
         // keys past Nkv (whole rows) and queries before the key on the causal diagonal
         // get P = 0; a separate pass, taken only by the few rows and blocks that need it
-        if (__any_sync(0xffffffffu, !key_ok) || diag || far) {
+        if (__any_sync(0xffffffffu, !key_ok) || diag) {
 #pragma unroll
           for (int i = 0; i < 32; ++i) {
-            const bool m0 = !key_ok || (diag && qh + 2 * i < key) || (far && qh + 2 * i > until);
-            const bool m1 = !key_ok || (diag && qh + 2 * i + 1 < key) || (far && qh + 2 * i + 1 > until);
+            const bool m0 = !key_ok || (diag && qh + 2 * i < key);
+            const bool m1 = !key_ok || (diag && qh + 2 * i + 1 < key);
             Pp[i] &= (m0 ? 0xffff0000u : 0xffffffffu) & (m1 ? 0x0000ffffu : 0xffffffffu);
           }
         }
+        return store_pt(Pp);
       }
-      return store_pt(Pp);
     };
     // quant_mode 2 (the page's backward, "attn_qat_train.py" _attn_bwd_dkdv): the dV MMA
     // consumes P^T quantized per (query, 64-key tile) with the forward's rule.  The 64
@@ -561,8 +584,6 @@ __global__ void __launch_bounds__(384, 1)
       if (!wwait(bar(B_S_FULL), c & 1)) return false;
       tc_fence_after();
       const bool diag = (kWin || p.a.causal) && blk == kb;
-      const bool far = behind(blk, kb);
-      const int until = kWin ? newest(key) : 0;
       const int qh = blk * kBlk + 64 * h;
       uint32_t pf[64];                                 // P^T of this row, fp32 bits
       tmem_ld32(tbase + lrow + C::kTmemS + 64 * h, *reinterpret_cast<uint32_t(*)[32]>(&pf[0]));
@@ -575,14 +596,21 @@ __global__ void __launch_bounds__(384, 1)
         pf[i] = __float_as_uint(ex2f(x.x));
         pf[i + 1] = __float_as_uint(ex2f(x.y));
       }
-      if (__any_sync(0xffffffffu, !key_ok) || diag || far) {
+      if (__any_sync(0xffffffffu, !key_ok) || diag || behind(blk, kb)) {
+        const unsigned long long seen = kWin ? seen_by(qh, key, key_ok) : 0ull;
 #pragma unroll
         for (int i = 0; i < 64; ++i)
-          if (!key_ok || (diag && qh + i < key) || (far && qh + i > until)) pf[i] = 0u;
+          if (kWin ? !(seen >> i & 1) : !key_ok || (diag && qh + i < key)) pf[i] = 0u;
       }
 #pragma unroll
-      for (int i = 0; i < 64; i += 2)
-        Pp[i / 2] = pack_bf16x2(__uint_as_float(pf[i]), __uint_as_float(pf[i + 1]));
+      for (int i = 0; i < 64; i += 2) {
+        if constexpr (kWin) {
+          Pp[i] = pf[i];
+          Pp[i + 1] = pf[i + 1];
+        } else {
+          Pp[i / 2] = pack_bf16x2(__uint_as_float(pf[i]), __uint_as_float(pf[i + 1]));
+        }
+      }
       // column maxima over this warp's 32 keys (non-negative floats order as their bits)
       uint32_t mine0 = 0u, mine1 = 0u;
 #pragma unroll
@@ -632,9 +660,10 @@ __global__ void __launch_bounds__(384, 1)
         uint32_t pk[16];
 #pragma unroll
         for (int i = 0; i < 32; i += 2) {           // TMEM holds dP^T - Delta
-          const uint32_t pa = Pp[16 * cc + i / 2];
+          const uint32_t pa = Pp[kWin ? 32 * cc + i : 16 * cc + i / 2];
           const float2 d = mul_rn_f32x2(
-              make_float2(__uint_as_float(pa << 16), __uint_as_float(pa & 0xffff0000u)),
+              kWin ? make_float2(__uint_as_float(pa), __uint_as_float(Pp[kWin ? 32 * cc + i + 1 : 0]))
+                   : make_float2(__uint_as_float(pa << 16), __uint_as_float(pa & 0xffff0000u)),
               make_float2(__uint_as_float(dr[i]), __uint_as_float(dr[i + 1])));
           pk[i / 2] = pack_bf16x2(d.x, d.y);
         }

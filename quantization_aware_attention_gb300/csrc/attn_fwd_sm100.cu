@@ -481,10 +481,12 @@ __global__ void __launch_bounds__(384, 1)
         if constexpr (kWin) {
           // the diagonal (and with it the end of the keys), and blocks where some row's window begins
           if (jb == mt || (jb * kBN < mt * kBM + kBM - p.a.window && jb * kBN + kBN > p.a.sinks)) {
-            const int lim = min(p.a.Nkv - 1, row), low = row - p.a.window;
+            const unsigned long long seen = window_seen(row, key0, p.a.window, p.a.sinks, p.a.Nkv);
+            if (__any_sync(0xffffffffu, seen != ~0ull)) {
 #pragma unroll
-            for (int i = 0; i < 64; ++i)
-              if (key0 + i > lim || (key0 + i <= low && key0 + i >= p.a.sinks)) s[i] = -INFINITY;
+              for (int i = 0; i < 64; ++i)
+                if (!(seen >> i & 1)) s[i] = -INFINITY;
+            }
           }
         } else if (jb * kBN + kBN > p.a.Nkv || (p.a.causal && jb == mt)) {
           const int lim = p.a.causal ? min(p.a.Nkv - 1, row) : p.a.Nkv - 1;
@@ -604,14 +606,15 @@ cudaError_t launch_fwd_tc_d(const FwdArgs& a, unsigned int* err, int num_sms, cu
   // a causal item streams its head's K and V blocks
   p.hgroup = causal_head_group(4ll * a.Nkv * D, BH);
   // Deferred epilogues for items of at most 8 key blocks (not for causal ones, whose lengths differ).  With windows
-  // up to 5, and throughout where O_q is all (B4 H32 N8192 D128, us deferred / not, with and without O_hp: W 512
-  // 512 / 521 and 413 / 440, W 896 734 / 709 and 596 / 625, W 1024 S 4 878 / 834 and 716 / 746).
+  // throughout, but where O_q is all up to 5 blocks (B4 H32 N8192 D128, us deferred / not, with and without O_hp: W 128
+  // S 4 350 / 381 and 293 / 306, W 512 470 / 504 and 399 / 410, W 896 664 / 707 and 589 / 583, W 1024 S 4 785 / 831
+  // and 706 / 692; B1 H8 N32768 W 4096 S 64 614 / 620 and 566 / 547).
   const bool win = a.window > 0;
   const long long blocks = win ? (a.window + 254ll) / kBN + (a.sinks + kBN - 1) / kBN : (a.Nkv + kBN - 1) / kBN;
-  const bool defer = win ? a.o_hp == nullptr || blocks <= 5 : !a.causal && blocks <= 8;
+  const bool defer = win ? blocks <= 5 : !a.causal && blocks <= 8;
   auto kern = defer ? attn_fwd_tc_kernel<D, true, false, true> : attn_fwd_tc_kernel<D, false, false, true>;
   if (win && a.o_hp != nullptr)
-    kern = defer ? attn_fwd_tc_kernel<D, true, true, true> : attn_fwd_tc_kernel<D, false, true, true>;
+    kern = attn_fwd_tc_kernel<D, true, true, true>;
   else if (win)
     kern = defer ? attn_fwd_tc_kernel<D, true, true, false> : attn_fwd_tc_kernel<D, false, true, false>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,

@@ -125,15 +125,6 @@ __device__ __forceinline__ bool at_edge(const DecodeArgs& a, const Cursor& c, in
          (a.window > 0 && at * kStep < c.len - a.window && (at + 1) * kStep > a.sinks);
 }
 
-// Ones in bits [from, to), both clamped to 0 .. 64.
-__device__ __forceinline__ unsigned long long ones(int from, int to) {
-  from = min(max(from, 0), 64);
-  to = min(max(to, 0), 64);
-  if (to <= from) return 0ull;
-  const unsigned long long upto = to == 64 ? ~0ull : (1ull << to) - 1;
-  return upto & ~((1ull << from) - 1);
-}
-
 // The keys of key0 .. key0 + 63 that a row does not see; mask: the tokens it sees; pos: its position.
 __device__ __forceinline__ unsigned long long hidden_keys(const DecodeArgs& a, int len, int key0, int pos,
                                                           unsigned long long mask) {
