@@ -199,8 +199,10 @@ __device__ __forceinline__ unsigned long long window_seen(int row, int key0, int
 // few, each is cut into this many pieces of query blocks, whose fp32 sums one more kernel adds in order.  (Every
 // CTA gets as many items as the others: with pieces of a quarter of an SM's share of the work, 8 heads of 32768
 // tokens with windows of 4096 and 64 sinks took 15 percent longer than without sinks, of which there are 3.)
-// A piece has about as many query blocks as another key block's windows, or a sixteenth of an SM's share of the
-// work if that is more; none is empty, and their sums take at most 1216 slots (160 MB at D 128).
+// A piece has about as many query blocks as another key block's windows, or a 32nd of an SM's share of the work if
+// that is more, but 10 blocks if a 16th of the share is (backward, us, with a 16th / this: B4 H32 N8192 D128 W1024 S4
+// 1870 / 1803, B1 H8 N131072 D64 W512 S4 1085 / 1040; with a 32nd alone B1 H8 N65536 D128 W512 S4 742 / 780).  None
+// is empty, and their sums take at most 1216 slots (160 MB at D 128).
 inline int window_sink_pieces(int B, int H, int N, int window, int sinks) {
   const double heads = static_cast<double>(B) * H;
   const int M = (N + 127) / 128, blocks = (sinks + 127) / 128;
@@ -208,7 +210,9 @@ inline int window_sink_pieces(int B, int H, int N, int window, int sinks) {
   const int each = (window + 254) / 128 < M ? (window + 254) / 128 : M;  // query blocks that see a key block
   if (heads * blocks >= 4 * 152) return 1;
   const double share = heads * (static_cast<double>(blocks) * M + static_cast<double>(M - blocks) * each) / 152.0;
-  const double piece = share / 16.0 < each ? each : share / 16.0;
+  double piece = share / 32.0;
+  if (piece < 10.0) piece = share / 16.0 < 10.0 ? share / 16.0 : 10.0;
+  if (piece < each) piece = each;
   int most = static_cast<int>(1216 / (heads * blocks));
   if (most > M - blocks + 1) most = M - blocks + 1;
   const int want = static_cast<int>(ceil(M / (piece < 4.0 ? 4.0 : piece)));
