@@ -421,6 +421,8 @@ QAT_API qat_status_t qat_attn_decode(const void* q, const void* k_codes, const v
  *   The work follows the pairs that are seen, in blocks of 128 x 128.  The sums of dK and dV of sinks may be cut
  *   into pieces, kept in the workspace and added in order; results are deterministic.
  *   Values of keys (queries) that share a 128-block with seen ones are multiplied by zero: they must be finite.
+ *   Rounded to bf16 on the way: P for O_hp and dV, quantized P for O_q, dS for dQ and dK (from fp32 P), each half a
+ *   step, 2^-8 relative; the outputs once more.
  * Errors: as qat_attn_fwd and qat_attn_bwd; QAT_ERR_INVALID_ARG also for window < 1 or sinks < 0,
  *   QAT_ERR_UNSUPPORTED for N > 2^30.
  */
@@ -456,8 +458,11 @@ QAT_API qat_status_t qat_attn_decode_window(const void* q, const void* k_codes, 
  *   T        1 .. 64 (0: nothing to do)
  *   window   0: none (then sinks is 0); else a key j before the tree also needs j > i - window or
  *            j < sinks, with i = seq_lens[b] - T + popcount(mask) - 1, the token's position by its depth; tokens
- *            of the tree are seen by their bits alone
- *   everything else as qat_attn_decode; workspace of qat_attn_tree_workspace_bytes(Hq, Hkv, T, D) bytes.
+ *            of the tree are seen by their bits alone.  Pages of keys before seq_lens[b] - T - window that hold no
+ *            sinks are not looked up
+ *   everything else as qat_attn_decode; workspace of qat_attn_tree_workspace_bytes(Hq, Hkv, T, D) bytes.  The weights
+ *   of V, P times the value's scale, are rounded to f16 as there for up to 32 query rows (Hq / Hkv x T) a KV head at
+ *   D 128, 64 at D 64, and to bf16, 2^-8 relative at most, for more.
  */
 QAT_API size_t qat_attn_tree_workspace_bytes(int Hq, int Hkv, int T, int D);
 QAT_API qat_status_t qat_attn_tree(const void* q, const void* k_codes, const void* v_codes, const float* k_scales,

@@ -97,7 +97,7 @@ def qat_attention_forward(q, k, v, causal: bool = False, sm_scale: float | None 
         else:
             st = capi.qat_attn_fwd(q, k, v, o_q, o_hp, lse, B, H, Nq, Nkv, D, sm_scale,
                                    int(causal), quant_mode)
-    _raise(st, "qat_attn_fwd")
+    _raise(st, "qat_attn_fwd" if win is None else "qat_attn_fwd_window")
     return o_q, o_hp, lse
 
 

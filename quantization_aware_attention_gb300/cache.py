@@ -85,7 +85,6 @@ class KVCache:
         return capi.torch_ops().kv_read(self._k, self._v, self._k_scale, self._v_scale, block_table,
                                         seq_lens, begin, length, check)
 
-
     def keep(self, block_table, seq_lens, drafted: int, path, path_lens, check: bool | None = None):
         """After the last ``drafted`` tokens of each sequence were checked: moves the accepted ones' rows behind
         the text before them.  ``path`` (int32 [B, L], L <= drafted <= 64) names drafted tokens in their order in
@@ -127,9 +126,11 @@ def qat_attention_tree(q, cache: KVCache, block_table, seq_lens, tree, sm_scale:
     ``tree`` (int64 [B, T], or [T] for all sequences; from ``qat_draft_tree``) says which of them each token sees:
     bit s of tree[b, t] for token s.  Every token sees the whole text before the tree; with ``window``, only keys
     j > i - window of it, and the first ``sinks``, i being the token's position by its depth, seq_lens[b] - T +
-    popcount - 1 (the tree itself is seen by its bits alone).  P's tiles are of 64 slots, so a drafted token's P may be
-    quantized in another tile than after ``KVCache.keep``.  Everything else as ``qat_attention_decode``; the workspace has ``capi.qat_attn_tree_workspace_bytes(Hq, cache.heads, T, D)``
-    bytes."""
+    popcount - 1 (the tree itself is seen by its bits alone).  P's tiles are of 64 slots, so a drafted token's P may
+    be quantized in another tile than after ``KVCache.keep``.  Where a KV head has more than 32 query rows (64 channels:
+    64) the weights of V are rounded to bf16, else to f16.  Everything else as ``qat_attention_decode``, but that with a
+    window the page of key seq_lens - T - window is looked up (a token with an empty mask sees it); the workspace has
+    ``capi.qat_attn_tree_workspace_bytes(Hq, cache.heads, T, D)`` bytes."""
     if not isinstance(cache, KVCache):
         raise TypeError("cache must be a KVCache")
     if not isinstance(tree, torch.Tensor):

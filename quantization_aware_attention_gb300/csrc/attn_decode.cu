@@ -48,6 +48,14 @@
 // With so few rows these products need a tenth of the tensor rate, and a 128-row tcgen05 tile would want the
 // codes of V transposed and P in 8 bits with a scale per key; the memory pipeline is what has to be fed.
 //
+// Windows (kWindow) and drafted trees of few rows (kTree) are instances of the same kernel: only keys that some row
+// sees are units, a sequence's sinks and then its windows' tiles (cache_split.cuh), so the work follows the window and
+// not the length; masks are looked at in the tiles that an edge of a window, the sequence's end or the tree lie in.
+//   64 sequences of 129 to 8192 keys, window 1024, 4 sinks, D 128, 32 / 8 heads   35 us; 132 MB are 20 us of HBM, the
+//                                                                                rest start, table and merge as above
+//   2 sequences of 250001 and 262144 keys, window 4096, 130 sinks, 40 / 8 heads   12.2 us, all of it latency
+//   a tree of 8 tokens over 1537 keys, 32 / 8 heads                               13.7 us: 16 items, each cut in many
+//
 // Operand layout: the order of d in Q K^T and of the output rows in V^T P^T is free, so each lane
 // (g = lane / 4, t = lane % 4) takes 16-byte runs of a row: for K chunk t + 4 h of keys g and g + 8
 // (k-step s of the run: bytes 4 s .. 4 s + 3), for V the g-th eighth of keys 2t, 2t + 1, 2t + 8, 2t + 9,

@@ -27,6 +27,12 @@
 //               the kDefer instance) after the next item's first block of P.
 // TMEM (512 columns): S0 [0,128), S1 [128,256), O_q [256,256+D), O_hp [256+D,256+2D).
 //
+// Sliding windows with sinks (causal; the kWin instances): an item takes the key blocks that its rows' windows and
+// the sinks lie in, from the diagonal down, so that each row sees a key in its first block; the blocks that an edge
+// crosses are masked by a row's 64 bits.  The executed products are whole 128 x 128 blocks: at N 8192, W 1024, S 4 ten
+// a row block for 1028 keys a row.  B4 H32 N8192 D128 W1024 S4 with O_hp 785 us (990 TFLOP/s of seen pairs), W4096 S64
+// at B1 H8 N32768 without 547 us (956); the softmax warps bound it as in the others.
+//
 // The running max is updated only when it grows by more than 8 (base-2 units), so P
 // may reach 2^8 and the O rescale is rare.  The FP8 code depends only on p / amax, so
 // this leaves the quantization unchanged in exact arithmetic (the max element of every

@@ -1,10 +1,43 @@
-// attn_tree_sm100.cu -- attention of many rows a KV head over the FP8 cache (a drafted tree, the tokens of a window)
-// on the Blackwell tensor core: tcgen05 products with the queries as the 128-row operand.
+// attn_tree_sm100.cu -- attention of a drafted tree over the FP8 cache where a KV head has many query rows, on the
+// Blackwell tensor core: tcgen05 products with the queries as the 128-row operand.  (Fewer rows: attn_decode.cu,
+// whose launch_decode has the rule and both sides' times.)
 //
 // Per query row (head, token) and key j that it sees:
 //   s_j = sm_scale <q, k_j>,  k_j = code_j scale_j;  p_j = exp(s_j - m);  l = sum p_j
 //   quantized: per absolute 64-key tile amax = max p, p'_j = E4M3(p_j 448 / amax) amax / 448
 //   o = sum p'_j v_j / l;  lse = log2 sum exp(s_j).  A row that sees no key: o = 0, lse = -inf.
+//
+// What bounds it.  A key and KV head is 2 (D + 4) bytes and 4 D flops for each of up to 128 rows: HBM would be read
+// in 47 us for 16 trees of 32 tokens over 2001 to 16384 keys (8 KV heads, 4 query heads each, D 128), the tensor
+// core done in 40.  The kernel takes 151: a step of 128 keys goes from warp to warp -- codes, K as an operand, S,
+// softmax, P, O -- and takes 2 us whatever D and the rows are.  With parts left out of a copy (8 trees of 128 rows
+// over 16384 keys, 126 us): without conversions 113, softmax 101, products 117, all three 79, loads too 61; so it is
+// hand-overs and their latencies, and each part's own time comes on top.  64 trees of 64 tokens of 129 to 4096 keys
+// (8 query heads each, four items a KV head): 605 us against 146 of products.
+//
+// An item is a sequence's KV head and 128 of its rows; the batch's 128-key steps are cut into equal ranges, one for a
+// CTA, and cut items added up as in cache_split.cuh.  512 threads:
+//   warp 0       producer: pages looked up for four steps at once, codes and scales by bulk copies of 16 keys (the
+//                keys that certainly share a page), three steps of codes ahead, six of scales (read by the softmax,
+//                which ends later); zeros in place of chunks that are not there
+//   warp 1       one lane issues S_n = Q K^T (SS) two steps ahead of O += P_n V (TS, P in TMEM over S_n's columns)
+//   warps 4-7    E4M3 codes to bf16, exact, in the swizzled layout that the products read
+//   warps 8-15   softmax and quantization: two groups that take steps in turn, each a row a thread with a maximum, a
+//                sum and an accumulator of its own, added up at the end of a range's part of an item.  (Both groups on
+//                one step, a 64-key tile each, wait for each other's maximum: 165 against 156 us, 667 against 655.)
+// TMEM (512 columns): S, then P, of even and odd steps [0,128), [128,256); their O [256,256+D), [256+D,256+2D).
+// Shared memory: Q, K and V as bf16 operands (32 KB each at D 128), three steps of codes (96 KB), scales.
+//
+// Roundings to fewer than 32 bits: q is exact (bf16 times a power of two); codes are exact in bf16; the weights,
+// p' times the value's scale, are rounded to bf16, 2^-8 relative at most, as TMEM operands of one type with V
+// (f16 would be 2^-11 but cannot hold V's scales' range without a power of two for each row and tile; K in f16 took
+// 150 against 132 us and lost keys near 2^-105); o is rounded to bf16 once.  448 / amax is an approximate reciprocal,
+// 2^-22 off as ex2 is.
+//
+// Built and not kept, us against the kernel of the time (8 trees of 128 rows, 16384 keys): sixteen softmax warps 128 ->
+// 131; K and V converted straight from global memory with loads ahead in registers 126 -> 137 to 165; V in two
+// buffers and K two steps ahead 128 -> 134; two issuing warps 126 -> 127 to 130; TMEM loads of the softmax 16 or 32
+// keys ahead 128 -> 136 to 186.
 #include "cache_split.cuh"
 #include "qat_internal.h"
 #include "qat_quant.cuh"
@@ -39,15 +72,16 @@ struct Tc {
   static constexpr uint32_t kOffSc = kOffRing + kStages * 2 * kCodes;  // scales: K, then V
   static constexpr uint32_t kOffBar = kOffSc + kScStages * 8 * kStep;
   static constexpr uint32_t kOffMisc = kOffBar + 320;
-  static constexpr uint32_t kOffX = kOffMisc + 64;                // the rows' largest |q|, m and l, [2 groups][128] each
+  static constexpr uint32_t kOffX = kOffMisc + 64;  // the rows' largest |q|, m and l, [2 groups][128] each
   static constexpr uint32_t kOffSum = kOffX + 3072;               // the warps' sums, then B + 1 prefix sums
   static constexpr uint32_t kUsed = kOffSum + 4 * (kThreads / 32);
-  static constexpr uint32_t kTmemO = 256;  // S, then P, of even and odd steps at 0 and 128; their sums at kTmemO, + D
+  static constexpr uint32_t kTmemO = 256;
 };
 
 enum : uint32_t {
   T_CODES = 0, T_CODES_FREE = T_CODES + kStages, T_SC = T_CODES_FREE + kStages, T_SC_FREE = T_SC + kScStages,
-  T_Q = T_SC_FREE + kScStages, T_Q_FREE, T_K, T_K_FREE, T_V, T_V_FREE, T_S, T_P = T_S + 2, T_O_LAST = T_P + 2, T_O_FREE, T_DRAIN, T_X, T_COUNT = T_X + 4
+  T_Q = T_SC_FREE + kScStages, T_Q_FREE, T_K, T_K_FREE, T_V, T_V_FREE, T_S, T_P = T_S + 2, T_O_LAST = T_P + 2,
+  T_O_FREE, T_DRAIN, T_X, T_COUNT = T_X + 4
 };
 static_assert(T_COUNT * 8 <= 320, "barrier block");
 
@@ -76,7 +110,10 @@ __device__ __forceinline__ void fence_async() { asm volatile("fence.proxy.async.
 
 __device__ __forceinline__ uint4 lds16(uint32_t a) {
   uint4 v;
-  asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a) : "memory");
+  asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "r"(a)
+               : "memory");
   return v;
 }
 __device__ __forceinline__ void sts16(uint32_t a, uint4 v) {
@@ -269,14 +306,16 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const Params p) {
           const int page = a.table[static_cast<long long>(c.b) * a.max_pages + (pos >> a.page_shift)];
           rows_of = kBadPage;
           if (page >= 0 && page < a.num_pages)
-            rows_of = ((static_cast<uint32_t>(page) * a.Hkv + c.h) << a.page_shift) + (pos & ((1 << a.page_shift) - 1));
+            rows_of = ((static_cast<uint32_t>(page) * a.Hkv + c.h) << a.page_shift) +
+                      (pos & ((1 << a.page_shift) - 1));
           else
             atomicOr(a.err, kErrBadPage);
         }
         fresh = false;
       }
       const uint32_t st = n % kStages, sc = n % kScStages;
-      if (!(ok = wwait(T_CODES_FREE + st, (n / kStages & 1) ^ 1) && wwait(T_SC_FREE + sc, (n / kScStages & 1) ^ 1))) break;
+      if (!(ok = wwait(T_CODES_FREE + st, (n / kStages & 1) ^ 1) && wwait(T_SC_FREE + sc, (n / kScStages & 1) ^ 1)))
+        break;
       const uint32_t rc = __shfl_sync(0xffffffffu, rows_of, (c.tile & 3) * 8 + (lane & 7));
       const uint32_t there = __ballot_sync(0xffffffffu, rc < kBadPage) & 0xffu;
       const uint32_t bad = __ballot_sync(0xffffffffu, rc == kBadPage) & 0xffu;
@@ -316,8 +355,10 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const Params p) {
       fresh = c.b != b || c.h != h;
     }
     // every copy lands before the CTA exits
-    for (uint32_t i = n > kStages ? n - kStages : 0; i < n; ++i) mbar_wait_drain(bar(T_CODES + i % kStages), i / kStages & 1, a.err);
-    for (uint32_t i = n > kScStages ? n - kScStages : 0; i < n; ++i) mbar_wait_drain(bar(T_SC + i % kScStages), i / kScStages & 1, a.err);
+    for (uint32_t i = n > kStages ? n - kStages : 0; i < n; ++i)
+      mbar_wait_drain(bar(T_CODES + i % kStages), i / kStages & 1, a.err);
+    for (uint32_t i = n > kScStages ? n - kScStages : 0; i < n; ++i)
+      mbar_wait_drain(bar(T_SC + i % kScStages), i / kScStages & 1, a.err);
   } else if (warp == 1) {
     // ------------------------------------------------------------ products
     if (elect_one()) {
@@ -515,8 +556,10 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const Params p) {
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
             const uint4 k = lds16(ks + 128 * q + 16 * i);
-            const float2 lo = mul_rn_f32x2(make_float2(s[4 * i], s[4 * i + 1]), make_float2(__uint_as_float(k.x), __uint_as_float(k.y)));
-            const float2 hi = mul_rn_f32x2(make_float2(s[4 * i + 2], s[4 * i + 3]), make_float2(__uint_as_float(k.z), __uint_as_float(k.w)));
+            const float2 lo = mul_rn_f32x2(make_float2(s[4 * i], s[4 * i + 1]),
+                                           make_float2(__uint_as_float(k.x), __uint_as_float(k.y)));
+            const float2 hi = mul_rn_f32x2(make_float2(s[4 * i + 2], s[4 * i + 3]),
+                                           make_float2(__uint_as_float(k.z), __uint_as_float(k.w)));
             s[4 * i] = lo.x; s[4 * i + 1] = lo.y; s[4 * i + 2] = hi.x; s[4 * i + 3] = hi.y;
           }
           if (edge) {
@@ -556,8 +599,8 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const Params p) {
         float inv0 = 0.f, back0 = 0.f, inv1 = 0.f, back1 = 0.f;
         if (kQuant) {
           const float a0 = ex2(fmaf(t0, rf, neg)), a1 = ex2(fmaf(t1, rf, neg));
-          // 448 / amax by the approximate reciprocal, off by 2^-22 as exp2 is (four divisions took 700 of the group's
-          // 7700 cycles a step)
+          // (four divisions in place of two approximate reciprocals and two products took 700 of a group's 7700 cycles
+          // a step)
           inv0 = a0 < kTinyP ? 0.f : kE4M3Max * rcp(a0);
           inv1 = a1 < kTinyP ? 0.f : kE4M3Max * rcp(a1);
           back0 = a0 < kTinyP ? 0.f : a0 * (1.f / kE4M3Max);

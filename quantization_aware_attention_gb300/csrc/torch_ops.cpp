@@ -530,7 +530,8 @@ struct WindowAttention : torch::autograd::Function<WindowAttention> {
 };
 
 Tensor window_attention(const Tensor& q, const Tensor& k, const Tensor& v, const WindowTensors& x,
-                        std::optional<double> sm_scale, int64_t quant_mode, int64_t window, int64_t sinks, std::optional<bool> check) {
+                        std::optional<double> sm_scale, int64_t quant_mode, int64_t window, int64_t sinks,
+                        std::optional<bool> check) {
   no_tangent("windowed attention", {&q, &k, &v});
   TORCH_CHECK_VALUE(quant_mode >= 0 && quant_mode <= 2, "quant_mode ", quant_mode);
   TORCH_CHECK_VALUE(window >= 1 && sinks >= 0, "window must be at least 1 and sinks at least 0, got ", window, " and ",
@@ -898,9 +899,10 @@ PyMethodDef method(const char* name) {
 
 PYBIND11_MODULE(_qat_torch, m) {
   m.def("norm_rope_bwd", &norm_rope_bwd);
-  static PyMethodDef methods[] = {method<py_norm_rope>("norm_rope"), method<py_window_attention>("window_attention"), method<py_kv_append>("kv_append"),
-                                  method<py_kv_read>("kv_read"), method<py_decode>("decode"),
-                                  method<py_draft_tree>("draft_tree"), method<py_kv_keep>("kv_keep"),
+  static PyMethodDef methods[] = {method<py_norm_rope>("norm_rope"), method<py_window_attention>("window_attention"),
+                                  method<py_kv_append>("kv_append"), method<py_kv_read>("kv_read"),
+                                  method<py_decode>("decode"), method<py_draft_tree>("draft_tree"),
+                                  method<py_kv_keep>("kv_keep"),
                                   {nullptr, nullptr, 0, nullptr}};
   if (PyModule_AddFunctions(m.ptr(), methods) != 0) throw py::error_already_set();
 }

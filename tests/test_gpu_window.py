@@ -279,7 +279,8 @@ def test_gradient_layouts():
 def test_offsets_beyond_32_bits():
     """Tensors of more than 2^31 elements: the last head's results are those of a call with that head alone."""
     H, N, D, window, sinks = 136, 131072, 128, 200, 4
-    x = torch.empty((1, H, N, D), dtype=torch.bfloat16, device="cuda").normal_(generator=torch.Generator("cuda").manual_seed(3))
+    x = torch.empty((1, H, N, D), dtype=torch.bfloat16, device="cuda")
+    x.normal_(generator=torch.Generator("cuda").manual_seed(3))
     how = dict(window=window, sinks=sinks)
     o_q, o_hp, lse = qat_attention_forward(x, x, x, True, **how)
     last = x[:, -1:].contiguous()
