@@ -50,7 +50,8 @@
 // blocks that hold sinks are seen by all later queries and are cut into pieces of those, whose fp32 sums
 // bwd_sink_sum_kernel adds in order.  dK/dV of B4 H32 N8192 D128 W1024: 916 us of about 9 query blocks an item, 2.0 us
 // a block against 1.6 in long items; the difference is an item's end (TMEM to global memory) and the refill behind
-// it.  (K and V of the next item loaded while the last block's dV and dK are still to come: no gain.)
+// it.  (Tried there: K and V of the next item loaded while the last block's dV and dK are still to come, no gain; the
+// next item's first P before an item's end, 4 percent slower alone and no gain with the other.)
 // TMEM (512 columns): S^T [0,128), dP^T [128,256), dV [256,256+D), dK [256+D,256+2D).
 // Shared memory: K, V (one tile each), Q and dO (2 stages each, 128-byte swizzle), the
 // ones tile and the lse_ext / d_ext rows (128 x 16 bf16, 32-byte swizzle).
