@@ -692,3 +692,32 @@ def test_expired_waits_of_the_wide_kernel():
         assert capi.qat_debug_set_wait_limit_us(4000000) == Status.OK
         capi.qat_attn_device_status()
     assert torch.equal(qat_attention_tree(*args, check=True), want)
+
+
+def test_nothing_to_do():
+    """No sequences, no tokens, no drafted tokens."""
+    cache = KVCache.empty(4, 2, 16, 64)
+    table, lens = _i32([[0, 1]]), _i32([20])
+
+    def q(B, T):
+        return torch.zeros((B, 4, T, 64), dtype=torch.bfloat16, device="cuda")
+
+    tree = torch.zeros((1, 3), dtype=torch.int64, device="cuda")
+    assert qat_attention_tree(q(1, 0), cache, table, lens, tree[:, :0]).shape == (1, 4, 0, 64)
+    for given in (tree[:0], tree[0]):
+        assert qat_attention_tree(q(0, 3), cache, table[:0], lens[:0], given).shape == (0, 4, 3, 64)
+    assert qat_attention_decode(q(1, 0), cache, table, lens, window=3).shape == (1, 4, 0, 64)
+    assert cache.keep(table[:0], lens[:0], 3, _i32([[0]])[:0], lens[:0]).shape == (0,)
+    assert cache.keep(table, lens, 0, _i32(np.zeros((1, 0))), _i32([0])).tolist() == [20]
+    check_device_status()
+
+
+def test_many_rows_of_one_head():
+    """64 query heads a KV head and 64 tokens: 4096 rows, 32 row tiles."""
+    lens, D, page, T, Hq = [150], 64, 16, 64, 64
+    cache, table, codes, scales = _cache(lens, 1, D, page, 6)
+    masks = _trees(np.random.default_rng(9), 1, T, "tree")
+    q = dev_bf16(normal_bf16(14, (1, Hq, T, D)))
+    o, lse = qat_attention_tree(q, cache, _i32(table), _i32(lens), _i64(masks), return_lse=True, check=True)
+    _compare(o, lse, q, lens, lambda b: do_.tree_seen(lens[b], masks[b]), cache, page, (table, codes, scales), 1,
+             _eps(Hq, 1, T, D))

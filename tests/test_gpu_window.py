@@ -324,3 +324,47 @@ def test_expired_waits():
         capi.qat_attn_device_status()
     got = _run(t, 700, 4)
     assert all(torch.equal(got[n], want[n]) for n in want)
+
+
+def test_one_tensor_three_times_and_none():
+    """q, k and v as one leaf: its gradient is the sum of the three; an empty batch; a single token."""
+    f, (q, k, v, do) = _inputs(20, 1, 2, 200, 64)
+    how = dict(causal=True, window=30, sinks=2)
+    x = q.clone().requires_grad_(True)
+    got = torch.autograd.grad(attention(x, x, x, **how), x, do)[0]
+    each = [q.clone().requires_grad_(True) for _ in range(3)]
+    parts = torch.autograd.grad(attention(*each, **how), each, do)
+    assert rel_l2(host_f64(got), sum(host_f64(p) for p in parts)) <= 2.0 ** -7  # two sums rounded to bf16
+    none = [x[:0].clone().requires_grad_(True) for x in (q, k, v)]
+    assert all(g.shape == (0, 2, 200, 64) for g in torch.autograd.grad(attention(*none, **how).sum(), none))
+    one = [x[:, :, :1].contiguous().requires_grad_(True) for x in (q, k, v)]
+    o = attention(*one, **how, check=True)
+    assert torch.equal(o, one[2]) and torch.equal(torch.autograd.grad(o, one[2:], do[:, :, :1])[0], do[:, :, :1])
+
+
+def test_threads_on_streams_of_their_own():
+    """Training passes of four host threads at once, each on its stream, give the same bits."""
+    import threading
+    _, t = _inputs(21, 2, 4, 700, 128)
+    out, errors = {}, []
+
+    def work(i):
+        try:
+            with torch.cuda.stream(torch.cuda.Stream()):
+                leaves = [x.clone().requires_grad_(True) for x in t[:3]]
+                for _ in range(5):
+                    o = attention(*leaves, causal=True, window=100, sinks=3)
+                    grads = torch.autograd.grad(o, leaves, t[3])
+                torch.cuda.current_stream().synchronize()
+                out[i] = (o,) + grads
+        except Exception as e:  # shown by the test, not by the thread
+            errors.append(e)
+
+    torch.cuda.synchronize()
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(4)]
+    for x in threads:
+        x.start()
+    for x in threads:
+        x.join()
+    assert not errors
+    assert all(torch.equal(a, b) for i in range(1, 4) for a, b in zip(out[0], out[i]))
