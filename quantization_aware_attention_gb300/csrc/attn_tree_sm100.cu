@@ -73,7 +73,7 @@ struct Tc {
   static constexpr uint32_t kOffBar = kOffSc + kScStages * 8 * kStep;
   static constexpr uint32_t kOffMisc = kOffBar + 320;
   static constexpr uint32_t kOffX = kOffMisc + 64;  // the rows' largest |q|, m and l, [2 groups][128] each
-  static constexpr uint32_t kOffSum = kOffX + 3072;               // the warps' sums, then B + 1 prefix sums
+  static constexpr uint32_t kOffSum = kOffX + 3 * 1024;               // the warps' sums, then B + 1 prefix sums
   static constexpr uint32_t kUsed = kOffSum + 4 * (kThreads / 32);
   static constexpr uint32_t kTmemO = 256;
 };
