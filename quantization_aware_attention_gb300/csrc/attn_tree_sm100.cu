@@ -10,8 +10,8 @@
 // What bounds it.  A key and KV head is 2 (D + 4) bytes and 4 D flops for each of up to 128 rows: HBM would be read
 // in 47 us for 16 trees of 32 tokens over 2001 to 16384 keys (8 KV heads, 4 query heads each, D 128), the tensor
 // core done in 40.  The kernel takes 151: a step of 128 keys goes from warp to warp -- codes, K as an operand, S,
-// softmax, P, O -- and takes 2 us whatever D and the rows are.  With parts left out of a copy (8 trees of 128 rows
-// over 16384 keys, 126 us): without conversions 113, softmax 101, products 117, all three 79, loads too 61; so it is
+// softmax, P, O -- and takes 2 us (1.7 at D 64) whatever the rows are.  With parts left out of a copy (8 trees of
+// 128 rows over 16384 keys, 126 us): without conversions 113, softmax 101, products 117, all three 79, loads too 61; so it is
 // hand-overs and their latencies, and each part's own time comes on top.  64 trees of 64 tokens of 129 to 4096 keys
 // (8 query heads each, four items a KV head): 605 us against 146 of products.
 //
@@ -35,11 +35,11 @@
 // 2^-22 off as ex2 is.
 //
 // Built and not kept, us against the kernel of the time (8 trees of 128 rows, 16384 keys): sixteen softmax warps 128 ->
-// 131; K and V converted straight from global memory with loads ahead in registers 126 -> 137 to 165; V in two
-// buffers and K two steps ahead 128 -> 134; K and V in two buffers each, codes in three half steps 126 -> 138; two
-// issuing warps 126 -> 127 to 130; TMEM loads of the softmax 16 or 32 keys ahead 128 -> 136 to 186.  Two row tiles
-// beside each other on every step, a group each, with K and V converted once for both: 0 to 10 percent faster for even
-// numbers of tiles, 9 to 20 slower for odd ones, and twice the workspace.
+// 131; K and V converted straight from global memory with loads ahead in registers 126 -> 137 to 165; V in two buffers
+// and K two steps ahead 128 -> 134; K and V in two buffers each, codes in three half steps 126 -> 138; scales multiplied
+// in twice in place of S written back 126 -> 129; two issuing warps 126 -> 127 to 130; TMEM loads of the softmax 16 or
+// 32 keys ahead 128 -> 136 to 186.  Two row tiles beside each other on every step, a group each, with K and V converted
+// once for both: 0 to 10 percent faster for even numbers of tiles, 9 to 20 slower for odd ones, and twice the workspace.
 #include "cache_split.cuh"
 #include "qat_internal.h"
 #include "qat_quant.cuh"
