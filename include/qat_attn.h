@@ -414,7 +414,9 @@ QAT_API qat_status_t qat_attn_decode(const void* q, const void* k_codes, const v
  *   N        queries and keys;  N <= 2^30
  *   window   >= 1; the query's own key counts, so 1 leaves it alone (and the sinks); N or more: no window
  *   sinks    >= 0, the first keys, which every later query goes on seeing
- *   o_hp     NULL where no backward will follow: O_q alone, by two products in place of three
+ *   o_hp     fp32 [B, H, N, D]; forward: NULL where no backward will follow: O_q alone, by two products in place of
+ *            three.  (Rows that see few keys have a small dS = P (dP - Delta), which Delta of a bf16 O_hp would blur.)
+ *            Backward, quant_mode 2: the forward's O_q, bf16
  *   k_mean   fp32 [D] or NULL, as in qat_attn_bwd_smooth_k
  *   everything else as in qat_attn_fwd and qat_attn_bwd with Nq = Nkv = N and causal 1.  Tiles of the
  *   quantization are the same absolute 64 keys; a tile's amax is that of the keys that the row sees.
@@ -422,13 +424,12 @@ QAT_API qat_status_t qat_attn_decode(const void* q, const void* k_codes, const v
  *   into pieces, kept in the workspace and added in order; results are deterministic.
  *   Values of keys (queries) that share a 128-block with seen ones are multiplied by zero: they must be finite.
  *   Rounded to bf16 on the way, half a step, 2^-8 relative at most: P for O_hp and dV, quantized P for O_q, dS (of
- *   fp32 P) for dQ and dK; O_hp, of which Delta is formed; the outputs.  With keys that share an offset of half
- *   their spread in each channel dQ is off by 3.0e-3 to 3.2e-3, dK 2.5e-3, dV 2.3e-3 (relative L2); 1.7e-3 of that is the
- *   rounding of the output alone.
+ *   fp32 P) for dQ and dK; the outputs.  With keys that share an offset of half their spread in each channel dQ is off
+ *   by 2.7e-3, dK 2.5e-3, dV 2.3e-3 (relative L2), of which 1.7e-3 is the rounding of the output alone.
  * Errors: as qat_attn_fwd and qat_attn_bwd; QAT_ERR_INVALID_ARG also for window < 1 or sinks < 0,
  *   QAT_ERR_UNSUPPORTED for N > 2^30.
  */
-QAT_API qat_status_t qat_attn_fwd_window(const void* q, const void* k, const void* v, void* o_q, void* o_hp,
+QAT_API qat_status_t qat_attn_fwd_window(const void* q, const void* k, const void* v, void* o_q, float* o_hp,
                                          float* lse, int B, int H, int N, int D, float sm_scale, int window,
                                          int sinks, int quant_mode, void* stream);
 QAT_API size_t qat_attn_bwd_window_workspace_bytes(int B, int H, int N, int D, int window, int sinks);

@@ -82,12 +82,12 @@ def qat_attention_forward(q, k, v, causal: bool = False, sm_scale: float | None 
                           quant_mode: int = capi.QUANT_P_FP8E4M3_ROW_TILE64, window: int | None = None,
                           sinks: int = 0):
     """Returns (o_q, o_hp, lse): bf16 [B,H,Nq,D], bf16 [B,H,Nq,D], fp32 [B,H,Nq] (base 2).  ``window`` and
-    ``sinks``: see ``attention``."""
+    ``sinks``: see ``attention``; with a window o_hp is fp32."""
     win = _window(causal, window, sinks)
     B, H, Nq, Nkv, D = _dims(q, k, v)
     sm_scale = 1.0 / math.sqrt(D) if sm_scale is None else float(sm_scale)
     o_q = torch.empty_like(q)
-    o_hp = torch.empty_like(q)
+    o_hp = torch.empty_like(q, dtype=torch.bfloat16 if win is None else torch.float32)
     lse = torch.empty((B, H, Nq), dtype=torch.float32, device=q.device)
     if win is not None and Nq != Nkv:
         raise ValueError(f"a window needs as many keys as queries, got {Nkv} and {Nq}")
@@ -110,10 +110,11 @@ def qat_attention_backward(q, k, v, o_hp, lse, do, causal: bool = False,
     """Returns (dq, dk, dv) of L = <dO, O_hp> (straight-through estimator; quant_mode 2:
     the page's backward, with the forward's O_q passed as ``o_hp``).  With ``k_mean``
     (fp32 [D], smooth_k's channel mean; k is the smoothed key) dQ gets the page's
-    SMOOTH_K term.  ``window`` and ``sinks`` as in the forward."""
+    SMOOTH_K term.  ``window`` and ``sinks`` as in the forward, whose fp32 o_hp they go with."""
     win = _window(causal, window, sinks)
     B, H, Nq, Nkv, D = _dims(q, k, v)
-    _check(o_hp, "o_hp", (B, H, Nq, D))
+    page = quant_mode == capi.QUANT_P_FP8E4M3_ROW_TILE64_PAGE_BWD
+    _check(o_hp, "o_hp", (B, H, Nq, D), torch.bfloat16 if win is None or page else torch.float32)
     _check(do, "do", (B, H, Nq, D))
     _check(lse, "lse", (B, H, Nq), torch.float32)
     if k_mean is not None:

@@ -769,7 +769,10 @@ __device__ __forceinline__ void bf16_split3(float x, uint16_t (&t)[3]) {
 // lse_ext / d_ext entries (-lse / qk_scale and -Delta as three bf16 terms; padding rows
 // get -1e30 and 0, so P = 0 there).  D / 8 lanes cover a row with 16-byte loads, so a
 // warp has 32 / (D / 8) rows in flight per pass.  Block 0 also writes the ones tile.
-template <int D>
+// kF32 (windows): O_hp as fp32.  Where a row sees few keys, P lies near 1 and dS = P (dP - Delta) is a small
+// difference, so that an O_hp rounded to bf16 is most of dQ's and dK's error: 5.2e-3 and 4.5e-3 relative for windows
+// of 1 key and a sink, 4.2e-3 and 3.7e-3 for 3 keys, against 2.7e-3 and 2.5e-3.
+template <int D, bool kF32>
 __global__ void __launch_bounds__(256) bwd_prep_kernel(BwdArgs a, int nq_pad) {
   if (blockIdx.x == 0)
     for (int i = threadIdx.x; i < 128 * 16; i += blockDim.x)
@@ -793,13 +796,25 @@ __global__ void __launch_bounds__(256) bwd_prep_kernel(BwdArgs a, int nq_pad) {
     const float lse = in ? a.lse[bh * a.Nq + q] : 0.f;
     if (in) {
       const long long src = (bh * a.Nq + q) * D + 8 * sub;
-      const uint4 ov = *reinterpret_cast<const uint4*>(a.o_hp + src);
+      float2 o[4];
+      if constexpr (kF32) {
+        const float4* from = reinterpret_cast<const float4*>(a.o_f32 + src);
+        const float4 x = from[0], y = from[1];
+        o[0] = make_float2(x.x, x.y);
+        o[1] = make_float2(x.z, x.w);
+        o[2] = make_float2(y.x, y.y);
+        o[3] = make_float2(y.z, y.w);
+      } else {
+        const uint4 ov = *reinterpret_cast<const uint4*>(a.o_hp + src);
+        const __nv_bfloat162* o2 = reinterpret_cast<const __nv_bfloat162*>(&ov);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) o[i] = __bfloat1622float2(o2[i]);
+      }
       const uint4 dv = *reinterpret_cast<const uint4*>(a.dO + src);
-      const __nv_bfloat162* o2 = reinterpret_cast<const __nv_bfloat162*>(&ov);
       const __nv_bfloat162* d2 = reinterpret_cast<const __nv_bfloat162*>(&dv);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const float2 of = __bfloat1622float2(o2[i]);
+        const float2 of = o[i];
         const float2 df = __bfloat1622float2(d2[i]);
         acc = fmaf(of.x, df.x, acc);
         acc = fmaf(of.y, df.y, acc);
@@ -928,7 +943,8 @@ cudaError_t launch_bwd_tc_d(const BwdArgs& a, unsigned int* err, int num_sms, cu
   constexpr long long kPrepRowsPerBlock = 8 * (256 / D);  // 8 warps of 32 / (D / 8) rows
   long long pblocks = (prow + kPrepRowsPerBlock - 1) / kPrepRowsPerBlock;
   if (pblocks > static_cast<long long>(num_sms) * 64) pblocks = static_cast<long long>(num_sms) * 64;
-  bwd_prep_kernel<D><<<static_cast<unsigned>(pblocks), 256, 0, s>>>(a, p.nq_pad);
+  const auto prep = a.o_f32 != nullptr ? bwd_prep_kernel<D, true> : bwd_prep_kernel<D, false>;
+  prep<<<static_cast<unsigned>(pblocks), 256, 0, s>>>(a, p.nq_pad);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
 

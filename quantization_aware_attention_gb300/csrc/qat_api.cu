@@ -138,6 +138,10 @@ qat_status_t fwd_impl(const void* q, const void* k, const void* v, void* o_q, vo
   a.kv_head_rows = Nkv;
   a.o_q_f32 = nullptr;
   a.o_hp_f32 = nullptr;
+  if (window > 0) {
+    a.o_hp_f32 = static_cast<float*>(o_hp);
+    a.o_hp = nullptr;
+  }
   unsigned int* err = nullptr;
   int num_sms = 0;
   cudaError_t e = qat::device_context(&err, &num_sms);
@@ -155,7 +159,7 @@ qat_status_t qat_attn_fwd(const void* q, const void* k, const void* v, void* o_q
   return fwd_impl(q, k, v, o_q, o_hp, lse, B, H, Nq, Nkv, D, sm_scale, causal, 0, 0, quant_mode, stream);
 }
 
-qat_status_t qat_attn_fwd_window(const void* q, const void* k, const void* v, void* o_q, void* o_hp, float* lse,
+qat_status_t qat_attn_fwd_window(const void* q, const void* k, const void* v, void* o_q, float* o_hp, float* lse,
                                  int B, int H, int N, int D, float sm_scale, int window, int sinks, int quant_mode,
                                  void* stream) {
   int w = 0, s = 0;
@@ -290,6 +294,11 @@ qat_status_t bwd_impl(const void* q, const void* k, const void* v, const void* o
   a.d_ext = reinterpret_cast<uint16_t*>(ws + wl.off_d_ext);
   a.ones = reinterpret_cast<uint16_t*>(ws + wl.off_ones);
   a.part = sk > 0 || need > base ? reinterpret_cast<float*>(ws + wl.off_part) : nullptr;
+  a.o_f32 = nullptr;
+  if (window > 0 && quant_mode != QAT_QUANT_P_FP8E4M3_ROW_TILE64_PAGE_BWD) {
+    a.o_f32 = static_cast<const float*>(o_hp);
+    a.o_hp = nullptr;
+  }
   a.window = window;
   a.sinks = sinks;
   a.sink_pieces = window > 0 ? qat::window_sink_pieces(B, H, Nq, window, sinks) : 1;

@@ -127,7 +127,7 @@ struct FwdArgs {
   int window, sinks;  // window > 0 (causal only): key j also needs j > i - window or j < sinks;
                       // both at most Nkv
   int kv_head_rows;  // rows between consecutive heads in K/V memory (Nkv unless a chunk)
-  float* o_q_f32;    // when set (with o_hp_f32), fp32 outputs replace the bf16 ones
+  float* o_q_f32;    // when set (with o_hp_f32), fp32 outputs replace the bf16 ones; windows: o_hp_f32 alone
   float* o_hp_f32;
 };
 
@@ -147,6 +147,7 @@ struct BwdArgs {
   uint16_t* lse_ext;  // bf16 [B, H, Nq_pad, 16] (see BwdWorkspace)
   uint16_t* d_ext;    // bf16 [B, H, Nq_pad, 16]
   uint16_t* ones;     // bf16 [128, 16]
+  const float* o_f32; // windows: O_hp, then o_hp is null (null: o_hp)
   float* part;        // dK/dV segment sums (BwdWorkspace::off_part) when sk_ctas > 0, or of the
                       // sinks' key blocks when sink_pieces > 1
   const float* k_mean;  // fp32 [D] or null: smooth_k's channel mean (dQ's SMOOTH_K term)

@@ -471,9 +471,9 @@ std::array<Tensor, 3> window_forward(const Tensor& q, const Tensor& k, const Ten
   const int64_t B = q.size(0), H = q.size(1), N = q.size(2), D = q.size(3);
   const c10::cuda::CUDAGuard guard(dev);
   std::array<Tensor, 3> out{new_tensor(q.sizes(), at::kBFloat16, dev), Tensor(), new_tensor({B, H, N}, at::kFloat, dev)};
-  if (hp) out[1] = new_tensor(q.sizes(), at::kBFloat16, dev);
+  if (hp) out[1] = new_tensor(q.sizes(), at::kFloat, dev);
   ok(qat_attn_fwd_window(q.const_data_ptr(), k.const_data_ptr(), v.const_data_ptr(), out[0].mutable_data_ptr(),
-                         hp ? out[1].mutable_data_ptr() : nullptr, out[2].mutable_data_ptr<float>(), static_cast<int>(B),
+                         hp ? out[1].mutable_data_ptr<float>() : nullptr, out[2].mutable_data_ptr<float>(), static_cast<int>(B),
                          static_cast<int>(H), static_cast<int>(N), static_cast<int>(D), static_cast<float>(a.sm_scale),
                          a.window, a.sinks, a.quant_mode, stream_of(dev)),
      "qat_attn_fwd_window");
@@ -486,9 +486,10 @@ std::array<Tensor, 3> window_forward(const Tensor& q, const Tensor& k, const Ten
 struct WindowAttention : torch::autograd::Function<WindowAttention> {
   static variable_list forward(AutogradContext* ctx, const Tensor& q, const Tensor& k, const Tensor& v,
                                const WindowTensors& x, const WindowArgs& a) {
-    const auto out = window_forward(x.by[0], x.by[1], x.by[2], a, true);
     // the page's backward variant forms Delta from O_q, the straight-through one from O_hp
-    const Tensor& o = a.quant_mode == QAT_QUANT_P_FP8E4M3_ROW_TILE64_PAGE_BWD ? out[0] : out[1];
+    const bool page = a.quant_mode == QAT_QUANT_P_FP8E4M3_ROW_TILE64_PAGE_BWD;
+    const auto out = window_forward(x.by[0], x.by[1], x.by[2], a, !page);
+    const Tensor& o = page ? out[0] : out[1];
     ctx->save_for_backward({x.back[0], x.back[1], x.back[2], o, out[2], x.k_mean});
     ctx->saved_data["sm_scale"] = a.sm_scale;
     ctx->saved_data["quant_mode"] = static_cast<int64_t>(a.quant_mode);
