@@ -30,8 +30,9 @@
 // Sliding windows with sinks (causal; the kWin instances): an item takes the key blocks that its rows' windows and
 // the sinks lie in, from the diagonal down, so that each row sees a key in its first block; the blocks that an edge
 // crosses are masked by a row's 64 bits.  The executed products are whole 128 x 128 blocks: at N 8192, W 1024, S 4 ten
-// a row block for 1028 keys a row.  B4 H32 N8192 D128 W1024 S4 with O_hp 785 us (990 TFLOP/s of seen pairs), W4096 S64
-// at B1 H8 N32768 without 547 us (956); the softmax warps bound it as in the others.
+// a row block for 1028 keys a row.  O_hp is stored as fp32, for the backward's Delta.  B4 H32 N8192 D128 W1024 S4 with
+// it 824 us (942 TFLOP/s of seen pairs; 785 with O_hp as bf16), W4096 S64 at B1 H8 N32768 without O_hp 547 us (956); the
+// softmax warps bound it as in the others.
 //
 // The running max is updated only when it grows by more than 8 (base-2 units), so P
 // may reach 2^8 and the O rescale is rare.  The FP8 code depends only on p / amax, so
@@ -613,8 +614,8 @@ cudaError_t launch_fwd_tc_d(const FwdArgs& a, unsigned int* err, int num_sms, cu
   // a causal item streams its head's K and V blocks
   p.hgroup = causal_head_group(4ll * a.Nkv * D, BH);
   // Deferred epilogues for items of at most 8 key blocks (not for causal ones, whose lengths differ).  With windows
-  // throughout, but where O_q is all up to 5 blocks (B4 H32 N8192 D128, us deferred / not, with and without O_hp: W 128
-  // S 4 350 / 381 and 293 / 306, W 512 470 / 504 and 399 / 410, W 896 664 / 707 and 589 / 583, W 1024 S 4 785 / 831
+  // throughout, but where O_q is all up to 5 blocks (B4 H32 N8192 D128, us deferred / not, with a bf16 O_hp and without:
+  // W 128 S 4 350 / 381 and 293 / 306, W 512 470 / 504 and 399 / 410, W 896 664 / 707 and 589 / 583, W 1024 S 4 785 / 831
   // and 706 / 692; B1 H8 N32768 W 4096 S 64 614 / 620 and 566 / 547).
   const bool win = a.window > 0;
   const long long blocks = win ? (a.window + 254ll) / kBN + (a.sinks + kBN - 1) / kBN : (a.Nkv + kBN - 1) / kBN;
