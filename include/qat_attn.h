@@ -339,7 +339,9 @@ QAT_API qat_status_t qat_qk_norm_rope_bwd(
  *   amax = max |x|; code = E4M3_RNE_SATFINITE(fl32(x fl32(448 / amax))); scale = fl32(amax / 448);
  *   value = code * scale.
  * A row whose amax is below 2^-110 is stored as zeros.  A row with a NaN or an infinity is stored
- * as codes 0 with scale NaN, and reads as NaN.
+ * as codes 0 with scale NaN, and reads as NaN.  Codes 0x7f and 0xff (NaN) are never stored; a cache filled
+ * otherwise may hold them: they read as NaN, and make NaN of the rows of attention that see such a key, of
+ * such a value's channel in these and possibly in other rows of its KV head.
  * A block table entry outside [0, num_pages) that a call needs, or a length above
  * max_pages * page_size, is reported by the next qat_attn_device_status as QAT_ERR_BAD_PAGE; no
  * memory outside the cache is touched.

@@ -21,7 +21,8 @@ class KVCache:
     ``block_table`` (int32 [B, pages per sequence]) and ``seq_lens`` (int32 [B]) place the
     sequences: position i of sequence b is slot i % page_size of page block_table[b, i // page_size].
     Entries outside the cache are never followed: such rows are dropped by ``append``, read as NaN,
-    and reported by ``check_device_status`` (or at once with check=True)."""
+    and reported by ``check_device_status`` (or at once with check=True).  ``append`` stores no NaN
+    codes; in a cache filled otherwise they count as NaN."""
 
     def __init__(self, k, v, k_scale, v_scale):
         if not isinstance(k, torch.Tensor) or not k.is_cuda:
