@@ -770,8 +770,7 @@ int partial_rows(int R) { return R >= kRows ? kRows : (R + 1) / 2 * 2; }
 }  // namespace
 
 size_t decode_workspace_bytes(int R, int D) {
-  return kPartsAt + static_cast<size_t>(kMaxCtas) * warps_of(D, R <= 8 ? 1 : 2) * 2 * partial_rows(R) * (D + 2) *
-                         sizeof(float);
+  return workspace_of(kMaxCtas * warps_of(D, R <= 8 ? 1 : 2), partial_rows(R), D);
 }
 
 cudaError_t launch_decode(const DecodeArgs& a, int D, int num_sms, cudaStream_t s) {
@@ -779,7 +778,7 @@ cudaError_t launch_decode(const DecodeArgs& a, int D, int num_sms, cudaStream_t 
   // or 64 (D 64) of those.  16 sequences of 8192 keys, 8 KV heads, us (items of 16 / tensor core):
   //   D 128   20 rows  94 / 118   32 rows  95 / 120   64 rows 175 / 123   128 rows 326 / 134   256 rows 629 / 244
   //   D 64    20 rows  61 / 108   32 rows  62 / 108   64 rows 111 / 110   128 rows 209 / 115   256 rows 403 / 212
-  if (a.tree != nullptr && a.Hq / a.Hkv * a.T > (D == 64 ? 64 : 32)) return launch_tree(a, D, num_sms, s);
+  if (a.tree != nullptr && tree_is_wide(a.Hq / a.Hkv * a.T, D)) return launch_tree(a, D, num_sms, s);
   Params p;
   p.a = a;
   p.R = a.Hq / a.Hkv * a.T;

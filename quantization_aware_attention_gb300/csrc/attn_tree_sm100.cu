@@ -760,7 +760,12 @@ cudaError_t run(Params p, int ctas, int most, cudaStream_t s) {
   return launch_merge<D>(p, most, ctas, s);
 }
 
+// Rows of a partial, even so that partials stay 16-byte aligned.
+int partial_rows(int R) { return R < kM ? (R + 1) / 2 * 2 : kM; }
+
 }  // namespace
+
+size_t tree_workspace_bytes(int R, int D) { return workspace_of(kMaxCtas, partial_rows(R), D); }
 
 cudaError_t launch_tree(const DecodeArgs& a, int D, int num_sms, cudaStream_t s) {
   Params p;
@@ -768,7 +773,7 @@ cudaError_t launch_tree(const DecodeArgs& a, int D, int num_sms, cudaStream_t s)
   p.R = a.Hq / a.Hkv * a.T;
   p.rows = kM;
   p.mtiles = (p.R + kM - 1) / kM;
-  p.prows = p.R < kM ? (p.R + 1) / 2 * 2 : kM;
+  p.prows = partial_rows(p.R);
   const long long cap = static_cast<long long>(a.max_pages) << a.page_shift;
   const long long units = static_cast<long long>(a.B) * a.Hkv * p.mtiles * ((cap + kStep - 1) / kStep);
   int ctas = num_sms < kMaxCtas ? num_sms : kMaxCtas;

@@ -42,6 +42,10 @@ struct Chain {
 };
 constexpr size_t kPartsAt = sizeof(Header) + kWorkers * sizeof(Chain);
 static_assert(kPartsAt % 16 == 0, "partials are read 16 bytes at a time");
+// of a kernel's workspace: what partial_of gives each worker, behind the rest
+constexpr size_t workspace_of(int workers, int prows, int D) {
+  return kPartsAt + static_cast<size_t>(workers) * 2 * prows * (D + 2) * sizeof(float);
+}
 
 struct Params {
   DecodeArgs a;

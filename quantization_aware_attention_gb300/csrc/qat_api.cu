@@ -700,7 +700,11 @@ namespace {
 size_t over_cache_workspace(int Hq, int Hkv, int T, int D, int most) {
   if ((D != 64 && D != 128) || Hkv < 1 || Hq < 1 || Hq % Hkv != 0 || T < 0 || T > most) return 0;
   const long long R = static_cast<long long>(Hq / Hkv) * T;
-  return qat::decode_workspace_bytes(static_cast<int>(R < 16 ? R : 16), D);
+  const size_t few = qat::decode_workspace_bytes(static_cast<int>(R < 16 ? R : 16), D);
+  if (most != qat::kTreeMaxTokens || !qat::tree_is_wide(R, D)) return few;
+  // what holds a tree's partials holds a smaller tree's too
+  const size_t many = qat::tree_workspace_bytes(static_cast<int>(R < kMaxRows ? R : kMaxRows), D);
+  return few > many ? few : many;
 }
 
 // The attention of new tokens over the cache, `most` of them: decoding, with a window (0: none), or of a tree.

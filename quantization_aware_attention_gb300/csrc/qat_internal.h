@@ -337,7 +337,10 @@ struct KvKeepArgs {
 };
 constexpr int kDecodeMaxBatch = 4096;  // the kernel keeps the batch's prefix sums in shared memory
 constexpr int kDecodeMaxTokens = 16;
-size_t decode_workspace_bytes(int R, int D);  // R = Hq / Hkv * T
+size_t decode_workspace_bytes(int R, int D);  // R = Hq / Hkv * T, at most 16 of them
+// A tree of R = Hq / Hkv * T rows is the tensor core's (attn_tree_sm100.cu) and not decode_kernel's: see launch_decode.
+inline bool tree_is_wide(long long R, int D) { return R > (D == 64 ? 64 : 32); }
+size_t tree_workspace_bytes(int R, int D);    // of the tensor core's kernel
 
 #ifdef __CUDACC__
 // Launches a kernel that may be brought up while the stream's previous kernel still runs: it begins with

@@ -128,6 +128,20 @@ def test_tree_workspace():
     assert capi.qat_attn_decode_workspace_bytes(4, 2, 17, 64) == 0
 
 
+def test_tree_workspace_holds_both_kernels_partials():
+    """Two partials of a row tile, fp32 sums, maximum and sum a row, for each of 152 blocks of the tensor core's kernel
+    (more than 32 rows a KV head at D 128, 64 at D 64); from 16 rows on a larger tree's workspace does for a smaller."""
+    for D, rows in ((128, 32), (64, 64)):
+        for T in (9, 16, 17, 33, 64):
+            for G in (1, 2, 5, 8, 64):
+                R, f = G * T, capi.qat_attn_tree_workspace_bytes
+                if R > rows:
+                    assert f(G, 1, T, D) >= 152 * 2 * min(R, 128) * (D + 2) * 4
+                assert f(2 * G, 2, T, D) == f(G, 1, T, D)
+                if G * (T - 1) >= 16:
+                    assert f(G, 1, T, D) >= f(G, 1, T - 1, D)
+
+
 DRAFT = dict(parents=A, parents_stride=0, seq_lens=A, tree=A, positions=A, B=2, T=4, stream=0)
 
 
