@@ -8,6 +8,8 @@ import torch
 from oracle import drafted_oracle as do_
 from quantization_aware_attention_gb300 import check_device_status, qat_attention_tree
 from quantization_aware_attention_gb300 import build as qbuild
+from quantization_aware_attention_gb300 import capi
+from quantization_aware_attention_gb300.capi import Status
 from quantization_aware_attention_gb300.inputs import normal_bf16
 
 from gpu_util import dev_bf16
@@ -53,3 +55,56 @@ def test_codes_that_are_not_a_number(Hq, T, D, quant):
             assert torch.equal(o[..., others], clean[..., others]) and torch.equal(lse, clean_lse)
     assert torch.equal(qat_attention_tree(*args)[0], clean)
     check_device_status()
+
+
+SHAPES = [(4, 2, 3, 128), (6, 1, 7, 64), (4, 1, 40, 128), (6, 2, 30, 64)]  # 6 and 42 rows, 160 and 90
+
+
+def _masks(rng, B, T):
+    """Trees whose first token's mask is empty, as padding's is."""
+    out = [do_.draft([int(rng.integers(max(-1, t - 8), t)) for t in range(T)], T)[0] for _ in range(B)]
+    for m in out:
+        m[0] = 0
+    return out
+
+
+@pytest.mark.parametrize("window,sinks", [(1, 0), (5, 3), (64, 64), (70, 17), (200, 130)])
+@pytest.mark.parametrize("page", [16, 128])
+@pytest.mark.parametrize("Hq,Hkv,T,D", SHAPES)
+def test_pages_that_no_token_sees(Hq, Hkv, T, D, page, window, sinks):
+    """Pages of keys before seq_lens - T - window that hold no sinks may be anything in the block table."""
+    lens = [1500, 700, 130, 20, 2]
+    masks = _masks(np.random.default_rng(T), len(lens), T)
+    cache, table, _, _ = _cache(lens, Hkv, D, page, 21)
+    given, gone = table.copy(), 0
+    for b, n in enumerate(lens):
+        for p in range(table.shape[1]):
+            if (p + 1) * page <= n - T - window and p * page >= sinks:
+                given[b, p] = -1 if p % 2 else 1 << 30
+                gone += 1
+    assert gone > 0
+    q = dev_bf16(normal_bf16(41, (len(lens), Hq, T, D)))
+    how = dict(return_lse=True, check=True, window=window, sinks=sinks)
+    want = qat_attention_tree(q, cache, _i32(table), _i32(lens), _i64(masks), **how)
+    got = qat_attention_tree(q, cache, _i32(given), _i32(lens), _i64(masks), **how)
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
+@pytest.mark.parametrize("page,sinks", [(16, 0), (32, 33), (256, 1)])
+@pytest.mark.parametrize("Hq,Hkv,T,D", SHAPES)
+def test_a_page_that_begins_with_the_first_key_seen(Hq, Hkv, T, D, page, sinks):
+    """Key seq_lens - T - window begins a page: a token with an empty mask sees it, and none the page before."""
+    window = 2 * page - T % 5
+    lens = [3 * page + window + T]
+    masks = _masks(np.random.default_rng(T), 1, T)
+    cache, table, _, _ = _cache(lens, Hkv, D, page, 9)
+    q = dev_bf16(normal_bf16(13, (1, Hq, T, D)))
+    how = dict(window=window, sinks=sinks)
+    want = qat_attention_tree(q, cache, _i32(table), _i32(lens), _i64(masks), check=True, **how)
+    given = table.copy()
+    given[0, 2] = -1
+    assert torch.equal(qat_attention_tree(q, cache, _i32(given), _i32(lens), _i64(masks), check=True, **how), want)
+    given[0, 3] = 1 << 30
+    got = qat_attention_tree(q, cache, _i32(given), _i32(lens), _i64(masks), **how)
+    assert capi.qat_attn_device_status() == Status.BAD_PAGE
+    assert torch.isnan(got[:, :, 0]).all()
