@@ -463,8 +463,8 @@ QAT_API qat_status_t qat_attn_decode_window(const void* q, const void* k_codes, 
  *   T        1 .. 64 (0: nothing to do)
  *   window   0: none (then sinks is 0); else a key j before the tree also needs j > i - window or
  *            j < sinks, with i = seq_lens[b] - T + popcount(mask) - 1, the token's position by its depth; tokens
- *            of the tree are seen by their bits alone.  Pages of keys before seq_lens[b] - T - window that hold no
- *            sinks are not looked up
+ *            of the tree are seen by their bits alone, also where a path is longer than the window.  Pages of keys
+ *            before seq_lens[b] - T - window that hold no sinks are not looked up
  *   everything else as qat_attn_decode; workspace of qat_attn_tree_workspace_bytes(Hq, Hkv, T, D) bytes.  The weights
  *   of V, P times the value's scale, are rounded to f16 as there for up to 32 query rows (Hq / Hkv x T) a KV head at
  *   D 128, 64 at D 64, and to bf16, 2^-8 relative at most, for more.

@@ -256,7 +256,8 @@ def attention(q, k, v, causal: bool = False, sm_scale: float | None = None,
     call cut short is never consumed silently.
     window (causal only): query i sees key j if j <= i and (j > i - window or j < sinks), a
     sliding window beside which the first ``sinks`` keys stay visible; forward and backward
-    take work in proportion to what is seen.  The same in all but what is seen, but that
+    take work in proportion to what is seen; the backward is saved an fp32 O_hp, 2 bytes an element of q
+    more than without a window.  The same in all but what is seen, but that
     without gradients O_hp is not computed, that second and forward-mode derivatives are
     refused, and that a backward is refused under capture while a graph made on the default
     stream lives that ends in the same leaves or that it passes through."""

@@ -127,7 +127,8 @@ def qat_attention_tree(q, cache: KVCache, block_table, seq_lens, tree, sm_scale:
     ``tree`` (int64 [B, T], or [T] for all sequences; from ``qat_draft_tree``) says which of them each token sees:
     bit s of tree[b, t] for token s.  Every token sees the whole text before the tree; with ``window``, only keys
     j > i - window of it, and the first ``sinks``, i being the token's position by its depth, seq_lens[b] - T +
-    popcount - 1 (the tree itself is seen by its bits alone).  P's tiles are of 64 slots, so a drafted token's P may
+    popcount - 1 (the tree itself is seen by its bits alone, so where a path is longer than the window its tokens see
+    ancestors that ``qat_attention_decode`` would leave out).  P's tiles are of 64 slots, so a drafted token's P may
     be quantized in another tile than after ``KVCache.keep``.  Where a KV head has more than 32 query rows (64 channels:
     64) the weights of V are rounded to bf16, else to f16.  Everything else as ``qat_attention_decode``, but that with a
     window the page of key seq_lens - T - window is looked up (a token with an empty mask sees it); the workspace has

@@ -774,10 +774,21 @@ size_t decode_workspace_bytes(int R, int D) {
 }
 
 cudaError_t launch_decode(const DecodeArgs& a, int D, int num_sms, cudaStream_t s) {
-  // A tree's rows: items of 16 read the cache once each, the tensor core's 128 rows take the time of about 40 (D 128)
-  // or 64 (D 64) of those.  16 sequences of 8192 keys, 8 KV heads, us (items of 16 / tensor core):
-  //   D 128   20 rows  94 / 118   32 rows  95 / 120   64 rows 175 / 123   128 rows 326 / 134   256 rows 629 / 244
-  //   D 64    20 rows  61 / 108   32 rows  62 / 108   64 rows 111 / 110   128 rows 209 / 115   256 rows 403 / 212
+  // A tree's rows: items of 16 read and convert the cache's tiles once each, the tensor core's 128 rows take the time of
+  // about 40 (D 128) or 56 (D 64) of those.  8 KV heads, us (items of 16 / tensor core):
+  //   keys           D    20 rows    32 rows    36 rows    48 rows    56 rows    64 rows    128 rows   256 rows
+  //   16 x 8192      128  96 / 119   98 / 120   134 / 121  136 / 122  176 / 123  177 / 124  330 / 135  639 / 243
+  //   64 x 2048      128  104 / 129  107 / 130  151 / 131  154 / 132  193 / 134  195 / 136  359 / 150  686 / 267
+  //   2 x 100000     128  132 / 173  132 / 173  194 / 173  197 / 173  250 / 174  250 / 174  482 / 179  947 / 332
+  //   1 x 1537       128  14.1/13.4  14.4/13.3  14.7/13.5  14.7/13.6  15.8/14.1  15.9/14.2  24.8/17.4  27.4/21.3
+  //   window 1024    128  36.7/33.8  37.5/35.1  47.3/35.8  48.0/36.9  58.8/37.8  59.2/39.1  98.5/48.4  177/71.2
+  //   16 x 8192      64   64 / 110   65 / 110   89 / 110   89 / 111   113 / 112  114 / 112  212 / 117  408 / 215
+  //   64 x 2048      64   70 / 116   72 / 116   99 / 117   101 / 118  128 / 118  130 / 119  231 / 125  434 / 226
+  //   2 x 100000     64   87 / 160   88 / 160   124 / 160  125 / 160  160 / 160  160 / 160  302 / 161  588 / 305
+  //   1 x 1537       64   13.0/12.4  13.1/12.5  13.3/12.6  13.4/12.8  14.2/13.0  14.1/13.1  17.2/14.3  21.5/17.6
+  //   window 1024    64   31.2/30.6  31.3/30.9  34.1/31.0  34.6/32.3  43.4/32.8  43.2/33.2  66.3/37.9  115/56.2
+  // (The windows: 4 sinks, 16 x 8192.)  Up to there the weights of V are f16, behind it bf16; 49 to 64 rows of 64 channels
+  // pay for that with 9 percent on many short contexts and with 10 us of 43 with a window.
   if (a.tree != nullptr && tree_is_wide(a.Hq / a.Hkv * a.T, D)) return launch_tree(a, D, num_sms, s);
   Params p;
   p.a = a;

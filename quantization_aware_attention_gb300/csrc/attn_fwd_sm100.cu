@@ -622,7 +622,10 @@ cudaError_t launch_fwd_tc_d(const FwdArgs& a, unsigned int* err, int num_sms, cu
   // Of the few keys that a row sees one often carries nearly all weight: its P is exactly 1, and O_hp the nearer to
   // its value, where the maximum is always the row's own.  dQ's and dK's relative errors with the maximum raised at 8 / at
   // once: window 1 and 1 sink 3.8e-3, 3.6e-3 / 2.6e-3, 2.5e-3, 2 and 1 3.2e-3, 2.9e-3 / 2.7e-3, 2.4e-3; 100 and 5
-  // 2.7e-3, 2.4e-3 / the same.  B4 H32 N8192 D128 forward 309 / 315 us for windows of 16, 833 / 964 of 1024.
+  // 2.7e-3, 2.4e-3 / the same.  From 8 keys on (8, 16, 24, 32, 33, 48, 64 measured) 2.6e-3 to 2.7e-3 and 2.4e-3 either
+  // way; a window of 1 with 40 sinks, in another block, 2.8e-3, 2.5e-3 / 2.6e-3, 2.4e-3.  The first rows of a long window
+  // also see few keys, but in one block: their maximum is their own from the start.  B4 H32 N8192 D128 forward 309 / 315 us
+  // for windows of 16, 833 / 964 of 1024.
   p.raise = win && static_cast<long long>(a.window) + a.sinks <= 32 ? 0.f : kRescaleThreshold;
   const bool defer = win ? blocks <= 5 : !a.causal && blocks <= 8;
   auto kern = defer ? attn_fwd_tc_kernel<D, true, false, true> : attn_fwd_tc_kernel<D, false, false, true>;

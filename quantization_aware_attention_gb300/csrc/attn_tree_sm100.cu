@@ -9,11 +9,12 @@
 //
 // What bounds it.  A key and KV head is 2 (D + 4) bytes and 4 D flops for each of up to 128 rows: HBM would be read
 // in 47 us for 16 trees of 32 tokens over 2001 to 16384 keys (8 KV heads, 4 query heads each, D 128), the tensor
-// core done in 40.  The kernel takes 151: a step of 128 keys goes from warp to warp -- codes, K as an operand, S,
+// core done in 40.  The kernel takes 153: a step of 128 keys goes from warp to warp -- codes, K as an operand, S,
 // softmax, P, O -- and takes 2 us (1.7 at D 64) whatever the rows are.  With parts left out of a copy (8 trees of
-// 128 rows over 16384 keys, 126 us): without conversions 113, softmax 101, products 117, all three 79, loads too 61;
+// 128 rows over 16384 keys, then 126 us): without conversions 113, softmax 101, products 117, all three 79, loads too 61;
 // so it is hand-overs and their latencies, and each part's own time comes on top.  64 trees of 64 tokens of 129 to
-// 4096 keys (8 query heads each, four items a KV head): 605 to 640 us against 146 of products.
+// 4096 keys (8 query heads each, four items a KV head): 625 to 645 us against 146 of products; with 64 channels 498
+// against 73.
 //
 // An item is a sequence's KV head and 128 of its rows; the batch's 128-key steps are cut into equal ranges, one for a
 // CTA, and cut items added up as in cache_split.cuh.  512 threads:
