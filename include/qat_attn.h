@@ -340,8 +340,9 @@ QAT_API qat_status_t qat_qk_norm_rope_bwd(
  *   value = code * scale.
  * A row whose amax is below 2^-110 is stored as zeros.  A row with a NaN or an infinity is stored
  * as codes 0 with scale NaN, and reads as NaN.  Codes 0x7f and 0xff (NaN) are never stored; a cache filled
- * otherwise may hold them: they read as NaN, and make NaN of the rows of attention that see such a key, of
- * such a value's channel in these and possibly in other rows of its KV head.
+ * otherwise may hold them: they read as NaN, a row of attention that sees such a key is NaN, and one that sees
+ * such a value is NaN in its channel.  (In qat_attn_decode, and for trees of up to 32 query rows a KV head, 64 at
+ * D 64, so may other rows of that head be.)
  * A block table entry outside [0, num_pages) that a call needs, or a length above
  * max_pages * page_size, is reported by the next qat_attn_device_status as QAT_ERR_BAD_PAGE; no
  * memory outside the cache is touched.

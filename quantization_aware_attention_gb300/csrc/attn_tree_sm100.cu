@@ -9,7 +9,7 @@
 //
 // What bounds it.  A key and KV head is 2 (D + 4) bytes and 4 D flops for each of up to 128 rows: HBM would be read
 // in 47 us for 16 trees of 32 tokens over 2001 to 16384 keys (8 KV heads, 4 query heads each, D 128), the tensor
-// core done in 40.  The kernel takes 153: a step of 128 keys goes from warp to warp -- codes, K as an operand, S,
+// core done in 40.  The kernel takes 154: a step of 128 keys goes from warp to warp -- codes, K as an operand, S,
 // softmax, P, O -- and takes 2 us (1.7 at D 64) whatever the rows are.  With parts left out of a copy (8 trees of
 // 128 rows over 16384 keys, then 126 us): without conversions 113, softmax 101, products 117, all three 79, loads too 61;
 // so it is hand-overs and their latencies, and each part's own time comes on top.  64 trees of 64 tokens of 129 to
@@ -186,8 +186,68 @@ __device__ __forceinline__ unsigned long long hidden_keys(const DecodeArgs& a, i
   return ~seen;
 }
 
+// Of 16 codes that lane t of the converters' 128 takes i-th: their row, where they are and where the first eight go (the
+// others 16 bytes across).
+struct Piece {
+  int row;
+  uint32_t from, to;
+};
+template <int D>
+__device__ __forceinline__ Piece piece_at(int t, uint32_t ring, uint32_t out, int i) {
+  const int g = t >> 2, half = D == 64 ? 0 : (g & 1) ^ (i & 1), row = D == 64 ? g + 32 * i : g + 32 * (i >> 1);
+  return Piece{row, ring + row * D + 16 * ((t & 3) + 4 * half),
+               out + half * Tc<D>::kChunkBytes + row * 128 + (((2 * t & 6) ^ (row & 7)) << 4)};
+}
+// NaN operands where lane t's codes are NaN.  (Not inlined, as what follows: the kernel's warps share the instruction cache.)
+template <int D>
+__device__ __noinline__ void put_nan(int t, uint32_t ring, uint32_t out, int left) {
+#pragma unroll 1
+  for (int k = 0; k < D / 16 * kStep / 8; ++k) {
+    const Piece piece = piece_at<D>(t, ring, out, k >> 4);
+    const uint4 x = lds16(piece.from);
+    const uint32_t w = (k & 8) ? ((k & 4) ? x.w : x.z) : ((k & 4) ? x.y : x.x);
+    if (piece.row < left && (w >> 8 * (k & 3) & 0x7fu) == 0x7fu) sts2((piece.to ^ (2 * k & 16)) + 2 * (k & 7), 0x7fc0);
+  }
+}
+
+// The channels D / 2 h .. D / 2 (h + 1) - 1 in which a value that the row sees has a NaN code, as bits: in `count` steps
+// from `tile` on of sequence and KV head `seq`, read once more (where there are such codes at all: append stores none, but
+// a cache may have been filled otherwise).
+template <int D>
+__device__ __noinline__ unsigned long long nan_channels(const Params& p, const int* prefix, int seq, int row, int tile,
+                                                           int count, int h) {
+  const DecodeArgs& a = p.a;
+  Cursor c;
+  c.b = seq / a.Hkv;
+  c.h = seq - c.b * a.Hkv;
+  enter_seq<kTree, kStep>(p, prefix, c);
+  const unsigned long long mask = mask_of(a, c.b, row % a.T);
+  const int pos = c.len - a.T + __popcll(mask) - 1;
+  unsigned long long nan = 0ull;
+#pragma unroll 1
+  for (int i = 0; i < 2 * count; ++i) {
+    const int key0 = place_of<kTree>(c, tile + (i >> 1)) * kStep + 64 * (i & 1);
+    unsigned long long seen = ~hidden_keys(a, c.len, key0, pos, mask);
+    while (seen != 0ull) {
+      const int key = key0 + __ffsll(seen) - 1;
+      seen &= seen - 1;
+      const int page = a.table[static_cast<long long>(c.b) * a.max_pages + (key >> a.page_shift)];
+      if (page < 0 || page >= a.num_pages) continue;
+      const uint32_t at = ((static_cast<uint32_t>(page) * a.Hkv + c.h) << a.page_shift) + (key & ((1 << a.page_shift) - 1));
+      const uint32_t* codes = reinterpret_cast<const uint32_t*>(a.v_codes + static_cast<size_t>(at) * D + D / 2 * h);
+#pragma unroll 1
+      for (int w = 0; w < D / 8; ++w) {
+        const uint32_t x = codes[w];
+        if (nan_codes(x) & 0x80808080u)
+          for (int y = 0; y < 4; ++y) nan |= static_cast<unsigned long long>((x >> 8 * y & 0x7fu) == 0x7fu) << (4 * w + y);
+      }
+    }
+  }
+  return nan;
+}
+
 template <int D, bool kQuant>
-__global__ void __launch_bounds__(kThreads, 1) tree_kernel(const Params p) {
+__global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant__ Params p) {
   using C = Tc<D>;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = smem_addr(smem_raw), base = (raw + 1023u) & ~1023u;
@@ -195,6 +255,8 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const Params p) {
   const uint32_t bars = base + C::kOffBar;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(gbase + C::kOffMisc);
   volatile WaitCtl* ctl = reinterpret_cast<volatile WaitCtl*>(gbase + C::kOffMisc + 8);
+  // up to the last step with NaN codes in V
+  volatile uint32_t* nan_steps = reinterpret_cast<volatile uint32_t*>(gbase + C::kOffMisc + 60);
   int* warp_sum = reinterpret_cast<int*>(gbase + C::kOffSum);
   int* prefix = warp_sum + kThreads / 32;
   const auto bar = [&](uint32_t i) { return bars + 8u * i; };
@@ -203,6 +265,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const Params p) {
 
   if (tid == 0) {
     wait_ctl_init(ctl, a.err);
+    *nan_steps = 0u;
     for (int i = 0; i < kStages; ++i) {
       mbar_init(bar(T_CODES + i), 1);
       mbar_init(bar(T_CODES_FREE + i), 128);
@@ -416,22 +479,15 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const Params p) {
     // ------------------------------------------------------------ codes to bf16 operands
     // Each step's K and V from E4M3 codes into the 128-byte swizzled layout that the products read, K of the next step
     // before V of this one.  A lane takes 16 codes at a time; groups of four lanes take the halves of two rows
-    // crosswise, so that eight lanes are on different banks both reading and writing.  NaN codes, which the conversion
-    // would make 480, are looked for in all 16 at once (16 trees of 32 tokens 152.5 -> 153.9 us, 64 of 64 tokens 619 -> 629;
-    // with a branch at every 16 codes 162 and 657) and put right afterwards.
+    // crosswise, so that eight lanes are on different banks both reading and writing.
+    // NaN codes, which the conversion would make 480, are looked for in a lane's part of a step at once (16 trees of 32
+    // tokens 152.0 -> 154.2 us, 64 of 64 tokens 617 -> 630; with a branch at every 16 codes 162 and 657; as the largest of
+    // the bf16 numbers 156 and 637; by the two warps with nothing else to do, in the codes as they land, 160 and 686).  Keys
+    // get a NaN operand, whose scores are NaN where they count.  A value's would reach rows that do not see it: the step
+    // is noted, and the softmax warps look again at the end of their segment.
     const int t = tid & 127;
     constexpr int kEach = kStep * (D / 16) / 128;  // 16-code pieces of a lane
-    // The lane's piece i: its row, where its codes are and where its first eight go (the others 16 bytes across).
-    struct Piece {
-      int row;
-      uint32_t from, to;
-    };
-    const auto piece_at = [&](uint32_t ring, uint32_t out, int i) {
-      const int g = t >> 2, half = D == 64 ? 0 : (g & 1) ^ (i & 1), row = D == 64 ? g + 32 * i : g + 32 * (i >> 1);
-      return Piece{row, ring + row * D + 16 * ((t & 3) + 4 * half),
-                   out + half * C::kChunkBytes + row * 128 + (((2 * t & 6) ^ (row & 7)) << 4)};
-    };
-    const auto convert = [&](uint32_t ring, uint32_t out, int left) {
+    const auto convert = [&](uint32_t ring, uint32_t out, int left) {  // whether there was a NaN code
       uint32_t nan = 0u;
 #pragma unroll 1
       for (int i0 = 0; i0 < kEach; i0 += 2) {
@@ -439,7 +495,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const Params p) {
         Piece at[2];
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-          at[i] = piece_at(ring, out, i0 + i);
+          at[i] = piece_at<D>(t, ring, out, i0 + i);
           x[i] = lds16(at[i].from);
         }
         if (left < kStep) {  // behind the end: may hold anything
@@ -456,22 +512,15 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const Params p) {
           sts16(at[i].to ^ 16, make_uint4(w2.x, w2.y, w3.x, w3.y));
         }
       }
-      if (nan & 0x80808080u) {  // append stores none, but a cache may have been filled otherwise
-#pragma unroll 1
-        for (int k = 0; k < 16 * kEach; ++k) {
-          const Piece a16 = piece_at(ring, out, k >> 4);
-          const uint4 x = lds16(a16.from);
-          const uint32_t w = (k & 8) ? ((k & 4) ? x.w : x.z) : ((k & 4) ? x.y : x.x);
-          if (a16.row < left && ((w >> 8 * (k & 3)) & 0x7fu) == 0x7fu) sts2((a16.to ^ (2 * k & 16)) + 2 * (k & 7), 0x7fc0);
-        }
-      }
-      fence_async();
+      return (nan & 0x80808080u) != 0;
     };
     const auto left_at = [&](const Cursor& x) { return x.len - place_of<kTree>(x, x.tile) * kStep; };
     const auto do_k = [&](uint32_t n, int left) {
       const uint32_t st = n % kStages;
       if (!wait(T_CODES + st, n / kStages) || !wait(T_K_FREE, n + 1)) return false;
-      convert(base + C::kOffRing + st * 2 * C::kCodes, base + C::kOffK, left);
+      const uint32_t ring = base + C::kOffRing + st * 2 * C::kCodes;
+      if (convert(ring, base + C::kOffK, left)) put_nan<D>(t, ring, base + C::kOffK, left);
+      fence_async();
       mbar_arrive(bar(T_K));
       return true;
     };
@@ -483,7 +532,8 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const Params p) {
       if (u < u1 && !do_k(n + 1, next = left_at(c))) break;
       const uint32_t st = n % kStages;
       if (!wait(T_V_FREE, n + 1)) break;
-      convert(base + C::kOffRing + st * 2 * C::kCodes + C::kCodes, base + C::kOffV, left);
+      if (convert(base + C::kOffRing + st * 2 * C::kCodes + C::kCodes, base + C::kOffV, left)) *nan_steps = n + 1;
+      fence_async();
       mbar_arrive(bar(T_V));
       mbar_arrive(bar(T_CODES_FREE + st));
       left = next;
@@ -677,7 +727,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const Params p) {
       if (!ok) break;
       // the segment's end: the next one's rows first, whose scores can follow while this one's sums are stored
       const bool head = c.tile != 0, ends = c.tile + count == c.tiles, whole = !head && ends;
-      const int row = c.mt * kM + r, item = item_of(p, c), seq = c.b * a.Hkv + c.h;
+      const int row = c.mt * kM + r, item = item_of(p, c), seq = c.b * a.Hkv + c.h, tile = c.tile;
       if (!head && warp == 8 && lane == 0) {
         const long long end = u - c.tile + c.tiles;  // the unit behind the item
         if (whole) {
@@ -728,6 +778,15 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const Params p) {
       }
       tc_fence_before();
       mbar_arrive(bar(T_O_FREE));
+      if (*nan_steps > first_n - count && in) {
+        for (unsigned long long nan = nan_channels<D>(p, prefix, seq, row, tile, count, h); nan != 0ull; nan &= nan - 1) {
+          const int ch = (D / 2) * h + __ffsll(nan) - 1;
+          if (whole)
+            a.o[(static_cast<size_t>(seq) * p.R + row) * D + ch] = 0x7fc0;
+          else
+            part[r * D + ch] = __uint_as_float(0x7fc00000u);
+        }
+      }
       if (in && h == 0) {
         if (!whole)
           *reinterpret_cast<float2*>(part + p.prows * D + 2 * r) = make_float2(both, lr);

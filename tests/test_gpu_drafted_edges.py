@@ -27,7 +27,8 @@ def built():
 @pytest.mark.parametrize("quant", [0, 1])
 def test_codes_that_are_not_a_number(Hq, T, D, quant):
     """An E4M3 NaN, which a cache that others filled may hold, counts as NaN: in a key it is the whole row of every token
-    that sees the key and of no other, in a value its channel."""
+    that sees the key and of no other; in a value the channel of every token that sees it (with the kernel of few rows
+    possibly of others as well)."""
     lens, page = [190], 16
     cache, table, _, _ = _cache(lens, 1, D, page, 8)
     masks = do_.draft([-1] + [0 if t % 2 else -1 for t in range(1, T)], T)[0]
@@ -51,8 +52,10 @@ def test_codes_that_are_not_a_number(Hq, T, D, quant):
             o, lse = qat_attention_tree(*args)
             v[at][d] = keep
             assert torch.isnan(o[:, :, rows, d]).all(), (pos, d)
+            if Hq * T > (64 if D == 64 else 32):
+                assert torch.equal(o[:, :, ~rows], clean[:, :, ~rows]), (pos, d)
             others = [c for c in range(D) if c != d]
-            assert torch.equal(o[..., others], clean[..., others]) and torch.equal(lse, clean_lse)
+            assert torch.equal(o[..., others], clean[..., others]) and torch.equal(lse, clean_lse), (pos, d)
     assert torch.equal(qat_attention_tree(*args)[0], clean)
     check_device_status()
 
@@ -108,3 +111,31 @@ def test_a_page_that_begins_with_the_first_key_seen(Hq, Hkv, T, D, page, sinks):
     got = qat_attention_tree(q, cache, _i32(given), _i32(lens), _i64(masks), **how)
     assert capi.qat_attn_device_status() == Status.BAD_PAGE
     assert torch.isnan(got[:, :, 0]).all()
+
+
+@pytest.mark.parametrize("window,sinks", [(None, 0), (300, 20)])
+@pytest.mark.parametrize("Hq,T,D", [(8, 16, 128), (4, 40, 64)])  # 128 and 160 rows a KV head
+def test_codes_that_are_not_a_number_in_many_steps(Hq, T, D, window, sinks):
+    """In some sequences' pages, at several places of many steps, and behind a sequence's end: with the kernel of many rows
+    what no token sees changes nothing, and the other sequences keep their bits."""
+    lens, page = [5000, 131, 2600, 700], 32
+    masks = _masks(np.random.default_rng(T), len(lens), T)
+    cache, table, _, _ = _cache(lens, 1, D, page, 25)
+    q = dev_bf16(normal_bf16(17, (len(lens), Hq, T, D)))
+    how = {} if window is None else dict(window=window, sinks=sinks)
+    args = (q, cache, _i32(table), _i32(lens), _i64(masks), None, 1, True)
+    clean, clean_lse = qat_attention_tree(*args, **how)
+    assert torch.isfinite(clean).all()
+    hit = torch.zeros((len(lens), T), dtype=torch.bool, device="cuda")
+    for b, places in ((0, (0, 15, 1000, 2047, 4700)), (2, (3, 1100, 2590))):
+        seen = do_.tree_seen(lens[b], masks[b], window, sinks)
+        for i, pos in enumerate(places):
+            at = table[b, pos // page], 0, pos % page
+            codes = (cache.k, cache.v)[i % 2].view(torch.uint8)
+            codes[at][(37 * i + 5) % D] = 0x7f + 0x80 * (i % 2)
+            hit[b] |= torch.from_numpy(seen[:, pos]).cuda()
+    assert hit[0].any() and not hit[1].any()
+    o, lse = qat_attention_tree(*args, **how, check=True)
+    hit = hit[:, None].expand(-1, Hq, -1)
+    assert torch.isnan(o[hit]).any(-1).all()
+    assert torch.equal(o[~hit], clean[~hit]) and torch.equal(lse[~hit], clean_lse[~hit])
